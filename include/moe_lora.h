@@ -435,6 +435,123 @@ moe_lora_status moe_lora_route_noalloc(const moe_lora_bf16* router_logits, const
                                        int32_t* topk_ids, float* topk_weights, int32_t* expert_offsets,
                                        int32_t* perm, int32_t* inv_perm, moe_lora_stream stream);
 
+/* ---------------------------------------------------------------------------------------
+ * Operators around the expert layer: the choice of experts from the router's logits in its
+ * general form, a projection with per-token adapters beside it, and the norm of query and key
+ * heads with the position rotation.  They follow the conventions above except where a struct
+ * gives strides (in elements) and alignments of its own.  Forward only, as the layer itself.
+ * ------------------------------------------------------------------------------------- */
+
+/* Scores and group scores of moe_lora_select_experts. */
+enum { MOE_LORA_SCORE_SOFTMAX = 0, MOE_LORA_SCORE_SIGMOID = 1 };
+enum { MOE_LORA_GROUP_MAX = 0, MOE_LORA_GROUP_TOP2 = 1 };
+
+/* Arguments of moe_lora_select_experts. */
+typedef struct {
+  const void* logits;         /* [T, E] bf16, or float32 when logits_f32; rows logits_stride apart  */
+  const float* bias;          /* [E] added to the scores for the choice only; NULL: none            */
+  int32_t* topk_ids;          /* [T, top_k] out: experts in order of choice                         */
+  float* topk_weights;        /* [T, top_k] out                                                     */
+  int32_t* packed_topk_ids;   /* [T, top_k] out, optional: (id << 16) | bf16 bits of the weight,
+                                 the input of moe_lora_forward_routed                               */
+  int64_t logits_stride;      /* >= E                                                               */
+  int T, E, top_k;            /* T >= 0, E 1..1024, top_k 1..32 and <= topk_group * E / n_group     */
+  int logits_f32;
+  int scoring;                /* MOE_LORA_SCORE_*                                                   */
+  int n_group, topk_group;    /* E a multiple of n_group, n_group <= 32; 1 and 1: no groups         */
+  int group_score;            /* MOE_LORA_GROUP_*: a group's best key, or the sum of its best two   */
+  int renormalize;            /* divide the chosen scores by their sum                              */
+  float routed_scaling_factor;
+} moe_lora_select_args;
+
+/* Experts of every token: s = softmax(z) or sigmoid(z); key = s + bias; the topk_group groups
+   of E / n_group neighbouring experts with the best group score stay; ids = the top_k largest
+   keys in them, ties to the lower id (of groups: the lower group); weight = s of the chosen
+   expert, divided by the sum of the chosen when renormalize, times routed_scaling_factor.  All
+   in float32; the softmax sum does not depend on any order.
+   A logit of -inf or NaN rules its expert out: it comes after every other expert whatever its
+   bias, and so do the experts of groups that do not stay; where fewer than top_k experts are
+   left the rest are the lowest ids of these, with weight 0 (a token whose experts are all ruled
+   out gets ids 0..top_k-1 with weights 0).  +inf counts as the largest finite value.
+   logits aligned to their type.  One launch, no workspace.
+   Errors: INVALID_ARG, UNSUPPORTED (n_group > 32), CUDA. */
+moe_lora_status moe_lora_select_experts(moe_lora_handle* h, const moe_lora_select_args* a, moe_lora_stream stream);
+
+/* Stacked copy of the adapters of one projection: A [S, R, K] and B [S, N, R] (bf16, dense, A
+   16-byte aligned) of S slots (1..64) with ranks h_ranks[s] <= R <= 128, side by side: rows of
+   A_s then columns of B_s, each rank rounded up to 8, all together at most 4096.  Rows of A and
+   columns of B past a slot's rank are never read.  Made once when the adapters in the slots
+   change; `adapters` is caller-owned, 16-byte aligned, moe_lora_linear_adapters_size() bytes
+   (0 when every rank is 0).  K a multiple of 8.
+   Errors: INVALID_ARG, UNSUPPORTED (more than 4096 stacked ranks), CUDA. */
+moe_lora_status moe_lora_linear_adapters_size(int S, int N, int K, const int32_t* h_ranks, size_t* bytes);
+moe_lora_status moe_lora_linear_pack_adapters(moe_lora_handle* h, const moe_lora_bf16* A, const moe_lora_bf16* B,
+                                              int S, int N, int K, int R, const int32_t* h_ranks, void* adapters,
+                                              moe_lora_stream stream);
+
+/* Arguments of moe_lora_linear.  Strides in elements between rows. */
+typedef struct {
+  const moe_lora_bf16* x;       /* [T, K], 16-byte aligned, x_stride a multiple of 8                */
+  const moe_lora_bf16* w;       /* [N, K], 16-byte aligned, w_stride a multiple of 8                */
+  const float* bias;            /* [N] or NULL                                                      */
+  void* y;                      /* [T, N] bf16, or float32 when y_f32; must not overlap an input    */
+  const void* adapters;         /* moe_lora_linear_pack_adapters of the same S, N, K, h_ranks       */
+  const int32_t* slot_idx;      /* [T] adapter slot of each token, -1: none (S > 0)                 */
+  const int32_t* h_ranks;       /* [S] host                                                         */
+  const float* h_scalings;      /* [S] host, 0 disables the slot                                    */
+  int64_t x_stride, w_stride, y_stride;
+  int T, N, K;                  /* T >= 0, N >= 1, K a multiple of 8                                */
+  int S;                        /* 0: no adapters                                                   */
+  int y_f32;
+} moe_lora_linear_args;
+
+/* Host-only: bytes of workspace that moe_lora_linear needs at most for T tokens. */
+moe_lora_status moe_lora_linear_workspace_size(int T, int S, const int32_t* h_ranks, size_t* bytes);
+
+/* A shared projection with per-token adapters beside it:
+     y[t] = w x[t] + bias + scaling[s] B_s (A_s x[t]),   s = slot_idx[t]
+   summed in float32 and rounded once to y's type.  The shrunk row scaling[s] A_s x[t] is an
+   operand of the tensor cores in between: bf16 for a bf16 y, three bf16 pieces (24 significant
+   bits) for a float32 y.  Two launches (shrink, then the product, which starts beside it), one
+   without active adapters.  `workspace` (16-byte aligned, contents on entry do not matter)
+   starts with the status word that moe_lora_check_status reads: DEVICE_CHECK when a slot index
+   lies outside [-1, S) (such a token gets no adapter), TIMEOUT when a bounded wait ran out.
+   Errors: INVALID_ARG, UNSUPPORTED (more than 4096 stacked ranks), WORKSPACE_TOO_SMALL, CUDA. */
+moe_lora_status moe_lora_linear(moe_lora_handle* h, const moe_lora_linear_args* a, void* workspace,
+                                size_t workspace_bytes, moe_lora_stream stream);
+
+/* Arguments of moe_lora_qk_norm_rope.  Strides in elements; values of a head are adjacent. */
+typedef struct {
+  const moe_lora_bf16* q;       /* [T, q_heads, head_dim], for instance slices of merged q/k/v rows  */
+  const moe_lora_bf16* k;       /* [T, k_heads, head_dim]                                            */
+  moe_lora_bf16* q_out;         /* the same shapes; may be q and k themselves                        */
+  moe_lora_bf16* k_out;
+  const void* q_weight;         /* [head_dim] bf16, or float32 when weight_f32                       */
+  const void* k_weight;
+  const float* cos_sin;         /* [num_positions, rotary_dim]: cosines, then sines                  */
+  const void* positions;        /* [T] int32, or int64 when positions_i64                            */
+  int64_t q_stride_t, q_stride_h, k_stride_t, k_stride_h;
+  int64_t q_out_stride_t, q_out_stride_h, k_out_stride_t, k_out_stride_h;
+  int64_t cos_sin_stride;       /* >= rotary_dim                                                     */
+  int T, q_heads, k_heads;      /* either count of heads may be 0 (its pointers are then ignored)    */
+  int head_dim;                 /* 1..512                                                            */
+  int rotary_dim;               /* even, 0..head_dim: the leading values of a head that are rotated  */
+  int num_positions;
+  int weight_f32, positions_i64;
+  int interleaved;              /* rotate pairs (2i, 2i+1) instead of (i, i + rotary_dim / 2)        */
+  float eps;
+} moe_lora_qk_args;
+
+/* Every query and key head: x / sqrt(mean(x^2) + eps) * weight, then the rotation of its first
+   rotary_dim values by the token's row of cos_sin.  float32 throughout, one rounding to bf16 at
+   the end.  Any alignment of a bf16 element is taken; addresses and strides of whole 16-byte
+   pieces are the fast case.  `workspace` (optional, 4 bytes): its first word is the status that
+   moe_lora_check_status reads: DEVICE_CHECK when a position lies outside [0, num_positions)
+   (those tokens are normed and not rotated).  One launch.
+   Errors: INVALID_ARG, UNSUPPORTED (head_dim > 512), WORKSPACE_TOO_SMALL, CUDA. */
+moe_lora_status moe_lora_qk_norm_rope(moe_lora_handle* h, const moe_lora_qk_args* a, void* workspace,
+                                      size_t workspace_bytes, moe_lora_stream stream);
+
 /* Cumulative number of this library's kernels launched through `h` (each route, permute,
    forward or routed forward adds the kernels it enqueued; a memset is not counted).  For
    measurement; the pages have no counterpart.  Host-only.  Errors: INVALID_ARG. */

@@ -11,5 +11,7 @@ from .binding import (  # noqa: F401
     packed_lora_b_shape, moe_lora_pack_lora_a, moe_lora_packed_lora_a_size, packed_lora_a_shape,
     moe_lora_workspace_size, FLAG_LORA_OFF, FLAG_FORCE_SINGLE_STREAM, FLAG_FORCE_TWO_STREAM, FLAG_UNFUSED_LORA, FLAG_NO_PDL, FLAG_SHARED_OUTER,
     FLAG_DOWN_LORA_SIDE, FLAG_SEPARATE_SHRINK,
-    ROUTE_RENORMALIZE, ROUTE_DEEPSEEK_V3, STAGES, NUM_STAGES,
+    moe_lora_select_experts, moe_lora_qk_norm_rope, alloc_qk_norm_rope_workspace, moe_lora_linear,
+    moe_lora_linear_adapters, moe_lora_linear_workspace_size, alloc_linear_workspace, LinearAdapters,
+    ROUTE_RENORMALIZE, ROUTE_DEEPSEEK_V3, SCORE_SOFTMAX, SCORE_SIGMOID, GROUP_MAX, GROUP_TOP2, STAGES, NUM_STAGES,
 )

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Sequence
 
 import torch
@@ -30,6 +31,10 @@ FLAG_NO_PDL = 16
 FLAG_SHARED_OUTER = 32
 FLAG_DOWN_LORA_SIDE = 64
 FLAG_SEPARATE_SHRINK = 128
+SCORE_SOFTMAX = 0
+SCORE_SIGMOID = 1
+GROUP_MAX = 0
+GROUP_TOP2 = 1
 STAGES = ["route", "permute", "gate_up_gemm", "lora_gate_up", "activation", "down_gemm",
           "lora_down", "finalize"]
 NUM_STAGES = len(STAGES)
@@ -40,7 +45,9 @@ EXPORTED = ["moe_lora_create", "moe_lora_destroy", "moe_lora_status_string", "mo
             "moe_lora_launch_count", "moe_lora_forward_fp8", "moe_lora_quant_fp8", "moe_lora_grouped_gemm_fp8",
             "moe_lora_forward_nvfp4", "moe_lora_quant_nvfp4", "moe_lora_grouped_gemm_nvfp4",
             "moe_lora_packed_lora_b_size", "moe_lora_pack_lora_b", "moe_lora_packed_lora_a_size",
-            "moe_lora_pack_lora_a"]
+            "moe_lora_pack_lora_a", "moe_lora_select_experts", "moe_lora_qk_norm_rope",
+            "moe_lora_linear_adapters_size", "moe_lora_linear_pack_adapters", "moe_lora_linear_workspace_size",
+            "moe_lora_linear"]
 
 
 class MoELoRAError(RuntimeError):
@@ -139,6 +146,14 @@ def lib() -> ctypes.CDLL:
                                               ctypes.POINTER(c_size_t)]
     L.moe_lora_pack_lora_a.argtypes = [c_void_p, c_void_p, c_int, c_int, c_int, c_int,
                                        ctypes.POINTER(ctypes.c_int32), c_void_p, c_void_p]
+    # the argument structs of these come as packed bytes
+    L.moe_lora_select_experts.argtypes = [c_void_p, ctypes.c_char_p, c_void_p]
+    L.moe_lora_qk_norm_rope.argtypes = [c_void_p, ctypes.c_char_p, c_void_p, c_size_t, c_void_p]
+    L.moe_lora_linear.argtypes = [c_void_p, ctypes.c_char_p, c_void_p, c_size_t, c_void_p]
+    L.moe_lora_linear_adapters_size.argtypes = [c_int, c_int, c_int, c_void_p, ctypes.POINTER(c_size_t)]
+    L.moe_lora_linear_pack_adapters.argtypes = [c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_void_p,
+                                                c_void_p, c_void_p]
+    L.moe_lora_linear_workspace_size.argtypes = [c_int, c_int, c_void_p, ctypes.POINTER(c_size_t)]
     for name in EXPORTED:
         if name not in ("moe_lora_status_string", "moe_lora_last_cuda_error"):
             getattr(L, name).restype = c_int
@@ -718,3 +733,227 @@ def moe_lora_check_status(workspace: torch.Tensor, stream=None):
     word = ctypes.c_uint32()
     st = lib().moe_lora_check_status(_ptr(workspace, torch.uint8, "workspace"), _stream(stream), ctypes.byref(word))
     return st, word.value
+
+
+# ---------------------------------------------------------------- operators around the layer
+# These are called once or more per layer on batches down to one token, where the host's time
+# is the call's time: each argument struct is packed in one go, and results are allocated only
+# when the caller brings none.
+_select_args = struct.Struct("@5P1q9if").pack       # moe_lora_select_args
+_qk_args = struct.Struct("@8P9q9if").pack           # moe_lora_qk_args
+_linear_args = struct.Struct("@8P3q5i4x").pack        # moe_lora_linear_args
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
+
+
+def _stream_on(device: torch.device, stream) -> int:
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(device.index)
+    return _stream(stream)
+
+
+def _need(cond, msg):
+    if not cond:
+        raise ValueError(msg)
+
+
+def _need_vec(t: torch.Tensor, n: int, dtypes, dev, name: str) -> int:
+    """The address of a dense vector of n values on `dev`."""
+    if t.dtype not in dtypes or t.shape != (n,) or t.device != dev or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a dense [{n}] tensor of {' or '.join(str(d) for d in dtypes)} on {dev}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _need_out(t: torch.Tensor, shape, dtype, dev, name: str) -> int:
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} {tuple(shape)} tensor on {dev}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+_F32 = (torch.float32,)
+_BF16_F32 = (torch.bfloat16, torch.float32)
+
+
+def moe_lora_select_experts(handle: Handle, logits: torch.Tensor, top_k: int, scoring: int = SCORE_SOFTMAX,
+                            bias: Optional[torch.Tensor] = None, n_group: int = 1, topk_group: int = 1,
+                            group_score: int = GROUP_MAX, renormalize: bool = True,
+                            routed_scaling_factor: float = 1.0, packed: bool = False,
+                            outputs: Optional[dict] = None, stream=None) -> dict:
+    """Experts of every token from the router's logits [T, E] (bf16 or float32, rows may be
+    strided): scores softmax(z) or sigmoid(z), chosen by score + bias [E] inside the topk_group
+    best of n_group groups, ties to the lower id; weights are the chosen scores, divided by their
+    sum when `renormalize`, times routed_scaling_factor.  Returns a dict of topk_ids [T, top_k]
+    int32 and topk_weights [T, top_k] float32, and with `packed` packed_topk_ids [T, top_k], the
+    words that moe_lora_forward_routed takes.  Logits of -inf or NaN rule an expert out."""
+    _need(logits.dim() == 2 and logits.is_cuda and logits.dtype in _BF16_F32 and
+          (logits.stride(1) == 1 or logits.shape[1] <= 1),
+          "logits must be a bf16 or float32 CUDA tensor [T, E] with adjacent columns")
+    T, E = logits.shape
+    dev = logits.device
+    o = outputs if outputs is not None else {}
+    ids, w, pk = o.get("topk_ids"), o.get("topk_weights"), o.get("packed_topk_ids")
+    shape = (T, top_k)
+    if ids is None:
+        o["topk_ids"] = ids = torch.empty(shape, dtype=torch.int32, device=dev)
+    if w is None:
+        o["topk_weights"] = w = torch.empty(shape, dtype=torch.float32, device=dev)
+    if pk is None and packed:
+        o["packed_topk_ids"] = pk = torch.empty(shape, dtype=torch.int32, device=dev)
+    args = _select_args(
+        logits.data_ptr(), 0 if bias is None else _need_vec(bias, E, _F32, dev, "bias"),
+        _need_out(ids, shape, torch.int32, dev, "topk_ids"), _need_out(w, shape, torch.float32, dev, "topk_weights"),
+        0 if pk is None else _need_out(pk, shape, torch.int32, dev, "packed_topk_ids"),
+        logits.stride(0) if T > 1 else E, T, E, top_k, logits.dtype is torch.float32, scoring, n_group, topk_group,
+        group_score, bool(renormalize), routed_scaling_factor)
+    st = lib().moe_lora_select_experts(handle.ptr, args, _stream_on(dev, stream))
+    if st:
+        _check(st, "moe_lora_select_experts")
+    return o
+
+
+class LinearAdapters:
+    """The adapters of one projection, stacked by moe_lora_linear_adapters: what a serving program
+    keeps per projection while its slots hold the same adapters."""
+
+    def __init__(self, packed: torch.Tensor, S: int, N: int, K: int, ranks: Sequence[int], scalings: Sequence[float]):
+        self.packed = packed
+        self.S, self.N, self.K = S, N, K
+        self.ranks = (ctypes.c_int32 * S)(*ranks)
+        self.scalings = (c_float * S)(*scalings)
+        self.address = packed.data_ptr()
+        self.ranks_address, self.scalings_address = ctypes.addressof(self.ranks), ctypes.addressof(self.scalings)
+
+
+def moe_lora_linear_adapters(handle: Handle, A: torch.Tensor, B: torch.Tensor, ranks: Sequence[int],
+                             scalings: Sequence[float], stream=None) -> LinearAdapters:
+    """Stacks the adapters A [S, R, K] and B [S, N, R] (dense bf16; slot s uses its first ranks[s]
+    ranks, times scalings[s]) of one projection for moe_lora_linear.  Once per adapter load."""
+    _need(A.dim() == 3 and B.dim() == 3 and A.dtype == B.dtype == torch.bfloat16 and A.is_cuda and
+          A.device == B.device and A.is_contiguous() and B.is_contiguous(),
+          "A [S, R, K] and B [S, N, R] must be dense bf16 tensors on the same CUDA device")
+    S, R, K = A.shape
+    N = B.shape[1]
+    _need(B.shape[0] == S and B.shape[2] == R, f"B must have shape ({S}, N, {R}), got {tuple(B.shape)}")
+    _need(len(ranks) == S and len(scalings) == S, f"need {S} ranks and scalings, got {len(ranks)} and {len(scalings)}")
+    ranks = [int(r) for r in ranks]
+    arr = (ctypes.c_int32 * max(S, 1))(*ranks)
+    n = c_size_t()
+    _check(lib().moe_lora_linear_adapters_size(S, N, K, arr, ctypes.byref(n)), "moe_lora_linear_adapters_size")
+    packed = torch.empty(max(n.value, 16), dtype=torch.uint8, device=A.device)
+    _check(lib().moe_lora_linear_pack_adapters(handle.ptr, A.data_ptr(), B.data_ptr(), S, N, K, R, arr,
+                                               packed.data_ptr(), _stream_on(A.device, stream)),
+           "moe_lora_linear_pack_adapters")
+    return LinearAdapters(packed, S, N, K, ranks, [float(s) for s in scalings])
+
+
+def moe_lora_linear_workspace_size(T: int, adapters: Optional[LinearAdapters] = None) -> int:
+    """Bytes of workspace that moe_lora_linear needs at most for T tokens."""
+    n = c_size_t()
+    _check(lib().moe_lora_linear_workspace_size(T, adapters.S if adapters else 0,
+                                                adapters.ranks_address if adapters else None, ctypes.byref(n)),
+           "moe_lora_linear_workspace_size")
+    return n.value
+
+
+def alloc_linear_workspace(T: int, adapters: Optional[LinearAdapters] = None, device="cuda") -> torch.Tensor:
+    return torch.empty(moe_lora_linear_workspace_size(T, adapters), dtype=torch.uint8, device=device)
+
+
+def _rows(t: torch.Tensor, cols: int, dev, name: str) -> int:
+    if t.dim() != 2 or t.dtype != torch.bfloat16 or t.shape[1] != cols or t.device != dev or (t.stride(1) != 1 and cols > 1):
+        raise ValueError(f"{name} must be a bf16 [rows, {cols}] tensor on {dev} with adjacent columns, got {t.dtype} "
+                         f"{tuple(t.shape)} strides {t.stride()} on {t.device}")
+    return t.data_ptr()
+
+
+def moe_lora_linear(handle: Handle, x: torch.Tensor, w: torch.Tensor, adapters: Optional[LinearAdapters] = None,
+                    slot_idx: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                    out: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
+                    workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """A shared projection with per-token adapters beside it: row t of the result is w x[t] + bias +
+    scaling_s B_s (A_s x[t]) with s = slot_idx[t] (-1: none).  x [T, K] and w [N, K] bf16 (rows may
+    be strided, by multiples of 8), bias [N] float32, slot_idx [T] int32.  The result is a new
+    [T, N] tensor of out_dtype (bf16 or float32), or `out`, whose rows may be strided (a column
+    range of a wider tensor).  `workspace`: alloc_linear_workspace(T, adapters), or allocated."""
+    _need(x.dim() == 2 and x.is_cuda, "x must be a CUDA tensor [T, K]")
+    T, K = x.shape
+    dev = x.device
+    N = w.shape[0]
+    xp, wp = _rows(x, K, dev, "x"), _rows(w, K, dev, "w")
+    if out is None:
+        _need(out_dtype in _BF16_F32, "out_dtype must be torch.bfloat16 or torch.float32")
+        out = torch.empty((T, N), dtype=out_dtype, device=dev)
+    else:
+        _need(out.dtype in _BF16_F32 and out.shape == (T, N) and out.device == dev and (out.stride(1) == 1 or N == 1),
+              f"out must be a bf16 or float32 ({T}, {N}) tensor on {dev} with adjacent columns")
+    if adapters is not None:
+        _need(adapters.N == N and adapters.K == K and adapters.packed.device == dev,
+              f"the adapters are for a [{adapters.N}, {adapters.K}] projection on {adapters.packed.device}, w is "
+              f"[{N}, {K}] on {dev}")
+        _need(slot_idx is not None, "slot_idx [T] is required with adapters")
+        S, ap, rp, sp = adapters.S, adapters.address, adapters.ranks_address, adapters.scalings_address
+        ip = _need_vec(slot_idx, T, (torch.int32,), dev, "slot_idx")
+    else:
+        S = ap = rp = sp = ip = 0
+    if workspace is None:
+        workspace = alloc_linear_workspace(T, adapters, dev)
+    args = _linear_args(xp, wp, 0 if bias is None else _need_vec(bias, N, _F32, dev, "bias"), out.data_ptr(), ap, ip,
+                        rp, sp, x.stride(0), w.stride(0), out.stride(0), T, N, K, S, out.dtype is torch.float32)
+    st = lib().moe_lora_linear(handle.ptr, args, _ptr(workspace, torch.uint8, "workspace"), workspace.numel(),
+                               _stream_on(dev, stream))
+    if st:
+        _check(st, "moe_lora_linear")
+    return out
+
+
+def alloc_qk_norm_rope_workspace(device="cuda") -> torch.Tensor:
+    """The status word of moe_lora_qk_norm_rope, for moe_lora_check_status."""
+    return torch.zeros(256, dtype=torch.uint8, device=device)
+
+
+def _heads(t: torch.Tensor, T: int, D: int, dev, name: str):
+    if (t.dim() != 3 or t.dtype != torch.bfloat16 or t.device != dev or t.shape[0] != T or t.shape[2] != D or
+            (t.stride(2) != 1 and D > 1)):
+        raise ValueError(f"{name} must be a bf16 [T, heads, {D}] tensor on {dev} with T = {T} and adjacent head values, "
+                         f"got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
+    return t.data_ptr(), t.stride(0), t.stride(1)
+
+
+def moe_lora_qk_norm_rope(handle: Handle, q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor,
+                          k_weight: torch.Tensor, cos_sin: torch.Tensor, positions: torch.Tensor, eps: float = 1e-6,
+                          interleaved: bool = False, q_out: Optional[torch.Tensor] = None,
+                          k_out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """Norm of every head of q [T, Hq, D] and k [T, Hk, D] (bf16, for instance slices of merged
+    q/k/v rows) by its root mean square, times q_weight / k_weight [D] (bf16 or float32), then the
+    rotation of the first R values by row positions[t] (int32 or int64) of cos_sin [P, R]
+    (float32: R/2 cosines, R/2 sines); pairs (i, i + R/2), or (2i, 2i + 1) when interleaved.
+    Returns (q_out, k_out), new dense tensors unless given; they may be q and k themselves."""
+    _need(q.dim() == 3 and q.is_cuda, "q must be a CUDA tensor [T, heads, D]")
+    T, Hq, D = q.shape
+    dev = q.device
+    _need(cos_sin.dim() == 2 and cos_sin.dtype == torch.float32 and cos_sin.device == dev and
+          (cos_sin.stride(1) == 1 or cos_sin.shape[1] <= 1), "cos_sin must be a float32 [positions, R] tensor")
+    P, R = cos_sin.shape
+    if q_out is None:
+        q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+    if k_out is None:
+        k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=dev)
+    qp, q_t, q_h = _heads(q, T, D, dev, "q")
+    kp, k_t, k_h = _heads(k, T, D, dev, "k")
+    qop, qo_t, qo_h = _heads(q_out, T, D, dev, "q_out")
+    kop, ko_t, ko_h = _heads(k_out, T, D, dev, "k_out")
+    Hk = k.shape[1]
+    _need(q_out.shape[1] == Hq and k_out.shape[1] == Hk, "q_out and k_out must have as many heads as q and k")
+    _need(q_weight.dtype == k_weight.dtype, "q_weight and k_weight must have the same type")
+    args = _qk_args(
+        qp, kp, qop, kop, _need_vec(q_weight, D, _BF16_F32, dev, "q_weight"),
+        _need_vec(k_weight, D, _BF16_F32, dev, "k_weight"), cos_sin.data_ptr(),
+        _need_vec(positions, T, (torch.int32, torch.int64), dev, "positions"), q_t, q_h, k_t, k_h, qo_t, qo_h, ko_t,
+        ko_h, cos_sin.stride(0) if P > 1 else R, T, Hq, Hk, D, R, P, q_weight.dtype is torch.float32,
+        positions.dtype is torch.int64, bool(interleaved), eps)
+    wp, wn = (None, 0) if workspace is None else (_ptr(workspace, torch.uint8, "workspace"), workspace.numel())
+    st = lib().moe_lora_qk_norm_rope(handle.ptr, args, wp, wn, _stream_on(dev, stream))
+    if st:
+        _check(st, "moe_lora_qk_norm_rope")
+    return q_out, k_out

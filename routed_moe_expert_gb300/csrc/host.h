@@ -1,0 +1,48 @@
+// What the C-ABI sources share on the host: the handle, error reporting and pointer checks.
+#pragma once
+
+#include "../../include/moe_lora.h"
+#include "kernels.h"
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+struct moe_lora_handle {
+  int device = 0;
+  int num_sms = 0;
+  cudaStream_t side = nullptr;
+  cudaEvent_t ev_fork = nullptr, ev_ready = nullptr;
+  EncodeTiledFn encode = nullptr;
+  int coop_ctas[mlk::kMaxExperts + 1];   // cache of route_max_coop_ctas by E (0 = unknown)
+  uint64_t launches = 0;                  // kernels launched through this handle
+  bool linear_ready = false;              // the projection kernels have their shared memory limits
+};
+
+namespace mlk {
+
+// Records `err` as the calling thread's last CUDA error and returns MOE_LORA_ERR_CUDA.
+moe_lora_status cuda_fail(cudaError_t err, const char* what);
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+inline bool aligned2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
+
+}  // namespace mlk
+
+#define ML_CUDA(call, what)                                  \
+  do {                                                       \
+    cudaError_t _e = (call);                                 \
+    if (_e != cudaSuccess) return mlk::cuda_fail(_e, what);  \
+  } while (0)
+
+// A launch of one of this library's kernels, counted on the handle (moe_lora_launch_count).
+#define ML_LAUNCH(h, call, what)                    \
+  do {                                              \
+    ML_CUDA(call, what);                            \
+    ++(h)->launches;                                \
+  } while (0)

@@ -21,7 +21,7 @@ constexpr int kMaxLoraPanels = 8;   // 64-column panels of the stacked ranks of 
 enum : uint32_t {
   kWhereRouteBarrier = 1, kWhereGemmProducer = 2, kWhereGemmMma = 3, kWhereGemmEpilogue = 4,
   kWhereLoraShrinkGu = 5, kWhereLoraExpandGu = 6, kWhereLoraShrinkDn = 7, kWhereFinalize = 8,
-  kWhereLoraShrinkTc = 9, kWhereRouteExpert = 10,
+  kWhereLoraShrinkTc = 9, kWhereRouteExpert = 10, kWhereQkPosition = 11, kWhereLinear = 12,
 };
 
 struct LoraSlots {

@@ -1,0 +1,199 @@
+// Host side of moe_lora_linear: argument checks, the layout of stacked adapters and of the
+// workspace, tensor maps, the choice of tiles and the launches.
+#include "linear.h"
+#include "host.h"
+
+#include <cstring>
+
+using namespace mlk;
+
+namespace {
+
+// Stacked columns: every slot's rank rounded up to 8 (16-byte pieces of a row), the end to a
+// whole 64-column block.  lo[s] is slot s's first column, lo[S] the end.
+int stacked_ranks(const int32_t* h_ranks, int S, int* lo) {
+  int c = 0;
+  for (int s = 0; s < S; ++s) {
+    lo[s] = c;
+    c += (h_ranks[s] + 7) / 8 * 8;
+  }
+  lo[S] = c;
+  return (c + kAdapterBlock - 1) / kAdapterBlock * kAdapterBlock;
+}
+
+moe_lora_status check_ranks(int S, const int32_t* h_ranks, int most) {
+  if (S < 0 || S > kMaxSlots || (S > 0 && h_ranks == nullptr)) return MOE_LORA_ERR_INVALID_ARG;
+  for (int s = 0; s < S; ++s)
+    if (h_ranks[s] < 0 || h_ranks[s] > most) return MOE_LORA_ERR_INVALID_ARG;
+  int lo[kMaxSlots + 1];
+  return stacked_ranks(h_ranks, S, lo) <= kMaxStackedRanks ? MOE_LORA_OK : MOE_LORA_ERR_UNSUPPORTED;
+}
+
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+bool tile_map(const moe_lora_handle* h, CUtensorMap* m, const void* base, long long rows, long long cols,
+              long long stride, int box_rows) {
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride) * 2};
+  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[2] = {1, 1};
+  return h->encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int token_tile(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128; }
+
+// CTAs that share a tile's K: as many as keep the grid at two CTAs per SM, each with at least
+// four 64-wide K blocks.
+int pick_split(long long tiles, int nk, int sms) {
+  int split = 1;
+  while (split < kLinearMaxSplit && tiles * split * 2 <= 2LL * sms && nk / (split * 2) >= 4) split *= 2;
+  return split;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_lora_status moe_lora_linear_adapters_size(int S, int N, int K, const int32_t* h_ranks, size_t* bytes) {
+  if (bytes == nullptr || S < 1 || N < 1 || K < 8 || K % 8 != 0) return MOE_LORA_ERR_INVALID_ARG;
+  const moe_lora_status st = check_ranks(S, h_ranks, kMaxRank);
+  if (st != MOE_LORA_OK) return st;
+  int lo[kMaxSlots + 1];
+  const size_t rs = static_cast<size_t>(stacked_ranks(h_ranks, S, lo));
+  *bytes = align256(rs * K * 2) + align256(rs * N * 2);
+  return MOE_LORA_OK;
+}
+
+moe_lora_status moe_lora_linear_pack_adapters(moe_lora_handle* h, const moe_lora_bf16* A, const moe_lora_bf16* B,
+                                              int S, int N, int K, int R, const int32_t* h_ranks, void* adapters,
+                                              moe_lora_stream stream) {
+  if (h == nullptr || R < 0 || R > kMaxRank) return MOE_LORA_ERR_INVALID_ARG;
+  size_t bytes = 0;
+  moe_lora_status st = moe_lora_linear_adapters_size(S, N, K, h_ranks, &bytes);
+  if (st != MOE_LORA_OK) return st;
+  st = check_ranks(S, h_ranks, R);
+  if (st != MOE_LORA_OK) return st;
+  if (bytes == 0) return MOE_LORA_OK;   // every rank is 0
+  if (A == nullptr || B == nullptr || adapters == nullptr || !aligned16(A) || !aligned2(B) || !aligned16(adapters))
+    return MOE_LORA_ERR_INVALID_ARG;
+  LinearPackParams p;
+  int lo[kMaxSlots + 1];
+  p.Rs = stacked_ranks(h_ranks, S, lo);
+  for (int s = 0; s <= S; ++s) p.lo[s] = static_cast<uint16_t>(lo[s]);
+  for (int s = 0; s < S; ++s) p.ranks[s] = static_cast<uint16_t>(h_ranks[s]);
+  p.A = reinterpret_cast<const __nv_bfloat16*>(A);
+  p.B = reinterpret_cast<const __nv_bfloat16*>(B);
+  p.Ap = static_cast<__nv_bfloat16*>(adapters);
+  p.Bp = p.Ap + align256(static_cast<size_t>(p.Rs) * K * 2) / 2;
+  p.S = S;
+  p.N = N;
+  p.K = K;
+  p.R = R;
+  if (static_cast<long long>(p.Rs) * (K / 8) > 255LL * 0x7fffffff || static_cast<long long>(N) * p.Rs > 255LL * 0x7fffffff)
+    return MOE_LORA_ERR_INVALID_ARG;
+  ML_LAUNCH(h, launch_linear_pack(p, stream), "linear pack launch");
+  return MOE_LORA_OK;
+}
+
+moe_lora_status moe_lora_linear_workspace_size(int T, int S, const int32_t* h_ranks, size_t* bytes) {
+  if (bytes == nullptr || T < 0) return MOE_LORA_ERR_INVALID_ARG;
+  const moe_lora_status st = check_ranks(S, h_ranks, kMaxRank);
+  if (st != MOE_LORA_OK) return st;
+  int lo[kMaxSlots + 1];
+  *bytes = 256 + align256(static_cast<size_t>(T) * stacked_ranks(h_ranks, S, lo) * kFloatPieces * 2);
+  return MOE_LORA_OK;
+}
+
+moe_lora_status moe_lora_linear(moe_lora_handle* h, const moe_lora_linear_args* a, void* workspace,
+                                size_t workspace_bytes, moe_lora_stream stream) {
+  if (h == nullptr || a == nullptr) return MOE_LORA_ERR_INVALID_ARG;
+  if (a->T < 0 || a->N < 1 || a->K < 8 || a->K % 8 != 0) return MOE_LORA_ERR_INVALID_ARG;
+  moe_lora_status st = check_ranks(a->S, a->h_ranks, kMaxRank);
+  if (st != MOE_LORA_OK) return st;
+  if (a->S > 0) {
+    if (a->h_scalings == nullptr) return MOE_LORA_ERR_INVALID_ARG;
+    for (int s = 0; s < a->S; ++s)
+      if (a->h_scalings[s] != a->h_scalings[s]) return MOE_LORA_ERR_INVALID_ARG;   // NaN
+  }
+  const long long kMaxStride = 1LL << 38;   // a tensor map's row pitch is below 2^40 bytes
+  if (a->T > 1 && (a->x_stride < a->K || a->x_stride % 8 != 0 || a->x_stride > kMaxStride || a->y_stride < a->N))
+    return MOE_LORA_ERR_INVALID_ARG;
+  if (a->N > 1 && (a->w_stride < a->K || a->w_stride % 8 != 0 || a->w_stride > kMaxStride))
+    return MOE_LORA_ERR_INVALID_ARG;
+  if (a->T == 0) return MOE_LORA_OK;
+  if (a->x == nullptr || a->w == nullptr || a->y == nullptr || workspace == nullptr) return MOE_LORA_ERR_INVALID_ARG;
+  if (!aligned16(a->x) || !aligned16(a->w) || !aligned4(a->bias) || !(a->y_f32 ? aligned4(a->y) : aligned2(a->y)) ||
+      !aligned16(workspace))
+    return MOE_LORA_ERR_INVALID_ARG;
+  if (a->S > 0 && (a->slot_idx == nullptr || !aligned4(a->slot_idx))) return MOE_LORA_ERR_INVALID_ARG;
+
+  LinearParams p;
+  std::memset(&p, 0, sizeof(p));
+  int lo[kMaxSlots + 1];
+  const int Rs = stacked_ranks(a->h_ranks, a->S, lo);
+  p.slots.S = a->S;
+  bool active = false;   // some slot adds something
+  for (int s = 0; s < a->S; ++s) {
+    p.slots.lo[s] = p.slots.hi[s] = static_cast<uint16_t>(lo[s]);
+    p.slots.scal[s] = a->h_scalings[s];
+    if (a->h_scalings[s] != 0.0f && a->h_ranks[s] > 0) {
+      p.slots.hi[s] = static_cast<uint16_t>(lo[s] + a->h_ranks[s]);
+      active = true;
+    }
+  }
+  const size_t need = 256 + (active ? align256(static_cast<size_t>(a->T) * Rs * kFloatPieces * 2) : 0);
+  if (workspace_bytes < need) return MOE_LORA_ERR_WORKSPACE_TOO_SMALL;
+  if (active && (a->adapters == nullptr || !aligned16(a->adapters))) return MOE_LORA_ERR_INVALID_ARG;
+  if (!h->linear_ready) {
+    ML_CUDA(linear_narrow_setup(), "linear setup");
+    h->linear_ready = true;
+  }
+
+  const int bn = token_tile(a->T);
+  p.T = a->T;
+  p.K = a->K;
+  p.slot_idx = a->slot_idx;
+  p.status = static_cast<uint32_t*>(workspace);
+  p.token_tiles = (a->T + bn - 1) / bn;
+  p.pieces = a->y_f32 ? kFloatPieces : 1;
+  void* u = static_cast<uint8_t*>(workspace) + 256;
+  const long long ldu = static_cast<long long>(p.pieces) * Rs;
+  const long long x_stride = a->T > 1 ? a->x_stride : a->K, w_stride = a->N > 1 ? a->w_stride : a->K;
+  bool ok = tile_map(h, &p.tmap_x, a->x, a->T, a->K, x_stride, bn);
+  const int nk = (a->K + 63) / 64;
+  if (active) {
+    const uint8_t* Ap = static_cast<const uint8_t*>(a->adapters);
+    LinearParams q = p;
+    ok = ok && tile_map(h, &q.tmap_w, Ap, Rs, a->K, a->K, 128);
+    q.N = q.Rs = Rs;
+    q.y = u;
+    q.ldy = ldu;
+    q.window = bn;
+    q.check_slots = 1;
+    if (!ok) return MOE_LORA_ERR_INVALID_ARG;
+    const long long tiles = static_cast<long long>((Rs + 127) / 128) * p.token_tiles;
+    ML_LAUNCH(h, launch_linear_narrow(q, kLinShrink, bn, pick_split(tiles, nk, h->num_sms), stream, false),
+              "linear shrink launch");
+    p.Rs = Rs;
+    ok = tile_map(h, &p.tmap_b, Ap + align256(static_cast<size_t>(Rs) * a->K * 2), a->N, Rs, Rs, 128) &&
+         tile_map(h, &p.tmap_u, u, a->T, ldu, ldu, bn);
+  } else {
+    p.check_slots = 1;
+  }
+  ok = ok && tile_map(h, &p.tmap_w, a->w, a->N, a->K, w_stride, 128);
+  if (!ok) return MOE_LORA_ERR_INVALID_ARG;
+  p.N = a->N;
+  p.bias = a->bias;
+  p.y = a->y;
+  p.ldy = a->T > 1 ? a->y_stride : a->N;
+  p.y_f32 = a->y_f32 != 0;
+  p.y_vec = p.ldy % 4 == 0 && (reinterpret_cast<uintptr_t>(a->y) & (p.y_f32 ? 15u : 7u)) == 0;
+  const long long tiles = static_cast<long long>((a->N + 127) / 128) * p.token_tiles;
+  ML_LAUNCH(h, launch_linear_narrow(p, kLinOut, bn, pick_split(tiles, nk, h->num_sms), stream, active),
+            "linear launch");
+  return MOE_LORA_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,400 @@
+// Projection with per-token adapters, tiles of 128 weight rows x BN tokens (moe_lora_linear):
+//
+//   y[t, n] = sum_k W[n, k] x[t, k] + sum_c Bs[n, c] u[t, c] (+ bias[n])
+//   u[t, c] = scaling[s] sum_k As[c, k] x[t, k]  where column c belongs to the token's slot s,
+//             and 0 elsewhere
+//
+// with every slot's A rows and B columns stacked side by side (As [Rs, K], Bs [N, Rs]), so
+// adapters of any ranks and number are one more K range of the same product.  The shrink (u)
+// is this kernel too, with As in the place of W and an epilogue that scales, masks and rounds.
+//
+// The weights are the MMA's M = 128 operand and the tokens its N = BN, so a batch of one token
+// still streams whole weight rows.  A cluster of CTAs shares a tile: each takes a part of K
+// into its own TMEM accumulator, parks the float32 part sums in its shared memory, and the
+// cluster adds them through distributed shared memory in rank order (a fixed order, so results
+// do not vary from run to run), each CTA writing its share of the tile.  That keeps enough
+// CTAs streaming when N alone gives few tiles, in one launch and without global partial sums.
+//
+// The product runs as a programmatic dependent of the shrink: it streams W and x at once and
+// waits for u only in front of the adapter blocks, which come last.  64-column blocks of the
+// stack in which no token of the tile has its adapter are skipped.
+//
+// Warp 0: TMA producer; warp 1: MMA issuer; warps 2-5: slots of the tile's tokens, epilogue.
+// Every wait is bounded; a timeout raises the CTA's abort flag, is recorded in the status
+// word, and every role still walks through the cluster barriers to the end.
+#include "common.cuh"
+#include "linear.h"
+
+namespace mlk {
+
+namespace {
+
+constexpr int kThreads = 192;
+constexpr int kABytes = 128 * 128;
+constexpr int kSmemBudget = 112 * 1024;   // two CTAs per SM
+constexpr int kMaxSplit = kLinearMaxSplit;
+
+__host__ __device__ constexpr int stage_bytes(int bn) { return kABytes + bn * 128; }
+__host__ __device__ constexpr int stages_of(int bn) { return (kSmemBudget - 2048) / stage_bytes(bn); }
+constexpr int smem_bytes(int bn) { return 1024 + stages_of(bn) * stage_bytes(bn) + 512; }
+
+// Four floats at this CTA's shared address `at`, in CTA `rank` of the cluster.
+MLDEV float4 ld_cluster_f4(uint32_t at, int rank) {
+  float4 v;
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\t"
+      "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+      : "r"(at), "r"(rank)
+      : "memory");
+  return v;
+}
+MLDEV uint32_t cluster_nctas() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+
+template <int BN, int MODE>
+__global__ void __launch_bounds__(kThreads, 2) linear_narrow_kernel(const __grid_constant__ LinearParams p) {
+  constexpr int kStages = stages_of(BN);
+  constexpr uint32_t STAGE = stage_bytes(BN);
+  constexpr uint32_t TMEM_COLS = BN <= 32 ? 32u : static_cast<uint32_t>(BN);
+  static_assert(kStages * static_cast<int>(STAGE) >= BN * 128 * 4, "the part sums fit the stage buffers");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * STAGE);
+  uint64_t* empty = full + kStages;
+  uint64_t* tfull = empty + kStages;
+  uint64_t* mask_bar = tfull + 1;
+  uint64_t* drain = mask_bar + 1;
+  uint32_t* mask_s = reinterpret_cast<uint32_t*>(drain + 1);   // [2] adapter blocks present in the tile
+  uint32_t* tmem_slot = mask_s + 2;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int C = static_cast<int>(cluster_nctas()), rank = static_cast<int>(cluster_ctarank());
+  const int tile = static_cast<int>(blockIdx.x) / C;
+  const int nt = tile / p.token_tiles, qt = tile - nt * p.token_tiles;
+  const int row0 = nt * 128, t0 = qt * BN;
+  const int nk = (p.K + 63) >> 6;
+  const int k_lo = static_cast<int>(static_cast<long long>(nk) * rank / C);
+  const int k_hi = static_cast<int>(static_cast<long long>(nk) * (rank + 1) / C);
+  const bool lora = MODE == kLinOut && p.Rs > 0;
+
+  // the 64-column blocks of the stack that slot sl's adapter lies in
+  auto blocks_of = [&](int sl) -> uint64_t {
+    if (sl < 0 || sl >= p.slots.S || p.slots.hi[sl] <= p.slots.lo[sl]) return 0ull;
+    const int b0 = p.slots.lo[sl] >> 6, b1 = (p.slots.hi[sl] - 1) >> 6;
+    return (~0ull >> (63 - b1)) & (~0ull << b0);
+  };
+
+  if constexpr (MODE == kLinShrink) {
+    pdl_trigger();   // the product may start: it waits for this grid's end itself
+    if (p.N > 128 && (tile > 0 || !p.check_slots)) {
+      // a stack of several row tiles: leave out those that no token of the window needs (the
+      // whole cluster decides alike; a tile that writes the status word stays)
+      const int w0 = t0 / p.window * p.window;
+      uint64_t m = 0;
+      for (int j = threadIdx.x; j < p.window && w0 + j < p.T; j += kThreads) m |= blocks_of(p.slot_idx[w0 + j]);
+      if (!__syncthreads_or(((m >> (row0 >> 6)) & 3ull) != 0)) return;
+    }
+  }
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(tfull, 1);
+    mbar_init(mask_bar, 128);
+    mbar_init(drain, 1);
+    mask_s[0] = mask_s[1] = 0u;
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&p.tmap_w);
+    tma_prefetch_desc(&p.tmap_x);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  if (warp == 0) {   // ------------------------------------------------ TMA producer
+    if (lane == 0) {
+      const uint64_t pol_w = l2_policy_evict_first(), pol_x = l2_policy_evict_last();
+      int stage = 0, ok = 1;
+      uint32_t phase = 0, issued = 0, parity = 0;
+      auto issue = [&](const CUtensorMap* wm, int kw, const CUtensorMap* xm, int kx) -> bool {
+        if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status, kWhereLinear)) return false;
+        uint8_t* a = smem + stage * STAGE;
+        mbar_arrive_expect_tx(&full[stage], STAGE);
+        tma_load_2d(a, wm, &full[stage], kw, row0, p.token_tiles == 1 ? pol_w : pol_x);
+        tma_load_2d(a + kABytes, xm, &full[stage], kx, t0, pol_x);
+        issued |= 1u << stage;
+        parity = (parity & ~(1u << stage)) | (phase << stage);
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+        return true;
+      };
+      for (int kb = k_lo; ok && kb < k_hi; ++kb) ok = issue(&p.tmap_w, kb * 64, &p.tmap_x, kb * 64);
+      if (ok && lora) {
+        ok = mbar_wait(mask_bar, 0, abort_flag, p.status, kWhereLinear);
+        const uint64_t mask = mask_s[0] | (static_cast<uint64_t>(mask_s[1]) << 32);
+        if (ok && mask) {
+          pdl_wait();   // u is written
+          int i = 0;
+          for (int piece = 0; piece < p.pieces; ++piece)
+            for (uint64_t m = mask; ok && m; m &= m - 1, ++i)
+              if (i % C == C - 1 - rank) {
+                const int c = (__ffsll(static_cast<long long>(m)) - 1) * 64;
+                ok = issue(&p.tmap_b, c, &p.tmap_u, piece * p.Rs + c);
+              }
+        }
+      }
+      if (!ok)
+        for (int s = 0; s < kStages; ++s)
+          if ((issued >> s) & 1u) mbar_wait_drain(&full[s], (parity >> s) & 1u);
+    }
+  } else if (warp == 1) {   // ------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(128, BN);
+      int stage = 0, ok = 1, first = 1;
+      uint32_t phase = 0;
+      auto consume = [&]() -> bool {
+        if (!mbar_wait(&full[stage], phase, abort_flag, p.status, kWhereLinear)) return false;
+        tc_fence_after();
+        const uint32_t a = smem_u32(smem + stage * STAGE);
+        const uint64_t ad = sw128_kmajor_desc(a), bd = sw128_kmajor_desc(a + kABytes);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          umma_bf16(tmem_base, ad + 2 * kk, bd + 2 * kk, idesc, first ? 0u : 1u);
+          first = 0;
+        }
+        umma_commit(&empty[stage]);
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+        return true;
+      };
+      for (int kb = k_lo; ok && kb < k_hi; ++kb) ok = consume();
+      if (ok && lora) {
+        ok = mbar_wait(mask_bar, 0, abort_flag, p.status, kWhereLinear);
+        const int n = __popc(mask_s[0]) + __popc(mask_s[1]);
+        for (int i = 0; ok && i < p.pieces * n; ++i)
+          if (i % C == C - 1 - rank) ok = consume();
+      }
+      if (ok) {
+        umma_commit(tfull);
+      } else {   // let what was issued finish before TMEM is released
+        umma_commit(drain);
+        mbar_wait_drain(drain, 0);
+      }
+    }
+  } else {   // ---------------------------------------------- slots, then TMEM -> shared memory
+    const int et = threadIdx.x - 64;
+    if (lora) {
+      uint64_t m = 0;
+      for (int j = et; j < BN && t0 + j < p.T; j += 128) m |= blocks_of(p.slot_idx[t0 + j]);
+      if (static_cast<uint32_t>(m)) atomicOr(&mask_s[0], static_cast<uint32_t>(m));
+      if (static_cast<uint32_t>(m >> 32)) atomicOr(&mask_s[1], static_cast<uint32_t>(m >> 32));
+      mbar_arrive(mask_bar);
+    }
+    if (p.check_slots && blockIdx.x == 0) {   // the only writer of the status word before a timeout
+      int bad = 0;
+      if (p.slot_idx != nullptr)
+        for (int t = et; t < p.T; t += 128) {
+          const int sl = p.slot_idx[t];
+          bad |= sl < -1 || sl >= p.slots.S;
+        }
+      int any;
+      asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 2, 128, p;\n\t"
+                   "selp.u32 %0, 1, 0, q;\n\t}"
+                   : "=r"(any)
+                   : "r"(bad)
+                   : "memory");
+      if (et == 0) *p.status = any ? (kDevBadSlot | (kWhereLinear << 8)) : 0u;
+    }
+    const int quarter = warp & 3;
+    const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
+    float* part = reinterpret_cast<float*>(smem) + quarter * 32 + lane;   // [BN][128]
+    if (mbar_wait_sleep(tfull, 0, abort_flag, p.status, kWhereLinear)) {
+      tc_fence_after();
+#pragma unroll 1
+      for (int c = 0; c < BN && t0 + c < p.T; c += 16) {   // warp-uniform bound
+        uint32_t v[16];
+        __syncwarp();   // tcgen05.ld is .aligned
+        tmem_ld_x16(taddr + c, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) part[(c + j) * 128] = __uint_as_float(v[j]);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncwarp();
+  cluster_arrive();
+  cluster_wait();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, TMEM_COLS);
+  }
+
+  if (lora) pdl_wait();   // nothing of this grid is written before the shrink has ended
+
+  // this CTA's share of the tile: quads of 4 rows of a token, part sums added in rank order
+  const int nvalid = min(BN, p.T - t0);
+  const int quads = nvalid * 32;
+  const int q_lo = static_cast<int>(static_cast<long long>(quads) * rank / C);
+  const int q_hi = static_cast<int>(static_cast<long long>(quads) * (rank + 1) / C);
+  const uint32_t part0 = smem_u32(smem);
+  for (int q = q_lo + static_cast<int>(threadIdx.x); q < q_hi; q += kThreads) {
+    const int j = q >> 5, r = (q & 31) * 4;
+    const int t = t0 + j, n = row0 + r;
+    if (n >= p.N) continue;
+    float4 v[kMaxSplit];
+#pragma unroll
+    for (int c = 0; c < kMaxSplit; ++c)   // all in flight together
+      if (c < C) v[c] = ld_cluster_f4(part0 + static_cast<uint32_t>(q) * 16u, c);
+    float f[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+    for (int c = 1; c < kMaxSplit; ++c)
+      if (c < C) {
+        f[0] += v[c].x;
+        f[1] += v[c].y;
+        f[2] += v[c].z;
+        f[3] += v[c].w;
+      }
+    if constexpr (MODE == kLinShrink) {
+      const int sl = p.slot_idx[t];
+      const bool has = sl >= 0 && sl < p.slots.S;
+      const int lo = has ? p.slots.lo[sl] : 0, hi = has ? p.slots.hi[sl] : 0;
+      const float sc = has ? p.slots.scal[sl] : 0.0f;
+      __nv_bfloat16* u = static_cast<__nv_bfloat16*>(p.y) + static_cast<long long>(t) * p.ldy + n;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] = (n + i >= lo && n + i < hi) ? sc * f[i] : 0.0f;
+      for (int piece = 0; piece < p.pieces; ++piece) {   // the float32 as a sum of bf16 pieces
+        const uint2 v = pack4(f);
+        *reinterpret_cast<uint2*>(u + static_cast<long long>(piece) * p.Rs) = v;
+        f[0] -= __uint_as_float(v.x << 16);
+        f[1] -= __uint_as_float(v.x & 0xffff0000u);
+        f[2] -= __uint_as_float(v.y << 16);
+        f[3] -= __uint_as_float(v.y & 0xffff0000u);
+      }
+    } else {
+      if (p.bias != nullptr) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (n + i < p.N) f[i] += __ldg(p.bias + n + i);
+      }
+      const long long at = static_cast<long long>(t) * p.ldy + n;
+      if (p.y_vec && n + 4 <= p.N) {
+        if (p.y_f32) *reinterpret_cast<float4*>(static_cast<float*>(p.y) + at) = make_float4(f[0], f[1], f[2], f[3]);
+        else *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.y) + at) = pack4(f);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (n + i < p.N) {
+            if (p.y_f32) static_cast<float*>(p.y)[at + i] = f[i];
+            else static_cast<__nv_bfloat16*>(p.y)[at + i] = f2bf(f[i]);
+          }
+      }
+    }
+  }
+  if (C > 1) {   // no CTA leaves while others read its part sums
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+  }
+}
+
+template <int BN, int MODE>
+cudaError_t setup_one() {
+  return cudaFuncSetAttribute(linear_narrow_kernel<BN, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              smem_bytes(BN));
+}
+
+template <int MODE>
+cudaError_t launch_mode(const LinearParams& p, int bn, int split, cudaStream_t stream, bool pdl) {
+  const long long tiles = static_cast<long long>((p.N + 127) / 128) * p.token_tiles;
+  if (tiles * split > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>(tiles * split)), block(kThreads);
+  switch (bn) {
+    case 16: return launch_kc(linear_narrow_kernel<16, MODE>, grid, block, smem_bytes(16), stream, pdl, split, p);
+    case 32: return launch_kc(linear_narrow_kernel<32, MODE>, grid, block, smem_bytes(32), stream, pdl, split, p);
+    case 64: return launch_kc(linear_narrow_kernel<64, MODE>, grid, block, smem_bytes(64), stream, pdl, split, p);
+    case 128: return launch_kc(linear_narrow_kernel<128, MODE>, grid, block, smem_bytes(128), stream, pdl, split, p);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+// Stacked copies of the adapters: As [Rs, K] (blocks below gridDim.y = 0) and Bs [N, Rs].
+// Ranks past a slot's own are never read; columns of no slot are zero.
+__global__ void __launch_bounds__(256) linear_pack_kernel(const __grid_constant__ LinearPackParams p) {
+  const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+  auto slot_of = [&](int c) -> int {   // the slot whose columns hold c (p.S: past the last)
+    int lo = 0, hi = p.S;
+    while (lo < hi) {   // first s with lo[s + 1] > c
+      const int mid = (lo + hi) >> 1;
+      if (p.lo[mid + 1] > c) hi = mid; else lo = mid + 1;
+    }
+    return lo;
+  };
+  if (blockIdx.y == 0) {   // 8 values of a row of As
+    const int per = p.K >> 3;
+    if (i >= static_cast<long long>(p.Rs) * per) return;
+    const int c = static_cast<int>(i / per), k = static_cast<int>(i - static_cast<long long>(c) * per) * 8;
+    const int s = slot_of(c);
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (s < p.S && c - p.lo[s] < p.ranks[s])
+      v = *reinterpret_cast<const uint4*>(p.A + (static_cast<long long>(s) * p.R + c - p.lo[s]) * p.K + k);
+    *reinterpret_cast<uint4*>(p.Ap + static_cast<long long>(c) * p.K + k) = v;
+  } else {   // one value of Bs
+    if (i >= static_cast<long long>(p.N) * p.Rs) return;
+    const long long n = i / p.Rs;
+    const int c = static_cast<int>(i - n * p.Rs);
+    const int s = slot_of(c);
+    __nv_bfloat16 v = __float2bfloat16_rn(0.0f);
+    if (s < p.S && c - p.lo[s] < p.ranks[s]) v = p.B[(static_cast<long long>(s) * p.N + n) * p.R + c - p.lo[s]];
+    p.Bp[i] = v;
+  }
+}
+
+}  // namespace
+
+cudaError_t linear_narrow_setup() {
+  cudaError_t err;
+#define ML_SETUP(BN)                                                              \
+  if ((err = setup_one<BN, kLinOut>()) != cudaSuccess) return err;                \
+  if ((err = setup_one<BN, kLinShrink>()) != cudaSuccess) return err;
+  ML_SETUP(16)
+  ML_SETUP(32)
+  ML_SETUP(64)
+  ML_SETUP(128)
+#undef ML_SETUP
+  return cudaSuccess;
+}
+
+cudaError_t launch_linear_narrow(const LinearParams& p, int mode, int bn, int split, cudaStream_t stream, bool pdl) {
+  return mode == kLinShrink ? launch_mode<kLinShrink>(p, bn, split, stream, pdl)
+                            : launch_mode<kLinOut>(p, bn, split, stream, pdl);
+}
+
+cudaError_t launch_linear_pack(const LinearPackParams& p, cudaStream_t stream) {
+  const long long a = static_cast<long long>(p.Rs) * (p.K / 8), b = static_cast<long long>(p.N) * p.Rs;
+  const long long most = a > b ? a : b;
+  const dim3 grid(static_cast<unsigned>((most + 255) / 256), 2);
+  return launch_k(linear_pack_kernel, grid, dim3(256), 0, stream, false, p);
+}
+
+}  // namespace mlk

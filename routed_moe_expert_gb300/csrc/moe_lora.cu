@@ -15,6 +15,7 @@
 // before the fork, so nothing is allocated while a graph may be capturing (the
 // multi-slot replay bug of sglang PR #28091, Motivation 3, cannot arise).
 #include "../../include/moe_lora.h"
+#include "host.h"
 #include "kernels.h"
 
 #include <algorithm>
@@ -24,7 +25,7 @@
 
 using namespace mlk;
 
-namespace {
+namespace mlk {
 
 thread_local char g_last_cuda_error[256] = "";
 
@@ -33,22 +34,9 @@ moe_lora_status cuda_fail(cudaError_t err, const char* what) {
   return MOE_LORA_ERR_CUDA;
 }
 
-#define ML_CUDA(call, what)                         \
-  do {                                              \
-    cudaError_t _e = (call);                        \
-    if (_e != cudaSuccess) return cuda_fail(_e, what); \
-  } while (0)
+}  // namespace mlk
 
-// A launch of one of this library's kernels, counted on the handle (moe_lora_launch_count).
-#define ML_LAUNCH(h, call, what)                    \
-  do {                                              \
-    ML_CUDA(call, what);                            \
-    ++(h)->launches;                                \
-  } while (0)
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+namespace {
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
@@ -101,9 +89,6 @@ Layout layout_for(int T, int H, int I, int E, int k, int R, int S) {
   return L;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-
 moe_lora_status check_routing_args(int T, int E, int top_k, int method, const void* logits, const float* bias,
                                    int n_group, int topk_group) {
   if (T < 0 || E < 1 || E > kMaxExperts) return MOE_LORA_ERR_INVALID_ARG;
@@ -126,16 +111,6 @@ bool lora_active(const moe_lora_args* a) {
 }
 
 }  // namespace
-
-struct moe_lora_handle {
-  int device = 0;
-  int num_sms = 0;
-  cudaStream_t side = nullptr;
-  cudaEvent_t ev_fork = nullptr, ev_ready = nullptr;
-  EncodeTiledFn encode = nullptr;
-  int coop_ctas[kMaxExperts + 1];   // cache of route_max_coop_ctas by E (0 = unknown)
-  uint64_t launches = 0;             // kernels launched through this handle
-};
 
 extern "C" {
 
