@@ -515,7 +515,7 @@ moe_lora_status moe_lora_linear_workspace_size(int T, int S, const int32_t* h_ra
    bits) for a float32 y.  Two launches (shrink, then the product, which starts beside it), one
    without active adapters.  `workspace` (16-byte aligned, contents on entry do not matter)
    starts with the status word that moe_lora_check_status reads: DEVICE_CHECK when a slot index
-   lies outside [-1, S) (such a token gets no adapter), TIMEOUT when a bounded wait ran out.
+   lies outside [-1, S) (such a token gets no adapter; checked when some slot is active), TIMEOUT when a bounded wait ran out.
    Errors: INVALID_ARG, UNSUPPORTED (more than 4096 stacked ranks), WORKSPACE_TOO_SMALL, CUDA. */
 moe_lora_status moe_lora_linear(moe_lora_handle* h, const moe_lora_linear_args* a, void* workspace,
                                 size_t workspace_bytes, moe_lora_stream stream);

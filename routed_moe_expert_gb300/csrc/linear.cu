@@ -3,6 +3,7 @@
 #include "linear.h"
 #include "host.h"
 
+#include <algorithm>
 #include <cstring>
 
 using namespace mlk;
@@ -42,14 +43,35 @@ bool tile_map(const moe_lora_handle* h, CUtensorMap* m, const void* base, long l
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int token_tile(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128; }
-
 // CTAs that share a tile's K: as many as keep the grid at two CTAs per SM, each with at least
 // four 64-wide K blocks.
 int pick_split(long long tiles, int nk, int sms) {
   int split = 1;
   while (split < kLinearMaxSplit && tiles * split * 2 <= 2LL * sms && nk / (split * 2) >= 4) split *= 2;
   return split;
+}
+
+struct Tiles {
+  bool wide;        // CTA pairs, 256 tokens x `rows` weight rows
+  int tokens;       // token tile
+  int rows;         // weight rows of a tile
+  int split;        // (narrow) CTAs that share a tile's K
+};
+
+Tiles pick_tiles(int T, int N, int K, bool f32, int sms) {
+  const int nk = (K + 63) / 64;
+  Tiles c = {false, T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128, 128, 1};
+  const long long tiles = static_cast<long long>((N + 127) / 128) * ((T + c.tokens - 1) / c.tokens);
+  c.split = pick_split(tiles, nk, sms);
+  if (f32) {
+    // The tensor cores truncate as they accumulate, which adds up over a long K: a float32 result
+    // takes at most 1024 of K per accumulator (while the cluster allows it), whatever the grid.
+    while (c.split < kLinearMaxSplit && nk > 16 * c.split) c.split *= 2;
+    return c;
+  }
+  const long long t256 = (T + 255) / 256;
+  if (t256 * ((N + 255) / 256) >= sms / 2) return {true, 256, 256, 1};
+  return c;
 }
 
 }  // namespace
@@ -148,51 +170,60 @@ moe_lora_status moe_lora_linear(moe_lora_handle* h, const moe_lora_linear_args* 
   if (active && (a->adapters == nullptr || !aligned16(a->adapters))) return MOE_LORA_ERR_INVALID_ARG;
   if (!h->linear_ready) {
     ML_CUDA(linear_narrow_setup(), "linear setup");
+    ML_CUDA(linear_wide_setup(), "linear setup");
     h->linear_ready = true;
   }
 
-  const int bn = token_tile(a->T);
+  const Tiles c = pick_tiles(a->T, a->N, a->K, a->y_f32 != 0, h->num_sms);
   p.T = a->T;
   p.K = a->K;
-  p.slot_idx = a->slot_idx;
+  p.slot_idx = active ? a->slot_idx : nullptr;
   p.status = static_cast<uint32_t*>(workspace);
-  p.token_tiles = (a->T + bn - 1) / bn;
   p.pieces = a->y_f32 ? kFloatPieces : 1;
   void* u = static_cast<uint8_t*>(workspace) + 256;
   const long long ldu = static_cast<long long>(p.pieces) * Rs;
   const long long x_stride = a->T > 1 ? a->x_stride : a->K, w_stride = a->N > 1 ? a->w_stride : a->K;
-  bool ok = tile_map(h, &p.tmap_x, a->x, a->T, a->K, x_stride, bn);
+  const int x_box = c.wide ? 128 : c.tokens, w_box = c.wide ? c.rows / 2 : 128;
   const int nk = (a->K + 63) / 64;
+  bool ok = tile_map(h, &p.tmap_x, a->x, a->T, a->K, x_stride, x_box);
   if (active) {
     const uint8_t* Ap = static_cast<const uint8_t*>(a->adapters);
+    const int bn = std::min(c.tokens, 128);   // the shrink's token tile
     LinearParams q = p;
     ok = ok && tile_map(h, &q.tmap_w, Ap, Rs, a->K, a->K, 128);
     q.N = q.Rs = Rs;
     q.y = u;
     q.ldy = ldu;
-    q.window = bn;
+    q.window = c.tokens;
     q.check_slots = 1;
+    q.token_tiles = (a->T + bn - 1) / bn;
     if (!ok) return MOE_LORA_ERR_INVALID_ARG;
-    const long long tiles = static_cast<long long>((Rs + 127) / 128) * p.token_tiles;
+    const long long tiles = static_cast<long long>((Rs + 127) / 128) * q.token_tiles;
     ML_LAUNCH(h, launch_linear_narrow(q, kLinShrink, bn, pick_split(tiles, nk, h->num_sms), stream, false),
               "linear shrink launch");
     p.Rs = Rs;
-    ok = tile_map(h, &p.tmap_b, Ap + align256(static_cast<size_t>(Rs) * a->K * 2), a->N, Rs, Rs, 128) &&
-         tile_map(h, &p.tmap_u, u, a->T, ldu, ldu, bn);
+    ok = tile_map(h, &p.tmap_b, Ap + align256(static_cast<size_t>(Rs) * a->K * 2), a->N, Rs, Rs, w_box) &&
+         tile_map(h, &p.tmap_u, u, a->T, ldu, ldu, x_box);
   } else {
     p.check_slots = 1;
   }
-  ok = ok && tile_map(h, &p.tmap_w, a->w, a->N, a->K, w_stride, 128);
-  if (!ok) return MOE_LORA_ERR_INVALID_ARG;
+  ok = ok && tile_map(h, &p.tmap_w, a->w, a->N, a->K, w_stride, w_box);
   p.N = a->N;
   p.bias = a->bias;
   p.y = a->y;
   p.ldy = a->T > 1 ? a->y_stride : a->N;
   p.y_f32 = a->y_f32 != 0;
-  p.y_vec = p.ldy % 4 == 0 && (reinterpret_cast<uintptr_t>(a->y) & (p.y_f32 ? 15u : 7u)) == 0;
-  const long long tiles = static_cast<long long>((a->N + 127) / 128) * p.token_tiles;
-  ML_LAUNCH(h, launch_linear_narrow(p, kLinOut, bn, pick_split(tiles, nk, h->num_sms), stream, active),
-            "linear launch");
+  p.token_tiles = (a->T + c.tokens - 1) / c.tokens;
+  if (c.wide) {
+    p.y_vec = p.ldy % 8 == 0 && aligned16(a->y) && p.ldy <= kMaxStride;
+    if (p.y_vec) ok = ok && tile_map(h, &p.tmap_y, a->y, a->T, a->N, p.ldy, 32);
+    if (!ok) return MOE_LORA_ERR_INVALID_ARG;
+    ML_LAUNCH(h, launch_linear_wide(p, c.rows, h->num_sms, stream, active), "linear launch");
+  } else {
+    p.y_vec = p.ldy % 4 == 0 && (reinterpret_cast<uintptr_t>(a->y) & (p.y_f32 ? 15u : 7u)) == 0;
+    if (!ok) return MOE_LORA_ERR_INVALID_ARG;
+    ML_LAUNCH(h, launch_linear_narrow(p, kLinOut, c.tokens, c.split, stream, active), "linear launch");
+  }
   return MOE_LORA_OK;
 }
 

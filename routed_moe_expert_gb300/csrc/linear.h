@@ -22,6 +22,7 @@ struct LinearParams {
   CUtensorMap tmap_x;    // [T, K] box {64, token tile}
   CUtensorMap tmap_b;    // [N, Rs] box {64, 128}: the stacked B
   CUtensorMap tmap_u;    // [T, pieces * Rs] box {64, token tile}: the shrunk rows
+  CUtensorMap tmap_y;    // (wide tiles, y_vec) [T, N] box {64, 32}
   int T, N, K;           // N: rows of tmap_w that count
   int Rs;                // stacked columns, a multiple of 64 (0: no adapters)
   int pieces;            // 1, or kFloatPieces bf16 pieces of a float32 u
@@ -31,7 +32,8 @@ struct LinearParams {
   void* y;               // [T, ldy] bf16 or float32; the shrink writes u [T, pieces * Rs] bf16
   long long ldy;
   int y_f32;
-  int y_vec;             // rows of y start on 4-value boundaries (vector stores)
+  int y_vec;             // rows of y start on 4-value boundaries (vector stores); wide tiles: on
+                         // 16-byte boundaries (TMA stores)
   int token_tiles;
   int check_slots;       // this launch writes the status word (first CTA)
   uint32_t* status;
@@ -45,6 +47,11 @@ enum { kLinOut = 0, kLinShrink = 1 };
 constexpr int kLinearMaxSplit = 8;
 cudaError_t linear_narrow_setup();   // once per device
 cudaError_t launch_linear_narrow(const LinearParams& p, int mode, int bn, int split, cudaStream_t stream, bool pdl);
+
+// Tiles of 256 tokens x bn (128 or 256) weight rows on CTA pairs, bf16 y; the maps' boxes are
+// {64, 128} tokens and {64, bn / 2} weight rows.
+cudaError_t linear_wide_setup();
+cudaError_t launch_linear_wide(const LinearParams& p, int bn, int sms, cudaStream_t stream, bool pdl);
 
 struct LinearPackParams {
   const __nv_bfloat16 *A, *B;   // [S, R, K], [S, N, R]

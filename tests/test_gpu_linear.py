@@ -81,6 +81,15 @@ def test_widths(handle, T, N, K):
     _check(_run(handle, c := _case(T, N, K, (), seed=N + T, bias=True), True), c, True)
 
 
+@pytest.mark.parametrize("T,N,K", [(2500, 2050, 136), (2560, 2048, 512), (5121, 1000, 72), (19500, 130, 64), (1281, 4096, 264)])
+@pytest.mark.parametrize("slots", ["mixed", "runs", "none", None])
+def test_long_batches(handle, T, N, K, slots):
+    """Enough tokens for the widest tiles: ragged in every direction, rows of y on and off 16-byte
+    boundaries, adapters of several 64-column blocks."""
+    c = _case(T, N, K, (16, 40, 64, 5) if slots else (), seed=T, bias=N % 2 == 0, slots=slots or "none")
+    _check(_run(handle, c), c)
+
+
 @pytest.mark.parametrize("ranks", [(1,), (128,), (0, 8), (64, 64, 64), (8, 16, 32, 64), (16,) * 40, (64,) * 64],
                          ids=lambda r: f"{len(r)}x{max(r)}")
 @pytest.mark.parametrize("T,slots", [(5, "mixed"), (200, "mixed"), (500, "runs"), (40, "none")])
@@ -101,7 +110,7 @@ def test_factors_of_zero_and_all_ranks_zero(handle):
     _check(_run(handle, c), c)
 
 
-@pytest.mark.parametrize("T", [1, 20, 150, 700])
+@pytest.mark.parametrize("T", [1, 20, 150, 700, 19700])
 @pytest.mark.parametrize("f32", [False, True], ids=["bf16", "fp32"])
 def test_strided_rows_and_nothing_else_written(handle, T, f32):
     """Rows of x and w inside wider tensors, the result as a column range of a wider tensor, from
@@ -148,7 +157,7 @@ def test_same_bits_every_time_and_on_other_streams(handle):
 
 
 def test_graph_replay_on_new_inputs(handle):
-    for T in (4, 600):
+    for T in (4, 600, 10000):
         c = _case(T, 264, 512, (8, 16), seed=T)
         ad = pkg.moe_lora_linear_adapters(handle, c["A"].cuda(), c["B"].cuda(), c["ranks"], c["scalings"])
         x, w, slots = c["x"].cuda(), c["w"].cuda(), c["slots"].cuda()
