@@ -115,6 +115,18 @@ MLDEV void build_tile_schedule(const int32_t* offsets, int E, int tile, int mult
   if (lane == 0) tile_start[E] = carry;
 }
 
+// Whether any of 128 threads (four whole warps, named barrier 2) brings a nonzero value.
+MLDEV bool any_of_128(int value) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 2, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(value)
+      : "memory");
+  return any != 0;
+}
+
 MLDEV uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }

@@ -20,6 +20,7 @@ struct moe_lora_handle {
   EncodeTiledFn encode = nullptr;
   int coop_ctas[mlk::kMaxExperts + 1];   // cache of route_max_coop_ctas by E (0 = unknown)
   uint64_t launches = 0;                  // kernels launched through this handle
+  int2* linear_flags = nullptr;            // flags of the projection kernels, zero between calls
   bool linear_ready = false;              // the projection kernels have their shared memory limits
 };
 

@@ -43,14 +43,6 @@ bool tile_map(const moe_lora_handle* h, CUtensorMap* m, const void* base, long l
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// CTAs that share a tile's K: as many as keep the grid at two CTAs per SM, each with at least
-// four 64-wide K blocks.
-int pick_split(long long tiles, int nk, int sms) {
-  int split = 1;
-  while (split < kLinearMaxSplit && tiles * split * 2 <= 2LL * sms && nk / (split * 2) >= 4) split *= 2;
-  return split;
-}
-
 struct Tiles {
   bool wide;        // CTA pairs, 256 tokens x `rows` weight rows
   int tokens;       // token tile
@@ -58,20 +50,46 @@ struct Tiles {
   int split;        // (narrow) CTAs that share a tile's K
 };
 
-Tiles pick_tiles(int T, int N, int K, bool f32, int sms) {
+// Microseconds of a product on narrow tiles, a model fitted to measured calls (T 1 to 2048, N 384
+// to 5120, K 2048 and 7168): launch, first bytes and epilogue; the bytes that an SM's shared memory
+// takes in, at 75 GB/s for one CTA and 115 GB/s for two; the sum over a cluster.
+double narrow_us(int T, int N, int nk, int bn, int split, int sms) {
+  const long long ctas = static_cast<long long>((N + 127) / 128) * ((T + bn - 1) / bn) * split;
+  const double mb = (nk + split - 1) / split * (16.0 + bn / 8.0) * 1e-3;   // per CTA
+  const long long waves = (ctas + 2 * sms - 1) / (2 * sms);
+  double us = 4.2 + (bn / 128.0 * (split > 1 ? 1.2 : 0.6) + (split > 1 ? 0.4 : 0.0));
+  us += ctas <= sms ? mb / 0.075 : static_cast<double>(waves) * 2.0 * mb / 0.115 + 3.5 * static_cast<double>(waves - 1);
+  if (split == 8 && ctas > sms) us += 2.0;   // clusters of 8 do not pack two CTAs to an SM
+  return us;
+}
+// ... on pairs: a 64-deep K step of a 256 x 256 tile takes 0.3 us, a pair walks whole tiles.
+double wide_us(long long tiles, int nk, int sms) {
+  const long long waves = (tiles + sms / 2 - 1) / (sms / 2);
+  return 5.0 + 0.3 * static_cast<double>(waves) * nk;
+}
+
+Tiles pick_tiles(int T, int N, int K, bool f32, bool adapters, int sms) {
   const int nk = (K + 63) / 64;
-  Tiles c = {false, T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128, 128, 1};
-  const long long tiles = static_cast<long long>((N + 127) / 128) * ((T + c.tokens - 1) / c.tokens);
-  c.split = pick_split(tiles, nk, sms);
-  if (f32) {
-    // The tensor cores truncate as they accumulate, which adds up over a long K: a float32 result
-    // takes at most 1024 of K per accumulator (while the cluster allows it), whatever the grid.
-    while (c.split < kLinearMaxSplit && nk > 16 * c.split) c.split *= 2;
-    return c;
+  Tiles best = {false, 16, 128, 1};
+  double us = 1e30;
+  for (int bn = 16; bn <= 128; bn *= 2) {
+    if (bn > 16 && bn >= 2 * T) break;
+    for (int split = 1; split <= kLinearMaxSplit && split <= nk; split *= 2) {
+      // The tensor cores truncate as they accumulate, which adds up over a long K: a float32
+      // result takes at most 1024 of K per accumulator (as far as a cluster goes).
+      if (f32 && nk > 16 * split && split < kLinearMaxSplit && 2 * split <= nk) continue;
+      // the shrink runs at the product's pace, and its result then takes 4.5 us to come back in
+      const double t = narrow_us(T, N, nk, bn, split, sms) + (adapters ? 4.5 : 0.0);
+      if (t < us) {
+        us = t;
+        best = {false, bn, 128, split};
+      }
+    }
   }
-  const long long t256 = (T + 255) / 256;
-  if (t256 * ((N + 255) / 256) >= sms / 2) return {true, 256, 256, 1};
-  return c;
+  if (f32) return best;
+  const long long tiles = static_cast<long long>((T + 255) / 256) * ((N + 255) / 256);
+  if (T > 128 && wide_us(tiles, nk, sms) + (adapters ? 4.0 : 0.0) < us) best = {true, 256, 256, 1};
+  return best;
 }
 
 }  // namespace
@@ -174,55 +192,42 @@ moe_lora_status moe_lora_linear(moe_lora_handle* h, const moe_lora_linear_args* 
     h->linear_ready = true;
   }
 
-  const Tiles c = pick_tiles(a->T, a->N, a->K, a->y_f32 != 0, h->num_sms);
+  const Tiles c = pick_tiles(a->T, a->N, a->K, a->y_f32 != 0, active, h->num_sms);
   p.T = a->T;
   p.K = a->K;
   p.slot_idx = active ? a->slot_idx : nullptr;
   p.status = static_cast<uint32_t*>(workspace);
   p.pieces = a->y_f32 ? kFloatPieces : 1;
-  void* u = static_cast<uint8_t*>(workspace) + 256;
-  const long long ldu = static_cast<long long>(p.pieces) * Rs;
   const long long x_stride = a->T > 1 ? a->x_stride : a->K, w_stride = a->N > 1 ? a->w_stride : a->K;
   const int x_box = c.wide ? 128 : c.tokens, w_box = c.wide ? c.rows / 2 : 128;
-  const int nk = (a->K + 63) / 64;
-  bool ok = tile_map(h, &p.tmap_x, a->x, a->T, a->K, x_stride, x_box);
+  bool ok = tile_map(h, &p.tmap_x, a->x, a->T, a->K, x_stride, x_box) &&
+            tile_map(h, &p.tmap_w, a->w, a->N, a->K, w_stride, w_box);
+  p.token_tiles = (a->T + c.tokens - 1) / c.tokens;
   if (active) {
+    if (p.token_tiles > kLinearFlags) return MOE_LORA_ERR_UNSUPPORTED;
     const uint8_t* Ap = static_cast<const uint8_t*>(a->adapters);
-    const int bn = std::min(c.tokens, 128);   // the shrink's token tile
-    LinearParams q = p;
-    ok = ok && tile_map(h, &q.tmap_w, Ap, Rs, a->K, a->K, 128);
-    q.N = q.Rs = Rs;
-    q.y = u;
-    q.ldy = ldu;
-    q.window = c.tokens;
-    q.check_slots = 1;
-    q.token_tiles = (a->T + bn - 1) / bn;
-    if (!ok) return MOE_LORA_ERR_INVALID_ARG;
-    const long long tiles = static_cast<long long>((Rs + 127) / 128) * q.token_tiles;
-    ML_LAUNCH(h, launch_linear_narrow(q, kLinShrink, bn, pick_split(tiles, nk, h->num_sms), stream, false),
-              "linear shrink launch");
+    const uint8_t* Bp = Ap + align256(static_cast<size_t>(Rs) * a->K * 2);
     p.Rs = Rs;
-    ok = tile_map(h, &p.tmap_b, Ap + align256(static_cast<size_t>(Rs) * a->K * 2), a->N, Rs, Rs, w_box) &&
-         tile_map(h, &p.tmap_u, u, a->T, ldu, ldu, x_box);
-  } else {
-    p.check_slots = 1;
+    p.u = reinterpret_cast<__nv_bfloat16*>(static_cast<uint8_t*>(workspace) + 256);
+    p.flags = h->linear_flags;
+    const long long ldu = static_cast<long long>(p.pieces) * Rs;
+    ok = ok && tile_map(h, &p.tmap_a, Ap, Rs, a->K, a->K, c.wide ? linear_shrink_cols(Rs, c.rows) / 2 : 128) &&
+         tile_map(h, &p.tmap_b, Bp, a->N, Rs, Rs, w_box) && tile_map(h, &p.tmap_u, p.u, a->T, ldu, ldu, x_box);
   }
-  ok = ok && tile_map(h, &p.tmap_w, a->w, a->N, a->K, w_stride, w_box);
   p.N = a->N;
   p.bias = a->bias;
   p.y = a->y;
   p.ldy = a->T > 1 ? a->y_stride : a->N;
   p.y_f32 = a->y_f32 != 0;
-  p.token_tiles = (a->T + c.tokens - 1) / c.tokens;
   if (c.wide) {
     p.y_vec = p.ldy % 8 == 0 && aligned16(a->y) && p.ldy <= kMaxStride;
     if (p.y_vec) ok = ok && tile_map(h, &p.tmap_y, a->y, a->T, a->N, p.ldy, 32);
     if (!ok) return MOE_LORA_ERR_INVALID_ARG;
-    ML_LAUNCH(h, launch_linear_wide(p, c.rows, h->num_sms, stream, active), "linear launch");
+    ML_LAUNCH(h, launch_linear_wide(p, c.rows, h->num_sms, stream), "linear launch");
   } else {
     p.y_vec = p.ldy % 4 == 0 && (reinterpret_cast<uintptr_t>(a->y) & (p.y_f32 ? 15u : 7u)) == 0;
     if (!ok) return MOE_LORA_ERR_INVALID_ARG;
-    ML_LAUNCH(h, launch_linear_narrow(p, kLinOut, c.tokens, c.split, stream, active), "linear launch");
+    ML_LAUNCH(h, launch_linear_narrow(p, c.tokens, c.split, stream), "linear launch");
   }
   return MOE_LORA_OK;
 }

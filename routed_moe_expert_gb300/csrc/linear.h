@@ -18,40 +18,42 @@ struct LinearSlots {
 };
 
 struct LinearParams {
-  CUtensorMap tmap_w;    // [rows, K] box {64, 128}: weights, or the stacked A of the shrink
-  CUtensorMap tmap_x;    // [T, K] box {64, token tile}
-  CUtensorMap tmap_b;    // [N, Rs] box {64, 128}: the stacked B
-  CUtensorMap tmap_u;    // [T, pieces * Rs] box {64, token tile}: the shrunk rows
+  CUtensorMap tmap_w;    // weights [N, K]
+  CUtensorMap tmap_x;    // [T, K]
+  CUtensorMap tmap_a;    // the stacked A [Rs, K]
+  CUtensorMap tmap_b;    // the stacked B [N, Rs]
+  CUtensorMap tmap_u;    // the shrunk rows [T, pieces * Rs]
   CUtensorMap tmap_y;    // (wide tiles, y_vec) [T, N] box {64, 32}
-  int T, N, K;           // N: rows of tmap_w that count
+  int T, N, K;
   int Rs;                // stacked columns, a multiple of 64 (0: no adapters)
   int pieces;            // 1, or kFloatPieces bf16 pieces of a float32 u
-  int window;            // (shrink) tokens whose slots decide which stacked rows are needed
+  int token_tiles;
   const int32_t* slot_idx;
   const float* bias;     // [N] or null
-  void* y;               // [T, ldy] bf16 or float32; the shrink writes u [T, pieces * Rs] bf16
+  void* y;               // [T, ldy] bf16 or float32
+  __nv_bfloat16* u;      // [T, pieces * Rs]
   long long ldy;
   int y_f32;
   int y_vec;             // rows of y start on 4-value boundaries (vector stores); wide tiles: on
                          // 16-byte boundaries (TMA stores)
-  int token_tiles;
-  int check_slots;       // this launch writes the status word (first CTA)
-  uint32_t* status;
+  int2* flags;           // per token tile: {shrink parts done, product parts past them}; zero
+                         // between calls
+  uint32_t* status;      // written by the first CTA
   LinearSlots slots;
 };
-
-enum { kLinOut = 0, kLinShrink = 1 };
+constexpr int kLinearFlags = 8192;   // token tiles of a call with adapters
 
 // One 128-row x bn-token tile per cluster of `split` CTAs, which share the tile's K; split is at
-// most the number of 64-wide K blocks.
+// most the number of 64-wide K blocks.  Maps' boxes: {64, 128} of w, a, b, {64, bn} of x, u.
 constexpr int kLinearMaxSplit = 8;
 cudaError_t linear_narrow_setup();   // once per device
-cudaError_t launch_linear_narrow(const LinearParams& p, int mode, int bn, int split, cudaStream_t stream, bool pdl);
+cudaError_t launch_linear_narrow(const LinearParams& p, int bn, int split, cudaStream_t stream);
 
-// Tiles of 256 tokens x bn (128 or 256) weight rows on CTA pairs, bf16 y; the maps' boxes are
-// {64, 128} tokens and {64, bn / 2} weight rows.
+// Tiles of 256 tokens x bn (128 or 256) weight rows on CTA pairs, bf16 y.  Maps' boxes: {64, 128}
+// of x and u, {64, bn / 2} of w and b, {64, linear_shrink_cols(Rs, bn) / 2} of a.
 cudaError_t linear_wide_setup();
-cudaError_t launch_linear_wide(const LinearParams& p, int bn, int sms, cudaStream_t stream, bool pdl);
+cudaError_t launch_linear_wide(const LinearParams& p, int bn, int sms, cudaStream_t stream);
+inline __host__ __device__ int linear_shrink_cols(int Rs, int bn) { return Rs < bn ? Rs : bn; }   // per shrink tile
 
 struct LinearPackParams {
   const __nv_bfloat16 *A, *B;   // [S, R, K], [S, N, R]

@@ -6,7 +6,8 @@
 //
 // with every slot's A rows and B columns stacked side by side (As [Rs, K], Bs [N, Rs]), so
 // adapters of any ranks and number are one more K range of the same product.  The shrink (u)
-// is this kernel too, with As in the place of W and an epilogue that scales, masks and rounds.
+// is the same tile with As in the place of W and an epilogue that scales, masks and rounds; its
+// tiles are the grid's first, so one launch does all.
 //
 // The weights are the MMA's M = 128 operand and the tokens its N = BN, so a batch of one token
 // still streams whole weight rows.  A cluster of CTAs shares a tile: each takes a part of K
@@ -15,9 +16,11 @@
 // do not vary from run to run), each CTA writing its share of the tile.  That keeps enough
 // CTAs streaming when N alone gives few tiles, in one launch and without global partial sums.
 //
-// The product runs as a programmatic dependent of the shrink: it streams W and x at once and
-// waits for u only in front of the adapter blocks, which come last.  64-column blocks of the
-// stack in which no token of the tile has its adapter are skipped.
+// The product's tiles stream W and x at once and wait for u (a flag per token tile) only in front
+// of the adapter blocks, which come last.  64-column blocks of the stack in which no token of the
+// tile has its adapter are skipped.  The last of a token tile's product CTAs to pass the flag
+// sets it back, so the flags are zero again when the kernel ends.  Blocks start in index order,
+// so the tiles waited for are running before those that wait; every wait is bounded all the same.
 //
 // Warp 0: TMA producer; warp 1: MMA issuer; warps 2-5: slots of the tile's tokens, epilogue.
 // Every wait is bounded; a timeout raises the CTA's abort flag, is recorded in the status
@@ -55,7 +58,7 @@ MLDEV uint32_t cluster_nctas() {
   return r;
 }
 
-template <int BN, int MODE>
+template <int BN>
 __global__ void __launch_bounds__(kThreads, 2) linear_narrow_kernel(const __grid_constant__ LinearParams p) {
   constexpr int kStages = stages_of(BN);
   constexpr uint32_t STAGE = stage_bytes(BN);
@@ -74,13 +77,19 @@ __global__ void __launch_bounds__(kThreads, 2) linear_narrow_kernel(const __grid
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int C = static_cast<int>(cluster_nctas()), rank = static_cast<int>(cluster_ctarank());
-  const int tile = static_cast<int>(blockIdx.x) / C;
+  const int shrink_tiles = (p.Rs + 127) / 128 * p.token_tiles;
+  const int index = static_cast<int>(blockIdx.x) / C;
+  const bool shrink = index < shrink_tiles;
+  const int tile = shrink ? index : index - shrink_tiles;
   const int nt = tile / p.token_tiles, qt = tile - nt * p.token_tiles;
   const int row0 = nt * 128, t0 = qt * BN;
+  const int N = shrink ? p.Rs : p.N;
   const int nk = (p.K + 63) >> 6;
   const int k_lo = static_cast<int>(static_cast<long long>(nk) * rank / C);
   const int k_hi = static_cast<int>(static_cast<long long>(nk) * (rank + 1) / C);
-  const bool lora = MODE == kLinOut && p.Rs > 0;
+  const bool lora = !shrink && p.Rs > 0;
+  int* ready = reinterpret_cast<int*>(p.flags + qt);
+  const int ready_target = (p.Rs + 127) / 128 * C;
 
   // the 64-column blocks of the stack that slot sl's adapter lies in
   auto blocks_of = [&](int sl) -> uint64_t {
@@ -89,15 +98,14 @@ __global__ void __launch_bounds__(kThreads, 2) linear_narrow_kernel(const __grid
     return (~0ull >> (63 - b1)) & (~0ull << b0);
   };
 
-  if constexpr (MODE == kLinShrink) {
-    pdl_trigger();   // the product may start: it waits for this grid's end itself
-    if (p.N > 128 && (tile > 0 || !p.check_slots)) {
-      // a stack of several row tiles: leave out those that no token of the window needs (the
-      // whole cluster decides alike; a tile that writes the status word stays)
-      const int w0 = t0 / p.window * p.window;
-      uint64_t m = 0;
-      for (int j = threadIdx.x; j < p.window && w0 + j < p.T; j += kThreads) m |= blocks_of(p.slot_idx[w0 + j]);
-      if (!__syncthreads_or(((m >> (row0 >> 6)) & 3ull) != 0)) return;
+  if (shrink && p.Rs > 128 && index > 0) {
+    // a stack of several row tiles: leave out those that no token needs (the whole cluster decides
+    // alike; the first tile stays, it writes the status word)
+    uint64_t m = 0;
+    for (int j = threadIdx.x; j < BN && t0 + j < p.T; j += kThreads) m |= blocks_of(p.slot_idx[t0 + j]);
+    if (!__syncthreads_or(((m >> (row0 >> 6)) & 3ull) != 0)) {
+      if (threadIdx.x == 0) red_release_add(ready, 1);
+      return;
     }
   }
 
@@ -114,7 +122,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_narrow_kernel(const __grid
     fence_mbar_init();
   }
   if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&p.tmap_w);
+    tma_prefetch_desc(shrink ? &p.tmap_a : &p.tmap_w);
     tma_prefetch_desc(&p.tmap_x);
   }
   if (warp == 1) {
@@ -145,12 +153,14 @@ __global__ void __launch_bounds__(kThreads, 2) linear_narrow_kernel(const __grid
         }
         return true;
       };
-      for (int kb = k_lo; ok && kb < k_hi; ++kb) ok = issue(&p.tmap_w, kb * 64, &p.tmap_x, kb * 64);
+      const CUtensorMap* wmap = shrink ? &p.tmap_a : &p.tmap_w;
+      for (int kb = k_lo; ok && kb < k_hi; ++kb) ok = issue(wmap, kb * 64, &p.tmap_x, kb * 64);
       if (ok && lora) {
         ok = mbar_wait(mask_bar, 0, abort_flag, p.status, kWhereLinear);
         const uint64_t mask = mask_s[0] | (static_cast<uint64_t>(mask_s[1]) << 32);
         if (ok && mask) {
-          pdl_wait();   // u is written
+          ok = wait_flag_geq(ready, ready_target, abort_flag, p.status, kWhereLinear);   // u is written,
+          fence_proxy_async_global();                                                   // read next by TMA
           int i = 0;
           for (int piece = 0; piece < p.pieces; ++piece)
             for (uint64_t m = mask; ok && m; m &= m - 1, ++i)
@@ -158,6 +168,12 @@ __global__ void __launch_bounds__(kThreads, 2) linear_narrow_kernel(const __grid
                 const int c = (__ffsll(static_cast<long long>(m)) - 1) * 64;
                 ok = issue(&p.tmap_b, c, &p.tmap_u, piece * p.Rs + c);
               }
+        }
+        // past the flag: the last of the token tile's product CTAs sets it back
+        if (ok && atomicAdd(ready + 1, 1) == (p.N + 127) / 128 * C - 1 &&
+            wait_flag_geq(ready, ready_target, abort_flag, p.status, kWhereLinear)) {
+          atomicExch(ready, 0);
+          atomicExch(ready + 1, 0);
         }
       }
       if (!ok)
@@ -209,19 +225,15 @@ __global__ void __launch_bounds__(kThreads, 2) linear_narrow_kernel(const __grid
       if (static_cast<uint32_t>(m >> 32)) atomicOr(&mask_s[1], static_cast<uint32_t>(m >> 32));
       mbar_arrive(mask_bar);
     }
-    if (p.check_slots && blockIdx.x == 0) {   // the only writer of the status word before a timeout
+    if (blockIdx.x == 0) {   // the only writer of the status word before a timeout
       int bad = 0;
       if (p.slot_idx != nullptr)
+#pragma unroll 8
         for (int t = et; t < p.T; t += 128) {
           const int sl = p.slot_idx[t];
           bad |= sl < -1 || sl >= p.slots.S;
         }
-      int any;
-      asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 2, 128, p;\n\t"
-                   "selp.u32 %0, 1, 0, q;\n\t}"
-                   : "=r"(any)
-                   : "r"(bad)
-                   : "memory");
+      const bool any = any_of_128(bad);
       if (et == 0) *p.status = any ? (kDevBadSlot | (kWhereLinear << 8)) : 0u;
     }
     const int quarter = warp & 3;
@@ -250,8 +262,6 @@ __global__ void __launch_bounds__(kThreads, 2) linear_narrow_kernel(const __grid
     tmem_dealloc(tmem_base, TMEM_COLS);
   }
 
-  if (lora) pdl_wait();   // nothing of this grid is written before the shrink has ended
-
   // this CTA's share of the tile: quads of 4 rows of a token, part sums added in rank order
   const int nvalid = min(BN, p.T - t0);
   const int quads = nvalid * 32;
@@ -261,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_narrow_kernel(const __grid
   for (int q = q_lo + static_cast<int>(threadIdx.x); q < q_hi; q += kThreads) {
     const int j = q >> 5, r = (q & 31) * 4;
     const int t = t0 + j, n = row0 + r;
-    if (n >= p.N) continue;
+    if (n >= N) continue;
     float4 v[kMaxSplit];
 #pragma unroll
     for (int c = 0; c < kMaxSplit; ++c)   // all in flight together
@@ -275,12 +285,12 @@ __global__ void __launch_bounds__(kThreads, 2) linear_narrow_kernel(const __grid
         f[2] += v[c].z;
         f[3] += v[c].w;
       }
-    if constexpr (MODE == kLinShrink) {
+    if (shrink) {
       const int sl = p.slot_idx[t];
       const bool has = sl >= 0 && sl < p.slots.S;
       const int lo = has ? p.slots.lo[sl] : 0, hi = has ? p.slots.hi[sl] : 0;
       const float sc = has ? p.slots.scal[sl] : 0.0f;
-      __nv_bfloat16* u = static_cast<__nv_bfloat16*>(p.y) + static_cast<long long>(t) * p.ldy + n;
+      __nv_bfloat16* u = p.u + static_cast<long long>(t) * p.pieces * p.Rs + n;
 #pragma unroll
       for (int i = 0; i < 4; ++i) f[i] = (n + i >= lo && n + i < hi) ? sc * f[i] : 0.0f;
       for (int piece = 0; piece < p.pieces; ++piece) {   // the float32 as a sum of bf16 pieces
@@ -311,30 +321,16 @@ __global__ void __launch_bounds__(kThreads, 2) linear_narrow_kernel(const __grid
       }
     }
   }
+  if (shrink) {   // this CTA's part of u is written: read next by other CTAs' TMA copies
+    __threadfence();
+    fence_proxy_async_global();
+    __syncthreads();
+    if (threadIdx.x == 0) red_release_add(ready, 1);
+  }
   if (C > 1) {   // no CTA leaves while others read its part sums
     __syncwarp();
     cluster_arrive();
     cluster_wait();
-  }
-}
-
-template <int BN, int MODE>
-cudaError_t setup_one() {
-  return cudaFuncSetAttribute(linear_narrow_kernel<BN, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              smem_bytes(BN));
-}
-
-template <int MODE>
-cudaError_t launch_mode(const LinearParams& p, int bn, int split, cudaStream_t stream, bool pdl) {
-  const long long tiles = static_cast<long long>((p.N + 127) / 128) * p.token_tiles;
-  if (tiles * split > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(tiles * split)), block(kThreads);
-  switch (bn) {
-    case 16: return launch_kc(linear_narrow_kernel<16, MODE>, grid, block, smem_bytes(16), stream, pdl, split, p);
-    case 32: return launch_kc(linear_narrow_kernel<32, MODE>, grid, block, smem_bytes(32), stream, pdl, split, p);
-    case 64: return launch_kc(linear_narrow_kernel<64, MODE>, grid, block, smem_bytes(64), stream, pdl, split, p);
-    case 128: return launch_kc(linear_narrow_kernel<128, MODE>, grid, block, smem_bytes(128), stream, pdl, split, p);
-    default: return cudaErrorInvalidValue;
   }
 }
 
@@ -374,9 +370,10 @@ __global__ void __launch_bounds__(256) linear_pack_kernel(const __grid_constant_
 
 cudaError_t linear_narrow_setup() {
   cudaError_t err;
-#define ML_SETUP(BN)                                                              \
-  if ((err = setup_one<BN, kLinOut>()) != cudaSuccess) return err;                \
-  if ((err = setup_one<BN, kLinShrink>()) != cudaSuccess) return err;
+#define ML_SETUP(BN)                                                                                        \
+  err = cudaFuncSetAttribute(linear_narrow_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,          \
+                             smem_bytes(BN));                                                                \
+  if (err != cudaSuccess) return err;
   ML_SETUP(16)
   ML_SETUP(32)
   ML_SETUP(64)
@@ -385,9 +382,17 @@ cudaError_t linear_narrow_setup() {
   return cudaSuccess;
 }
 
-cudaError_t launch_linear_narrow(const LinearParams& p, int mode, int bn, int split, cudaStream_t stream, bool pdl) {
-  return mode == kLinShrink ? launch_mode<kLinShrink>(p, bn, split, stream, pdl)
-                            : launch_mode<kLinOut>(p, bn, split, stream, pdl);
+cudaError_t launch_linear_narrow(const LinearParams& p, int bn, int split, cudaStream_t stream) {
+  const long long tiles = static_cast<long long>((p.N + 127) / 128 + (p.Rs + 127) / 128) * p.token_tiles;
+  if (tiles * split > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>(tiles * split)), block(kThreads);
+  switch (bn) {
+    case 16: return launch_kc(linear_narrow_kernel<16>, grid, block, smem_bytes(16), stream, false, split, p);
+    case 32: return launch_kc(linear_narrow_kernel<32>, grid, block, smem_bytes(32), stream, false, split, p);
+    case 64: return launch_kc(linear_narrow_kernel<64>, grid, block, smem_bytes(64), stream, false, split, p);
+    case 128: return launch_kc(linear_narrow_kernel<128>, grid, block, smem_bytes(128), stream, false, split, p);
+    default: return cudaErrorInvalidValue;
+  }
 }
 
 cudaError_t launch_linear_pack(const LinearPackParams& p, cudaStream_t stream) {

@@ -7,7 +7,12 @@
 // traffic for 128 x 256 x 64 products.  Accumulators are double-buffered in TMEM, so a tile's
 // epilogue runs under the next tile's main loop.  The adapter blocks (u against the stacked B)
 // are further K steps at the end of a tile's main loop, those that no token of the tile needs
-// left out; the first tile waits there for the shrink kernel, beside which this grid starts.
+// left out.  The shrink's tiles (256 tokens x up to BN rows of the stacked A) come before a pair's
+// product tiles and go first to the pairs that have one product tile less than others; a product
+// tile waits for its token tile's flag only in front of its adapter blocks, by
+// when the shrink tiles, which every pair runs before any product tile, are long done.  The grid
+// is resident as a whole (a pair per TPC), and the last product tile of a token tile sets the flag
+// back.
 //
 // Persistent pairs walk the tiles in groups of 8 token tiles, token tile fastest, so the pairs
 // running at one time share weight and token tiles in L2.
@@ -16,8 +21,10 @@
 // memory (16-byte pieces, exclusive-or swizzled as the TMA store expects) and one lane stores the
 // box, or, where y's rows do not start on 16-byte boundaries, the warp stores it row by row.
 //
-// Warp 0: TMA producer; warp 1: MMA issuer (even CTA); warps 2-5: epilogue.  Waits are bounded as
-// everywhere: a timeout is recorded, raises the CTA's abort flag, and the roles leave.
+// Warp 0: TMA producer; warp 1: MMA issuer (even CTA); warps 2-5: epilogue; warp 6: a tile or two
+// ahead of them, which adapter blocks a tile needs, and the wait for its u (in the producer itself
+// these loads and the flag's atomics cost 2 us a tile, 24 us at T 8192, K 2048, N 4096).  Waits are
+// bounded as everywhere: a timeout is recorded, raises the CTA's abort flag, and the roles leave.
 #include "common.cuh"
 #include "linear.h"
 
@@ -25,7 +32,7 @@ namespace mlk {
 
 namespace {
 
-constexpr int kThreads = 192;
+constexpr int kThreads = 224;
 constexpr int kABytes = 128 * 128;
 constexpr int kBoxBytes = 32 * 128;            // a warp's store box: 32 tokens x 64 columns
 constexpr int kYBytes = 4 * 2 * kBoxBytes;     // two per epilogue warp
@@ -48,17 +55,39 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
   uint64_t* empty = full + kStages;
   uint64_t* tfull = empty + kStages;   // [2]
   uint64_t* tempty = tfull + 2;        // [2]
-  uint64_t* drain = tempty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* mfull = tempty + 2;        // [2] the tile's block mask is there
+  uint64_t* mempty = mfull + 2;        // [2] ... and read
+  uint64_t* drain = mempty + 2;
+  volatile uint64_t* mask_s = drain + 1;   // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 3);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t crank = cluster_ctarank();
   const bool leader = crank == 0;
   const int pair = static_cast<int>(blockIdx.x) >> 1, pairs = static_cast<int>(gridDim.x) >> 1;
-  const int NT = (p.N + BN - 1) / BN, TT = p.token_tiles, total = NT * TT;
+  const int NT = (p.N + BN - 1) / BN, TT = p.token_tiles;
   const int nk = (p.K + 63) >> 6;
   const bool lora = p.Rs > 0;
+  const int sh_cols = linear_shrink_cols(p.Rs, BN);            // stacked rows of a shrink tile
+  const int sh_parts = lora ? (p.Rs + sh_cols - 1) / sh_cols : 0;
+  const int nshrink = sh_parts * TT;
+
+  // This pair's tiles, in order: shrink tiles (numbers below nshrink), then product tiles.  Of the
+  // NT * TT product tiles the last pairs get one more than the first `spare` ones, which take the
+  // shrink tiles: two each where a shrink tile costs half a product tile.  What is left over goes
+  // round all pairs.
+  const int vpair = pairs - 1 - pair;
+  const int spare = pairs - NT * TT % pairs;   // pairs with NT * TT / pairs tiles
+  const int to_spare = min(nshrink, spare * (2 * sh_cols <= BN ? 2 : 1));
+  const int n_spare = pair < spare && pair < to_spare ? (to_spare - pair + spare - 1) / spare : 0;
+  const int n_shrink = n_spare + (nshrink - to_spare > pair ? (nshrink - to_spare - pair + pairs - 1) / pairs : 0);
+  const int n_tiles = n_shrink + (NT * TT > vpair ? (NT * TT - vpair + pairs - 1) / pairs : 0);
+  auto tile_at = [&](int i) -> int {
+    if (i < n_spare) return pair + i * spare;
+    if (i < n_shrink) return to_spare + pair + (i - n_spare) * pairs;
+    return nshrink + vpair + (i - n_shrink) * pairs;
+  };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -69,10 +98,13 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
     mbar_init(&tfull[1], 1);
     mbar_init(&tempty[0], 8);   // the pair's epilogue warps
     mbar_init(&tempty[1], 8);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&mfull[i], 1);
+      mbar_init(&mempty[i], leader ? 2 : 1);   // the producer and, in the even CTA, the MMA issuer
+    }
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
-    if (p.check_slots && blockIdx.x == 0) *p.status = 0u;   // no adapters: nothing to check
   }
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&p.tmap_w);
@@ -88,41 +120,35 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
-  auto decode = [&](int tile, int& tt, int& nt) {
+  auto decode = [&](int tile, int& tt, int& nt) {   // a shrink tile's nt: its part of the stack
+    if (tile < nshrink) {
+      tt = tile / sh_parts;
+      nt = tile - tt * sh_parts;
+      return;
+    }
+    tile -= nshrink;
     const int g = tile / (kTokenGroup * NT), r = tile - g * kTokenGroup * NT;
     const int size = min(kTokenGroup, TT - g * kTokenGroup);
     nt = r / size;
     tt = g * kTokenGroup + r - nt * size;
   };
-  // (whole warp) the 64-column blocks that some token of tile tt has its adapter in
-  auto blocks_of_tile = [&](int tt) -> uint64_t {
-    uint64_t m = 0;
-    int sl[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int t = tt * 256 + i * 32 + lane;
-      sl[i] = t < p.T ? __ldg(p.slot_idx + t) : -1;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (sl[i] >= 0 && sl[i] < p.slots.S && p.slots.hi[sl[i]] > p.slots.lo[sl[i]]) {
-        const int b0 = p.slots.lo[sl[i]] >> 6, b1 = (p.slots.hi[sl[i]] - 1) >> 6;
-        m |= (~0ull >> (63 - b1)) & (~0ull << b0);
-      }
-    const uint32_t lo = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(m));
-    const uint32_t hi = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(m >> 32));
-    return lo | (static_cast<uint64_t>(hi) << 32);
+  // the block mask of the i-th product tile of this pair, handed over by warp 6
+  auto take_mask = [&](int i, uint64_t& mask) -> bool {
+    if (!mbar_wait(&mfull[i & 1], (i >> 1) & 1, abort_flag, p.status, kWhereLinear)) return false;
+    mask = mask_s[i & 1];
+    mbar_arrive(&mempty[i & 1]);
+    return true;
   };
 
   if (warp == 0) {   // ------------------------------------------------ TMA producer
     const uint64_t pol = l2_policy_evict_last();
     int stage = 0, ok = 1;
     uint32_t phase = 0, issued = 0, parity = 0;
-    bool waited = false;
-    auto issue = [&](const CUtensorMap* xm, int kx, int t, const CUtensorMap* wm, int kw, int n) -> bool {
+    auto issue = [&](const CUtensorMap* xm, int kx, int t, const CUtensorMap* wm, int kw, int n,
+                     uint32_t bytes) -> bool {
       if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status, kWhereLinear)) return false;
       uint8_t* a = smem + stage * STAGE;
-      if (leader) mbar_arrive_expect_tx(&full[stage], 2 * STAGE);
+      if (leader) mbar_arrive_expect_tx(&full[stage], 2 * bytes);
       const uint32_t bar = cluster_addr(&full[stage], 0);
       tma_load_2d_pair(a, xm, bar, kx, t, pol);
       tma_load_2d_pair(a + kABytes, wm, bar, kw, n, pol);
@@ -134,25 +160,32 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
       }
       return true;
     };
-    for (int tile = pair; tile < total; tile += pairs) {
-      int tt, nt;
-      decode(tile, tt, nt);
-      const uint64_t mask = lora ? blocks_of_tile(tt) : 0ull;
-      if (lane == 0) {
-        const int t = tt * 256 + static_cast<int>(crank) * 128, n = nt * BN + static_cast<int>(crank) * (BN / 2);
-        for (int kb = 0; ok && kb < nk; ++kb) ok = issue(&p.tmap_x, kb * 64, t, &p.tmap_w, kb * 64, n);
-        if (ok && mask && !waited) {
-          pdl_wait();   // u is written
-          waited = true;
+    int nmask = 0;
+    if (lane == 0)
+      for (int i = 0; ok && i < n_tiles; ++i) {
+        const int tile = tile_at(i);
+        int tt, nt;
+        decode(tile, tt, nt);
+        const int t = tt * 256 + static_cast<int>(crank) * 128;
+        if (tile < nshrink) {
+          const int half = sh_cols / 2;
+          for (int kb = 0; ok && kb < nk; ++kb)
+            ok = issue(&p.tmap_x, kb * 64, t, &p.tmap_a, kb * 64, nt * sh_cols + static_cast<int>(crank) * half,
+                       kABytes + half * 128);
+          continue;
         }
-        for (uint64_t m = mask; ok && m; m &= m - 1) {
-          const int c = (__ffsll(static_cast<long long>(m)) - 1) * 64;
-          ok = issue(&p.tmap_u, c, t, &p.tmap_b, c, n);
+        const int n = nt * BN + static_cast<int>(crank) * (BN / 2);
+        for (int kb = 0; ok && kb < nk; ++kb) ok = issue(&p.tmap_x, kb * 64, t, &p.tmap_w, kb * 64, n, STAGE);
+        if (ok && lora) {
+          uint64_t mask = 0;
+          ok = take_mask(nmask++, mask);
+          if (mask) fence_proxy_async_global();   // u was written by st.global, read next by TMA
+          for (; ok && mask; mask &= mask - 1) {
+            const int c = (__ffsll(static_cast<long long>(mask)) - 1) * 64;
+            ok = issue(&p.tmap_u, c, t, &p.tmap_b, c, n, STAGE);
+          }
         }
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (!ok) break;
-    }
     if (lane == 0 && !ok) {   // let every issued copy land before the CTA exits
       if (leader) {
         for (int s = 0; s < kStages; ++s)
@@ -165,60 +198,145 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
     }
   } else if (warp == 1) {   // ------------------------------------------ MMA issuer (even CTA)
     if (leader) {
-      constexpr uint32_t idesc = idesc_bf16_f32(256, BN);
       int stage = 0, ok = 1, acc = 0;
       uint32_t phase = 0, aphase = 0;
-      for (int tile = pair; tile < total; tile += pairs) {
-        int tt, nt;
-        decode(tile, tt, nt);
-        const uint64_t mask = lora ? blocks_of_tile(tt) : 0ull;
-        if (lane == 0) {
-          const int steps = nk + __popcll(mask);
+      auto consume = [&](uint32_t d, uint32_t idesc, bool first) -> bool {
+        if (!mbar_wait(&full[stage], phase, abort_flag, p.status, kWhereLinear)) return false;
+        tc_fence_after();
+        const uint32_t a = smem_u32(smem + stage * STAGE);
+        const uint64_t ad = sw128_kmajor_desc(a), bd = sw128_kmajor_desc(a + kABytes);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) umma_bf16_pair(d, ad + 2 * kk, bd + 2 * kk, idesc, (first && kk == 0) ? 0u : 1u);
+        umma_commit_pair_mc(&empty[stage], 0x3);
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+        return true;
+      };
+      int nmask = 0;
+      if (lane == 0)
+        for (int i = 0; ok && i < n_tiles; ++i) {
+          const bool shrink = i < n_shrink;
+          const uint32_t d = tmem_base + static_cast<uint32_t>(acc * BN);
+          const uint32_t idesc = idesc_bf16_f32(256, shrink ? sh_cols : BN);
           ok = mbar_wait(&tempty[acc], aphase ^ 1u, abort_flag, p.status, kWhereLinear);
           tc_fence_after();
-          const uint32_t d = tmem_base + static_cast<uint32_t>(acc * BN);
-          for (int i = 0; ok && i < steps; ++i) {
-            ok = mbar_wait(&full[stage], phase, abort_flag, p.status, kWhereLinear);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t a = smem_u32(smem + stage * STAGE);
-            const uint64_t ad = sw128_kmajor_desc(a), bd = sw128_kmajor_desc(a + kABytes);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) umma_bf16_pair(d, ad + 2 * kk, bd + 2 * kk, idesc, (i | kk) ? 1u : 0u);
-            umma_commit_pair_mc(&empty[stage], 0x3);
-            if (++stage == kStages) {
-              stage = 0;
-              phase ^= 1u;
-            }
+          for (int kb = 0; ok && kb < nk; ++kb) ok = consume(d, idesc, kb == 0);
+          if (ok && lora && !shrink) {
+            uint64_t mask = 0;
+            ok = take_mask(nmask++, mask);
+            for (; ok && mask; mask &= mask - 1) ok = consume(d, idesc, false);
           }
           if (ok) umma_commit_pair_mc(&tfull[acc], 0x3);
+          if (++acc == 2) {
+            acc = 0;
+            aphase ^= 1u;
+          }
         }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) break;
-        if (++acc == 2) {
-          acc = 0;
-          aphase ^= 1u;
-        }
-      }
       if (!ok && lane == 0) {   // let what was issued finish before TMEM is released
         umma_commit_pair(drain);
         mbar_wait_drain(drain, 0);
       }
     }
+  } else if (warp == 6) {   // ---------------------------- adapter blocks and flags, tiles ahead
+    if (lora) {
+      int ok = 1;
+      for (int i = 0; i < n_tiles - n_shrink; ++i) {
+        int tt, nt;
+        decode(tile_at(n_shrink + i), tt, nt);
+        int sl[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int t = tt * 256 + j * 32 + lane;
+          sl[j] = t < p.T ? __ldg(p.slot_idx + t) : -1;
+        }
+        uint64_t m = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (sl[j] >= 0 && sl[j] < p.slots.S && p.slots.hi[sl[j]] > p.slots.lo[sl[j]]) {
+            const int b0 = p.slots.lo[sl[j]] >> 6, b1 = (p.slots.hi[sl[j]] - 1) >> 6;
+            m |= (~0ull >> (63 - b1)) & (~0ull << b0);
+          }
+        const uint32_t lo = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(m));
+        const uint32_t hi = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(m >> 32));
+        m = lo | (static_cast<uint64_t>(hi) << 32);
+        if (lane == 0) {
+          int* ready = reinterpret_cast<int*>(p.flags + tt);
+          const int target = 8 * sh_parts;   // the pair's epilogue warps, for every part
+          if (m) ok = wait_flag_geq(ready, target, abort_flag, p.status, kWhereLinear);   // u is written
+          ok = ok && mbar_wait_sleep(&mempty[i & 1], ((i >> 1) & 1) ^ 1, abort_flag, p.status, kWhereLinear);
+          if (ok) {
+            mask_s[i & 1] = m;
+            mbar_arrive(&mfull[i & 1]);
+            // past the flag: the last of the token tile's product CTAs sets it back
+            if (atomicAdd(ready + 1, 1) == 2 * NT - 1 &&
+                wait_flag_geq(ready, target, abort_flag, p.status, kWhereLinear)) {
+              atomicExch(ready, 0);
+              atomicExch(ready + 1, 0);
+            }
+          }
+        }
+        if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+      }
+    }
   } else {   // ------------------------------------------------------------ epilogue
-    if (lora) pdl_wait();   // nothing of this grid is written before the shrink has ended
+    if (blockIdx.x == 0) {   // the only writer of the status word before a timeout
+      const int et = static_cast<int>(threadIdx.x) - 64;
+      int bad = 0;
+      if (p.slot_idx != nullptr)
+#pragma unroll 8
+        for (int t = et; t < p.T; t += 128) {
+          const int sl = p.slot_idx[t];
+          bad |= sl < -1 || sl >= p.slots.S;
+        }
+      if (any_of_128(bad) && et == 0) *p.status = kDevBadSlot | (kWhereLinear << 8);
+      else if (et == 0) *p.status = 0u;
+    }
     const int quarter = warp & 3;
     uint8_t* box0 = ybuf + (warp - 2) * 2 * kBoxBytes;
     __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y);
     int acc = 0, nbox = 0;
     uint32_t aphase = 0;
-    for (int tile = pair; tile < total; tile += pairs) {
+    for (int i = 0; i < n_tiles; ++i) {
+      const int tile = tile_at(i);
       int tt, nt;
       decode(tile, tt, nt);
       const int t_warp = tt * 256 + static_cast<int>(crank) * 128 + quarter * 32;
       if (!mbar_wait_sleep(&tfull[acc], aphase, abort_flag, p.status, kWhereLinear)) break;
       tc_fence_after();
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * BN);
+      if (tile < nshrink) {   // u of a token's own columns, 0 in the others
+        const int t = t_warp + lane;
+        const int sl = t < p.T ? p.slot_idx[t] : -1;
+        const bool has = sl >= 0 && sl < p.slots.S;
+        const int lo = has ? p.slots.lo[sl] : 0, hi = has ? p.slots.hi[sl] : 0;
+        const float sc = has ? p.slots.scal[sl] : 0.0f;
+        __nv_bfloat16* u = p.u + static_cast<long long>(t) * p.Rs;
+#pragma unroll 1
+        for (int c = 0; c < sh_cols && nt * sh_cols + c < p.Rs; c += 32) {
+          uint32_t v[32];
+          __syncwarp();
+          tmem_ld_x32(taddr + c, v);
+          tmem_ld_wait();
+          if (t < p.T) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) {
+              float f[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const int col = nt * sh_cols + c + j + i;
+                f[i] = (col >= lo && col < hi) ? sc * __uint_as_float(v[j + i]) : 0.0f;
+              }
+              *reinterpret_cast<uint4*>(u + nt * sh_cols + c + j) = pack8(f);
+            }
+          }
+        }
+        __threadfence();
+        fence_proxy_async_global();   // read next by other CTAs' TMA copies
+        __syncwarp();
+        if (lane == 0) red_release_add(reinterpret_cast<int*>(p.flags + tt), 1);
+      } else
 #pragma unroll 1
       for (int c = 0; c < BN; c += 64) {
         const int n = nt * BN + c;
@@ -292,13 +410,15 @@ cudaError_t linear_wide_setup() {
   return cudaFuncSetAttribute(linear_wide_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(128));
 }
 
-cudaError_t launch_linear_wide(const LinearParams& p, int bn, int sms, cudaStream_t stream, bool pdl) {
-  const long long tiles = static_cast<long long>((p.N + bn - 1) / bn) * p.token_tiles;
+cudaError_t launch_linear_wide(const LinearParams& p, int bn, int sms, cudaStream_t stream) {
+  const int cols = linear_shrink_cols(p.Rs, bn);
+  const long long tiles =
+      static_cast<long long>((p.N + bn - 1) / bn + (cols ? (p.Rs + cols - 1) / cols : 0)) * p.token_tiles;
   if (tiles > 0x3fffffffLL || (bn != 128 && bn != 256)) return cudaErrorInvalidValue;
   const int pairs = static_cast<int>(tiles < sms / 2 ? tiles : sms / 2);
   const dim3 grid(2 * pairs), block(kThreads);
-  if (bn == 256) return launch_kc(linear_wide_kernel<256>, grid, block, smem_bytes(256), stream, pdl, 2, p);
-  return launch_kc(linear_wide_kernel<128>, grid, block, smem_bytes(128), stream, pdl, 2, p);
+  if (bn == 256) return launch_kc(linear_wide_kernel<256>, grid, block, smem_bytes(256), stream, false, 2, p);
+  return launch_kc(linear_wide_kernel<128>, grid, block, smem_bytes(128), stream, false, 2, p);
 }
 
 }  // namespace mlk

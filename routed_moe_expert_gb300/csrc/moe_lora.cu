@@ -16,6 +16,7 @@
 // multi-slot replay bug of sglang PR #28091, Motivation 3, cannot arise).
 #include "../../include/moe_lora.h"
 #include "host.h"
+#include "linear.h"
 #include "kernels.h"
 
 #include <algorithm>
@@ -196,6 +197,9 @@ moe_lora_status moe_lora_create(moe_lora_handle** out, int device) {
   cudaError_t err = cudaStreamCreateWithFlags(&h->side, cudaStreamNonBlocking);
   if (err == cudaSuccess) err = cudaEventCreateWithFlags(&h->ev_fork, cudaEventDisableTiming);
   if (err == cudaSuccess) err = cudaEventCreateWithFlags(&h->ev_ready, cudaEventDisableTiming);
+  if (err == cudaSuccess) err = cudaMalloc(reinterpret_cast<void**>(&h->linear_flags), kLinearFlags * sizeof(int2));
+  if (err == cudaSuccess) err = cudaMemset(h->linear_flags, 0, kLinearFlags * sizeof(int2));
+  if (err == cudaSuccess) err = cudaDeviceSynchronize();   // zero before any stream's first call
   void* fn = nullptr;
   cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
   if (err == cudaSuccess)
@@ -216,6 +220,7 @@ moe_lora_status moe_lora_destroy(moe_lora_handle* h) {
     cudaStreamSynchronize(h->side);
     cudaStreamDestroy(h->side);
   }
+  if (h->linear_flags) cudaFree(h->linear_flags);
   if (h->ev_fork) cudaEventDestroy(h->ev_fork);
   if (h->ev_ready) cudaEventDestroy(h->ev_ready);
   delete h;
