@@ -736,13 +736,17 @@ def moe_lora_check_status(workspace: torch.Tensor, stream=None):
 
 
 # ---------------------------------------------------------------- operators around the layer
-# These are called once or more per layer on batches down to one token, where the host's time
-# is the call's time: each argument struct is packed in one go, and results are allocated only
-# when the caller brings none.
+# These are called several times per layer on batches down to one token, where the host's time
+# is the call's time.  So each argument struct is packed in one go, messages are built only for
+# an error, and what this module has just allocated is not looked at again.
 _select_args = struct.Struct("@5P1q9if").pack       # moe_lora_select_args
 _qk_args = struct.Struct("@8P9q9if").pack           # moe_lora_qk_args
-_linear_args = struct.Struct("@8P3q5i4x").pack        # moe_lora_linear_args
-_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
+_linear_args = struct.Struct("@8P3q5i4x").pack      # moe_lora_linear_args
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_F32 = (torch.float32,)
+_I32 = (torch.int32,)
+_I32_I64 = (torch.int32, torch.int64)
+_BF16_F32 = (torch.bfloat16, torch.float32)
 
 
 def _stream_on(device: torch.device, stream) -> int:
@@ -751,28 +755,28 @@ def _stream_on(device: torch.device, stream) -> int:
     return _stream(stream)
 
 
-def _need(cond, msg):
-    if not cond:
-        raise ValueError(msg)
+def _refuse(t, name: str, want: str):
+    got = f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}" if isinstance(t, torch.Tensor) else repr(t)
+    raise ValueError(f"{name} must be {want}, got {got}")
 
 
-def _need_vec(t: torch.Tensor, n: int, dtypes, dev, name: str) -> int:
+def _vec(t: torch.Tensor, n: int, dtypes, dev, name: str) -> int:
     """The address of a dense vector of n values on `dev`."""
-    if t.dtype not in dtypes or t.shape != (n,) or t.device != dev or (n > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name} must be a dense [{n}] tensor of {' or '.join(str(d) for d in dtypes)} on {dev}, got "
-                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    if t.dtype not in dtypes or t.dim() != 1 or t.shape[0] != n or t.device != dev or (n > 1 and t.stride(0) != 1):
+        _refuse(t, name, f"a dense [{n}] tensor of {' or '.join(str(d) for d in dtypes)} on {dev}")
     return t.data_ptr()
 
 
-def _need_out(t: torch.Tensor, shape, dtype, dev, name: str) -> int:
+def _dense(t: torch.Tensor, shape, dtype, dev, name: str) -> int:
     if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != dev or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} {tuple(shape)} tensor on {dev}, got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}")
+        _refuse(t, name, f"a contiguous {dtype} {tuple(shape)} tensor on {dev}")
     return t.data_ptr()
 
 
-_F32 = (torch.float32,)
-_BF16_F32 = (torch.bfloat16, torch.float32)
+def _bytes(t: torch.Tensor, dev, name: str) -> int:
+    if t.dtype is not torch.uint8 or t.device != dev or not t.is_contiguous():
+        _refuse(t, name, f"a contiguous uint8 tensor on {dev}")
+    return t.data_ptr()
 
 
 def moe_lora_select_experts(handle: Handle, logits: torch.Tensor, top_k: int, scoring: int = SCORE_SOFTMAX,
@@ -785,28 +789,39 @@ def moe_lora_select_experts(handle: Handle, logits: torch.Tensor, top_k: int, sc
     best of n_group groups, ties to the lower id; weights are the chosen scores, divided by their
     sum when `renormalize`, times routed_scaling_factor.  Returns a dict of topk_ids [T, top_k]
     int32 and topk_weights [T, top_k] float32, and with `packed` packed_topk_ids [T, top_k], the
-    words that moe_lora_forward_routed takes.  Logits of -inf or NaN rule an expert out."""
-    _need(logits.dim() == 2 and logits.is_cuda and logits.dtype in _BF16_F32 and
-          (logits.stride(1) == 1 or logits.shape[1] <= 1),
-          "logits must be a bf16 or float32 CUDA tensor [T, E] with adjacent columns")
+    words that moe_lora_forward_routed takes; `outputs` may bring any of them.  Logits of -inf or
+    NaN rule an expert out."""
+    dt = logits.dtype
+    if logits.dim() != 2 or not logits.is_cuda or dt not in _BF16_F32:
+        _refuse(logits, "logits", "a bf16 or float32 CUDA tensor [T, E]")
     T, E = logits.shape
+    row, col = logits.stride()
+    if col != 1 and E > 1:
+        _refuse(logits, "logits", "a tensor with adjacent columns")
     dev = logits.device
-    o = outputs if outputs is not None else {}
-    ids, w, pk = o.get("topk_ids"), o.get("topk_weights"), o.get("packed_topk_ids")
+    o = {} if outputs is None else outputs
     shape = (T, top_k)
+    ids, w, pk = o.get("topk_ids"), o.get("topk_weights"), o.get("packed_topk_ids")
     if ids is None:
         o["topk_ids"] = ids = torch.empty(shape, dtype=torch.int32, device=dev)
+        ids_at = ids.data_ptr()
+    else:
+        ids_at = _dense(ids, shape, torch.int32, dev, "topk_ids")
     if w is None:
         o["topk_weights"] = w = torch.empty(shape, dtype=torch.float32, device=dev)
-    if pk is None and packed:
+        w_at = w.data_ptr()
+    else:
+        w_at = _dense(w, shape, torch.float32, dev, "topk_weights")
+    pk_at = 0
+    if pk is not None:
+        pk_at = _dense(pk, shape, torch.int32, dev, "packed_topk_ids")
+    elif packed:
         o["packed_topk_ids"] = pk = torch.empty(shape, dtype=torch.int32, device=dev)
-    args = _select_args(
-        logits.data_ptr(), 0 if bias is None else _need_vec(bias, E, _F32, dev, "bias"),
-        _need_out(ids, shape, torch.int32, dev, "topk_ids"), _need_out(w, shape, torch.float32, dev, "topk_weights"),
-        0 if pk is None else _need_out(pk, shape, torch.int32, dev, "packed_topk_ids"),
-        logits.stride(0) if T > 1 else E, T, E, top_k, logits.dtype is torch.float32, scoring, n_group, topk_group,
-        group_score, bool(renormalize), routed_scaling_factor)
-    st = lib().moe_lora_select_experts(handle.ptr, args, _stream_on(dev, stream))
+        pk_at = pk.data_ptr()
+    args = _select_args(logits.data_ptr(), 0 if bias is None else _vec(bias, E, _F32, dev, "bias"), ids_at, w_at, pk_at,
+                        row if T > 1 else E, T, E, top_k, dt is torch.float32, scoring, n_group, topk_group,
+                        group_score, bool(renormalize), routed_scaling_factor)
+    st = (_lib or lib()).moe_lora_select_experts(handle._h, args, _stream_on(dev, stream))
     if st:
         _check(st, "moe_lora_select_experts")
     return o
@@ -818,6 +833,7 @@ class LinearAdapters:
 
     def __init__(self, packed: torch.Tensor, S: int, N: int, K: int, ranks: Sequence[int], scalings: Sequence[float]):
         self.packed = packed
+        self.device = packed.device
         self.S, self.N, self.K = S, N, K
         self.ranks = (ctypes.c_int32 * S)(*ranks)
         self.scalings = (c_float * S)(*scalings)
@@ -829,13 +845,15 @@ def moe_lora_linear_adapters(handle: Handle, A: torch.Tensor, B: torch.Tensor, r
                              scalings: Sequence[float], stream=None) -> LinearAdapters:
     """Stacks the adapters A [S, R, K] and B [S, N, R] (dense bf16; slot s uses its first ranks[s]
     ranks, times scalings[s]) of one projection for moe_lora_linear.  Once per adapter load."""
-    _need(A.dim() == 3 and B.dim() == 3 and A.dtype == B.dtype == torch.bfloat16 and A.is_cuda and
-          A.device == B.device and A.is_contiguous() and B.is_contiguous(),
-          "A [S, R, K] and B [S, N, R] must be dense bf16 tensors on the same CUDA device")
+    if A.dim() != 3 or A.dtype != torch.bfloat16 or not A.is_cuda or not A.is_contiguous():
+        _refuse(A, "A", "a dense bf16 CUDA tensor [S, R, K]")
     S, R, K = A.shape
+    if (B.dim() != 3 or B.dtype != torch.bfloat16 or B.device != A.device or not B.is_contiguous() or
+            B.shape[0] != S or B.shape[2] != R):
+        _refuse(B, "B", f"a dense bf16 [{S}, N, {R}] tensor on {A.device}")
     N = B.shape[1]
-    _need(B.shape[0] == S and B.shape[2] == R, f"B must have shape ({S}, N, {R}), got {tuple(B.shape)}")
-    _need(len(ranks) == S and len(scalings) == S, f"need {S} ranks and scalings, got {len(ranks)} and {len(scalings)}")
+    if len(ranks) != S or len(scalings) != S:
+        raise ValueError(f"need {S} ranks and scalings, got {len(ranks)} and {len(scalings)}")
     ranks = [int(r) for r in ranks]
     arr = (ctypes.c_int32 * max(S, 1))(*ranks)
     n = c_size_t()
@@ -860,13 +878,6 @@ def alloc_linear_workspace(T: int, adapters: Optional[LinearAdapters] = None, de
     return torch.empty(moe_lora_linear_workspace_size(T, adapters), dtype=torch.uint8, device=device)
 
 
-def _rows(t: torch.Tensor, cols: int, dev, name: str) -> int:
-    if t.dim() != 2 or t.dtype != torch.bfloat16 or t.shape[1] != cols or t.device != dev or (t.stride(1) != 1 and cols > 1):
-        raise ValueError(f"{name} must be a bf16 [rows, {cols}] tensor on {dev} with adjacent columns, got {t.dtype} "
-                         f"{tuple(t.shape)} strides {t.stride()} on {t.device}")
-    return t.data_ptr()
-
-
 def moe_lora_linear(handle: Handle, x: torch.Tensor, w: torch.Tensor, adapters: Optional[LinearAdapters] = None,
                     slot_idx: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
                     out: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
@@ -876,32 +887,46 @@ def moe_lora_linear(handle: Handle, x: torch.Tensor, w: torch.Tensor, adapters: 
     be strided, by multiples of 8), bias [N] float32, slot_idx [T] int32.  The result is a new
     [T, N] tensor of out_dtype (bf16 or float32), or `out`, whose rows may be strided (a column
     range of a wider tensor).  `workspace`: alloc_linear_workspace(T, adapters), or allocated."""
-    _need(x.dim() == 2 and x.is_cuda, "x must be a CUDA tensor [T, K]")
+    if x.dim() != 2 or not x.is_cuda or x.dtype is not torch.bfloat16:
+        _refuse(x, "x", "a bf16 CUDA tensor [T, K]")
     T, K = x.shape
+    x_row, x_col = x.stride()
+    if x_col != 1 and K > 1:
+        _refuse(x, "x", "a tensor with adjacent columns")
     dev = x.device
+    if w.dim() != 2 or w.dtype is not torch.bfloat16 or w.device != dev or w.shape[1] != K:
+        _refuse(w, "w", f"a bf16 [N, {K}] tensor on {dev}")
     N = w.shape[0]
-    xp, wp = _rows(x, K, dev, "x"), _rows(w, K, dev, "w")
+    w_row, w_col = w.stride()
+    if w_col != 1 and K > 1:
+        _refuse(w, "w", "a tensor with adjacent columns")
     if out is None:
-        _need(out_dtype in _BF16_F32, "out_dtype must be torch.bfloat16 or torch.float32")
+        if out_dtype not in _BF16_F32:
+            raise ValueError(f"out_dtype must be torch.bfloat16 or torch.float32, got {out_dtype}")
         out = torch.empty((T, N), dtype=out_dtype, device=dev)
+        y_row = N
     else:
-        _need(out.dtype in _BF16_F32 and out.shape == (T, N) and out.device == dev and (out.stride(1) == 1 or N == 1),
-              f"out must be a bf16 or float32 ({T}, {N}) tensor on {dev} with adjacent columns")
+        out_dtype = out.dtype
+        if out_dtype not in _BF16_F32 or out.shape != (T, N) or out.device != dev or (out.stride(1) != 1 and N > 1):
+            _refuse(out, "out", f"a bf16 or float32 ({T}, {N}) tensor on {dev} with adjacent columns")
+        y_row = out.stride(0)
+    S = ad_at = ranks_at = scalings_at = slots_at = 0
     if adapters is not None:
-        _need(adapters.N == N and adapters.K == K and adapters.packed.device == dev,
-              f"the adapters are for a [{adapters.N}, {adapters.K}] projection on {adapters.packed.device}, w is "
-              f"[{N}, {K}] on {dev}")
-        _need(slot_idx is not None, "slot_idx [T] is required with adapters")
-        S, ap, rp, sp = adapters.S, adapters.address, adapters.ranks_address, adapters.scalings_address
-        ip = _need_vec(slot_idx, T, (torch.int32,), dev, "slot_idx")
-    else:
-        S = ap = rp = sp = ip = 0
+        if adapters.N != N or adapters.K != K or adapters.device != dev:
+            raise ValueError(f"the adapters are for a [{adapters.N}, {adapters.K}] projection on {adapters.device}, "
+                             f"w is [{N}, {K}] on {dev}")
+        if slot_idx is None:
+            raise ValueError("slot_idx [T] is required with adapters")
+        S, ad_at = adapters.S, adapters.address
+        ranks_at, scalings_at = adapters.ranks_address, adapters.scalings_address
+        slots_at = _vec(slot_idx, T, _I32, dev, "slot_idx")
     if workspace is None:
         workspace = alloc_linear_workspace(T, adapters, dev)
-    args = _linear_args(xp, wp, 0 if bias is None else _need_vec(bias, N, _F32, dev, "bias"), out.data_ptr(), ap, ip,
-                        rp, sp, x.stride(0), w.stride(0), out.stride(0), T, N, K, S, out.dtype is torch.float32)
-    st = lib().moe_lora_linear(handle.ptr, args, _ptr(workspace, torch.uint8, "workspace"), workspace.numel(),
-                               _stream_on(dev, stream))
+    args = _linear_args(x.data_ptr(), w.data_ptr(), 0 if bias is None else _vec(bias, N, _F32, dev, "bias"),
+                        out.data_ptr(), ad_at, slots_at, ranks_at, scalings_at, x_row, w_row, y_row, T, N, K, S,
+                        out_dtype is torch.float32)
+    st = (_lib or lib()).moe_lora_linear(handle._h, args, _bytes(workspace, dev, "workspace"), workspace.numel(),
+                                         _stream_on(dev, stream))
     if st:
         _check(st, "moe_lora_linear")
     return out
@@ -912,12 +937,14 @@ def alloc_qk_norm_rope_workspace(device="cuda") -> torch.Tensor:
     return torch.zeros(256, dtype=torch.uint8, device=device)
 
 
-def _heads(t: torch.Tensor, T: int, D: int, dev, name: str):
-    if (t.dim() != 3 or t.dtype != torch.bfloat16 or t.device != dev or t.shape[0] != T or t.shape[2] != D or
-            (t.stride(2) != 1 and D > 1)):
-        raise ValueError(f"{name} must be a bf16 [T, heads, {D}] tensor on {dev} with T = {T} and adjacent head values, "
-                         f"got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
-    return t.data_ptr(), t.stride(0), t.stride(1)
+def _heads(t: torch.Tensor, T: int, H: int, D: int, dev, name: str):
+    """Address and strides of [T, H, D] heads."""
+    if t.dtype is not torch.bfloat16 or t.dim() != 3 or t.shape != (T, H, D) or t.device != dev:
+        _refuse(t, name, f"a bf16 [{T}, {H}, {D}] tensor on {dev}")
+    row, head, one = t.stride()
+    if one != 1 and D > 1:
+        _refuse(t, name, "a tensor whose heads' values are adjacent")
+    return t.data_ptr(), row, head
 
 
 def moe_lora_qk_norm_rope(handle: Handle, q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor,
@@ -925,35 +952,47 @@ def moe_lora_qk_norm_rope(handle: Handle, q: torch.Tensor, k: torch.Tensor, q_we
                           interleaved: bool = False, q_out: Optional[torch.Tensor] = None,
                           k_out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
     """Norm of every head of q [T, Hq, D] and k [T, Hk, D] (bf16, for instance slices of merged
-    q/k/v rows) by its root mean square, times q_weight / k_weight [D] (bf16 or float32), then the
-    rotation of the first R values by row positions[t] (int32 or int64) of cos_sin [P, R]
+    q/k/v rows) by its root mean square, times q_weight / k_weight [D] (both bf16 or both float32),
+    then the rotation of the first R values by row positions[t] (int32 or int64) of cos_sin [P, R]
     (float32: R/2 cosines, R/2 sines); pairs (i, i + R/2), or (2i, 2i + 1) when interleaved.
     Returns (q_out, k_out), new dense tensors unless given; they may be q and k themselves."""
-    _need(q.dim() == 3 and q.is_cuda, "q must be a CUDA tensor [T, heads, D]")
+    if q.dim() != 3 or not q.is_cuda:
+        _refuse(q, "q", "a bf16 CUDA tensor [T, heads, D]")
+    if k.dim() != 3:
+        _refuse(k, "k", "a bf16 CUDA tensor [T, heads, D]")
     T, Hq, D = q.shape
+    Hk = k.shape[1]
     dev = q.device
-    _need(cos_sin.dim() == 2 and cos_sin.dtype == torch.float32 and cos_sin.device == dev and
-          (cos_sin.stride(1) == 1 or cos_sin.shape[1] <= 1), "cos_sin must be a float32 [positions, R] tensor")
+    q_at, q_t, q_h = _heads(q, T, Hq, D, dev, "q")
+    k_at, k_t, k_h = _heads(k, T, Hk, D, dev, "k")
+    if cos_sin.dim() != 2 or cos_sin.dtype is not torch.float32 or cos_sin.device != dev:
+        _refuse(cos_sin, "cos_sin", f"a float32 [positions, R] tensor on {dev}")
     P, R = cos_sin.shape
+    cs_row, cs_col = cos_sin.stride()
+    if cs_col != 1 and R > 1:
+        _refuse(cos_sin, "cos_sin", "a tensor with adjacent columns")
+    wt = q_weight.dtype
+    if k_weight.dtype != wt:
+        _refuse(k_weight, "k_weight", f"of q_weight's type ({wt})")
     if q_out is None:
         q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+        qo_at, qo_t, qo_h = q_out.data_ptr(), Hq * D, D
+    else:
+        qo_at, qo_t, qo_h = _heads(q_out, T, Hq, D, dev, "q_out")
     if k_out is None:
-        k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=dev)
-    qp, q_t, q_h = _heads(q, T, D, dev, "q")
-    kp, k_t, k_h = _heads(k, T, D, dev, "k")
-    qop, qo_t, qo_h = _heads(q_out, T, D, dev, "q_out")
-    kop, ko_t, ko_h = _heads(k_out, T, D, dev, "k_out")
-    Hk = k.shape[1]
-    _need(q_out.shape[1] == Hq and k_out.shape[1] == Hk, "q_out and k_out must have as many heads as q and k")
-    _need(q_weight.dtype == k_weight.dtype, "q_weight and k_weight must have the same type")
-    args = _qk_args(
-        qp, kp, qop, kop, _need_vec(q_weight, D, _BF16_F32, dev, "q_weight"),
-        _need_vec(k_weight, D, _BF16_F32, dev, "k_weight"), cos_sin.data_ptr(),
-        _need_vec(positions, T, (torch.int32, torch.int64), dev, "positions"), q_t, q_h, k_t, k_h, qo_t, qo_h, ko_t,
-        ko_h, cos_sin.stride(0) if P > 1 else R, T, Hq, Hk, D, R, P, q_weight.dtype is torch.float32,
-        positions.dtype is torch.int64, bool(interleaved), eps)
-    wp, wn = (None, 0) if workspace is None else (_ptr(workspace, torch.uint8, "workspace"), workspace.numel())
-    st = lib().moe_lora_qk_norm_rope(handle.ptr, args, wp, wn, _stream_on(dev, stream))
+        k_out = torch.empty((T, Hk, D), dtype=torch.bfloat16, device=dev)
+        ko_at, ko_t, ko_h = k_out.data_ptr(), Hk * D, D
+    else:
+        ko_at, ko_t, ko_h = _heads(k_out, T, Hk, D, dev, "k_out")
+    args = _qk_args(q_at, k_at, qo_at, ko_at, _vec(q_weight, D, _BF16_F32, dev, "q_weight"),
+                    _vec(k_weight, D, _BF16_F32, dev, "k_weight"), cos_sin.data_ptr(),
+                    _vec(positions, T, _I32_I64, dev, "positions"), q_t, q_h, k_t, k_h, qo_t, qo_h, ko_t, ko_h, cs_row,
+                    T, Hq, Hk, D, R, P, wt is torch.float32, positions.dtype is torch.int64, bool(interleaved), eps)
+    if workspace is None:
+        ws_at = ws_n = 0
+    else:
+        ws_at, ws_n = _bytes(workspace, dev, "workspace"), workspace.numel()
+    st = (_lib or lib()).moe_lora_qk_norm_rope(handle._h, args, ws_at, ws_n, _stream_on(dev, stream))
     if st:
         _check(st, "moe_lora_qk_norm_rope")
     return q_out, k_out
