@@ -11,9 +11,16 @@
 // not rounded before the rotation).
 //
 // It is bound by memory: each value is read once and written once.  L lanes hold a head, so a
-// warp holds 32 / L heads of one token at a time; a lane's V-value pieces are chosen so that
-// both members of every rotated pair sit in the same lane (pieces i and i + R/2 of a half-split
-// rotation), so the only exchange between lanes is the sum of squares.
+// warp holds 32 / L heads at a time; a lane's pieces are chosen so that both members of every
+// rotated pair sit in the same lane (pieces i and i + R/2 of a half-split rotation), so the only
+// exchange between lanes is the sum of squares.
+//
+// Where everything starts on 16-byte boundaries (qk_norm_rope_kernel) a lane's 16 values of every
+// head of a token have the same weights and angles: out_i = scale (x_i C_i + x_partner S_i), with
+// C = w c and S = -+ w_partner s made once per token and kind of head and kept in registers, and
+// the next heads' values are loaded before the current ones are used.  Everything else (odd
+// strides, offsets and sizes) goes through qk_norm_rope_any_kernel, which works its indices out
+// value by value.
 #include "common.cuh"
 #include "host.h"
 #include "kernels.h"
@@ -30,10 +37,12 @@ struct QkParams {
   const void* positions;
   uint32_t* status;
   long long q_t, q_h, k_t, k_h, qo_t, qo_h, ko_t, ko_h, table_t;   // strides in elements
-  int T, Hq, Hk, D, R, num_positions, w_f32, pos_i64, interleaved;
+  int T, Hq, Hk, D, R, num_positions, w_f32, pos_i64, interleaved, table_vec;
   int lanes;        // L: lanes per head, a power of two
-  int heads_per_warp;   // heads one warp goes through
-  int splits;       // warps per token
+  int heads_per_warp, splits;   // (any alignment) heads one warp goes through, warps per token
+  // (aligned) rounds in all, of a warp, of a token; heads packed across tokens, and then the steps
+  unsigned rounds, run;
+  int token_rounds, packed, step_t, step_h;
   float eps;
 };
 
@@ -103,27 +112,219 @@ MLDEV void unit_at(const QkParams& p, int u, int& a, int& b, bool& rotated) {
   if (b >= p.D) b = -1;
 }
 
-// V values per piece, NU units per lane.
-template <int V, int NU>
-__global__ void __launch_bounds__(256) qk_norm_rope_kernel(const QkParams p) {
-  const int lane = threadIdx.x & 31;
-  const long long warp = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (blockIdx.x == gridDim.x - 1) {   // one more block than the work needs: the positions' check
-    if (p.status == nullptr) return;
-    __shared__ int bad_s;
-    if (threadIdx.x == 0) bad_s = 0;
-    __syncthreads();
-    bool bad = false;
-    for (int t = threadIdx.x; t < p.T; t += blockDim.x) {
-      const long long pos = p.pos_i64 ? static_cast<const long long*>(p.positions)[t]
-                                      : static_cast<const int32_t*>(p.positions)[t];
-      bad |= pos < 0 || pos >= p.num_positions;
-    }
-    if (bad) bad_s = 1;
-    __syncthreads();
-    if (threadIdx.x == 0) *p.status = bad_s ? (kDevBadSlot | (kWhereQkPosition << 8)) : 0u;
+// The last block, one more than the work needs: the positions' check, the only write of the status.
+MLDEV void check_positions(const QkParams& p) {
+  if (p.status == nullptr) return;
+  __shared__ int bad_s;
+  if (threadIdx.x == 0) bad_s = 0;
+  __syncthreads();
+  bool bad = false;
+#pragma unroll 4
+  for (int t = threadIdx.x; t < p.T; t += blockDim.x) {
+    const long long pos = p.pos_i64 ? static_cast<const long long*>(p.positions)[t]
+                                    : static_cast<const int32_t*>(p.positions)[t];
+    bad |= pos < 0 || pos >= p.num_positions;
+  }
+  if (bad) bad_s = 1;
+  __syncthreads();
+  if (threadIdx.x == 0) *p.status = bad_s ? (kDevBadSlot | (kWhereQkPosition << 8)) : 0u;
+}
+
+constexpr int kAhead = 3;             // rounds whose copies are in flight
+constexpr int kRing = kAhead + 1;
+
+MLDEV void copy16(uint4* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+MLDEV void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+MLDEV void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// The aligned case: a lane's 16 values of a head are two 16-byte pieces.  A round is one head per
+// lane group: 32 / L heads of a token (the rest of a token's last round idle), or, with few heads
+// (`packed`), any 32 / L consecutive (token, head) pairs.  Each warp takes a run of rounds.
+template <bool INTERLEAVED>
+__global__ void __launch_bounds__(256, 3) qk_norm_rope_kernel(const QkParams p) {
+  if (blockIdx.x == gridDim.x - 1) {
+    check_positions(p);
     return;
   }
+  __shared__ uint4 ring[kRing][2][256];
+  const int lane = threadIdx.x & 31;
+  const unsigned warp = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  const int H = p.Hq + p.Hk;
+  const int L = p.lanes, per = 32 / L, group = lane / L, sub = lane & (L - 1);
+  const unsigned g0 = min(warp * p.run, p.rounds), g1 = min(g0 + p.run, p.rounds);
+  const int n = static_cast<int>(g1 - g0);   // rounds of this warp
+
+  // this lane's pieces (-1: none)
+  int a, b;
+  bool turned;
+  if constexpr (INTERLEAVED) {
+    a = sub * 16;
+    b = a + 8;
+    turned = true;   // decided piece by piece
+  } else {
+    const int rot = p.R >> 4;
+    turned = sub < rot;
+    a = turned ? sub * 8 : p.R + (sub - rot) * 16;
+    b = turned ? a + (p.R >> 1) : a + 8;
+  }
+  if (a >= p.D) a = -1;
+  if (b >= p.D) b = -1;
+
+  // a lane group's (token, head) in round g0, and its step from round to round
+  struct At {
+    int t, h;
+  };
+  auto first = [&]() -> At {
+    if (p.packed) {
+      const unsigned task = g0 * per + group;
+      return {static_cast<int>(task / H), static_cast<int>(task % H)};
+    }
+    return {static_cast<int>(g0 / p.token_rounds), static_cast<int>(g0 % p.token_rounds) * per + group};
+  };
+  auto next = [&](At& x) {
+    if (p.packed) {
+      x.t += p.step_t;
+      x.h += p.step_h;
+      if (x.h >= H) {
+        x.h -= H;
+        ++x.t;
+      }
+    } else {
+      x.h += per;
+      if (x.h - group >= H) {
+        x.h = group;
+        ++x.t;
+      }
+    }
+  };
+  auto live = [&](const At& x) -> bool { return x.h < H && x.t < p.T; };
+  auto head_in = [&](const At& x) -> const __nv_bfloat16* {
+    return x.h < p.Hq ? p.q + x.t * p.q_t + x.h * p.q_h : p.k + x.t * p.k_t + (x.h - p.Hq) * p.k_h;
+  };
+  At now = first(), ahead = now;
+  int fetched = 0;
+  auto fetch = [&]() {   // the copies of the next round not yet on its way
+    if (fetched < n && live(ahead)) {
+      const __nv_bfloat16* x = head_in(ahead);
+      if (a >= 0) copy16(&ring[fetched % kRing][0][threadIdx.x], x + a);
+      if (b >= 0) copy16(&ring[fetched % kRing][1][threadIdx.x], x + b);
+    }
+    copy_commit();
+    ++fetched;
+    next(ahead);
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) fetch();
+
+  float ca[8], sa[8], cb[8], sb[8];   // coefficients of the own value and of the partner
+  int kind = -1, token = -1;          // the heads they are for: 0 query, 1 key; of which token
+  const float inv_d = 1.0f / static_cast<float>(p.D);
+
+  for (int i = 0; i < n; ++i, next(now)) {
+    fetch();
+    const bool on = live(now);
+    const int is_k = now.h >= p.Hq;
+    if (on && (token != now.t || kind != is_k)) {
+      const void* w = is_k ? p.wk : p.wq;
+      kind = is_k;
+      token = now.t;
+      const long long pos = p.pos_i64 ? static_cast<const long long*>(p.positions)[token]
+                                      : static_cast<const int32_t*>(p.positions)[token];
+      // angles of the lane's values: half-split, one per pair of pieces; interleaved, four pairs of
+      // piece a, then four of piece b.  A bad position: no rotation (and reported)
+      float c[8], s[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        c[j] = 1.0f;
+        s[j] = 0.0f;
+      }
+      if (pos >= 0 && pos < p.num_positions) {
+        const float* row = p.table + pos * p.table_t;
+        if constexpr (INTERLEAVED) {
+          if (a >= 0 && a < p.R) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              c[j] = __ldg(row + a / 2 + j);
+              s[j] = __ldg(row + p.R / 2 + a / 2 + j);
+            }
+          }
+          if (b >= 0 && b < p.R) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              c[4 + j] = __ldg(row + b / 2 + j);
+              s[4 + j] = __ldg(row + p.R / 2 + b / 2 + j);
+            }
+          }
+        } else if (turned) {
+          if (p.table_vec) {
+#pragma unroll
+            for (int j = 0; j < 8; j += 4) {
+              const float4 cv = __ldg(reinterpret_cast<const float4*>(row + a + j));
+              const float4 sv = __ldg(reinterpret_cast<const float4*>(row + p.R / 2 + a + j));
+              c[j] = cv.x, c[j + 1] = cv.y, c[j + 2] = cv.z, c[j + 3] = cv.w;
+              s[j] = sv.x, s[j + 1] = sv.y, s[j + 2] = sv.z, s[j + 3] = sv.w;
+            }
+          } else {
+            load_f32<8>(row + a, c);
+            load_f32<8>(row + p.R / 2 + a, s);
+          }
+        }
+      }
+      float wa[8] = {}, wb[8] = {};
+      if (a >= 0) load_w<8>(w, p.w_f32, a, wa);
+      if (b >= 0) load_w<8>(w, p.w_f32, b, wb);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if constexpr (INTERLEAVED) {
+          ca[j] = wa[j] * c[j / 2];
+          cb[j] = wb[j] * c[4 + j / 2];
+          sa[j] = (j & 1) ? wa[j ^ 1] * s[j / 2] : -wa[j ^ 1] * s[j / 2];
+          sb[j] = (j & 1) ? wb[j ^ 1] * s[4 + j / 2] : -wb[j ^ 1] * s[4 + j / 2];
+        } else {
+          ca[j] = wa[j] * c[j];
+          cb[j] = wb[j] * c[j];
+          sa[j] = -wb[j] * s[j];
+          sb[j] = wa[j] * s[j];
+        }
+      }
+    }
+    copy_wait<kAhead>();
+    float fa[8] = {}, fb[8] = {};
+    if (on && a >= 0) unpack8(ring[i % kRing][0][threadIdx.x], fa);
+    if (on && b >= 0) unpack8(ring[i % kRing][1][threadIdx.x], fb);
+    float ss = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss += fa[j] * fa[j] + fb[j] * fb[j];
+    for (int off = L >> 1; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+    const float scale = rsqrtf(ss * inv_d + p.eps);
+    if (on) {
+      float oa[8], ob[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float pa = INTERLEAVED ? fa[j ^ 1] : fb[j], pb = INTERLEAVED ? fb[j ^ 1] : fa[j];
+        oa[j] = scale * (fa[j] * ca[j] + pa * sa[j]);
+        ob[j] = scale * (fb[j] * cb[j] + pb * sb[j]);
+      }
+      __nv_bfloat16* out = is_k ? p.k_out + now.t * p.ko_t + (now.h - p.Hq) * p.ko_h
+                                : p.q_out + now.t * p.qo_t + now.h * p.qo_h;
+      if (a >= 0) *reinterpret_cast<uint4*>(out + a) = pack8(oa);
+      if (b >= 0) *reinterpret_cast<uint4*>(out + b) = pack8(ob);
+    }
+  }
+}
+
+// Any alignment: V values per piece, NU units per lane.
+template <int V, int NU>
+__global__ void __launch_bounds__(256) qk_norm_rope_any_kernel(const QkParams p) {
+  if (blockIdx.x == gridDim.x - 1) {
+    check_positions(p);
+    return;
+  }
+  const int lane = threadIdx.x & 31;
+  const long long warp = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
   const long long t = warp / p.splits;
   if (t >= p.T) return;   // whole warps
   const int part = static_cast<int>(warp - t * p.splits);
@@ -286,24 +487,44 @@ extern "C" moe_lora_status moe_lora_qk_norm_rope(moe_lora_handle* h, const moe_l
   const int units = (p.D + 2 * V - 1) / (2 * V);
   p.lanes = 1;
   while (p.lanes < units && p.lanes < 32) p.lanes *= 2;
-  // a warp takes a token's heads in turn; short batches spread them over more warps
+  p.table_vec = p.table_t % 4 == 0 && p.R % 8 == 0 && aligned16(p.table);
   const int per = 32 / p.lanes;
-  const int rounds = (H + per - 1) / per;   // warp rounds per token
-  int splits = static_cast<int>(std::min<long long>(rounds, (16LL * h->num_sms + a->T - 1) / a->T));
-  if (splits < 1) splits = 1;
-  p.heads_per_warp = (rounds + splits - 1) / splits * per;
-  p.splits = (H + p.heads_per_warp - 1) / p.heads_per_warp;
-  const long long warps = static_cast<long long>(p.T) * p.splits;
+  p.token_rounds = (H + per - 1) / per;
+  long long warps;
+  if (V == 8) {
+    // heads that would leave half of a token's rounds idle are packed, whatever their token
+    p.packed = 2 * H <= p.token_rounds * per;
+    p.step_t = per / H;
+    p.step_h = per % H;
+    const long long tasks = static_cast<long long>(a->T) * H;
+    const long long rounds = p.packed ? (tasks + per - 1) / per : static_cast<long long>(a->T) * p.token_rounds;
+    if (rounds * per > 0x7fffffffLL) return MOE_LORA_ERR_INVALID_ARG;
+    // as many warps as the GPU holds (three blocks of eight an SM), each a run of rounds
+    const long long most = 24LL * h->num_sms;
+    p.rounds = static_cast<unsigned>(rounds);
+    p.run = static_cast<unsigned>((rounds + most - 1) / most);
+    warps = (rounds + p.run - 1) / p.run;
+  } else {
+    // a warp takes a token's heads in turn, short batches spread them over more warps
+    int splits = static_cast<int>(std::min<long long>(p.token_rounds, (16LL * h->num_sms + a->T - 1) / a->T));
+    if (splits < 1) splits = 1;
+    p.heads_per_warp = (p.token_rounds + splits - 1) / splits * per;
+    p.splits = (H + p.heads_per_warp - 1) / p.heads_per_warp;
+    warps = static_cast<long long>(p.T) * p.splits;
+  }
   const int block = warps < 4LL * h->num_sms ? 32 : 256;
   const long long blocks = (warps * 32 + block - 1) / block + 1;   // and the positions' check
   if (blocks > 0x7fffffffLL) return MOE_LORA_ERR_INVALID_ARG;
   const dim3 grid(static_cast<unsigned>(blocks)), threads(block);
   cudaError_t err;
   switch (V) {
-    case 8: err = launch_k(qk_norm_rope_kernel<8, 1>, grid, threads, 0, stream, false, p); break;
-    case 4: err = launch_k(qk_norm_rope_kernel<4, 2>, grid, threads, 0, stream, false, p); break;
-    case 2: err = launch_k(qk_norm_rope_kernel<2, 4>, grid, threads, 0, stream, false, p); break;
-    default: err = launch_k(qk_norm_rope_kernel<1, 8>, grid, threads, 0, stream, false, p); break;
+    case 8:
+      err = p.interleaved ? launch_k(qk_norm_rope_kernel<true>, grid, threads, 0, stream, false, p)
+                          : launch_k(qk_norm_rope_kernel<false>, grid, threads, 0, stream, false, p);
+      break;
+    case 4: err = launch_k(qk_norm_rope_any_kernel<4, 2>, grid, threads, 0, stream, false, p); break;
+    case 2: err = launch_k(qk_norm_rope_any_kernel<2, 4>, grid, threads, 0, stream, false, p); break;
+    default: err = launch_k(qk_norm_rope_any_kernel<1, 8>, grid, threads, 0, stream, false, p); break;
   }
   ML_LAUNCH(h, err, "qk_norm_rope launch");
   return MOE_LORA_OK;

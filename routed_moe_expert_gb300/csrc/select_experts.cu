@@ -8,14 +8,17 @@
 //   w_j   = s of id j (0 where its key is -inf) [/ sum of these] * factor
 //
 // Every value that decides a choice is one float32 operation sequence that no order of
-// threads changes: the exponentials and divisions are IEEE float32 operations of one lane,
-// and the softmax sum is taken in fixed point with steps of 2^-52 (the terms lie in [0, 1],
-// so 1024 of them fit 64 bits), exact for every term of 2^-28 and more.
+// threads changes: exponentials and quotients are IEEE float32 results, and the softmax sum is
+// taken in fixed point with steps of 2^-52 (the terms lie in [0, 1], so 1024 of them fit 64
+// bits), exact for every term of 2^-28 and more.
 //
-// A lane holds NQ chunks of V consecutive experts, so loads are one vector per chunk and a
-// chunk lies in one group.  A pick is a warp maximum over order-preserving unsigned keys and
-// a warp minimum over the ids that hold it (redux.sync), then the owning lane alone looks
-// through its values again.
+// A lane holds NQ chunks of V consecutive experts, so loads are one vector per chunk and, where
+// groups are a power of two of chunks, a group's best is a few shuffles among neighbouring
+// lanes.  The choice itself: the top_k-th largest of the lanes' best keys is a bound below which
+// nothing is chosen; the (few) keys on or above it are handed to one lane each, and top_k rounds
+// of a warp maximum and a warp minimum of the ids that hold it put them in order.  That takes a
+// third of the instructions of looking through the lane's values again after every pick
+// (1426 -> 470 a token at E 256, top_k 6), and instruction issue is what bounds long batches.
 #include "common.cuh"
 #include "host.h"
 #include "kernels.h"
@@ -39,15 +42,13 @@ namespace {
 
 constexpr int kSelectMaxGroups = 32;   // a lane per group
 
-// Unsigned integer with the order of the float keys; 0 is free for "taken".
-MLDEV uint32_t ordered(float f) {
-  uint32_t u = __float_as_uint(f);
-  if (u == 0x80000000u) u = 0u;   // -0 and +0 are equal
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-constexpr uint32_t kRuledOut = 0x007fffffu;   // ordered(-inf)
+constexpr unsigned kAll = 0xffffffffu;
 
-MLDEV float unordered(uint32_t v) { return __uint_as_float((v & 0x80000000u) ? (v & 0x7fffffffu) : ~v); }
+MLDEV float warp_max(float v) {
+  float m;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+  return m;
+}
 
 // A logit as it counts: NaN is a ruled-out expert, +inf the largest finite value.
 MLDEV float usable(float z) { return (z != z) ? -INFINITY : fminf(z, FLT_MAX); }
@@ -82,157 +83,275 @@ MLDEV unsigned long long warp_sum_u58(unsigned long long v) {
   return a + (static_cast<unsigned long long>(b) << 26) + (static_cast<unsigned long long>(c) << 52);
 }
 
-MLDEV float exp_above(float z, float zmax) { return z == -INFINITY ? 0.0f : expf(__fsub_rn(z, zmax)); }
+// Scores of a token's logits: what its softmax divides by, or nothing (sigmoid).
+struct Scoring {
+  bool sigmoid;
+  float zmax, total;   // softmax: the largest logit (0 when all are ruled out) and the sum
+  MLDEV float numerator(float z) const { return expf(__fsub_rn(z, zmax)); }
+  MLDEV float operator()(float z) const {
+    if (sigmoid) return __frcp_rn(__fadd_rn(1.0f, expf(-z)));
+    return total > 0.0f ? __fdiv_rn(numerator(z), total) : 0.0f;
+  }
+};
 
-template <typename TL, int NQ, int V>
+// Keys (and their ids) on or above a bound, one per lane, for the ordered choice.
+constexpr int kCandidates = 32;
+
+// GROUPS: 0 no groups, 1 groups of 2^n chunks (shuffles), 2 any groups (a warp maximum each).
+template <typename TL, int NQ, int V, int GROUPS>
 __global__ void __launch_bounds__(256) select_experts_kernel(const SelectParams p) {
+  constexpr int NV = NQ * V;
+  __shared__ float2 cand_s[8][kCandidates];
   const int lane = threadIdx.x & 31;
   const int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (t >= p.T) return;   // whole warps
+  float2* cand = cand_s[threadIdx.x >> 5];
   const TL* row = static_cast<const TL*>(p.logits) + static_cast<long long>(t) * p.stride;
-  constexpr unsigned kAll = 0xffffffffu;
+  auto id_of = [&](int n) -> int { return ((n / V) * 32 + lane) * V + n % V; };   // lane's n-th value
 
-  float z[NQ][V];
+  float key[NV];   // logits, then scores, then keys; -inf: ruled out
 #pragma unroll
   for (int i = 0; i < NQ; ++i) {
+    float z[V];
     const int e = (i * 32 + lane) * V;   // V == 4: E is a multiple of 4
     if (e < p.E) {
-      load_logits<TL, V>(row, e, z[i]);
+      load_logits<TL, V>(row, e, z);
     } else {
 #pragma unroll
-      for (int v = 0; v < V; ++v) z[i][v] = -INFINITY;
+      for (int v = 0; v < V; ++v) z[v] = -INFINITY;
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v) z[i][v] = usable(z[i][v]);
+    for (int v = 0; v < V; ++v) key[i * V + v] = usable(z[v]);
   }
 
-  // scores and keys
-  uint32_t key[NQ][V];
-  float zmax = 0.0f, total = 1.0f;
-  if (!p.sigmoid) {
-    uint32_t m = 0;
+  Scoring score = {p.sigmoid != 0, 0.0f, 1.0f};
+  uint32_t out[(NV + 31) / 32] = {};   // ruled-out values of this lane
 #pragma unroll
-    for (int i = 0; i < NQ; ++i)
+  for (int n = 0; n < NV; ++n)
+    if (key[n] == -INFINITY) out[n / 32] |= 1u << (n % 32);
+  if (!score.sigmoid) {
+    float m = key[0];
 #pragma unroll
-      for (int v = 0; v < V; ++v) m = max(m, ordered(z[i][v]));
-    zmax = unordered(__reduce_max_sync(kAll, m));
+    for (int n = 1; n < NV; ++n) m = fmaxf(m, key[n]);
+    m = warp_max(m);
+    score.zmax = m == -INFINITY ? 0.0f : m;   // (all ruled out: every term is exp(-inf) = 0)
     unsigned long long sum = 0;
+    uint32_t least = 0xffffffffu;   // bits of the smallest nonzero term, less 1
 #pragma unroll
-    for (int i = 0; i < NQ; ++i)
+    for (int n = 0; n < NV; ++n) {
+      key[n] = score.numerator(key[n]);
+      least = min(least, __float_as_uint(key[n]) - 1u);
+      sum += __float2ull_rz(key[n] * 0x1p52f);
+    }
+    score.total = __ull2float_rn(warp_sum_u58(sum)) * 0x1p-52f;
+    // e / total, correctly rounded: with r the correctly rounded reciprocal, one residual makes
+    // q = e r exact (P. Markstein, "Computation of elementary functions on the IBM RISC System/6000
+    // processor", IBM J. Res. Dev. 34, 1990) while the residual does not underflow; with smaller
+    // nonzero terms all take the division.
+    if (least >= __float_as_uint(0x1p-100f)) {
+      const float r = __frcp_rn(score.total);
 #pragma unroll
-      for (int v = 0; v < V; ++v) sum += __float2ull_rz(exp_above(z[i][v], zmax) * 0x1p52f);
-    total = __ull2float_rn(warp_sum_u58(sum)) * 0x1p-52f;   // 0 only when every expert is ruled out
-  }
-  auto score = [&](float zz) -> float {
-    if (p.sigmoid) return __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-zz)));
-    return total > 0.0f ? __fdiv_rn(exp_above(zz, zmax), total) : 0.0f;
-  };
-#pragma unroll
-  for (int i = 0; i < NQ; ++i) {
-    const int e = (i * 32 + lane) * V;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      if (e < p.E) {
-        float f = score(z[i][v]);
-        if (p.bias != nullptr) f = __fadd_rn(f, __ldg(p.bias + e + v));
-        key[i][v] = (z[i][v] == -INFINITY || f != f) ? kRuledOut : ordered(f);
-      } else {
-        key[i][v] = 0u;
+      for (int n = 0; n < NV; ++n) {
+        const float q = __fmul_rn(key[n], r);
+        key[n] = __fmaf_rn(__fmaf_rn(-q, score.total, key[n]), r, q);
       }
+    } else {
+#pragma unroll
+      for (int n = 0; n < NV; ++n) key[n] = score.total > 0.0f ? __fdiv_rn(key[n], score.total) : 0.0f;
+    }
+  } else {
+#pragma unroll
+    for (int n = 0; n < NV; ++n) key[n] = score(key[n]);
+  }
+  if (p.bias != nullptr) {
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+      const int e = id_of(n);
+      if (e < p.E) key[n] = __fadd_rn(key[n], __ldg(p.bias + e));
     }
   }
+#pragma unroll
+  for (int n = 0; n < NV; ++n)   // (a NaN bias rules out as well)
+    if (((out[n / 32] >> (n % 32)) & 1u) || key[n] != key[n]) key[n] = -INFINITY;
 
-  if (p.n_group > 1) {
-    // each chunk's best two keys (a chunk lies in one group), then a warp maximum per group
-    uint32_t b1[NQ], b2[NQ];
-    int group[NQ];
+  if constexpr (GROUPS != 0) {
+    // the best two keys of each chunk (it lies in one group)
+    float b1[NQ], b2[NQ];
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
-      const int e = (i * 32 + lane) * V;
-      group[i] = e < p.E ? e / p.group_size : -1;
-      b1[i] = key[i][0];
-      b2[i] = 0u;
+      b1[i] = key[i * V];
+      b2[i] = -INFINITY;
 #pragma unroll
       for (int v = 1; v < V; ++v) {
-        b2[i] = max(b2[i], min(b1[i], key[i][v]));
-        b1[i] = max(b1[i], key[i][v]);
+        b2[i] = fmaxf(b2[i], fminf(b1[i], key[i * V + v]));
+        b1[i] = fmaxf(b1[i], key[i * V + v]);
       }
     }
-    uint32_t mine = 0u;   // lane g: the order key of group g's score
-    for (int g = 0; g < p.n_group; ++g) {
-      uint32_t l1 = 0u, l2 = 0u;
+    float mine = -INFINITY;   // lane g: group g's score
+    if constexpr (GROUPS == 1) {
+      const int width = p.group_size / V;   // chunks (lanes) of a group: 2^n <= 32
+      for (int off = 1; off < width; off *= 2) {
 #pragma unroll
-      for (int i = 0; i < NQ; ++i) {
-        if (group[i] == g) {
-          l2 = max(max(l2, b2[i]), min(l1, b1[i]));
-          l1 = max(l1, b1[i]);
+        for (int i = 0; i < NQ; ++i) {
+          const float o1 = __shfl_xor_sync(kAll, b1[i], off);
+          if (p.top2) {
+            const float o2 = __shfl_xor_sync(kAll, b2[i], off);
+            b2[i] = fmaxf(fmaxf(b2[i], o2), fminf(b1[i], o1));
+          }
+          b1[i] = fmaxf(b1[i], o1);
         }
       }
-      const uint32_t m1 = __reduce_max_sync(kAll, l1);
-      uint32_t score_g = m1;
-      if (p.top2) {
-        const unsigned owners = __ballot_sync(kAll, l1 == m1);
-        const uint32_t m2 = __reduce_max_sync(kAll, lane == __ffs(owners) - 1 ? l2 : l1);
-        const float f = __fadd_rn(unordered(m1), unordered(m2));
-        score_g = f != f ? kRuledOut : ordered(f);
+      const int first = lane * width;   // group g's first chunk
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) {
+        const float own = p.top2 ? __fadd_rn(b1[i], b2[i]) : b1[i];
+        const float of = __shfl_sync(kAll, own, first & 31);
+        if ((first >> 5) == i) mine = of;
       }
-      if (lane == g) mine = score_g;
+    } else {
+      for (int g = 0; g < p.n_group; ++g) {
+        float l1 = -INFINITY, l2 = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+          if ((i * 32 + lane) * V / p.group_size == g) {
+            l2 = fmaxf(fmaxf(l2, b2[i]), fminf(l1, b1[i]));
+            l1 = fmaxf(l1, b1[i]);
+          }
+        }
+        const float m1 = warp_max(l1);
+        float s = m1;
+        if (p.top2) {
+          const int owner = __ffs(__ballot_sync(kAll, l1 == m1)) - 1;
+          s = __fadd_rn(m1, warp_max(lane == owner ? l2 : l1));
+        }
+        if (lane == g) mine = s;
+      }
     }
-    unsigned stay = 0;
+    if (mine != mine) mine = -INFINITY;   // +inf (a bias) and a ruled-out second
+    unsigned stay = 0;   // ties, also of groups without an expert left: the lower group
+    bool taken = lane >= p.n_group;
     for (int j = 0; j < p.topk_group; ++j) {
-      const uint32_t m = __reduce_max_sync(kAll, mine);
-      const int g = __ffs(__ballot_sync(kAll, mine == m)) - 1;   // the lowest group that holds it
+      const float m = warp_max(taken ? -INFINITY : mine);
+      const int g = __ffs(__ballot_sync(kAll, !taken && mine == m)) - 1;
       stay |= 1u << g;
-      if (lane == g) mine = 0u;
+      taken |= lane == g;
     }
 #pragma unroll
     for (int i = 0; i < NQ; ++i)
-      if (group[i] >= 0 && !((stay >> group[i]) & 1u)) {
+      if (!((stay >> ((i * 32 + lane) * V / p.group_size & 31)) & 1u)) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) key[i][v] = kRuledOut;
+        for (int v = 0; v < V; ++v) key[i * V + v] = -INFINITY;
       }
   }
 
-  // top_k: lane j keeps pick j
-  int my_id = 0;
-  uint32_t my_key = 0u;
-  uint32_t best = 0u;   // this lane's largest key and the lowest id that holds it
-  int best_id = 0;
-  auto look = [&]() {
-    best = 0u;
+  // the bound: the top_k-th largest of the lanes' best keys (-inf when fewer lanes have one)
+  float best = key[0];
 #pragma unroll
-    for (int i = 0; i < NQ; ++i)
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (key[i][v] > best) {
-          best = key[i][v];
-          best_id = (i * 32 + lane) * V + v;
-        }
-  };
-  look();
-  for (int j = 0; j < p.k; ++j) {
-    const uint32_t m = __reduce_max_sync(kAll, best);
-    const int id = __reduce_min_sync(kAll, best == m ? best_id : 0x7fffffff);
-    if (lane == j) {
-      my_id = id;
-      my_key = m;
+  for (int n = 1; n < NV; ++n) best = fmaxf(best, key[n]);
+  float bound = -INFINITY;
+  {
+    float left = best;
+    for (int j = 0; j < p.k; ++j) {
+      bound = warp_max(left);
+      if (bound == -INFINITY) break;
+      if (lane == __ffs(__ballot_sync(kAll, left == bound)) - 1) left = -INFINITY;
     }
-    if (best == m && best_id == id) {   // the owner
+  }
+  // candidates: keys on or above the bound (all that is left when there is no bound)
+  int count = 0;
+  if (bound > -INFINITY) {
 #pragma unroll
-      for (int i = 0; i < NQ; ++i)
+    for (int n = 0; n < NV; ++n) {
+      const bool in = key[n] >= bound;
+      const unsigned who = __ballot_sync(kAll, in);
+      const int at = count + __popc(who & ((1u << lane) - 1u));
+      if (in && at < kCandidates) cand[at] = make_float2(key[n], __int_as_float(id_of(n)));
+      count += __popc(who);
+    }
+  } else {
+    count = kCandidates + 1;
+  }
+  int my_id = 0, chosen = 0;   // lane j keeps pick j
+  if (count <= kCandidates) {
+    __syncwarp();
+    const float2 c = lane < count ? cand[lane] : make_float2(-INFINITY, 0.0f);
+    float left = c.x;
+    const int id = __float_as_int(c.y);
+    for (int j = 0; j < p.k; ++j) {   // count >= top_k: the bound's lanes alone give that many
+      const float m = warp_max(left);
+      const int pick = __reduce_min_sync(kAll, left == m ? id : 0x7fffffff);
+      if (lane == j) my_id = pick;
+      if (left == m && id == pick) left = -INFINITY;
+    }
+    chosen = p.k;
+  } else {
+    // many equal keys, or fewer lanes with an expert left than top_k: pick by pick
+    int best_n = 0;
+    auto look = [&]() {
+      best = -INFINITY;
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-          if ((i * 32 + lane) * V + v == id) key[i][v] = 0u;
-      look();
+      for (int n = 0; n < NV; ++n)
+        if (key[n] > best) {
+          best = key[n];
+          best_n = n;
+        }
+    };
+    // ids of a lane ascend with n, so the first of its equal keys is its lowest id
+    uint32_t gone[(NV + 31) / 32] = {};
+    look();
+    for (; chosen < p.k; ++chosen) {
+      const float m = warp_max(best);
+      if (m == -INFINITY) break;
+      const int mine = id_of(0) + (best_n / V) * 32 * V + best_n % V;
+      const int pick = __reduce_min_sync(kAll, best == m ? mine : 0x7fffffff);
+      if (lane == chosen) my_id = pick;
+      if (best == m && mine == pick) {
+#pragma unroll
+        for (int n = 0; n < NV; ++n)
+          if (n == best_n) {
+            key[n] = -INFINITY;
+            gone[n / 32] |= 1u << (n % 32);
+          }
+        look();
+      }
+    }
+    // the rest: the lowest ids that are ruled out, in order, with weight 0
+    int next = chosen;
+    for (int i = 0; i < NQ && next < p.k; ++i) {
+      int mine = 0;   // this lane's ruled-out values of chunk i
+#pragma unroll
+      for (int n = 0; n < NV; ++n)
+        if (n / V == i) mine += id_of(n) < p.E && !((gone[n / 32] >> (n % 32)) & 1u);
+      int incl = mine;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(kAll, incl, off);
+        if (lane >= off) incl += y;
+      }
+      int at = next + incl - mine;
+#pragma unroll
+      for (int n = 0; n < NV; ++n)
+        if (n / V == i && id_of(n) < p.E && !((gone[n / 32] >> (n % 32)) & 1u)) {
+          if (at < p.k) {
+            const float w = __fmul_rn(0.0f, p.factor);
+            const long long o = static_cast<long long>(t) * p.k + at;
+            p.ids[o] = id_of(n);
+            p.weights[o] = w;
+            if (p.packed != nullptr)
+              p.packed[o] = (id_of(n) << 16) | static_cast<int>(__bfloat16_as_ushort(f2bf(w)));
+          }
+          ++at;
+        }
+      next += __shfl_sync(kAll, incl, 31);
     }
   }
 
   // weights: lane j's score again, from its logit
   float w = 0.0f;
-  if (lane < p.k && my_key > kRuledOut) {
-    float zz[1];
-    load_logits<TL, 1>(row, my_id, zz);
-    w = score(usable(zz[0]));
+  if (lane < chosen) {
+    float z[1];
+    load_logits<TL, 1>(row, my_id, z);
+    w = score(usable(z[0]));
   }
   if (p.renormalize) {
     float sum = w;
@@ -241,7 +360,7 @@ __global__ void __launch_bounds__(256) select_experts_kernel(const SelectParams 
     w = sum > 0.0f ? __fdiv_rn(w, sum) : 0.0f;
   }
   w = __fmul_rn(w, p.factor);
-  if (lane < p.k) {
+  if (lane < chosen) {
     const long long at = static_cast<long long>(t) * p.k + lane;
     p.ids[at] = my_id;
     p.weights[at] = w;
@@ -255,17 +374,29 @@ cudaError_t launch_select(const SelectParams& p, bool vec, cudaStream_t stream) 
   // one warp per block while that leaves SMs idle, then eight
   const int warps = p.T <= 1024 ? 1 : 8;
   const dim3 grid((p.T + warps - 1) / warps), block(32 * warps);
-#define ML_SELECT(NQ, V) \
-  return launch_k(select_experts_kernel<TL, NQ, V>, grid, block, 0, stream, false, p)
+  const int width = p.group_size / 4;   // chunks of a group on the vector path
+  const int groups = p.n_group == 1 ? 0 : vec && width <= 32 && (width & (width - 1)) == 0 ? 1 : 2;
+#define ML_SELECT(NQ, V, G) return launch_k(select_experts_kernel<TL, NQ, V, G>, grid, block, 0, stream, false, p)
+#define ML_SELECT_G(NQ)              \
+  do {                               \
+    if (groups == 0) ML_SELECT(NQ, 4, 0); \
+    if (groups == 1) ML_SELECT(NQ, 4, 1); \
+    ML_SELECT(NQ, 4, 2);             \
+  } while (0)
   if (vec) {
-    if (p.E <= 128) ML_SELECT(1, 4);
-    if (p.E <= 256) ML_SELECT(2, 4);
-    if (p.E <= 384) ML_SELECT(3, 4);
-    if (p.E <= 512) ML_SELECT(4, 4);
-    ML_SELECT(8, 4);
+    if (p.E <= 128) ML_SELECT_G(1);
+    if (p.E <= 256) ML_SELECT_G(2);
+    if (p.E <= 384) ML_SELECT_G(3);
+    if (p.E <= 512) ML_SELECT_G(4);
+    ML_SELECT_G(8);
   }
-  if (p.E <= 256) ML_SELECT(8, 1);
-  ML_SELECT(32, 1);
+  if (p.E <= 256) {
+    if (groups == 0) ML_SELECT(8, 1, 0);
+    ML_SELECT(8, 1, 2);
+  }
+  if (groups == 0) ML_SELECT(32, 1, 0);
+  ML_SELECT(32, 1, 2);
+#undef ML_SELECT_G
 #undef ML_SELECT
 }
 
