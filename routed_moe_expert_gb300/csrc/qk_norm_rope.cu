@@ -26,6 +26,7 @@
 #include "kernels.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace mlk {
 
@@ -140,10 +141,55 @@ MLDEV void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); 
 template <int N>
 MLDEV void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
+// Two float32 operations in one instruction.
+struct F2 {
+  unsigned long long v;
+};
+MLDEV F2 pair_of(float x, float y) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+  return r;
+}
+MLDEV float2 floats_of(F2 x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x.v));
+  return r;
+}
+MLDEV F2 mul2(F2 x, F2 y) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(x.v), "l"(y.v));
+  return r;
+}
+MLDEV F2 fma2(F2 x, F2 y, F2 z) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(x.v), "l"(y.v), "l"(z.v));
+  return r;
+}
+MLDEV F2 swapped(F2 x) {
+  const float2 f = floats_of(x);
+  return pair_of(f.y, f.x);
+}
+MLDEV void unpack_pairs(const uint4& x, F2 (&f)[4]) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = pair_of(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+MLDEV uint4 pack_pairs(const F2 (&f)[4]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = floats_of(f[i]);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // The aligned case: a lane's 16 values of a head are two 16-byte pieces.  A round is one head per
 // lane group: 32 / L heads of a token (the rest of a token's last round idle), or, with few heads
 // (`packed`), any 32 / L consecutive (token, head) pairs.  Each warp takes a run of rounds.
-template <bool INTERLEAVED>
+// LANES > 0: that many lanes per head, each with both pieces (D = 16 LANES); 0: as p says.
+template <bool INTERLEAVED, int LANES>
 __global__ void __launch_bounds__(256, 3) qk_norm_rope_kernel(const QkParams p) {
   if (blockIdx.x == gridDim.x - 1) {
     check_positions(p);
@@ -153,11 +199,11 @@ __global__ void __launch_bounds__(256, 3) qk_norm_rope_kernel(const QkParams p) 
   const int lane = threadIdx.x & 31;
   const unsigned warp = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   const int H = p.Hq + p.Hk;
-  const int L = p.lanes, per = 32 / L, group = lane / L, sub = lane & (L - 1);
+  const int L = LANES > 0 ? LANES : p.lanes, per = 32 / L, group = lane / L, sub = lane & (L - 1);
   const unsigned g0 = min(warp * p.run, p.rounds), g1 = min(g0 + p.run, p.rounds);
   const int n = static_cast<int>(g1 - g0);   // rounds of this warp
 
-  // this lane's pieces (-1: none)
+  // this lane's pieces (has_a, has_b: they lie in the head)
   int a, b;
   bool turned;
   if constexpr (INTERLEAVED) {
@@ -170,20 +216,24 @@ __global__ void __launch_bounds__(256, 3) qk_norm_rope_kernel(const QkParams p) 
     a = turned ? sub * 8 : p.R + (sub - rot) * 16;
     b = turned ? a + (p.R >> 1) : a + 8;
   }
-  if (a >= p.D) a = -1;
-  if (b >= p.D) b = -1;
+  const bool has_a = LANES > 0 || a < p.D, has_b = LANES > 0 || b < p.D;
 
-  // a lane group's (token, head) in round g0, and its step from round to round
+  // a lane group's place: (token, head) and where the head's values are read and written
   struct At {
     int t, h;
+    const __nv_bfloat16* in;
+    __nv_bfloat16* out;
   };
-  auto first = [&]() -> At {
-    if (p.packed) {
-      const unsigned task = g0 * per + group;
-      return {static_cast<int>(task / H), static_cast<int>(task % H)};
+  auto settle = [&](At& x) {
+    if (x.h < p.Hq) {
+      x.in = p.q + x.t * p.q_t + x.h * p.q_h;
+      x.out = p.q_out + x.t * p.qo_t + x.h * p.qo_h;
+    } else {
+      x.in = p.k + x.t * p.k_t + (x.h - p.Hq) * p.k_h;
+      x.out = p.k_out + x.t * p.ko_t + (x.h - p.Hq) * p.ko_h;
     }
-    return {static_cast<int>(g0 / p.token_rounds), static_cast<int>(g0 % p.token_rounds) * per + group};
   };
+  const long long in_step = per * p.q_h, out_step = per * p.qo_h;
   auto next = [&](At& x) {
     if (p.packed) {
       x.t += p.step_t;
@@ -192,25 +242,38 @@ __global__ void __launch_bounds__(256, 3) qk_norm_rope_kernel(const QkParams p) 
         x.h -= H;
         ++x.t;
       }
+      settle(x);
     } else {
       x.h += per;
-      if (x.h - group >= H) {
-        x.h = group;
-        ++x.t;
+      if (x.h < p.Hq) {
+        x.in += in_step;
+        x.out += out_step;
+      } else {
+        if (x.h - group >= H) {
+          x.h = group;
+          ++x.t;
+        }
+        settle(x);
       }
     }
   };
   auto live = [&](const At& x) -> bool { return x.h < H && x.t < p.T; };
-  auto head_in = [&](const At& x) -> const __nv_bfloat16* {
-    return x.h < p.Hq ? p.q + x.t * p.q_t + x.h * p.q_h : p.k + x.t * p.k_t + (x.h - p.Hq) * p.k_h;
-  };
-  At now = first(), ahead = now;
+  At now;
+  if (p.packed) {
+    const unsigned task = g0 * per + group;
+    now.t = static_cast<int>(task / H);
+    now.h = static_cast<int>(task % H);
+  } else {
+    now.t = static_cast<int>(g0 / p.token_rounds);
+    now.h = static_cast<int>(g0 % p.token_rounds) * per + group;
+  }
+  settle(now);
+  At ahead = now;
   int fetched = 0;
   auto fetch = [&]() {   // the copies of the next round not yet on its way
     if (fetched < n && live(ahead)) {
-      const __nv_bfloat16* x = head_in(ahead);
-      if (a >= 0) copy16(&ring[fetched % kRing][0][threadIdx.x], x + a);
-      if (b >= 0) copy16(&ring[fetched % kRing][1][threadIdx.x], x + b);
+      if (has_a) copy16(&ring[fetched % kRing][0][threadIdx.x], ahead.in + a);
+      if (has_b) copy16(&ring[fetched % kRing][1][threadIdx.x], ahead.in + b);
     }
     copy_commit();
     ++fetched;
@@ -219,8 +282,8 @@ __global__ void __launch_bounds__(256, 3) qk_norm_rope_kernel(const QkParams p) 
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) fetch();
 
-  float ca[8], sa[8], cb[8], sb[8];   // coefficients of the own value and of the partner
-  int kind = -1, token = -1;          // the heads they are for: 0 query, 1 key; of which token
+  F2 ca[4], sa[4], cb[4], sb[4];   // coefficients of the own values and of the partners
+  int kind = -1, token = -1;       // the heads they are for: 0 query, 1 key; of which token
   const float inv_d = 1.0f / static_cast<float>(p.D);
 
   for (int i = 0; i < n; ++i, next(now)) {
@@ -243,75 +306,74 @@ __global__ void __launch_bounds__(256, 3) qk_norm_rope_kernel(const QkParams p) 
       }
       if (pos >= 0 && pos < p.num_positions) {
         const float* row = p.table + pos * p.table_t;
-        if constexpr (INTERLEAVED) {
-          if (a >= 0 && a < p.R) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              c[j] = __ldg(row + a / 2 + j);
-              s[j] = __ldg(row + p.R / 2 + a / 2 + j);
-            }
-          }
-          if (b >= 0 && b < p.R) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              c[4 + j] = __ldg(row + b / 2 + j);
-              s[4 + j] = __ldg(row + p.R / 2 + b / 2 + j);
-            }
-          }
-        } else if (turned) {
+        auto angles = [&](int at, float* cp, float* sp, auto count) {
+          constexpr int kN = decltype(count)::value;
           if (p.table_vec) {
 #pragma unroll
-            for (int j = 0; j < 8; j += 4) {
-              const float4 cv = __ldg(reinterpret_cast<const float4*>(row + a + j));
-              const float4 sv = __ldg(reinterpret_cast<const float4*>(row + p.R / 2 + a + j));
-              c[j] = cv.x, c[j + 1] = cv.y, c[j + 2] = cv.z, c[j + 3] = cv.w;
-              s[j] = sv.x, s[j + 1] = sv.y, s[j + 2] = sv.z, s[j + 3] = sv.w;
+            for (int j = 0; j < kN; j += 4) {
+              const float4 cv = __ldg(reinterpret_cast<const float4*>(row + at + j));
+              const float4 sv = __ldg(reinterpret_cast<const float4*>(row + p.R / 2 + at + j));
+              cp[j] = cv.x, cp[j + 1] = cv.y, cp[j + 2] = cv.z, cp[j + 3] = cv.w;
+              sp[j] = sv.x, sp[j + 1] = sv.y, sp[j + 2] = sv.z, sp[j + 3] = sv.w;
             }
           } else {
-            load_f32<8>(row + a, c);
-            load_f32<8>(row + p.R / 2 + a, s);
+#pragma unroll
+            for (int j = 0; j < kN; ++j) {
+              cp[j] = __ldg(row + at + j);
+              sp[j] = __ldg(row + p.R / 2 + at + j);
+            }
           }
+        };
+        if constexpr (INTERLEAVED) {
+          if (a < p.R) angles(a / 2, c, s, std::integral_constant<int, 4>());
+          if (b < p.R) angles(b / 2, c + 4, s + 4, std::integral_constant<int, 4>());
+        } else if (turned) {
+          angles(a, c, s, std::integral_constant<int, 8>());
         }
       }
       float wa[8] = {}, wb[8] = {};
-      if (a >= 0) load_w<8>(w, p.w_f32, a, wa);
-      if (b >= 0) load_w<8>(w, p.w_f32, b, wb);
+      if (has_a) load_w<8>(w, p.w_f32, a, wa);
+      if (has_b) load_w<8>(w, p.w_f32, b, wb);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < 4; ++j) {   // values 2j and 2j + 1 of each piece
+        const int u = 2 * j, v = u + 1;
         if constexpr (INTERLEAVED) {
-          ca[j] = wa[j] * c[j / 2];
-          cb[j] = wb[j] * c[4 + j / 2];
-          sa[j] = (j & 1) ? wa[j ^ 1] * s[j / 2] : -wa[j ^ 1] * s[j / 2];
-          sb[j] = (j & 1) ? wb[j ^ 1] * s[4 + j / 2] : -wb[j ^ 1] * s[4 + j / 2];
+          ca[j] = pair_of(wa[u] * c[j], wa[v] * c[j]);
+          cb[j] = pair_of(wb[u] * c[4 + j], wb[v] * c[4 + j]);
+          sa[j] = pair_of(-wa[v] * s[j], wa[u] * s[j]);
+          sb[j] = pair_of(-wb[v] * s[4 + j], wb[u] * s[4 + j]);
         } else {
-          ca[j] = wa[j] * c[j];
-          cb[j] = wb[j] * c[j];
-          sa[j] = -wb[j] * s[j];
-          sb[j] = wa[j] * s[j];
+          ca[j] = pair_of(wa[u] * c[u], wa[v] * c[v]);
+          cb[j] = pair_of(wb[u] * c[u], wb[v] * c[v]);
+          sa[j] = pair_of(-wb[u] * s[u], -wb[v] * s[v]);
+          sb[j] = pair_of(wa[u] * s[u], wa[v] * s[v]);
         }
       }
     }
     copy_wait<kAhead>();
-    float fa[8] = {}, fb[8] = {};
-    if (on && a >= 0) unpack8(ring[i % kRing][0][threadIdx.x], fa);
-    if (on && b >= 0) unpack8(ring[i % kRing][1][threadIdx.x], fb);
-    float ss = 0.0f;
+    F2 fa[4] = {}, fb[4] = {};
+    if (on && has_a) unpack_pairs(ring[i % kRing][0][threadIdx.x], fa);
+    if (on && has_b) unpack_pairs(ring[i % kRing][1][threadIdx.x], fb);
+    F2 sq = {0ull};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) ss += fa[j] * fa[j] + fb[j] * fb[j];
-    for (int off = L >> 1; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+    for (int j = 0; j < 4; ++j) sq = fma2(fb[j], fb[j], fma2(fa[j], fa[j], sq));
+    const float2 both = floats_of(sq);
+    float ss = both.x + both.y;
+#pragma unroll
+    for (int off = (LANES > 0 ? LANES : 32) / 2; off > 0; off >>= 1)
+      if (LANES > 0 || off < L) ss += __shfl_xor_sync(0xffffffffu, ss, off);
     const float scale = rsqrtf(ss * inv_d + p.eps);
     if (on) {
-      float oa[8], ob[8];
+      const F2 scale2 = pair_of(scale, scale);
+      F2 oa[4], ob[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float pa = INTERLEAVED ? fa[j ^ 1] : fb[j], pb = INTERLEAVED ? fb[j ^ 1] : fa[j];
-        oa[j] = scale * (fa[j] * ca[j] + pa * sa[j]);
-        ob[j] = scale * (fb[j] * cb[j] + pb * sb[j]);
+      for (int j = 0; j < 4; ++j) {
+        const F2 pa = INTERLEAVED ? swapped(fa[j]) : fb[j], pb = INTERLEAVED ? swapped(fb[j]) : fa[j];
+        oa[j] = mul2(scale2, fma2(pa, sa[j], mul2(fa[j], ca[j])));
+        ob[j] = mul2(scale2, fma2(pb, sb[j], mul2(fb[j], cb[j])));
       }
-      __nv_bfloat16* out = is_k ? p.k_out + now.t * p.ko_t + (now.h - p.Hq) * p.ko_h
-                                : p.q_out + now.t * p.qo_t + now.h * p.qo_h;
-      if (a >= 0) *reinterpret_cast<uint4*>(out + a) = pack8(oa);
-      if (b >= 0) *reinterpret_cast<uint4*>(out + b) = pack8(ob);
+      if (has_a) *reinterpret_cast<uint4*>(now.out + a) = pack_pairs(oa);
+      if (has_b) *reinterpret_cast<uint4*>(now.out + b) = pack_pairs(ob);
     }
   }
 }
@@ -519,8 +581,14 @@ extern "C" moe_lora_status moe_lora_qk_norm_rope(moe_lora_handle* h, const moe_l
   cudaError_t err;
   switch (V) {
     case 8:
-      err = p.interleaved ? launch_k(qk_norm_rope_kernel<true>, grid, threads, 0, stream, false, p)
-                          : launch_k(qk_norm_rope_kernel<false>, grid, threads, 0, stream, false, p);
+#define ML_QK(LANES)                                                                        \
+  (p.interleaved ? launch_k(qk_norm_rope_kernel<true, LANES>, grid, threads, 0, stream, false, p) \
+                 : launch_k(qk_norm_rope_kernel<false, LANES>, grid, threads, 0, stream, false, p))
+      if (p.D == 64) err = ML_QK(4);
+      else if (p.D == 128) err = ML_QK(8);
+      else if (p.D == 256) err = ML_QK(16);
+      else err = ML_QK(0);
+#undef ML_QK
       break;
     case 4: err = launch_k(qk_norm_rope_any_kernel<4, 2>, grid, threads, 0, stream, false, p); break;
     case 2: err = launch_k(qk_norm_rope_any_kernel<2, 4>, grid, threads, 0, stream, false, p); break;

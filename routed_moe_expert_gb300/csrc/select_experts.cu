@@ -18,7 +18,7 @@
 // nothing is chosen; the (few) keys on or above it are handed to one lane each, and top_k rounds
 // of a warp maximum and a warp minimum of the ids that hold it put them in order.  That takes a
 // third of the instructions of looking through the lane's values again after every pick
-// (1426 -> 470 a token at E 256, top_k 6), and instruction issue is what bounds long batches.
+// (E 256, top_k 6), and instruction issue is what bounds long batches.
 #include "common.cuh"
 #include "host.h"
 #include "kernels.h"
@@ -34,6 +34,7 @@ struct SelectParams {
   float* weights;
   int32_t* packed;
   long long stride;      // elements between two tokens' logits
+  int bias_vec;          // bias starts on a 16-byte boundary
   int T, E, k, sigmoid, n_group, topk_group, top2, renormalize, group_size;
   float factor;
 };
@@ -50,8 +51,11 @@ MLDEV float warp_max(float v) {
   return m;
 }
 
-// A logit as it counts: NaN is a ruled-out expert, +inf the largest finite value.
-MLDEV float usable(float z) { return (z != z) ? -INFINITY : fminf(z, FLT_MAX); }
+// A logit as it counts: +inf is the largest finite value, a ruled-out expert (-inf or NaN) is NaN,
+// which maxima pass over and arithmetic keeps.
+MLDEV float usable(float z) {
+  return z == -INFINITY ? __int_as_float(0x7fffffff) : z == INFINITY ? FLT_MAX : z;
+}
 
 template <typename TL, int V>
 MLDEV void load_logits(const TL* row, int e, float (&z)[V]) {
@@ -86,11 +90,11 @@ MLDEV unsigned long long warp_sum_u58(unsigned long long v) {
 // Scores of a token's logits: what its softmax divides by, or nothing (sigmoid).
 struct Scoring {
   bool sigmoid;
-  float zmax, total;   // softmax: the largest logit (0 when all are ruled out) and the sum
+  float zmax, total;   // softmax: the largest logit and the sum
   MLDEV float numerator(float z) const { return expf(__fsub_rn(z, zmax)); }
   MLDEV float operator()(float z) const {
     if (sigmoid) return __frcp_rn(__fadd_rn(1.0f, expf(-z)));
-    return total > 0.0f ? __fdiv_rn(numerator(z), total) : 0.0f;
+    return __fdiv_rn(numerator(z), total);
   }
 };
 
@@ -109,7 +113,7 @@ __global__ void __launch_bounds__(256) select_experts_kernel(const SelectParams 
   const TL* row = static_cast<const TL*>(p.logits) + static_cast<long long>(t) * p.stride;
   auto id_of = [&](int n) -> int { return ((n / V) * 32 + lane) * V + n % V; };   // lane's n-th value
 
-  float key[NV];   // logits, then scores, then keys; -inf: ruled out
+  float key[NV];   // logits, then scores, then keys; NaN, in the end -inf: ruled out
 #pragma unroll
   for (int i = 0; i < NQ; ++i) {
     float z[V];
@@ -125,25 +129,20 @@ __global__ void __launch_bounds__(256) select_experts_kernel(const SelectParams 
   }
 
   Scoring score = {p.sigmoid != 0, 0.0f, 1.0f};
-  uint32_t out[(NV + 31) / 32] = {};   // ruled-out values of this lane
-#pragma unroll
-  for (int n = 0; n < NV; ++n)
-    if (key[n] == -INFINITY) out[n / 32] |= 1u << (n % 32);
   if (!score.sigmoid) {
     float m = key[0];
 #pragma unroll
     for (int n = 1; n < NV; ++n) m = fmaxf(m, key[n]);
-    m = warp_max(m);
-    score.zmax = m == -INFINITY ? 0.0f : m;   // (all ruled out: every term is exp(-inf) = 0)
+    score.zmax = warp_max(m);   // (NaN when all are ruled out, and so is every score)
     unsigned long long sum = 0;
     uint32_t least = 0xffffffffu;   // bits of the smallest nonzero term, less 1
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
       key[n] = score.numerator(key[n]);
       least = min(least, __float_as_uint(key[n]) - 1u);
-      sum += __float2ull_rz(key[n] * 0x1p52f);
+      sum += __float2ull_rz(fmaxf(key[n], 0.0f) * 0x1p52f);
     }
-    score.total = __ull2float_rn(warp_sum_u58(sum)) * 0x1p-52f;
+    score.total = __ull2float_rn(warp_sum_u58(sum)) * 0x1p-52f;   // at least 1, or all are ruled out
     // e / total, correctly rounded: with r the correctly rounded reciprocal, one residual makes
     // q = e r exact (P. Markstein, "Computation of elementary functions on the IBM RISC System/6000
     // processor", IBM J. Res. Dev. 34, 1990) while the residual does not underflow; with smaller
@@ -157,7 +156,7 @@ __global__ void __launch_bounds__(256) select_experts_kernel(const SelectParams 
       }
     } else {
 #pragma unroll
-      for (int n = 0; n < NV; ++n) key[n] = score.total > 0.0f ? __fdiv_rn(key[n], score.total) : 0.0f;
+      for (int n = 0; n < NV; ++n) key[n] = __fdiv_rn(key[n], score.total);
     }
   } else {
 #pragma unroll
@@ -165,14 +164,27 @@ __global__ void __launch_bounds__(256) select_experts_kernel(const SelectParams 
   }
   if (p.bias != nullptr) {
 #pragma unroll
-    for (int n = 0; n < NV; ++n) {
-      const int e = id_of(n);
-      if (e < p.E) key[n] = __fadd_rn(key[n], __ldg(p.bias + e));
+    for (int i = 0; i < NQ; ++i) {
+      const int e = (i * 32 + lane) * V;
+      if (e < p.E) {
+        float b[V];
+        if (V == 4 && p.bias_vec) {
+          const float4 v = __ldg(reinterpret_cast<const float4*>(p.bias + e));
+          b[0] = v.x;
+          b[V > 1 ? 1 : 0] = v.y;
+          b[V > 1 ? 2 : 0] = v.z;
+          b[V > 1 ? 3 : 0] = v.w;
+        } else {
+#pragma unroll
+          for (int v = 0; v < V; ++v) b[v] = __ldg(p.bias + e + v);
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) key[i * V + v] = __fadd_rn(key[i * V + v], b[v]);
+      }
     }
   }
 #pragma unroll
-  for (int n = 0; n < NV; ++n)   // (a NaN bias rules out as well)
-    if (((out[n / 32] >> (n % 32)) & 1u) || key[n] != key[n]) key[n] = -INFINITY;
+  for (int n = 0; n < NV; ++n) key[n] = fmaxf(key[n], -INFINITY);   // NaN (a NaN bias too): ruled out
 
   if constexpr (GROUPS != 0) {
     // the best two keys of each chunk (it lies in one group)
@@ -244,7 +256,8 @@ __global__ void __launch_bounds__(256) select_experts_kernel(const SelectParams 
       }
   }
 
-  // the bound: the top_k-th largest of the lanes' best keys (-inf when fewer lanes have one)
+  // the bound: the top_k-th largest of the lanes' best keys (equal ones taken out together, which
+  // only lowers it; -inf when that leaves fewer)
   float best = key[0];
 #pragma unroll
   for (int n = 1; n < NV; ++n) best = fmaxf(best, key[n]);
@@ -253,23 +266,30 @@ __global__ void __launch_bounds__(256) select_experts_kernel(const SelectParams 
     float left = best;
     for (int j = 0; j < p.k; ++j) {
       bound = warp_max(left);
-      if (bound == -INFINITY) break;
-      if (lane == __ffs(__ballot_sync(kAll, left == bound)) - 1) left = -INFINITY;
+      if (left == bound) left = -INFINITY;
     }
   }
-  // candidates: keys on or above the bound (all that is left when there is no bound)
-  int count = 0;
+  // candidates: keys on or above the bound (all that is left when there is no bound), each lane's
+  // after those of the lanes below it
+  int count = kCandidates + 1;
   if (bound > -INFINITY) {
+    int own = 0;
 #pragma unroll
-    for (int n = 0; n < NV; ++n) {
-      const bool in = key[n] >= bound;
-      const unsigned who = __ballot_sync(kAll, in);
-      const int at = count + __popc(who & ((1u << lane) - 1u));
-      if (in && at < kCandidates) cand[at] = make_float2(key[n], __int_as_float(id_of(n)));
-      count += __popc(who);
+    for (int n = 0; n < NV; ++n) own += key[n] >= bound;
+    const unsigned below = (1u << lane) - 1u;
+    int at = 0;
+    count = 0;
+#pragma unroll
+    for (int bit = 0; (1 << bit) <= NV; ++bit) {
+      const unsigned who = __ballot_sync(kAll, (own >> bit) & 1);
+      at += __popc(who & below) << bit;
+      count += __popc(who) << bit;
     }
-  } else {
-    count = kCandidates + 1;
+    if (own != 0 && count <= kCandidates) {
+#pragma unroll
+      for (int n = 0; n < NV; ++n)
+        if (key[n] >= bound) cand[at++] = make_float2(key[n], __int_as_float(id_of(n)));
+    }
   }
   int my_id = 0, chosen = 0;   // lane j keeps pick j
   if (count <= kCandidates) {
@@ -277,7 +297,7 @@ __global__ void __launch_bounds__(256) select_experts_kernel(const SelectParams 
     const float2 c = lane < count ? cand[lane] : make_float2(-INFINITY, 0.0f);
     float left = c.x;
     const int id = __float_as_int(c.y);
-    for (int j = 0; j < p.k; ++j) {   // count >= top_k: the bound's lanes alone give that many
+    for (int j = 0; j < p.k; ++j) {   // count >= top_k: the lanes taken out give that many
       const float m = warp_max(left);
       const int pick = __reduce_min_sync(kAll, left == m ? id : 0x7fffffff);
       if (lane == j) my_id = pick;
@@ -441,6 +461,7 @@ extern "C" moe_lora_status moe_lora_select_experts(moe_lora_handle* h, const moe
   p.top2 = a->group_score == MOE_LORA_GROUP_TOP2;
   p.renormalize = a->renormalize != 0;
   p.group_size = group_size;
+  p.bias_vec = aligned16(a->bias);
   p.factor = a->routed_scaling_factor;
   // four experts per load when rows and groups divide into aligned quads
   const bool vec = a->E % 4 == 0 && group_size % 4 == 0 && a->logits_stride % 4 == 0 &&
