@@ -14,7 +14,7 @@
 //
 // A lane holds NQ chunks of V consecutive experts, so loads are one vector per chunk and, where
 // groups are a power of two of chunks, a group's best is a few shuffles among neighbouring
-// lanes.  The choice itself: the top_k-th largest of the lanes' best keys is a bound below which
+// lanes; other groups go through shared memory, a few lanes to a group.  The choice itself: the top_k-th largest of the lanes' best keys is a bound below which
 // nothing is chosen; the (few) keys on or above it are handed to one lane each, and top_k rounds
 // of a warp maximum and a warp minimum of the ids that hold it put them in order.  That takes a
 // third of the instructions of looking through the lane's values again after every pick
@@ -36,6 +36,8 @@ struct SelectParams {
   long long stride;      // elements between two tokens' logits
   int bias_vec;          // bias starts on a 16-byte boundary
   int T, E, k, sigmoid, n_group, topk_group, top2, renormalize, group_size;
+  int group_inv;         // ceil(2^20 / group_size): e * group_inv >> 20 = e / group_size for e < 1024
+  int group_lanes;       // (any groups) lanes that look through a group
   float factor;
 };
 
@@ -101,7 +103,8 @@ struct Scoring {
 // Keys (and their ids) on or above a bound, one per lane, for the ordered choice.
 constexpr int kCandidates = 32;
 
-// GROUPS: 0 no groups, 1 groups of 2^n chunks (shuffles), 2 any groups (a warp maximum each).
+// GROUPS: 0 no groups, 1 groups of 2^n chunks (shuffles), 2 any groups (shared memory, E floats a
+// warp).
 template <typename TL, int NQ, int V, int GROUPS>
 __global__ void __launch_bounds__(256) select_experts_kernel(const SelectParams p) {
   constexpr int NV = NQ * V;
@@ -187,20 +190,20 @@ __global__ void __launch_bounds__(256) select_experts_kernel(const SelectParams 
   for (int n = 0; n < NV; ++n) key[n] = fmaxf(key[n], -INFINITY);   // NaN (a NaN bias too): ruled out
 
   if constexpr (GROUPS != 0) {
-    // the best two keys of each chunk (it lies in one group)
-    float b1[NQ], b2[NQ];
-#pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-      b1[i] = key[i * V];
-      b2[i] = -INFINITY;
-#pragma unroll
-      for (int v = 1; v < V; ++v) {
-        b2[i] = fmaxf(b2[i], fminf(b1[i], key[i * V + v]));
-        b1[i] = fmaxf(b1[i], key[i * V + v]);
-      }
-    }
     float mine = -INFINITY;   // lane g: group g's score
     if constexpr (GROUPS == 1) {
+      // the best two keys of each chunk (it lies in one group), then of the group's chunks
+      float b1[NQ], b2[NQ];
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) {
+        b1[i] = key[i * V];
+        b2[i] = -INFINITY;
+#pragma unroll
+        for (int v = 1; v < V; ++v) {
+          b2[i] = fmaxf(b2[i], fminf(b1[i], key[i * V + v]));
+          b1[i] = fmaxf(b1[i], key[i * V + v]);
+        }
+      }
       const int width = p.group_size / V;   // chunks (lanes) of a group: 2^n <= 32
       for (int off = 1; off < width; off *= 2) {
 #pragma unroll
@@ -221,23 +224,27 @@ __global__ void __launch_bounds__(256) select_experts_kernel(const SelectParams 
         if ((first >> 5) == i) mine = of;
       }
     } else {
-      for (int g = 0; g < p.n_group; ++g) {
-        float l1 = -INFINITY, l2 = -INFINITY;
+      extern __shared__ float keys_s[];
+      float* keys = keys_s + (threadIdx.x >> 5) * p.E;
 #pragma unroll
-        for (int i = 0; i < NQ; ++i) {
-          if ((i * 32 + lane) * V / p.group_size == g) {
-            l2 = fmaxf(fmaxf(l2, b2[i]), fminf(l1, b1[i]));
-            l1 = fmaxf(l1, b1[i]);
-          }
+      for (int n = 0; n < NV; ++n)
+        if (id_of(n) < p.E) keys[id_of(n)] = key[n];
+      __syncwarp();
+      const int width = p.group_lanes;   // lanes of a group: 2^n, width * n_group <= 32
+      const int g = lane / width;
+      float b1 = -INFINITY, b2 = -INFINITY;
+      if (g < p.n_group)
+        for (int e = lane & (width - 1); e < p.group_size; e += width) {
+          const float f = keys[g * p.group_size + e];
+          b2 = fmaxf(b2, fminf(b1, f));
+          b1 = fmaxf(b1, f);
         }
-        const float m1 = warp_max(l1);
-        float s = m1;
-        if (p.top2) {
-          const int owner = __ffs(__ballot_sync(kAll, l1 == m1)) - 1;
-          s = __fadd_rn(m1, warp_max(lane == owner ? l2 : l1));
-        }
-        if (lane == g) mine = s;
+      for (int off = 1; off < width; off *= 2) {
+        const float o1 = __shfl_xor_sync(kAll, b1, off), o2 = __shfl_xor_sync(kAll, b2, off);
+        b2 = fmaxf(fmaxf(b2, o2), fminf(b1, o1));
+        b1 = fmaxf(b1, o1);
       }
+      mine = __shfl_sync(kAll, p.top2 ? __fadd_rn(b1, b2) : b1, (lane * width) & 31);
     }
     if (mine != mine) mine = -INFINITY;   // +inf (a bias) and a ruled-out second
     unsigned stay = 0;   // ties, also of groups without an expert left: the lower group
@@ -249,11 +256,13 @@ __global__ void __launch_bounds__(256) select_experts_kernel(const SelectParams 
       taken |= lane == g;
     }
 #pragma unroll
-    for (int i = 0; i < NQ; ++i)
-      if (!((stay >> ((i * 32 + lane) * V / p.group_size & 31)) & 1u)) {
+    for (int i = 0; i < NQ; ++i) {
+      const int g = ((i * 32 + lane) * V * p.group_inv) >> 20;   // the chunk's group: e / group_size
+      if (!((stay >> (g & 31)) & 1u)) {
 #pragma unroll
         for (int v = 0; v < V; ++v) key[i * V + v] = -INFINITY;
       }
+    }
   }
 
   // the bound: the top_k-th largest of the lanes' best keys (equal ones taken out together, which
@@ -396,7 +405,8 @@ cudaError_t launch_select(const SelectParams& p, bool vec, cudaStream_t stream) 
   const dim3 grid((p.T + warps - 1) / warps), block(32 * warps);
   const int width = p.group_size / 4;   // chunks of a group on the vector path
   const int groups = p.n_group == 1 ? 0 : vec && width <= 32 && (width & (width - 1)) == 0 ? 1 : 2;
-#define ML_SELECT(NQ, V, G) return launch_k(select_experts_kernel<TL, NQ, V, G>, grid, block, 0, stream, false, p)
+#define ML_SELECT(NQ, V, G) \
+  return launch_k(select_experts_kernel<TL, NQ, V, G>, grid, block, G == 2 ? warps * p.E * 4 : 0, stream, false, p)
 #define ML_SELECT_G(NQ)              \
   do {                               \
     if (groups == 0) ML_SELECT(NQ, 4, 0); \
@@ -410,12 +420,17 @@ cudaError_t launch_select(const SelectParams& p, bool vec, cudaStream_t stream) 
     if (p.E <= 512) ML_SELECT_G(4);
     ML_SELECT_G(8);
   }
-  if (p.E <= 256) {
-    if (groups == 0) ML_SELECT(8, 1, 0);
-    ML_SELECT(8, 1, 2);
-  }
-  if (groups == 0) ML_SELECT(32, 1, 0);
-  ML_SELECT(32, 1, 2);
+#define ML_SELECT_1(NQ)              \
+  do {                               \
+    if (groups == 0) ML_SELECT(NQ, 1, 0); \
+    ML_SELECT(NQ, 1, 2);             \
+  } while (0)
+  if (p.E <= 128) ML_SELECT_1(4);
+  if (p.E <= 256) ML_SELECT_1(8);
+  if (p.E <= 384) ML_SELECT_1(12);
+  if (p.E <= 512) ML_SELECT_1(16);
+  ML_SELECT_1(32);
+#undef ML_SELECT_1
 #undef ML_SELECT_G
 #undef ML_SELECT
 }
@@ -462,6 +477,9 @@ extern "C" moe_lora_status moe_lora_select_experts(moe_lora_handle* h, const moe
   p.renormalize = a->renormalize != 0;
   p.group_size = group_size;
   p.bias_vec = aligned16(a->bias);
+  p.group_inv = ((1 << 20) + group_size - 1) / group_size;
+  p.group_lanes = 32;
+  while (p.group_lanes * p.n_group > 32) p.group_lanes /= 2;
   p.factor = a->routed_scaling_factor;
   // four experts per load when rows and groups divide into aligned quads
   const bool vec = a->E % 4 == 0 && group_size % 4 == 0 && a->logits_stride % 4 == 0 &&
