@@ -1,4 +1,5 @@
-"""Build the in-tree shared library libmoelora.so (sm_103a) with nvcc.
+"""Build the in-tree shared library libmoelora.so (sm_103a) with nvcc, and the Python module
+_marshal.so (argument marshalling against PyTorch's C++ interface) with g++.
 
 Each .cu file is compiled in parallel to an object under _build/, then linked into
 routed_moe_expert_gb300/libmoelora.so with the CUDA runtime linked statically, so the
@@ -11,12 +12,14 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoelora.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 SOURCES = ["moe_lora.cu", "route_align.cu", "grouped_gemm.cu", "gemm_fp8.cu", "elementwise.cu", "lora.cu", "route_noalloc.cu",
            "lora_tc.cu", "permute_shrink.cu", "nvfp4.cu", "select_experts.cu", "qk_norm_rope.cu",
            "linear.cu", "linear_narrow.cu", "linear_wide.cu"]
@@ -39,9 +42,29 @@ def _deps_mtime() -> float:
     return max(os.path.getmtime(f) for f in files)
 
 
+def _build_marshal(verbose: bool) -> None:
+    import torch
+    base = os.path.dirname(torch.__file__)
+    inc = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")]
+    lib = os.path.join(base, "lib")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", os.path.join(CSRC, "binding.cpp"), "-o", MARSHAL + ".tmp"]
+    for d in inc:
+        cmd += ["-isystem", d]
+    cmd += [f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-L", lib, f"-Wl,-rpath,{lib}",
+            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
+    if verbose:
+        print(r.stdout + r.stderr)
+    os.replace(MARSHAL + ".tmp", MARSHAL)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile and link libmoelora.so if any source is newer than it.  Returns its path."""
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime():
+    """Compile and link libmoelora.so and _marshal.so if any source is newer than either.  Returns
+    the library's path."""
+    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _deps_mtime() for f in (LIB, MARSHAL)):
         return LIB
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
@@ -56,8 +79,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
             print(r.stdout + r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        marshal = ex.submit(_build_marshal, verbose)
         objs = list(ex.map(compile_one, SOURCES))
+        marshal.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

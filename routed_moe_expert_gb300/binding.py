@@ -1,4 +1,5 @@
-"""Thin Python binding of libmoelora.so (ctypes): argument marshalling only.
+"""Thin Python binding of libmoelora.so (ctypes, and the module _marshal for the operators around
+the layer): argument marshalling only.
 
 Every step of the layer runs in the library's CUDA kernels; this module checks tensor
 dtypes/devices/contiguity, passes raw device pointers and the current CUDA stream, and
@@ -9,8 +10,8 @@ fallback path.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
-import struct
 from typing import Optional, Sequence
 
 import torch
@@ -146,10 +147,6 @@ def lib() -> ctypes.CDLL:
                                               ctypes.POINTER(c_size_t)]
     L.moe_lora_pack_lora_a.argtypes = [c_void_p, c_void_p, c_int, c_int, c_int, c_int,
                                        ctypes.POINTER(ctypes.c_int32), c_void_p, c_void_p]
-    # the argument structs of these come as packed bytes
-    L.moe_lora_select_experts.argtypes = [c_void_p, ctypes.c_char_p, c_void_p]
-    L.moe_lora_qk_norm_rope.argtypes = [c_void_p, ctypes.c_char_p, c_void_p, c_size_t, c_void_p]
-    L.moe_lora_linear.argtypes = [c_void_p, ctypes.c_char_p, c_void_p, c_size_t, c_void_p]
     L.moe_lora_linear_adapters_size.argtypes = [c_int, c_int, c_int, c_void_p, ctypes.POINTER(c_size_t)]
     L.moe_lora_linear_pack_adapters.argtypes = [c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_void_p,
                                                 c_void_p, c_void_p]
@@ -192,6 +189,7 @@ class Handle:
         h = c_void_p()
         _check(lib().moe_lora_create(ctypes.byref(h), int(device)), "moe_lora_create")
         self._h = h
+        self.address = h.value
         self.device = device
 
     @property
@@ -208,6 +206,7 @@ class Handle:
         if getattr(self, "_h", None) is not None and self._h.value:
             lib().moe_lora_destroy(self._h)
             self._h = c_void_p()
+            self.address = 0
 
     def __del__(self):
         try:
@@ -737,46 +736,27 @@ def moe_lora_check_status(workspace: torch.Tensor, stream=None):
 
 # ---------------------------------------------------------------- operators around the layer
 # These are called several times per layer on batches down to one token, where the host's time
-# is the call's time.  So each argument struct is packed in one go, messages are built only for
-# an error, and what this module has just allocated is not looked at again.
-_select_args = struct.Struct("@5P1q9if").pack       # moe_lora_select_args
-_qk_args = struct.Struct("@8P9q9if").pack           # moe_lora_qk_args
-_linear_args = struct.Struct("@8P3q5i4x").pack      # moe_lora_linear_args
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-_F32 = (torch.float32,)
-_I32 = (torch.int32,)
-_I32_I64 = (torch.int32, torch.int64)
-_BF16_F32 = (torch.bfloat16, torch.float32)
+# is the call's time, so their arguments are marshalled by the compiled module _marshal
+# (csrc/binding.cpp): it raises ValueError for a tensor of the wrong shape, type, device or strides,
+# and returns the C call's status when that is not 0.
+_marshal = None
 
 
-def _stream_on(device: torch.device, stream) -> int:
-    if stream is None and _raw_stream is not None:
-        return _raw_stream(device.index)
-    return _stream(stream)
-
-
-def _refuse(t, name: str, want: str):
-    got = f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}" if isinstance(t, torch.Tensor) else repr(t)
-    raise ValueError(f"{name} must be {want}, got {got}")
-
-
-def _vec(t: torch.Tensor, n: int, dtypes, dev, name: str) -> int:
-    """The address of a dense vector of n values on `dev`."""
-    if t.dtype not in dtypes or t.dim() != 1 or t.shape[0] != n or t.device != dev or (n > 1 and t.stride(0) != 1):
-        _refuse(t, name, f"a dense [{n}] tensor of {' or '.join(str(d) for d in dtypes)} on {dev}")
-    return t.data_ptr()
-
-
-def _dense(t: torch.Tensor, shape, dtype, dev, name: str) -> int:
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != dev or not t.is_contiguous():
-        _refuse(t, name, f"a contiguous {dtype} {tuple(shape)} tensor on {dev}")
-    return t.data_ptr()
-
-
-def _bytes(t: torch.Tensor, dev, name: str) -> int:
-    if t.dtype is not torch.uint8 or t.device != dev or not t.is_contiguous():
-        _refuse(t, name, f"a contiguous uint8 tensor on {dev}")
-    return t.data_ptr()
+def _native():
+    """The module _marshal, holding this library's entry points (raises MoELoRAError if it is not built)."""
+    global _marshal
+    if _marshal is None:
+        path = os.path.join(PKG, "_marshal.so")
+        if not os.path.exists(path):
+            raise MoELoRAError(4, "_marshal.so not found", f"{path}; build it with routed_moe_expert_gb300._build.build()")
+        spec = importlib.util.spec_from_file_location("_marshal", path)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        L = lib()
+        m.entry_points(*(ctypes.cast(getattr(L, n), c_void_p).value for n in (
+            "moe_lora_select_experts", "moe_lora_linear", "moe_lora_linear_workspace_size", "moe_lora_qk_norm_rope")))
+        _marshal = m
+    return _marshal
 
 
 def moe_lora_select_experts(handle: Handle, logits: torch.Tensor, top_k: int, scoring: int = SCORE_SOFTMAX,
@@ -791,40 +771,12 @@ def moe_lora_select_experts(handle: Handle, logits: torch.Tensor, top_k: int, sc
     int32 and topk_weights [T, top_k] float32, and with `packed` packed_topk_ids [T, top_k], the
     words that moe_lora_forward_routed takes; `outputs` may bring any of them.  Logits of -inf or
     NaN rule an expert out."""
-    dt = logits.dtype
-    if logits.dim() != 2 or not logits.is_cuda or dt not in _BF16_F32:
-        _refuse(logits, "logits", "a bf16 or float32 CUDA tensor [T, E]")
-    T, E = logits.shape
-    row, col = logits.stride()
-    if col != 1 and E > 1:
-        _refuse(logits, "logits", "a tensor with adjacent columns")
-    dev = logits.device
-    o = {} if outputs is None else outputs
-    shape = (T, top_k)
-    ids, w, pk = o.get("topk_ids"), o.get("topk_weights"), o.get("packed_topk_ids")
-    if ids is None:
-        o["topk_ids"] = ids = torch.empty(shape, dtype=torch.int32, device=dev)
-        ids_at = ids.data_ptr()
-    else:
-        ids_at = _dense(ids, shape, torch.int32, dev, "topk_ids")
-    if w is None:
-        o["topk_weights"] = w = torch.empty(shape, dtype=torch.float32, device=dev)
-        w_at = w.data_ptr()
-    else:
-        w_at = _dense(w, shape, torch.float32, dev, "topk_weights")
-    pk_at = 0
-    if pk is not None:
-        pk_at = _dense(pk, shape, torch.int32, dev, "packed_topk_ids")
-    elif packed:
-        o["packed_topk_ids"] = pk = torch.empty(shape, dtype=torch.int32, device=dev)
-        pk_at = pk.data_ptr()
-    args = _select_args(logits.data_ptr(), 0 if bias is None else _vec(bias, E, _F32, dev, "bias"), ids_at, w_at, pk_at,
-                        row if T > 1 else E, T, E, top_k, dt is torch.float32, scoring, n_group, topk_group,
-                        group_score, bool(renormalize), routed_scaling_factor)
-    st = (_lib or lib()).moe_lora_select_experts(handle._h, args, _stream_on(dev, stream))
-    if st:
-        _check(st, "moe_lora_select_experts")
-    return o
+    r = (_marshal or _native()).select_experts(handle.address, logits, top_k, scoring, bias, n_group, topk_group,
+                                               group_score, renormalize, routed_scaling_factor, packed, outputs,
+                                               None if stream is None else _stream(stream))
+    if type(r) is int:
+        _check(r, "moe_lora_select_experts")
+    return r
 
 
 class LinearAdapters:
@@ -833,12 +785,9 @@ class LinearAdapters:
 
     def __init__(self, packed: torch.Tensor, S: int, N: int, K: int, ranks: Sequence[int], scalings: Sequence[float]):
         self.packed = packed
-        self.device = packed.device
         self.S, self.N, self.K = S, N, K
         self.ranks = (ctypes.c_int32 * S)(*ranks)
-        self.scalings = (c_float * S)(*scalings)
-        self.address = packed.data_ptr()
-        self.ranks_address, self.scalings_address = ctypes.addressof(self.ranks), ctypes.addressof(self.scalings)
+        self.native = _native().adapters(packed, S, N, K, list(ranks), list(scalings))
 
 
 def moe_lora_linear_adapters(handle: Handle, A: torch.Tensor, B: torch.Tensor, ranks: Sequence[int],
@@ -846,11 +795,12 @@ def moe_lora_linear_adapters(handle: Handle, A: torch.Tensor, B: torch.Tensor, r
     """Stacks the adapters A [S, R, K] and B [S, N, R] (dense bf16; slot s uses its first ranks[s]
     ranks, times scalings[s]) of one projection for moe_lora_linear.  Once per adapter load."""
     if A.dim() != 3 or A.dtype != torch.bfloat16 or not A.is_cuda or not A.is_contiguous():
-        _refuse(A, "A", "a dense bf16 CUDA tensor [S, R, K]")
+        raise ValueError(f"A must be a dense bf16 CUDA tensor [S, R, K], got {A.dtype} {tuple(A.shape)} on {A.device}")
     S, R, K = A.shape
     if (B.dim() != 3 or B.dtype != torch.bfloat16 or B.device != A.device or not B.is_contiguous() or
             B.shape[0] != S or B.shape[2] != R):
-        _refuse(B, "B", f"a dense bf16 [{S}, N, {R}] tensor on {A.device}")
+        raise ValueError(f"B must be a dense bf16 [{S}, N, {R}] tensor on {A.device}, got {B.dtype} {tuple(B.shape)} on "
+                         f"{B.device}")
     N = B.shape[1]
     if len(ranks) != S or len(scalings) != S:
         raise ValueError(f"need {S} ranks and scalings, got {len(ranks)} and {len(scalings)}")
@@ -859,18 +809,18 @@ def moe_lora_linear_adapters(handle: Handle, A: torch.Tensor, B: torch.Tensor, r
     n = c_size_t()
     _check(lib().moe_lora_linear_adapters_size(S, N, K, arr, ctypes.byref(n)), "moe_lora_linear_adapters_size")
     packed = torch.empty(max(n.value, 16), dtype=torch.uint8, device=A.device)
-    _check(lib().moe_lora_linear_pack_adapters(handle.ptr, A.data_ptr(), B.data_ptr(), S, N, K, R, arr,
-                                               packed.data_ptr(), _stream_on(A.device, stream)),
-           "moe_lora_linear_pack_adapters")
+    with torch.cuda.device(A.device):   # _stream: the current stream of the current device
+        _check(lib().moe_lora_linear_pack_adapters(handle.ptr, A.data_ptr(), B.data_ptr(), S, N, K, R, arr,
+                                                   packed.data_ptr(), _stream(stream)),
+               "moe_lora_linear_pack_adapters")
     return LinearAdapters(packed, S, N, K, ranks, [float(s) for s in scalings])
 
 
 def moe_lora_linear_workspace_size(T: int, adapters: Optional[LinearAdapters] = None) -> int:
     """Bytes of workspace that moe_lora_linear needs at most for T tokens."""
     n = c_size_t()
-    _check(lib().moe_lora_linear_workspace_size(T, adapters.S if adapters else 0,
-                                                adapters.ranks_address if adapters else None, ctypes.byref(n)),
-           "moe_lora_linear_workspace_size")
+    _check(lib().moe_lora_linear_workspace_size(T, adapters.S if adapters else 0, adapters.ranks if adapters else None,
+                                                ctypes.byref(n)), "moe_lora_linear_workspace_size")
     return n.value
 
 
@@ -887,64 +837,19 @@ def moe_lora_linear(handle: Handle, x: torch.Tensor, w: torch.Tensor, adapters: 
     be strided, by multiples of 8), bias [N] float32, slot_idx [T] int32.  The result is a new
     [T, N] tensor of out_dtype (bf16 or float32), or `out`, whose rows may be strided (a column
     range of a wider tensor).  `workspace`: alloc_linear_workspace(T, adapters), or allocated."""
-    if x.dim() != 2 or not x.is_cuda or x.dtype is not torch.bfloat16:
-        _refuse(x, "x", "a bf16 CUDA tensor [T, K]")
-    T, K = x.shape
-    x_row, x_col = x.stride()
-    if x_col != 1 and K > 1:
-        _refuse(x, "x", "a tensor with adjacent columns")
-    dev = x.device
-    if w.dim() != 2 or w.dtype is not torch.bfloat16 or w.device != dev or w.shape[1] != K:
-        _refuse(w, "w", f"a bf16 [N, {K}] tensor on {dev}")
-    N = w.shape[0]
-    w_row, w_col = w.stride()
-    if w_col != 1 and K > 1:
-        _refuse(w, "w", "a tensor with adjacent columns")
-    if out is None:
-        if out_dtype not in _BF16_F32:
-            raise ValueError(f"out_dtype must be torch.bfloat16 or torch.float32, got {out_dtype}")
-        out = torch.empty((T, N), dtype=out_dtype, device=dev)
-        y_row = N
-    else:
-        out_dtype = out.dtype
-        if out_dtype not in _BF16_F32 or out.shape != (T, N) or out.device != dev or (out.stride(1) != 1 and N > 1):
-            _refuse(out, "out", f"a bf16 or float32 ({T}, {N}) tensor on {dev} with adjacent columns")
-        y_row = out.stride(0)
-    S = ad_at = ranks_at = scalings_at = slots_at = 0
-    if adapters is not None:
-        if adapters.N != N or adapters.K != K or adapters.device != dev:
-            raise ValueError(f"the adapters are for a [{adapters.N}, {adapters.K}] projection on {adapters.device}, "
-                             f"w is [{N}, {K}] on {dev}")
-        if slot_idx is None:
-            raise ValueError("slot_idx [T] is required with adapters")
-        S, ad_at = adapters.S, adapters.address
-        ranks_at, scalings_at = adapters.ranks_address, adapters.scalings_address
-        slots_at = _vec(slot_idx, T, _I32, dev, "slot_idx")
-    if workspace is None:
-        workspace = alloc_linear_workspace(T, adapters, dev)
-    args = _linear_args(x.data_ptr(), w.data_ptr(), 0 if bias is None else _vec(bias, N, _F32, dev, "bias"),
-                        out.data_ptr(), ad_at, slots_at, ranks_at, scalings_at, x_row, w_row, y_row, T, N, K, S,
-                        out_dtype is torch.float32)
-    st = (_lib or lib()).moe_lora_linear(handle._h, args, _bytes(workspace, dev, "workspace"), workspace.numel(),
-                                         _stream_on(dev, stream))
-    if st:
-        _check(st, "moe_lora_linear")
-    return out
+    f32 = out_dtype is torch.float32
+    if not f32 and out_dtype is not torch.bfloat16:
+        raise ValueError(f"out_dtype must be torch.bfloat16 or torch.float32, got {out_dtype}")
+    r = (_marshal or _native()).linear(handle.address, x, w, None if adapters is None else adapters.native, slot_idx, bias,
+                                       out, f32, workspace, None if stream is None else _stream(stream))
+    if type(r) is int:
+        _check(r, "moe_lora_linear")
+    return r
 
 
 def alloc_qk_norm_rope_workspace(device="cuda") -> torch.Tensor:
     """The status word of moe_lora_qk_norm_rope, for moe_lora_check_status."""
     return torch.zeros(256, dtype=torch.uint8, device=device)
-
-
-def _heads(t: torch.Tensor, T: int, H: int, D: int, dev, name: str):
-    """Address and strides of [T, H, D] heads."""
-    if t.dtype is not torch.bfloat16 or t.dim() != 3 or t.shape != (T, H, D) or t.device != dev:
-        _refuse(t, name, f"a bf16 [{T}, {H}, {D}] tensor on {dev}")
-    row, head, one = t.stride()
-    if one != 1 and D > 1:
-        _refuse(t, name, "a tensor whose heads' values are adjacent")
-    return t.data_ptr(), row, head
 
 
 def moe_lora_qk_norm_rope(handle: Handle, q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor,
@@ -956,43 +861,9 @@ def moe_lora_qk_norm_rope(handle: Handle, q: torch.Tensor, k: torch.Tensor, q_we
     then the rotation of the first R values by row positions[t] (int32 or int64) of cos_sin [P, R]
     (float32: R/2 cosines, R/2 sines); pairs (i, i + R/2), or (2i, 2i + 1) when interleaved.
     Returns (q_out, k_out), new dense tensors unless given; they may be q and k themselves."""
-    if q.dim() != 3 or not q.is_cuda:
-        _refuse(q, "q", "a bf16 CUDA tensor [T, heads, D]")
-    if k.dim() != 3:
-        _refuse(k, "k", "a bf16 CUDA tensor [T, heads, D]")
-    T, Hq, D = q.shape
-    Hk = k.shape[1]
-    dev = q.device
-    q_at, q_t, q_h = _heads(q, T, Hq, D, dev, "q")
-    k_at, k_t, k_h = _heads(k, T, Hk, D, dev, "k")
-    if cos_sin.dim() != 2 or cos_sin.dtype is not torch.float32 or cos_sin.device != dev:
-        _refuse(cos_sin, "cos_sin", f"a float32 [positions, R] tensor on {dev}")
-    P, R = cos_sin.shape
-    cs_row, cs_col = cos_sin.stride()
-    if cs_col != 1 and R > 1:
-        _refuse(cos_sin, "cos_sin", "a tensor with adjacent columns")
-    wt = q_weight.dtype
-    if k_weight.dtype != wt:
-        _refuse(k_weight, "k_weight", f"of q_weight's type ({wt})")
-    if q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
-        qo_at, qo_t, qo_h = q_out.data_ptr(), Hq * D, D
-    else:
-        qo_at, qo_t, qo_h = _heads(q_out, T, Hq, D, dev, "q_out")
-    if k_out is None:
-        k_out = torch.empty((T, Hk, D), dtype=torch.bfloat16, device=dev)
-        ko_at, ko_t, ko_h = k_out.data_ptr(), Hk * D, D
-    else:
-        ko_at, ko_t, ko_h = _heads(k_out, T, Hk, D, dev, "k_out")
-    args = _qk_args(q_at, k_at, qo_at, ko_at, _vec(q_weight, D, _BF16_F32, dev, "q_weight"),
-                    _vec(k_weight, D, _BF16_F32, dev, "k_weight"), cos_sin.data_ptr(),
-                    _vec(positions, T, _I32_I64, dev, "positions"), q_t, q_h, k_t, k_h, qo_t, qo_h, ko_t, ko_h, cs_row,
-                    T, Hq, Hk, D, R, P, wt is torch.float32, positions.dtype is torch.int64, bool(interleaved), eps)
-    if workspace is None:
-        ws_at = ws_n = 0
-    else:
-        ws_at, ws_n = _bytes(workspace, dev, "workspace"), workspace.numel()
-    st = (_lib or lib()).moe_lora_qk_norm_rope(handle._h, args, ws_at, ws_n, _stream_on(dev, stream))
-    if st:
-        _check(st, "moe_lora_qk_norm_rope")
-    return q_out, k_out
+    r = (_marshal or _native()).qk_norm_rope(handle.address, q, k, q_weight, k_weight, cos_sin, positions, eps,
+                                             interleaved, q_out, k_out, workspace,
+                                             None if stream is None else _stream(stream))
+    if type(r) is int:
+        _check(r, "moe_lora_qk_norm_rope")
+    return r

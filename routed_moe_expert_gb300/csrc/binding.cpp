@@ -1,0 +1,448 @@
+// Argument marshalling of the operators around the layer for Python (module _marshal).
+//
+// These calls come several times per layer on batches down to one token, where the host's time is
+// the call's time.  Tensors are looked at through PyTorch's C++ interface instead of attribute by
+// attribute in Python, which takes the Python side of a call from 5-9 us to about 2.  Nothing is
+// computed here: shapes, types, devices and strides are checked (ValueError names the argument and
+// what it was), results that the caller does not bring are allocated, and the C ABI is called with
+// raw pointers and the stream.  A nonzero status of the C call is returned as an int, which the
+// Python side turns into its exception.
+#include "../../include/moe_lora.h"
+
+#define PY_SSIZE_T_CLEAN
+#include <Python.h>
+
+#include <ATen/core/Tensor.h>
+#include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <cstring>
+#include <sstream>
+#include <string>
+
+namespace {
+
+using at::ScalarType;
+using at::Tensor;
+
+// The C ABI's entry points, handed over by the Python side from the library that it has loaded.
+decltype(&moe_lora_select_experts) g_select = nullptr;
+decltype(&moe_lora_linear) g_linear = nullptr;
+decltype(&moe_lora_linear_workspace_size) g_linear_workspace = nullptr;
+decltype(&moe_lora_qk_norm_rope) g_qk = nullptr;
+
+struct Refused {};   // a Python exception is set
+
+[[noreturn]] void refuse(const std::string& msg) {
+  PyErr_SetString(PyExc_ValueError, msg.c_str());
+  throw Refused();
+}
+[[noreturn]] void refuse(const Tensor& t, const char* name, const std::string& want) {
+  std::ostringstream s;
+  s << name << " must be " << want << ", got " << t.scalar_type() << " " << t.sizes() << " strides " << t.strides()
+    << " on " << t.device();
+  refuse(s.str());
+}
+
+const Tensor& tensor(PyObject* o, const char* name) {
+  if (!THPVariable_Check(o)) refuse(std::string(name) + " must be a tensor");
+  return THPVariable_Unpack(o);
+}
+long integer(PyObject* o) {
+  const long v = PyLong_AsLong(o);
+  if (v == -1 && PyErr_Occurred()) throw Refused();
+  return v;
+}
+int int32(PyObject* o) {
+  const long v = integer(o);
+  if (v != static_cast<int>(v)) refuse("an integer argument does not fit 32 bits");
+  return static_cast<int>(v);
+}
+double number(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw Refused();
+  return v;
+}
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Refused();
+  return v != 0;
+}
+int size(int64_t v, const char* name) {
+  if (v > 0x7fffffff) refuse(std::string(name) + " has a dimension past 2^31");
+  return static_cast<int>(v);
+}
+
+std::string on(const at::Device& d) { return " on " + d.str(); }
+
+const void* dense_vector(const Tensor& t, int64_t n, at::Device dev, const char* name) {
+  if (t.dim() != 1 || t.size(0) != n || t.device() != dev || !t.is_contiguous())
+    refuse(t, name, "a dense [" + std::to_string(n) + "] tensor" + on(dev));
+  return t.data_ptr();
+}
+const void* vector_of(PyObject* o, ScalarType type, int64_t n, at::Device dev, const char* name) {
+  const Tensor& t = tensor(o, name);
+  if (t.scalar_type() != type) refuse(t, name, std::string("of type ") + c10::toString(type));
+  return dense_vector(t, n, dev, name);
+}
+void* dense_out(const Tensor& t, int64_t rows, int64_t cols, ScalarType type, at::Device dev, const char* name) {
+  if (t.scalar_type() != type || t.dim() != 2 || t.size(0) != rows || t.size(1) != cols || t.device() != dev ||
+      !t.is_contiguous())
+    refuse(t, name, std::string("a contiguous ") + c10::toString(type) + " [" + std::to_string(rows) + ", " +
+                        std::to_string(cols) + "] tensor" + on(dev));
+  return t.data_ptr();
+}
+// [rows, cols] with adjacent columns; the row stride
+int64_t rows_of(const Tensor& t, const char* name) {
+  if (t.size(1) > 1 && t.stride(1) != 1) refuse(t, name, "a tensor with adjacent columns");
+  return t.stride(0);
+}
+moe_lora_stream stream_of(PyObject* o, at::Device dev) {
+  if (o == Py_None) return reinterpret_cast<moe_lora_stream>(c10::cuda::getCurrentCUDAStream(dev.index()).stream());
+  void* p = PyLong_AsVoidPtr(o);
+  if (p == nullptr && PyErr_Occurred()) throw Refused();
+  return static_cast<moe_lora_stream>(p);
+}
+moe_lora_handle* handle_of(PyObject* o) {
+  void* p = PyLong_AsVoidPtr(o);
+  if (p == nullptr && PyErr_Occurred()) throw Refused();
+  return static_cast<moe_lora_handle*>(p);
+}
+Tensor allocate(at::IntArrayRef sizes, ScalarType type, at::Device dev) {
+  return at::empty(sizes, at::TensorOptions().dtype(type).device(dev));
+}
+
+// A call on a stream of the caller's naming: what was allocated for it (on the current stream) is
+// not handed out again before that stream is past the call.
+void used_on(const Tensor& t, PyObject* stream, at::Device dev) {
+  if (stream == Py_None || !t.defined()) return;
+  t.record_stream(
+      c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(PyLong_AsVoidPtr(stream)), dev.index()).unwrap());
+}
+
+void need_args(Py_ssize_t n, Py_ssize_t want) {
+  if (n != want) {
+    PyErr_Format(PyExc_TypeError, "%zd arguments, got %zd", want, n);
+    throw Refused();
+  }
+}
+
+// Runs f, turning C++ exceptions into Python ones.
+template <typename F>
+PyObject* guarded(F f) {
+  try {
+    return f();
+  } catch (const Refused&) {
+    return nullptr;
+  } catch (const std::exception& e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+    return nullptr;
+  }
+}
+
+PyObject* kIds;
+PyObject* kWeights;
+PyObject* kPacked;
+
+// (handle, logits, top_k, scoring, bias, n_group, topk_group, group_score, renormalize, factor, packed, outputs, stream)
+PyObject* select_experts(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    need_args(n, 13);
+    const Tensor& z = tensor(a[1], "logits");
+    const ScalarType type = z.scalar_type();
+    if (z.dim() != 2 || !z.is_cuda() || (type != ScalarType::Float && type != ScalarType::BFloat16))
+      refuse(z, "logits", "a bf16 or float32 CUDA tensor [T, E]");
+    const at::Device dev = z.device();
+    const int64_t T = z.size(0), E = z.size(1), row = rows_of(z, "logits");
+    moe_lora_select_args p;
+    p.logits = z.data_ptr();
+    p.logits_stride = T > 1 ? row : E;
+    p.T = size(T, "logits");
+    p.E = size(E, "logits");
+    p.top_k = int32(a[2]);
+    p.logits_f32 = type == ScalarType::Float;
+    p.scoring = int32(a[3]);
+    p.bias = a[4] == Py_None ? nullptr : static_cast<const float*>(vector_of(a[4], ScalarType::Float, E, dev, "bias"));
+    p.n_group = int32(a[5]);
+    p.topk_group = int32(a[6]);
+    p.group_score = int32(a[7]);
+    p.renormalize = truth(a[8]);
+    p.routed_scaling_factor = static_cast<float>(number(a[9]));
+    const bool packed = truth(a[10]);
+    const int64_t k = p.top_k < 0 ? 0 : p.top_k;
+    PyObject* o = a[11];
+    const bool given = o != Py_None;
+    if (given && !PyDict_Check(o)) refuse("outputs must be a dict");
+    if (given) Py_INCREF(o);
+    else if ((o = PyDict_New()) == nullptr) throw Refused();
+    auto output = [&](PyObject* key, ScalarType t, const char* name, bool wanted) -> void* {
+      if (given)
+        if (PyObject* have = PyDict_GetItem(o, key); have != nullptr && have != Py_None)
+          return dense_out(tensor(have, name), T, k, t, dev, name);
+      if (!wanted) return nullptr;
+      Tensor made = allocate({T, k}, t, dev);
+      void* at = made.data_ptr();
+      used_on(made, a[12], dev);
+      PyObject* w = THPVariable_Wrap(std::move(made));
+      if (w == nullptr) throw Refused();
+      const int bad = PyDict_SetItem(o, key, w);
+      Py_DECREF(w);
+      if (bad) throw Refused();
+      return at;
+    };
+    int st;
+    try {
+      p.topk_ids = static_cast<int32_t*>(output(kIds, ScalarType::Int, "topk_ids", true));
+      p.topk_weights = static_cast<float*>(output(kWeights, ScalarType::Float, "topk_weights", true));
+      p.packed_topk_ids = static_cast<int32_t*>(output(kPacked, ScalarType::Int, "packed_topk_ids", packed));
+      st = g_select(handle_of(a[0]), &p, stream_of(a[12], dev));
+    } catch (...) {
+      Py_DECREF(o);
+      throw;
+    }
+    if (st != 0) {
+      Py_DECREF(o);
+      return PyLong_FromLong(st);
+    }
+    return o;
+  });
+}
+
+// The adapters of a projection, as moe_lora_linear_adapters stacked them (a capsule).
+struct Adapters {
+  int S, N, K, device;
+  const void* address;
+  int32_t ranks[64];
+  float scalings[64];
+};
+constexpr const char* kAdapters = "moe_lora.adapters";
+
+// (packed, S, N, K, ranks, scalings)
+PyObject* adapters(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    need_args(n, 6);
+    const Tensor& t = tensor(a[0], "packed");
+    Adapters* d = new Adapters();
+    std::memset(d, 0, sizeof(*d));
+    try {
+      d->S = int32(a[1]);
+      d->N = int32(a[2]);
+      d->K = int32(a[3]);
+      d->device = t.device().index();
+      d->address = t.data_ptr();
+      if (d->S < 1 || d->S > 64 || !PyList_Check(a[4]) || !PyList_Check(a[5]) || PyList_Size(a[4]) != d->S ||
+          PyList_Size(a[5]) != d->S)
+        refuse("ranks and scalings must be lists of S <= 64 values");
+      for (int s = 0; s < d->S; ++s) {
+        d->ranks[s] = int32(PyList_GetItem(a[4], s));
+        d->scalings[s] = static_cast<float>(number(PyList_GetItem(a[5], s)));
+      }
+    } catch (...) {
+      delete d;
+      throw;
+    }
+    PyObject* c = PyCapsule_New(d, kAdapters, [](PyObject* o) {
+      delete static_cast<Adapters*>(PyCapsule_GetPointer(o, kAdapters));
+    });
+    if (c == nullptr) delete d;
+    return c;
+  });
+}
+
+// (handle, x, w, adapters or None, slot_idx, bias, out, out is float32, workspace, stream)
+PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    need_args(n, 10);
+    const Tensor& x = tensor(a[1], "x");
+    if (x.dim() != 2 || !x.is_cuda() || x.scalar_type() != ScalarType::BFloat16)
+      refuse(x, "x", "a bf16 CUDA tensor [T, K]");
+    const at::Device dev = x.device();
+    const int64_t T = x.size(0), K = x.size(1);
+    const Tensor& w = tensor(a[2], "w");
+    if (w.dim() != 2 || w.scalar_type() != ScalarType::BFloat16 || w.device() != dev || w.size(1) != K)
+      refuse(w, "w", "a bf16 [N, " + std::to_string(K) + "] tensor" + on(dev));
+    const int64_t N = w.size(0);
+    moe_lora_linear_args p;
+    p.x = static_cast<const moe_lora_bf16*>(x.data_ptr());
+    p.w = static_cast<const moe_lora_bf16*>(w.data_ptr());
+    p.x_stride = rows_of(x, "x");
+    p.w_stride = rows_of(w, "w");
+    p.T = size(T, "x");
+    p.N = size(N, "w");
+    p.K = size(K, "x");
+    p.bias = a[5] == Py_None ? nullptr : static_cast<const float*>(vector_of(a[5], ScalarType::Float, N, dev, "bias"));
+    p.S = 0;
+    p.adapters = nullptr;
+    p.slot_idx = nullptr;
+    p.h_ranks = nullptr;
+    p.h_scalings = nullptr;
+    if (a[3] != Py_None) {
+      const Adapters* d = static_cast<const Adapters*>(PyCapsule_GetPointer(a[3], kAdapters));
+      if (d == nullptr) throw Refused();
+      if (d->N != N || d->K != K || d->device != dev.index())
+        refuse("the adapters are for a [" + std::to_string(d->N) + ", " + std::to_string(d->K) + "] projection on cuda:" +
+               std::to_string(d->device) + ", w is [" + std::to_string(N) + ", " + std::to_string(K) + "]" + on(dev));
+      if (a[4] == Py_None) refuse("slot_idx [T] is required with adapters");
+      p.S = d->S;
+      p.adapters = d->address;
+      p.h_ranks = d->ranks;
+      p.h_scalings = d->scalings;
+      p.slot_idx = static_cast<const int32_t*>(vector_of(a[4], ScalarType::Int, T, dev, "slot_idx"));
+    }
+    Tensor made;
+    const Tensor* out;
+    if (a[6] == Py_None) {
+      made = allocate({T, N}, truth(a[7]) ? ScalarType::Float : ScalarType::BFloat16, dev);
+      out = &made;
+      p.y_stride = N;
+    } else {
+      out = &tensor(a[6], "out");
+      if ((out->scalar_type() != ScalarType::BFloat16 && out->scalar_type() != ScalarType::Float) || out->dim() != 2 ||
+          out->size(0) != T || out->size(1) != N || out->device() != dev)
+        refuse(*out, "out", "a bf16 or float32 [" + std::to_string(T) + ", " + std::to_string(N) + "] tensor" + on(dev));
+      p.y_stride = rows_of(*out, "out");
+    }
+    p.y = out->data_ptr();
+    p.y_f32 = out->scalar_type() == ScalarType::Float;
+    Tensor scratch;
+    const Tensor* ws;
+    if (a[8] == Py_None) {
+      size_t bytes = 0;
+      const int st = g_linear_workspace(p.T, p.S, p.h_ranks, &bytes);
+      if (st != 0) return PyLong_FromLong(st);
+      scratch = allocate({static_cast<int64_t>(bytes)}, ScalarType::Byte, dev);
+      ws = &scratch;
+    } else {
+      ws = &tensor(a[8], "workspace");
+      if (ws->scalar_type() != ScalarType::Byte || ws->device() != dev || !ws->is_contiguous())
+        refuse(*ws, "workspace", "a contiguous uint8 tensor" + on(dev));
+    }
+    used_on(made, a[9], dev);
+    used_on(scratch, a[9], dev);
+    const int st = g_linear(handle_of(a[0]), &p, ws->data_ptr(), static_cast<size_t>(ws->numel()), stream_of(a[9], dev));
+    if (st != 0) return PyLong_FromLong(st);
+    if (a[6] == Py_None) return THPVariable_Wrap(std::move(made));
+    Py_INCREF(a[6]);
+    return a[6];
+  });
+}
+
+// [T, H, D] heads with adjacent values
+const Tensor& heads(PyObject* o, int64_t T, int64_t H, int64_t D, at::Device dev, const char* name) {
+  const Tensor& t = tensor(o, name);
+  if (t.scalar_type() != ScalarType::BFloat16 || t.dim() != 3 || t.size(0) != T || (H >= 0 && t.size(1) != H) ||
+      t.size(2) != D || t.device() != dev || (D > 1 && t.stride(2) != 1))
+    refuse(t, name, "a bf16 [" + std::to_string(T) + ", heads, " + std::to_string(D) + "] tensor with adjacent head values" +
+                        on(dev));
+  return t;
+}
+
+// (handle, q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved, q_out, k_out, workspace, stream)
+PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    need_args(n, 13);
+    const Tensor& q = tensor(a[1], "q");
+    if (q.dim() != 3 || !q.is_cuda()) refuse(q, "q", "a bf16 CUDA tensor [T, heads, D]");
+    const at::Device dev = q.device();
+    const int64_t T = q.size(0), Hq = q.size(1), D = q.size(2);
+    heads(a[1], T, Hq, D, dev, "q");
+    const Tensor& k = heads(a[2], T, -1, D, dev, "k");
+    const int64_t Hk = k.size(1);
+    const Tensor& table = tensor(a[5], "cos_sin");
+    if (table.dim() != 2 || table.scalar_type() != ScalarType::Float || table.device() != dev)
+      refuse(table, "cos_sin", "a float32 [positions, R] tensor" + on(dev));
+    const Tensor& wq = tensor(a[3], "q_weight");
+    const ScalarType wt = wq.scalar_type();
+    if (wt != ScalarType::BFloat16 && wt != ScalarType::Float) refuse(wq, "q_weight", "bf16 or float32");
+    const Tensor& pos = tensor(a[6], "positions");
+    const ScalarType pt = pos.scalar_type();
+    if (pt != ScalarType::Int && pt != ScalarType::Long) refuse(pos, "positions", "int32 or int64");
+    moe_lora_qk_args p;
+    p.q = static_cast<const moe_lora_bf16*>(q.data_ptr());
+    p.k = static_cast<const moe_lora_bf16*>(k.data_ptr());
+    p.q_stride_t = q.stride(0);
+    p.q_stride_h = q.stride(1);
+    p.k_stride_t = k.stride(0);
+    p.k_stride_h = k.stride(1);
+    p.q_weight = dense_vector(wq, D, dev, "q_weight");
+    p.k_weight = vector_of(a[4], wt, D, dev, "k_weight");
+    p.cos_sin = static_cast<const float*>(table.data_ptr());
+    p.cos_sin_stride = rows_of(table, "cos_sin");
+    p.positions = dense_vector(pos, T, dev, "positions");
+    p.T = size(T, "q");
+    p.q_heads = size(Hq, "q");
+    p.k_heads = size(Hk, "k");
+    p.head_dim = size(D, "q");
+    p.rotary_dim = size(table.size(1), "cos_sin");
+    p.num_positions = size(table.size(0), "cos_sin");
+    p.weight_f32 = wt == ScalarType::Float;
+    p.positions_i64 = pt == ScalarType::Long;
+    p.eps = static_cast<float>(number(a[7]));
+    p.interleaved = truth(a[8]);
+    Tensor made[2];
+    auto output = [&](PyObject* o, int64_t H, Tensor& mine, const char* name, moe_lora_bf16*& at, int64_t& st, int64_t& sh) {
+      if (o == Py_None) mine = allocate({T, H, D}, ScalarType::BFloat16, dev);
+      const Tensor& t = o == Py_None ? mine : heads(o, T, H, D, dev, name);
+      at = static_cast<moe_lora_bf16*>(t.data_ptr());
+      st = t.stride(0);
+      sh = t.stride(1);
+    };
+    output(a[9], Hq, made[0], "q_out", p.q_out, p.q_out_stride_t, p.q_out_stride_h);
+    output(a[10], Hk, made[1], "k_out", p.k_out, p.k_out_stride_t, p.k_out_stride_h);
+    void* ws = nullptr;
+    size_t ws_bytes = 0;
+    if (a[11] != Py_None) {
+      const Tensor& t = tensor(a[11], "workspace");
+      if (t.scalar_type() != ScalarType::Byte || t.device() != dev || !t.is_contiguous())
+        refuse(t, "workspace", "a contiguous uint8 tensor" + on(dev));
+      ws = t.data_ptr();
+      ws_bytes = static_cast<size_t>(t.numel());
+    }
+    for (const Tensor& t : made) used_on(t, a[12], dev);
+    const int st = g_qk(handle_of(a[0]), &p, ws, ws_bytes, stream_of(a[12], dev));
+    if (st != 0) return PyLong_FromLong(st);
+    PyObject* r = PyTuple_New(2);
+    if (r == nullptr) throw Refused();
+    for (int i = 0; i < 2; ++i) {
+      PyObject* o = a[9 + i];
+      if (o == Py_None) o = THPVariable_Wrap(std::move(made[i]));
+      else Py_INCREF(o);
+      if (o == nullptr) {
+        Py_DECREF(r);
+        throw Refused();
+      }
+      PyTuple_SET_ITEM(r, i, o);
+    }
+    return r;
+  });
+}
+
+// (addresses of select_experts, linear, linear_workspace_size, qk_norm_rope)
+PyObject* entry_points(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    need_args(n, 4);
+    void* at[4];
+    for (int i = 0; i < 4; ++i)
+      if ((at[i] = PyLong_AsVoidPtr(a[i])) == nullptr) refuse("an entry point is missing");
+    g_select = reinterpret_cast<decltype(g_select)>(at[0]);
+    g_linear = reinterpret_cast<decltype(g_linear)>(at[1]);
+    g_linear_workspace = reinterpret_cast<decltype(g_linear_workspace)>(at[2]);
+    g_qk = reinterpret_cast<decltype(g_qk)>(at[3]);
+    Py_RETURN_NONE;
+  });
+}
+
+#define ML_METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
+PyMethodDef kMethods[] = {ML_METHOD(select_experts), ML_METHOD(adapters),     ML_METHOD(linear),
+                          ML_METHOD(qk_norm_rope),   ML_METHOD(entry_points), {nullptr, nullptr, 0, nullptr}};
+PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__marshal(void) {
+  kIds = PyUnicode_InternFromString("topk_ids");
+  kWeights = PyUnicode_InternFromString("topk_weights");
+  kPacked = PyUnicode_InternFromString("packed_topk_ids");
+  return PyModule_Create(&kModule);
+}
