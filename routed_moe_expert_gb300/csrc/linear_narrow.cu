@@ -98,17 +98,6 @@ __global__ void __launch_bounds__(kThreads, 2) linear_narrow_kernel(const __grid
     return (~0ull >> (63 - b1)) & (~0ull << b0);
   };
 
-  if (shrink && p.Rs > 128 && index > 0) {
-    // a stack of several row tiles: leave out those that no token needs (the whole cluster decides
-    // alike; the first tile stays, it writes the status word)
-    uint64_t m = 0;
-    for (int j = threadIdx.x; j < BN && t0 + j < p.T; j += kThreads) m |= blocks_of(p.slot_idx[t0 + j]);
-    if (!__syncthreads_or(((m >> (row0 >> 6)) & 3ull) != 0)) {
-      if (threadIdx.x == 0) red_release_add(ready, 1);
-      return;
-    }
-  }
-
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
@@ -133,6 +122,22 @@ __global__ void __launch_bounds__(kThreads, 2) linear_narrow_kernel(const __grid
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  // Up to here nothing of the call's data was touched: it may still be in the making by the kernel
+  // before, whose end comes next; then the kernel after this one may start as far.
+  pdl_wait();
+  pdl_trigger();
+
+  if (shrink && p.Rs > 128 && index > 0) {
+    // a stack of several row tiles: leave out those that no token needs (the whole cluster decides
+    // alike; the first tile stays, it writes the status word)
+    uint64_t m = 0;
+    for (int j = threadIdx.x; j < BN && t0 + j < p.T; j += kThreads) m |= blocks_of(p.slot_idx[t0 + j]);
+    if (!__syncthreads_or(((m >> (row0 >> 6)) & 3ull) != 0)) {
+      if (threadIdx.x == 0) red_release_add(ready, 1);
+      if (warp == 1) tmem_dealloc(tmem_base, TMEM_COLS);
+      return;
+    }
+  }
 
   if (warp == 0) {   // ------------------------------------------------ TMA producer
     if (lane == 0) {
@@ -387,10 +392,10 @@ cudaError_t launch_linear_narrow(const LinearParams& p, int bn, int split, cudaS
   if (tiles * split > 0x7fffffffLL) return cudaErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(tiles * split)), block(kThreads);
   switch (bn) {
-    case 16: return launch_kc(linear_narrow_kernel<16>, grid, block, smem_bytes(16), stream, false, split, p);
-    case 32: return launch_kc(linear_narrow_kernel<32>, grid, block, smem_bytes(32), stream, false, split, p);
-    case 64: return launch_kc(linear_narrow_kernel<64>, grid, block, smem_bytes(64), stream, false, split, p);
-    case 128: return launch_kc(linear_narrow_kernel<128>, grid, block, smem_bytes(128), stream, false, split, p);
+    case 16: return launch_kc(linear_narrow_kernel<16>, grid, block, smem_bytes(16), stream, true, split, p);
+    case 32: return launch_kc(linear_narrow_kernel<32>, grid, block, smem_bytes(32), stream, true, split, p);
+    case 64: return launch_kc(linear_narrow_kernel<64>, grid, block, smem_bytes(64), stream, true, split, p);
+    case 128: return launch_kc(linear_narrow_kernel<128>, grid, block, smem_bytes(128), stream, true, split, p);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -119,6 +119,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
   cluster_wait();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  // Nothing of the call's data is touched before the kernel in front has ended; then the kernel
+  // after this one may start as far.
+  pdl_wait();
+  pdl_trigger();
 
   auto decode = [&](int tile, int& tt, int& nt) {   // a shrink tile's nt: its part of the stack
     if (tile < nshrink) {
@@ -417,8 +421,8 @@ cudaError_t launch_linear_wide(const LinearParams& p, int bn, int sms, cudaStrea
   if (tiles > 0x3fffffffLL || (bn != 128 && bn != 256)) return cudaErrorInvalidValue;
   const int pairs = static_cast<int>(tiles < sms / 2 ? tiles : sms / 2);
   const dim3 grid(2 * pairs), block(kThreads);
-  if (bn == 256) return launch_kc(linear_wide_kernel<256>, grid, block, smem_bytes(256), stream, false, 2, p);
-  return launch_kc(linear_wide_kernel<128>, grid, block, smem_bytes(128), stream, false, 2, p);
+  if (bn == 256) return launch_kc(linear_wide_kernel<256>, grid, block, smem_bytes(256), stream, true, 2, p);
+  return launch_kc(linear_wide_kernel<128>, grid, block, smem_bytes(128), stream, true, 2, p);
 }
 
 }  // namespace mlk

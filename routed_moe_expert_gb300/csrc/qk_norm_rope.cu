@@ -191,6 +191,8 @@ MLDEV uint4 pack_pairs(const F2 (&f)[4]) {
 // LANES > 0: that many lanes per head, each with both pieces (D = 16 LANES); 0: as p says.
 template <bool INTERLEAVED, int LANES>
 __global__ void __launch_bounds__(256, 3) qk_norm_rope_kernel(const QkParams p) {
+  pdl_wait();
+  pdl_trigger();
   if (blockIdx.x == gridDim.x - 1) {
     check_positions(p);
     return;
@@ -381,6 +383,8 @@ __global__ void __launch_bounds__(256, 3) qk_norm_rope_kernel(const QkParams p) 
 // Any alignment: V values per piece, NU units per lane.
 template <int V, int NU>
 __global__ void __launch_bounds__(256) qk_norm_rope_any_kernel(const QkParams p) {
+  pdl_wait();
+  pdl_trigger();
   if (blockIdx.x == gridDim.x - 1) {
     check_positions(p);
     return;
@@ -582,17 +586,17 @@ extern "C" moe_lora_status moe_lora_qk_norm_rope(moe_lora_handle* h, const moe_l
   switch (V) {
     case 8:
 #define ML_QK(LANES)                                                                        \
-  (p.interleaved ? launch_k(qk_norm_rope_kernel<true, LANES>, grid, threads, 0, stream, false, p) \
-                 : launch_k(qk_norm_rope_kernel<false, LANES>, grid, threads, 0, stream, false, p))
+  (p.interleaved ? launch_k(qk_norm_rope_kernel<true, LANES>, grid, threads, 0, stream, true, p) \
+                 : launch_k(qk_norm_rope_kernel<false, LANES>, grid, threads, 0, stream, true, p))
       if (p.D == 64) err = ML_QK(4);
       else if (p.D == 128) err = ML_QK(8);
       else if (p.D == 256) err = ML_QK(16);
       else err = ML_QK(0);
 #undef ML_QK
       break;
-    case 4: err = launch_k(qk_norm_rope_any_kernel<4, 2>, grid, threads, 0, stream, false, p); break;
-    case 2: err = launch_k(qk_norm_rope_any_kernel<2, 4>, grid, threads, 0, stream, false, p); break;
-    default: err = launch_k(qk_norm_rope_any_kernel<1, 8>, grid, threads, 0, stream, false, p); break;
+    case 4: err = launch_k(qk_norm_rope_any_kernel<4, 2>, grid, threads, 0, stream, true, p); break;
+    case 2: err = launch_k(qk_norm_rope_any_kernel<2, 4>, grid, threads, 0, stream, true, p); break;
+    default: err = launch_k(qk_norm_rope_any_kernel<1, 8>, grid, threads, 0, stream, true, p); break;
   }
   ML_LAUNCH(h, err, "qk_norm_rope launch");
   return MOE_LORA_OK;

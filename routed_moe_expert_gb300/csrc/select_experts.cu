@@ -111,6 +111,8 @@ __global__ void __launch_bounds__(256) select_experts_kernel(const SelectParams 
   __shared__ float2 cand_s[8][kCandidates];
   const int lane = threadIdx.x & 31;
   const int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  pdl_wait();
+  pdl_trigger();
   if (t >= p.T) return;   // whole warps
   float2* cand = cand_s[threadIdx.x >> 5];
   const TL* row = static_cast<const TL*>(p.logits) + static_cast<long long>(t) * p.stride;
@@ -406,7 +408,7 @@ cudaError_t launch_select(const SelectParams& p, bool vec, cudaStream_t stream) 
   const int width = p.group_size / 4;   // chunks of a group on the vector path
   const int groups = p.n_group == 1 ? 0 : vec && width <= 32 && (width & (width - 1)) == 0 ? 1 : 2;
 #define ML_SELECT(NQ, V, G) \
-  return launch_k(select_experts_kernel<TL, NQ, V, G>, grid, block, G == 2 ? warps * p.E * 4 : 0, stream, false, p)
+  return launch_k(select_experts_kernel<TL, NQ, V, G>, grid, block, G == 2 ? warps * p.E * 4 : 0, stream, true, p)
 #define ML_SELECT_G(NQ)              \
   do {                               \
     if (groups == 0) ML_SELECT(NQ, 4, 0); \
