@@ -22,7 +22,7 @@ LIB = os.path.join(PKG, "libmoelora.so")
 MARSHAL = os.path.join(PKG, "_marshal.so")
 SOURCES = ["moe_lora.cu", "route_align.cu", "grouped_gemm.cu", "gemm_fp8.cu", "elementwise.cu", "lora.cu", "route_noalloc.cu",
            "lora_tc.cu", "permute_shrink.cu", "nvfp4.cu", "select_experts.cu", "qk_norm_rope.cu",
-           "linear.cu", "linear_narrow.cu", "linear_wide.cu"]
+           "linear.cu", "linear_narrow.cu", "linear_wide.cu", "linear_cluster.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "-I", os.path.join(ROOT, "include"), "-I", CSRC]

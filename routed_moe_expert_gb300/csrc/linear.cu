@@ -43,52 +43,75 @@ bool tile_map(const moe_lora_handle* h, CUtensorMap* m, const void* base, long l
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+enum Kernel { kNarrow, kWide, kCluster };
 struct Tiles {
-  bool wide;        // CTA pairs, 256 tokens x `rows` weight rows
+  Kernel kernel;    // kWide: CTA pairs, 256 tokens x `rows` weight rows
   int tokens;       // token tile
   int rows;         // weight rows of a tile
   int split;        // (narrow) CTAs that share a tile's K
 };
 
-// Microseconds of a product on narrow tiles, a model fitted to measured calls (T 1 to 2048, N 384
-// to 5120, K 2048 and 7168): launch, first bytes and epilogue; the bytes that an SM's shared memory
-// takes in, at 75 GB/s for one CTA and 115 GB/s for two; the sum over a cluster.
-double narrow_us(int T, int N, int nk, int bn, int split, int sms) {
-  const long long ctas = static_cast<long long>((N + 127) / 128) * ((T + bn - 1) / bn) * split;
-  const double mb = (nk + split - 1) / split * (16.0 + bn / 8.0) * 1e-3;   // per CTA
+// Microseconds of a call on each kernel: models fitted to measured calls in a row (T 1 to 2048, N 384
+// to 16384, K 2048 and 7168, adapters of 16 to 512 stacked ranks), good to a microsecond or so and
+// meant to rank the choices.
+//
+// Copies of a step (a 64-wide K block of a tile): an SM's shared memory takes in `one` GB/s with one
+// CTA there, 115 with two; the weights come from HBM, and from L2 again for further token tiles.
+double copies_us(long long ctas, double kb_step, int steps, double one, double weight_mb, int sms) {
+  const double mb = kb_step * steps * 1e-3;
   const long long waves = (ctas + 2 * sms - 1) / (2 * sms);
-  double us = 4.2 + (bn / 128.0 * (split > 1 ? 1.2 : 0.6) + (split > 1 ? 0.4 : 0.0));
-  us += ctas <= sms ? mb / 0.075 : static_cast<double>(waves) * 2.0 * mb / 0.115 + 3.5 * static_cast<double>(waves - 1);
-  if (split == 8 && ctas > sms) us += 2.0;   // clusters of 8 do not pack two CTAs to an SM
+  const double us = ctas <= sms ? mb / (one * 1e-3)
+                                : static_cast<double>(waves) * 2.0 * mb / 0.115 + 3.5 * static_cast<double>(waves - 1);
+  return std::max(us, weight_mb / 6.0);
+}
+double weight_mb(int T, int N, int K, int bn) { return 2e-6 * N * K * (T > bn ? 1.2 : 1.0); }
+// Narrow tiles: set-up, first bytes and epilogue; the sum over a cluster (clusters of 8 do not pack
+// two CTAs to every SM); with adapters what of the shrink and its way back the copies do not hide.
+double narrow_us(int T, int N, int K, int Rs, int bn, int split, int sms) {
+  const int steps = ((K + 63) / 64 + split - 1) / split;
+  const long long ctas = static_cast<long long>((N + 127) / 128) * ((T + bn - 1) / bn) * split;
+  const double copy = copies_us(ctas, 16.0 + bn / 8.0, steps, 75.0, weight_mb(T, N, K, bn), sms);
+  double us = 2.7 + copy + bn / 128.0 * (split > 1 ? 1.2 : 0.6) + (split > 1 ? 0.4 : 0.0);
+  if (split == 8 && bn > 16 && (ctas > 128 || bn == 128)) us += bn == 128 ? 2.5 : 0.85;
+  if (Rs > 0)
+    us += bn == 16 ? std::min(3.9, std::max(split == 8 ? 1.4 : 1.8, 5.3 - 0.4 * copy)) : bn == 128 ? 7.0 : 4.4 - 0.1 * copy;
   return us;
 }
-// ... on pairs: a 64-deep K step of a 256 x 256 tile takes 0.3 us, a pair walks whole tiles.
-double wide_us(long long tiles, int nk, int sms) {
+// Each cluster shrinking for itself: As beside W in every step, the exchange in the cluster.
+double cluster_us(int T, int N, int K, int Rs, int bn, int split, int sms) {
+  const int steps = ((K + 63) / 64 + split - 1) / split;
+  const long long ctas = static_cast<long long>((N + 127) / 128) * ((T + bn - 1) / bn) * split;
+  const double copy = copies_us(ctas, 16.0 + (Rs + 63) / 64 * 8.0 + bn / 8.0, steps, 87.0, weight_mb(T, N, K, bn), sms);
+  return 5.2 + copy + (bn == 32 ? 0.4 : 0.0) + (split == 8 ? 0.85 : 0.0);
+}
+// Pairs: a 64-deep K step of a 256 x 256 tile takes 0.3 us, a pair walks whole tiles.
+double wide_us(int T, int N, int K, int Rs, int sms) {
+  const long long tiles = static_cast<long long>((T + 255) / 256) * ((N + 255) / 256);
   const long long waves = (tiles + sms / 2 - 1) / (sms / 2);
-  return 5.0 + 0.3 * static_cast<double>(waves) * nk;
+  return 3.5 + 0.3 * static_cast<double>(waves) * ((K + 63) / 64) + (Rs > 0 ? 3.5 : 0.0);
 }
 
-Tiles pick_tiles(int T, int N, int K, bool f32, bool adapters, int sms) {
+Tiles pick_tiles(int T, int N, int K, bool f32, int Rs, int sms) {
   const int nk = (K + 63) / 64;
-  Tiles best = {false, 16, 128, 1};
+  Tiles best = {kNarrow, 16, 128, 1};
   double us = 1e30;
+  auto offer = [&](double t, const Tiles& c) {
+    if (t < us) {
+      us = t;
+      best = c;
+    }
+  };
   for (int bn = 16; bn <= 128; bn *= 2) {
     if (bn > 16 && bn >= 2 * T) break;
     for (int split = 1; split <= kLinearMaxSplit && split <= nk; split *= 2) {
       // The tensor cores truncate as they accumulate, which adds up over a long K: a float32
       // result takes at most 1024 of K per accumulator (as far as a cluster goes).
       if (f32 && nk > 16 * split && split < kLinearMaxSplit && 2 * split <= nk) continue;
-      // the shrink runs at the product's pace, and its result then takes 4.5 us to come back in
-      const double t = narrow_us(T, N, nk, bn, split, sms) + (adapters ? 4.5 : 0.0);
-      if (t < us) {
-        us = t;
-        best = {false, bn, 128, split};
-      }
+      offer(narrow_us(T, N, K, Rs, bn, split, sms), {kNarrow, bn, 128, split});
+      if (Rs > 0 && Rs <= 128 && bn <= 32) offer(cluster_us(T, N, K, Rs, bn, split, sms), {kCluster, bn, 128, split});
     }
   }
-  if (f32) return best;
-  const long long tiles = static_cast<long long>((T + 255) / 256) * ((N + 255) / 256);
-  if (T > 128 && wide_us(tiles, nk, sms) + (adapters ? 4.0 : 0.0) < us) best = {true, 256, 256, 1};
+  if (!f32 && T > 128) offer(wide_us(T, N, K, Rs, sms), {kWide, 256, 256, 1});
   return best;
 }
 
@@ -189,17 +212,20 @@ moe_lora_status moe_lora_linear(moe_lora_handle* h, const moe_lora_linear_args* 
   if (!h->linear_ready) {
     ML_CUDA(linear_narrow_setup(), "linear setup");
     ML_CUDA(linear_wide_setup(), "linear setup");
+    ML_CUDA(linear_cluster_setup(), "linear setup");
     h->linear_ready = true;
   }
 
-  const Tiles c = pick_tiles(a->T, a->N, a->K, a->y_f32 != 0, active, h->num_sms);
+  const Tiles c = pick_tiles(a->T, a->N, a->K, a->y_f32 != 0, active ? Rs : 0, h->num_sms);
   p.T = a->T;
   p.K = a->K;
   p.slot_idx = active ? a->slot_idx : nullptr;
   p.status = static_cast<uint32_t*>(workspace);
   p.pieces = a->y_f32 ? kFloatPieces : 1;
   const long long x_stride = a->T > 1 ? a->x_stride : a->K, w_stride = a->N > 1 ? a->w_stride : a->K;
-  const int x_box = c.wide ? 128 : c.tokens, w_box = c.wide ? c.rows / 2 : 128;
+  const bool wide = c.kernel == kWide;
+  const int x_box = wide ? 128 : c.tokens, w_box = wide ? c.rows / 2 : 128;
+  const int a_box = wide ? linear_shrink_cols(Rs, c.rows) / 2 : c.kernel == kCluster ? 64 : 128;
   bool ok = tile_map(h, &p.tmap_x, a->x, a->T, a->K, x_stride, x_box) &&
             tile_map(h, &p.tmap_w, a->w, a->N, a->K, w_stride, w_box);
   p.token_tiles = (a->T + c.tokens - 1) / c.tokens;
@@ -211,7 +237,7 @@ moe_lora_status moe_lora_linear(moe_lora_handle* h, const moe_lora_linear_args* 
     p.u = reinterpret_cast<__nv_bfloat16*>(static_cast<uint8_t*>(workspace) + 256);
     p.flags = h->linear_flags;
     const long long ldu = static_cast<long long>(p.pieces) * Rs;
-    ok = ok && tile_map(h, &p.tmap_a, Ap, Rs, a->K, a->K, c.wide ? linear_shrink_cols(Rs, c.rows) / 2 : 128) &&
+    ok = ok && tile_map(h, &p.tmap_a, Ap, Rs, a->K, a->K, a_box) &&
          tile_map(h, &p.tmap_b, Bp, a->N, Rs, Rs, w_box) && tile_map(h, &p.tmap_u, p.u, a->T, ldu, ldu, x_box);
   }
   p.N = a->N;
@@ -219,7 +245,7 @@ moe_lora_status moe_lora_linear(moe_lora_handle* h, const moe_lora_linear_args* 
   p.y = a->y;
   p.ldy = a->T > 1 ? a->y_stride : a->N;
   p.y_f32 = a->y_f32 != 0;
-  if (c.wide) {
+  if (wide) {
     p.y_vec = p.ldy % 8 == 0 && aligned16(a->y) && p.ldy <= kMaxStride;
     if (p.y_vec) ok = ok && tile_map(h, &p.tmap_y, a->y, a->T, a->N, p.ldy, 32);
     if (!ok) return MOE_LORA_ERR_INVALID_ARG;
@@ -227,7 +253,10 @@ moe_lora_status moe_lora_linear(moe_lora_handle* h, const moe_lora_linear_args* 
   } else {
     p.y_vec = p.ldy % 4 == 0 && (reinterpret_cast<uintptr_t>(a->y) & (p.y_f32 ? 15u : 7u)) == 0;
     if (!ok) return MOE_LORA_ERR_INVALID_ARG;
-    ML_LAUNCH(h, launch_linear_narrow(p, c.tokens, c.split, stream), "linear launch");
+    ML_LAUNCH(h,
+              c.kernel == kCluster ? launch_linear_cluster(p, c.tokens, c.split, stream)
+                                   : launch_linear_narrow(p, c.tokens, c.split, stream),
+              "linear launch");
   }
   return MOE_LORA_OK;
 }

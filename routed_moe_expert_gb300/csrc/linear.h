@@ -49,6 +49,11 @@ constexpr int kLinearMaxSplit = 8;
 cudaError_t linear_narrow_setup();   // once per device
 cudaError_t launch_linear_narrow(const LinearParams& p, int bn, int split, cudaStream_t stream);
 
+// The same tiles (bn 16 or 32) with at most 128 stacked columns, each cluster shrinking for
+// itself.  Maps' boxes: {64, 128} of w and b, {64, 64} of a, {64, bn} of x.
+cudaError_t linear_cluster_setup();
+cudaError_t launch_linear_cluster(const LinearParams& p, int bn, int split, cudaStream_t stream);
+
 // Tiles of 256 tokens x bn (128 or 256) weight rows on CTA pairs, bf16 y.  Maps' boxes: {64, 128}
 // of x and u, {64, bn / 2} of w and b, {64, linear_shrink_cols(Rs, bn) / 2} of a.
 cudaError_t linear_wide_setup();

@@ -36,10 +36,11 @@ constexpr int kThreads = 192;
 constexpr int kABytes = 128 * 128;
 constexpr int kSmemBudget = 112 * 1024;   // two CTAs per SM
 constexpr int kMaxSplit = kLinearMaxSplit;
+constexpr int kBatch = 3;                 // quads of the tile that a thread sums at a time
 
 __host__ __device__ constexpr int stage_bytes(int bn) { return kABytes + bn * 128; }
 __host__ __device__ constexpr int stages_of(int bn) { return (kSmemBudget - 2048) / stage_bytes(bn); }
-constexpr int smem_bytes(int bn) { return 1024 + stages_of(bn) * stage_bytes(bn) + 512; }
+constexpr int smem_bytes(int bn) { return 1024 + stages_of(bn) * stage_bytes(bn) + 256 + 12 * bn; }
 
 // Four floats at this CTA's shared address `at`, in CTA `rank` of the cluster.
 MLDEV float4 ld_cluster_f4(uint32_t at, int rank) {
@@ -74,6 +75,9 @@ __global__ void __launch_bounds__(kThreads, 2) linear_narrow_kernel(const __grid
   uint32_t* mask_s = reinterpret_cast<uint32_t*>(drain + 1);   // [2] adapter blocks present in the tile
   uint32_t* tmem_slot = mask_s + 2;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* lo_s = reinterpret_cast<int*>(tmem_slot + 2);   // (shrink) [BN] a token's columns of the stack
+  int* hi_s = lo_s + BN;                               // and its factor
+  float* sc_s = reinterpret_cast<float*>(hi_s + BN);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int C = static_cast<int>(cluster_nctas()), rank = static_cast<int>(cluster_ctarank());
@@ -230,6 +234,13 @@ __global__ void __launch_bounds__(kThreads, 2) linear_narrow_kernel(const __grid
       if (static_cast<uint32_t>(m >> 32)) atomicOr(&mask_s[1], static_cast<uint32_t>(m >> 32));
       mbar_arrive(mask_bar);
     }
+    if (shrink && et < BN) {
+      const int sl = t0 + et < p.T ? p.slot_idx[t0 + et] : -1;
+      const bool has = sl >= 0 && sl < p.slots.S;
+      lo_s[et] = has ? p.slots.lo[sl] : 0;
+      hi_s[et] = has ? p.slots.hi[sl] : 0;
+      sc_s[et] = has ? p.slots.scal[sl] : 0.0f;
+    }
     if (blockIdx.x == 0) {   // the only writer of the status word before a timeout
       int bad = 0;
       if (p.slot_idx != nullptr)
@@ -273,31 +284,43 @@ __global__ void __launch_bounds__(kThreads, 2) linear_narrow_kernel(const __grid
   const int q_lo = static_cast<int>(static_cast<long long>(quads) * rank / C);
   const int q_hi = static_cast<int>(static_cast<long long>(quads) * (rank + 1) / C);
   const uint32_t part0 = smem_u32(smem);
-  for (int q = q_lo + static_cast<int>(threadIdx.x); q < q_hi; q += kThreads) {
-    const int j = q >> 5, r = (q & 31) * 4;
-    const int t = t0 + j, n = row0 + r;
-    if (n >= N) continue;
-    float4 v[kMaxSplit];
+  for (int q0 = q_lo + static_cast<int>(threadIdx.x); q0 < q_hi; q0 += kBatch * kThreads) {
+   float4 v[kBatch][kMaxSplit], bias[kBatch];
 #pragma unroll
-    for (int c = 0; c < kMaxSplit; ++c)   // all in flight together
-      if (c < C) v[c] = ld_cluster_f4(part0 + static_cast<uint32_t>(q) * 16u, c);
-    float f[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+   for (int i = 0; i < kBatch; ++i) {   // all loads of a batch in flight together
+    const int q = q0 + i * kThreads, n = row0 + (q & 31) * 4;
+    bias[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (q >= q_hi || n >= N) continue;
+    if (!shrink && p.bias != nullptr) {
+      bias[i].x = __ldg(p.bias + n);
+      if (n + 1 < N) bias[i].y = __ldg(p.bias + n + 1);
+      if (n + 2 < N) bias[i].z = __ldg(p.bias + n + 2);
+      if (n + 3 < N) bias[i].w = __ldg(p.bias + n + 3);
+    }
+#pragma unroll
+    for (int c = 0; c < kMaxSplit; ++c)
+      if (c < C) v[i][c] = ld_cluster_f4(part0 + static_cast<uint32_t>(q) * 16u, c);
+   }
+#pragma unroll
+   for (int i = 0; i < kBatch; ++i) {
+    const int q = q0 + i * kThreads;
+    const int j = q >> 5, t = t0 + j, n = row0 + (q & 31) * 4;
+    if (q >= q_hi || n >= N) continue;
+    float f[4] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w};
 #pragma unroll
     for (int c = 1; c < kMaxSplit; ++c)
       if (c < C) {
-        f[0] += v[c].x;
-        f[1] += v[c].y;
-        f[2] += v[c].z;
-        f[3] += v[c].w;
+        f[0] += v[i][c].x;
+        f[1] += v[i][c].y;
+        f[2] += v[i][c].z;
+        f[3] += v[i][c].w;
       }
     if (shrink) {
-      const int sl = p.slot_idx[t];
-      const bool has = sl >= 0 && sl < p.slots.S;
-      const int lo = has ? p.slots.lo[sl] : 0, hi = has ? p.slots.hi[sl] : 0;
-      const float sc = has ? p.slots.scal[sl] : 0.0f;
+      const int lo = lo_s[j], hi = hi_s[j];
+      const float sc = sc_s[j];
       __nv_bfloat16* u = p.u + static_cast<long long>(t) * p.pieces * p.Rs + n;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) f[i] = (n + i >= lo && n + i < hi) ? sc * f[i] : 0.0f;
+      for (int e = 0; e < 4; ++e) f[e] = (n + e >= lo && n + e < hi) ? sc * f[e] : 0.0f;
       for (int piece = 0; piece < p.pieces; ++piece) {   // the float32 as a sum of bf16 pieces
         const uint2 v = pack4(f);
         *reinterpret_cast<uint2*>(u + static_cast<long long>(piece) * p.Rs) = v;
@@ -307,29 +330,28 @@ __global__ void __launch_bounds__(kThreads, 2) linear_narrow_kernel(const __grid
         f[3] -= __uint_as_float(v.y & 0xffff0000u);
       }
     } else {
-      if (p.bias != nullptr) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (n + i < p.N) f[i] += __ldg(p.bias + n + i);
-      }
+      f[0] += bias[i].x;
+      f[1] += bias[i].y;
+      f[2] += bias[i].z;
+      f[3] += bias[i].w;
       const long long at = static_cast<long long>(t) * p.ldy + n;
       if (p.y_vec && n + 4 <= p.N) {
         if (p.y_f32) *reinterpret_cast<float4*>(static_cast<float*>(p.y) + at) = make_float4(f[0], f[1], f[2], f[3]);
         else *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.y) + at) = pack4(f);
       } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (n + i < p.N) {
-            if (p.y_f32) static_cast<float*>(p.y)[at + i] = f[i];
-            else static_cast<__nv_bfloat16*>(p.y)[at + i] = f2bf(f[i]);
+        for (int e = 0; e < 4; ++e)
+          if (n + e < p.N) {
+            if (p.y_f32) static_cast<float*>(p.y)[at + e] = f[e];
+            else static_cast<__nv_bfloat16*>(p.y)[at + e] = f2bf(f[e]);
           }
       }
     }
+   }
   }
   if (shrink) {   // this CTA's part of u is written: read next by other CTAs' TMA copies
-    __threadfence();
     fence_proxy_async_global();
-    __syncthreads();
+    __syncthreads();   // the release below covers every thread's writes before this barrier
     if (threadIdx.x == 0) red_release_add(ready, 1);
   }
   if (C > 1) {   // no CTA leaves while others read its part sums

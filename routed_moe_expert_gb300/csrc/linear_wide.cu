@@ -336,9 +336,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
             }
           }
         }
-        __threadfence();
         fence_proxy_async_global();   // read next by other CTAs' TMA copies
-        __syncwarp();
+        __syncwarp();                 // the release below covers every lane's writes before this
         if (lane == 0) red_release_add(reinterpret_cast<int*>(p.flags + tt), 1);
       } else
 #pragma unroll 1
