@@ -133,6 +133,19 @@ def test_ruled_out_experts(handle, sigmoid):
     assert ids[0].tolist() == [5, 0] and w[0, 0] == 1.0 and w[0, 1] == 0.0
 
 
+@pytest.mark.parametrize("spread", [1.0, 8.0, 60.0])
+@pytest.mark.parametrize("E", [128, 200, 384])
+def test_softmax_scores_are_the_correctly_rounded_quotients(handle, E, spread):
+    """The kernel's quotient (a reciprocal and one residual) against IEEE division of the same
+    exponentials by the same sum, bit for bit; at the largest spread the small terms underflow."""
+    g = torch.Generator(device="cuda").manual_seed(E)
+    z = torch.randn((400, E), generator=g, device="cuda") * spread
+    e = torch.exp(z - z.amax(1, keepdim=True))
+    p = e / e.double().sum(1, keepdim=True).float()
+    o = pkg.moe_lora_select_experts(handle, z, 32, renormalize=False)
+    assert torch.equal(o["topk_weights"], p.gather(1, o["topk_ids"].long()))
+
+
 def test_strided_and_unaligned_logits(handle):
     wide = torch.full((30, 300), float("nan"), dtype=torch.float32, device="cuda")
     for lead, E, dtype in ((3, 256, torch.float32), (4, 256, torch.float32), (1, 129, torch.bfloat16), (2, 128, torch.bfloat16)):
