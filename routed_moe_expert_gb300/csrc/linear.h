@@ -20,6 +20,7 @@ struct LinearSlots {
 struct LinearParams {
   CUtensorMap tmap_w;    // weights [N, K]
   CUtensorMap tmap_x;    // [T, K]
+  CUtensorMap tmap_xs;   // (narrow) the same with the shrink's token tile
   CUtensorMap tmap_a;    // the stacked A [Rs, K]
   CUtensorMap tmap_b;    // the stacked B [N, Rs]
   CUtensorMap tmap_u;    // the shrunk rows [T, pieces * Rs]
@@ -28,6 +29,7 @@ struct LinearParams {
   int Rs;                // stacked columns, a multiple of 64 (0: no adapters)
   int pieces;            // 1, or kFloatPieces bf16 pieces of a float32 u
   int token_tiles;
+  int shrink_tokens;     // (narrow) tokens of a shrink tile, a divisor of the token tile
   const int32_t* slot_idx;
   const float* bias;     // [N] or null
   void* y;               // [T, ldy] bf16 or float32
@@ -44,7 +46,8 @@ struct LinearParams {
 constexpr int kLinearFlags = 8192;   // token tiles of a call with adapters
 
 // One 128-row x bn-token tile per cluster of `split` CTAs, which share the tile's K; split is at
-// most the number of 64-wide K blocks.  Maps' boxes: {64, 128} of w, a, b, {64, bn} of x, u.
+// most the number of 64-wide K blocks.  Maps' boxes: {64, 128} of w, a, b, {64, bn} of
+// x and u, {64, shrink_tokens} of xs.
 constexpr int kLinearMaxSplit = 8;
 cudaError_t linear_narrow_setup();   // once per device
 cudaError_t launch_linear_narrow(const LinearParams& p, int bn, int split, cudaStream_t stream);

@@ -6,8 +6,9 @@
 //
 // with every slot's A rows and B columns stacked side by side (As [Rs, K], Bs [N, Rs]), so
 // adapters of any ranks and number are one more K range of the same product.  The shrink (u)
-// is the same tile with As in the place of W and an epilogue that scales, masks and rounds; its
-// tiles are the grid's first, so one launch does all.
+// is the same tile with As in the place of W, fewer tokens (so that it is done sooner: its result is
+// waited for), and an epilogue that scales, masks and rounds; its tiles are the grid's first, so
+// one launch does all.
 //
 // The weights are the MMA's M = 128 operand and the tokens its N = BN, so a batch of one token
 // still streams whole weight rows.  A cluster of CTAs shares a tile: each takes a part of K
@@ -81,19 +82,25 @@ __global__ void __launch_bounds__(kThreads, 2) linear_narrow_kernel(const __grid
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int C = static_cast<int>(cluster_nctas()), rank = static_cast<int>(cluster_ctarank());
-  const int shrink_tiles = (p.Rs + 127) / 128 * p.token_tiles;
   const int index = static_cast<int>(blockIdx.x) / C;
-  const bool shrink = index < shrink_tiles;
-  const int tile = shrink ? index : index - shrink_tiles;
-  const int nt = tile / p.token_tiles, qt = tile - nt * p.token_tiles;
-  const int row0 = nt * 128, t0 = qt * BN;
+  const int a_tiles = (p.Rs + 127) / 128;   // row tiles of the stacked A
+  const int shrink_parts = p.Rs > 0 ? (p.T + p.shrink_tokens - 1) / p.shrink_tokens : 0;
+  const bool shrink = index < a_tiles * shrink_parts;
+  const int tile = shrink ? index : index - a_tiles * shrink_parts;
+  const int across = shrink ? shrink_parts : p.token_tiles;
+  const int nt = tile / across, part_t = tile - nt * across;
+  const int bn = shrink ? p.shrink_tokens : BN;   // tokens of the tile
+  const int row0 = nt * 128, t0 = part_t * bn;
+  const int qt = t0 / BN;                         // the product's token tile
   const int N = shrink ? p.Rs : p.N;
   const int nk = (p.K + 63) >> 6;
   const int k_lo = static_cast<int>(static_cast<long long>(nk) * rank / C);
   const int k_hi = static_cast<int>(static_cast<long long>(nk) * (rank + 1) / C);
   const bool lora = !shrink && p.Rs > 0;
   int* ready = reinterpret_cast<int*>(p.flags + qt);
-  const int ready_target = (p.Rs + 127) / 128 * C;
+  // shrink CTAs of this token tile
+  const int ready_target =
+      lora ? a_tiles * C * ((min(BN, p.T - t0) + p.shrink_tokens - 1) / p.shrink_tokens) : 0;
 
   // the 64-column blocks of the stack that slot sl's adapter lies in
   auto blocks_of = [&](int sl) -> uint64_t {
@@ -116,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_narrow_kernel(const __grid
   }
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(shrink ? &p.tmap_a : &p.tmap_w);
-    tma_prefetch_desc(&p.tmap_x);
+    tma_prefetch_desc(shrink ? &p.tmap_xs : &p.tmap_x);
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, TMEM_COLS);
@@ -135,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_narrow_kernel(const __grid
     // a stack of several row tiles: leave out those that no token needs (the whole cluster decides
     // alike; the first tile stays, it writes the status word)
     uint64_t m = 0;
-    for (int j = threadIdx.x; j < BN && t0 + j < p.T; j += kThreads) m |= blocks_of(p.slot_idx[t0 + j]);
+    for (int j = threadIdx.x; j < bn && t0 + j < p.T; j += kThreads) m |= blocks_of(p.slot_idx[t0 + j]);
     if (!__syncthreads_or(((m >> (row0 >> 6)) & 3ull) != 0)) {
       if (threadIdx.x == 0) red_release_add(ready, 1);
       if (warp == 1) tmem_dealloc(tmem_base, TMEM_COLS);
@@ -151,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_narrow_kernel(const __grid
       auto issue = [&](const CUtensorMap* wm, int kw, const CUtensorMap* xm, int kx) -> bool {
         if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status, kWhereLinear)) return false;
         uint8_t* a = smem + stage * STAGE;
-        mbar_arrive_expect_tx(&full[stage], STAGE);
+        mbar_arrive_expect_tx(&full[stage], kABytes + bn * 128);
         tma_load_2d(a, wm, &full[stage], kw, row0, p.token_tiles == 1 ? pol_w : pol_x);
         tma_load_2d(a + kABytes, xm, &full[stage], kx, t0, pol_x);
         issued |= 1u << stage;
@@ -163,7 +170,8 @@ __global__ void __launch_bounds__(kThreads, 2) linear_narrow_kernel(const __grid
         return true;
       };
       const CUtensorMap* wmap = shrink ? &p.tmap_a : &p.tmap_w;
-      for (int kb = k_lo; ok && kb < k_hi; ++kb) ok = issue(wmap, kb * 64, &p.tmap_x, kb * 64);
+      const CUtensorMap* xmap = shrink ? &p.tmap_xs : &p.tmap_x;
+      for (int kb = k_lo; ok && kb < k_hi; ++kb) ok = issue(wmap, kb * 64, xmap, kb * 64);
       if (ok && lora) {
         ok = mbar_wait(mask_bar, 0, abort_flag, p.status, kWhereLinear);
         const uint64_t mask = mask_s[0] | (static_cast<uint64_t>(mask_s[1]) << 32);
@@ -191,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_narrow_kernel(const __grid
     }
   } else if (warp == 1) {   // ------------------------------------------ MMA issuer
     if (lane == 0) {
-      constexpr uint32_t idesc = idesc_bf16_f32(128, BN);
+      const uint32_t idesc = idesc_bf16_f32(128, bn);
       int stage = 0, ok = 1, first = 1;
       uint32_t phase = 0;
       auto consume = [&]() -> bool {
@@ -234,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_narrow_kernel(const __grid
       if (static_cast<uint32_t>(m >> 32)) atomicOr(&mask_s[1], static_cast<uint32_t>(m >> 32));
       mbar_arrive(mask_bar);
     }
-    if (shrink && et < BN) {
+    if (shrink && et < bn) {
       const int sl = t0 + et < p.T ? p.slot_idx[t0 + et] : -1;
       const bool has = sl >= 0 && sl < p.slots.S;
       lo_s[et] = has ? p.slots.lo[sl] : 0;
@@ -258,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_narrow_kernel(const __grid
     if (mbar_wait_sleep(tfull, 0, abort_flag, p.status, kWhereLinear)) {
       tc_fence_after();
 #pragma unroll 1
-      for (int c = 0; c < BN && t0 + c < p.T; c += 16) {   // warp-uniform bound
+      for (int c = 0; c < bn && t0 + c < p.T; c += 16) {   // warp-uniform bound
         uint32_t v[16];
         __syncwarp();   // tcgen05.ld is .aligned
         tmem_ld_x16(taddr + c, v);
@@ -279,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_narrow_kernel(const __grid
   }
 
   // this CTA's share of the tile: quads of 4 rows of a token, part sums added in rank order
-  const int nvalid = min(BN, p.T - t0);
+  const int nvalid = min(bn, p.T - t0);
   const int quads = nvalid * 32;
   const int q_lo = static_cast<int>(static_cast<long long>(quads) * rank / C);
   const int q_hi = static_cast<int>(static_cast<long long>(quads) * (rank + 1) / C);
@@ -410,7 +418,9 @@ cudaError_t linear_narrow_setup() {
 }
 
 cudaError_t launch_linear_narrow(const LinearParams& p, int bn, int split, cudaStream_t stream) {
-  const long long tiles = static_cast<long long>((p.N + 127) / 128 + (p.Rs + 127) / 128) * p.token_tiles;
+  const long long tiles =
+      static_cast<long long>((p.N + 127) / 128) * p.token_tiles +
+      (p.Rs > 0 ? static_cast<long long>((p.Rs + 127) / 128) * ((p.T + p.shrink_tokens - 1) / p.shrink_tokens) : 0);
   if (tiles * split > 0x7fffffffLL) return cudaErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(tiles * split)), block(kThreads);
   switch (bn) {
