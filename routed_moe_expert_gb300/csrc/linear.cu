@@ -84,11 +84,14 @@ double cluster_us(int T, int N, int K, int Rs, int bn, int split, int sms) {
   const double copy = copies_us(ctas, 16.0 + (Rs + 63) / 64 * 8.0 + bn / 8.0, steps, 87.0, weight_mb(T, N, K, bn), sms);
   return 5.2 + copy + (bn == 32 ? 0.4 : 0.0) + (split == 8 ? 0.85 : 0.0);
 }
-// Pairs: a 64-deep K step of a 256 x 256 tile takes 0.3 us, a pair walks whole tiles.
-double wide_us(int T, int N, int K, int Rs, int sms) {
-  const long long tiles = static_cast<long long>((T + 255) / 256) * ((N + 255) / 256);
-  const long long waves = (tiles + sms / 2 - 1) / (sms / 2);
-  return 3.5 + 0.3 * static_cast<double>(waves) * ((K + 63) / 64) + (Rs > 0 ? 3.5 : 0.0);
+// Pairs: a pair walks whole tiles of 256 tokens x `rows`; a 64-deep K step takes 0.30 us at 256 rows
+// (the tensor cores' rate), 0.285 at 192 and 0.28 at 128 (an SM's intake of copies), so the smaller ones pay
+// only where they bring no further wave: T 3066, N 1551, K 6624: 66.6 / 62.9 / 87.6 us.
+double wide_us(int T, int N, int K, int Rs, int rows, int sms) {
+  const long long tt = (T + 255) / 256, tiles = tt * ((N + rows - 1) / rows);
+  const long long shrinks = Rs > 0 ? tt * ((Rs + rows - 1) / rows) : 0;
+  const long long waves = (tiles + (tiles <= sms / 2 ? shrinks : 0) + sms / 2 - 1) / (sms / 2);
+  return 3.5 + (rows == 256 ? 0.3 : rows == 192 ? 0.285 : 0.28) * static_cast<double>(waves) * ((K + 63) / 64) + (Rs > 0 ? 3.5 : 0.0);
 }
 
 Tiles pick_tiles(int T, int N, int K, bool f32, int Rs, int sms) {
@@ -111,12 +114,8 @@ Tiles pick_tiles(int T, int N, int K, bool f32, int Rs, int sms) {
       if (Rs > 0 && Rs <= 128 && bn <= 32) offer(cluster_us(T, N, K, Rs, bn, split, sms), {kCluster, bn, 128, split});
     }
   }
-  if (!f32 && T > 128) {
-    offer(wide_us(T, N, K, Rs, sms), {kWide, 256, 256, 1});
-    // half as many weight rows per tile where that still is one tile per pair (T 777, N 1536: 0.5 us)
-    if (static_cast<long long>((T + 255) / 256) * ((N + 127) / 128) <= sms / 2)
-      offer(wide_us(T, N, K, Rs, sms) - 0.5, {kWide, 256, 128, 1});
-  }
+  if (!f32 && T > 128)
+    for (int rows = 256; rows >= 128; rows -= 64) offer(wide_us(T, N, K, Rs, rows, sms), {kWide, 256, rows, 1});
   return best;
 }
 

@@ -40,14 +40,14 @@ constexpr int kTokenGroup = 8;
 constexpr uint64_t kPeerDrainNs = 100000;      // 100 us for an aborted odd CTA's copies to land
 
 __host__ __device__ constexpr int stage_bytes(int bn) { return kABytes + bn / 2 * 128; }
-__host__ __device__ constexpr int stages_of(int bn) { return bn == 256 ? 6 : 8; }
+__host__ __device__ constexpr int stages_of(int bn) { return bn == 256 ? 6 : bn == 192 ? 6 : 8; }
 __host__ __device__ constexpr int smem_bytes(int bn) { return 1024 + stages_of(bn) * stage_bytes(bn) + kYBytes + 256; }
 
 template <int BN>
 __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_constant__ LinearParams p) {
   constexpr int kStages = stages_of(BN);
   constexpr uint32_t STAGE = stage_bytes(BN);
-  constexpr uint32_t TMEM_COLS = 2 * BN;
+  constexpr uint32_t TMEM_COLS = BN == 128 ? 256u : 512u;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* ybuf = smem + kStages * STAGE;
@@ -410,6 +410,8 @@ cudaError_t linear_wide_setup() {
   cudaError_t err = cudaFuncSetAttribute(linear_wide_kernel<256>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          smem_bytes(256));
   if (err != cudaSuccess) return err;
+  err = cudaFuncSetAttribute(linear_wide_kernel<192>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(192));
+  if (err != cudaSuccess) return err;
   return cudaFuncSetAttribute(linear_wide_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(128));
 }
 
@@ -417,10 +419,11 @@ cudaError_t launch_linear_wide(const LinearParams& p, int bn, int sms, cudaStrea
   const int cols = linear_shrink_cols(p.Rs, bn);
   const long long tiles =
       static_cast<long long>((p.N + bn - 1) / bn + (cols ? (p.Rs + cols - 1) / cols : 0)) * p.token_tiles;
-  if (tiles > 0x3fffffffLL || (bn != 128 && bn != 256)) return cudaErrorInvalidValue;
+  if (tiles > 0x3fffffffLL || (bn != 128 && bn != 192 && bn != 256)) return cudaErrorInvalidValue;
   const int pairs = static_cast<int>(tiles < sms / 2 ? tiles : sms / 2);
   const dim3 grid(2 * pairs), block(kThreads);
   if (bn == 256) return launch_kc(linear_wide_kernel<256>, grid, block, smem_bytes(256), stream, true, 2, p);
+  if (bn == 192) return launch_kc(linear_wide_kernel<192>, grid, block, smem_bytes(192), stream, true, 2, p);
   return launch_kc(linear_wide_kernel<128>, grid, block, smem_bytes(128), stream, true, 2, p);
 }
 

@@ -81,7 +81,8 @@ def test_widths(handle, T, N, K):
     _check(_run(handle, c := _case(T, N, K, (), seed=N + T, bias=True), True), c, True)
 
 
-@pytest.mark.parametrize("T,N,K", [(2500, 2050, 136), (2560, 2048, 512), (5121, 1000, 72), (19500, 130, 64), (1281, 4096, 264)])
+@pytest.mark.parametrize("T,N,K", [(2500, 2050, 136), (2560, 2048, 512), (5121, 1000, 72), (19500, 130, 64), (1281, 4096, 264),
+                                   (3066, 1551, 136), (400, 1536, 2048), (1536, 3008, 328)])
 @pytest.mark.parametrize("slots", ["mixed", "runs", "none", None])
 def test_long_batches(handle, T, N, K, slots):
     """Enough tokens for the widest tiles: ragged in every direction, rows of y on and off 16-byte
