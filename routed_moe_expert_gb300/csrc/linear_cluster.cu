@@ -60,6 +60,25 @@ MLDEV uint32_t cluster_nctas() {
   return r;
 }
 
+// Sums of two neighbouring tokens' values over the C CTAs of the cluster, in rank order; all loads
+// go out before the first is used.
+template <int C>
+MLDEV float2 cluster_sum2(uint32_t at) {
+  float u[C], v[C];
+#pragma unroll
+  for (int r = 0; r < C; ++r) {
+    u[r] = ld_cluster_f(at, r);
+    v[r] = ld_cluster_f(at + 512, r);
+  }
+  float2 s = make_float2(u[0], v[0]);
+#pragma unroll
+  for (int r = 1; r < C; ++r) {
+    s.x += u[r];
+    s.y += v[r];
+  }
+  return s;
+}
+
 template <int BN, int NB>
 __global__ void __launch_bounds__(kThreads, 2) linear_cluster_kernel(const __grid_constant__ LinearParams p) {
   constexpr int kStages = stages_of(BN, NB);
@@ -342,23 +361,17 @@ __global__ void __launch_bounds__(kThreads, 2) linear_cluster_kernel(const __gri
 #pragma unroll 1
     for (int c = 0; c < count; c += 8) {   // warp-uniform bound
       float f[8];
+      const uint32_t at = part0 + static_cast<uint32_t>(((j_lo + c) * 128 + row) * 4);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = 0.0f;
-#pragma unroll
-      for (int r = 0; r < kMaxSplit; ++r)
-        if (r < C) {
-          float v[8];
-          const uint32_t at = part0 + static_cast<uint32_t>(((j_lo + c) * 128 + row) * 4);
-          if (c + 8 <= count) {   // no test between the loads: they go out together
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = ld_cluster_f(at + j * 512, r);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = c + j < count ? ld_cluster_f(at + j * 512, r) : 0.0f;
-          }
-#pragma unroll
-          for (int j = 0; j < 8; ++j) f[j] += v[j];
-        }
+      for (int j = 0; j < 8; j += 2) {
+        if (c + j >= count) break;   // (the second token of a pair may lie past the share: not used)
+        const float2 s = C == 8   ? cluster_sum2<8>(at + j * 512)
+                         : C == 4 ? cluster_sum2<4>(at + j * 512)
+                         : C == 2 ? cluster_sum2<2>(at + j * 512)
+                                  : cluster_sum2<1>(at + j * 512);
+        f[j] = s.x;
+        f[j + 1] = s.y;
+      }
       if (mask != 0u) {
         if (!waited && !mbar_wait_sleep(dfull, 0, abort_flag, p.status, kWhereLinear)) break;
         waited = true;
