@@ -56,13 +56,15 @@ struct Tiles {
 // meant to rank the choices.
 //
 // Copies of a step (a 64-wide K block of a tile): an SM's shared memory takes in `one` GB/s with one
-// CTA there, 115 with two; the weights come from HBM, and from L2 again for further token tiles.
-double copies_us(long long ctas, double kb_step, int steps, double one, double weight_mb, int sms) {
+// CTA there, 115 with two.  The weights come from HBM, and from L2 again for further token tiles;
+// how fast goes by the weight stages in flight on an SM (16 KB each, `stages` per CTA).
+double copies_us(long long ctas, double kb_step, int steps, double one, double weight_mb, int stages, int sms) {
   const double mb = kb_step * steps * 1e-3;
   const long long waves = (ctas + 2 * sms - 1) / (2 * sms);
   const double us = ctas <= sms ? mb / (one * 1e-3)
                                 : static_cast<double>(waves) * 2.0 * mb / 0.115 + 3.5 * static_cast<double>(waves - 1);
-  return std::max(us, weight_mb / 6.0);
+  const double hbm = ctas > sms || stages >= 6 ? 6.3 : stages == 5 ? 5.8 : stages == 4 ? 5.3 : 4.6;   // MB/us
+  return std::max(us, weight_mb / hbm);
 }
 double weight_mb(int T, int N, int K, int bn) { return 2e-6 * N * K * (T > bn ? 1.2 : 1.0); }
 // Narrow tiles: set-up, first bytes and epilogue; the sum over a cluster (clusters of 8 do not pack
@@ -70,7 +72,8 @@ double weight_mb(int T, int N, int K, int bn) { return 2e-6 * N * K * (T > bn ? 
 double narrow_us(int T, int N, int K, int Rs, int bn, int split, int sms) {
   const int steps = ((K + 63) / 64 + split - 1) / split;
   const long long ctas = static_cast<long long>((N + 127) / 128) * ((T + bn - 1) / bn) * split;
-  const double copy = copies_us(ctas, 16.0 + bn / 8.0, steps, 75.0, weight_mb(T, N, K, bn), sms);
+  const double copy = copies_us(ctas, 16.0 + bn / 8.0, steps, 75.0, weight_mb(T, N, K, bn),
+                                bn == 16 ? 6 : bn == 32 ? 5 : bn == 64 ? 4 : 3, sms);
   double us = 2.7 + copy + bn / 128.0 * (split > 1 ? 1.2 : 0.6) + (split > 1 ? 0.4 : 0.0);
   if (split == 8 && bn > 16 && (ctas > 128 || bn == 128)) us += bn == 128 ? 2.5 : 0.85;
   if (Rs > 0)
@@ -81,8 +84,9 @@ double narrow_us(int T, int N, int K, int Rs, int bn, int split, int sms) {
 double cluster_us(int T, int N, int K, int Rs, int bn, int split, int sms) {
   const int steps = ((K + 63) / 64 + split - 1) / split;
   const long long ctas = static_cast<long long>((N + 127) / 128) * ((T + bn - 1) / bn) * split;
-  const double copy = copies_us(ctas, 16.0 + (Rs + 63) / 64 * 8.0 + bn / 8.0, steps, 87.0, weight_mb(T, N, K, bn), sms);
-  return 5.2 + copy + (bn == 32 ? 0.4 : 0.0) + (split == 8 ? 0.85 : 0.0);
+  const double copy = copies_us(ctas, 16.0 + (Rs + 63) / 64 * 8.0 + bn / 8.0, steps, 87.0,
+                                weight_mb(T, N, K, bn), Rs <= 64 && bn == 16 ? 4 : 3, sms);
+  return 4.4 + copy + (bn == 32 ? 0.9 : 0.0);
 }
 // Pairs: a pair walks whole tiles of 256 tokens x `rows`; a 64-deep K step takes 0.30 us at 256 rows
 // (the tensor cores' rate), 0.285 at 192 and 0.28 at 128 (an SM's intake of copies), so the smaller ones pay
