@@ -33,12 +33,12 @@ moe_lora_status check_ranks(int S, const int32_t* h_ranks, int most) {
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 bool tile_map(const moe_lora_handle* h, CUtensorMap* m, const void* base, long long rows, long long cols,
-              long long stride, int box_rows) {
+              long long stride, int box_rows, bool f32 = false) {   // boxes of 128 bytes x box_rows
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride) * 2};
-  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride) * (f32 ? 4 : 2)};
+  const cuuint32_t box[2] = {f32 ? 32u : 64u, static_cast<cuuint32_t>(box_rows)};
   const cuuint32_t estr[2] = {1, 1};
-  return h->encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+  return h->encode(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -58,11 +58,14 @@ struct Tiles {
 // Copies of a step (a 64-wide K block of a tile): an SM's shared memory takes in `one` GB/s with one
 // CTA there, 115 with two.  The weights come from HBM, and from L2 again for further token tiles;
 // how fast goes by the weight stages in flight on an SM (16 KB each, `stages` per CTA).
-double copies_us(long long ctas, double kb_step, int steps, double one, double weight_mb, int stages, int sms) {
+double copies_us(long long ctas, int split, double kb_step, int steps, double one, double weight_mb, int stages,
+                 double wave, int sms) {
   const double mb = kb_step * steps * 1e-3;
-  const long long waves = (ctas + 2 * sms - 1) / (2 * sms);
+  // CTAs that are resident together: clusters stay within a GPC and leave some of its SMs' places
+  const int room = 2 * sms - (split == 8 ? sms / 3 : split == 4 ? sms / 9 : 0);
+  const long long waves = (ctas + room - 1) / room;
   const double us = ctas <= sms ? mb / (one * 1e-3)
-                                : static_cast<double>(waves) * 2.0 * mb / 0.115 + 3.5 * static_cast<double>(waves - 1);
+                                : static_cast<double>(waves) * 2.0 * mb / 0.115 + wave * static_cast<double>(waves - 1);
   const double hbm = ctas > sms || stages >= 6 ? 6.3 : stages == 5 ? 5.8 : stages == 4 ? 5.3 : 4.6;   // MB/us
   return std::max(us, weight_mb / hbm);
 }
@@ -72,8 +75,9 @@ double weight_mb(int T, int N, int K, int bn) { return 2e-6 * N * K * (T > bn ? 
 double narrow_us(int T, int N, int K, int Rs, int bn, int split, int sms) {
   const int steps = ((K + 63) / 64 + split - 1) / split;
   const long long ctas = static_cast<long long>((N + 127) / 128) * ((T + bn - 1) / bn) * split;
-  const double copy = copies_us(ctas, 16.0 + bn / 8.0, steps, 75.0, weight_mb(T, N, K, bn),
-                                bn == 16 ? 6 : bn == 32 ? 5 : bn == 64 ? 4 : 3, sms);
+  const double copy = copies_us(ctas, split, 16.0 + bn / 8.0, steps, 75.0, weight_mb(T, N, K, bn),
+                                bn == 16 ? 6 : bn == 32 ? 5 : bn == 64 ? 4 : 3,
+                                3.5 + (split == 8 ? 4.0 : 0.0) + (Rs > 0 ? 4.0 : 0.0), sms);
   double us = 2.7 + copy + bn / 128.0 * (split > 1 ? 1.2 : 0.6) + (split > 1 ? 0.4 : 0.0);
   if (split == 8 && bn > 16 && (ctas > 128 || bn == 128)) us += bn == 128 ? 2.5 : 0.85;
   if (Rs > 0)
@@ -84,8 +88,8 @@ double narrow_us(int T, int N, int K, int Rs, int bn, int split, int sms) {
 double cluster_us(int T, int N, int K, int Rs, int bn, int split, int sms) {
   const int steps = ((K + 63) / 64 + split - 1) / split;
   const long long ctas = static_cast<long long>((N + 127) / 128) * ((T + bn - 1) / bn) * split;
-  const double copy = copies_us(ctas, 16.0 + (Rs + 63) / 64 * 8.0 + bn / 8.0, steps, 87.0,
-                                weight_mb(T, N, K, bn), Rs <= 64 && bn == 16 ? 4 : 3, sms);
+  const double copy = copies_us(ctas, split, 16.0 + (Rs + 63) / 64 * 8.0 + bn / 8.0, steps, 87.0,
+                                weight_mb(T, N, K, bn), Rs <= 64 && bn == 16 ? 4 : 3, 3.5 + (split == 8 ? 4.0 : 0.0), sms);
   return 4.4 + copy + (bn == 32 ? 0.9 : 0.0);
 }
 // Pairs: a pair walks whole tiles of 256 tokens x `rows`; a 64-deep K step takes 0.30 us at 256 rows
@@ -118,8 +122,9 @@ Tiles pick_tiles(int T, int N, int K, bool f32, int Rs, int sms) {
       if (Rs > 0 && Rs <= 128 && bn <= 32) offer(cluster_us(T, N, K, Rs, bn, split, sms), {kCluster, bn, 128, split});
     }
   }
-  if (!f32 && T > 128)
-    for (int rows = 256; rows >= 128; rows -= 64) offer(wide_us(T, N, K, Rs, rows, sms), {kWide, 256, rows, 1});
+  if (T > 128)
+    for (int rows = f32 ? 128 : 256; rows >= 128; rows -= 64)
+      offer(wide_us(T, N, K, Rs, rows, sms), {kWide, 256, rows, 1});
   return best;
 }
 
@@ -258,8 +263,11 @@ moe_lora_status moe_lora_linear(moe_lora_handle* h, const moe_lora_linear_args* 
   p.ldy = a->T > 1 ? a->y_stride : a->N;
   p.y_f32 = a->y_f32 != 0;
   if (wide) {
-    p.y_vec = p.ldy % 8 == 0 && aligned16(a->y) && p.ldy <= kMaxStride;
-    if (p.y_vec) ok = ok && tile_map(h, &p.tmap_y, a->y, a->T, a->N, p.ldy, 32);
+    // TMA stores write whole 16-byte pieces, also the one that the last column lies in: only where
+    // rows and the last column end on such pieces is nothing else written
+    const int piece = p.y_f32 ? 4 : 8;
+    p.y_vec = p.ldy % piece == 0 && a->N % piece == 0 && aligned16(a->y) && p.ldy < kMaxStride;
+    if (p.y_vec) ok = ok && tile_map(h, &p.tmap_y, a->y, a->T, a->N, p.ldy, 32, p.y_f32 != 0);
     if (!ok) return MOE_LORA_ERR_INVALID_ARG;
     ML_LAUNCH(h, launch_linear_wide(p, c.rows, h->num_sms, stream), "linear launch");
   } else {

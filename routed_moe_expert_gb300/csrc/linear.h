@@ -24,7 +24,7 @@ struct LinearParams {
   CUtensorMap tmap_a;    // the stacked A [Rs, K]
   CUtensorMap tmap_b;    // the stacked B [N, Rs]
   CUtensorMap tmap_u;    // the shrunk rows [T, pieces * Rs]
-  CUtensorMap tmap_y;    // (wide tiles, y_vec) [T, N] box {64, 32}
+  CUtensorMap tmap_y;    // (wide tiles, y_vec) [T, N], boxes of 32 tokens x 128 bytes
   int T, N, K;
   int Rs;                // stacked columns, a multiple of 64 (0: no adapters)
   int pieces;            // 1, or kFloatPieces bf16 pieces of a float32 u
@@ -57,7 +57,7 @@ cudaError_t launch_linear_narrow(const LinearParams& p, int bn, int split, cudaS
 cudaError_t linear_cluster_setup();
 cudaError_t launch_linear_cluster(const LinearParams& p, int bn, int split, cudaStream_t stream);
 
-// Tiles of 256 tokens x bn (128, 192 or 256) weight rows on CTA pairs, bf16 y.  Maps' boxes: {64, 128}
+// Tiles of 256 tokens x bn (128, 192 or 256; float32 y: 128) weight rows on CTA pairs.  Maps' boxes: {64, 128}
 // of x and u, {64, bn / 2} of w and b, {64, linear_shrink_cols(Rs, bn) / 2} of a.
 cudaError_t linear_wide_setup();
 cudaError_t launch_linear_wide(const LinearParams& p, int bn, int sms, cudaStream_t stream);

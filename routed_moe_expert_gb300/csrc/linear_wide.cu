@@ -1,5 +1,5 @@
-// The projection of linear_narrow.cu for long batches with a bf16 result: tiles of 256 tokens x
-// BN weight rows on CTA pairs.
+// The projection of linear_narrow.cu for long batches: tiles of 256 tokens x BN weight rows on CTA
+// pairs.
 //
 // Here the tokens are the MMA's M operand: a pair (cluster of two CTAs on one TPC) computes
 // 256 tokens x BN columns with cta_group::2 MMAs, each CTA loading its 128 token rows and BN / 2
@@ -21,6 +21,10 @@
 // memory (16-byte pieces, exclusive-or swizzled as the TMA store expects) and one lane stores the
 // box, or, where y's rows do not start on 16-byte boundaries, the warp stores it row by row.
 //
+// A float32 result (F32, BN = 128) is summed in parts: the tensor cores truncate as they accumulate,
+// which adds up over a long K, so after every 1024 of K the epilogue takes the accumulator into
+// registers (a token's 128 columns per thread) while the MMAs go on in the other one.
+//
 // Warp 0: TMA producer; warp 1: MMA issuer (even CTA); warps 2-5: epilogue; warp 6: a tile or two
 // ahead of them, which adapter blocks a tile needs, and the wait for its u (in the producer itself
 // these loads and the flag's atomics cost 2 us a tile, 24 us at T 8192, K 2048, N 4096).  Waits are
@@ -37,14 +41,16 @@ constexpr int kABytes = 128 * 128;
 constexpr int kBoxBytes = 32 * 128;            // a warp's store box: 32 tokens x 64 columns
 constexpr int kYBytes = 4 * 2 * kBoxBytes;     // two per epilogue warp
 constexpr int kTokenGroup = 8;
+constexpr int kPartSteps = 16;                 // (F32) 64-wide K blocks of an accumulator
 constexpr uint64_t kPeerDrainNs = 100000;      // 100 us for an aborted odd CTA's copies to land
 
 __host__ __device__ constexpr int stage_bytes(int bn) { return kABytes + bn / 2 * 128; }
 __host__ __device__ constexpr int stages_of(int bn) { return bn == 256 ? 6 : bn == 192 ? 6 : 8; }
 __host__ __device__ constexpr int smem_bytes(int bn) { return 1024 + stages_of(bn) * stage_bytes(bn) + kYBytes + 256; }
 
-template <int BN>
+template <int BN, bool F32>
 __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_constant__ LinearParams p) {
+  static_assert(!F32 || BN == 128, "a thread's columns fit its registers");
   constexpr int kStages = stages_of(BN);
   constexpr uint32_t STAGE = stage_bytes(BN);
   constexpr uint32_t TMEM_COLS = BN == 128 ? 256u : 512u;
@@ -184,10 +190,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
           uint64_t mask = 0;
           ok = take_mask(nmask++, mask);
           if (mask) fence_proxy_async_global();   // u was written by st.global, read next by TMA
-          for (; ok && mask; mask &= mask - 1) {
-            const int c = (__ffsll(static_cast<long long>(mask)) - 1) * 64;
-            ok = issue(&p.tmap_u, c, t, &p.tmap_b, c, n, STAGE);
-          }
+          for (int piece = 0; piece < (F32 ? kFloatPieces : 1); ++piece)
+            for (uint64_t m = mask; ok && m; m &= m - 1) {
+              const int c = (__ffsll(static_cast<long long>(m)) - 1) * 64;
+              ok = issue(&p.tmap_u, piece * p.Rs + c, t, &p.tmap_b, c, n, STAGE);
+            }
         }
       }
     if (lane == 0 && !ok) {   // let every issued copy land before the CTA exits
@@ -222,21 +229,38 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
       if (lane == 0)
         for (int i = 0; ok && i < n_tiles; ++i) {
           const bool shrink = i < n_shrink;
-          const uint32_t d = tmem_base + static_cast<uint32_t>(acc * BN);
           const uint32_t idesc = idesc_bf16_f32(256, shrink ? sh_cols : BN);
-          ok = mbar_wait(&tempty[acc], aphase ^ 1u, abort_flag, p.status, kWhereLinear);
-          tc_fence_after();
-          for (int kb = 0; ok && kb < nk; ++kb) ok = consume(d, idesc, kb == 0);
+          uint32_t d = 0;
+          auto begin = [&]() -> bool {   // the accumulator, once its last use has been read out
+            if (!mbar_wait(&tempty[acc], aphase ^ 1u, abort_flag, p.status, kWhereLinear)) return false;
+            tc_fence_after();
+            d = tmem_base + static_cast<uint32_t>(acc * BN);
+            return true;
+          };
+          auto finish = [&]() {
+            umma_commit_pair_mc(&tfull[acc], 0x3);
+            if (++acc == 2) {
+              acc = 0;
+              aphase ^= 1u;
+            }
+          };
+          ok = begin();
+          for (int kb = 0; ok && kb < nk; ++kb) {
+            bool first = kb == 0;
+            if (F32 && kb > 0 && kb % kPartSteps == 0) {
+              finish();
+              ok = begin();
+              first = true;
+            }
+            ok = ok && consume(d, idesc, first);
+          }
           if (ok && lora && !shrink) {
             uint64_t mask = 0;
             ok = take_mask(nmask++, mask);
-            for (; ok && mask; mask &= mask - 1) ok = consume(d, idesc, false);
+            const int steps = __popcll(mask) * (F32 ? kFloatPieces : 1);
+            for (int j = 0; ok && j < steps; ++j) ok = consume(d, idesc, false);
           }
-          if (ok) umma_commit_pair_mc(&tfull[acc], 0x3);
-          if (++acc == 2) {
-            acc = 0;
-            aphase ^= 1u;
-          }
+          if (ok) finish();
         }
       if (!ok && lane == 0) {   // let what was issued finish before TMEM is released
         umma_commit_pair(drain);
@@ -302,11 +326,116 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
     __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y);
     int acc = 0, nbox = 0;
     uint32_t aphase = 0;
+    auto release = [&]() {   // the accumulator has been read out
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(cluster_addr(&tempty[acc], 0));
+      if (++acc == 2) {
+        acc = 0;
+        aphase ^= 1u;
+      }
+    };
+    auto epilogue_f32 = [&](int tile, int tt, int nt, int t_warp) -> bool {
+      float f[128];
+#pragma unroll
+      for (int j = 0; j < 128; ++j) f[j] = 0.0f;
+      for (int part = 0; part < (nk + kPartSteps - 1) / kPartSteps; ++part) {
+        if (!mbar_wait_sleep(&tfull[acc], aphase, abort_flag, p.status, kWhereLinear)) return false;
+        tc_fence_after();
+        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * BN);
+#pragma unroll
+        for (int c = 0; c < 128; c += 32) {   // (a shrink tile of 64 columns: the others are not used)
+          uint32_t v[32];
+          __syncwarp();
+          tmem_ld_x32(taddr + c, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) f[c + j] += __uint_as_float(v[j]);
+        }
+        release();
+      }
+      const int t = t_warp + lane;
+      if (tile < nshrink) {   // u of a token's own columns in bf16 pieces, 0 in the others
+        const int sl = t < p.T ? p.slot_idx[t] : -1;
+        const bool has = sl >= 0 && sl < p.slots.S;
+        const int lo = has ? p.slots.lo[sl] : 0, hi = has ? p.slots.hi[sl] : 0;
+        const float sc = has ? p.slots.scal[sl] : 0.0f;
+        __nv_bfloat16* u = p.u + static_cast<long long>(t) * kFloatPieces * p.Rs;
+#pragma unroll
+        for (int c = 0; c < 128; c += 8) {
+          const int col = nt * sh_cols + c;
+          if (c >= sh_cols || col >= p.Rs || t >= p.T) continue;
+          float g[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) g[j] = (col + j >= lo && col + j < hi) ? sc * f[c + j] : 0.0f;
+#pragma unroll
+          for (int piece = 0; piece < kFloatPieces; ++piece) {
+            const uint4 v = pack8(g);
+            *reinterpret_cast<uint4*>(u + piece * p.Rs + col) = v;
+            float back[8];
+            unpack8(v, back);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) g[j] -= back[j];
+          }
+        }
+        fence_proxy_async_global();   // read next by other CTAs' TMA copies
+        __syncwarp();                 // the release below covers every lane's writes before this
+        if (lane == 0) red_release_add(reinterpret_cast<int*>(p.flags + tt), 1);
+        return true;
+      }
+      float* y32 = static_cast<float*>(p.y);
+#pragma unroll
+      for (int c = 0; c < 128; c += 32) {
+        const int n = nt * BN + c;
+        if (n >= p.N || t_warp >= p.T) continue;   // warp-uniform
+        if (p.bias != nullptr) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (n + j < p.N) f[c + j] += __ldg(p.bias + n + j);
+        }
+        uint8_t* box = box0 + (nbox & 1) * kBoxBytes;
+        ++nbox;
+        if (lane == 0) bulk_wait_read_1();   // the store that last read this box is done
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          *reinterpret_cast<float4*>(box + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+              make_float4(f[c + 4 * j], f[c + 4 * j + 1], f[c + 4 * j + 2], f[c + 4 * j + 3]);
+        if (p.y_vec) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&p.tmap_y, box, n, t_warp);
+            bulk_commit();
+          }
+        } else {   // a column per lane, a row at a time
+          __syncwarp();
+          const int rows = min(32, p.T - t_warp);
+          const bool in = n + lane < p.N;
+          float* row = y32 + static_cast<long long>(t_warp) * p.ldy + n + lane;
+#pragma unroll
+          for (int r0 = 0; r0 < 32; r0 += 8) {   // eight rows' values at a time
+            float one[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+              one[r] = *reinterpret_cast<const float*>(box + (r0 + r) * 128 + (((lane >> 2) ^ r) << 4) + (lane & 3) * 4);
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+              if (in && r0 + r < rows) row[(r0 + r) * p.ldy] = one[r];
+          }
+        }
+      }
+      return true;
+    };
     for (int i = 0; i < n_tiles; ++i) {
       const int tile = tile_at(i);
       int tt, nt;
       decode(tile, tt, nt);
       const int t_warp = tt * 256 + static_cast<int>(crank) * 128 + quarter * 32;
+      if constexpr (F32) {
+        if (!epilogue_f32(tile, tt, nt, t_warp)) break;
+        continue;
+      }
       if (!mbar_wait_sleep(&tfull[acc], aphase, abort_flag, p.status, kWhereLinear)) break;
       tc_fence_after();
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * BN);
@@ -375,21 +504,24 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
         } else {   // two columns per lane, a row at a time
           __syncwarp();
           const int rows = min(32, p.T - t_warp);
-          for (int r = 0; r < rows; ++r) {
-            const uint32_t two = *reinterpret_cast<const uint32_t*>(box + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
-            __nv_bfloat16* row = y + static_cast<long long>(t_warp + r) * p.ldy + n + 2 * lane;
-            if (n + 2 * lane < p.N) row[0] = __ushort_as_bfloat16(static_cast<unsigned short>(two & 0xffffu));
-            if (n + 2 * lane + 1 < p.N) row[1] = __ushort_as_bfloat16(static_cast<unsigned short>(two >> 16));
+          const bool in0 = n + 2 * lane < p.N, in1 = n + 2 * lane + 1 < p.N;
+          __nv_bfloat16* row = y + static_cast<long long>(t_warp) * p.ldy + n + 2 * lane;
+#pragma unroll
+          for (int r0 = 0; r0 < 32; r0 += 8) {   // eight rows' values at a time
+            uint32_t two[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+              two[r] = *reinterpret_cast<const uint32_t*>(box + (r0 + r) * 128 + (((lane >> 2) ^ r) << 4) + (lane & 3) * 4);
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+              __nv_bfloat16* at = row + (r0 + r) * p.ldy;
+              if (in0 && r0 + r < rows) at[0] = __ushort_as_bfloat16(static_cast<unsigned short>(two[r] & 0xffffu));
+              if (in1 && r0 + r < rows) at[1] = __ushort_as_bfloat16(static_cast<unsigned short>(two[r] >> 16));
+            }
           }
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(cluster_addr(&tempty[acc], 0));
-      if (++acc == 2) {
-        acc = 0;
-        aphase ^= 1u;
-      }
+      release();
     }
     bulk_wait_all();   // the stores have read their boxes and landed
   }
@@ -407,24 +539,35 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
 }  // namespace
 
 cudaError_t linear_wide_setup() {
-  cudaError_t err = cudaFuncSetAttribute(linear_wide_kernel<256>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         smem_bytes(256));
+  cudaError_t err;
+#define ML_SETUP(BN, F32)                                                                                         \
+  err = cudaFuncSetAttribute(linear_wide_kernel<BN, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(BN)); \
   if (err != cudaSuccess) return err;
-  err = cudaFuncSetAttribute(linear_wide_kernel<192>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(192));
-  if (err != cudaSuccess) return err;
-  return cudaFuncSetAttribute(linear_wide_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(128));
+  ML_SETUP(256, false)
+  ML_SETUP(192, false)
+  ML_SETUP(128, false)
+  ML_SETUP(128, true)
+#undef ML_SETUP
+  return cudaSuccess;
 }
 
 cudaError_t launch_linear_wide(const LinearParams& p, int bn, int sms, cudaStream_t stream) {
   const int cols = linear_shrink_cols(p.Rs, bn);
   const long long tiles =
       static_cast<long long>((p.N + bn - 1) / bn + (cols ? (p.Rs + cols - 1) / cols : 0)) * p.token_tiles;
-  if (tiles > 0x3fffffffLL || (bn != 128 && bn != 192 && bn != 256)) return cudaErrorInvalidValue;
+  if (tiles > 0x3fffffffLL || (p.y_f32 && bn != 128)) return cudaErrorInvalidValue;
   const int pairs = static_cast<int>(tiles < sms / 2 ? tiles : sms / 2);
   const dim3 grid(2 * pairs), block(kThreads);
-  if (bn == 256) return launch_kc(linear_wide_kernel<256>, grid, block, smem_bytes(256), stream, true, 2, p);
-  if (bn == 192) return launch_kc(linear_wide_kernel<192>, grid, block, smem_bytes(192), stream, true, 2, p);
-  return launch_kc(linear_wide_kernel<128>, grid, block, smem_bytes(128), stream, true, 2, p);
+#define ML_LINEAR(BN, F32) \
+  return launch_kc(linear_wide_kernel<BN, F32>, grid, block, smem_bytes(BN), stream, true, 2, p)
+  if (p.y_f32) ML_LINEAR(128, true);
+  switch (bn) {
+    case 256: ML_LINEAR(256, false);
+    case 192: ML_LINEAR(192, false);
+    case 128: ML_LINEAR(128, false);
+    default: return cudaErrorInvalidValue;
+  }
+#undef ML_LINEAR
 }
 
 }  // namespace mlk

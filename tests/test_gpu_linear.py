@@ -87,8 +87,22 @@ def test_widths(handle, T, N, K):
 def test_long_batches(handle, T, N, K, slots):
     """Enough tokens for the widest tiles: ragged in every direction, rows of y on and off 16-byte
     boundaries, adapters of several 64-column blocks."""
-    c = _case(T, N, K, (16, 40, 64, 5) if slots else (), seed=T, bias=N % 2 == 0, slots=slots or "none")
-    _check(_run(handle, c), c)
+    for f32 in (False, True):
+        c = _case(T, N, K, (16, 40, 64, 5) if slots else (), seed=T, bias=N % 2 == 0, slots=slots or "none")
+        _check(_run(handle, c, f32), c, f32)
+
+
+@pytest.mark.parametrize("T,N,K", [(3, 130, 7168), (200, 384, 7168), (1500, 384, 7168), (900, 200, 4104)])
+def test_long_sums_in_float32(handle, T, N, K):
+    """The tensor cores truncate as they accumulate; in parts of 1024 the error of a float32 result
+    over a long K stays that of a float32 sum of such parts: at most 64 steps of 16 products each
+    truncated to 24 bits (2^-23 of the running sum, which stays below the part's largest sum of
+    |terms| / sqrt of their count times 4 for these zero-mean terms), half of it on average: 32 * 2^-23
+    relative to the result's size, here held in the 2-norm."""
+    c = _case(T, N, K, (), seed=T)
+    got = ref.f64(_run(handle, c, True))
+    y = ref.f64(c["x"]) @ ref.f64(c["w"]).T
+    assert np.linalg.norm(got - y) <= 32 * 2.0 ** -23 * np.linalg.norm(y)
 
 
 @pytest.mark.parametrize("ranks", [(1,), (128,), (0, 8), (64, 64, 64), (8, 16, 32, 64), (16,) * 40, (64,) * 64],
@@ -122,7 +136,7 @@ def test_strided_rows_and_nothing_else_written(handle, T, f32):
     xw[:T, 16:16 + K] = c["x"].cuda()
     ww = torch.full((N + 2, K + 8), float("nan"), dtype=torch.bfloat16, device="cuda")
     ww[1:N + 1, :K] = c["w"].cuda()
-    for lead, width in ((3, N + 10), (4, 152)):
+    for lead, width in ((3, N + 10), (4, 152), (8, 160)):
         buf = torch.full((T + 2, width), 77.0, dtype=torch.float32 if f32 else torch.bfloat16, device="cuda")
         got = _run(handle, c, f32, out=buf[1:T + 1, lead:lead + N], x=xw[:T, 16:16 + K], w=ww[1:N + 1, :K])
         _check(got, c, f32)
