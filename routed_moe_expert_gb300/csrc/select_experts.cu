@@ -24,6 +24,7 @@
 #include "kernels.h"
 
 #include <cfloat>
+#include <climits>
 
 namespace mlk {
 
@@ -51,12 +52,6 @@ MLDEV float warp_max(float v) {
   float m;
   asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
   return m;
-}
-
-// A logit as it counts: +inf is the largest finite value, a ruled-out expert (-inf or NaN) is NaN,
-// which maxima pass over and arithmetic keeps.
-MLDEV float usable(float z) {
-  return z == -INFINITY ? __int_as_float(0x7fffffff) : z == INFINITY ? FLT_MAX : z;
 }
 
 template <typename TL, int V>
@@ -89,16 +84,29 @@ MLDEV unsigned long long warp_sum_u58(unsigned long long v) {
   return a + (static_cast<unsigned long long>(b) << 26) + (static_cast<unsigned long long>(c) << 52);
 }
 
-// Scores of a token's logits: what its softmax divides by, or nothing (sigmoid).
-struct Scoring {
-  bool sigmoid;
-  float zmax, total;   // softmax: the largest logit and the sum
+// 1 / d, correctly rounded, for 1 <= d < 2^100: a reciprocal within an ulp and one residual
+// (P. Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor", IBM J.
+// Res. Dev. 34, 1990).
+MLDEV float reciprocal(float d) {
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(d));
+  return __fmaf_rn(__fmaf_rn(-d, r, 1.0f), r, r);
+}
+
+// What a token's softmax subtracts and divides by.
+struct Softmax {
+  float zmax, total, inverse;   // inverse: the correctly rounded reciprocal of total
   MLDEV float numerator(float z) const { return expf(__fsub_rn(z, zmax)); }
-  MLDEV float operator()(float z) const {
-    if (sigmoid) return __frcp_rn(__fadd_rn(1.0f, expf(-z)));
-    return __fdiv_rn(numerator(z), total);
+  // e / total, correctly rounded: with the correctly rounded reciprocal one residual makes
+  // q = e / total exact (Markstein) while it does not underflow
+  MLDEV float quotient(float e) const {
+    const float q = __fmul_rn(e, inverse);
+    return __fmaf_rn(__fmaf_rn(-q, total, e), inverse, q);
   }
+  MLDEV float any_quotient(float e) const { return e < 0x1p-100f ? __fdiv_rn(e, total) : quotient(e); }
 };
+
+MLDEV float sigmoid_score(float z) { return __frcp_rn(__fadd_rn(1.0f, expf(-z))); }
 
 // Keys (and their ids) on or above a bound, one per lane, for the ordered choice.
 constexpr int kCandidates = 32;
@@ -108,7 +116,7 @@ constexpr int kCandidates = 32;
 template <typename TL, int NQ, int V, int GROUPS>
 __global__ void __launch_bounds__(256) select_experts_kernel(const SelectParams p) {
   constexpr int NV = NQ * V;
-  __shared__ float2 cand_s[8][kCandidates];
+  __shared__ __align__(16) float2 cand_s[8][kCandidates];
   const int lane = threadIdx.x & 31;
   const int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   pdl_wait();
@@ -118,56 +126,75 @@ __global__ void __launch_bounds__(256) select_experts_kernel(const SelectParams 
   const TL* row = static_cast<const TL*>(p.logits) + static_cast<long long>(t) * p.stride;
   auto id_of = [&](int n) -> int { return ((n / V) * 32 + lane) * V + n % V; };   // lane's n-th value
 
-  float key[NV];   // logits, then scores, then keys; NaN, in the end -inf: ruled out
+  float z[NV];   // logits; -inf: ruled out
 #pragma unroll
   for (int i = 0; i < NQ; ++i) {
-    float z[V];
+    float c[V];
     const int e = (i * 32 + lane) * V;   // V == 4: E is a multiple of 4
     if (e < p.E) {
-      load_logits<TL, V>(row, e, z);
+      load_logits<TL, V>(row, e, c);
     } else {
 #pragma unroll
-      for (int v = 0; v < V; ++v) z[v] = -INFINITY;
+      for (int v = 0; v < V; ++v) c[v] = -INFINITY;
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v) key[i * V + v] = usable(z[v]);
+    for (int v = 0; v < V; ++v) z[i * V + v] = fmaxf(c[v], -INFINITY);
   }
 
-  Scoring score = {p.sigmoid != 0, 0.0f, 1.0f};
-  if (!score.sigmoid) {
-    float m = key[0];
+  // Keys; NaN, which maxima and comparisons pass over, or -inf: ruled out.  Without a bias a softmax's
+  // are its numerators: dividing by the sum keeps their order (rounding can make neighbours equal).
+  float key[NV];
+  Softmax soft = {0.0f, 1.0f, 1.0f};
+  const bool numerators = !p.sigmoid && p.bias == nullptr;
+  if (!p.sigmoid) {
+    float m = z[0];
 #pragma unroll
-    for (int n = 1; n < NV; ++n) m = fmaxf(m, key[n]);
-    score.zmax = warp_max(m);   // (NaN when all are ruled out, and so is every score)
+    for (int n = 1; n < NV; ++n) m = fmaxf(m, z[n]);
+    soft.zmax = warp_max(m);
+    if (soft.zmax == INFINITY) {   // +inf counts as the largest finite value
+      soft.zmax = FLT_MAX;
+#pragma unroll
+      for (int n = 0; n < NV; ++n) z[n] = fminf(z[n], FLT_MAX);
+    }
+    if (soft.zmax == -INFINITY) soft.zmax = 0.0f;   // all ruled out
     unsigned long long sum = 0;
-    uint32_t least = 0xffffffffu;   // bits of the smallest nonzero term, less 1
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
-      key[n] = score.numerator(key[n]);
-      least = min(least, __float_as_uint(key[n]) - 1u);
-      sum += __float2ull_rz(fmaxf(key[n], 0.0f) * 0x1p52f);
+      const float e = soft.numerator(z[n]);
+      sum += __float2ull_rz(e * 0x1p52f);
+      key[n] = __fmaf_rn(z[n], 0.0f, e);   // NaN where z is -inf
     }
-    score.total = __ull2float_rn(warp_sum_u58(sum)) * 0x1p-52f;   // at least 1, or all are ruled out
-    // e / total, correctly rounded: with r the correctly rounded reciprocal, one residual makes
-    // q = e r exact (P. Markstein, "Computation of elementary functions on the IBM RISC System/6000
-    // processor", IBM J. Res. Dev. 34, 1990) while the residual does not underflow; with smaller
-    // nonzero terms all take the division.
-    if (least >= __float_as_uint(0x1p-100f)) {
-      const float r = __frcp_rn(score.total);
+    // at least 1, or all are ruled out
+    soft.total = fmaxf(__ull2float_rn(warp_sum_u58(sum)) * 0x1p-52f, 1.0f);
+    soft.inverse = reciprocal(soft.total);
+    if (!numerators) {
+      uint32_t least = 0xffffffffu;   // bits of the smallest nonzero numerator, less 1
 #pragma unroll
-      for (int n = 0; n < NV; ++n) {
-        const float q = __fmul_rn(key[n], r);
-        key[n] = __fmaf_rn(__fmaf_rn(-q, score.total, key[n]), r, q);
+      for (int n = 0; n < NV; ++n) least = min(least, __float_as_uint(key[n]) - 1u);
+      if (least >= __float_as_uint(0x1p-100f)) {
+#pragma unroll
+        for (int n = 0; n < NV; ++n) key[n] = soft.quotient(key[n]);
+      } else {
+#pragma unroll
+        for (int n = 0; n < NV; ++n) key[n] = __fdiv_rn(key[n], soft.total);
       }
-    } else {
-#pragma unroll
-      for (int n = 0; n < NV; ++n) key[n] = __fdiv_rn(key[n], score.total);
     }
   } else {
+    // 1 + exp(-z) stays below 2^100 for z >= -60; with lower (finite) ones all take the division
+    uint32_t low = 0xffffffffu;
 #pragma unroll
-    for (int n = 0; n < NV; ++n) key[n] = score(key[n]);
+    for (int n = 0; n < NV; ++n) {
+      low = min(low, __float_as_uint(z[n]) - (__float_as_uint(-60.0f) + 1u));
+      const float s = reciprocal(__fadd_rn(1.0f, expf(-fmaxf(z[n], -60.0f))));
+      key[n] = z[n] > -INFINITY ? s : __int_as_float(0x7fffffff);
+    }
+    if (low < __float_as_uint(-INFINITY) - (__float_as_uint(-60.0f) + 1u)) {
+#pragma unroll
+      for (int n = 0; n < NV; ++n)
+        if (z[n] > -INFINITY) key[n] = sigmoid_score(z[n]);
+    }
   }
-  if (p.bias != nullptr) {
+  if (p.bias != nullptr) {   // (a NaN bias rules out, too)
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
       const int e = (i * 32 + lane) * V;
@@ -188,8 +215,8 @@ __global__ void __launch_bounds__(256) select_experts_kernel(const SelectParams 
       }
     }
   }
-#pragma unroll
-  for (int n = 0; n < NV; ++n) key[n] = fmaxf(key[n], -INFINITY);   // NaN (a NaN bias too): ruled out
+  // the score that a group's best key stands for
+  auto scored = [&](float f) { return !numerators ? f : f >= 0.0f ? soft.any_quotient(f) : -INFINITY; };
 
   if constexpr (GROUPS != 0) {
     float mine = -INFINITY;   // lane g: group g's score
@@ -198,12 +225,18 @@ __global__ void __launch_bounds__(256) select_experts_kernel(const SelectParams 
       float b1[NQ], b2[NQ];
 #pragma unroll
       for (int i = 0; i < NQ; ++i) {
-        b1[i] = key[i * V];
+        b1[i] = fmaxf(key[i * V], -INFINITY);
         b2[i] = -INFINITY;
+        if (p.top2) {
 #pragma unroll
-        for (int v = 1; v < V; ++v) {
-          b2[i] = fmaxf(b2[i], fminf(b1[i], key[i * V + v]));
-          b1[i] = fmaxf(b1[i], key[i * V + v]);
+          for (int v = 1; v < V; ++v) {
+            const float f = fmaxf(key[i * V + v], -INFINITY);
+            b2[i] = fmaxf(b2[i], fminf(b1[i], f));
+            b1[i] = fmaxf(b1[i], f);
+          }
+        } else {
+#pragma unroll
+          for (int v = 1; v < V; ++v) b1[i] = fmaxf(b1[i], key[i * V + v]);
         }
       }
       const int width = p.group_size / V;   // chunks (lanes) of a group: 2^n <= 32
@@ -221,7 +254,7 @@ __global__ void __launch_bounds__(256) select_experts_kernel(const SelectParams 
       const int first = lane * width;   // group g's first chunk
 #pragma unroll
       for (int i = 0; i < NQ; ++i) {
-        const float own = p.top2 ? __fadd_rn(b1[i], b2[i]) : b1[i];
+        const float own = p.top2 ? __fadd_rn(scored(b1[i]), scored(b2[i])) : scored(b1[i]);
         const float of = __shfl_sync(kAll, own, first & 31);
         if ((first >> 5) == i) mine = of;
       }
@@ -230,7 +263,7 @@ __global__ void __launch_bounds__(256) select_experts_kernel(const SelectParams 
       float* keys = keys_s + (threadIdx.x >> 5) * p.E;
 #pragma unroll
       for (int n = 0; n < NV; ++n)
-        if (id_of(n) < p.E) keys[id_of(n)] = key[n];
+        if (id_of(n) < p.E) keys[id_of(n)] = fmaxf(key[n], -INFINITY);
       __syncwarp();
       const int width = p.group_lanes;   // lanes of a group: 2^n, width * n_group <= 32
       const int g = lane / width;
@@ -246,7 +279,7 @@ __global__ void __launch_bounds__(256) select_experts_kernel(const SelectParams 
         b2 = fmaxf(fmaxf(b2, o2), fminf(b1, o1));
         b1 = fmaxf(b1, o1);
       }
-      mine = __shfl_sync(kAll, p.top2 ? __fadd_rn(b1, b2) : b1, (lane * width) & 31);
+      mine = __shfl_sync(kAll, p.top2 ? __fadd_rn(scored(b1), scored(b2)) : scored(b1), (lane * width) & 31);
     }
     if (mine != mine) mine = -INFINITY;   // +inf (a bias) and a ruled-out second
     unsigned stay = 0;   // ties, also of groups without an expert left: the lower group
@@ -280,6 +313,9 @@ __global__ void __launch_bounds__(256) select_experts_kernel(const SelectParams 
       if (left == bound) left = -INFINITY;
     }
   }
+  // numerators a little below the bound may give the same quotient (within 2^-23 while it is no
+  // subnormal number)
+  if (numerators) bound = bound >= 0x1p-100f ? bound * 0x1.fffffp-1f : -INFINITY;
   // candidates: keys on or above the bound (all that is left when there is no bound), each lane's
   // after those of the lanes below it
   int count = kCandidates + 1;
@@ -303,19 +339,38 @@ __global__ void __launch_bounds__(256) select_experts_kernel(const SelectParams 
     }
   }
   int my_id = 0, chosen = 0;   // lane j keeps pick j
+  float w = 0.0f;              // and its weight
   if (count <= kCandidates) {
+    // count >= top_k.  A lane ranks its candidate among all: larger keys first, then lower ids; as
+    // 64-bit numbers, the key's bits above the id's complement.
     __syncwarp();
-    const float2 c = lane < count ? cand[lane] : make_float2(-INFINITY, 0.0f);
-    float left = c.x;
+    const float2 c = lane < count ? cand[lane] : make_float2(0.0f, 0.0f);
+    const float s = numerators && lane < count ? soft.any_quotient(c.x) : c.x;
     const int id = __float_as_int(c.y);
-    for (int j = 0; j < p.k; ++j) {   // count >= top_k: the lanes taken out give that many
-      const float m = warp_max(left);
-      const int pick = __reduce_min_sync(kAll, left == m ? id : 0x7fffffff);
-      if (lane == j) my_id = pick;
-      if (left == m && id == pick) left = -INFINITY;
+    const int bits = __float_as_int(s);
+    const uint32_t up = static_cast<uint32_t>(bits ^ ((bits >> 31) | INT_MIN));   // in the order of s
+    const unsigned long long mine =
+        lane < count ? static_cast<unsigned long long>(up) << 32 | static_cast<uint32_t>(~id) : 0ull;
+    unsigned long long* order = reinterpret_cast<unsigned long long*>(cand);
+    __syncwarp();
+    order[lane] = mine;
+    __syncwarp();
+    int rank = 0;
+    for (int j = 0; j < count; j += 2) {
+      const ulonglong2 other = *reinterpret_cast<const ulonglong2*>(order + j);
+      rank += other.x > mine;
+      rank += other.y > mine;
     }
+    __syncwarp();
+    if (lane < count) cand[rank] = make_float2(s, c.y);
+    __syncwarp();
+    const float2 pick = cand[lane];
+    my_id = __float_as_int(pick.y);
+    w = pick.x;
     chosen = p.k;
   } else {
+#pragma unroll
+    for (int n = 0; n < NV; ++n) key[n] = fmaxf(scored(key[n]), -INFINITY);
     // many equal keys, or fewer lanes with an expert left than top_k: pick by pick
     int best_n = 0;
     auto look = [&]() {
@@ -335,7 +390,10 @@ __global__ void __launch_bounds__(256) select_experts_kernel(const SelectParams 
       if (m == -INFINITY) break;
       const int mine = id_of(0) + (best_n / V) * 32 * V + best_n % V;
       const int pick = __reduce_min_sync(kAll, best == m ? mine : 0x7fffffff);
-      if (lane == chosen) my_id = pick;
+      if (lane == chosen) {
+        my_id = pick;
+        w = m;
+      }
       if (best == m && mine == pick) {
 #pragma unroll
         for (int n = 0; n < NV; ++n)
@@ -377,12 +435,11 @@ __global__ void __launch_bounds__(256) select_experts_kernel(const SelectParams 
     }
   }
 
-  // weights: lane j's score again, from its logit
-  float w = 0.0f;
-  if (lane < chosen) {
-    float z[1];
-    load_logits<TL, 1>(row, my_id, z);
-    w = score(usable(z[0]));
+  if (lane >= chosen) w = 0.0f;
+  if (p.bias != nullptr && lane < chosen) {   // the score without the bias, again from the logit
+    float c[1];
+    load_logits<TL, 1>(row, my_id, c);
+    w = p.sigmoid ? sigmoid_score(c[0]) : soft.any_quotient(soft.numerator(fminf(c[0], FLT_MAX)));
   }
   if (p.renormalize) {
     float sum = w;

@@ -146,6 +146,37 @@ def test_softmax_scores_are_the_correctly_rounded_quotients(handle, E, spread):
     assert torch.equal(o["topk_weights"], p.gather(1, o["topk_ids"].long()))
 
 
+@pytest.mark.parametrize("spread", [1.0, 8.0, 60.0])
+def test_sigmoid_scores_are_the_correctly_rounded_reciprocals(handle, spread):
+    """The kernel's reciprocal against IEEE division, bit for bit; the largest spread has scores that
+    are subnormal or 0."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    z = torch.randn((20000, 32), generator=g, device="cuda") * spread
+    s = 1.0 / (1.0 + torch.exp(-z))
+    o = pkg.moe_lora_select_experts(handle, z, 32, scoring=pkg.SCORE_SIGMOID, renormalize=False)
+    assert torch.equal(o["topk_weights"], s.gather(1, o["topk_ids"].long()))
+    assert torch.equal(o["topk_ids"].long(), torch.sort(s, dim=1, descending=True, stable=True).indices)
+
+
+@pytest.mark.parametrize("scale", [1e-38, 1e-3, 1.0, 40.0])
+@pytest.mark.parametrize("n_group,topk_group", [(1, 1), (8, 3)])
+def test_softmax_ties_of_the_quotients_go_to_the_lower_id(handle, scale, n_group, topk_group):
+    """Neighbouring numerators can have one quotient; the choice is by the quotient, then by the id."""
+    g = torch.Generator(device="cuda").manual_seed(17)
+    z = torch.randn((3000, 256), generator=g, device="cuda") * scale * 2.0 ** torch.randint(
+        -20, 1, (3000, 1), generator=g, device="cuda")
+    e = torch.exp(z - z.amax(1, keepdim=True))
+    s = e / e.double().sum(1, keepdim=True).float()
+    if n_group > 1:
+        best = torch.sort(s.view(3000, n_group, -1).amax(2), dim=1, descending=True, stable=True).indices
+        keep = torch.zeros((3000, n_group), dtype=torch.bool, device="cuda").scatter(1, best[:, :topk_group], True)
+        s = torch.where(keep.repeat_interleave(256 // n_group, 1), s, -1.0)
+    o = pkg.moe_lora_select_experts(handle, z, 8, n_group=n_group, topk_group=topk_group, renormalize=False)
+    ids = torch.sort(s, dim=1, descending=True, stable=True).indices[:, :8]
+    assert torch.equal(o["topk_ids"].long(), ids)
+    assert torch.equal(o["topk_weights"], s.gather(1, ids))
+
+
 def test_strided_and_unaligned_logits(handle):
     wide = torch.full((30, 300), float("nan"), dtype=torch.float32, device="cuda")
     for lead, E, dtype in ((3, 256, torch.float32), (4, 256, torch.float32), (1, 129, torch.bfloat16), (2, 128, torch.bfloat16)):
