@@ -9,8 +9,7 @@
 //
 // Every value that decides a choice is one float32 operation sequence that no order of
 // threads changes: exponentials and quotients are IEEE float32 results, and the softmax sum is
-// taken in fixed point with steps of 2^-52 (the terms lie in [0, 1], so 1024 of them fit 64
-// bits), exact for every term of 2^-28 and more.
+// taken in fixed point with steps of 2^-43, exact for every term of 2^-20 and more.
 //
 // A lane holds NQ chunks of V consecutive experts, so loads are one vector per chunk and, where
 // groups are a power of two of chunks, a group's best is a few shuffles among neighbouring
@@ -75,14 +74,37 @@ MLDEV void load_logits(const TL* row, int e, float (&z)[V]) {
   }
 }
 
-// The sum over the warp of values below 2^58, through three 32-bit reductions of 26 bits.
-MLDEV unsigned long long warp_sum_u58(unsigned long long v) {
-  constexpr unsigned kMask = (1u << 26) - 1;
-  const unsigned a = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(v) & kMask);
-  const unsigned b = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(v >> 26) & kMask);
-  const unsigned c = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(v >> 52));
-  return a + (static_cast<unsigned long long>(b) << 26) + (static_cast<unsigned long long>(c) << 52);
+// (x0 + y, x1 + y) in one instruction, each rounded as an addition is.
+MLDEV float2 add_pair(float x0, float x1, float y) {
+  unsigned long long r;
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %3};\n\tadd.rn.f32x2 %0, a, b;\n\t}"
+      : "=l"(r)
+      : "f"(x0), "f"(x1), "f"(y));
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(r));
+  return f;
 }
+
+// A sum of values in [0, 1] in fixed point, with steps of 2^-43 in two parts: adding 4 rounds a value
+// to steps of 2^-21, whose number is then the low bits of the result; adding 1.5 x 2^-20 does it to
+// what that left out, |rest| <= 2^-22.  (A conversion to 64-bit integers would be exact, but it runs at
+// the rate of double precision, a quarter of this kernel's time.)
+struct FixedSum {
+  uint32_t high = 0, low = 0;   // low: a signed number
+  MLDEV void add(float e0, float e1) {
+    const float2 h = add_pair(e0, e1, 4.0f);
+    const float2 r = add_pair(h.x, h.y, -4.0f);
+    const float2 l = add_pair(__fsub_rn(e0, r.x), __fsub_rn(e1, r.y), 0x1.8p-20f);
+    high += __float_as_uint(h.x) + __float_as_uint(h.y) - 2 * __float_as_uint(4.0f);
+    low += __float_as_uint(l.x) + __float_as_uint(l.y) - 2 * __float_as_uint(0x1.8p-20f);
+  }
+  // over the warp, rounded once; up to 1024 values, the largest of them 1 (or none above 0)
+  MLDEV float warp_total() const {
+    const unsigned long long h = __reduce_add_sync(0xffffffffu, high);
+    const long long l = __reduce_add_sync(0xffffffffu, static_cast<int>(low));
+    return __ull2float_rn((h << 22) + l) * 0x1p-43f;
+  }
+};
 
 // 1 / d, correctly rounded, for 1 <= d < 2^100: a reciprocal within an ulp and one residual
 // (P. Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor", IBM J.
@@ -157,15 +179,15 @@ __global__ void __launch_bounds__(256) select_experts_kernel(const SelectParams 
       for (int n = 0; n < NV; ++n) z[n] = fminf(z[n], FLT_MAX);
     }
     if (soft.zmax == -INFINITY) soft.zmax = 0.0f;   // all ruled out
-    unsigned long long sum = 0;
+    FixedSum sum;
 #pragma unroll
-    for (int n = 0; n < NV; ++n) {
-      const float e = soft.numerator(z[n]);
-      sum += __float2ull_rz(e * 0x1p52f);
-      key[n] = __fmaf_rn(z[n], 0.0f, e);   // NaN where z is -inf
+    for (int n = 0; n < NV; n += 2) {
+      const float e0 = soft.numerator(z[n]), e1 = soft.numerator(z[n + 1]);
+      sum.add(e0, e1);
+      key[n] = __fmaf_rn(z[n], 0.0f, e0);   // NaN where z is -inf
+      key[n + 1] = __fmaf_rn(z[n + 1], 0.0f, e1);
     }
-    // at least 1, or all are ruled out
-    soft.total = fmaxf(__ull2float_rn(warp_sum_u58(sum)) * 0x1p-52f, 1.0f);
+    soft.total = fmaxf(sum.warp_total(), 1.0f);   // at least 1, or all are ruled out
     soft.inverse = reciprocal(soft.total);
     if (!numerators) {
       uint32_t least = 0xffffffffu;   // bits of the smallest nonzero numerator, less 1
@@ -259,18 +281,26 @@ __global__ void __launch_bounds__(256) select_experts_kernel(const SelectParams 
         if ((first >> 5) == i) mine = of;
       }
     } else {
-      extern __shared__ float keys_s[];
+      extern __shared__ __align__(16) float keys_s[];
       float* keys = keys_s + (threadIdx.x >> 5) * p.E;
 #pragma unroll
-      for (int n = 0; n < NV; ++n)
-        if (id_of(n) < p.E) keys[id_of(n)] = fmaxf(key[n], -INFINITY);
+      for (int i = 0; i < NQ; ++i) {
+        const int e = (i * 32 + lane) * V;
+        if (e < p.E) {
+          if constexpr (V == 4)
+            *reinterpret_cast<float4*>(keys + e) =
+                make_float4(key[i * V], key[i * V + 1], key[i * V + 2], key[i * V + 3]);
+          else
+            keys[e] = key[i];
+        }
+      }
       __syncwarp();
       const int width = p.group_lanes;   // lanes of a group: 2^n, width * n_group <= 32
       const int g = lane / width;
       float b1 = -INFINITY, b2 = -INFINITY;
       if (g < p.n_group)
         for (int e = lane & (width - 1); e < p.group_size; e += width) {
-          const float f = keys[g * p.group_size + e];
+          const float f = fmaxf(keys[g * p.group_size + e], -INFINITY);
           b2 = fmaxf(b2, fminf(b1, f));
           b1 = fmaxf(b1, f);
         }
@@ -292,10 +322,15 @@ __global__ void __launch_bounds__(256) select_experts_kernel(const SelectParams 
     }
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
-      const int g = ((i * 32 + lane) * V * p.group_inv) >> 20;   // the chunk's group: e / group_size
-      if (!((stay >> (g & 31)) & 1u)) {
+      // groups of 2^n chunks: a chunk's group is its first value's
+      bool stays = false;
 #pragma unroll
-        for (int v = 0; v < V; ++v) key[i * V + v] = -INFINITY;
+      for (int v = 0; v < V; ++v) {
+        if (GROUPS == 2 || v == 0) {
+          const int g = (((i * 32 + lane) * V + v) * p.group_inv) >> 20;   // e / group_size
+          stays = (stay >> (g & 31)) & 1u;
+        }
+        if (!stays) key[i * V + v] = -INFINITY;
       }
     }
   }
@@ -463,7 +498,8 @@ cudaError_t launch_select(const SelectParams& p, bool vec, cudaStream_t stream) 
   const int warps = p.T <= 1024 ? 1 : 8;
   const dim3 grid((p.T + warps - 1) / warps), block(32 * warps);
   const int width = p.group_size / 4;   // chunks of a group on the vector path
-  const int groups = p.n_group == 1 ? 0 : vec && width <= 32 && (width & (width - 1)) == 0 ? 1 : 2;
+  const int groups = p.n_group == p.topk_group ? 0   // all of them stay
+                     : vec && p.group_size % 4 == 0 && width <= 32 && (width & (width - 1)) == 0 ? 1 : 2;
 #define ML_SELECT(NQ, V, G) \
   return launch_k(select_experts_kernel<TL, NQ, V, G>, grid, block, G == 2 ? warps * p.E * 4 : 0, stream, true, p)
 #define ML_SELECT_G(NQ)              \
@@ -540,8 +576,8 @@ extern "C" moe_lora_status moe_lora_select_experts(moe_lora_handle* h, const moe
   p.group_lanes = 32;
   while (p.group_lanes * p.n_group > 32) p.group_lanes /= 2;
   p.factor = a->routed_scaling_factor;
-  // four experts per load when rows and groups divide into aligned quads
-  const bool vec = a->E % 4 == 0 && group_size % 4 == 0 && a->logits_stride % 4 == 0 &&
+  // four experts per load when rows divide into aligned quads
+  const bool vec = a->E % 4 == 0 && a->logits_stride % 4 == 0 &&
                    (at & (a->logits_f32 ? 15u : 7u)) == 0;
   ML_LAUNCH(h, a->logits_f32 ? launch_select<float>(p, vec, stream) : launch_select<__nv_bfloat16>(p, vec, stream),
             "select_experts launch");
