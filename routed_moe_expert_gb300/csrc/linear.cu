@@ -32,14 +32,25 @@ moe_lora_status check_ranks(int S, const int32_t* h_ranks, int most) {
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
+// A shrink cut into slices (shrink_slices): up to 128 stacked columns, 80 slices in all.
+constexpr int kMaxSliced = 80, kMaxSlicedRanks = 128;
+
+// Bytes of u, and of the slices' part sums behind it.
+size_t u_bytes(int T, int Rs) { return align256(static_cast<size_t>(T) * Rs * kFloatPieces * 2); }
+size_t part_bytes(int T, int Rs) {
+  const size_t tt = (static_cast<size_t>(T) + 255) / 256;
+  if (T <= 128 || 2 * tt > kMaxSliced || Rs > kMaxSlicedRanks) return 0;
+  return std::min<size_t>(kMaxSliced, kLinearMaxSlices * tt) * Rs * 1024;
+}
+
 bool tile_map(const moe_lora_handle* h, CUtensorMap* m, const void* base, long long rows, long long cols,
               long long stride, int box_rows, bool f32 = false) {   // boxes of 128 bytes x box_rows
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride) * (f32 ? 4 : 2)};
   const cuuint32_t box[2] = {f32 ? 32u : 64u, static_cast<cuuint32_t>(box_rows)};
   const cuuint32_t estr[2] = {1, 1};
-  return h->encode(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  return h->encode(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                   const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -92,14 +103,30 @@ double cluster_us(int T, int N, int K, int Rs, int bn, int split, int sms) {
                                 weight_mb(T, N, K, bn), Rs <= 64 && bn == 16 ? 4 : 3, 3.5 + (split == 8 ? 4.0 : 0.0), sms);
   return 4.4 + copy + (bn == 32 ? 0.9 : 0.0);
 }
+// Pairs that share the K of a shrink tile.  With at most one product tile per pair a whole shrink
+// tile takes about as long as those that wait for it, and several in a row far longer (T 2450, N 1560,
+// K 3632, 56 ranks: 40.3 us, 21.7 without adapters, 27.4 in slices).  So they are cut along K: over the pairs that have no
+// product tile where these come to two or more per shrink tile, or over all of them.
+int shrink_slices(int T, int N, int K, int Rs, int rows, int sms) {
+  const long long tt = (T + 255) / 256, tiles = tt * ((N + rows - 1) / rows);
+  const long long pairs = std::min(sms / 2, kMaxSliced), idle = sms / 2 - tiles;
+  if (Rs == 0 || Rs > kMaxSlicedRanks || idle < 0) return 1;
+  const long long slices = idle >= 2 * tt ? std::min(idle, pairs) / tt : pairs / tt;
+  const long long most = std::min<long long>(kLinearMaxSlices, (K + 63) / 64 / 4);   // four K blocks or more each
+  return static_cast<int>(std::max(1LL, std::min(slices, most)));
+}
+
 // Pairs: a pair walks whole tiles of 256 tokens x `rows`; a 64-deep K step takes 0.30 us at 256 rows
 // (the tensor cores' rate), 0.285 at 192 and 0.28 at 128 (an SM's intake of copies), so the smaller ones pay
 // only where they bring no further wave: T 3066, N 1551, K 6624: 66.6 / 62.9 / 87.6 us.
 double wide_us(int T, int N, int K, int Rs, int rows, int sms) {
-  const long long tt = (T + 255) / 256, tiles = tt * ((N + rows - 1) / rows);
+  const long long tt = (T + 255) / 256, tiles = tt * ((N + rows - 1) / rows), nk = (K + 63) / 64;
   const long long shrinks = Rs > 0 ? tt * ((Rs + rows - 1) / rows) : 0;
-  const long long waves = (tiles + (tiles <= sms / 2 ? shrinks : 0) + sms / 2 - 1) / (sms / 2);
-  return 3.5 + (rows == 256 ? 0.3 : rows == 192 ? 0.285 : 0.28) * static_cast<double>(waves) * ((K + 63) / 64) + (Rs > 0 ? 3.5 : 0.0);
+  const int slices = shrink_slices(T, N, K, Rs, rows, sms);
+  const long long waves = (tiles + (slices == 1 && tiles <= sms / 2 ? shrinks : 0) + sms / 2 - 1) / (sms / 2);
+  double us = 3.5 + (rows == 256 ? 0.3 : rows == 192 ? 0.285 : 0.28) * static_cast<double>(waves * nk);
+  if (Rs > 0) us += slices == 1 ? 3.5 : 1.0 + (tiles + shrinks * slices > sms / 2 ? 0.2 * static_cast<double>(nk / slices) : 0.0);
+  return us;
 }
 
 Tiles pick_tiles(int T, int N, int K, bool f32, int Rs, int sms) {
@@ -178,7 +205,8 @@ moe_lora_status moe_lora_linear_workspace_size(int T, int S, const int32_t* h_ra
   const moe_lora_status st = check_ranks(S, h_ranks, kMaxRank);
   if (st != MOE_LORA_OK) return st;
   int lo[kMaxSlots + 1];
-  *bytes = 256 + align256(static_cast<size_t>(T) * stacked_ranks(h_ranks, S, lo) * kFloatPieces * 2);
+  const int Rs = stacked_ranks(h_ranks, S, lo);
+  *bytes = 256 + u_bytes(T, Rs) + part_bytes(T, Rs);
   return MOE_LORA_OK;
 }
 
@@ -219,7 +247,7 @@ moe_lora_status moe_lora_linear(moe_lora_handle* h, const moe_lora_linear_args* 
       active = true;
     }
   }
-  const size_t need = 256 + (active ? align256(static_cast<size_t>(a->T) * Rs * kFloatPieces * 2) : 0);
+  const size_t need = 256 + (active ? u_bytes(a->T, Rs) + part_bytes(a->T, Rs) : 0);
   if (workspace_bytes < need) return MOE_LORA_ERR_WORKSPACE_TOO_SMALL;
   if (active && (a->adapters == nullptr || !aligned16(a->adapters))) return MOE_LORA_ERR_INVALID_ARG;
   if (!h->linear_ready) {
@@ -235,6 +263,7 @@ moe_lora_status moe_lora_linear(moe_lora_handle* h, const moe_lora_linear_args* 
   p.slot_idx = active ? a->slot_idx : nullptr;
   p.status = static_cast<uint32_t*>(workspace);
   p.pieces = a->y_f32 ? kFloatPieces : 1;
+  p.shrink_slices = 1;
   const long long x_stride = a->T > 1 ? a->x_stride : a->K, w_stride = a->N > 1 ? a->w_stride : a->K;
   const bool wide = c.kernel == kWide;
   const int x_box = wide ? 128 : c.tokens, w_box = wide ? c.rows / 2 : 128;
@@ -249,6 +278,8 @@ moe_lora_status moe_lora_linear(moe_lora_handle* h, const moe_lora_linear_args* 
     p.Rs = Rs;
     p.u = reinterpret_cast<__nv_bfloat16*>(static_cast<uint8_t*>(workspace) + 256);
     p.flags = h->linear_flags;
+    p.shrink_slices = wide ? shrink_slices(a->T, a->N, a->K, Rs, c.rows, h->num_sms) : 1;
+    p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 256 + u_bytes(a->T, Rs));
     const long long ldu = static_cast<long long>(p.pieces) * Rs;
     // Small shrink tiles are done sooner, but each reads the stacked A again: 16 tokens at T 64 take
     // 1.1 us off (13.4 -> 12.3, N 5120, K 2048) and add 1.9 at T 256 (12.3 -> 14.1, N 2048).

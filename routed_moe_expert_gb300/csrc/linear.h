@@ -29,6 +29,8 @@ struct LinearParams {
   int Rs;                // stacked columns, a multiple of 64 (0: no adapters)
   int pieces;            // 1, or kFloatPieces bf16 pieces of a float32 u
   int token_tiles;
+  int shrink_slices;     // (wide) pairs that share a shrink tile's K, 1 to kLinearMaxSlices
+  float* part;           // (wide, slices) their part sums, 1024 bytes per tile and column
   int shrink_tokens;     // (narrow) tokens of a shrink tile, a divisor of the token tile
   const int32_t* slot_idx;
   const float* bias;     // [N] or null
@@ -38,12 +40,13 @@ struct LinearParams {
   int y_f32;
   int y_vec;             // rows of y start on 4-value boundaries (vector stores); wide tiles: on
                          // 16-byte boundaries (TMA stores)
-  int2* flags;           // per token tile: {shrink parts done, product parts past them}; zero
-                         // between calls
+  int2* flags;           // per token tile: {shrink parts done, product parts past them}, and after
+                         // these (slices) {part sums written, unused}; zero between calls
   uint32_t* status;      // written by the first CTA
   LinearSlots slots;
 };
 constexpr int kLinearFlags = 8192;   // token tiles of a call with adapters
+constexpr int kLinearMaxSlices = 8;
 
 // One 128-row x bn-token tile per cluster of `split` CTAs, which share the tile's K; split is at
 // most the number of 64-wide K blocks.  Maps' boxes: {64, 128} of w, a, b, {64, bn} of

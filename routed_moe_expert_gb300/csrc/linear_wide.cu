@@ -14,6 +14,12 @@
 // is resident as a whole (a pair per TPC), and the last product tile of a token tile sets the flag
 // back.
 //
+// With at most one product tile per pair the shrink is cut along K into slices, one to a pair: a pair
+// writes its slice's part sums, waits for the token tile's others, and adds up its share of the
+// columns in the slices' order.  All of that runs under the product tiles' main loops.  T 777, N 1536,
+// K 2048, 48 ranks: 15.2 us with whole shrink tiles, 13.6 in slices, 12.5 without adapters; T 2450,
+// N 1560, K 3632, 56 ranks: 40.3, 27.4 and 21.7 (there every pair has a product tile as well).
+//
 // Persistent pairs walk the tiles in groups of 8 token tiles, token tile fastest, so the pairs
 // running at one time share weight and token tiles in L2.
 //
@@ -77,15 +83,17 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
   const bool lora = p.Rs > 0;
   const int sh_cols = linear_shrink_cols(p.Rs, BN);            // stacked rows of a shrink tile
   const int sh_parts = lora ? (p.Rs + sh_cols - 1) / sh_cols : 0;
-  const int nshrink = sh_parts * TT;
+  const int kparts = p.shrink_slices;                          // shrink tiles that share a K
+  const int nshrink = sh_parts * TT * kparts;
 
   // This pair's tiles, in order: shrink tiles (numbers below nshrink), then product tiles.  Of the
   // NT * TT product tiles the last pairs get one more than the first `spare` ones, which take the
   // shrink tiles: two each where a shrink tile costs half a product tile.  What is left over goes
-  // round all pairs.
+  // round all pairs.  Slices of a shrink (kparts > 1) go one to a pair, from the pairs without a
+  // product tile on.
   const int vpair = pairs - 1 - pair;
   const int spare = pairs - NT * TT % pairs;   // pairs with NT * TT / pairs tiles
-  const int to_spare = min(nshrink, spare * (2 * sh_cols <= BN ? 2 : 1));
+  const int to_spare = kparts > 1 ? 0 : min(nshrink, spare * (2 * sh_cols <= BN ? 2 : 1));
   const int n_spare = pair < spare && pair < to_spare ? (to_spare - pair + spare - 1) / spare : 0;
   const int n_shrink = n_spare + (nshrink - to_spare > pair ? (nshrink - to_spare - pair + pairs - 1) / pairs : 0);
   const int n_tiles = n_shrink + (NT * TT > vpair ? (NT * TT - vpair + pairs - 1) / pairs : 0);
@@ -130,10 +138,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
   pdl_wait();
   pdl_trigger();
 
-  auto decode = [&](int tile, int& tt, int& nt) {   // a shrink tile's nt: its part of the stack
+  // a shrink tile's nt: its part of the stack; its K blocks are those from first_k(tile) to last_k(tile)
+  auto decode = [&](int tile, int& tt, int& nt) {
     if (tile < nshrink) {
-      tt = tile / sh_parts;
-      nt = tile - tt * sh_parts;
+      const int g = tile / kparts;
+      tt = g / sh_parts;
+      nt = g - tt * sh_parts;
       return;
     }
     tile -= nshrink;
@@ -142,6 +152,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
     nt = r / size;
     tt = g * kTokenGroup + r - nt * size;
   };
+  auto first_k = [&](int tile) -> int { return tile < nshrink ? tile % kparts * nk / kparts : 0; };
+  auto last_k = [&](int tile) -> int { return tile < nshrink ? (tile % kparts + 1) * nk / kparts : nk; };
   // the block mask of the i-th product tile of this pair, handed over by warp 6
   auto take_mask = [&](int i, uint64_t& mask) -> bool {
     if (!mbar_wait(&mfull[i & 1], (i >> 1) & 1, abort_flag, p.status, kWhereLinear)) return false;
@@ -178,8 +190,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
         decode(tile, tt, nt);
         const int t = tt * 256 + static_cast<int>(crank) * 128;
         if (tile < nshrink) {
-          const int half = sh_cols / 2;
-          for (int kb = 0; ok && kb < nk; ++kb)
+          const int half = sh_cols / 2, k1 = last_k(tile);
+          for (int kb = first_k(tile); ok && kb < k1; ++kb)
             ok = issue(&p.tmap_x, kb * 64, t, &p.tmap_a, kb * 64, nt * sh_cols + static_cast<int>(crank) * half,
                        kABytes + half * 128);
           continue;
@@ -244,8 +256,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
               aphase ^= 1u;
             }
           };
+          const int tile = tile_at(i), steps_k = last_k(tile) - first_k(tile);
           ok = begin();
-          for (int kb = 0; ok && kb < nk; ++kb) {
+          for (int kb = 0; ok && kb < steps_k; ++kb) {
             bool first = kb == 0;
             if (F32 && kb > 0 && kb % kPartSteps == 0) {
               finish();
@@ -291,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
         m = lo | (static_cast<uint64_t>(hi) << 32);
         if (lane == 0) {
           int* ready = reinterpret_cast<int*>(p.flags + tt);
-          const int target = 8 * sh_parts;   // the pair's epilogue warps, for every part
+          const int target = 8 * sh_parts * kparts;   // the pair's epilogue warps, for every shrink tile
           if (m) ok = wait_flag_geq(ready, target, abort_flag, p.status, kWhereLinear);   // u is written
           ok = ok && mbar_wait_sleep(&mempty[i & 1], ((i >> 1) & 1) ^ 1, abort_flag, p.status, kWhereLinear);
           if (ok) {
@@ -302,6 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
                 wait_flag_geq(ready, target, abort_flag, p.status, kWhereLinear)) {
               atomicExch(ready, 0);
               atomicExch(ready + 1, 0);
+              if (kparts > 1) atomicExch(reinterpret_cast<int*>(p.flags + TT + tt), 0);   // all are past it, too
             }
           }
         }
@@ -335,11 +349,66 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
         aphase ^= 1u;
       }
     };
+    // Columns c to c + 4 of u for this lane's token, scaled, where they are its slot's, and 0 elsewhere
+    auto store_u4 = [&](int t, int c, const float4& sum, int lo, int hi, float sc) {
+      const float f[4] = {sum.x, sum.y, sum.z, sum.w};
+      float g[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) g[j] = (c + j >= lo && c + j < hi) ? sc * f[j] : 0.0f;
+      __nv_bfloat16* u = p.u + static_cast<long long>(t) * (F32 ? kFloatPieces : 1) * p.Rs + c;
+#pragma unroll
+      for (int piece = 0; piece < (F32 ? kFloatPieces : 1); ++piece) {
+        const uint2 v = pack4(g);
+        *reinterpret_cast<uint2*>(u + piece * p.Rs) = v;
+        g[0] -= __uint_as_float(v.x << 16);
+        g[1] -= __uint_as_float(v.x & 0xffff0000u);
+        g[2] -= __uint_as_float(v.y << 16);
+        g[3] -= __uint_as_float(v.y & 0xffff0000u);
+      }
+    };
+    // A slice's part sums, [column / 4][token][4] (a warp's stores are 512 bytes in a row).
+    auto slice_at = [&](int tile, int quad) -> float4* {
+      return reinterpret_cast<float4*>(p.part) + (static_cast<long long>(tile) * (sh_cols / 4) + quad) * 256 +
+             static_cast<int>(crank) * 128 + quarter * 32 + lane;
+    };
+    // Once every slice of the token tile has written its part sums, each adds up its share of the
+    // columns, in the slices' order.
+    auto join_slices = [&](int tile, int tt, int nt, int t) -> bool {
+      int* arrived = reinterpret_cast<int*>(p.flags + TT + tt);
+      const int sl = t < p.T ? p.slot_idx[t] : -1;
+      const bool has = sl >= 0 && sl < p.slots.S;
+      const int lo = has ? p.slots.lo[sl] : 0, hi = has ? p.slots.hi[sl] : 0;
+      const float sc = has ? p.slots.scal[sl] : 0.0f;
+      __syncwarp();   // the release covers every lane's writes before this
+      int ok = 1;
+      if (lane == 0) {
+        red_release_add(arrived, 1);
+        ok = wait_flag_geq(arrived, 8 * sh_parts * kparts, abort_flag, p.status, kWhereLinear);
+      }
+      if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
+      const int slice = tile % kparts, first = tile - slice, quads = sh_cols / 4;
+#pragma unroll 2
+      for (int q = slice * quads / kparts; q < (slice + 1) * quads / kparts; ++q) {
+        float4 v[kLinearMaxSlices];
+#pragma unroll
+        for (int i = 0; i < kLinearMaxSlices; ++i)
+          v[i] = i < kparts ? __ldcg(slice_at(first + i, q)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int i = 1; i < kLinearMaxSlices; ++i)
+          if (i < kparts) v[0].x += v[i].x, v[0].y += v[i].y, v[0].z += v[i].z, v[0].w += v[i].w;
+        if (t < p.T) store_u4(t, nt * sh_cols + 4 * q, v[0], lo, hi, sc);
+      }
+      fence_proxy_async_global();   // read next by other CTAs' TMA copies
+      __syncwarp();
+      if (lane == 0) red_release_add(reinterpret_cast<int*>(p.flags + tt), 1);
+      return true;
+    };
     auto epilogue_f32 = [&](int tile, int tt, int nt, int t_warp) -> bool {
       float f[128];
 #pragma unroll
       for (int j = 0; j < 128; ++j) f[j] = 0.0f;
-      for (int part = 0; part < (nk + kPartSteps - 1) / kPartSteps; ++part) {
+      const int parts = (last_k(tile) - first_k(tile) + kPartSteps - 1) / kPartSteps;
+      for (int part = 0; part < parts; ++part) {
         if (!mbar_wait_sleep(&tfull[acc], aphase, abort_flag, p.status, kWhereLinear)) return false;
         tc_fence_after();
         const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * BN);
@@ -355,6 +424,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
         release();
       }
       const int t = t_warp + lane;
+      if (tile < nshrink && kparts > 1) {
+#pragma unroll
+        for (int c = 0; c < 128; c += 4)
+          if (c < sh_cols) *slice_at(tile, c / 4) = make_float4(f[c], f[c + 1], f[c + 2], f[c + 3]);
+        return join_slices(tile, tt, nt, t);
+      }
       if (tile < nshrink) {   // u of a token's own columns in bf16 pieces, 0 in the others
         const int sl = t < p.T ? p.slot_idx[t] : -1;
         const bool has = sl >= 0 && sl < p.slots.S;
@@ -439,6 +514,22 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
       if (!mbar_wait_sleep(&tfull[acc], aphase, abort_flag, p.status, kWhereLinear)) break;
       tc_fence_after();
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * BN);
+      if (tile < nshrink && kparts > 1) {
+#pragma unroll 1
+        for (int c = 0; c < sh_cols; c += 32) {
+          uint32_t v[32];
+          __syncwarp();
+          tmem_ld_x32(taddr + c, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 32; j += 4)
+            *slice_at(tile, (c + j) / 4) = make_float4(__uint_as_float(v[j]), __uint_as_float(v[j + 1]),
+                                                       __uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
+        }
+        release();
+        if (!join_slices(tile, tt, nt, t_warp + lane)) break;
+        continue;
+      }
       if (tile < nshrink) {   // u of a token's own columns, 0 in the others
         const int t = t_warp + lane;
         const int sl = t < p.T ? p.slot_idx[t] : -1;
@@ -553,8 +644,11 @@ cudaError_t linear_wide_setup() {
 
 cudaError_t launch_linear_wide(const LinearParams& p, int bn, int sms, cudaStream_t stream) {
   const int cols = linear_shrink_cols(p.Rs, bn);
-  const long long tiles =
-      static_cast<long long>((p.N + bn - 1) / bn + (cols ? (p.Rs + cols - 1) / cols : 0)) * p.token_tiles;
+  const long long shrinks = cols ? (p.Rs + cols - 1) / cols * p.shrink_slices : 0;
+  const long long tiles = ((p.N + bn - 1) / bn + shrinks) * p.token_tiles;
+  // slices wait for one another, so each is the first tile of a pair of its own
+  if (p.shrink_slices > 1 && (shrinks * p.token_tiles > sms / 2 || 2 * p.token_tiles > kLinearFlags))
+    return cudaErrorInvalidValue;
   if (tiles > 0x3fffffffLL || (p.y_f32 && bn != 128)) return cudaErrorInvalidValue;
   const int pairs = static_cast<int>(tiles < sms / 2 ? tiles : sms / 2);
   const dim3 grid(2 * pairs), block(kThreads);

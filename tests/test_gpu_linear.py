@@ -92,6 +92,20 @@ def test_long_batches(handle, T, N, K, slots):
         _check(_run(handle, c, f32), c, f32)
 
 
+@pytest.mark.parametrize("f32", [False, True], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("ranks", [(16, 40), (64, 48)], ids=["64", "128"])
+@pytest.mark.parametrize("T,N,K", [(777, 1536, 2048), (2450, 1560, 1640), (2304, 1000, 520), (300, 8000, 512), (513, 3200, 776)])
+def test_shrinks_shared_by_several_pairs(handle, T, N, K, ranks, f32):
+    """At most one product tile for each pair of SMs, with pairs to spare and without; run twice for the
+    same bits, and once more after a call without adapters."""
+    c = _case(T, N, K, ranks, seed=N, slots="runs", bias=True)
+    got = _run(handle, c, f32)
+    _check(got, c, f32)
+    assert torch.equal(got, _run(handle, c, f32))
+    _run(handle, dict(c, A=None, slots=None), f32)
+    assert torch.equal(got, _run(handle, c, f32))
+
+
 @pytest.mark.parametrize("T,N,K", [(3, 130, 7168), (200, 384, 7168), (1500, 384, 7168), (900, 200, 4104)])
 def test_long_sums_in_float32(handle, T, N, K):
     """The tensor cores truncate as they accumulate; in parts of 1024 the error of a float32 result
