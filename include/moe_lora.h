@@ -514,9 +514,12 @@ moe_lora_status moe_lora_linear_workspace_size(int T, int S, const int32_t* h_ra
    operand of the tensor cores in between: bf16 for a bf16 y, three bf16 pieces (24 significant
    bits) for a float32 y.  One launch.  `workspace` (16-byte aligned, contents on entry do not matter)
    starts with the status word that moe_lora_check_status reads: DEVICE_CHECK when a slot index
-   lies outside [-1, S) (such a token gets no adapter; checked when some slot is active), TIMEOUT when a bounded wait ran out (then destroy the
-   handle: its flags may be left set).  The handle holds 64 KB of flags on the device that calls with
-   adapters use, so calls through one handle run one after another, as its stream rule says.
+   lies outside [-1, S) (such a token gets no adapter; checked when some slot is active), TIMEOUT
+   when a bounded wait ran out (then destroy the handle: its flags may be left set).  The handle holds 64 KB of flags on the device that calls with
+   adapters use, so calls through one handle run one after another, as its stream rule says.  A long batch with
+   adapters takes every SM and its blocks wait for one another: other streams' kernels that end by
+   themselves only delay it, two such calls (of two handles) on streams of different priority can
+   hold each other up until their waits end.
    Errors: INVALID_ARG, UNSUPPORTED (more than 4096 stacked ranks; adapters on more than 2^20
    tokens), WORKSPACE_TOO_SMALL, CUDA. */
 moe_lora_status moe_lora_linear(moe_lora_handle* h, const moe_lora_linear_args* a, void* workspace,

@@ -52,7 +52,7 @@ def _build_marshal(verbose: bool) -> None:
     for d in inc:
         cmd += ["-isystem", d]
     cmd += [f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-L", lib, f"-Wl,-rpath,{lib}",
-            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+            "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
