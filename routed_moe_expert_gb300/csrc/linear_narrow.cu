@@ -139,10 +139,11 @@ __global__ void __launch_bounds__(kThreads, 2) linear_narrow_kernel(const __grid
   pdl_trigger();
 
   if (shrink && p.Rs > 128 && index > 0) {
-    // a stack of several row tiles: leave out those that no token needs (the whole cluster decides
-    // alike; the first tile stays, it writes the status word)
+    // a stack of several row tiles: leave out those that no token of the product's tile needs (the
+    // others' blocks are read for all of its tokens; the whole cluster decides alike; the first tile
+    // stays, it writes the status word)
     uint64_t m = 0;
-    for (int j = threadIdx.x; j < bn && t0 + j < p.T; j += kThreads) m |= blocks_of(p.slot_idx[t0 + j]);
+    for (int j = qt * BN + threadIdx.x; j < (qt + 1) * BN && j < p.T; j += kThreads) m |= blocks_of(p.slot_idx[j]);
     if (!__syncthreads_or(((m >> (row0 >> 6)) & 3ull) != 0)) {
       if (threadIdx.x == 0) red_release_add(ready, 1);
       if (warp == 1) tmem_dealloc(tmem_base, TMEM_COLS);

@@ -106,6 +106,20 @@ def test_shrinks_shared_by_several_pairs(handle, T, N, K, ranks, f32):
     assert torch.equal(got, _run(handle, c, f32))
 
 
+@pytest.mark.parametrize("f32", [False, True], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("ranks", [(16,), (64, 64, 64), (40,) * 20], ids=["64", "192", "800"])
+@pytest.mark.parametrize("T,N,K", [(1, 200, 512), (40, 384, 1024), (100, 384, 2048), (250, 384, 4104), (1281, 384, 4104),
+                                   (777, 1536, 1024), (5000, 1536, 264)])
+def test_what_the_workspace_held_does_not_matter(handle, T, N, K, ranks, f32):
+    """NaN in every byte of it, and slots in runs, so that neighbouring tokens need different blocks of
+    the stacked adapters."""
+    c = _case(T, N, K, ranks, seed=T, slots="runs")
+    ad = pkg.moe_lora_linear_adapters(handle, c["A"].cuda(), c["B"].cuda(), c["ranks"], c["scalings"])
+    ws = pkg.alloc_linear_workspace(T, ad)
+    ws.fill_(255)
+    _check(_run(handle, c, f32, workspace=ws), c, f32)
+
+
 @pytest.mark.parametrize("T,N,K", [(3, 130, 7168), (200, 384, 7168), (1500, 384, 7168), (900, 200, 4104)])
 def test_long_sums_in_float32(handle, T, N, K):
     """The tensor cores truncate as they accumulate; in parts of 1024 the error of a float32 result
