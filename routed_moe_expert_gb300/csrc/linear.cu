@@ -59,7 +59,7 @@ struct Tiles {
   Kernel kernel;    // kWide: CTA pairs, 256 tokens x `rows` weight rows
   int tokens;       // token tile
   int rows;         // weight rows of a tile
-  int split;        // (narrow) CTAs that share a tile's K
+  int split;        // CTAs (kWide: pairs) that share a tile's K
 };
 
 // Microseconds of a call on each kernel: models fitted to measured calls in a row (T 1 to 2048, N 384
@@ -73,7 +73,7 @@ double copies_us(long long ctas, int split, double kb_step, int steps, double on
                  double wave, int sms) {
   const double mb = kb_step * steps * 1e-3;
   // CTAs that are resident together: clusters stay within a GPC and leave some of its SMs' places
-  const int room = 2 * sms - (split == 8 ? sms / 3 : split == 4 ? sms / 9 : 0);
+  const int room = 2 * sms - (split == 8 ? sms / 4 : split == 4 ? sms / 9 : 0);
   const long long waves = (ctas + room - 1) / room;
   const double us = ctas <= sms ? mb / (one * 1e-3)
                                 : static_cast<double>(waves) * 2.0 * mb / 0.115 + wave * static_cast<double>(waves - 1);
@@ -81,11 +81,15 @@ double copies_us(long long ctas, int split, double kb_step, int steps, double on
   return std::max(us, weight_mb / hbm);
 }
 double weight_mb(int T, int N, int K, int bn) { return 2e-6 * N * K * (T > bn ? 1.2 : 1.0); }
+// Small shrink tiles are done sooner, but each reads the stacked A again: 16 tokens at T 64 take
+// 1.1 us off (13.4 -> 12.3, N 5120, K 2048) and add 1.9 at T 256 (12.3 -> 14.1, N 2048).
+int shrink_tokens(int T, int bn) { return std::min(bn, T <= 64 ? 16 : T <= 128 ? 32 : 64); }
 // Narrow tiles: set-up, first bytes and epilogue; the sum over a cluster (clusters of 8 do not pack
 // two CTAs to every SM); with adapters what of the shrink and its way back the copies do not hide.
 double narrow_us(int T, int N, int K, int Rs, int bn, int split, int sms) {
   const int steps = ((K + 63) / 64 + split - 1) / split;
-  const long long ctas = static_cast<long long>((N + 127) / 128) * ((T + bn - 1) / bn) * split;
+  const long long shrinks = static_cast<long long>((Rs + 127) / 128) * ((T + shrink_tokens(T, bn) - 1) / shrink_tokens(T, bn));
+  const long long ctas = (static_cast<long long>((N + 127) / 128) * ((T + bn - 1) / bn) + shrinks) * split;
   const double copy = copies_us(ctas, split, 16.0 + bn / 8.0, steps, 75.0, weight_mb(T, N, K, bn),
                                 bn == 16 ? 6 : bn == 32 ? 5 : bn == 64 ? 4 : 3,
                                 3.5 + (split == 8 ? 4.0 : 0.0) + (Rs > 0 ? 4.0 : 0.0), sms);
@@ -107,9 +111,9 @@ double cluster_us(int T, int N, int K, int Rs, int bn, int split, int sms) {
 // tile takes about as long as those that wait for it, and several in a row far longer (T 2450, N 1560,
 // K 3632, 56 ranks: 40.3 us, 21.7 without adapters, 27.4 in slices).  So they are cut along K: over the pairs that have no
 // product tile where these come to two or more per shrink tile, or over all of them.
-int shrink_slices(int T, int N, int K, int Rs, int rows, int sms) {
-  const long long tt = (T + 255) / 256, tiles = tt * ((N + rows - 1) / rows);
-  const long long pairs = std::min(sms / 2, kMaxSliced), idle = sms / 2 - tiles;
+int shrink_slices(int T, int N, int K, int Rs, int rows, int split, int sms) {
+  const long long tt = (T + 255) / 256, tiles = tt * ((N + rows - 1) / rows) * split;
+  const long long room = linear_wide_pairs(split, sms), pairs = std::min<long long>(room, kMaxSliced), idle = room - tiles;
   if (Rs == 0 || Rs > kMaxSlicedRanks || idle < 0) return 1;
   const long long slices = idle >= 2 * tt ? std::min(idle, pairs) / tt : pairs / tt;
   const long long most = std::min<long long>(kLinearMaxSlices, (K + 63) / 64 / 4);   // four K blocks or more each
@@ -119,14 +123,23 @@ int shrink_slices(int T, int N, int K, int Rs, int rows, int sms) {
 // Pairs: a pair walks whole tiles of 256 tokens x `rows`; a 64-deep K step takes 0.30 us at 256 rows
 // (the tensor cores' rate), 0.285 at 192 and 0.28 at 128 (an SM's intake of copies), so the smaller ones pay
 // only where they bring no further wave: T 3066, N 1551, K 6624: 66.6 / 62.9 / 87.6 us.
-double wide_us(int T, int N, int K, int Rs, int rows, int sms) {
-  const long long tt = (T + 255) / 256, tiles = tt * ((N + rows - 1) / rows), nk = (K + 63) / 64;
+// Two pairs with half of a tile's K each (split 2) exchange their part sums through shared memory,
+// about 4 us, and have less of a main loop to hide the shrink under: T 512, N 4096, K 7168, rank 16:
+// 26.5 us, one pair per tile 35.9; T 512, N 2048, K 2048: 14.8 and 13.4.  (Four pairs, clusters of 8,
+// came out slower everywhere.)
+double wide_us(int T, int N, int K, int Rs, int rows, int split, int sms) {
+  const long long tt = (T + 255) / 256, tiles = tt * ((N + rows - 1) / rows) * split, nk = (K + 63) / 64;
   const long long shrinks = Rs > 0 ? tt * ((Rs + rows - 1) / rows) : 0;
-  const int slices = shrink_slices(T, N, K, Rs, rows, sms);
-  const long long waves = (tiles + (slices == 1 && tiles <= sms / 2 ? shrinks : 0) + sms / 2 - 1) / (sms / 2);
-  double us = 3.5 + (rows == 256 ? 0.3 : rows == 192 ? 0.285 : 0.28) * static_cast<double>(waves * nk);
-  if (Rs > 0) us += slices == 1 ? 3.5 : 1.0 + (tiles + shrinks * slices > sms / 2 ? 0.2 * static_cast<double>(nk / slices) : 0.0);
-  return us;
+  const int slices = shrink_slices(T, N, K, Rs, rows, split, sms), pairs = linear_wide_pairs(split, sms);
+  const double steps = static_cast<double>(nk) / split, slice = 0.2 * static_cast<double>(nk) / slices;
+  if (split == 2) {   // fits K 2048 to 7168
+    const double us = rows == 256 ? 9.2 + 0.26 * steps : 8.0 + 0.235 * steps;
+    return Rs == 0 ? us : us + 1.5 + std::max(0.0, slice + 5.0 - 0.25 * steps);
+  }
+  const long long waves = (tiles + (slices == 1 && tiles <= pairs ? shrinks : 0) + pairs - 1) / pairs;
+  const double us = 3.5 + (rows == 256 ? 0.3 : rows == 192 ? 0.285 : 0.28) * steps * static_cast<double>(waves);
+  if (Rs == 0) return us;
+  return us + (slices == 1 ? 3.5 : std::max(1.0, 6.0 - 0.16 * steps) + (tiles + shrinks * slices > pairs ? slice : 0.0));
 }
 
 Tiles pick_tiles(int T, int N, int K, bool f32, int Rs, int sms) {
@@ -146,12 +159,17 @@ Tiles pick_tiles(int T, int N, int K, bool f32, int Rs, int sms) {
       // result takes at most 1024 of K per accumulator (as far as a cluster goes).
       if (f32 && nk > 16 * split && split < kLinearMaxSplit && 2 * split <= nk) continue;
       offer(narrow_us(T, N, K, Rs, bn, split, sms), {kNarrow, bn, 128, split});
-      if (Rs > 0 && Rs <= 128 && bn <= 32) offer(cluster_us(T, N, K, Rs, bn, split, sms), {kCluster, bn, 128, split});
+      if (Rs > 0 && Rs <= 128 && bn <= 32)
+        offer(cluster_us(T, N, K, Rs, bn, split, sms), {kCluster, bn, 128, split});
     }
   }
   if (T > 128)
-    for (int rows = f32 ? 128 : 256; rows >= 128; rows -= 64)
-      offer(wide_us(T, N, K, Rs, rows, sms), {kWide, 256, rows, 1});
+    for (int rows = f32 ? 128 : 256; rows >= 128; rows -= 64) {
+      const long long tiles = static_cast<long long>((T + 255) / 256) * ((N + rows - 1) / rows);
+      for (int split = 1; split <= 2; ++split)
+        if (split == 1 || (rows != 192 && nk >= 16 && 2 * tiles <= linear_wide_pairs(2, sms)))
+          offer(wide_us(T, N, K, Rs, rows, split, sms), {kWide, 256, rows, split});
+    }
   return best;
 }
 
@@ -263,7 +281,8 @@ moe_lora_status moe_lora_linear(moe_lora_handle* h, const moe_lora_linear_args* 
   p.slot_idx = active ? a->slot_idx : nullptr;
   p.status = static_cast<uint32_t*>(workspace);
   p.pieces = a->y_f32 ? kFloatPieces : 1;
-  p.shrink_slices = 1;
+  p.shrink_slices = p.k_slices = 1;
+  if (c.kernel == kWide) p.k_slices = c.split;
   const long long x_stride = a->T > 1 ? a->x_stride : a->K, w_stride = a->N > 1 ? a->w_stride : a->K;
   const bool wide = c.kernel == kWide;
   const int x_box = wide ? 128 : c.tokens, w_box = wide ? c.rows / 2 : 128;
@@ -278,12 +297,10 @@ moe_lora_status moe_lora_linear(moe_lora_handle* h, const moe_lora_linear_args* 
     p.Rs = Rs;
     p.u = reinterpret_cast<__nv_bfloat16*>(static_cast<uint8_t*>(workspace) + 256);
     p.flags = h->linear_flags;
-    p.shrink_slices = wide ? shrink_slices(a->T, a->N, a->K, Rs, c.rows, h->num_sms) : 1;
+    p.shrink_slices = wide ? shrink_slices(a->T, a->N, a->K, Rs, c.rows, c.split, h->num_sms) : 1;
     p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 256 + u_bytes(a->T, Rs));
     const long long ldu = static_cast<long long>(p.pieces) * Rs;
-    // Small shrink tiles are done sooner, but each reads the stacked A again: 16 tokens at T 64 take
-    // 1.1 us off (13.4 -> 12.3, N 5120, K 2048) and add 1.9 at T 256 (12.3 -> 14.1, N 2048).
-    p.shrink_tokens = std::min(c.tokens, a->T <= 64 ? 16 : a->T <= 128 ? 32 : 64);
+    p.shrink_tokens = shrink_tokens(a->T, c.tokens);
     if (c.kernel == kNarrow) ok = ok && tile_map(h, &p.tmap_xs, a->x, a->T, a->K, x_stride, p.shrink_tokens);
     ok = ok && tile_map(h, &p.tmap_a, Ap, Rs, a->K, a->K, a_box) &&
          tile_map(h, &p.tmap_b, Bp, a->N, Rs, Rs, w_box) && tile_map(h, &p.tmap_u, p.u, a->T, ldu, ldu, x_box);

@@ -31,6 +31,7 @@ struct LinearParams {
   int token_tiles;
   int shrink_slices;     // (wide) pairs that share a shrink tile's K, 1 to kLinearMaxSlices
   float* part;           // (wide, slices) their part sums, 1024 bytes per tile and column
+  int k_slices;          // (wide) pairs that share a product tile's K: 1 or 2
   int shrink_tokens;     // (narrow) tokens of a shrink tile, a divisor of the token tile
   const int32_t* slot_idx;
   const float* bias;     // [N] or null
@@ -63,6 +64,7 @@ cudaError_t launch_linear_cluster(const LinearParams& p, int bn, int split, cuda
 // Tiles of 256 tokens x bn (128, 192 or 256; float32 y: 128) weight rows on CTA pairs.  Maps' boxes: {64, 128}
 // of x and u, {64, bn / 2} of w and b, {64, linear_shrink_cols(Rs, bn) / 2} of a.
 cudaError_t linear_wide_setup();
+int linear_wide_pairs(int k_slices, int sms);   // pairs that run at one time, after the set-up
 cudaError_t launch_linear_wide(const LinearParams& p, int bn, int sms, cudaStream_t stream);
 inline __host__ __device__ int linear_shrink_cols(int Rs, int bn) { return Rs < bn ? Rs : bn; }   // per shrink tile
 

@@ -20,6 +20,11 @@
 // K 2048, 48 ranks: 15.2 us with whole shrink tiles, 13.6 in slices, 12.5 without adapters; T 2450,
 // N 1560, K 3632, 56 ranks: 40.3, 27.4 and 21.7 (there every pair has a product tile as well).
 //
+// With so few tiles that two pairs are there for each, a cluster of two pairs shares a tile, half of
+// its K each: the part sums (float32, over the stages, which are free by then) are exchanged through
+// distributed shared memory, and each pair stores half of the columns.  T 512, N 4096, K 7168, rank 16:
+// 35.9 us with a pair per tile, 26.5 with two; through L2 instead of shared memory it was 29.4.
+//
 // Persistent pairs walk the tiles in groups of 8 token tiles, token tile fastest, so the pairs
 // running at one time share weight and token tiles in L2.
 //
@@ -38,6 +43,9 @@
 #include "common.cuh"
 #include "linear.h"
 
+#include <algorithm>
+#include <atomic>
+
 namespace mlk {
 
 namespace {
@@ -53,6 +61,16 @@ constexpr uint64_t kPeerDrainNs = 100000;      // 100 us for an aborted odd CTA'
 __host__ __device__ constexpr int stage_bytes(int bn) { return kABytes + bn / 2 * 128; }
 __host__ __device__ constexpr int stages_of(int bn) { return bn == 256 ? 6 : bn == 192 ? 6 : 8; }
 __host__ __device__ constexpr int smem_bytes(int bn) { return 1024 + stages_of(bn) * stage_bytes(bn) + kYBytes + 256; }
+
+MLDEV float4 ld_cluster4(uint32_t cluster_address) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(cluster_address)
+               : "memory");
+  return v;
+}
+MLDEV void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 
 template <int BN, bool F32>
 __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_constant__ LinearParams p) {
@@ -73,9 +91,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
   volatile uint64_t* mask_s = drain + 1;   // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 3);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  uint64_t* parts_bar = drain + 4;   // [4] (ks 2) the part sums of an epilogue warp and its like are written
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t crank = cluster_ctarank();
+  // A cluster is the ks pairs that share a product tile's K: one, or two with half of it each.  This CTA's place in its
+  // pair, and the rank of the pair's even CTA.
+  const uint32_t crank = cluster_ctarank() & 1u, even = cluster_ctarank() & ~1u;
   const bool leader = crank == 0;
   const int pair = static_cast<int>(blockIdx.x) >> 1, pairs = static_cast<int>(gridDim.x) >> 1;
   const int NT = (p.N + BN - 1) / BN, TT = p.token_tiles;
@@ -85,18 +106,20 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
   const int sh_parts = lora ? (p.Rs + sh_cols - 1) / sh_cols : 0;
   const int kparts = p.shrink_slices;                          // shrink tiles that share a K
   const int nshrink = sh_parts * TT * kparts;
+  const int ks = p.k_slices;                                   // pairs that share a product tile's K
+  const int nprod = NT * TT * ks;
 
   // This pair's tiles, in order: shrink tiles (numbers below nshrink), then product tiles.  Of the
-  // NT * TT product tiles the last pairs get one more than the first `spare` ones, which take the
+  // nprod product tiles the last pairs get one more than the first `spare` ones, which take the
   // shrink tiles: two each where a shrink tile costs half a product tile.  What is left over goes
   // round all pairs.  Slices of a shrink (kparts > 1) go one to a pair, from the pairs without a
   // product tile on.
   const int vpair = pairs - 1 - pair;
-  const int spare = pairs - NT * TT % pairs;   // pairs with NT * TT / pairs tiles
+  const int spare = pairs - nprod % pairs;   // pairs with nprod / pairs tiles
   const int to_spare = kparts > 1 ? 0 : min(nshrink, spare * (2 * sh_cols <= BN ? 2 : 1));
   const int n_spare = pair < spare && pair < to_spare ? (to_spare - pair + spare - 1) / spare : 0;
   const int n_shrink = n_spare + (nshrink - to_spare > pair ? (nshrink - to_spare - pair + pairs - 1) / pairs : 0);
-  const int n_tiles = n_shrink + (NT * TT > vpair ? (NT * TT - vpair + pairs - 1) / pairs : 0);
+  const int n_tiles = n_shrink + (nprod > vpair ? (nprod - vpair + pairs - 1) / pairs : 0);
   auto tile_at = [&](int i) -> int {
     if (i < n_spare) return pair + i * spare;
     if (i < n_shrink) return to_spare + pair + (i - n_spare) * pairs;
@@ -117,6 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
       mbar_init(&mempty[i], leader ? 2 : 1);   // the producer and, in the even CTA, the MMA issuer
     }
     mbar_init(drain, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&parts_bar[i], static_cast<uint32_t>(ks));
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -146,14 +170,21 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
       nt = g - tt * sh_parts;
       return;
     }
-    tile -= nshrink;
+    tile = (tile - nshrink) / ks;
     const int g = tile / (kTokenGroup * NT), r = tile - g * kTokenGroup * NT;
     const int size = min(kTokenGroup, TT - g * kTokenGroup);
     nt = r / size;
     tt = g * kTokenGroup + r - nt * size;
   };
-  auto first_k = [&](int tile) -> int { return tile < nshrink ? tile % kparts * nk / kparts : 0; };
-  auto last_k = [&](int tile) -> int { return tile < nshrink ? (tile % kparts + 1) * nk / kparts : nk; };
+  auto first_k = [&](int tile) -> int {
+    return tile < nshrink ? tile % kparts * nk / kparts : (tile - nshrink) % ks * nk / ks;
+  };
+  auto last_k = [&](int tile) -> int {
+    return tile < nshrink ? (tile % kparts + 1) * nk / kparts : ((tile - nshrink) % ks + 1) * nk / ks;
+  };
+  auto adds = [&](int tile) -> bool {   // the slice of a product tile that takes the adapter blocks: the last
+    return lora && tile >= nshrink && (tile - nshrink) % ks == ks - 1;
+  };
   // the block mask of the i-th product tile of this pair, handed over by warp 6
   auto take_mask = [&](int i, uint64_t& mask) -> bool {
     if (!mbar_wait(&mfull[i & 1], (i >> 1) & 1, abort_flag, p.status, kWhereLinear)) return false;
@@ -171,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
       if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status, kWhereLinear)) return false;
       uint8_t* a = smem + stage * STAGE;
       if (leader) mbar_arrive_expect_tx(&full[stage], 2 * bytes);
-      const uint32_t bar = cluster_addr(&full[stage], 0);
+      const uint32_t bar = cluster_addr(&full[stage], even);
       tma_load_2d_pair(a, xm, bar, kx, t, pol);
       tma_load_2d_pair(a + kABytes, wm, bar, kw, n, pol);
       issued |= 1u << stage;
@@ -197,8 +228,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
           continue;
         }
         const int n = nt * BN + static_cast<int>(crank) * (BN / 2);
-        for (int kb = 0; ok && kb < nk; ++kb) ok = issue(&p.tmap_x, kb * 64, t, &p.tmap_w, kb * 64, n, STAGE);
-        if (ok && lora) {
+        const int k1 = last_k(tile);
+        for (int kb = first_k(tile); ok && kb < k1; ++kb)
+          ok = issue(&p.tmap_x, kb * 64, t, &p.tmap_w, kb * 64, n, STAGE);
+        if (ok && adds(tile)) {
           uint64_t mask = 0;
           ok = take_mask(nmask++, mask);
           if (mask) fence_proxy_async_global();   // u was written by st.global, read next by TMA
@@ -230,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
         const uint64_t ad = sw128_kmajor_desc(a), bd = sw128_kmajor_desc(a + kABytes);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) umma_bf16_pair(d, ad + 2 * kk, bd + 2 * kk, idesc, (first && kk == 0) ? 0u : 1u);
-        umma_commit_pair_mc(&empty[stage], 0x3);
+        umma_commit_pair_mc(&empty[stage], static_cast<uint16_t>(0x3u << even));
         if (++stage == kStages) {
           stage = 0;
           phase ^= 1u;
@@ -250,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
             return true;
           };
           auto finish = [&]() {
-            umma_commit_pair_mc(&tfull[acc], 0x3);
+            umma_commit_pair_mc(&tfull[acc], static_cast<uint16_t>(0x3u << even));
             if (++acc == 2) {
               acc = 0;
               aphase ^= 1u;
@@ -267,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
             }
             ok = ok && consume(d, idesc, first);
           }
-          if (ok && lora && !shrink) {
+          if (ok && adds(tile)) {
             uint64_t mask = 0;
             ok = take_mask(nmask++, mask);
             const int steps = __popcll(mask) * (F32 ? kFloatPieces : 1);
@@ -284,6 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
     if (lora) {
       int ok = 1;
       for (int i = 0; i < n_tiles - n_shrink; ++i) {
+        if (!adds(tile_at(n_shrink + i))) continue;   // (slices: the pair's only product tile)
         int tt, nt;
         decode(tile_at(n_shrink + i), tt, nt);
         int sl[8];
@@ -343,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
     auto release = [&]() {   // the accumulator has been read out
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(cluster_addr(&tempty[acc], 0));
+      if (lane == 0) mbar_arrive_cluster(cluster_addr(&tempty[acc], even));
       if (++acc == 2) {
         acc = 0;
         aphase ^= 1u;
@@ -403,6 +437,37 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
       if (lane == 0) red_release_add(reinterpret_cast<int*>(p.flags + tt), 1);
       return true;
     };
+    // Halves of a product tile's K: every warp writes its part sums over the stages (all MMAs are done),
+    // [column / 4][token][4], tells the same warp of the other half, waits for that one, and stores its
+    // half of the columns.  The first half is the cluster's second pair's (tiles go out from the last
+    // pair on).
+    auto part_at = [&](int quad) -> uint32_t {
+      return static_cast<uint32_t>((quad * 128 + quarter * 32 + lane) * 16);
+    };
+    auto all_parts = [&]() -> bool {
+      __syncwarp();   // the release covers every lane's writes before this
+      if (lane < ks) mbar_arrive_cluster(cluster_addr(&parts_bar[quarter], 2 * lane + crank));
+      if (!mbar_wait_sleep(&parts_bar[quarter], 0, abort_flag, p.status, kWhereLinear)) return false;
+      fence_cluster();
+      return true;
+    };
+    auto sum_parts = [&](int quad, auto& sum) {   // columns from 4 quad on; all loads in flight together
+      constexpr int Q = sizeof(sum) / 16;
+      const uint32_t a_at = cluster_addr(smem, 2 + crank), b_at = cluster_addr(smem, crank);
+      float4 a[Q], b[Q];
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        a[q] = ld_cluster4(a_at + part_at(quad + q));
+        b[q] = ld_cluster4(b_at + part_at(quad + q));
+      }
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        sum[4 * q] = a[q].x + b[q].x;
+        sum[4 * q + 1] = a[q].y + b[q].y;
+        sum[4 * q + 2] = a[q].z + b[q].z;
+        sum[4 * q + 3] = a[q].w + b[q].w;
+      }
+    };
     auto epilogue_f32 = [&](int tile, int tt, int nt, int t_warp) -> bool {
       float f[128];
 #pragma unroll
@@ -459,10 +524,27 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
         return true;
       }
       float* y32 = static_cast<float*>(p.y);
+      if (t_warp >= p.T) return true;   // (for this warp of every slice)
+      const int prod = tile - nshrink;
+      int c_lo = 0, c_hi = 128;
+      if (ks > 1) {
+#pragma unroll
+        for (int c = 0; c < 128; c += 4)
+          *reinterpret_cast<float4*>(smem + part_at(c / 4)) = make_float4(f[c], f[c + 1], f[c + 2], f[c + 3]);
+        if (!all_parts()) return false;
+        c_lo = prod % ks * (128 / ks);
+        c_hi = c_lo + 128 / ks;
+      }
 #pragma unroll
       for (int c = 0; c < 128; c += 32) {
         const int n = nt * BN + c;
-        if (n >= p.N || t_warp >= p.T) continue;   // warp-uniform
+        if (n >= p.N || c < c_lo || c >= c_hi) continue;   // warp-uniform
+        if (ks > 1) {
+          float sum[32];
+          sum_parts(c / 4, sum);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) f[c + j] = sum[j];
+        }
         if (p.bias != nullptr) {
 #pragma unroll
           for (int j = 0; j < 32; ++j)
@@ -559,16 +641,43 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
         fence_proxy_async_global();   // read next by other CTAs' TMA copies
         __syncwarp();                 // the release below covers every lane's writes before this
         if (lane == 0) red_release_add(reinterpret_cast<int*>(p.flags + tt), 1);
-      } else
+        release();
+        continue;
+      }
+      const int prod = tile - nshrink;
+      int c_lo = 0, c_hi = BN;
+      if (ks > 1 && t_warp < p.T) {   // (the same for this warp of every slice)
 #pragma unroll 1
-      for (int c = 0; c < BN; c += 64) {
+        for (int c = 0; c < BN; c += 32) {
+          uint32_t v[32];
+          __syncwarp();
+          tmem_ld_x32(taddr + c, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 32; j += 4)
+            *reinterpret_cast<float4*>(smem + part_at((c + j) / 4)) =
+                make_float4(__uint_as_float(v[j]), __uint_as_float(v[j + 1]), __uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
+        }
+        if (!all_parts()) break;
+        c_lo = prod % ks * (BN / ks);
+        c_hi = c_lo + BN / ks;
+      }
+#pragma unroll 1
+      for (int c = c_lo; c < c_hi; c += 64) {
         const int n = nt * BN + c;
         if (n >= p.N || t_warp >= p.T) break;   // warp-uniform
         uint32_t v[64];
         __syncwarp();
-        tmem_ld_x32(taddr + c, *reinterpret_cast<uint32_t(*)[32]>(v));
-        tmem_ld_x32(taddr + c + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
-        tmem_ld_wait();
+        if (ks > 1) {
+          float sum[64];
+          sum_parts(c / 4, sum);
+#pragma unroll
+          for (int j = 0; j < 64; ++j) v[j] = __float_as_uint(sum[j]);
+        } else {
+          tmem_ld_x32(taddr + c, *reinterpret_cast<uint32_t(*)[32]>(v));
+          tmem_ld_x32(taddr + c + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+          tmem_ld_wait();
+        }
         if (p.bias != nullptr) {
 #pragma unroll
           for (int j = 0; j < 64; ++j)
@@ -629,6 +738,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
 
 }  // namespace
 
+// Pairs that run at the same time in clusters of two pairs (which stay within a GPC, so not every SM
+// finds a place in one).
+std::atomic<int> g_pairs_by_two = 0;
+
 cudaError_t linear_wide_setup() {
   cudaError_t err;
 #define ML_SETUP(BN, F32)                                                                                         \
@@ -639,21 +752,42 @@ cudaError_t linear_wide_setup() {
   ML_SETUP(128, false)
   ML_SETUP(128, true)
 #undef ML_SETUP
-  return cudaSuccess;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(4);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem_bytes(256);
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 4;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  err = cudaOccupancyMaxActiveClusters(&n, linear_wide_kernel<256, false>, &cfg);
+  g_pairs_by_two = 2 * n;
+  return err;
+}
+
+int linear_wide_pairs(int k_slices, int sms) {
+  return k_slices == 1 ? sms / 2 : std::min(sms / 2, g_pairs_by_two.load());
 }
 
 cudaError_t launch_linear_wide(const LinearParams& p, int bn, int sms, cudaStream_t stream) {
   const int cols = linear_shrink_cols(p.Rs, bn);
   const long long shrinks = cols ? (p.Rs + cols - 1) / cols * p.shrink_slices : 0;
-  const long long tiles = ((p.N + bn - 1) / bn + shrinks) * p.token_tiles;
-  // slices wait for one another, so each is the first tile of a pair of its own
-  if (p.shrink_slices > 1 && (shrinks * p.token_tiles > sms / 2 || 2 * p.token_tiles > kLinearFlags))
+  const long long tiles = ((p.N + bn - 1) / bn * p.k_slices + shrinks) * p.token_tiles;
+  const int room = linear_wide_pairs(p.k_slices, sms);
+  // slices of a shrink wait for one another, so each is the first tile of a pair of its own
+  if (p.shrink_slices > 1 && (shrinks * p.token_tiles > room || 2 * p.token_tiles > kLinearFlags))
     return cudaErrorInvalidValue;
-  if (tiles > 0x3fffffffLL || (p.y_f32 && bn != 128)) return cudaErrorInvalidValue;
-  const int pairs = static_cast<int>(tiles < sms / 2 ? tiles : sms / 2);
+  // halves of a product store whole boxes of columns each, and are their pairs' only product tiles
+  const int ks = p.k_slices;
+  if (ks != 1 && (ks != 2 || bn == 192 || static_cast<long long>((p.N + bn - 1) / bn) * p.token_tiles * 2 > room))
+    return cudaErrorInvalidValue;
+  const int pairs = static_cast<int>(tiles < room ? (tiles + ks - 1) / ks * ks : room);
   const dim3 grid(2 * pairs), block(kThreads);
 #define ML_LINEAR(BN, F32) \
-  return launch_kc(linear_wide_kernel<BN, F32>, grid, block, smem_bytes(BN), stream, true, 2, p)
+  return launch_kc(linear_wide_kernel<BN, F32>, grid, block, smem_bytes(BN), stream, true, 2 * ks, p)
   if (p.y_f32) ML_LINEAR(128, true);
   switch (bn) {
     case 256: ML_LINEAR(256, false);

@@ -107,6 +107,21 @@ def test_shrinks_shared_by_several_pairs(handle, T, N, K, ranks, f32):
 
 
 @pytest.mark.parametrize("f32", [False, True], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("ranks", [(), (16, 40), (64, 64, 64)], ids=["none", "64", "192"])
+@pytest.mark.parametrize("T,N,K", [(300, 1000, 2056), (777, 1536, 2048), (600, 641, 2304), (1281, 384, 4104), (200, 2400, 3080)])
+def test_products_shared_by_several_pairs(handle, T, N, K, ranks, f32):
+    """So few tiles that pairs of SMs share a tile's K; again for the same bits, and into a column range
+    of a wider tensor, of which nothing else is written."""
+    c = _case(T, N, K, ranks, seed=N + 1, slots="runs", bias=True)
+    got = _run(handle, c, f32)
+    _check(got, c, f32)
+    buf = torch.full((T + 2, N + 11), 77.0, dtype=torch.float32 if f32 else torch.bfloat16, device="cuda")
+    assert torch.equal(got, _run(handle, c, f32, out=buf[1:T + 1, 3:N + 3]))
+    buf[1:T + 1, 3:N + 3] = 77.0
+    assert (buf == 77.0).all()
+
+
+@pytest.mark.parametrize("f32", [False, True], ids=["bf16", "fp32"])
 @pytest.mark.parametrize("ranks", [(16,), (64, 64, 64), (40,) * 20], ids=["64", "192", "800"])
 @pytest.mark.parametrize("T,N,K", [(1, 200, 512), (40, 384, 1024), (100, 384, 2048), (250, 384, 4104), (1281, 384, 4104),
                                    (777, 1536, 1024), (5000, 1536, 264)])
