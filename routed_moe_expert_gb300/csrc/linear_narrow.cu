@@ -23,6 +23,12 @@
 // sets it back, so the flags are zero again when the kernel ends.  Blocks start in index order,
 // so the tiles waited for are running before those that wait; every wait is bounded all the same.
 //
+// What bounds it is latency, not bandwidth: start, first copies, a few K steps, the shrink's flag, the
+// adapter blocks, the sum over the cluster, each a memory round trip or two.  T 64, N 5120, K 2048,
+// 120 ranks (64-token tiles, K over 4 CTAs): 12.3 us, 8.0 without adapters, 3.5 for its 24 MB at
+// 6.8 TB/s; tensor pipe 5%, DRAM 18% busy.  T 128, N 384, K 7168, float32 (32-token tiles, K over 8
+// CTAs): 7.4 us for 7.5 MB.
+//
 // Warp 0: TMA producer; warp 1: MMA issuer; warps 2-5: slots of the tile's tokens, epilogue.
 // Every wait is bounded; a timeout raises the CTA's abort flag, is recorded in the status
 // word, and every role still walks through the cluster barriers to the end.

@@ -10,10 +10,13 @@
 // All in float32 from the bf16 inputs, rounded to bf16 once at the end (the norm's result is
 // not rounded before the rotation).
 //
-// It is bound by memory: each value is read once and written once.  L lanes hold a head, so a
-// warp holds 32 / L heads at a time; a lane's pieces are chosen so that both members of every
-// rotated pair sit in the same lane (pieces i and i + R/2 of a half-split rotation), so the only
-// exchange between lanes is the sum of squares.
+// It is bound by memory: each value is read once and written once.  T 8192, 32 + 4 heads of 128:
+// 28.3 us for 155 MB, 5.5 TB/s (81% of a plain copy's rate).  T 333, 24 + 8 heads of 192: 4.4 us for
+// 8.3 MB, one token 2.3 us: latency.
+//
+// L lanes hold a head, so a warp holds 32 / L heads at a time; a lane's pieces are chosen so that both
+// members of every rotated pair sit in the same lane (pieces i and i + R/2 of a half-split rotation),
+// so the only exchange between lanes is the sum of squares.
 //
 // Where everything starts on 16-byte boundaries (qk_norm_rope_kernel) a lane's 16 values of every
 // head of a token have the same weights and angles: out_i = scale (x_i C_i + x_partner S_i), with

@@ -13,11 +13,16 @@
 //
 // A lane holds NQ chunks of V consecutive experts, so loads are one vector per chunk and, where
 // groups are a power of two of chunks, a group's best is a few shuffles among neighbouring
-// lanes; other groups go through shared memory, a few lanes to a group.  The choice itself: the top_k-th largest of the lanes' best keys is a bound below which
-// nothing is chosen; the (few) keys on or above it are handed to one lane each, and top_k rounds
-// of a warp maximum and a warp minimum of the ids that hold it put them in order.  That takes a
-// third of the instructions of looking through the lane's values again after every pick
-// (E 256, top_k 6), and instruction issue is what bounds long batches.
+// lanes; other groups go through shared memory, a few lanes to a group.  The choice itself: the
+// top_k-th largest of the lanes' best keys is a bound below which nothing is chosen; the (few) keys on
+// or above it are handed to one lane each, and every lane counts how many come before its own.
+//
+// Instruction issue bounds long batches: T 16384, E 256, softmax, 8 groups, top_k 6: 11.3 us, 660
+// instructions a token, issue slots 79% busy (17 MB at 1.5 TB/s; 2.6 us at 6.8).  So what is computed
+// is cut: a softmax without a bias is ordered by its numerators and only the last candidates are
+// divided (all divided, and a maximum and a minimum over the warp per pick: 14.4 us with the sum in
+// 64-bit integers, whose conversions run at the rate of double precision).  T 4095, E 384, sigmoid with
+// a bias, bf16: 5.1 us.  One token: 3.2 us, latency.
 #include "common.cuh"
 #include "host.h"
 #include "kernels.h"
