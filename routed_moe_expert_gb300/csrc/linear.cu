@@ -32,15 +32,16 @@ moe_lora_status check_ranks(int S, const int32_t* h_ranks, int most) {
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
-// A shrink cut into slices (shrink_slices): up to 128 stacked columns, 80 slices in all.
-constexpr int kMaxSliced = 80, kMaxSlicedRanks = 128;
+// A shrink cut into slices (deal_shrink): up to 128 stacked columns; with at most one product tile per
+// pair up to 8 slices of each shrink tile and 80 in all, with more 3 of each of up to 106 (T 27136).
+constexpr int kMaxSlicedRanks = 128, kMaxSliced = 80, kDealtSlices = 3, kDealtTiles = 106;
 
 // Bytes of u, and of the slices' part sums behind it.
 size_t u_bytes(int T, int Rs) { return align256(static_cast<size_t>(T) * Rs * kFloatPieces * 2); }
 size_t part_bytes(int T, int Rs) {
-  const size_t tt = (static_cast<size_t>(T) + 255) / 256;
-  if (T <= 128 || 2 * tt > kMaxSliced || Rs > kMaxSlicedRanks) return 0;
-  return std::min<size_t>(kMaxSliced, kLinearMaxSlices * tt) * Rs * 1024;
+  const int tt = T / 256 + (T % 256 != 0);
+  if (T <= 128 || tt > kDealtTiles || Rs > kMaxSlicedRanks) return 0;
+  return static_cast<size_t>(std::max(std::min(kMaxSliced, kLinearMaxSlices * tt), kDealtSlices * tt)) * Rs * 1024;
 }
 
 bool tile_map(const moe_lora_handle* h, CUtensorMap* m, const void* base, long long rows, long long cols,
@@ -50,8 +51,8 @@ bool tile_map(const moe_lora_handle* h, CUtensorMap* m, const void* base, long l
   const cuuint32_t box[2] = {f32 ? 32u : 64u, static_cast<cuuint32_t>(box_rows)};
   const cuuint32_t estr[2] = {1, 1};
   return h->encode(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-                   const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                   const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 enum Kernel { kNarrow, kWide, kCluster };
@@ -88,7 +89,8 @@ int shrink_tokens(int T, int bn) { return std::min(bn, T <= 64 ? 16 : T <= 128 ?
 // two CTAs to every SM); with adapters what of the shrink and its way back the copies do not hide.
 double narrow_us(int T, int N, int K, int Rs, int bn, int split, int sms) {
   const int steps = ((K + 63) / 64 + split - 1) / split;
-  const long long shrinks = static_cast<long long>((Rs + 127) / 128) * ((T + shrink_tokens(T, bn) - 1) / shrink_tokens(T, bn));
+  const int st = shrink_tokens(T, bn);
+  const long long shrinks = static_cast<long long>((Rs + 127) / 128) * ((T + st - 1) / st);
   const long long ctas = (static_cast<long long>((N + 127) / 128) * ((T + bn - 1) / bn) + shrinks) * split;
   const double copy = copies_us(ctas, split, 16.0 + bn / 8.0, steps, 75.0, weight_mb(T, N, K, bn),
                                 bn == 16 ? 6 : bn == 32 ? 5 : bn == 64 ? 4 : 3,
@@ -107,17 +109,53 @@ double cluster_us(int T, int N, int K, int Rs, int bn, int split, int sms) {
                                 weight_mb(T, N, K, bn), Rs <= 64 && bn == 16 ? 4 : 3, 3.5 + (split == 8 ? 4.0 : 0.0), sms);
   return 4.4 + copy + (bn == 32 ? 0.9 : 0.0);
 }
-// Pairs that share the K of a shrink tile.  With at most one product tile per pair a whole shrink
-// tile takes about as long as those that wait for it, and several in a row far longer (T 2450, N 1560,
-// K 3632, 56 ranks: 40.3 us, 21.7 without adapters, 27.4 in slices).  So they are cut along K: over the pairs that have no
-// product tile where these come to two or more per shrink tile, or over all of them.
-int shrink_slices(int T, int N, int K, int Rs, int rows, int split, int sms) {
-  const long long tt = (T + 255) / 256, tiles = tt * ((N + rows - 1) / rows) * split;
-  const long long room = linear_wide_pairs(split, sms), pairs = std::min<long long>(room, kMaxSliced), idle = room - tiles;
-  if (Rs == 0 || Rs > kMaxSlicedRanks || idle < 0) return 1;
-  const long long slices = idle >= 2 * tt ? std::min(idle, pairs) / tt : pairs / tt;
-  const long long most = std::min<long long>(kLinearMaxSlices, (K + 63) / 64 / 4);   // four K blocks or more each
-  return static_cast<int>(std::max(1LL, std::min(slices, most)));
+// How a shrink is cut and dealt out (wide tiles): the slices of a shrink tile's K, how many of all
+// slices go round every pair instead of the spare ones, and the K blocks of the busiest pair.
+//
+// A K block of a shrink tile takes as long as one of a product tile (what is in flight bounds both), so
+// whole shrink tiles are in the way: with at most one product tile per pair they take as long as those
+// that wait for them, and several in a row far longer (T 2450, N 1560, K 3632, 56 ranks: 40.3 us, 21.7
+// without adapters, 27.4 in slices); with more they leave a few pairs a tile behind the others.
+struct Shrink {
+  int slices;
+  long long spread, busiest;
+};
+Shrink deal_shrink(int T, int N, int K, int Rs, int rows, int split, int sms) {
+  const long long tt = (T + 255) / 256, prods = tt * ((N + rows - 1) / rows) * split, nk = (K + 63) / 64;
+  const long long cols = std::min(Rs, rows), tiles = Rs > 0 ? tt * ((Rs + cols - 1) / cols) : 0;
+  const long long room = linear_wide_pairs(split, sms), waves = (prods + room - 1) / room;
+  if (tiles == 0) return {1, 0, waves * (nk / split)};
+  const long long most =   // four K blocks or more each
+      Rs > kMaxSlicedRanks ? 1 : std::min<long long>(kLinearMaxSlices, nk / 4);
+  if (prods <= room) {   // one to a pair: those without a product tile, where they come to two or more a tile
+    const long long idle = room - prods, over = std::min<long long>(kMaxSliced, idle >= 2 * tiles ? idle : room);
+    const long long slices = std::min(most, over / tiles);
+    if (slices > 1) {
+      const bool all = idle < 2 * tiles;
+      return {static_cast<int>(slices), all ? slices * tiles : 0, nk / split + (all ? (nk + slices - 1) / slices : 0)};
+    }
+  }
+  // (as the kernel deals: pairs with a product tile less than others are spare)
+  auto deal = [&](long long slices) -> Shrink {
+    const long long n = tiles * slices, pairs = std::min(room, prods + n), left = prods % pairs;
+    const long long spare = pairs - left, own = prods / pairs * (nk / split), block = (nk + slices - 1) / slices;
+    const long long fill = spare * (slices == 1 && 2 * cols <= rows ? 2 : slices);
+    // (a pair may hold no three slices of one shrink tile: linear_wide.cu's join_slice)
+    const long long spread = slices > spare ? n : std::max(0LL, n - fill);
+    const long long each = (spread + pairs - 1) / pairs, more = (n - spread + spare - 1) / spare;
+    const long long cost = block + (slices > 1 ? 12 : 0);
+    return {static_cast<int>(slices), spread,
+            std::max(own + (each + more) * cost, left ? own + nk / split + each * cost : 0)};
+  };
+  // Writing and joining a slice holds up its pair for about 12 K blocks, more with more slices, so these
+  // pay with a long K only: T 8192, N 4096, K 7168, 128 ranks: 280.5, 275.4, 269.3 and 284.8 us in 1 to 4
+  // slices; N 4096, K 2048, 48 ranks: 88.0, 98.7, 91.9 and 91.6.
+  Shrink best = deal(1);
+  for (long long slices = 2; slices <= (tt > kDealtTiles ? 1 : std::min<long long>(most, kDealtSlices)); ++slices) {
+    const Shrink s = deal(slices);
+    if (s.busiest < best.busiest) best = s;
+  }
+  return best;
 }
 
 // Pairs: a pair walks whole tiles of 256 tokens x `rows`; a 64-deep K step takes 0.30 us at 256 rows
@@ -128,18 +166,15 @@ int shrink_slices(int T, int N, int K, int Rs, int rows, int split, int sms) {
 // 26.5 us, one pair per tile 35.9; T 512, N 2048, K 2048: 14.8 and 13.4.  (Four pairs, clusters of 8,
 // came out slower everywhere.)
 double wide_us(int T, int N, int K, int Rs, int rows, int split, int sms) {
-  const long long tt = (T + 255) / 256, tiles = tt * ((N + rows - 1) / rows) * split, nk = (K + 63) / 64;
-  const long long shrinks = Rs > 0 ? tt * ((Rs + rows - 1) / rows) : 0;
-  const int slices = shrink_slices(T, N, K, Rs, rows, split, sms), pairs = linear_wide_pairs(split, sms);
-  const double steps = static_cast<double>(nk) / split, slice = 0.2 * static_cast<double>(nk) / slices;
+  const long long nk = (K + 63) / 64;
+  const Shrink s = deal_shrink(T, N, K, Rs, rows, split, sms);
+  const double steps = static_cast<double>(nk) / split;
   if (split == 2) {   // fits K 2048 to 7168
     const double us = rows == 256 ? 9.2 + 0.26 * steps : 8.0 + 0.235 * steps;
-    return Rs == 0 ? us : us + 1.5 + std::max(0.0, slice + 5.0 - 0.25 * steps);
+    return Rs == 0 ? us : us + 1.5 + std::max(0.0, 0.2 * static_cast<double>(nk) / s.slices + 5.0 - 0.25 * steps);
   }
-  const long long waves = (tiles + (slices == 1 && tiles <= pairs ? shrinks : 0) + pairs - 1) / pairs;
-  const double us = 3.5 + (rows == 256 ? 0.3 : rows == 192 ? 0.285 : 0.28) * steps * static_cast<double>(waves);
-  if (Rs == 0) return us;
-  return us + (slices == 1 ? 3.5 : std::max(1.0, 6.0 - 0.16 * steps) + (tiles + shrinks * slices > pairs ? slice : 0.0));
+  const double us = 3.5 + (rows == 256 ? 0.3 : rows == 192 ? 0.285 : 0.28) * static_cast<double>(s.busiest);
+  return Rs == 0 ? us : us + (s.slices == 1 ? 3.5 : std::max(1.0, 6.0 - 0.16 * steps));
 }
 
 Tiles pick_tiles(int T, int N, int K, bool f32, int Rs, int sms) {
@@ -297,7 +332,11 @@ moe_lora_status moe_lora_linear(moe_lora_handle* h, const moe_lora_linear_args* 
     p.Rs = Rs;
     p.u = reinterpret_cast<__nv_bfloat16*>(static_cast<uint8_t*>(workspace) + 256);
     p.flags = h->linear_flags;
-    p.shrink_slices = wide ? shrink_slices(a->T, a->N, a->K, Rs, c.rows, c.split, h->num_sms) : 1;
+    if (wide) {
+      const Shrink s = deal_shrink(a->T, a->N, a->K, Rs, c.rows, c.split, h->num_sms);
+      p.shrink_slices = s.slices;
+      p.shrink_spread = static_cast<int>(s.spread);
+    }
     p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 256 + u_bytes(a->T, Rs));
     const long long ldu = static_cast<long long>(p.pieces) * Rs;
     p.shrink_tokens = shrink_tokens(a->T, c.tokens);

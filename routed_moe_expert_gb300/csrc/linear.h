@@ -30,6 +30,7 @@ struct LinearParams {
   int pieces;            // 1, or kFloatPieces bf16 pieces of a float32 u
   int token_tiles;
   int shrink_slices;     // (wide) pairs that share a shrink tile's K, 1 to kLinearMaxSlices
+  int shrink_spread;     // (wide) shrink tiles that go round all pairs, the first ones
   float* part;           // (wide, slices) their part sums, 1024 bytes per tile and column
   int k_slices;          // (wide) pairs that share a product tile's K: 1 or 2
   int shrink_tokens;     // (narrow) tokens of a shrink tile, a divisor of the token tile

@@ -14,11 +14,13 @@
 // is resident as a whole (a pair per TPC), and the last product tile of a token tile sets the flag
 // back.
 //
-// With at most one product tile per pair the shrink is cut along K into slices, one to a pair: a pair
-// writes its slice's part sums, waits for the token tile's others, and adds up its share of the
-// columns in the slices' order.  All of that runs under the product tiles' main loops.  T 777, N 1536,
-// K 2048, 48 ranks: 15.2 us with whole shrink tiles, 13.6 in slices, 12.5 without adapters; T 2450,
-// N 1560, K 3632, 56 ranks: 40.3, 27.4 and 21.7 (there every pair has a product tile as well).
+// The shrink is cut along K into slices: a pair writes its slices' part sums, waits for the token tile's
+// others, and adds up its share of the columns in the slices' order.  With at most one product tile per
+// pair that is one slice to a pair, and all of it runs under the product tiles' main loops: T 777,
+// N 1536, K 2048, 48 ranks: 15.2 us with whole shrink tiles, 13.6 in slices, 12.5 without adapters;
+// T 2450, N 1560, K 3632, 56 ranks: 40.3, 27.4 and 21.7 (there every pair has a product tile as well).
+// With more, and a long K, slices fill up the pairs that have a product tile less than others and what
+// is left over is spread evenly (T 8192, N 4096, K 7168, 128 ranks: 280.5 us whole, 269.3 in three).
 //
 // With so few tiles that two pairs are there for each, a cluster of two pairs shares a tile, half of
 // its K each: the part sums (float32, over the stages, which are free by then) are exchanged through
@@ -37,8 +39,8 @@
 // registers (a token's 128 columns per thread) while the MMAs go on in the other one.
 //
 // Long batches are bound by the tensor cores: T 8192, N 4096, K 7168, 128 ranks of which 64 to 128 at
-// work in a tile: 284 us, 1.71 PFLOP/s of bf16 (91% of a burst of plain library products), tensor pipe
-// 90% active; without adapters 282.  In a row for seconds, at the power limit, 320 and 291.
+// work in a tile: 271 us, 1.79 PFLOP/s of bf16 (95% of a burst of plain library products); without
+// adapters 248 to 255, the rate of these.  In a row for seconds, at the power limit, 305 and 282.
 //
 // Warp 0: TMA producer; warp 1: MMA issuer (even CTA); warps 2-5: epilogue; warp 6: a tile or two
 // ahead of them, which adapter blocks a tile needs, and the wait for its u (in the producer itself
@@ -116,19 +118,18 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
   const int nprod = NT * TT * ks;
 
   // This pair's tiles, in order: shrink tiles (numbers below nshrink), then product tiles.  Of the
-  // nprod product tiles the last pairs get one more than the first `spare` ones, which take the
-  // shrink tiles: two each where a shrink tile costs half a product tile.  What is left over goes
-  // round all pairs.  Slices of a shrink (kparts > 1) go one to a pair, from the pairs without a
-  // product tile on.
+  // nprod product tiles the last pairs get one more than the first `spare` ones.  The first
+  // p.shrink_spread shrink tiles go round all pairs, the others round the spare ones.
   const int vpair = pairs - 1 - pair;
   const int spare = pairs - nprod % pairs;   // pairs with nprod / pairs tiles
-  const int to_spare = kparts > 1 ? 0 : min(nshrink, spare * (2 * sh_cols <= BN ? 2 : 1));
-  const int n_spare = pair < spare && pair < to_spare ? (to_spare - pair + spare - 1) / spare : 0;
-  const int n_shrink = n_spare + (nshrink - to_spare > pair ? (nshrink - to_spare - pair + pairs - 1) / pairs : 0);
+  const int spread = p.shrink_spread;
+  const int n_spread = spread > pair ? (spread - pair + pairs - 1) / pairs : 0;
+  const int n_spare = pair < spare && nshrink - spread > pair ? (nshrink - spread - pair + spare - 1) / spare : 0;
+  const int n_shrink = n_spread + n_spare;
   const int n_tiles = n_shrink + (nprod > vpair ? (nprod - vpair + pairs - 1) / pairs : 0);
   auto tile_at = [&](int i) -> int {
-    if (i < n_spare) return pair + i * spare;
-    if (i < n_shrink) return to_spare + pair + (i - n_spare) * pairs;
+    if (i < n_spread) return pair + i * pairs;
+    if (i < n_shrink) return spread + pair + (i - n_spread) * spare;
     return nshrink + vpair + (i - n_shrink) * pairs;
   };
 
@@ -240,7 +241,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
         if (ok && adds(tile)) {
           uint64_t mask = 0;
           ok = take_mask(nmask++, mask);
-          if (mask) fence_proxy_async_global();   // u was written by st.global, read next by TMA
           for (int piece = 0; piece < (F32 ? kFloatPieces : 1); ++piece)
             for (uint64_t m = mask; ok && m; m &= m - 1) {
               const int c = (__ffsll(static_cast<long long>(m)) - 1) * 64;
@@ -345,7 +345,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
         if (lane == 0) {
           int* ready = reinterpret_cast<int*>(p.flags + tt);
           const int target = 8 * sh_parts * kparts;   // the pair's epilogue warps, for every shrink tile
-          if (m) ok = wait_flag_geq(ready, target, abort_flag, p.status, kWhereLinear);   // u is written
+          if (m) {   // u is written, by st.global, and read next by TMA
+            ok = wait_flag_geq(ready, target, abort_flag, p.status, kWhereLinear);
+            fence_proxy_async_global();
+          }
           ok = ok && mbar_wait_sleep(&mempty[i & 1], ((i >> 1) & 1) ^ 1, abort_flag, p.status, kWhereLinear);
           if (ok) {
             mask_s[i & 1] = m;
@@ -411,23 +414,29 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
       return reinterpret_cast<float4*>(p.part) + (static_cast<long long>(tile) * (sh_cols / 4) + quad) * 256 +
              static_cast<int>(crank) * 128 + quarter * 32 + lane;
     };
+    auto slice_written = [&](int tt) {
+      __syncwarp();   // the release covers every lane's writes before this
+      if (lane == 0) red_release_add(reinterpret_cast<int*>(p.flags + TT + tt), 1);
+    };
     // Once every slice of the token tile has written its part sums, each adds up its share of the
-    // columns, in the slices' order.
-    auto join_slices = [&](int tile, int tt, int nt, int t) -> bool {
-      int* arrived = reinterpret_cast<int*>(p.flags + TT + tt);
+    // columns, in the slices' order.  A pair writes its next slice before it waits for one.  No pairs
+    // wait for one another: a pair's slices are in the order of token tiles, at most two of them of
+    // one, so of all token tiles waited for the first one's slices are never behind another wait.
+    auto join_slice = [&](int tile) -> bool {
+      int tt, nt;
+      decode(tile, tt, nt);
+      const int t = tt * 256 + static_cast<int>(crank) * 128 + quarter * 32 + lane;
       const int sl = t < p.T ? p.slot_idx[t] : -1;
       const bool has = sl >= 0 && sl < p.slots.S;
       const int lo = has ? p.slots.lo[sl] : 0, hi = has ? p.slots.hi[sl] : 0;
       const float sc = has ? p.slots.scal[sl] : 0.0f;
-      __syncwarp();   // the release covers every lane's writes before this
       int ok = 1;
-      if (lane == 0) {
-        red_release_add(arrived, 1);
-        ok = wait_flag_geq(arrived, 8 * sh_parts * kparts, abort_flag, p.status, kWhereLinear);
-      }
+      if (lane == 0)
+        ok = wait_flag_geq(reinterpret_cast<int*>(p.flags + TT + tt), 8 * sh_parts * kparts, abort_flag, p.status,
+                           kWhereLinear);
       if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
       const int slice = tile % kparts, first = tile - slice, quads = sh_cols / 4;
-#pragma unroll 2
+#pragma unroll 4
       for (int q = slice * quads / kparts; q < (slice + 1) * quads / kparts; ++q) {
         float4 v[kLinearMaxSlices];
 #pragma unroll
@@ -499,7 +508,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
 #pragma unroll
         for (int c = 0; c < 128; c += 4)
           if (c < sh_cols) *slice_at(tile, c / 4) = make_float4(f[c], f[c + 1], f[c + 2], f[c + 3]);
-        return join_slices(tile, tt, nt, t);
+        slice_written(tt);
+        return true;
       }
       if (tile < nshrink) {   // u of a token's own columns in bf16 pieces, 0 in the others
         const int sl = t < p.T ? p.slot_idx[t] : -1;
@@ -590,6 +600,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
       }
       return true;
     };
+    // After slice i of this pair is written: join the one before, and the last one, too.
+    auto join_behind = [&](int i) -> bool {
+      if (i >= n_shrink) return true;
+      if (i > 0 && !join_slice(tile_at(i - 1))) return false;
+      return i < n_shrink - 1 || join_slice(tile_at(i));
+    };
     for (int i = 0; i < n_tiles; ++i) {
       const int tile = tile_at(i);
       int tt, nt;
@@ -597,6 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
       const int t_warp = tt * 256 + static_cast<int>(crank) * 128 + quarter * 32;
       if constexpr (F32) {
         if (!epilogue_f32(tile, tt, nt, t_warp)) break;
+        if (kparts > 1 && !join_behind(i)) break;
         continue;
       }
       if (!mbar_wait_sleep(&tfull[acc], aphase, abort_flag, p.status, kWhereLinear)) break;
@@ -615,7 +632,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
                                                        __uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
         }
         release();
-        if (!join_slices(tile, tt, nt, t_warp + lane)) break;
+        slice_written(tt);
+        if (!join_behind(i)) break;
         continue;
       }
       if (tile < nshrink) {   // u of a token's own columns, 0 in the others
@@ -662,7 +680,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
 #pragma unroll
           for (int j = 0; j < 32; j += 4)
             *reinterpret_cast<float4*>(smem + part_at((c + j) / 4)) =
-                make_float4(__uint_as_float(v[j]), __uint_as_float(v[j + 1]), __uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
+                make_float4(__uint_as_float(v[j]), __uint_as_float(v[j + 1]), __uint_as_float(v[j + 2]),
+                            __uint_as_float(v[j + 3]));
         }
         if (!all_parts()) break;
         c_lo = prod % ks * (BN / ks);
@@ -786,9 +805,7 @@ cudaError_t launch_linear_wide(const LinearParams& p, int bn, int sms, cudaStrea
   const long long shrinks = cols ? (p.Rs + cols - 1) / cols * p.shrink_slices : 0;
   const long long tiles = ((p.N + bn - 1) / bn * p.k_slices + shrinks) * p.token_tiles;
   const int room = linear_wide_pairs(p.k_slices, sms);
-  // slices of a shrink wait for one another, so each is the first tile of a pair of its own
-  if (p.shrink_slices > 1 && (shrinks * p.token_tiles > room || 2 * p.token_tiles > kLinearFlags))
-    return cudaErrorInvalidValue;
+  if (p.shrink_slices > 1 && 2 * p.token_tiles > kLinearFlags) return cudaErrorInvalidValue;
   // halves of a product store whole boxes of columns each, and are their pairs' only product tiles
   const int ks = p.k_slices;
   if (ks != 1 && (ks != 2 || bn == 192 || static_cast<long long>((p.N + bn - 1) / bn) * p.token_tiles * 2 > room))

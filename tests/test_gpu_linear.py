@@ -107,6 +107,19 @@ def test_shrinks_shared_by_several_pairs(handle, T, N, K, ranks, f32):
 
 
 @pytest.mark.parametrize("f32", [False, True], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("ranks", [(16, 40), (64, 48)], ids=["64", "128"])
+@pytest.mark.parametrize("T,N,K", [(4000, 2300, 1040), (6000, 1800, 1104), (5000, 1792, 7168)])
+def test_shrinks_dealt_out_over_several_tiles_per_pair(handle, T, N, K, ranks, f32):
+    c = _case(T, N, K, ranks, seed=K, slots="runs", bias=True)
+    ad = pkg.moe_lora_linear_adapters(handle, c["A"].cuda(), c["B"].cuda(), c["ranks"], c["scalings"])
+    ws = pkg.alloc_linear_workspace(T, ad)
+    ws.fill_(255)
+    got = _run(handle, c, f32, workspace=ws)
+    _check(got, c, f32)
+    assert torch.equal(got, _run(handle, c, f32, workspace=ws))
+
+
+@pytest.mark.parametrize("f32", [False, True], ids=["bf16", "fp32"])
 @pytest.mark.parametrize("ranks", [(), (16, 40), (64, 64, 64)], ids=["none", "64", "192"])
 @pytest.mark.parametrize("T,N,K", [(300, 1000, 2056), (777, 1536, 2048), (600, 641, 2304), (1281, 384, 4104), (200, 2400, 3080)])
 def test_products_shared_by_several_pairs(handle, T, N, K, ranks, f32):
