@@ -435,6 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
         ok = wait_flag_geq(reinterpret_cast<int*>(p.flags + TT + tt), 8 * sh_parts * kparts, abort_flag, p.status,
                            kWhereLinear);
       if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
+      __syncwarp();   // lane 0's acquire comes before every lane's loads (a shuffle orders no memory)
       const int slice = tile % kparts, first = tile - slice, quads = sh_cols / 4;
 #pragma unroll 4
       for (int q = slice * quads / kparts; q < (slice + 1) * quads / kparts; ++q) {
