@@ -480,8 +480,9 @@ moe_lora_status moe_lora_select_experts(moe_lora_handle* h, const moe_lora_selec
 /* Stacked copy of the adapters of one projection: A [S, R, K] and B [S, N, R] (bf16, dense, A
    16-byte aligned) of S slots (1..64) with ranks h_ranks[s] <= R <= 128, side by side: rows of
    A_s then columns of B_s, each rank rounded up to 8, all together at most 4096.  Rows of A and
-   columns of B past a slot's rank are never read.  Made once when the adapters in the slots
-   change; `adapters` is caller-owned, 16-byte aligned, moe_lora_linear_adapters_size() bytes
+   columns of B past a slot's rank are never read.  Values that are not finite count in the results
+   of their own slot's tokens as the formula says, and in no other token's.  Made once when the adapters
+   in the slots change; `adapters` is caller-owned, 16-byte aligned, moe_lora_linear_adapters_size() bytes
    (0 when every rank is 0).  K a multiple of 8.
    Errors: INVALID_ARG, UNSUPPORTED (more than 4096 stacked ranks), CUDA. */
 moe_lora_status moe_lora_linear_adapters_size(int S, int N, int K, const int32_t* h_ranks, size_t* bytes);

@@ -32,6 +32,23 @@ moe_lora_status check_ranks(int S, const int32_t* h_ranks, int most) {
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
+// Stacked adapters: As [Rs, K], Bs [N, Rs], and the marks of weights that are not finite
+// (linear_pack_kernel): a word of 64 slots, and 8 words of 16 bits per row.  Where the last slot's columns leave
+// some of their 64-column block, these lie there: the word at the start of a row of As that is no
+// slot's (u of its column is masked), the marks in columns of Bs that are no slot's (bf16 values below
+// 2^-125, times u = 0).  Otherwise behind Bs.
+struct Stack {
+  size_t b, sick, marks;   // byte offsets
+  int mark_stride;
+  size_t bytes;
+};
+Stack stack_of(int Rs, int used, int N, int K) {
+  const size_t a = align256(static_cast<size_t>(Rs) * K * 2), b = align256(static_cast<size_t>(Rs) * N * 2);
+  if (used < Rs) return {a, static_cast<size_t>(used) * K * 2, a + static_cast<size_t>(used) * 2, Rs, a + b};
+  const size_t marks = align256(static_cast<size_t>(N) * kMarkWords * 2);
+  return {a, a + b + marks, a + b, kMarkWords, Rs > 0 ? a + b + marks + 256 : 0};
+}
+
 // A shrink cut into slices (deal_shrink): up to 128 stacked columns; with at most one product tile per
 // pair up to 8 slices of each shrink tile and 80 in all, with more 3 of each of up to 106 (T 27136).
 constexpr int kMaxSlicedRanks = 128, kMaxSliced = 80, kDealtSlices = 3, kDealtTiles = 106;
@@ -217,8 +234,8 @@ moe_lora_status moe_lora_linear_adapters_size(int S, int N, int K, const int32_t
   const moe_lora_status st = check_ranks(S, h_ranks, kMaxRank);
   if (st != MOE_LORA_OK) return st;
   int lo[kMaxSlots + 1];
-  const size_t rs = static_cast<size_t>(stacked_ranks(h_ranks, S, lo));
-  *bytes = align256(rs * K * 2) + align256(rs * N * 2);
+  const int Rs = stacked_ranks(h_ranks, S, lo);
+  *bytes = stack_of(Rs, lo[S], N, K).bytes;
   return MOE_LORA_OK;
 }
 
@@ -241,13 +258,18 @@ moe_lora_status moe_lora_linear_pack_adapters(moe_lora_handle* h, const moe_lora
   for (int s = 0; s < S; ++s) p.ranks[s] = static_cast<uint16_t>(h_ranks[s]);
   p.A = reinterpret_cast<const __nv_bfloat16*>(A);
   p.B = reinterpret_cast<const __nv_bfloat16*>(B);
-  p.Ap = static_cast<__nv_bfloat16*>(adapters);
-  p.Bp = p.Ap + align256(static_cast<size_t>(p.Rs) * K * 2) / 2;
+  uint8_t* at = static_cast<uint8_t*>(adapters);
+  const Stack k = stack_of(p.Rs, lo[S], N, K);
+  p.Ap = reinterpret_cast<__nv_bfloat16*>(at);
+  p.Bp = reinterpret_cast<__nv_bfloat16*>(at + k.b);
+  p.sick = reinterpret_cast<unsigned long long*>(at + k.sick);
+  p.marks = reinterpret_cast<uint16_t*>(at + k.marks);
+  p.mark_stride = k.mark_stride;
   p.S = S;
   p.N = N;
   p.K = K;
   p.R = R;
-  if (static_cast<long long>(p.Rs) * (K / 8) > 255LL * 0x7fffffff || static_cast<long long>(N) * p.Rs > 255LL * 0x7fffffff)
+  if (static_cast<long long>(p.Rs) * (K / 8) > 128LL * 0x7fffffff)   // 2^30 blocks for As, 2^28 for Bs at most
     return MOE_LORA_ERR_INVALID_ARG;
   ML_LAUNCH(h, launch_linear_pack(p, stream), "linear pack launch");
   return MOE_LORA_OK;
@@ -328,7 +350,12 @@ moe_lora_status moe_lora_linear(moe_lora_handle* h, const moe_lora_linear_args* 
   if (active) {
     if (p.token_tiles > kLinearFlags) return MOE_LORA_ERR_UNSUPPORTED;
     const uint8_t* Ap = static_cast<const uint8_t*>(a->adapters);
-    const uint8_t* Bp = Ap + align256(static_cast<size_t>(Rs) * a->K * 2);
+    const Stack k = stack_of(Rs, lo[a->S], a->N, a->K);
+    const uint8_t* Bp = Ap + k.b;
+    p.b = reinterpret_cast<const __nv_bfloat16*>(Bp);
+    p.sick = reinterpret_cast<const unsigned long long*>(Ap + k.sick);
+    p.marks = reinterpret_cast<const uint16_t*>(Ap + k.marks);
+    p.mark_stride = k.mark_stride;
     p.Rs = Rs;
     p.u = reinterpret_cast<__nv_bfloat16*>(static_cast<uint8_t*>(workspace) + 256);
     p.flags = h->linear_flags;

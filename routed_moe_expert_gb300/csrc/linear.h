@@ -8,6 +8,7 @@ namespace mlk {
 constexpr int kMaxStackedRanks = 4096;   // columns of the stacked adapters: 64 blocks of 64
 constexpr int kAdapterBlock = 64;
 constexpr int kFloatPieces = 3;          // bf16 pieces that carry a float32 (8 significant bits each)
+constexpr int kMarkWords = 8;            // 16-bit words of a row's marks, 8 slots each
 
 // Where each slot sits among the stacked adapter columns, and its factor; a slot that adds
 // nothing (rank 0, factor 0) has hi = lo.
@@ -45,6 +46,13 @@ struct LinearParams {
   int2* flags;           // per token tile: {shrink parts done, product parts past them}, and after
                          // these (slices) {part sums written, unused}; zero between calls
   uint32_t* status;      // written by the first CTA
+  // Weights that are not finite (pack_adapters): slots that have any, the marks of row n at
+  // marks + n * mark_stride (slot s: bit s % 8 of word s / 8), and the stacked B itself, in which a
+  // marked slot's values of that row are classes instead
+  const unsigned long long* sick;
+  const uint16_t* marks;
+  int mark_stride;
+  const __nv_bfloat16* b;
   LinearSlots slots;
 };
 constexpr int kLinearFlags = 8192;   // token tiles of a call with adapters
@@ -72,6 +80,9 @@ inline __host__ __device__ int linear_shrink_cols(int Rs, int bn) { return Rs < 
 struct LinearPackParams {
   const __nv_bfloat16 *A, *B;   // [S, R, K], [S, N, R]
   __nv_bfloat16 *Ap, *Bp;       // [Rs, K], [N, Rs]
+  unsigned long long* sick;     // (as in LinearParams; zero before the kernel)
+  uint16_t* marks;
+  int mark_stride;
   int S, N, K, R, Rs;
   uint16_t lo[kMaxSlots + 1];   // first column of each slot, lo[S] = the end of the last
   uint16_t ranks[kMaxSlots];

@@ -16,6 +16,7 @@
 // Warp 0: TMA producer (and the tile's slots); warp 1: MMA issuer; warps 2-5: epilogue.
 #include "common.cuh"
 #include "linear.h"
+#include "linear_nonfinite.cuh"
 
 namespace mlk {
 
@@ -153,6 +154,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_cluster_kernel(const __gri
   const uint32_t tmem_base = *tmem_slot;
   pdl_wait();   // the kernel in front may have made the call's data
   pdl_trigger();
+  unsigned long long sick = 0;   // (epilogue) slots with weights that are not finite
 
   if (warp == 0) {   // ------------------------------------------------ TMA producer
     const uint64_t pol_w = l2_policy_evict_first(), pol_x = l2_policy_evict_last();
@@ -245,6 +247,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_cluster_kernel(const __gri
     }
   } else {   // ---------------------------------------------- slots, then TMEM -> shared memory
     const int et = threadIdx.x - 64;
+    sick = __ldcg(p.sick);
     if (et < BN) {
       const int sl = et < nvalid ? p.slot_idx[t0 + et] : -1;
       const bool has = sl >= 0 && sl < p.slots.S;
@@ -406,6 +409,8 @@ __global__ void __launch_bounds__(kThreads, 2) linear_cluster_kernel(const __gri
     tc_fence_after();
     tmem_dealloc(tmem_base, TMEM_COLS);
   }
+  if (sick != 0 && mask != 0u)
+    add_nonfinite_of_operand<BN, NB>(p, sick, u_s, t0 + j_lo, count, row0 + (warp & 3) * 32 + lane);
 }
 
 }  // namespace

@@ -34,6 +34,7 @@
 // word, and every role still walks through the cluster barriers to the end.
 #include "common.cuh"
 #include "linear.h"
+#include "linear_nonfinite.cuh"
 
 namespace mlk {
 
@@ -143,6 +144,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_narrow_kernel(const __grid
   // before, whose end comes next; then the kernel after this one may start as far.
   pdl_wait();
   pdl_trigger();
+  const unsigned long long sick = lora ? __ldcg(p.sick) : 0;   // slots with weights that are not finite
 
   if (shrink && p.Rs > 128 && index > 0) {
     // a stack of several row tiles: leave out those that no token of the product's tile needs (the
@@ -374,38 +376,69 @@ __global__ void __launch_bounds__(kThreads, 2) linear_narrow_kernel(const __grid
     cluster_arrive();
     cluster_wait();
   }
+  if (sick != 0)   // (0 in shrink tiles); after all that others wait for
+    for (int q = q_lo + static_cast<int>(threadIdx.x); q < q_hi; q += kThreads)
+      add_nonfinite(p, sick, t0 + (q >> 5), row0 + (q & 31) * 4, 4);
 }
 
-// Stacked copies of the adapters: As [Rs, K] (blocks below gridDim.y = 0) and Bs [N, Rs].
+// Stacked copies of the adapters: As [Rs, K] (blocks up to a_blocks) and Bs [N, Rs] (a warp per row).
 // Ranks past a slot's own are never read; columns of no slot are zero.
-__global__ void __launch_bounds__(256) linear_pack_kernel(const __grid_constant__ LinearPackParams p) {
-  const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
-  auto slot_of = [&](int c) -> int {   // the slot whose columns hold c (p.S: past the last)
-    int lo = 0, hi = p.S;
-    while (lo < hi) {   // first s with lo[s + 1] > c
-      const int mid = (lo + hi) >> 1;
-      if (p.lo[mid + 1] > c) hi = mid; else lo = mid + 1;
-    }
-    return lo;
-  };
-  if (blockIdx.y == 0) {   // 8 values of a row of As
+//
+// A product takes whole blocks of Bs's columns, with u = 0 in those of other slots: fine while these are
+// finite, but 0 x inf is NaN.  So Bs holds finite values alone: where a row of a slot has one that is not,
+// the slot's values of that row are stored as classes (0 for 0, +-1 for finite, +-2 for +-inf, 3 for NaN),
+// the row is marked for that slot, and the epilogue adds what they stand for to the slot's own tokens
+// (linear_nonfinite.cuh).
+__global__ void __launch_bounds__(256) linear_pack_kernel(const __grid_constant__ LinearPackParams p, unsigned a_blocks) {
+  if (blockIdx.x < a_blocks) {   // 8 values of a row of As
+    const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
     const int per = p.K >> 3;
     if (i >= static_cast<long long>(p.Rs) * per) return;
     const int c = static_cast<int>(i / per), k = static_cast<int>(i - static_cast<long long>(c) * per) * 8;
-    const int s = slot_of(c);
+    int s = 0, hi = p.S;   // the slot whose columns hold c (p.S: past the last): first s with lo[s + 1] > c
+    while (s < hi) {
+      const int mid = (s + hi) >> 1;
+      if (p.lo[mid + 1] > c) hi = mid; else s = mid + 1;
+    }
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
     if (s < p.S && c - p.lo[s] < p.ranks[s])
       v = *reinterpret_cast<const uint4*>(p.A + (static_cast<long long>(s) * p.R + c - p.lo[s]) * p.K + k);
-    *reinterpret_cast<uint4*>(p.Ap + static_cast<long long>(c) * p.K + k) = v;
-  } else {   // one value of Bs
-    if (i >= static_cast<long long>(p.N) * p.Rs) return;
-    const long long n = i / p.Rs;
-    const int c = static_cast<int>(i - n * p.Rs);
-    const int s = slot_of(c);
-    __nv_bfloat16 v = __float2bfloat16_rn(0.0f);
-    if (s < p.S && c - p.lo[s] < p.ranks[s]) v = p.B[(static_cast<long long>(s) * p.N + n) * p.R + c - p.lo[s]];
-    p.Bp[i] = v;
+    uint4* at = reinterpret_cast<uint4*>(p.Ap + static_cast<long long>(c) * p.K + k);
+    if (static_cast<void*>(at) != static_cast<void*>(p.sick)) *at = v;
+    return;
   }
+  const int lane = threadIdx.x & 31;
+  const long long n = static_cast<long long>(blockIdx.x - a_blocks) * 8 + (threadIdx.x >> 5);
+  if (n >= p.N) return;   // whole warps
+  uint16_t* row = reinterpret_cast<uint16_t*>(p.Bp) + n * p.Rs;
+  unsigned long long mark = 0;
+  for (int s = 0; s < p.S; ++s) {
+    const int ranks = p.ranks[s], width = p.lo[s + 1] - p.lo[s];
+    const uint16_t* from = reinterpret_cast<const uint16_t*>(p.B) + (static_cast<long long>(s) * p.N + n) * p.R;
+    uint16_t v[kMaxRank / 32];
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < kMaxRank / 32; ++i) {
+      const int c = i * 32 + lane;
+      v[i] = c < ranks ? from[c] : 0;
+      bad |= (v[i] & 0x7f80u) == 0x7f80u;
+    }
+    bad = __any_sync(0xffffffffu, bad);
+    if (bad) mark |= 1ull << s;
+#pragma unroll
+    for (int i = 0; i < kMaxRank / 32; ++i) {
+      const int c = i * 32 + lane;
+      if (bad && (v[i] & 0x7fffu) != 0) {
+        const uint16_t sign = v[i] & 0x8000u, size = v[i] & 0x7fffu;
+        v[i] = size > 0x7f80u ? 0x4040 : size == 0x7f80u ? sign | 0x4000 : sign | 0x3f80;   // 3, +-2, +-1
+      }
+      if (c < width) row[p.lo[s] + c] = v[i];
+    }
+  }
+  for (int c = p.lo[p.S] + lane; c < p.Rs; c += 32) row[c] = 0;
+  __syncwarp();
+  if (lane < kMarkWords) p.marks[n * p.mark_stride + lane] = static_cast<uint16_t>((mark >> (8 * lane)) & 0xffu);
+  if (lane == 0 && mark != 0) atomicOr(p.sick, mark);
 }
 
 }  // namespace
@@ -440,10 +473,11 @@ cudaError_t launch_linear_narrow(const LinearParams& p, int bn, int split, cudaS
 }
 
 cudaError_t launch_linear_pack(const LinearPackParams& p, cudaStream_t stream) {
-  const long long a = static_cast<long long>(p.Rs) * (p.K / 8), b = static_cast<long long>(p.N) * p.Rs;
-  const long long most = a > b ? a : b;
-  const dim3 grid(static_cast<unsigned>((most + 255) / 256), 2);
-  return launch_k(linear_pack_kernel, grid, dim3(256), 0, stream, false, p);
+  const cudaError_t err = cudaMemsetAsync(p.sick, 0, sizeof(*p.sick), stream);
+  if (err != cudaSuccess) return err;
+  const unsigned a = static_cast<unsigned>((static_cast<long long>(p.Rs) * (p.K / 8) + 255) / 256);
+  const unsigned b = static_cast<unsigned>((static_cast<long long>(p.N) + 7) / 8);
+  return launch_k(linear_pack_kernel, dim3(a + b), dim3(256), 0, stream, false, p, a);
 }
 
 }  // namespace mlk

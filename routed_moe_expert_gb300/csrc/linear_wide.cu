@@ -48,6 +48,7 @@
 // bounded as everywhere: a timeout is recorded, raises the CTA's abort flag, and the roles leave.
 #include "common.cuh"
 #include "linear.h"
+#include "linear_nonfinite.cuh"
 
 #include <algorithm>
 #include <atomic>
@@ -378,6 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
       if (any_of_128(bad) && et == 0) *p.status = kDevBadSlot | (kWhereLinear << 8);
       else if (et == 0) *p.status = 0u;
     }
+    const unsigned long long sick = lora ? __ldcg(p.sick) : 0;   // slots with weights that are not finite
     const int quarter = warp & 3;
     uint8_t* box0 = ybuf + (warp - 2) * 2 * kBoxBytes;
     __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y);
@@ -575,6 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
         for (int j = 0; j < 8; ++j)
           *reinterpret_cast<float4*>(box + lane * 128 + ((j ^ (lane & 7)) << 4)) =
               make_float4(f[c + 4 * j], f[c + 4 * j + 1], f[c + 4 * j + 2], f[c + 4 * j + 3]);
+        if (sick != 0) add_nonfinite_to_box<true>(p, sick, box, t, n);
         if (p.y_vec) {
           fence_proxy_async_smem();
           __syncwarp();
@@ -720,6 +723,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
           for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[8 * j + i]);
           *reinterpret_cast<uint4*>(box + lane * 128 + ((j ^ (lane & 7)) << 4)) = pack8(f);
         }
+        if (sick != 0) add_nonfinite_to_box<false>(p, sick, box, t_warp + lane, n);
         if (p.y_vec) {
           fence_proxy_async_smem();
           __syncwarp();
