@@ -485,6 +485,18 @@ MLDEV uint2 pack4(const float (&f)[4]) {
   h[1] = __floats2bfloat162_rn(f[2], f[3]);
   return v;
 }
+// The leading 8 significant bits of each value as a bf16, taken from the value: three calls carry a
+// float32's 24 bits, each rest exact.  (Rounded to nearest, values past the largest bf16 would become
+// infinite.)  An infinity or NaN is its first piece and leaves 0.
+MLDEV uint2 take_leading4(float (&f)[4]) {
+  uint32_t h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    h[i] = __float_as_uint(f[i]) & 0xffff0000u;
+    f[i] = fabsf(f[i]) < INFINITY ? f[i] - __uint_as_float(h[i]) : 0.0f;
+  }
+  return make_uint2((h[0] >> 16) | h[1], (h[2] >> 16) | h[3]);
+}
 
 MLDEV uint32_t ld_acquire_gpu(const uint32_t* p) {
   uint32_t v;

@@ -330,13 +330,11 @@ __global__ void __launch_bounds__(kThreads, 2) linear_cluster_kernel(const __gri
         for (int q = 0; q < 4; ++q) f[q] = (c + q >= lo && c + q < hi) ? sc * f[q] : 0.0f;
       }
       uint8_t* at = u_s + b * BN * 128 + j * 128 + ((((c & 63) >> 3) ^ (j & 7)) << 4) + (c & 7) * 2;
-      for (int piece = 0; piece < p.pieces; ++piece) {   // a float32 as a sum of bf16 pieces
-        const uint2 v = pack4(f);
-        *reinterpret_cast<uint2*>(at + piece * NB * BN * 128) = v;
-        f[0] -= __uint_as_float(v.x << 16);
-        f[1] -= __uint_as_float(v.x & 0xffff0000u);
-        f[2] -= __uint_as_float(v.y << 16);
-        f[3] -= __uint_as_float(v.y & 0xffff0000u);
+      if (p.pieces == 1) {
+        *reinterpret_cast<uint2*>(at) = pack4(f);
+      } else {   // a float32 as a sum of bf16 pieces
+        for (int piece = 0; piece < p.pieces; ++piece)
+          *reinterpret_cast<uint2*>(at + piece * NB * BN * 128) = take_leading4(f);
       }
     }
     fence_proxy_async_smem();

@@ -338,13 +338,10 @@ __global__ void __launch_bounds__(kThreads, 2) linear_narrow_kernel(const __grid
       __nv_bfloat16* u = p.u + static_cast<long long>(t) * p.pieces * p.Rs + n;
 #pragma unroll
       for (int e = 0; e < 4; ++e) f[e] = (n + e >= lo && n + e < hi) ? sc * f[e] : 0.0f;
-      for (int piece = 0; piece < p.pieces; ++piece) {   // the float32 as a sum of bf16 pieces
-        const uint2 v = pack4(f);
-        *reinterpret_cast<uint2*>(u + static_cast<long long>(piece) * p.Rs) = v;
-        f[0] -= __uint_as_float(v.x << 16);
-        f[1] -= __uint_as_float(v.x & 0xffff0000u);
-        f[2] -= __uint_as_float(v.y << 16);
-        f[3] -= __uint_as_float(v.y & 0xffff0000u);
+      if (p.pieces == 1) {
+        *reinterpret_cast<uint2*>(u) = pack4(f);
+      } else {   // the float32 as a sum of bf16 pieces
+        for (int piece = 0; piece < p.pieces; ++piece) *reinterpret_cast<uint2*>(u + piece * p.Rs) = take_leading4(f);
       }
     } else {
       f[0] += bias[i].x;

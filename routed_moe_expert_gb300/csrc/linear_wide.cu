@@ -402,14 +402,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
       for (int j = 0; j < 4; ++j) g[j] = (c + j >= lo && c + j < hi) ? sc * f[j] : 0.0f;
       __nv_bfloat16* u = p.u + static_cast<long long>(t) * (F32 ? kFloatPieces : 1) * p.Rs + c;
 #pragma unroll
-      for (int piece = 0; piece < (F32 ? kFloatPieces : 1); ++piece) {
-        const uint2 v = pack4(g);
-        *reinterpret_cast<uint2*>(u + piece * p.Rs) = v;
-        g[0] -= __uint_as_float(v.x << 16);
-        g[1] -= __uint_as_float(v.x & 0xffff0000u);
-        g[2] -= __uint_as_float(v.y << 16);
-        g[3] -= __uint_as_float(v.y & 0xffff0000u);
-      }
+      for (int piece = 0; piece < (F32 ? kFloatPieces : 1); ++piece)
+        *reinterpret_cast<uint2*>(u + piece * p.Rs) = F32 ? take_leading4(g) : pack4(g);
     };
     // A slice's part sums, [column / 4][token][4] (a warp's stores are 512 bytes in a row).
     auto slice_at = [&](int tile, int quad) -> float4* {
@@ -524,17 +518,13 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
         for (int c = 0; c < 128; c += 8) {
           const int col = nt * sh_cols + c;
           if (c >= sh_cols || col >= p.Rs || t >= p.T) continue;
-          float g[8];
+          float g[2][4];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) g[j] = (col + j >= lo && col + j < hi) ? sc * f[c + j] : 0.0f;
+          for (int j = 0; j < 8; ++j) g[j >> 2][j & 3] = (col + j >= lo && col + j < hi) ? sc * f[c + j] : 0.0f;
 #pragma unroll
           for (int piece = 0; piece < kFloatPieces; ++piece) {
-            const uint4 v = pack8(g);
-            *reinterpret_cast<uint4*>(u + piece * p.Rs + col) = v;
-            float back[8];
-            unpack8(v, back);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) g[j] -= back[j];
+            const uint2 v0 = take_leading4(g[0]), v1 = take_leading4(g[1]);
+            *reinterpret_cast<uint4*>(u + piece * p.Rs + col) = make_uint4(v0.x, v0.y, v1.x, v1.y);
           }
         }
         fence_proxy_async_global();   // read next by other CTAs' TMA copies

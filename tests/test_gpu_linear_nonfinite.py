@@ -108,3 +108,33 @@ def test_many_nonfinite_values_of_one_slot(handle, T, N, K, ranks, f32):
     own = c["slots"].numpy() == 0
     assert np.isnan(got[own]).all()
     assert (np.abs(got - y) <= tol)[~own].all()
+
+
+@pytest.mark.parametrize("f32", [False, True], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("T,N,K", [(3, 136, 128), (100, 264, 512), (777, 1536, 2048), (2500, 2050, 136), (512, 2048, 2048)])
+def test_an_infinite_shrunk_value_keeps_its_sign(handle, T, N, K, f32):
+    """One rank whose A holds an infinity: u is +-infinite, and so is every value of the token's row, by
+    the sign of u and of B; nothing is subtracted from an infinity on the way."""
+    c = _case(T, N, K, (1, 8), T)
+    c["A"][0, 0, 3] = INF
+    got = _run(handle, c, f32)
+    y, tol = _finite_part(c, f32)
+    own = c["slots"].numpy() == 0
+    sign = np.sign(c["scalings"][0] * ref.f64(c["x"])[own, 3])[:, None] * np.sign(ref.f64(c["B"][0, :, 0]))[None]
+    assert (got[own] == sign * INF)[sign != 0].all()
+    assert (np.abs(got - y) <= tol)[~own].all()
+
+
+@pytest.mark.parametrize("T,N,K", [(3, 136, 128), (100, 264, 512), (777, 1536, 2048), (2500, 2050, 136)])
+def test_a_shrunk_value_past_the_largest_bf16_stays_finite_in_float32(handle, T, N, K):
+    """u = 3.4e38 is a float32, but rounds to an infinite bf16; times 2^-40 it is 3.1e26."""
+    c = _case(T, N, K, (1, 8), T)
+    c["A"][0] = 0.0
+    c["A"][0, 0, 3] = 1.0
+    c["x"][:, 3] = 1.0
+    c["B"][0] = 2.0 ** -40
+    c["scalings"][0] = 3.4e38
+    got = _run(handle, c, True)
+    own = c["slots"].numpy() == 0
+    # u is a product of exact values rounded once to 24 bits, in pieces that lose nothing; then one sum
+    np.testing.assert_allclose(got[own], float(np.float32(3.4e38)) * 2.0 ** -40, rtol=2.0 ** -22)
