@@ -78,7 +78,19 @@ struct Tiles {
   int tokens;       // token tile
   int rows;         // weight rows of a tile
   int split;        // CTAs (kWide: pairs) that share a tile's K
+  int accs, acc_steps;   // (kNarrow, kCluster) a CTA's accumulators and the K blocks of each
 };
+// The tensor cores truncate as they accumulate, which adds up over a long K: an accumulator of a
+// float32 result takes at most 1024 of it (on narrow tiles past K 131072, where TMEM has no room for more than
+// 16 accumulators of 16 columns on each of 8 CTAs, a 128th of K).  A bf16 result takes one accumulator.
+constexpr int kAccSteps = 16;
+void set_accumulators(Tiles& c, int nk, bool f32) {
+  const int steps = (nk + c.split - 1) / c.split, room = kLinearTmem / c.tokens;
+  c.accs = f32 ? (steps + kAccSteps - 1) / kAccSteps : 1;
+  if (c.kernel == kNarrow && c.tokens == 16) c.accs = std::min(c.accs, room);
+  c.acc_steps = std::max(kAccSteps, (steps + c.accs - 1) / c.accs);
+}
+bool fits_tmem(const Tiles& c) { return (c.kernel == kCluster ? 2 * c.accs + 1 : c.accs) * c.tokens <= kLinearTmem; }
 
 // Microseconds of a call on each kernel: models fitted to measured calls in a row (T 1 to 2048, N 384
 // to 16384, K 2048 and 7168, adapters of 16 to 512 stacked ranks), good to a microsecond or so and
@@ -196,9 +208,13 @@ double wide_us(int T, int N, int K, int Rs, int rows, int split, int sms) {
 
 Tiles pick_tiles(int T, int N, int K, bool f32, int Rs, int sms) {
   const int nk = (K + 63) / 64;
-  Tiles best = {kNarrow, 16, 128, 1};
+  Tiles best = {};
   double us = 1e30;
-  auto offer = [&](double t, const Tiles& c) {
+  auto offer = [&](double t, Tiles c) {
+    if (c.kernel != kWide) {
+      set_accumulators(c, nk, f32);
+      if (!fits_tmem(c)) return;
+    }
     if (t < us) {
       us = t;
       best = c;
@@ -207,8 +223,7 @@ Tiles pick_tiles(int T, int N, int K, bool f32, int Rs, int sms) {
   for (int bn = 16; bn <= 128; bn *= 2) {
     if (bn > 16 && bn >= 2 * T) break;
     for (int split = 1; split <= kLinearMaxSplit && split <= nk; split *= 2) {
-      // The tensor cores truncate as they accumulate, which adds up over a long K: a float32
-      // result takes at most 1024 of K per accumulator (as far as a cluster goes).
+      // a float32 result's accumulators lie in one CTA each as far as a cluster goes
       if (f32 && nk > 16 * split && split < kLinearMaxSplit && 2 * split <= nk) continue;
       offer(narrow_us(T, N, K, Rs, bn, split, sms), {kNarrow, bn, 128, split});
       if (Rs > 0 && Rs <= 128 && bn <= 32)
@@ -338,6 +353,8 @@ moe_lora_status moe_lora_linear(moe_lora_handle* h, const moe_lora_linear_args* 
   p.slot_idx = active ? a->slot_idx : nullptr;
   p.status = static_cast<uint32_t*>(workspace);
   p.pieces = a->y_f32 ? kFloatPieces : 1;
+  p.accs = c.accs;
+  p.acc_steps = c.acc_steps;
   p.shrink_slices = p.k_slices = 1;
   if (c.kernel == kWide) p.k_slices = c.split;
   const long long x_stride = a->T > 1 ? a->x_stride : a->K, w_stride = a->N > 1 ? a->w_stride : a->K;

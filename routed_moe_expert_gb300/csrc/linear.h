@@ -46,14 +46,13 @@ struct LinearParams {
   int2* flags;           // per token tile: {shrink parts done, product parts past them}, and after
                          // these (slices) {part sums written, unused}; zero between calls
   uint32_t* status;      // written by the first CTA
-  // Weights that are not finite (pack_adapters): slots that have any, the marks of row n at
-  // marks + n * mark_stride (slot s: bit s % 8 of word s / 8), and the stacked B itself, in which a
-  // marked slot's values of that row are classes instead
-  const unsigned long long* sick;
-  const uint16_t* marks;
-  int mark_stride;
-  const __nv_bfloat16* b;
+  const unsigned long long* sick;   // slots with weights that are not finite (linear_nonfinite.cuh)
   LinearSlots slots;
+  // From here on what few calls read.
+  const uint16_t* marks;   // of row n: marks + n * mark_stride; slot s: bit s % 8 of word s / 8
+  int mark_stride;
+  const __nv_bfloat16* b;  // the stacked B, in which a marked slot's values of that row are classes
+  int accs, acc_steps;     // (narrow, cluster) accumulators in TMEM of a CTA's K, and 64-wide blocks of each
 };
 constexpr int kLinearFlags = 8192;   // token tiles of a call with adapters
 constexpr int kLinearMaxSlices = 8;
@@ -62,6 +61,12 @@ constexpr int kLinearMaxSlices = 8;
 // most the number of 64-wide K blocks.  Maps' boxes: {64, 128} of w, a, b, {64, bn} of
 // x and u, {64, shrink_tokens} of xs.
 constexpr int kLinearMaxSplit = 8;
+constexpr int kLinearTmem = 256;     // TMEM columns of a CTA at most: two share an SM's 512
+inline __host__ __device__ unsigned linear_tmem_columns(int accs, int columns) {   // a power of two from 32
+  unsigned n = 32;
+  while (n < static_cast<unsigned>(accs * columns)) n *= 2;
+  return n;
+}
 cudaError_t linear_narrow_setup();   // once per device
 cudaError_t launch_linear_narrow(const LinearParams& p, int bn, int split, cudaStream_t stream);
 

@@ -83,12 +83,12 @@ MLDEV float2 cluster_sum2(uint32_t at) {
   return s;
 }
 
-template <int BN, int NB>
+// LONG: as in linear_narrow.cu.
+template <int BN, int NB, bool LONG>
 __global__ void __launch_bounds__(kThreads, 2) linear_cluster_kernel(const __grid_constant__ LinearParams p) {
   constexpr int kStages = stages_of(BN, NB);
   constexpr uint32_t STAGE = stage_bytes(BN, NB);
   constexpr uint32_t X_AT = kTile + NB * kTile / 2;          // the tokens' part of a stage
-  constexpr uint32_t TMEM_COLS = 4u * BN;                    // W x, As x, delta
   // after the main loop the stages hold part sums [BN][128] of W x and As x, u as an operand
   // [pieces][NB][BN rows x 128 B], and the stacked B's tile (NB blocks of 64 columns)
   constexpr uint32_t PART = BN * 128 * 4;
@@ -112,6 +112,9 @@ __global__ void __launch_bounds__(kThreads, 2) linear_cluster_kernel(const __gri
   int* hi_s = lo_s + BN;                                     // its factor
   float* sc_s = reinterpret_cast<float*>(hi_s + BN);
 
+  // TMEM: the accumulators of W x, those of As x, the delta
+  const uint32_t kaccs = LONG ? p.accs : 1, as_at = kaccs * BN, delta_at = 2 * as_at;
+  const uint32_t tmem_cols = linear_tmem_columns(2 * kaccs + 1, BN);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int C = static_cast<int>(cluster_nctas()), rank = static_cast<int>(cluster_ctarank());
   const int tile = static_cast<int>(blockIdx.x) / C;
@@ -145,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_cluster_kernel(const __gri
     tma_prefetch_desc(&p.tmap_b);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, TMEM_COLS);
+    tmem_alloc(tmem_slot, tmem_cols);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -214,24 +217,31 @@ __global__ void __launch_bounds__(kThreads, 2) linear_cluster_kernel(const __gri
   } else if (warp == 1) {   // ------------------------------------------ MMA issuer
     if (lane == 0) {
       constexpr uint32_t idesc = idesc_bf16_f32(128, BN);
-      int stage = 0;
-      uint32_t phase = 0;
+      int stage = 0, left = p.acc_steps;
+      bool first = true;
+      uint32_t phase = 0, d = tmem_base;
       int ok = mbar_wait(mask_bar, 0, abort_flag, p.status, kWhereLinear);
       const bool shrink = *mask_s != 0u;
       for (int kb = k_lo; ok && kb < k_hi; ++kb) {
         ok = mbar_wait(&full[stage], phase, abort_flag, p.status, kWhereLinear);
         if (!ok) break;
+        if (LONG && left-- == 0) {   // the next accumulators
+          d += BN;
+          first = true;
+          left = p.acc_steps - 1;
+        }
         tc_fence_after();
         const uint32_t a = smem_u32(smem + stage * STAGE);
         const uint64_t wd = sw128_kmajor_desc(a), ad = sw128_kmajor_desc(a + kTile), xd = sw128_kmajor_desc(a + X_AT);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          umma_bf16(tmem_base, wd + 2 * kk, xd + 2 * kk, idesc, (kb > k_lo || kk > 0) ? 1u : 0u);
+          umma_bf16(d, wd + 2 * kk, xd + 2 * kk, idesc, ((LONG ? !first : kb > k_lo) || kk > 0) ? 1u : 0u);
         if (shrink) {   // rows of blocks that were not copied give sums that nothing reads
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            umma_bf16(tmem_base + BN, ad + 2 * kk, xd + 2 * kk, idesc, (kb > k_lo || kk > 0) ? 1u : 0u);
+            umma_bf16(d + as_at, ad + 2 * kk, xd + 2 * kk, idesc, ((LONG ? !first : kb > k_lo) || kk > 0) ? 1u : 0u);
         }
+        first = false;
         umma_commit(&empty[stage]);
         if (++stage == kStages) {
           stage = 0;
@@ -272,6 +282,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_cluster_kernel(const __gri
         mbar_wait_sleep(tfull, 0, abort_flag, p.status, kWhereLinear)) {
       const unsigned mask = *mask_s;
       const bool shrink = mask != 0u;
+      const int accs = LONG ? (k_hi - k_lo - 1) / p.acc_steps + 1 : 1;   // of this CTA
       tc_fence_after();
       // The MMAs are past the stages: B's tile comes in, where tokens of this CTA will use it (a copy
       // that nothing waits for must not outlive the CTA).
@@ -286,8 +297,22 @@ __global__ void __launch_bounds__(kThreads, 2) linear_cluster_kernel(const __gri
         uint32_t v[16], w[16];
         __syncwarp();   // tcgen05.ld is .aligned
         tmem_ld_x16(taddr + c, v);
-        if (shrink) tmem_ld_x16(taddr + BN + c, w);   // (rows past NB * 64: never read)
+        if (shrink) tmem_ld_x16(taddr + as_at + c, w);   // (rows past NB * 64: never read)
         tmem_ld_wait();
+#pragma unroll 1
+        for (int a = 1; a < accs; ++a) {   // accumulators in order
+          uint32_t x[16], y[16];
+          __syncwarp();
+          tmem_ld_x16(taddr + a * BN + c, x);
+          if (shrink) tmem_ld_x16(taddr + as_at + a * BN + c, y);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(x[j]));
+          if (shrink) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(__uint_as_float(w[j]) + __uint_as_float(y[j]));
+          }
+        }
 #pragma unroll
         for (int j = 0; j < 16; ++j) part[(c + j) * 128] = __uint_as_float(v[j]);
         if (shrink) {
@@ -349,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_cluster_kernel(const __gri
           const uint64_t ud = sw128_kmajor_desc(smem_u32(u_s + (piece * NB + b) * BN * 128));
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
-            umma_bf16(tmem_base + 2 * BN, bd + 2 * kk, ud + 2 * kk, idesc, first ? 0u : 1u);
+            umma_bf16(tmem_base + delta_at, bd + 2 * kk, ud + 2 * kk, idesc, first ? 0u : 1u);
             first = 0;
           }
         }
@@ -360,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_cluster_kernel(const __gri
     const int quarter = warp & 3;
     const int row = quarter * 32 + lane, n = row0 + row;
     const float bias = (p.bias != nullptr && n < p.N) ? __ldg(p.bias + n) : 0.0f;
-    const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + 2 * BN;
+    const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + delta_at;
     bool waited = mask == 0u;
 #pragma unroll 1
     for (int c = 0; c < count; c += 8) {   // warp-uniform bound
@@ -405,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_cluster_kernel(const __gri
   cluster_wait();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, TMEM_COLS);
+    tmem_dealloc(tmem_base, tmem_cols);
   }
   if (sick != 0 && mask != 0u)
     add_nonfinite_of_operand<BN, NB>(p, sick, u_s, t0 + j_lo, count, row0 + (warp & 3) * 32 + lane);
@@ -415,24 +440,30 @@ __global__ void __launch_bounds__(kThreads, 2) linear_cluster_kernel(const __gri
 
 cudaError_t linear_cluster_setup() {
   cudaError_t err;
-#define ML_SETUP(BN, NB)                                                                                          \
-  err = cudaFuncSetAttribute(linear_cluster_kernel<BN, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,          \
+#define ML_SETUP(BN, NB, LONG)                                                                                    \
+  err = cudaFuncSetAttribute(linear_cluster_kernel<BN, NB, LONG>, cudaFuncAttributeMaxDynamicSharedMemorySize,    \
                              smem_bytes(BN, NB));                                                                 \
   if (err != cudaSuccess) return err;
-  ML_SETUP(16, 1)
-  ML_SETUP(16, 2)
-  ML_SETUP(32, 1)
-  ML_SETUP(32, 2)
+#define ML_SETUPS(BN, NB) ML_SETUP(BN, NB, false) ML_SETUP(BN, NB, true)
+  ML_SETUPS(16, 1)
+  ML_SETUPS(16, 2)
+  ML_SETUPS(32, 1)
+  ML_SETUPS(32, 2)
+#undef ML_SETUPS
 #undef ML_SETUP
   return cudaSuccess;
 }
 
 cudaError_t launch_linear_cluster(const LinearParams& p, int bn, int split, cudaStream_t stream) {
   const long long tiles = static_cast<long long>((p.N + 127) / 128) * p.token_tiles;
-  if (p.Rs < 1 || p.Rs > 128 || (bn != 16 && bn != 32) || tiles * split > 0x7fffffffLL) return cudaErrorInvalidValue;
+  if (p.Rs < 1 || p.Rs > 128 || (bn != 16 && bn != 32) || tiles * split > 0x7fffffffLL || p.accs < 1 ||
+      (2 * p.accs + 1) * bn > kLinearTmem)
+    return cudaErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(tiles * split)), block(kThreads);
-#define ML_LINEAR(BN, NB) \
-  return launch_kc(linear_cluster_kernel<BN, NB>, grid, block, smem_bytes(BN, NB), stream, true, split, p)
+#define ML_LINEAR(BN, NB)                                                                                             \
+  return p.accs > 1                                                                                                   \
+             ? launch_kc(linear_cluster_kernel<BN, NB, true>, grid, block, smem_bytes(BN, NB), stream, true, split, p) \
+             : launch_kc(linear_cluster_kernel<BN, NB, false>, grid, block, smem_bytes(BN, NB), stream, true, split, p)
   if (p.Rs <= 64) {
     if (bn == 16) ML_LINEAR(16, 1);
     ML_LINEAR(32, 1);

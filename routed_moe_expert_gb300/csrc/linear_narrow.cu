@@ -14,7 +14,8 @@
 // still streams whole weight rows.  A cluster of CTAs shares a tile: each takes a part of K
 // into its own TMEM accumulator, parks the float32 part sums in its shared memory, and the
 // cluster adds them through distributed shared memory in rank order (a fixed order, so results
-// do not vary from run to run), each CTA writing its share of the tile.  That keeps enough
+// do not vary from run to run), each CTA writing its share of the tile.  For a float32 result a part of
+// more than 1024 of K goes to several accumulators: the tensor cores truncate as they accumulate.  That keeps enough
 // CTAs streaming when N alone gives few tiles, in one launch and without global partial sums.
 //
 // The product's tiles stream W and x at once and wait for u (a flag per token tile) only in front
@@ -67,11 +68,12 @@ MLDEV uint32_t cluster_nctas() {
   return r;
 }
 
-template <int BN>
+// LONG: a CTA's part of K takes several accumulators (kernels of their own, also in linear_cluster.cu: the
+// arithmetic for them costs short calls 0.1 to 0.3 us; T 1, N 2048, K 2048, rank 16: 6.0 and 6.2 us).
+template <int BN, bool LONG>
 __global__ void __launch_bounds__(kThreads, 2) linear_narrow_kernel(const __grid_constant__ LinearParams p) {
   constexpr int kStages = stages_of(BN);
   constexpr uint32_t STAGE = stage_bytes(BN);
-  constexpr uint32_t TMEM_COLS = BN <= 32 ? 32u : static_cast<uint32_t>(BN);
   static_assert(kStages * static_cast<int>(STAGE) >= BN * 128 * 4, "the part sums fit the stage buffers");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -87,6 +89,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_narrow_kernel(const __grid
   int* hi_s = lo_s + BN;                               // and its factor
   float* sc_s = reinterpret_cast<float*>(hi_s + BN);
 
+  const uint32_t tmem_cols = linear_tmem_columns(LONG ? p.accs : 1, BN);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int C = static_cast<int>(cluster_nctas()), rank = static_cast<int>(cluster_ctarank());
   const int index = static_cast<int>(blockIdx.x) / C;
@@ -133,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_narrow_kernel(const __grid
     tma_prefetch_desc(shrink ? &p.tmap_xs : &p.tmap_x);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, TMEM_COLS);
+    tmem_alloc(tmem_slot, tmem_cols);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -154,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_narrow_kernel(const __grid
     for (int j = qt * BN + threadIdx.x; j < (qt + 1) * BN && j < p.T; j += kThreads) m |= blocks_of(p.slot_idx[j]);
     if (!__syncthreads_or(((m >> (row0 >> 6)) & 3ull) != 0)) {
       if (threadIdx.x == 0) red_release_add(ready, 1);
-      if (warp == 1) tmem_dealloc(tmem_base, TMEM_COLS);
+      if (warp == 1) tmem_dealloc(tmem_base, tmem_cols);
       return;
     }
   }
@@ -209,8 +212,8 @@ __global__ void __launch_bounds__(kThreads, 2) linear_narrow_kernel(const __grid
   } else if (warp == 1) {   // ------------------------------------------ MMA issuer
     if (lane == 0) {
       const uint32_t idesc = idesc_bf16_f32(128, bn);
-      int stage = 0, ok = 1, first = 1;
-      uint32_t phase = 0;
+      int stage = 0, ok = 1, first = 1, left = p.acc_steps;
+      uint32_t phase = 0, d = tmem_base;
       auto consume = [&]() -> bool {
         if (!mbar_wait(&full[stage], phase, abort_flag, p.status, kWhereLinear)) return false;
         tc_fence_after();
@@ -218,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_narrow_kernel(const __grid
         const uint64_t ad = sw128_kmajor_desc(a), bd = sw128_kmajor_desc(a + kABytes);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
-          umma_bf16(tmem_base, ad + 2 * kk, bd + 2 * kk, idesc, first ? 0u : 1u);
+          umma_bf16(d, ad + 2 * kk, bd + 2 * kk, idesc, first ? 0u : 1u);
           first = 0;
         }
         umma_commit(&empty[stage]);
@@ -228,7 +231,14 @@ __global__ void __launch_bounds__(kThreads, 2) linear_narrow_kernel(const __grid
         }
         return true;
       };
-      for (int kb = k_lo; ok && kb < k_hi; ++kb) ok = consume();
+      for (int kb = k_lo; ok && kb < k_hi; ++kb) {
+        if (LONG && left-- == 0) {   // the next accumulator
+          d += BN;
+          first = 1;
+          left = p.acc_steps - 1;
+        }
+        ok = consume();
+      }
       if (ok && lora) {
         ok = mbar_wait(mask_bar, 0, abort_flag, p.status, kWhereLinear);
         const int n = __popc(mask_s[0]) + __popc(mask_s[1]);
@@ -272,6 +282,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_narrow_kernel(const __grid
     const int quarter = warp & 3;
     const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
     float* part = reinterpret_cast<float*>(smem) + quarter * 32 + lane;   // [BN][128]
+    const int accs = LONG ? (k_hi - k_lo - 1) / p.acc_steps + 1 : 1;   // of this CTA
     if (mbar_wait_sleep(tfull, 0, abort_flag, p.status, kWhereLinear)) {
       tc_fence_after();
 #pragma unroll 1
@@ -280,6 +291,15 @@ __global__ void __launch_bounds__(kThreads, 2) linear_narrow_kernel(const __grid
         __syncwarp();   // tcgen05.ld is .aligned
         tmem_ld_x16(taddr + c, v);
         tmem_ld_wait();
+#pragma unroll 1
+        for (int a = 1; a < accs; ++a) {   // accumulators in order
+          uint32_t w[16];
+          __syncwarp();
+          tmem_ld_x16(taddr + a * BN + c, w);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(w[j]));
+        }
 #pragma unroll
         for (int j = 0; j < 16; ++j) part[(c + j) * 128] = __uint_as_float(v[j]);
       }
@@ -292,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_narrow_kernel(const __grid
   cluster_wait();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, TMEM_COLS);
+    tmem_dealloc(tmem_base, tmem_cols);
   }
 
   // this CTA's share of the tile: quads of 4 rows of a token, part sums added in rank order
@@ -442,14 +462,16 @@ __global__ void __launch_bounds__(256) linear_pack_kernel(const __grid_constant_
 
 cudaError_t linear_narrow_setup() {
   cudaError_t err;
-#define ML_SETUP(BN)                                                                                        \
-  err = cudaFuncSetAttribute(linear_narrow_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,          \
+#define ML_SETUP(BN, LONG)                                                                                  \
+  err = cudaFuncSetAttribute(linear_narrow_kernel<BN, LONG>, cudaFuncAttributeMaxDynamicSharedMemorySize,    \
                              smem_bytes(BN));                                                                \
   if (err != cudaSuccess) return err;
-  ML_SETUP(16)
-  ML_SETUP(32)
-  ML_SETUP(64)
-  ML_SETUP(128)
+#define ML_SETUPS(BN) ML_SETUP(BN, false) ML_SETUP(BN, true)
+  ML_SETUPS(16)
+  ML_SETUPS(32)
+  ML_SETUPS(64)
+  ML_SETUPS(128)
+#undef ML_SETUPS
 #undef ML_SETUP
   return cudaSuccess;
 }
@@ -458,15 +480,19 @@ cudaError_t launch_linear_narrow(const LinearParams& p, int bn, int split, cudaS
   const long long tiles =
       static_cast<long long>((p.N + 127) / 128) * p.token_tiles +
       (p.Rs > 0 ? static_cast<long long>((p.Rs + 127) / 128) * ((p.T + p.shrink_tokens - 1) / p.shrink_tokens) : 0);
-  if (tiles * split > 0x7fffffffLL) return cudaErrorInvalidValue;
+  if (tiles * split > 0x7fffffffLL || p.accs < 1 || p.accs * bn > kLinearTmem) return cudaErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(tiles * split)), block(kThreads);
+#define ML_LINEAR(BN)                                                                                               \
+  return p.accs > 1 ? launch_kc(linear_narrow_kernel<BN, true>, grid, block, smem_bytes(BN), stream, true, split, p) \
+                    : launch_kc(linear_narrow_kernel<BN, false>, grid, block, smem_bytes(BN), stream, true, split, p)
   switch (bn) {
-    case 16: return launch_kc(linear_narrow_kernel<16>, grid, block, smem_bytes(16), stream, true, split, p);
-    case 32: return launch_kc(linear_narrow_kernel<32>, grid, block, smem_bytes(32), stream, true, split, p);
-    case 64: return launch_kc(linear_narrow_kernel<64>, grid, block, smem_bytes(64), stream, true, split, p);
-    case 128: return launch_kc(linear_narrow_kernel<128>, grid, block, smem_bytes(128), stream, true, split, p);
+    case 16: ML_LINEAR(16);
+    case 32: ML_LINEAR(32);
+    case 64: ML_LINEAR(64);
+    case 128: ML_LINEAR(128);
     default: return cudaErrorInvalidValue;
   }
+#undef ML_LINEAR
 }
 
 cudaError_t launch_linear_pack(const LinearPackParams& p, cudaStream_t stream) {
