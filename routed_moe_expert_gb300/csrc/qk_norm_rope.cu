@@ -202,6 +202,10 @@ MLDEV uint4 pack_pairs(const F2 (&f)[4]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+MLDEV long long position_of(const QkParams& p, int t) {
+  return p.pos_i64 ? static_cast<const long long*>(p.positions)[t] : static_cast<const int32_t*>(p.positions)[t];
+}
+
 // The aligned case: a lane's 16 values of a head are two 16-byte pieces.  A round is one head per
 // lane group: 32 / L heads of a token (the rest of a token's last round idle), or, with few heads
 // (`packed`), any 32 / L consecutive (token, head) pairs.  Each warp takes a run of rounds.
@@ -317,8 +321,7 @@ __global__ void __launch_bounds__(256, 3) qk_norm_rope_kernel(const QkParams p) 
       const void* w = is_k ? p.wk : p.wq;
       kind = is_k;
       token = now.t;
-      const long long pos = p.pos_i64 ? static_cast<const long long*>(p.positions)[token]
-                                      : static_cast<const int32_t*>(p.positions)[token];
+      const long long pos = position_of(p, token);
       // angles of the lane's values: half-split, one per pair of pieces; interleaved, four pairs of
       // piece a, then four of piece b.  A bad position: no rotation (and reported)
       float c[8], s[8];
@@ -327,7 +330,9 @@ __global__ void __launch_bounds__(256, 3) qk_norm_rope_kernel(const QkParams p) 
         c[j] = 1.0f;
         s[j] = 0.0f;
       }
-      if (pos >= 0 && pos < p.num_positions) {
+      const bool known = pos >= 0 && pos < p.num_positions;
+      const bool turn_a = known && (INTERLEAVED ? a < p.R : turned), turn_b = known && (INTERLEAVED ? b < p.R : turned);
+      if (known) {
         const float* row = p.table + pos * p.table_t;
         auto angles = [&](int at, float* cp, float* sp, auto count) {
           constexpr int kN = decltype(count)::value;
@@ -348,9 +353,9 @@ __global__ void __launch_bounds__(256, 3) qk_norm_rope_kernel(const QkParams p) 
           }
         };
         if constexpr (INTERLEAVED) {
-          if (a < p.R) angles(a / 2, c, s, std::integral_constant<int, 4>());
-          if (b < p.R) angles(b / 2, c + 4, s + 4, std::integral_constant<int, 4>());
-        } else if (turned) {
+          if (turn_a) angles(a / 2, c, s, std::integral_constant<int, 4>());
+          if (turn_b) angles(b / 2, c + 4, s + 4, std::integral_constant<int, 4>());
+        } else if (turn_a) {
           angles(a, c, s, std::integral_constant<int, 8>());
         }
       }
@@ -371,6 +376,8 @@ __global__ void __launch_bounds__(256, 3) qk_norm_rope_kernel(const QkParams p) 
           sa[j] = pair_of(-wb[u] * s[u], -wb[v] * s[v]);
           sb[j] = pair_of(wa[u] * s[u], wa[v] * s[v]);
         }
+        if (!turn_a) sa[j] = F2{0ull};   // (a partner's weight may be infinite)
+        if (!turn_b) sb[j] = F2{0ull};
       }
     }
     copy_wait<kAhead>();
@@ -386,17 +393,27 @@ __global__ void __launch_bounds__(256, 3) qk_norm_rope_kernel(const QkParams p) 
     for (int off = (LANES > 0 ? LANES : 32) / 2; off > 0; off >>= 1)
       if (LANES > 0 || off < L) ss += __shfl_xor_sync(0xffffffffu, ss, off);
     const float scale = rsqrtf(ss * inv_d + p.eps);
-    if (on) {
-      const F2 scale2 = pair_of(scale, scale);
+    auto put = [&](bool turn_a, bool turn_b) {   // the round's values; a piece that is not turned takes nothing
+      const F2 scale2 = pair_of(scale, scale);   // from its partner
       F2 oa[4], ob[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const F2 pa = INTERLEAVED ? swapped(fa[j]) : fb[j], pb = INTERLEAVED ? swapped(fb[j]) : fa[j];
+        const F2 pa = !turn_a ? F2{0ull} : INTERLEAVED ? swapped(fa[j]) : fb[j];
+        const F2 pb = !turn_b ? F2{0ull} : INTERLEAVED ? swapped(fb[j]) : fa[j];
         oa[j] = mul2(scale2, fma2(pa, sa[j], mul2(fa[j], ca[j])));
         ob[j] = mul2(scale2, fma2(pb, sb[j], mul2(fb[j], cb[j])));
       }
       if (has_a) __stcs(reinterpret_cast<uint4*>(now.out + a), pack_pairs(oa));   // not read back soon
       if (has_b) __stcs(reinterpret_cast<uint4*>(now.out + b), pack_pairs(ob));
+    };
+    // Finite partners of a piece that is not turned have coefficients of 0; in a head with an infinite
+    // value (0 times it is NaN) they are left out.
+    if (on && scale != 0.0f) {
+      put(true, true);
+    } else if (on) {
+      const long long pos = position_of(p, now.t);
+      const bool known = pos >= 0 && pos < p.num_positions;
+      put(known && (INTERLEAVED ? a < p.R : turned), known && (INTERLEAVED ? b < p.R : turned));
     }
   }
 }
