@@ -22,6 +22,7 @@ struct moe_lora_handle {
   uint64_t launches = 0;                  // kernels launched through this handle
   int2* linear_flags = nullptr;            // flags of the projection kernels, zero between calls
   bool linear_ready = false;              // the projection kernels have their shared memory limits
+  int linear_pairs_by_two = 0;            // LinearMachine's, after that
 };
 
 namespace mlk {

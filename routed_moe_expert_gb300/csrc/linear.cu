@@ -149,10 +149,10 @@ struct Shrink {
   int slices;
   long long spread, busiest;
 };
-Shrink deal_shrink(int T, int N, int K, int Rs, int rows, int split, int sms) {
+Shrink deal_shrink(int T, int N, int K, int Rs, int rows, int split, const LinearMachine& m) {
   const long long tt = (T + 255) / 256, prods = tt * ((N + rows - 1) / rows) * split, nk = (K + 63) / 64;
   const long long cols = std::min(Rs, rows), tiles = Rs > 0 ? tt * ((Rs + cols - 1) / cols) : 0;
-  const long long room = linear_wide_pairs(split, sms), waves = (prods + room - 1) / room;
+  const long long room = m.pairs(split), waves = (prods + room - 1) / room;
   if (tiles == 0) return {1, 0, waves * (nk / split)};
   const long long most =   // four K blocks or more each
       Rs > kMaxSlicedRanks ? 1 : std::min<long long>(kLinearMaxSlices, nk / 4);
@@ -194,9 +194,9 @@ Shrink deal_shrink(int T, int N, int K, int Rs, int rows, int split, int sms) {
 // about 4 us, and have less of a main loop to hide the shrink under: T 512, N 4096, K 7168, rank 16:
 // 26.5 us, one pair per tile 35.9; T 512, N 2048, K 2048: 14.8 and 13.4.  (Four pairs, clusters of 8,
 // came out slower everywhere.)
-double wide_us(int T, int N, int K, int Rs, int rows, int split, int sms) {
+double wide_us(int T, int N, int K, int Rs, int rows, int split, const LinearMachine& m) {
   const long long nk = (K + 63) / 64;
-  const Shrink s = deal_shrink(T, N, K, Rs, rows, split, sms);
+  const Shrink s = deal_shrink(T, N, K, Rs, rows, split, m);
   const double steps = static_cast<double>(nk) / split;
   if (split == 2) {   // fits K 2048 to 7168
     const double us = rows == 256 ? 9.2 + 0.26 * steps : 8.0 + 0.235 * steps;
@@ -206,7 +206,7 @@ double wide_us(int T, int N, int K, int Rs, int rows, int split, int sms) {
   return Rs == 0 ? us : us + (s.slices == 1 ? 3.5 : std::max(1.0, 6.0 - 0.16 * steps));
 }
 
-Tiles pick_tiles(int T, int N, int K, bool f32, int Rs, int sms) {
+Tiles pick_tiles(int T, int N, int K, bool f32, int Rs, const LinearMachine& m) {
   const int nk = (K + 63) / 64;
   Tiles best = {};
   double us = 1e30;
@@ -225,17 +225,17 @@ Tiles pick_tiles(int T, int N, int K, bool f32, int Rs, int sms) {
     for (int split = 1; split <= kLinearMaxSplit && split <= nk; split *= 2) {
       // a float32 result's accumulators lie in one CTA each as far as a cluster goes
       if (f32 && nk > 16 * split && split < kLinearMaxSplit && 2 * split <= nk) continue;
-      offer(narrow_us(T, N, K, Rs, bn, split, sms), {kNarrow, bn, 128, split});
+      offer(narrow_us(T, N, K, Rs, bn, split, m.sms), {kNarrow, bn, 128, split});
       if (Rs > 0 && Rs <= 128 && bn <= 32)
-        offer(cluster_us(T, N, K, Rs, bn, split, sms), {kCluster, bn, 128, split});
+        offer(cluster_us(T, N, K, Rs, bn, split, m.sms), {kCluster, bn, 128, split});
     }
   }
   if (T > 128)
     for (int rows = f32 ? 128 : 256; rows >= 128; rows -= 64) {
       const long long tiles = static_cast<long long>((T + 255) / 256) * ((N + rows - 1) / rows);
       for (int split = 1; split <= 2; ++split)
-        if (split == 1 || (rows != 192 && nk >= 16 && 2 * tiles <= linear_wide_pairs(2, sms)))
-          offer(wide_us(T, N, K, Rs, rows, split, sms), {kWide, 256, rows, split});
+        if (split == 1 || (rows != 192 && nk >= 16 && 2 * tiles <= m.pairs(2)))
+          offer(wide_us(T, N, K, Rs, rows, split, m), {kWide, 256, rows, split});
     }
   return best;
 }
@@ -342,12 +342,13 @@ moe_lora_status moe_lora_linear(moe_lora_handle* h, const moe_lora_linear_args* 
   if (active && (a->adapters == nullptr || !aligned16(a->adapters))) return MOE_LORA_ERR_INVALID_ARG;
   if (!h->linear_ready) {
     ML_CUDA(linear_narrow_setup(), "linear setup");
-    ML_CUDA(linear_wide_setup(), "linear setup");
+    ML_CUDA(linear_wide_setup(&h->linear_pairs_by_two), "linear setup");
     ML_CUDA(linear_cluster_setup(), "linear setup");
     h->linear_ready = true;
   }
 
-  const Tiles c = pick_tiles(a->T, a->N, a->K, a->y_f32 != 0, active ? Rs : 0, h->num_sms);
+  const LinearMachine m = {h->num_sms, h->linear_pairs_by_two};
+  const Tiles c = pick_tiles(a->T, a->N, a->K, a->y_f32 != 0, active ? Rs : 0, m);
   p.T = a->T;
   p.K = a->K;
   p.slot_idx = active ? a->slot_idx : nullptr;
@@ -377,7 +378,7 @@ moe_lora_status moe_lora_linear(moe_lora_handle* h, const moe_lora_linear_args* 
     p.u = reinterpret_cast<__nv_bfloat16*>(static_cast<uint8_t*>(workspace) + 256);
     p.flags = h->linear_flags;
     if (wide) {
-      const Shrink s = deal_shrink(a->T, a->N, a->K, Rs, c.rows, c.split, h->num_sms);
+      const Shrink s = deal_shrink(a->T, a->N, a->K, Rs, c.rows, c.split, m);
       p.shrink_slices = s.slices;
       p.shrink_spread = static_cast<int>(s.spread);
     }
@@ -400,7 +401,7 @@ moe_lora_status moe_lora_linear(moe_lora_handle* h, const moe_lora_linear_args* 
     p.y_vec = p.ldy % piece == 0 && a->N % piece == 0 && aligned16(a->y) && p.ldy < kMaxStride;
     if (p.y_vec) ok = ok && tile_map(h, &p.tmap_y, a->y, a->T, a->N, p.ldy, 32, p.y_f32 != 0);
     if (!ok) return MOE_LORA_ERR_INVALID_ARG;
-    ML_LAUNCH(h, launch_linear_wide(p, c.rows, h->num_sms, stream), "linear launch");
+    ML_LAUNCH(h, launch_linear_wide(p, c.rows, m, stream), "linear launch");
   } else {
     p.y_vec = p.ldy % 4 == 0 && (reinterpret_cast<uintptr_t>(a->y) & (p.y_f32 ? 15u : 7u)) == 0;
     if (!ok) return MOE_LORA_ERR_INVALID_ARG;
@@ -410,6 +411,16 @@ moe_lora_status moe_lora_linear(moe_lora_handle* h, const moe_lora_linear_args* 
               "linear launch");
   }
   return MOE_LORA_OK;
+}
+
+// For tests, on the host alone (not part of the interface): the kernel (0 narrow, 1 wide, 2 cluster), token
+// tile, weight rows, split, accumulators and shrink slices that a call takes on such a device.
+void mlk_linear_choice(int T, int N, int K, int y_f32, int Rs, int sms, int pairs_by_two, int32_t* out) {
+  const LinearMachine m = {sms, pairs_by_two};
+  const Tiles c = pick_tiles(T, N, K, y_f32 != 0, Rs, m);
+  const int32_t v[6] = {c.kernel, c.tokens, c.rows, c.split, c.accs,
+                        c.kernel == kWide ? deal_shrink(T, N, K, Rs, c.rows, c.split, m).slices : 1};
+  std::copy(v, v + 6, out);
 }
 
 }  // extern "C"

@@ -75,11 +75,17 @@ cudaError_t launch_linear_narrow(const LinearParams& p, int bn, int split, cudaS
 cudaError_t linear_cluster_setup();
 cudaError_t launch_linear_cluster(const LinearParams& p, int bn, int split, cudaStream_t stream);
 
+// What the choice of tiles goes by of a device: its SMs, and the pairs of SMs that run at one time in
+// clusters of two pairs (which stay within a GPC, so not every SM finds a place in one).
+struct LinearMachine {
+  int sms, pairs_by_two;
+  int pairs(int k_slices) const { return k_slices == 1 || pairs_by_two > sms / 2 ? sms / 2 : pairs_by_two; }
+};
+
 // Tiles of 256 tokens x bn (128, 192 or 256; float32 y: 128) weight rows on CTA pairs.  Maps' boxes: {64, 128}
 // of x and u, {64, bn / 2} of w and b, {64, linear_shrink_cols(Rs, bn) / 2} of a.
-cudaError_t linear_wide_setup();
-int linear_wide_pairs(int k_slices, int sms);   // pairs that run at one time, after the set-up
-cudaError_t launch_linear_wide(const LinearParams& p, int bn, int sms, cudaStream_t stream);
+cudaError_t linear_wide_setup(int* pairs_by_two);
+cudaError_t launch_linear_wide(const LinearParams& p, int bn, const LinearMachine& m, cudaStream_t stream);
 inline __host__ __device__ int linear_shrink_cols(int Rs, int bn) { return Rs < bn ? Rs : bn; }   // per shrink tile
 
 struct LinearPackParams {

@@ -50,9 +50,6 @@
 #include "linear.h"
 #include "linear_nonfinite.cuh"
 
-#include <algorithm>
-#include <atomic>
-
 namespace mlk {
 
 namespace {
@@ -758,11 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
 
 }  // namespace
 
-// Pairs that run at the same time in clusters of two pairs (which stay within a GPC, so not every SM
-// finds a place in one).
-std::atomic<int> g_pairs_by_two = 0;
-
-cudaError_t linear_wide_setup() {
+cudaError_t linear_wide_setup(int* pairs_by_two) {
   cudaError_t err;
 #define ML_SETUP(BN, F32, SLICED)                                                                              \
   err = cudaFuncSetAttribute(linear_wide_kernel<BN, F32, SLICED>, cudaFuncAttributeMaxDynamicSharedMemorySize, \
@@ -787,19 +780,15 @@ cudaError_t linear_wide_setup() {
   cfg.numAttrs = 1;
   int n = 0;
   err = cudaOccupancyMaxActiveClusters(&n, linear_wide_kernel<256, false, true>, &cfg);
-  g_pairs_by_two = 2 * n;
+  *pairs_by_two = 2 * n;
   return err;
 }
 
-int linear_wide_pairs(int k_slices, int sms) {
-  return k_slices == 1 ? sms / 2 : std::min(sms / 2, g_pairs_by_two.load());
-}
-
-cudaError_t launch_linear_wide(const LinearParams& p, int bn, int sms, cudaStream_t stream) {
+cudaError_t launch_linear_wide(const LinearParams& p, int bn, const LinearMachine& m, cudaStream_t stream) {
   const int cols = linear_shrink_cols(p.Rs, bn);
   const long long shrinks = cols ? (p.Rs + cols - 1) / cols * p.shrink_slices : 0;
   const long long tiles = ((p.N + bn - 1) / bn * p.k_slices + shrinks) * p.token_tiles;
-  const int room = linear_wide_pairs(p.k_slices, sms);
+  const int room = m.pairs(p.k_slices);
   if (p.shrink_slices > 1 && 2 * p.token_tiles > kLinearFlags) return cudaErrorInvalidValue;
   // halves of a product store whole boxes of columns each, and are their pairs' only product tiles
   const int ks = p.k_slices;
