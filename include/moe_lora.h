@@ -440,6 +440,7 @@ moe_lora_status moe_lora_route_noalloc(const moe_lora_bf16* router_logits, const
  * general form, a projection with per-token adapters beside it, and the norm of query and key
  * heads with the position rotation.  They follow the conventions above except where a struct
  * gives strides (in elements) and alignments of its own.  Forward only, as the layer itself.
+ * They run on the handle's device, whichever is current, and all pointers are that device's.
  * ------------------------------------------------------------------------------------- */
 
 /* Scores and group scores of moe_lora_select_experts. */
@@ -562,6 +563,9 @@ moe_lora_status moe_lora_qk_norm_rope(moe_lora_handle* h, const moe_lora_qk_args
    forward or routed forward adds the kernels it enqueued; a memset is not counted).  For
    measurement; the pages have no counterpart.  Host-only.  Errors: INVALID_ARG. */
 moe_lora_status moe_lora_launch_count(const moe_lora_handle* h, uint64_t* count);
+
+/* The device that `h` was created on.  Host-only.  Errors: INVALID_ARG. */
+moe_lora_status moe_lora_device(const moe_lora_handle* h, int* device);
 
 /* Synchronizes `stream`, then reads the device status word the last route/forward on this
    workspace left: MOE_LORA_OK, MOE_LORA_ERR_TIMEOUT or MOE_LORA_ERR_DEVICE_CHECK.

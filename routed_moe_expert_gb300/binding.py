@@ -43,7 +43,7 @@ NUM_STAGES = len(STAGES)
 EXPORTED = ["moe_lora_create", "moe_lora_destroy", "moe_lora_status_string", "moe_lora_last_cuda_error",
             "moe_lora_workspace_size", "moe_lora_validate", "moe_lora_route", "moe_lora_permute",
             "moe_lora_forward", "moe_lora_check_status", "moe_lora_route_noalloc", "moe_lora_forward_routed",
-            "moe_lora_launch_count", "moe_lora_forward_fp8", "moe_lora_quant_fp8", "moe_lora_grouped_gemm_fp8",
+            "moe_lora_launch_count", "moe_lora_device", "moe_lora_forward_fp8", "moe_lora_quant_fp8", "moe_lora_grouped_gemm_fp8",
             "moe_lora_forward_nvfp4", "moe_lora_quant_nvfp4", "moe_lora_grouped_gemm_nvfp4",
             "moe_lora_packed_lora_b_size", "moe_lora_pack_lora_b", "moe_lora_packed_lora_a_size",
             "moe_lora_pack_lora_a", "moe_lora_select_experts", "moe_lora_qk_norm_rope",
@@ -126,6 +126,7 @@ def lib() -> ctypes.CDLL:
     L.moe_lora_forward.argtypes = [c_void_p, ctypes.POINTER(Args), c_void_p, c_void_p, c_size_t, c_void_p]
     L.moe_lora_check_status.argtypes = [c_void_p, c_void_p, ctypes.POINTER(ctypes.c_uint32)]
     L.moe_lora_launch_count.argtypes = [c_void_p, ctypes.POINTER(ctypes.c_uint64)]
+    L.moe_lora_device.argtypes = [c_void_p, ctypes.POINTER(c_int)]
     L.moe_lora_forward_routed.argtypes = [c_void_p, ctypes.POINTER(Args), ctypes.POINTER(Routed), c_void_p, c_void_p,
                                           c_size_t, c_void_p]
     L.moe_lora_forward_fp8.argtypes = [c_void_p, ctypes.POINTER(Args), ctypes.POINTER(Fp8Weights), c_void_p,
@@ -754,7 +755,8 @@ def _native():
         spec.loader.exec_module(m)
         L = lib()
         m.entry_points(*(ctypes.cast(getattr(L, n), c_void_p).value for n in (
-            "moe_lora_select_experts", "moe_lora_linear", "moe_lora_linear_workspace_size", "moe_lora_qk_norm_rope")))
+            "moe_lora_select_experts", "moe_lora_linear", "moe_lora_linear_workspace_size", "moe_lora_qk_norm_rope",
+            "moe_lora_device")))
         _marshal = m
     return _marshal
 
@@ -801,6 +803,8 @@ def moe_lora_linear_adapters(handle: Handle, A: torch.Tensor, B: torch.Tensor, r
             B.shape[0] != S or B.shape[2] != R):
         raise ValueError(f"B must be a dense bf16 [{S}, N, {R}] tensor on {A.device}, got {B.dtype} {tuple(B.shape)} on "
                          f"{B.device}")
+    if A.device.index != handle.device:
+        raise ValueError(f"A and B are on {A.device}, the handle is on cuda:{handle.device}")
     N = B.shape[1]
     if len(ranks) != S or len(scalings) != S:
         raise ValueError(f"need {S} ranks and scalings, got {len(ranks)} and {len(scalings)}")

@@ -32,6 +32,7 @@ decltype(&moe_lora_select_experts) g_select = nullptr;
 decltype(&moe_lora_linear) g_linear = nullptr;
 decltype(&moe_lora_linear_workspace_size) g_linear_workspace = nullptr;
 decltype(&moe_lora_qk_norm_rope) g_qk = nullptr;
+decltype(&moe_lora_device) g_device = nullptr;
 
 struct Refused {};   // a Python exception is set
 
@@ -105,10 +106,15 @@ moe_lora_stream stream_of(PyObject* o, at::Device dev) {
   if (p == nullptr && PyErr_Occurred()) throw Refused();
   return static_cast<moe_lora_stream>(p);
 }
-moe_lora_handle* handle_of(PyObject* o) {
+// The handle of a call on tensors of `dev` (null: a closed one, which the C call refuses).
+moe_lora_handle* handle_of(PyObject* o, at::Device dev) {
   void* p = PyLong_AsVoidPtr(o);
   if (p == nullptr && PyErr_Occurred()) throw Refused();
-  return static_cast<moe_lora_handle*>(p);
+  moe_lora_handle* h = static_cast<moe_lora_handle*>(p);
+  int own = 0;
+  if (g_device(h, &own) == MOE_LORA_OK && own != dev.index())
+    refuse("the tensors are" + on(dev) + ", the handle is on cuda:" + std::to_string(own));
+  return h;
 }
 // (at::empty would come to the same through PyTorch's dispatcher)
 Tensor allocate(at::IntArrayRef sizes, ScalarType type, at::Device dev) {
@@ -182,6 +188,7 @@ PyObject* select_experts(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (z.dim() != 2 || !z.is_cuda() || (type != ScalarType::Float && type != ScalarType::BFloat16))
       refuse(z, "logits", "a bf16 or float32 CUDA tensor [T, E]");
     const at::Device dev = z.device();
+    moe_lora_handle* h = handle_of(a[0], dev);
     const int64_t T = z.size(0), E = z.size(1), row = rows_of(z, "logits");
     moe_lora_select_args p;
     p.logits = z.data_ptr();
@@ -230,7 +237,7 @@ PyObject* select_experts(PyObject*, PyObject* const* a, Py_ssize_t n) {
       p.topk_ids = static_cast<int32_t*>(output(kIds, ScalarType::Int, "topk_ids", true));
       p.topk_weights = static_cast<float*>(output(kWeights, ScalarType::Float, "topk_weights", true));
       p.packed_topk_ids = static_cast<int32_t*>(output(kPacked, ScalarType::Int, "packed_topk_ids", packed));
-      st = g_select(handle_of(a[0]), &p, stream_of(a[12], dev));
+      st = g_select(h, &p, stream_of(a[12], dev));
     } catch (...) {
       Py_DECREF(o);
       throw;
@@ -292,6 +299,7 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (x.dim() != 2 || !x.is_cuda() || x.scalar_type() != ScalarType::BFloat16)
       refuse(x, "x", "a bf16 CUDA tensor [T, K]");
     const at::Device dev = x.device();
+    moe_lora_handle* h = handle_of(a[0], dev);
     const int64_t T = x.size(0), K = x.size(1);
     const Tensor& w = tensor(a[2], "w");
     if (w.dim() != 2 || w.scalar_type() != ScalarType::BFloat16 || w.device() != dev || w.size(1) != K)
@@ -354,7 +362,7 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     used_on(made, a[9], dev);
     used_on(scratch, a[9], dev);
-    const int st = g_linear(handle_of(a[0]), &p, ws->data_ptr(), static_cast<size_t>(ws->numel()), stream_of(a[9], dev));
+    const int st = g_linear(h, &p, ws->data_ptr(), static_cast<size_t>(ws->numel()), stream_of(a[9], dev));
     if (st != 0) return PyLong_FromLong(st);
     if (a[6] == Py_None) return THPVariable_Wrap(std::move(made));
     Py_INCREF(a[6]);
@@ -379,6 +387,7 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor& q = tensor(a[1], "q");
     if (q.dim() != 3 || !q.is_cuda()) refuse(q, "q", "a bf16 CUDA tensor [T, heads, D]");
     const at::Device dev = q.device();
+    moe_lora_handle* h = handle_of(a[0], dev);
     const int64_t T = q.size(0), Hq = q.size(1), D = q.size(2);
     heads(a[1], T, Hq, D, dev, "q");
     const Tensor& k = heads(a[2], T, -1, D, dev, "k");
@@ -437,7 +446,7 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
       ws_bytes = static_cast<size_t>(t.numel());
     }
     for (const Tensor& t : made) used_on(t, a[12], dev);
-    const int st = g_qk(handle_of(a[0]), &p, ws, ws_bytes, stream_of(a[12], dev));
+    const int st = g_qk(h, &p, ws, ws_bytes, stream_of(a[12], dev));
     if (st != 0) return PyLong_FromLong(st);
     PyObject* r = PyTuple_New(2);
     if (r == nullptr) throw Refused();
@@ -455,17 +464,18 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// (addresses of select_experts, linear, linear_workspace_size, qk_norm_rope)
+// (addresses of select_experts, linear, linear_workspace_size, qk_norm_rope, device)
 PyObject* entry_points(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
-    need_args(n, 4);
-    void* at[4];
-    for (int i = 0; i < 4; ++i)
+    need_args(n, 5);
+    void* at[5];
+    for (int i = 0; i < 5; ++i)
       if ((at[i] = PyLong_AsVoidPtr(a[i])) == nullptr) refuse("an entry point is missing");
     g_select = reinterpret_cast<decltype(g_select)>(at[0]);
     g_linear = reinterpret_cast<decltype(g_linear)>(at[1]);
     g_linear_workspace = reinterpret_cast<decltype(g_linear_workspace)>(at[2]);
     g_qk = reinterpret_cast<decltype(g_qk)>(at[3]);
+    g_device = reinterpret_cast<decltype(g_device)>(at[4]);
     Py_RETURN_NONE;
   });
 }

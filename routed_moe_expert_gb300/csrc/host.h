@@ -30,6 +30,28 @@ namespace mlk {
 // Records `err` as the calling thread's last CUDA error and returns MOE_LORA_ERR_CUDA.
 moe_lora_status cuda_fail(cudaError_t err, const char* what);
 
+// Makes the handle's device current for a call, and the caller's again after it.
+class OnDevice {
+ public:
+  explicit OnDevice(const moe_lora_handle* h) {
+    err_ = cudaGetDevice(&before_);
+    if (err_ != cudaSuccess || before_ == h->device) return;
+    err_ = cudaSetDevice(h->device);
+    set_ = err_ == cudaSuccess;
+  }
+  ~OnDevice() {
+    if (set_) cudaSetDevice(before_);
+  }
+  OnDevice(const OnDevice&) = delete;
+  OnDevice& operator=(const OnDevice&) = delete;
+  cudaError_t error() const { return err_; }
+
+ private:
+  int before_ = 0;
+  bool set_ = false;
+  cudaError_t err_ = cudaSuccess;
+};
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 inline bool aligned2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
@@ -41,6 +63,11 @@ inline bool aligned2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1
     cudaError_t _e = (call);                                 \
     if (_e != cudaSuccess) return mlk::cuda_fail(_e, what);  \
   } while (0)
+
+// From here to the end of the call on the handle's device.
+#define ML_ON_DEVICE(h)              \
+  const mlk::OnDevice on_device(h);  \
+  ML_CUDA(on_device.error(), "cudaSetDevice")
 
 // A launch of one of this library's kernels, counted on the handle (moe_lora_launch_count).
 #define ML_LAUNCH(h, call, what)                    \

@@ -286,6 +286,7 @@ moe_lora_status moe_lora_linear_pack_adapters(moe_lora_handle* h, const moe_lora
   p.R = R;
   if (static_cast<long long>(p.Rs) * (K / 8) > 128LL * 0x7fffffff)   // 2^30 blocks for As, 2^28 for Bs at most
     return MOE_LORA_ERR_INVALID_ARG;
+  ML_ON_DEVICE(h);
   ML_LAUNCH(h, launch_linear_pack(p, stream), "linear pack launch");
   return MOE_LORA_OK;
 }
@@ -340,6 +341,7 @@ moe_lora_status moe_lora_linear(moe_lora_handle* h, const moe_lora_linear_args* 
   const size_t need = 256 + (active ? u_bytes(a->T, Rs) + part_bytes(a->T, Rs) : 0);
   if (workspace_bytes < need) return MOE_LORA_ERR_WORKSPACE_TOO_SMALL;
   if (active && (a->adapters == nullptr || !aligned16(a->adapters))) return MOE_LORA_ERR_INVALID_ARG;
+  ML_ON_DEVICE(h);
   if (!h->linear_ready) {
     ML_CUDA(linear_narrow_setup(), "linear setup");
     ML_CUDA(linear_wide_setup(&h->linear_pairs_by_two), "linear setup");

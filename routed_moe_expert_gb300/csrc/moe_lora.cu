@@ -1621,6 +1621,12 @@ moe_lora_status moe_lora_grouped_gemm_nvfp4(moe_lora_handle* h, const uint8_t* w
                             false);
 }
 
+moe_lora_status moe_lora_device(const moe_lora_handle* h, int* device) {
+  if (h == nullptr || device == nullptr) return MOE_LORA_ERR_INVALID_ARG;
+  *device = h->device;
+  return MOE_LORA_OK;
+}
+
 moe_lora_status moe_lora_launch_count(const moe_lora_handle* h, uint64_t* count) {
   if (h == nullptr || count == nullptr) return MOE_LORA_ERR_INVALID_ARG;
   *count = h->launches;

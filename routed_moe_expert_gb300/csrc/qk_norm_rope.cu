@@ -621,6 +621,7 @@ extern "C" moe_lora_status moe_lora_qk_norm_rope(moe_lora_handle* h, const moe_l
   const long long blocks = (warps * 32 + block - 1) / block + 1;   // and the positions' check
   if (blocks > 0x7fffffffLL) return MOE_LORA_ERR_INVALID_ARG;
   const dim3 grid(static_cast<unsigned>(blocks)), threads(block);
+  ML_ON_DEVICE(h);
   cudaError_t err;
   switch (V) {
     case 8:

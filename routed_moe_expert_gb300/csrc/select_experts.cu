@@ -584,6 +584,7 @@ extern "C" moe_lora_status moe_lora_select_experts(moe_lora_handle* h, const moe
   // four experts per load when rows divide into aligned quads
   const bool vec = a->E % 4 == 0 && a->logits_stride % 4 == 0 &&
                    (at & (a->logits_f32 ? 15u : 7u)) == 0;
+  ML_ON_DEVICE(h);
   ML_LAUNCH(h, a->logits_f32 ? launch_select<float>(p, vec, stream) : launch_select<__nv_bfloat16>(p, vec, stream),
             "select_experts launch");
   return MOE_LORA_OK;
