@@ -364,21 +364,26 @@ __global__ void __launch_bounds__(kThreads, 2) linear_cluster_kernel(const __gri
     }
     fence_proxy_async_smem();
     __syncthreads();
-    if (warp == 1 && lane == 0 && mbar_wait(bfull, 0, abort_flag, p.status, kWhereLinear)) {
-      const uint32_t idesc = idesc_bf16_f32(128, (count + 15) / 16 * 16);
-      int first = 1;
-      for (int piece = 0; piece < p.pieces; ++piece)
-        for (int b = 0; b < NB; ++b) {
-          if (!((mask >> b) & 1u)) continue;
-          const uint64_t bd = sw128_kmajor_desc(smem_u32(b_s + b * kTile));
-          const uint64_t ud = sw128_kmajor_desc(smem_u32(u_s + (piece * NB + b) * BN * 128));
+    if (warp == 1 && lane == 0) {
+      if (mbar_wait(bfull, 0, abort_flag, p.status, kWhereLinear)) {
+        const uint32_t idesc = idesc_bf16_f32(128, (count + 15) / 16 * 16);
+        int first = 1;
+        for (int piece = 0; piece < p.pieces; ++piece)
+          for (int b = 0; b < NB; ++b) {
+            if (!((mask >> b) & 1u)) continue;
+            const uint64_t bd = sw128_kmajor_desc(smem_u32(b_s + b * kTile));
+            const uint64_t ud = sw128_kmajor_desc(smem_u32(u_s + (piece * NB + b) * BN * 128));
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            umma_bf16(tmem_base + delta_at, bd + 2 * kk, ud + 2 * kk, idesc, first ? 0u : 1u);
-            first = 0;
+            for (int kk = 0; kk < 4; ++kk) {
+              umma_bf16(tmem_base + delta_at, bd + 2 * kk, ud + 2 * kk, idesc, first ? 0u : 1u);
+              first = 0;
+            }
           }
-        }
-      umma_commit(dfull);
+        umma_commit(dfull);
+        mbar_wait_drain(dfull, 0);   // also where the epilogue has given up: nothing is freed under the MMAs
+      } else {
+        mbar_wait_drain(bfull, 0);   // given up: B's tile may be on its way, and lands before the CTA leaves
+      }
     }
   }
   if (count > 0 && warp >= 2) {   // a thread per weight row: sums in rank order, delta, bias
