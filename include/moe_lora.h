@@ -475,7 +475,7 @@ typedef struct {
    left the rest are the lowest ids of these, with weight 0 (a token whose experts are all ruled
    out gets ids 0..top_k-1 with weights 0).  +inf counts as the largest finite value.
    logits aligned to their type.  One launch, no workspace.
-   Errors: INVALID_ARG, UNSUPPORTED (n_group > 32), CUDA. */
+   Errors: INVALID_ARG, UNSUPPORTED (n_group > 32, T above 2^31 - 256), CUDA. */
 moe_lora_status moe_lora_select_experts(moe_lora_handle* h, const moe_lora_select_args* a, moe_lora_stream stream);
 
 /* Stacked copy of the adapters of one projection: A [S, R, K] and B [S, N, R] (bf16, dense, A
@@ -523,7 +523,7 @@ moe_lora_status moe_lora_linear_workspace_size(int T, int S, const int32_t* h_ra
    themselves only delay it, two such calls (of two handles) on streams of different priority can
    hold each other up until their waits end.
    Errors: INVALID_ARG, UNSUPPORTED (more than 4096 stacked ranks; adapters on more than 2^20
-   tokens), WORKSPACE_TOO_SMALL, CUDA. */
+   tokens; T, N or K above 2^31 - 256), WORKSPACE_TOO_SMALL, CUDA. */
 moe_lora_status moe_lora_linear(moe_lora_handle* h, const moe_lora_linear_args* a, void* workspace,
                                 size_t workspace_bytes, moe_lora_stream stream);
 
@@ -555,7 +555,7 @@ typedef struct {
    pieces are the fast case.  `workspace` (optional, 4 bytes): its first word is the status that
    moe_lora_check_status reads: DEVICE_CHECK when a position lies outside [0, num_positions)
    (those tokens are normed and not rotated).  One launch.
-   Errors: INVALID_ARG, UNSUPPORTED (head_dim > 512), WORKSPACE_TOO_SMALL, CUDA. */
+   Errors: INVALID_ARG, UNSUPPORTED (head_dim > 512, T above 2^31 - 256), WORKSPACE_TOO_SMALL, CUDA. */
 moe_lora_status moe_lora_qk_norm_rope(moe_lora_handle* h, const moe_lora_qk_args* a, void* workspace,
                                       size_t workspace_bytes, moe_lora_stream stream);
 

@@ -52,6 +52,9 @@ class OnDevice {
   cudaError_t err_ = cudaSuccess;
 };
 
+// Tokens, rows and columns that the operators around the layer take: indices of whole tiles stay in 32 bits.
+constexpr int kMaxExtent = 0x7fffffff - 255;
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 inline bool aligned2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }

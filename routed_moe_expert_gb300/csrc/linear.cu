@@ -221,7 +221,7 @@ Tiles pick_tiles(int T, int N, int K, bool f32, int Rs, const LinearMachine& m) 
     }
   };
   for (int bn = 16; bn <= 128; bn *= 2) {
-    if (bn > 16 && bn >= 2 * T) break;
+    if (bn > 16 && bn / 2 >= T) break;
     for (int split = 1; split <= kLinearMaxSplit && split <= nk; split *= 2) {
       // a float32 result's accumulators lie in one CTA each as far as a cluster goes
       if (f32 && nk > 16 * split && split < kLinearMaxSplit && 2 * split <= nk) continue;
@@ -246,6 +246,7 @@ extern "C" {
 
 moe_lora_status moe_lora_linear_adapters_size(int S, int N, int K, const int32_t* h_ranks, size_t* bytes) {
   if (bytes == nullptr || S < 1 || N < 1 || K < 8 || K % 8 != 0) return MOE_LORA_ERR_INVALID_ARG;
+  if (N > kMaxExtent || K > kMaxExtent) return MOE_LORA_ERR_UNSUPPORTED;
   const moe_lora_status st = check_ranks(S, h_ranks, kMaxRank);
   if (st != MOE_LORA_OK) return st;
   int lo[kMaxSlots + 1];
@@ -293,6 +294,7 @@ moe_lora_status moe_lora_linear_pack_adapters(moe_lora_handle* h, const moe_lora
 
 moe_lora_status moe_lora_linear_workspace_size(int T, int S, const int32_t* h_ranks, size_t* bytes) {
   if (bytes == nullptr || T < 0) return MOE_LORA_ERR_INVALID_ARG;
+  if (T > kMaxExtent) return MOE_LORA_ERR_UNSUPPORTED;
   const moe_lora_status st = check_ranks(S, h_ranks, kMaxRank);
   if (st != MOE_LORA_OK) return st;
   int lo[kMaxSlots + 1];
@@ -305,6 +307,7 @@ moe_lora_status moe_lora_linear(moe_lora_handle* h, const moe_lora_linear_args* 
                                 size_t workspace_bytes, moe_lora_stream stream) {
   if (h == nullptr || a == nullptr) return MOE_LORA_ERR_INVALID_ARG;
   if (a->T < 0 || a->N < 1 || a->K < 8 || a->K % 8 != 0) return MOE_LORA_ERR_INVALID_ARG;
+  if (a->T > kMaxExtent || a->N > kMaxExtent || a->K > kMaxExtent) return MOE_LORA_ERR_UNSUPPORTED;
   moe_lora_status st = check_ranks(a->S, a->h_ranks, kMaxRank);
   if (st != MOE_LORA_OK) return st;
   if (a->S > 0) {

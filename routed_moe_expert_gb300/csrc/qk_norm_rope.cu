@@ -530,11 +530,12 @@ extern "C" moe_lora_status moe_lora_qk_norm_rope(moe_lora_handle* h, const moe_l
                                                  size_t workspace_bytes, moe_lora_stream stream) {
   using namespace mlk;
   if (h == nullptr || a == nullptr) return MOE_LORA_ERR_INVALID_ARG;
-  const int H = a->q_heads + a->k_heads;
-  if (a->T < 0 || a->q_heads < 0 || a->k_heads < 0 || H < 1 || H > 65536 || a->head_dim < 1 || a->rotary_dim < 0 ||
+  const long long heads = static_cast<long long>(a->q_heads) + a->k_heads;
+  if (a->T < 0 || a->q_heads < 0 || a->k_heads < 0 || heads < 1 || heads > 65536 || a->head_dim < 1 || a->rotary_dim < 0 ||
       a->rotary_dim > a->head_dim || a->rotary_dim % 2 != 0 || a->num_positions < 0)
     return MOE_LORA_ERR_INVALID_ARG;
-  if (a->head_dim > 512) return MOE_LORA_ERR_UNSUPPORTED;
+  if (a->head_dim > 512 || a->T > kMaxExtent) return MOE_LORA_ERR_UNSUPPORTED;
+  const int H = static_cast<int>(heads);
   if (!(a->eps >= 0.0f)) return MOE_LORA_ERR_INVALID_ARG;
   if (a->T == 0) return MOE_LORA_OK;
   if ((a->q_heads > 0 && (a->q == nullptr || a->q_out == nullptr || a->q_weight == nullptr)) ||

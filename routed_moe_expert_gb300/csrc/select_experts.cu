@@ -548,7 +548,7 @@ extern "C" moe_lora_status moe_lora_select_experts(moe_lora_handle* h, const moe
   if (a->group_score != MOE_LORA_GROUP_MAX && a->group_score != MOE_LORA_GROUP_TOP2) return MOE_LORA_ERR_INVALID_ARG;
   if (a->n_group < 1 || a->topk_group < 1 || a->topk_group > a->n_group || a->E % a->n_group != 0)
     return MOE_LORA_ERR_INVALID_ARG;
-  if (a->n_group > kSelectMaxGroups) return MOE_LORA_ERR_UNSUPPORTED;
+  if (a->n_group > kSelectMaxGroups || a->T > kMaxExtent) return MOE_LORA_ERR_UNSUPPORTED;
   const int group_size = a->E / a->n_group;
   if (a->top_k > a->topk_group * group_size) return MOE_LORA_ERR_INVALID_ARG;
   if (a->n_group > 1 && a->group_score == MOE_LORA_GROUP_TOP2 && group_size < 2) return MOE_LORA_ERR_INVALID_ARG;
