@@ -507,7 +507,8 @@ typedef struct {
   int y_f32;
 } moe_lora_linear_args;
 
-/* Host-only: bytes of workspace that moe_lora_linear needs at most for T tokens. */
+/* Host-only: bytes of workspace that are enough for moe_lora_linear on up to T tokens, with these ranks or
+   any whose stack (each rank rounded up to 8, then all to 64) is no wider: never less for more tokens or ranks. */
 moe_lora_status moe_lora_linear_workspace_size(int T, int S, const int32_t* h_ranks, size_t* bytes);
 
 /* A shared projection with per-token adapters beside it:

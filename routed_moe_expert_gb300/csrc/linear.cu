@@ -55,10 +55,15 @@ constexpr int kMaxSlicedRanks = 128, kMaxSliced = 80, kDealtSlices = 3, kDealtTi
 
 // Bytes of u, and of the slices' part sums behind it.
 size_t u_bytes(int T, int Rs) { return align256(static_cast<size_t>(T) * Rs * kFloatPieces * 2); }
-size_t part_bytes(int T, int Rs) {
-  const int tt = T / 256 + (T % 256 != 0);
-  if (T <= 128 || tt > kDealtTiles || Rs > kMaxSlicedRanks) return 0;
-  return static_cast<size_t>(std::max(std::min(kMaxSliced, kLinearMaxSlices * tt), kDealtSlices * tt)) * Rs * 1024;
+size_t part_bytes(int T, int Rs, int slices) {
+  return slices == 1 ? 0 : static_cast<size_t>((T + 255) / 256) * slices * Rs * 1024;
+}
+// The most part sums of any call on up to T tokens with up to Rs stacked columns, so that what one size
+// of call needs is enough for every smaller one.
+size_t most_part_bytes(int T, int Rs) {
+  const long long tt = T <= 128 ? 0 : std::min<long long>(T / 256 + (T % 256 != 0), kDealtTiles);
+  const long long tiles = std::max(std::min<long long>(kMaxSliced, kLinearMaxSlices * tt), kDealtSlices * tt);
+  return static_cast<size_t>(tiles) * std::min(Rs, kMaxSlicedRanks) * 1024;
 }
 
 bool tile_map(const moe_lora_handle* h, CUtensorMap* m, const void* base, long long rows, long long cols,
@@ -299,7 +304,7 @@ moe_lora_status moe_lora_linear_workspace_size(int T, int S, const int32_t* h_ra
   if (st != MOE_LORA_OK) return st;
   int lo[kMaxSlots + 1];
   const int Rs = stacked_ranks(h_ranks, S, lo);
-  *bytes = 256 + u_bytes(T, Rs) + part_bytes(T, Rs);
+  *bytes = 256 + u_bytes(T, Rs) + most_part_bytes(T, Rs);
   return MOE_LORA_OK;
 }
 
@@ -341,7 +346,7 @@ moe_lora_status moe_lora_linear(moe_lora_handle* h, const moe_lora_linear_args* 
       active = true;
     }
   }
-  const size_t need = 256 + (active ? u_bytes(a->T, Rs) + part_bytes(a->T, Rs) : 0);
+  const size_t need = 256 + (active ? u_bytes(a->T, Rs) : 0);   // and the part sums of a sliced shrink
   if (workspace_bytes < need) return MOE_LORA_ERR_WORKSPACE_TOO_SMALL;
   if (active && (a->adapters == nullptr || !aligned16(a->adapters))) return MOE_LORA_ERR_INVALID_ARG;
   ML_ON_DEVICE(h);
@@ -386,6 +391,7 @@ moe_lora_status moe_lora_linear(moe_lora_handle* h, const moe_lora_linear_args* 
       const Shrink s = deal_shrink(a->T, a->N, a->K, Rs, c.rows, c.split, m);
       p.shrink_slices = s.slices;
       p.shrink_spread = static_cast<int>(s.spread);
+      if (workspace_bytes < need + part_bytes(a->T, Rs, s.slices)) return MOE_LORA_ERR_WORKSPACE_TOO_SMALL;
     }
     p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 256 + u_bytes(a->T, Rs));
     const long long ldu = static_cast<long long>(p.pieces) * Rs;
