@@ -12,6 +12,7 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -20,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoelora.so")
 MARSHAL = os.path.join(PKG, "_marshal.so")
+MARSHAL_ABI = os.path.join(PKG, "_marshal.abi")   # what the module beside it was built against
 SOURCES = ["moe_lora.cu", "route_align.cu", "grouped_gemm.cu", "gemm_fp8.cu", "elementwise.cu", "lora.cu", "route_noalloc.cu",
            "lora_tc.cu", "permute_shrink.cu", "nvfp4.cu", "select_experts.cu", "qk_norm_rope.cu",
            "linear.cu", "linear_narrow.cu", "linear_wide.cu", "linear_cluster.cu"]
@@ -42,6 +44,21 @@ def _deps_mtime() -> float:
     return max(os.path.getmtime(f) for f in files)
 
 
+def marshal_abi() -> str:
+    """What _marshal.so depends on besides its sources: this Python and this PyTorch."""
+    import torch
+    return f"Python {sys.version_info[0]}.{sys.version_info[1]}, PyTorch {torch.__version__}"
+
+
+def marshal_built_for() -> str:
+    """What the _marshal.so in place was built against ("" when that is not known)."""
+    try:
+        with open(MARSHAL_ABI) as f:
+            return f.read()
+    except OSError:
+        return ""
+
+
 def _build_marshal(verbose: bool) -> None:
     import torch
     base = os.path.dirname(torch.__file__)
@@ -58,16 +75,33 @@ def _build_marshal(verbose: bool) -> None:
         raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
     if verbose:
         print(r.stdout + r.stderr)
+    if os.path.exists(MARSHAL_ABI):
+        os.remove(MARSHAL_ABI)
     os.replace(MARSHAL + ".tmp", MARSHAL)
+    with open(MARSHAL_ABI, "w") as f:
+        f.write(marshal_abi())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile and link libmoelora.so and _marshal.so if any source is newer than either.  Returns
-    the library's path."""
-    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _deps_mtime() for f in (LIB, MARSHAL)):
+    """Compile and link libmoelora.so if any source is newer than it, and _marshal.so if any is or it was
+    built against another Python or PyTorch.  The library does not depend on the module: it is in
+    place also when building the module fails, which raises.  Returns the library's path."""
+    fresh = {f: not force and os.path.exists(f) and os.path.getmtime(f) >= _deps_mtime() for f in (LIB, MARSHAL)}
+    fresh[MARSHAL] = fresh[MARSHAL] and marshal_built_for() == marshal_abi()
+    if all(fresh.values()):
         return LIB
-    nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        marshal = None if fresh[MARSHAL] else ex.submit(_build_marshal, verbose)
+        if not fresh[LIB]:
+            _build_library(verbose)
+        if marshal is not None:
+            marshal.result()
+    return LIB
+
+
+def _build_library(verbose: bool) -> None:
+    nvcc = _nvcc()
 
     def compile_one(src):
         obj = os.path.join(BUILD, src.replace(".cu", ".o"))
@@ -79,17 +113,14 @@ def build(force: bool = False, verbose: bool = False) -> str:
             print(r.stdout + r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        marshal = ex.submit(_build_marshal, verbose)
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         objs = list(ex.map(compile_one, SOURCES))
-        marshal.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":

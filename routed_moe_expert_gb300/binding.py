@@ -16,6 +16,8 @@ from typing import Optional, Sequence
 
 import torch
 
+from . import _build
+
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libmoelora.so")
 
@@ -750,6 +752,11 @@ def _native():
         path = os.path.join(PKG, "_marshal.so")
         if not os.path.exists(path):
             raise MoELoRAError(4, "_marshal.so not found", f"{path}; build it with routed_moe_expert_gb300._build.build()")
+        have, want = _build.marshal_built_for(), _build.marshal_abi()
+        if have != want:
+            raise MoELoRAError(4, "_marshal.so is not of this Python and PyTorch",
+                               f"built against {have or 'unknown ones'}, this is {want}; build it again with "
+                               "routed_moe_expert_gb300._build.build()")
         spec = importlib.util.spec_from_file_location("_marshal", path)
         m = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(m)
