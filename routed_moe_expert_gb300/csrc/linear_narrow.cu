@@ -496,7 +496,7 @@ cudaError_t launch_linear_narrow(const LinearParams& p, int bn, int split, cudaS
 }
 
 cudaError_t launch_linear_pack(const LinearPackParams& p, cudaStream_t stream) {
-  const cudaError_t err = cudaMemsetAsync(p.sick, 0, sizeof(*p.sick), stream);
+  const cudaError_t err = cudaMemsetAsync(p.sick, 0, sizeof(uint4), stream);   // the piece that the kernel leaves out
   if (err != cudaSuccess) return err;
   const unsigned a = static_cast<unsigned>((static_cast<long long>(p.Rs) * (p.K / 8) + 255) / 256);
   const unsigned b = static_cast<unsigned>((static_cast<long long>(p.N) + 7) / 8);

@@ -138,3 +138,22 @@ def test_a_shrunk_value_past_the_largest_bf16_stays_finite_in_float32(handle, T,
     own = c["slots"].numpy() == 0
     # u is a product of exact values rounded once to 24 bits, in pieces that lose nothing; then one sum
     np.testing.assert_allclose(got[own], float(np.float32(3.4e38)) * 2.0 ** -40, rtol=2.0 ** -22)
+
+
+@pytest.mark.parametrize("ranks", [(16, 8), (64,), (64, 64), (40, 0, 16)], ids=str)
+def test_a_stack_is_the_same_whatever_its_memory_held(handle, ranks):
+    """Every byte of it is written, spare columns and marks among them."""
+    import ctypes
+    S, N, K, R = len(ranks), 256, 256, max(ranks)     # (sizes without a gap between the parts)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    A, B = (torch.randn(s, generator=g, device="cuda").bfloat16() for s in ((S, R, K), (S, N, R)))
+    r, n = (ctypes.c_int32 * S)(*ranks), ctypes.c_size_t()
+    L = pkg.lib()
+    assert L.moe_lora_linear_adapters_size(S, N, K, r, ctypes.byref(n)) == 0
+    stacks = []
+    for fill in (0, 255):
+        t = torch.full((n.value,), fill, dtype=torch.uint8, device="cuda")
+        assert L.moe_lora_linear_pack_adapters(handle.ptr, A.data_ptr(), B.data_ptr(), S, N, K, R, r, t.data_ptr(),
+                                               torch.cuda.current_stream().cuda_stream) == 0
+        stacks.append(t if sum(ranks) % 64 else t[:n.value - 240])    # (the last word's 256 bytes hold 16)
+    assert torch.equal(*stacks)
