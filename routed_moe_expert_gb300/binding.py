@@ -819,11 +819,15 @@ def moe_lora_linear_adapters(handle: Handle, A: torch.Tensor, B: torch.Tensor, r
     arr = (ctypes.c_int32 * max(S, 1))(*ranks)
     n = c_size_t()
     _check(lib().moe_lora_linear_adapters_size(S, N, K, arr, ctypes.byref(n)), "moe_lora_linear_adapters_size")
-    packed = torch.empty(max(n.value, 16), dtype=torch.uint8, device=A.device)
-    with torch.cuda.device(A.device):   # _stream: the current stream of the current device
+    here = torch.cuda.current_stream(A.device)
+    on = here if stream is None else torch.cuda.ExternalStream(_stream(stream), device=A.device)
+    with torch.cuda.stream(on):   # the memory is that stream's, as the kernel that fills it
+        packed = torch.empty(max(n.value, 16), dtype=torch.uint8, device=A.device)
         _check(lib().moe_lora_linear_pack_adapters(handle.ptr, A.data_ptr(), B.data_ptr(), S, N, K, R, arr,
-                                                   packed.data_ptr(), _stream(stream)),
+                                                   packed.data_ptr(), on.cuda_stream),
                "moe_lora_linear_pack_adapters")
+    if stream is not None:
+        packed.record_stream(here)
     return LinearAdapters(packed, S, N, K, ranks, [float(s) for s in scalings])
 
 

@@ -14,6 +14,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -116,9 +117,18 @@ moe_lora_handle* handle_of(PyObject* o, at::Device dev) {
     refuse("the tensors are" + on(dev) + ", the handle is on cuda:" + std::to_string(own));
   return h;
 }
+// Memory for a call on `stream` (None: the current one) comes from that stream's: whatever the block held
+// before was used there, so the call's kernels cannot run into it.
 // (at::empty would come to the same through PyTorch's dispatcher)
-Tensor allocate(at::IntArrayRef sizes, ScalarType type, at::Device dev) {
+Tensor allocate(at::IntArrayRef sizes, ScalarType type, at::Device dev, PyObject* stream) {
+  if (stream == Py_None) return Tensor(at::detail::empty_cuda(sizes, type, dev, std::nullopt));
+  const c10::cuda::CUDAStreamGuard on_it(
+      c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(PyLong_AsVoidPtr(stream)), dev.index()));
   return Tensor(at::detail::empty_cuda(sizes, type, dev, std::nullopt));
+}
+// A result of such a call goes to a caller on the current stream, whose uses a reuse of its memory waits for.
+void handed_over(const Tensor& t, PyObject* stream, at::Device dev) {
+  if (stream != Py_None && t.defined()) t.record_stream(c10::cuda::getCurrentCUDAStream(dev.index()).unwrap());
 }
 
 // A call's small results come from one allocation (select, two results: 3.9 -> 3.55 us of the host; results
@@ -126,9 +136,10 @@ Tensor allocate(at::IntArrayRef sizes, ScalarType type, at::Device dev) {
 struct Results {
   static constexpr int64_t kTogether = 1 << 20;
   at::Device dev;
+  PyObject* stream;
   int64_t bytes = 0, at = 0;
   Tensor block;
-  explicit Results(at::Device d) : dev(d) {}
+  Results(at::Device d, PyObject* s) : dev(d), stream(s) {}
   static int64_t size_of(at::IntArrayRef sizes, ScalarType type) {
     int64_t n = static_cast<int64_t>(c10::elementSize(type));
     for (int64_t s : sizes) n *= s;
@@ -136,8 +147,8 @@ struct Results {
   }
   void expect(at::IntArrayRef sizes, ScalarType type) { bytes += size_of(sizes, type); }   // each, first
   Tensor make(at::IntArrayRef sizes, ScalarType type) {
-    if (bytes > kTogether) return allocate(sizes, type, dev);
-    if (!block.defined()) block = allocate({bytes}, ScalarType::Byte, dev);
+    if (bytes > kTogether) return allocate(sizes, type, dev, stream);
+    if (!block.defined()) block = allocate({bytes}, ScalarType::Byte, dev, stream);
     Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(block.storage()), block.key_set(),
                                                         c10::scalarTypeToTypeMeta(type));
     t.unsafeGetTensorImpl()->set_storage_offset(at / static_cast<int64_t>(c10::elementSize(type)));
@@ -146,14 +157,6 @@ struct Results {
     return t;
   }
 };
-
-// A call on a stream of the caller's naming: what was allocated for it (on the current stream) is
-// not handed out again before that stream is past the call.
-void used_on(const Tensor& t, PyObject* stream, at::Device dev) {
-  if (stream == Py_None || !t.defined()) return;
-  t.record_stream(
-      c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(PyLong_AsVoidPtr(stream)), dev.index()).unwrap());
-}
 
 void need_args(Py_ssize_t n, Py_ssize_t want) {
   if (n != want) {
@@ -215,7 +218,7 @@ PyObject* select_experts(PyObject*, PyObject* const* a, Py_ssize_t n) {
       PyObject* have = given ? PyDict_GetItem(o, key) : nullptr;
       return have == Py_None ? nullptr : have;
     };
-    Results results(dev);
+    Results results(dev, a[12]);
     if (brought(kIds) == nullptr) results.expect({T, k}, ScalarType::Int);
     if (brought(kWeights) == nullptr) results.expect({T, k}, ScalarType::Float);
     if (packed && brought(kPacked) == nullptr) results.expect({T, k}, ScalarType::Int);
@@ -224,7 +227,7 @@ PyObject* select_experts(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (!wanted) return nullptr;
       Tensor made = results.make({T, k}, t);
       void* at = made.data_ptr();
-      used_on(made, a[12], dev);
+      handed_over(made, a[12], dev);
       PyObject* w = THPVariable_Wrap(std::move(made));
       if (w == nullptr) throw Refused();
       const int bad = PyDict_SetItem(o, key, w);
@@ -335,7 +338,7 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Tensor made;
     const Tensor* out;
     if (a[6] == Py_None) {
-      made = allocate({T, N}, truth(a[7]) ? ScalarType::Float : ScalarType::BFloat16, dev);
+      made = allocate({T, N}, truth(a[7]) ? ScalarType::Float : ScalarType::BFloat16, dev, a[9]);
       out = &made;
       p.y_stride = N;
     } else {
@@ -353,15 +356,14 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
       size_t bytes = 0;
       const int st = g_linear_workspace(p.T, p.S, p.h_ranks, &bytes);
       if (st != 0) return PyLong_FromLong(st);
-      scratch = allocate({static_cast<int64_t>(bytes)}, ScalarType::Byte, dev);
+      scratch = allocate({static_cast<int64_t>(bytes)}, ScalarType::Byte, dev, a[9]);
       ws = &scratch;
     } else {
       ws = &tensor(a[8], "workspace");
       if (ws->scalar_type() != ScalarType::Byte || ws->device() != dev || !ws->is_contiguous())
         refuse(*ws, "workspace", "a contiguous uint8 tensor" + on(dev));
     }
-    used_on(made, a[9], dev);
-    used_on(scratch, a[9], dev);
+    handed_over(made, a[9], dev);
     const int st = g_linear(h, &p, ws->data_ptr(), static_cast<size_t>(ws->numel()), stream_of(a[9], dev));
     if (st != 0) return PyLong_FromLong(st);
     if (a[6] == Py_None) return THPVariable_Wrap(std::move(made));
@@ -424,7 +426,7 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p.eps = static_cast<float>(number(a[7]));
     p.interleaved = truth(a[8]);
     Tensor made[2];
-    Results results(dev);
+    Results results(dev, a[12]);
     if (a[9] == Py_None) results.expect({T, Hq, D}, ScalarType::BFloat16);
     if (a[10] == Py_None) results.expect({T, Hk, D}, ScalarType::BFloat16);
     auto output = [&](PyObject* o, int64_t H, Tensor& mine, const char* name, moe_lora_bf16*& at, int64_t& st, int64_t& sh) {
@@ -445,7 +447,7 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
       ws = t.data_ptr();
       ws_bytes = static_cast<size_t>(t.numel());
     }
-    for (const Tensor& t : made) used_on(t, a[12], dev);
+    for (const Tensor& t : made) handed_over(t, a[12], dev);
     const int st = g_qk(h, &p, ws, ws_bytes, stream_of(a[12], dev));
     if (st != 0) return PyLong_FromLong(st);
     PyObject* r = PyTuple_New(2);
