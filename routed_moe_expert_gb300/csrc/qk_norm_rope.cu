@@ -403,8 +403,8 @@ __global__ void __launch_bounds__(256, 3) qk_norm_rope_kernel(const QkParams p) 
         oa[j] = mul2(scale2, fma2(pa, sa[j], mul2(fa[j], ca[j])));
         ob[j] = mul2(scale2, fma2(pb, sb[j], mul2(fb[j], cb[j])));
       }
-      if (has_a) __stcs(reinterpret_cast<uint4*>(now.out + a), pack_pairs(oa));   // not read back soon
-      if (has_b) __stcs(reinterpret_cast<uint4*>(now.out + b), pack_pairs(ob));
+      if (has_a) *reinterpret_cast<uint4*>(now.out + a) = pack_pairs(oa);
+      if (has_b) *reinterpret_cast<uint4*>(now.out + b) = pack_pairs(ob);
     };
     // Finite partners of a piece that is not turned have coefficients of 0; in a head with an infinite
     // value (0 times it is NaN) they are left out.
