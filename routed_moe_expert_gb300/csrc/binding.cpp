@@ -208,7 +208,8 @@ PyObject* select_experts(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p.renormalize = truth(a[8]);
     p.routed_scaling_factor = static_cast<float>(number(a[9]));
     const bool packed = truth(a[10]);
-    const int64_t k = p.top_k < 0 ? 0 : p.top_k;
+    if (p.top_k < 1 || p.top_k > E) return PyLong_FromLong(MOE_LORA_ERR_INVALID_ARG);   // before [T, top_k] is allocated
+    const int64_t k = p.top_k;
     PyObject* o = a[11];
     const bool given = o != Py_None;
     if (given && !PyDict_Check(o)) refuse("outputs must be a dict");

@@ -41,3 +41,18 @@ def test_tensors_of_another_device_are_refused():
         closed = B.Handle(0)
         closed.close()
         B.moe_lora_select_experts(closed, z, 4)
+
+
+@pytest.mark.gpu
+def test_a_top_k_past_the_experts_allocates_nothing():
+    h = B.Handle(0)
+    z = torch.zeros((1024, 64), device="cuda:0")
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.max_memory_allocated()
+    for k in (65, 2 ** 20, 2 ** 31 - 1, 0, -3):
+        with pytest.raises(B.MoELoRAError) as e:
+            B.moe_lora_select_experts(h, z, k, packed=True)
+        assert e.value.status == 1
+    assert torch.cuda.max_memory_allocated() == before
+    h.close()
