@@ -89,6 +89,39 @@ MLDEV uint32_t cluster_ctarank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
+MLDEV uint32_t cluster_nctas() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+// The float at this CTA's shared address `at`, or four of them, in CTA `rank` of the cluster; four at an
+// address of the cluster (cluster_addr).
+MLDEV float ld_cluster_f(uint32_t at, int rank) {
+  float v;
+  asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
+               : "=f"(v)
+               : "r"(at), "r"(rank)
+               : "memory");
+  return v;
+}
+MLDEV float4 ld_cluster_f4(uint32_t at, int rank) {
+  float4 v;
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\t"
+      "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+      : "r"(at), "r"(rank)
+      : "memory");
+  return v;
+}
+MLDEV float4 ld_cluster_f4(uint32_t cluster_address) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(cluster_address)
+               : "memory");
+  return v;
+}
 
 // Expert tile schedule, built by one warp: seg[e] = offsets[e] (e <= E, staged in shared
 // memory with all loads in flight at once, so the offsets cost one memory latency rather

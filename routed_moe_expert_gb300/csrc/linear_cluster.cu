@@ -39,31 +39,6 @@ __host__ __device__ constexpr int smem_bytes(int bn, int nb) {
   return 1024 + stages_of(bn, nb) * stage_bytes(bn, nb) + tail_bytes(bn, nb);
 }
 
-// The float at this CTA's shared address `at`, or four of them, in CTA `rank` of the cluster.
-MLDEV float ld_cluster_f(uint32_t at, int rank) {
-  float v;
-  asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
-               : "=f"(v)
-               : "r"(at), "r"(rank)
-               : "memory");
-  return v;
-}
-MLDEV float4 ld_cluster_f4(uint32_t at, int rank) {
-  float4 v;
-  asm volatile(
-      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\t"
-      "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
-      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-      : "r"(at), "r"(rank)
-      : "memory");
-  return v;
-}
-MLDEV uint32_t cluster_nctas() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
-
 // Sums of two neighbouring tokens' values over the C CTAs of the cluster, in rank order; all loads
 // go out before the first is used.
 template <int C>

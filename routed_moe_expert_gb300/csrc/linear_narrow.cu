@@ -51,23 +51,6 @@ __host__ __device__ constexpr int stage_bytes(int bn) { return kABytes + bn * 12
 __host__ __device__ constexpr int stages_of(int bn) { return (kSmemBudget - 2048) / stage_bytes(bn); }
 constexpr int smem_bytes(int bn) { return 1024 + stages_of(bn) * stage_bytes(bn) + 256 + 12 * bn; }
 
-// Four floats at this CTA's shared address `at`, in CTA `rank` of the cluster.
-MLDEV float4 ld_cluster_f4(uint32_t at, int rank) {
-  float4 v;
-  asm volatile(
-      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\t"
-      "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
-      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-      : "r"(at), "r"(rank)
-      : "memory");
-  return v;
-}
-MLDEV uint32_t cluster_nctas() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
-
 // LONG: a CTA's part of K takes several accumulators (kernels of their own, also in linear_cluster.cu: the
 // arithmetic for them costs short calls 0.1 to 0.3 us; T 1, N 2048, K 2048, rank 16: 6.0 and 6.2 us).
 template <int BN, bool LONG>

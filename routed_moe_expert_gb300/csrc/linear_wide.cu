@@ -66,14 +66,6 @@ __host__ __device__ constexpr int stage_bytes(int bn) { return kABytes + bn / 2 
 __host__ __device__ constexpr int stages_of(int bn) { return bn == 256 ? 6 : bn == 192 ? 6 : 8; }
 __host__ __device__ constexpr int smem_bytes(int bn) { return 1024 + stages_of(bn) * stage_bytes(bn) + kYBytes + 256; }
 
-MLDEV float4 ld_cluster4(uint32_t cluster_address) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(cluster_address)
-               : "memory");
-  return v;
-}
 MLDEV void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 
 // SLICED: a shrink's or a product's K may be in slices (in long batches, where neither is, the
@@ -466,8 +458,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_wide_kernel(const __grid_c
       float4 a[Q], b[Q];
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
-        a[q] = ld_cluster4(a_at + part_at(quad + q));
-        b[q] = ld_cluster4(b_at + part_at(quad + q));
+        a[q] = ld_cluster_f4(a_at + part_at(quad + q));
+        b[q] = ld_cluster_f4(b_at + part_at(quad + q));
       }
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
