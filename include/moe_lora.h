@@ -474,7 +474,8 @@ typedef struct {
    bias, and so do the experts of groups that do not stay; where fewer than top_k experts are
    left the rest are the lowest ids of these, with weight 0 (a token whose experts are all ruled
    out gets ids 0..top_k-1 with weights 0).  +inf counts as the largest finite value.
-   logits aligned to their type.  One launch, no workspace.
+   logits aligned to their type.  One launch, no workspace.  A packed word carries its weight as bf16, and
+   moe_lora_forward_routed goes by that; moe_lora_forward's own routing keeps float32 weights.
    Errors: INVALID_ARG, UNSUPPORTED (n_group > 32, T above 2^31 - 256), CUDA. */
 moe_lora_status moe_lora_select_experts(moe_lora_handle* h, const moe_lora_select_args* a, moe_lora_stream stream);
 
@@ -515,14 +516,17 @@ moe_lora_status moe_lora_linear_workspace_size(int T, int S, const int32_t* h_ra
      y[t] = w x[t] + bias + scaling[s] B_s (A_s x[t]),   s = slot_idx[t]
    summed in float32 and rounded once to y's type.  The shrunk row scaling[s] A_s x[t] is an
    operand of the tensor cores in between: bf16 for a bf16 y, three bf16 pieces (24 significant
-   bits) for a float32 y.  One launch.  `workspace` (16-byte aligned, contents on entry do not matter)
-   starts with the status word that moe_lora_check_status reads: DEVICE_CHECK when a slot index
-   lies outside [-1, S) (such a token gets no adapter; checked when some slot is active), TIMEOUT
-   when a bounded wait ran out (then destroy the handle: its flags may be left set).  The handle holds 64 KB of flags on the device that calls with
-   adapters use, so calls through one handle run one after another, as its stream rule says.  A long batch with
-   adapters takes every SM and its blocks wait for one another: other streams' kernels that end by
-   themselves only delay it, two such calls (of two handles) on streams of different priority can
-   hold each other up until their waits end.
+   bits) for a float32 y.  An accumulator of a float32 y takes at most 1024 of K, since the tensor cores
+   truncate as they accumulate (of few tokens past K 131072, a 128th of K).  One launch.
+   `workspace` (16-byte aligned, contents on entry do not matter) starts with the status word that
+   moe_lora_check_status reads: DEVICE_CHECK when a slot index lies outside [-1, S) (such a token gets no
+   adapter; checked when some slot is active), TIMEOUT when a bounded wait ran out (then destroy the
+   handle: its flags may be left set).  An empty batch writes nothing, the status word neither.
+   The handle holds 64 KB of flags on the device that calls with adapters use, so calls through one
+   handle run one after another, as its stream rule says.  A long batch with adapters takes every SM
+   and its blocks wait for one another: other streams' kernels that end by themselves only delay it, two
+   such calls (of two handles) on streams of different priority can hold each other up until their
+   waits end.
    Errors: INVALID_ARG, UNSUPPORTED (more than 4096 stacked ranks; adapters on more than 2^20
    tokens; T, N or K above 2^31 - 256), WORKSPACE_TOO_SMALL, CUDA. */
 moe_lora_status moe_lora_linear(moe_lora_handle* h, const moe_lora_linear_args* a, void* workspace,
@@ -555,7 +559,7 @@ typedef struct {
    the end.  Any alignment of a bf16 element is taken; addresses and strides of whole 16-byte
    pieces are the fast case.  `workspace` (optional, 4 bytes): its first word is the status that
    moe_lora_check_status reads: DEVICE_CHECK when a position lies outside [0, num_positions)
-   (those tokens are normed and not rotated).  One launch.
+   (those tokens are normed and not rotated); an empty batch does not write it.  One launch.
    Errors: INVALID_ARG, UNSUPPORTED (head_dim > 512, T above 2^31 - 256), WORKSPACE_TOO_SMALL, CUDA. */
 moe_lora_status moe_lora_qk_norm_rope(moe_lora_handle* h, const moe_lora_qk_args* a, void* workspace,
                                       size_t workspace_bytes, moe_lora_stream stream);

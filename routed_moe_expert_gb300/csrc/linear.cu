@@ -146,7 +146,7 @@ double cluster_us(int T, int N, int K, int Rs, int bn, int split, int sms) {
 // How a shrink is cut and dealt out (wide tiles): the slices of a shrink tile's K, how many of all
 // slices go round every pair instead of the spare ones, and the K blocks of the busiest pair.
 //
-// A K block of a shrink tile takes as long as one of a product tile (what is in flight bounds both), so
+// A K block of a shrink tile takes as long as one of a product tile (measured), so
 // whole shrink tiles are in the way: with at most one product tile per pair they take as long as those
 // that wait for them, and several in a row far longer (T 2450, N 1560, K 3632, 56 ranks: 40.3 us, 21.7
 // without adapters, 27.4 in slices); with more they leave a few pairs a tile behind the others.
@@ -193,8 +193,9 @@ Shrink deal_shrink(int T, int N, int K, int Rs, int rows, int split, const Linea
 }
 
 // Pairs: a pair walks whole tiles of 256 tokens x `rows`; a 64-deep K step takes 0.30 us at 256 rows
-// (the tensor cores' rate), 0.285 at 192 and 0.28 at 128 (an SM's intake of copies), so the smaller ones pay
-// only where they bring no further wave: T 3066, N 1551, K 6624: 66.6 / 62.9 / 87.6 us.
+// (the tensor cores' rate), 0.285 at 192 and 0.28 at 128 (24 KB an SM; at 256 rows 32 KB take 0.30, so it is
+// not the copies' rate: what it waits for was not found), so the smaller ones pay only where they bring no
+// further wave: T 3066, N 1551, K 6624: 66.6 / 62.9 / 87.6 us.
 // Two pairs with half of a tile's K each (split 2) exchange their part sums through shared memory,
 // about 4 us, and have less of a main loop to hide the shrink under: T 512, N 4096, K 7168, rank 16:
 // 26.5 us, one pair per tile 35.9; T 512, N 2048, K 2048: 14.8 and 13.4.  (Four pairs, clusters of 8,

@@ -8,7 +8,7 @@
 // tokens, scales and masks u, rounds it to bf16 pieces straight into an MMA operand, and the stacked
 // B (copied during the exchange) takes it to the delta in TMEM.  Against the flag of the narrow
 // kernel (u through global memory from other clusters) this reads the stacked A once per row tile,
-// from L2, and saves that round trip: T 1, N 2048, K 2048, rank 16 (K over 8 CTAs) takes 5.9 us, 7.9 on
+// from L2, and saves that round trip: T 1, N 2048, K 2048, rank 16 (K over 8 CTAs) takes 6.0 us, 7.9 on
 // the narrow kernel, 4.3 there without adapters; T 16, N 4096, K 7168: 13.7, 14.7 and 12.4 (8.7 for
 // its 59 MB at 6.8 TB/s).  Past 32 tokens a tile the narrow kernel is ahead (T 64, N 5120, K 2048:
 // 11.6 us against 14.6 here).

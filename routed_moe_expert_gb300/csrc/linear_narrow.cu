@@ -26,7 +26,7 @@
 //
 // What bounds it is latency, not bandwidth: start, first copies, a few K steps, the shrink's flag, the
 // adapter blocks, the sum over the cluster, each a memory round trip or two.  T 64, N 5120, K 2048,
-// 120 ranks (64-token tiles, K over 4 CTAs): 12.3 us, 8.0 without adapters, 3.5 for its 24 MB at
+// 120 ranks (64-token tiles, K over 4 CTAs): 12.2 us, 8.0 without adapters, 3.5 for its 24 MB at
 // 6.8 TB/s; tensor pipe 5%, DRAM 18% busy.  T 128, N 384, K 7168, float32 (32-token tiles, K over 8
 // CTAs): 7.4 us for 7.5 MB.
 //

@@ -39,8 +39,9 @@
 // registers (a token's 128 columns per thread) while the MMAs go on in the other one.
 //
 // Long batches are bound by the tensor cores: T 8192, N 4096, K 7168, 128 ranks of which 64 to 128 at
-// work in a tile: 271 us, 1.79 PFLOP/s of bf16 (95% of a burst of plain library products); without
-// adapters 248 to 255, the rate of these.  In a row for seconds, at the power limit, 305 and 282.
+// work in a tile: 268 to 274 us from a graph of a few calls, 1.79 PFLOP/s of bf16 (95% of a burst of plain
+// library products); without adapters 248 to 255, the rate of these.  In a row for seconds, at the power limit,
+// 317 and 289.
 //
 // Warp 0: TMA producer; warp 1: MMA issuer (even CTA); warps 2-5: epilogue; warp 6: a tile or two
 // ahead of them, which adapter blocks a tile needs, and the wait for its u (in the producer itself

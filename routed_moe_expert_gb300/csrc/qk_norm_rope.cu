@@ -11,8 +11,8 @@
 // not rounded before the rotation).
 //
 // It is bound by memory: each value is read once and written once.  T 8192, 32 + 4 heads of 128:
-// 28.3 us for 155 MB, 5.5 TB/s (81% of a plain copy's rate).  T 333, 24 + 8 heads of 192: 4.4 us for
-// 8.3 MB, one token 2.3 us: latency.
+// 28.4 us for 155 MB, 5.5 TB/s (80% of a plain copy's rate).  T 333, 24 + 8 heads of 192: 4.5 us for
+// 8.3 MB, one token 2.4 us: latency.
 //
 // L lanes hold a head, so a warp holds 32 / L heads at a time; a lane's pieces are chosen so that both
 // members of every rotated pair sit in the same lane (pieces i and i + R/2 of a half-split rotation),
@@ -23,7 +23,9 @@
 // C = w c and S = -+ w_partner s made once per token and kind of head and kept in registers, and
 // the next heads' values are loaded before the current ones are used.  Everything else (odd
 // strides, offsets and sizes) goes through qk_norm_rope_any_kernel, which works its indices out
-// value by value.
+// value by value: T 8192, 32 + 4 heads of 80 with R 40 (8-byte pieces) 62 us, with R 80
+// (16-byte pieces, the other kernel) 25; heads of 100 (4-byte pieces) 203, of 90 (2-byte) 359; 14 to 18 for
+// their bytes.  What bounds it was not measured.
 #include "common.cuh"
 #include "host.h"
 #include "kernels.h"
