@@ -792,11 +792,12 @@ class LinearAdapters:
     """The adapters of one projection, stacked by moe_lora_linear_adapters: what a serving program
     keeps per projection while its slots hold the same adapters."""
 
-    def __init__(self, packed: torch.Tensor, S: int, N: int, K: int, ranks: Sequence[int], scalings: Sequence[float]):
+    def __init__(self, packed: torch.Tensor, S: int, N: int, K: int, ranks: Sequence[int], scalings: Sequence[float],
+                 stream: Optional[int] = None):   # whose memory `packed` is (None: the current one's)
         self.packed = packed
         self.S, self.N, self.K = S, N, K
         self.ranks = (ctypes.c_int32 * S)(*ranks)
-        self.native = _native().adapters(packed, S, N, K, list(ranks), list(scalings))
+        self.native = _native().adapters(packed, S, N, K, list(ranks), list(scalings), stream)
 
 
 def moe_lora_linear_adapters(handle: Handle, A: torch.Tensor, B: torch.Tensor, ranks: Sequence[int],
@@ -828,7 +829,7 @@ def moe_lora_linear_adapters(handle: Handle, A: torch.Tensor, B: torch.Tensor, r
                "moe_lora_linear_pack_adapters")
     if stream is not None:
         packed.record_stream(here)
-    return LinearAdapters(packed, S, N, K, ranks, [float(s) for s in scalings])
+    return LinearAdapters(packed, S, N, K, ranks, [float(s) for s in scalings], on.cuda_stream)
 
 
 def moe_lora_linear_workspace_size(T: int, adapters: Optional[LinearAdapters] = None) -> int:

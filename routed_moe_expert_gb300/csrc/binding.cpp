@@ -18,7 +18,6 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
-#include <cstring>
 #include <optional>
 #include <sstream>
 #include <string>
@@ -254,27 +253,31 @@ PyObject* select_experts(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// The adapters of a projection, as moe_lora_linear_adapters stacked them (a capsule).
+// The adapters of a projection, as moe_lora_linear_adapters stacked them (a capsule).  Callers never see the
+// stack's tensor, so calls on other streams than its own are recorded on it here.
 struct Adapters {
-  int S, N, K, device;
-  const void* address;
-  int32_t ranks[64];
-  float scalings[64];
+  int S = 0, N = 0, K = 0, device = 0;
+  Tensor packed;
+  cudaStream_t stream = nullptr;   // whose memory it is
+  const void* address = nullptr;
+  int32_t ranks[64] = {};
+  float scalings[64] = {};
 };
 constexpr const char* kAdapters = "moe_lora.adapters";
 
-// (packed, S, N, K, ranks, scalings)
+// (packed, S, N, K, ranks, scalings, stream that packed is the memory of)
 PyObject* adapters(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
-    need_args(n, 6);
+    need_args(n, 7);
     const Tensor& t = tensor(a[0], "packed");
     Adapters* d = new Adapters();
-    std::memset(d, 0, sizeof(*d));
     try {
       d->S = int32(a[1]);
       d->N = int32(a[2]);
       d->K = int32(a[3]);
       d->device = t.device().index();
+      d->packed = t;
+      d->stream = reinterpret_cast<cudaStream_t>(stream_of(a[6], t.device()));
       d->address = t.data_ptr();
       if (d->S < 1 || d->S > 64 || !PyList_Check(a[4]) || !PyList_Check(a[5]) || PyList_Size(a[4]) != d->S ||
           PyList_Size(a[5]) != d->S)
@@ -323,8 +326,9 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p.slot_idx = nullptr;
     p.h_ranks = nullptr;
     p.h_scalings = nullptr;
+    const Adapters* used = nullptr;
     if (a[3] != Py_None) {
-      const Adapters* d = static_cast<const Adapters*>(PyCapsule_GetPointer(a[3], kAdapters));
+      const Adapters* d = used = static_cast<const Adapters*>(PyCapsule_GetPointer(a[3], kAdapters));
       if (d == nullptr) throw Refused();
       if (d->N != N || d->K != K || d->device != dev.index())
         refuse("the adapters are for a [" + std::to_string(d->N) + ", " + std::to_string(d->K) + "] projection on cuda:" +
@@ -365,7 +369,10 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
         refuse(*ws, "workspace", "a contiguous uint8 tensor" + on(dev));
     }
     handed_over(made, a[9], dev);
-    const int st = g_linear(h, &p, ws->data_ptr(), static_cast<size_t>(ws->numel()), stream_of(a[9], dev));
+    const moe_lora_stream stream = stream_of(a[9], dev);
+    if (used != nullptr && stream != used->stream)
+      used->packed.record_stream(c10::cuda::getStreamFromExternal(stream, dev.index()).unwrap());
+    const int st = g_linear(h, &p, ws->data_ptr(), static_cast<size_t>(ws->numel()), stream);
     if (st != 0) return PyLong_FromLong(st);
     if (a[6] == Py_None) return THPVariable_Wrap(std::move(made));
     Py_INCREF(a[6]);

@@ -70,3 +70,28 @@ def test_results_are_the_callers_after_a_wait(handle):
         other = [torch.full_like(want, 9.0) for _ in range(8)]
     torch.cuda.synchronize()
     assert torch.equal(copy, want) and len(other) == 8
+
+
+@pytest.mark.parametrize("named", [False, True])
+def test_adapters_let_go_of_while_another_stream_reads_them(handle, named):
+    g = torch.Generator(device="cuda").manual_seed(2)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda")
+    x, w = r(64, 256).bfloat16(), (r(384, 256) / 16).bfloat16()
+    A, B = (r(2, 16, 256) / 16).bfloat16(), r(2, 384, 16).bfloat16()
+    slots = torch.randint(-1, 2, (64,), generator=g, device="cuda").int()
+    make = lambda: pkg.moe_lora_linear_adapters(handle, A, B, [16, 8], [1.0, 2.0])
+    want = pkg.moe_lora_linear(handle, x, w, make(), slots).clone()
+    ad, side = make(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(40_000_000)
+        if not named:
+            got = pkg.moe_lora_linear(handle, x, w, ad, slots)
+    if named:
+        got = pkg.moe_lora_linear(handle, x, w, ad, slots, stream=side)
+    n = ad.packed.numel()
+    del ad
+    torch.cuda._sleep(1_000_000)
+    others = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and len(others) == 4
