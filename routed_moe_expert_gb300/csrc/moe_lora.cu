@@ -198,8 +198,8 @@ moe_lora_status moe_lora_create(moe_lora_handle** out, int device) {
   if (err == cudaSuccess) err = cudaEventCreateWithFlags(&h->ev_fork, cudaEventDisableTiming);
   if (err == cudaSuccess) err = cudaEventCreateWithFlags(&h->ev_ready, cudaEventDisableTiming);
   if (err == cudaSuccess) err = cudaMalloc(reinterpret_cast<void**>(&h->linear_flags), kLinearFlags * sizeof(int2));
-  if (err == cudaSuccess) err = cudaMemset(h->linear_flags, 0, kLinearFlags * sizeof(int2));
-  if (err == cudaSuccess) err = cudaDeviceSynchronize();   // zero before any stream's first call
+  if (err == cudaSuccess) err = cudaMemsetAsync(h->linear_flags, 0, kLinearFlags * sizeof(int2), h->side);
+  if (err == cudaSuccess) err = cudaStreamSynchronize(h->side);   // zero before any stream's first call
   void* fn = nullptr;
   cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
   if (err == cudaSuccess)
