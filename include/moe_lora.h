@@ -564,6 +564,114 @@ typedef struct {
 moe_lora_status moe_lora_qk_norm_rope(moe_lora_handle* h, const moe_lora_qk_args* a, void* workspace,
                                       size_t workspace_bytes, moe_lora_stream stream);
 
+/* ---------------------------------------------------------------------------------------
+ * Attention over a paged cache: what a step's tokens need from the requests' lengths, the write of new
+ * keys and values, and the attention that reads them.  A cache is pages of page_size tokens; token i of a
+ * request lies in page block_tables[b][i / page_size] at i % page_size, its slot is
+ * page * page_size + i % page_size.  The conventions of the operators around the expert layer hold here too:
+ * strides in elements, the handle's device, forward only.
+ * ------------------------------------------------------------------------------------- */
+
+/* Arguments of moe_lora_page_tables. */
+typedef struct {
+  int32_t* block_tables;        /* [B, table_width] in/out: the pages that a request has, in order     */
+  const int32_t* cached_lens;   /* [B] tokens of each request in the cache                             */
+  const int32_t* new_lens;      /* [B] tokens that this step adds to each, 0 allowed                   */
+  const int32_t* free_pages;    /* [num_free] pages that nobody has                                    */
+  const int32_t* taken;         /* [1] how many of them are taken, from the front                      */
+  int32_t* kv_lens;             /* [B] out: cached + new; may be cached_lens itself                    */
+  int32_t* query_offsets;       /* [B + 1] out: each request's first token among the step's            */
+  int32_t* slot_map;            /* [T] out: slot of each token, -1 behind the last request's           */
+  int32_t* positions;           /* [T] out: position of each token in its request, 0 behind the last   */
+  int32_t* taken_out;           /* [1] out: may be `taken` itself                                      */
+  int64_t table_stride;         /* >= table_width                                                      */
+  int B, table_width, page_size, num_free;   /* B * table_width and pages * page_size below 2^31      */
+  int T;                        /* tokens that slot_map and positions hold: a step's tokens, and padding */
+} moe_lora_page_tables_args;
+
+/* Block tables, slots and positions of a step from its requests' lengths, on the device: request b, in
+   order, takes the ceil((cached + new) / page_size) - ceil(cached / page_size) pages that it lacks from
+   the front of the free list and has them entered in its table; the step's tokens are the requests' new
+   ones one after another.  Only new entries of the tables are written, so a repeated call from the same
+   `taken` gives the same.  Captured in a graph it follows the lengths of each replay.
+   `workspace` (optional, 4 bytes): its first word is the status that moe_lora_check_status reads,
+   DEVICE_CHECK when a length is negative (it counts as 0), the free list ends (requests get what is left,
+   in order), a table is too narrow, `taken` lies outside the list, or the requests bring more than T
+   tokens (offsets stop at T).  A token without a page gets slot -1 and kv_lens counts those before it alone.
+   One launch.  Outputs must not overlap inputs but as named.  Errors: INVALID_ARG, WORKSPACE_TOO_SMALL, CUDA. */
+moe_lora_status moe_lora_page_tables(moe_lora_handle* h, const moe_lora_page_tables_args* a, void* workspace,
+                                     size_t workspace_bytes, moe_lora_stream stream);
+
+/* Arguments of moe_lora_cache_write. */
+typedef struct {
+  const moe_lora_bf16* k;       /* [T, heads, head_dim], for instance slices of merged q/k/v rows      */
+  const moe_lora_bf16* v;
+  moe_lora_bf16* k_cache;       /* [num_pages, heads, page_size, head_dim] in any order of strides     */
+  moe_lora_bf16* v_cache;
+  const int32_t* slot_map;      /* [T] page * page_size + place in it; negative: the token is left out */
+  int64_t k_stride_t, k_stride_h, v_stride_t, v_stride_h;
+  int64_t k_stride_page, k_stride_head, k_stride_token;   /* of k_cache */
+  int64_t v_stride_page, v_stride_head, v_stride_token;   /* of v_cache */
+  int T, heads, head_dim;       /* head_dim 1..512, adjacent values                                    */
+  int num_pages, page_size;     /* num_pages * page_size below 2^31                                    */
+} moe_lora_cache_write_args;
+
+/* Keys and values of a step's tokens into their slots of the cache.  Slots that are not named stay as they
+   are; each slot is to be named once (of two tokens with one slot either may be found there, or pieces of
+   both).  Any alignment of a bf16 element is taken; addresses and strides of whole 16-byte pieces are the
+   fast case.  `workspace` (optional, 4 bytes): status word, DEVICE_CHECK when a slot lies past the cache
+   (that token is left out); an empty batch does not write it.  One launch.
+   Errors: INVALID_ARG, UNSUPPORTED (head_dim > 512, T above 2^31 - 256), WORKSPACE_TOO_SMALL, CUDA. */
+moe_lora_status moe_lora_cache_write(moe_lora_handle* h, const moe_lora_cache_write_args* a, void* workspace,
+                                     size_t workspace_bytes, moe_lora_stream stream);
+
+/* Arguments of moe_lora_attention. */
+typedef struct {
+  const moe_lora_bf16* q;         /* [T, q_heads, head_dim]                                            */
+  const moe_lora_bf16* k_cache;   /* [num_pages, k_heads, page_size, head_dim] in any order of strides */
+  const moe_lora_bf16* v_cache;
+  const int32_t* block_tables;    /* [B, table_width]                                                  */
+  const int32_t* kv_lens;         /* [B] keys of each request, its new tokens' among them              */
+  const int32_t* query_offsets;   /* [B + 1] first query row of each request; NULL: row b is request b's */
+  moe_lora_bf16* out;             /* [T, q_heads, head_dim]; may be q itself                           */
+  float* lse;                     /* [T, q_heads], optional: natural logarithm of the softmax's sum    */
+  int64_t q_stride_t, q_stride_h, out_stride_t, out_stride_h;
+  int64_t k_stride_page, k_stride_head, k_stride_token;
+  int64_t v_stride_page, v_stride_head, v_stride_token;
+  int64_t table_stride;
+  int T, B;                       /* without query_offsets T == B                                      */
+  int q_heads, k_heads;           /* q_heads a multiple of k_heads: query head h reads key head h * k_heads / q_heads */
+  int head_dim;                   /* 1..512                                                            */
+  int num_pages, page_size, table_width;
+  int max_query_len;              /* the longest request's query rows; only chooses among the kernels  */
+  int shared_len;                 /* >= 0: the first shared_len keys of every request lie in the same pages */
+  float scale;                    /* of the scores, usually 1 / sqrt(head_dim)                         */
+} moe_lora_attention_args;
+
+/* Host-only: bytes of workspace that are enough for moe_lora_attention on up to T query rows of these heads,
+   whatever else: never less for more rows. */
+moe_lora_status moe_lora_attention_workspace_size(int T, int q_heads, int k_heads, int head_dim, size_t* bytes);
+
+/* Causal attention of a step's tokens to their requests' pages (prompts, pieces of prompts, drafts to verify,
+   single tokens, mixed at will): query row i of the n that request b has sees its keys
+   j < kv_lens[b] - n + i + 1, and
+     out[row, h] = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale q . k_j - max).
+   A row that sees no key, or whose every score is -inf, gets zeros and lse -inf.  Rows of no request are left
+   as they are.  Keys that a row does not see, the rest of a last page among them, may hold anything.
+   shared_len names keys that all requests have in common (a common prompt): they are read from request 0's
+   table, once for all rows instead of once for each request; the results are the same up to float32 sums.
+   Scores, sums and the result are float32, rounded once at the end; the weights p_j are an operand of the
+   tensor cores in between, as bf16 (two bf16 pieces where requests have up to 16 rows a key head).
+   head_dim a multiple of 8 up to 128, pages of a power of two of at least 16 tokens, and 16-byte pieces in q
+   and the caches are the fast case; anything else runs on plain cores.
+   `workspace` (16-byte aligned, contents on entry do not matter) starts with the status word:
+   DEVICE_CHECK when query_offsets are not rising within [0, T], a length is negative or past its table, or a
+   page that is read lies outside the cache (its keys count as zeros); TIMEOUT when a bounded wait ran out.
+   No atomics on values: the same call gives the same bits.
+   Errors: INVALID_ARG, UNSUPPORTED (head_dim > 512, sizes past 2^31 - 256), WORKSPACE_TOO_SMALL, CUDA. */
+moe_lora_status moe_lora_attention(moe_lora_handle* h, const moe_lora_attention_args* a, void* workspace,
+                                   size_t workspace_bytes, moe_lora_stream stream);
+
 /* Cumulative number of this library's kernels launched through `h` (each route, permute,
    forward or routed forward adds the kernels it enqueued; a memset is not counted).  For
    measurement; the pages have no counterpart.  Host-only.  Errors: INVALID_ARG. */

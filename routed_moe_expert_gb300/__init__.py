@@ -13,5 +13,7 @@ from .binding import (  # noqa: F401
     FLAG_DOWN_LORA_SIDE, FLAG_SEPARATE_SHRINK,
     moe_lora_select_experts, moe_lora_qk_norm_rope, alloc_qk_norm_rope_workspace, moe_lora_linear,
     moe_lora_linear_adapters, moe_lora_linear_workspace_size, alloc_linear_workspace, LinearAdapters,
+    moe_lora_page_tables, moe_lora_cache_write, alloc_cache_workspace, moe_lora_attention,
+    moe_lora_attention_workspace_size, alloc_attention_workspace,
     ROUTE_RENORMALIZE, ROUTE_DEEPSEEK_V3, SCORE_SOFTMAX, SCORE_SIGMOID, GROUP_MAX, GROUP_TOP2, STAGES, NUM_STAGES,
 )

@@ -154,6 +154,7 @@ def lib() -> ctypes.CDLL:
     L.moe_lora_linear_pack_adapters.argtypes = [c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_void_p,
                                                 c_void_p, c_void_p]
     L.moe_lora_linear_workspace_size.argtypes = [c_int, c_int, c_void_p, ctypes.POINTER(c_size_t)]
+    L.moe_lora_attention_workspace_size.argtypes = [c_int, c_int, c_int, c_int, ctypes.POINTER(c_size_t)]
     for name in EXPORTED:
         if name not in ("moe_lora_status_string", "moe_lora_last_cuda_error"):
             getattr(L, name).restype = c_int
@@ -763,7 +764,8 @@ def _native():
         L = lib()
         m.entry_points(*(ctypes.cast(getattr(L, n), c_void_p).value for n in (
             "moe_lora_select_experts", "moe_lora_linear", "moe_lora_linear_workspace_size", "moe_lora_qk_norm_rope",
-            "moe_lora_device")))
+            "moe_lora_device", "moe_lora_page_tables", "moe_lora_cache_write", "moe_lora_attention",
+            "moe_lora_attention_workspace_size")))
         _marshal = m
     return _marshal
 
@@ -882,4 +884,72 @@ def moe_lora_qk_norm_rope(handle: Handle, q: torch.Tensor, k: torch.Tensor, q_we
                                              None if stream is None else _stream(stream))
     if type(r) is int:
         _check(r, "moe_lora_qk_norm_rope")
+    return r
+
+
+# ---------------------------------------------------------------- attention over a paged cache
+def alloc_cache_workspace(device="cuda") -> torch.Tensor:
+    """The status word of moe_lora_page_tables or moe_lora_cache_write, for moe_lora_check_status."""
+    return torch.zeros(256, dtype=torch.uint8, device=device)
+
+
+def moe_lora_page_tables(handle: Handle, block_tables: torch.Tensor, cached_lens: torch.Tensor, new_lens: torch.Tensor,
+                         page_size: int, free_pages: torch.Tensor, taken: torch.Tensor, num_tokens: int,
+                         outputs: Optional[dict] = None, workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """Block tables, slots and positions of a step from its requests' lengths, on the device (all int32):
+    request b has cached_lens[b] tokens in the pages of block_tables[b] [B, width] and brings new_lens[b];
+    the pages that it lacks come from free_pages behind the first taken [1], in the requests' order, and
+    are entered in its row.  num_tokens: the rows of the step's batch, the requests' new tokens one after
+    another and padding.  Returns a dict of kv_lens [B] (cached and new), query_offsets [B + 1], slot_map
+    [num_tokens] (page * page_size + place, -1 for padding), positions [num_tokens] and taken [1];
+    `outputs` may bring any of them, also cached_lens as kv_lens and `taken` itself as taken."""
+    r = (_marshal or _native()).page_tables(handle.address, block_tables, cached_lens, new_lens, page_size, free_pages,
+                                            taken, num_tokens, outputs, workspace,
+                                            None if stream is None else _stream(stream))
+    if type(r) is int:
+        _check(r, "moe_lora_page_tables")
+    return r
+
+
+def moe_lora_cache_write(handle: Handle, k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                         slot_map: torch.Tensor, workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Keys and values k, v [T, heads, D] (bf16, for instance slices of merged q/k/v rows) into the slots
+    slot_map [T] (int32; negative: left out) of k_cache, v_cache [pages, heads, page size, D], which may be
+    views of other orders with adjacent head values."""
+    st = (_marshal or _native()).cache_write(handle.address, k, v, k_cache, v_cache, slot_map, workspace,
+                                             None if stream is None else _stream(stream))
+    if st != 0:
+        _check(st, "moe_lora_cache_write")
+
+
+def moe_lora_attention_workspace_size(T: int, q_heads: int, k_heads: int, head_dim: int) -> int:
+    """Bytes of workspace that are enough for moe_lora_attention on up to T query rows of these heads."""
+    n = c_size_t()
+    _check(lib().moe_lora_attention_workspace_size(T, q_heads, k_heads, head_dim, ctypes.byref(n)),
+           "moe_lora_attention_workspace_size")
+    return n.value
+
+
+def alloc_attention_workspace(T: int, q_heads: int, k_heads: int, head_dim: int, device="cuda") -> torch.Tensor:
+    return torch.empty(moe_lora_attention_workspace_size(T, q_heads, k_heads, head_dim), dtype=torch.uint8, device=device)
+
+
+def moe_lora_attention(handle: Handle, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                       block_tables: torch.Tensor, kv_lens: torch.Tensor, query_offsets: Optional[torch.Tensor] = None,
+                       max_query_len: Optional[int] = None, scale: Optional[float] = None, shared_len: int = 0,
+                       out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, return_lse: bool = False,
+                       workspace: Optional[torch.Tensor] = None, stream=None):
+    """Causal attention of the rows q [T, Hq, D] (bf16) to their requests' keys and values in the pages
+    block_tables [B, width] of k_cache, v_cache [pages, Hk, page size, D] (Hq a multiple of Hk).  Request b
+    has the rows from query_offsets[b] to query_offsets[b + 1] (without them: row b), the last of its
+    kv_lens[b] tokens; a row sees the keys up to its own.  max_query_len (the longest request's rows, for the
+    choice of the kernel), scale (1 / sqrt(D) unless given), shared_len: so many first keys of every request
+    are in the same pages (those of request 0) and are read once for all.  Returns out, a new dense tensor
+    unless given, or (out, lse) with return_lse or lse [T, Hq] float32, the logarithms of the softmax sums.
+    Rows that see no key are zero, rows of no request are left as they are."""
+    r = (_marshal or _native()).attention(handle.address, q, k_cache, v_cache, block_tables, kv_lens, query_offsets,
+                                          max_query_len, scale, shared_len, out, return_lse if lse is None else lse,
+                                          workspace, None if stream is None else _stream(stream))
+    if type(r) is int:
+        _check(r, "moe_lora_attention")
     return r

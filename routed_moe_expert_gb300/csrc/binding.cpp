@@ -1,4 +1,5 @@
-// Argument marshalling of the operators around the layer for Python (module _marshal).
+// Argument marshalling of the operators around the layer and of those over the paged cache for Python (module
+// _marshal).
 //
 // These calls come several times per layer on batches down to one token, where the host's time is
 // the call's time.  Tensors are looked at through PyTorch's C++ interface instead of attribute by
@@ -18,6 +19,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <optional>
 #include <sstream>
 #include <string>
@@ -33,6 +35,10 @@ decltype(&moe_lora_linear) g_linear = nullptr;
 decltype(&moe_lora_linear_workspace_size) g_linear_workspace = nullptr;
 decltype(&moe_lora_qk_norm_rope) g_qk = nullptr;
 decltype(&moe_lora_device) g_device = nullptr;
+decltype(&moe_lora_page_tables) g_page_tables = nullptr;
+decltype(&moe_lora_cache_write) g_cache_write = nullptr;
+decltype(&moe_lora_attention) g_attention = nullptr;
+decltype(&moe_lora_attention_workspace_size) g_attention_workspace = nullptr;
 
 struct Refused {};   // a Python exception is set
 
@@ -474,25 +480,278 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// (addresses of select_experts, linear, linear_workspace_size, qk_norm_rope, device)
+// An optional status word, or more, of the caller's.
+void* workspace_of(PyObject* o, at::Device dev, size_t& bytes) {
+  bytes = 0;
+  if (o == Py_None) return nullptr;
+  const Tensor& t = tensor(o, "workspace");
+  if (t.scalar_type() != ScalarType::Byte || t.device() != dev || !t.is_contiguous())
+    refuse(t, "workspace", "a contiguous uint8 tensor" + on(dev));
+  bytes = static_cast<size_t>(t.numel());
+  return t.data_ptr();
+}
+const int32_t* lengths(PyObject* o, int64_t n, at::Device dev, const char* name) {
+  return static_cast<const int32_t*>(vector_of(o, ScalarType::Int, n, dev, name));
+}
+// [B, width] int32 rows
+const Tensor& block_tables(PyObject* o) {
+  const Tensor& t = tensor(o, "block_tables");
+  if (t.dim() != 2 || !t.is_cuda() || t.scalar_type() != ScalarType::Int) refuse(t, "block_tables", "an int32 CUDA tensor [B, width]");
+  rows_of(t, "block_tables");
+  return t;
+}
+// [pages, heads, page size, D] with adjacent head values
+const Tensor& cache_of(PyObject* o, int64_t heads, int64_t D, at::Device dev, const Tensor* like, const char* name) {
+  const Tensor& t = tensor(o, name);
+  if (t.scalar_type() != ScalarType::BFloat16 || t.dim() != 4 || (heads >= 0 && t.size(1) != heads) || t.size(3) != D ||
+      t.device() != dev || (D > 1 && t.stride(3) != 1) || (like != nullptr && t.sizes() != like->sizes()))
+    refuse(t, name, "a bf16 [pages, heads, page size, " + std::to_string(D) + "] tensor with adjacent head values" + on(dev) +
+                        (like != nullptr ? ", of the sizes of k_cache" : ""));
+  return t;
+}
+
+PyObject* kKvLens;
+PyObject* kQueryOffsets;
+PyObject* kSlotMap;
+PyObject* kPositions;
+PyObject* kTaken;
+
+// (handle, block_tables, cached_lens, new_lens, page_size, free_pages, taken, num_tokens, outputs, workspace, stream)
+PyObject* page_tables(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    need_args(n, 11);
+    const Tensor& table = block_tables(a[1]);
+    const at::Device dev = table.device();
+    moe_lora_handle* h = handle_of(a[0], dev);
+    const int64_t B = table.size(0);
+    moe_lora_page_tables_args p;
+    p.block_tables = static_cast<int32_t*>(table.data_ptr());
+    p.table_stride = B > 1 ? table.stride(0) : table.size(1);
+    p.B = size(B, "block_tables");
+    p.table_width = size(table.size(1), "block_tables");
+    p.cached_lens = lengths(a[2], B, dev, "cached_lens");
+    p.new_lens = lengths(a[3], B, dev, "new_lens");
+    p.page_size = int32(a[4]);
+    const Tensor& free_pages = tensor(a[5], "free_pages");
+    if (free_pages.dim() != 1) refuse(free_pages, "free_pages", "a dense int32 vector" + on(dev));
+    p.num_free = size(free_pages.size(0), "free_pages");
+    p.free_pages = lengths(a[5], p.num_free, dev, "free_pages");
+    p.taken = lengths(a[6], 1, dev, "taken");
+    p.T = int32(a[7]);
+    if (p.T < 0) return PyLong_FromLong(MOE_LORA_ERR_INVALID_ARG);
+    PyObject* o = a[8];
+    const bool given = o != Py_None;
+    if (given && !PyDict_Check(o)) refuse("outputs must be a dict");
+    if (given) Py_INCREF(o);
+    else if ((o = PyDict_New()) == nullptr) throw Refused();
+    int st;
+    try {
+      const struct {
+        PyObject* key;
+        const char* name;
+        int64_t n;
+        int32_t** at;
+      } outs[5] = {{kKvLens, "kv_lens", B, &p.kv_lens},
+                   {kQueryOffsets, "query_offsets", B + 1, &p.query_offsets},
+                   {kSlotMap, "slot_map", p.T, &p.slot_map},
+                   {kPositions, "positions", p.T, &p.positions},
+                   {kTaken, "taken", 1, &p.taken_out}};
+      Results results(dev, a[10]);
+      bool have[5];
+      for (int i = 0; i < 5; ++i) {
+        PyObject* v = given ? PyDict_GetItem(o, outs[i].key) : nullptr;
+        have[i] = v != nullptr && v != Py_None;
+        if (have[i]) *outs[i].at = const_cast<int32_t*>(lengths(v, outs[i].n, dev, outs[i].name));
+        else results.expect({outs[i].n}, ScalarType::Int);
+      }
+      for (int i = 0; i < 5; ++i) {
+        if (have[i]) continue;
+        Tensor made = results.make({outs[i].n}, ScalarType::Int);
+        *outs[i].at = static_cast<int32_t*>(made.data_ptr());
+        handed_over(made, a[10], dev);
+        PyObject* w = THPVariable_Wrap(std::move(made));
+        if (w == nullptr) throw Refused();
+        const int bad = PyDict_SetItem(o, outs[i].key, w);
+        Py_DECREF(w);
+        if (bad) throw Refused();
+      }
+      size_t bytes;
+      void* ws = workspace_of(a[9], dev, bytes);
+      st = g_page_tables(h, &p, ws, bytes, stream_of(a[10], dev));
+    } catch (...) {
+      Py_DECREF(o);
+      throw;
+    }
+    if (st != 0) {
+      Py_DECREF(o);
+      return PyLong_FromLong(st);
+    }
+    return o;
+  });
+}
+
+// (handle, k, v, k_cache, v_cache, slot_map, workspace, stream)
+PyObject* cache_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    need_args(n, 8);
+    const Tensor& k = tensor(a[1], "k");
+    if (k.dim() != 3 || !k.is_cuda()) refuse(k, "k", "a bf16 CUDA tensor [T, heads, D]");
+    const at::Device dev = k.device();
+    moe_lora_handle* h = handle_of(a[0], dev);
+    const int64_t T = k.size(0), H = k.size(1), D = k.size(2);
+    heads(a[1], T, H, D, dev, "k");
+    const Tensor& v = heads(a[2], T, H, D, dev, "v");
+    const Tensor& kc = cache_of(a[3], H, D, dev, nullptr, "k_cache");
+    const Tensor& vc = cache_of(a[4], H, D, dev, &kc, "v_cache");
+    moe_lora_cache_write_args p;
+    p.k = static_cast<const moe_lora_bf16*>(k.data_ptr());
+    p.v = static_cast<const moe_lora_bf16*>(v.data_ptr());
+    p.k_cache = static_cast<moe_lora_bf16*>(kc.data_ptr());
+    p.v_cache = static_cast<moe_lora_bf16*>(vc.data_ptr());
+    p.slot_map = lengths(a[5], T, dev, "slot_map");
+    p.k_stride_t = k.stride(0);
+    p.k_stride_h = k.stride(1);
+    p.v_stride_t = v.stride(0);
+    p.v_stride_h = v.stride(1);
+    p.k_stride_page = kc.stride(0);
+    p.k_stride_head = kc.stride(1);
+    p.k_stride_token = kc.stride(2);
+    p.v_stride_page = vc.stride(0);
+    p.v_stride_head = vc.stride(1);
+    p.v_stride_token = vc.stride(2);
+    p.T = size(T, "k");
+    p.heads = size(H, "k");
+    p.head_dim = size(D, "k");
+    p.num_pages = size(kc.size(0), "k_cache");
+    p.page_size = size(kc.size(2), "k_cache");
+    size_t bytes;
+    void* ws = workspace_of(a[6], dev, bytes);
+    return PyLong_FromLong(g_cache_write(h, &p, ws, bytes, stream_of(a[7], dev)));
+  });
+}
+
+// (handle, q, k_cache, v_cache, block_tables, kv_lens, query_offsets, max_query_len, scale, shared_len, out, lse or
+//  whether it is wanted, workspace, stream)
+PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    need_args(n, 14);
+    const Tensor& q = tensor(a[1], "q");
+    if (q.dim() != 3 || !q.is_cuda()) refuse(q, "q", "a bf16 CUDA tensor [T, heads, D]");
+    const at::Device dev = q.device();
+    moe_lora_handle* h = handle_of(a[0], dev);
+    const int64_t T = q.size(0), Hq = q.size(1), D = q.size(2);
+    heads(a[1], T, Hq, D, dev, "q");
+    const Tensor& kc = cache_of(a[2], -1, D, dev, nullptr, "k_cache");
+    const Tensor& vc = cache_of(a[3], -1, D, dev, &kc, "v_cache");
+    const Tensor& table = block_tables(a[4]);
+    if (table.device() != dev) refuse(table, "block_tables", "a tensor" + on(dev));
+    const int64_t B = table.size(0);
+    moe_lora_attention_args p;
+    p.q = static_cast<const moe_lora_bf16*>(q.data_ptr());
+    p.k_cache = static_cast<const moe_lora_bf16*>(kc.data_ptr());
+    p.v_cache = static_cast<const moe_lora_bf16*>(vc.data_ptr());
+    p.block_tables = static_cast<const int32_t*>(table.data_ptr());
+    p.table_stride = B > 1 ? table.stride(0) : table.size(1);
+    p.kv_lens = lengths(a[5], B, dev, "kv_lens");
+    if (a[6] == Py_None && T != B)
+      refuse("without query_offsets q has a row for each of the " + std::to_string(B) + " requests, got " + std::to_string(T));
+    p.query_offsets = a[6] == Py_None ? nullptr : lengths(a[6], B + 1, dev, "query_offsets");
+    p.T = size(T, "q");
+    p.B = size(B, "block_tables");
+    p.q_heads = size(Hq, "q");
+    p.k_heads = size(kc.size(1), "k_cache");
+    if (p.k_heads < 1 || p.q_heads % p.k_heads != 0)
+      refuse("the heads of q, " + std::to_string(Hq) + ", must be a multiple of those of k_cache, " + std::to_string(p.k_heads));
+    p.head_dim = size(D, "q");
+    p.num_pages = size(kc.size(0), "k_cache");
+    p.page_size = size(kc.size(2), "k_cache");
+    p.table_width = size(table.size(1), "block_tables");
+    p.max_query_len = a[7] == Py_None ? (a[6] == Py_None ? 1 : p.T) : int32(a[7]);
+    p.scale = a[8] == Py_None ? 1.0f / std::sqrt(static_cast<float>(D)) : static_cast<float>(number(a[8]));
+    p.shared_len = int32(a[9]);
+    p.q_stride_t = q.stride(0);
+    p.q_stride_h = q.stride(1);
+    p.k_stride_page = kc.stride(0);
+    p.k_stride_head = kc.stride(1);
+    p.k_stride_token = kc.stride(2);
+    p.v_stride_page = vc.stride(0);
+    p.v_stride_head = vc.stride(1);
+    p.v_stride_token = vc.stride(2);
+    const bool lse_given = THPVariable_Check(a[11]), with_lse = lse_given || truth(a[11]);
+    Tensor made[2];
+    Results results(dev, a[13]);
+    if (a[10] == Py_None) results.expect({T, Hq, D}, ScalarType::BFloat16);
+    if (with_lse && !lse_given) results.expect({T, Hq}, ScalarType::Float);
+    if (a[10] == Py_None) made[0] = results.make({T, Hq, D}, ScalarType::BFloat16);
+    const Tensor& out = a[10] == Py_None ? made[0] : heads(a[10], T, Hq, D, dev, "out");
+    p.out = static_cast<moe_lora_bf16*>(out.data_ptr());
+    p.out_stride_t = out.stride(0);
+    p.out_stride_h = out.stride(1);
+    p.lse = nullptr;
+    if (lse_given) {
+      p.lse = static_cast<float*>(dense_out(tensor(a[11], "lse"), T, Hq, ScalarType::Float, dev, "lse"));
+    } else if (with_lse) {
+      made[1] = results.make({T, Hq}, ScalarType::Float);
+      p.lse = static_cast<float*>(made[1].data_ptr());
+    }
+    size_t bytes;
+    void* ws = workspace_of(a[12], dev, bytes);
+    Tensor scratch;
+    if (ws == nullptr) {
+      const int st = g_attention_workspace(p.T, p.q_heads, p.k_heads, p.head_dim, &bytes);
+      if (st != 0) return PyLong_FromLong(st);
+      scratch = allocate({static_cast<int64_t>(bytes)}, ScalarType::Byte, dev, a[13]);
+      ws = scratch.data_ptr();
+    }
+    for (const Tensor& t : made) handed_over(t, a[13], dev);
+    const int st = g_attention(h, &p, ws, bytes, stream_of(a[13], dev));
+    if (st != 0) return PyLong_FromLong(st);
+    PyObject* o = a[10];
+    if (o == Py_None) {
+      if ((o = THPVariable_Wrap(std::move(made[0]))) == nullptr) throw Refused();
+    } else {
+      Py_INCREF(o);
+    }
+    if (!with_lse) return o;
+    PyObject* e = a[11];
+    if (lse_given) Py_INCREF(e);
+    else if ((e = THPVariable_Wrap(std::move(made[1]))) == nullptr) {
+      Py_DECREF(o);
+      throw Refused();
+    }
+    PyObject* r = PyTuple_Pack(2, o, e);
+    Py_DECREF(o);
+    Py_DECREF(e);
+    if (r == nullptr) throw Refused();
+    return r;
+  });
+}
+
+// (addresses of select_experts, linear, linear_workspace_size, qk_norm_rope, device, page_tables, cache_write,
+//  attention, attention_workspace_size)
 PyObject* entry_points(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
-    need_args(n, 5);
-    void* at[5];
-    for (int i = 0; i < 5; ++i)
+    need_args(n, 9);
+    void* at[9];
+    for (int i = 0; i < 9; ++i)
       if ((at[i] = PyLong_AsVoidPtr(a[i])) == nullptr) refuse("an entry point is missing");
     g_select = reinterpret_cast<decltype(g_select)>(at[0]);
     g_linear = reinterpret_cast<decltype(g_linear)>(at[1]);
     g_linear_workspace = reinterpret_cast<decltype(g_linear_workspace)>(at[2]);
     g_qk = reinterpret_cast<decltype(g_qk)>(at[3]);
     g_device = reinterpret_cast<decltype(g_device)>(at[4]);
+    g_page_tables = reinterpret_cast<decltype(g_page_tables)>(at[5]);
+    g_cache_write = reinterpret_cast<decltype(g_cache_write)>(at[6]);
+    g_attention = reinterpret_cast<decltype(g_attention)>(at[7]);
+    g_attention_workspace = reinterpret_cast<decltype(g_attention_workspace)>(at[8]);
     Py_RETURN_NONE;
   });
 }
 
 #define ML_METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef kMethods[] = {ML_METHOD(select_experts), ML_METHOD(adapters),     ML_METHOD(linear),
-                          ML_METHOD(qk_norm_rope),   ML_METHOD(entry_points), {nullptr, nullptr, 0, nullptr}};
+                          ML_METHOD(qk_norm_rope),   ML_METHOD(page_tables),  ML_METHOD(cache_write),
+                          ML_METHOD(attention),      ML_METHOD(entry_points), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
@@ -501,5 +760,10 @@ PyMODINIT_FUNC PyInit__marshal(void) {
   kIds = PyUnicode_InternFromString("topk_ids");
   kWeights = PyUnicode_InternFromString("topk_weights");
   kPacked = PyUnicode_InternFromString("packed_topk_ids");
+  kKvLens = PyUnicode_InternFromString("kv_lens");
+  kQueryOffsets = PyUnicode_InternFromString("query_offsets");
+  kSlotMap = PyUnicode_InternFromString("slot_map");
+  kPositions = PyUnicode_InternFromString("positions");
+  kTaken = PyUnicode_InternFromString("taken");
   return PyModule_Create(&kModule);
 }

@@ -22,6 +22,7 @@ enum : uint32_t {
   kWhereRouteBarrier = 1, kWhereGemmProducer = 2, kWhereGemmMma = 3, kWhereGemmEpilogue = 4,
   kWhereLoraShrinkGu = 5, kWhereLoraExpandGu = 6, kWhereLoraShrinkDn = 7, kWhereFinalize = 8,
   kWhereLoraShrinkTc = 9, kWhereRouteExpert = 10, kWhereQkPosition = 11, kWhereLinear = 12,
+  kWherePageTables = 13, kWhereCacheWrite = 14, kWhereAttention = 15,
 };
 
 struct LoraSlots {
