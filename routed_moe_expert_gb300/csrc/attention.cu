@@ -1,6 +1,8 @@
-// Causal attention to a paged cache (moe_lora_attention): the entry point and the kernel for any layout.
+// Causal attention to a paged cache (moe_lora_attention): the entry point, the kernel for any layout, and the
+// sum of the pieces of items that were cut.
 #include "attention.h"
 #include "host.h"
+#include "linear.h"
 
 #include <algorithm>
 #include <cmath>
@@ -30,7 +32,7 @@ __global__ void __launch_bounds__(32 * kAnyWarps) attention_any_kernel(const __g
     for (int d = threadIdx.x; d < p.D; d += blockDim.x) q_s[d] = bf2f(p.q[row * p.q_t + h * p.q_h + d]);
     __syncthreads();
     const int sees = max(r.kv - r.n + i + 1, 0);
-    const int of_shared = min(sees, p.shared_len);
+    const int of_shared = min(sees, p.shared);
     float m = -INFINITY, l = 0.0f;
     float o[16];
 #pragma unroll
@@ -98,13 +100,161 @@ __global__ void __launch_bounds__(32 * kAnyWarps) attention_any_kernel(const __g
   }
 }
 
+
+// ---------------------------------------------------------------------------------------
+// The pieces of an item together: a block a record and row (rows blockIdx.y, + gridDim.y, ...).  Sixteen
+// groups of threads take the pieces in turn, DP / 8 threads a group with eight values each, so that a long
+// request's 76 pieces are five loads deep; the groups are added in order.  Blocks without a record leave at
+// once.  The shared keys' part comes on top.
+// ---------------------------------------------------------------------------------------
+constexpr int kGroups = 16;
+
+template <int DP>
+__global__ void __launch_bounds__(kGroups * DP / 8) attention_join_kernel(const __grid_constant__ AttentionParams p) {
+  constexpr int kLanes = DP / 8;
+  __shared__ float o_s[kGroups][DP];
+  __shared__ float m_s[kGroups], l_s[kGroups];
+  pdl_wait();
+  pdl_trigger();
+  const PieceRecord c = p.records[blockIdx.x];
+  if (c.pieces == 0) return;
+  const int group = threadIdx.x / kLanes, d = (threadIdx.x % kLanes) * 8;
+  for (int r = static_cast<int>(blockIdx.y); r < c.rows; r += static_cast<int>(gridDim.y)) {
+    float m = -INFINITY, l = 0.0f, o[8] = {};
+#pragma unroll 4
+    for (int i = group; i < c.pieces; i += kGroups) {
+      const int slot = i == 0 ? c.slot : 2 * (static_cast<int>(blockIdx.x) + i);
+      const long long at = static_cast<long long>(slot) * p.item_rows + r;
+      const float2 ml = p.piece_ml[at];
+      const float4* src = reinterpret_cast<const float4*>(p.piece_o + at * DP + d);
+      const float4 x = src[0], y = src[1];
+      const float top = fmaxf(m, ml.x), ref = reference_of(top);
+      const float f = exp2_approx(m - ref), g = exp2_approx(ml.x - ref);
+      m = top;
+      l = l * f + ml.y * g;
+      const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) o[k] = o[k] * f + v[k] * g;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) o_s[group][d + k] = o[k];
+    if (d == 0) {
+      m_s[group] = m;
+      l_s[group] = l;
+    }
+    __syncthreads();
+    if (group == 0) {
+      for (int g = 0; g < kGroups; ++g) m = fmaxf(m, m_s[g]);
+      const float ref = reference_of(m);
+      l = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) o[k] = 0.0f;
+      for (int g = 0; g < kGroups; ++g) {
+        const float f = exp2_approx(m_s[g] - ref);
+        l += l_s[g] * f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) o[k] += o_s[g][d + k] * f;
+      }
+      const long long token = c.q0 + (c.row0 + r) / p.G;
+      const int head = c.kh * p.G + (c.row0 + r) % p.G;
+      add_prefix<DP>(p, token * p.Hq + head, d, m, l, o);
+      write_row8(p, token, head, d, m, l, o);
+    }
+    __syncthreads();
+  }
+}
+
+cudaError_t launch_join(const AttentionParams& p, int dp, int across, cudaStream_t stream) {
+  const dim3 grid(p.plan.ctas, across), block(kGroups * dp / 8);
+  return dp == 64 ? launch_k(attention_join_kernel<64>, grid, block, 0, stream, true, p)
+                  : launch_k(attention_join_kernel<128>, grid, block, 0, stream, true, p);
+}
+
+// ---------------------------------------------------------------- workspace
+// The status word, then the records, then the pieces (2 slots a block), then the shared keys' part of each row.
+// Every part grows with T alone, so what is enough for T rows is enough for fewer.
+constexpr int kMaxSms = 160;   // blocks are a multiple of the GPU's 152
+constexpr int kPrefixSplits = 64, kPrefixBlocks = 2 * kMaxSms;
+constexpr size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+struct Workspace {
+  size_t records, ml, o, prefix_ml, prefix_o, bytes;
+};
+int slot_rows(bool tiles, long long T, int G) {
+  return static_cast<int>(std::min<long long>(tiles ? kTileRows : kFewRows, T * G));
+}
+Workspace workspace_for(int T, int Hq, int Hk, int D) {
+  const int G = Hq / Hk, dp = D <= 64 ? 64 : 128;
+  const size_t slots = std::max<size_t>(2 * kFewPerSm * kMaxSms * slot_rows(false, T, G), 2 * kMaxSms * slot_rows(true, T, G));
+  // rows x splits of the shared keys' launch: splits <= kPrefixBlocks / items + 1, rows <= 256 items
+  const size_t rows = static_cast<size_t>(T) * Hq;
+  const size_t parts = std::min<size_t>(kPrefixSplits * rows, kPrefixBlocks * kTileRows + rows);
+  Workspace w;
+  w.records = 256;
+  w.ml = w.records + round256(sizeof(PieceRecord) * kFewPerSm * kMaxSms);
+  w.o = w.ml + round256(sizeof(float2) * slots);
+  w.prefix_ml = w.o + round256(sizeof(float) * slots * dp);
+  w.prefix_o = w.prefix_ml + round256(sizeof(float2) * parts);
+  w.bytes = w.prefix_o + round256(sizeof(float) * parts * dp);
+  return w;
+}
+
+// Splits of the shared keys: the least time by units, a part costing about three more (its query tile, its
+// result) than its keys.
+PrefixRun prefix_run(int T, int G, int Hk, int keys, int sms) {
+  PrefixRun r;
+  r.units = keys / kTileKeys;
+  r.row_tiles = static_cast<int>((static_cast<long long>(T) * G + kTileRows - 1) / kTileRows);
+  const long long items = static_cast<long long>(r.row_tiles) * Hk;
+  r.splits = 1;
+  long long best = -1;
+  const long long most = std::min<long long>({r.units, kPrefixSplits, kPrefixBlocks / items + 1});
+  for (int s = 1; s <= most; ++s) {
+    const long long cost = (items * s + sms - 1) / sms * ((r.units + s - 1) / s + 3);
+    if (best < 0 || cost < best) {
+      best = cost;
+      r.splits = s;
+    }
+  }
+  return r;
+}
+
+// The caches' tensor map: 64 values of up to `keys` tokens of a page at a time.  Extents of one have no stride
+// of their own.
+CUresult page_map(moe_lora_handle* h, CUtensorMap* m, const void* base, const AttentionParams& p, long long s_token,
+                  long long s_head, long long s_page, int keys) {
+  const long long any = 2LL * p.D;   // (D is a multiple of 8)
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(p.D), static_cast<cuuint64_t>(p.page), static_cast<cuuint64_t>(p.Hk),
+                              static_cast<cuuint64_t>(p.num_pages)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(p.page > 1 ? 2 * s_token : any),
+                                 static_cast<cuuint64_t>(p.Hk > 1 ? 2 * s_head : any),
+                                 static_cast<cuuint64_t>(p.num_pages > 1 ? 2 * s_page : any)};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(p.page < keys ? p.page : keys), 1, 1};
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  return h->encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, ones,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
+// Whether whole 16-byte pieces and the caches' maps can be used.
+bool fast_layout(const moe_lora_attention_args* a) {
+  if (a->head_dim % 8 != 0 || a->head_dim > 128 || a->page_size < 16 || (a->page_size & (a->page_size - 1)) != 0 ||
+      a->num_pages < 1 || a->table_width < 1)
+    return false;
+  if (!aligned16(a->q) || !aligned16(a->k_cache) || !aligned16(a->v_cache) || a->q_stride_t % 8 != 0 || a->q_stride_h % 8 != 0)
+    return false;
+  const long long limit = 1LL << 38;   // of a map's strides, in elements
+  auto fits = [&](long long s, int extent) { return extent <= 1 || (s > 0 && s < limit && s % 8 == 0); };
+  return fits(a->k_stride_token, a->page_size) && fits(a->v_stride_token, a->page_size) && fits(a->k_stride_head, a->k_heads) &&
+         fits(a->v_stride_head, a->k_heads) && fits(a->k_stride_page, a->num_pages) && fits(a->v_stride_page, a->num_pages);
+}
+
 }  // namespace
 }  // namespace mlk
 
 extern "C" moe_lora_status moe_lora_attention_workspace_size(int T, int q_heads, int k_heads, int head_dim, size_t* bytes) {
   if (bytes == nullptr || T < 0 || q_heads < 1 || k_heads < 1 || q_heads % k_heads != 0 || head_dim < 1)
     return MOE_LORA_ERR_INVALID_ARG;
-  *bytes = 256;
+  *bytes = mlk::workspace_for(T, q_heads, k_heads, head_dim).bytes;
   return MOE_LORA_OK;
 }
 
@@ -162,13 +312,70 @@ extern "C" moe_lora_status moe_lora_attention(moe_lora_handle* h, const moe_lora
   p.num_pages = a->num_pages;
   p.page = a->page_size;
   p.width = a->table_width;
-  p.shared_len = a->shared_len;
+  p.shared = a->shared_len;
   p.scale_log2 = a->scale * 1.4426950408889634f;
   p.status = static_cast<uint32_t*>(workspace);
+  p.flags = reinterpret_cast<int*>(h->linear_flags + kLinearFlags);
+  p.prefix_splits = 0;
+  p.out_vec = aligned16(p.out) && p.o_t % 8 == 0 && p.o_h % 8 == 0;
+  p.records = nullptr;
   ML_ON_DEVICE(h);
-  ML_CUDA(cudaMemsetAsync(workspace, 0, 4, stream), "attention status");
-  const int across = std::max(1, std::min(a->T, 65536 / std::max(1, a->B)));
-  ML_LAUNCH(h, launch_k(attention_any_kernel, dim3(across, a->B, a->q_heads), dim3(32 * kAnyWarps), 0, stream, false, p),
+  if (!fast_layout(a) || p.scale_log2 == 0.0f || h->num_sms > kMaxSms) {
+    ML_CUDA(cudaMemsetAsync(workspace, 0, 4, stream), "attention status");
+    const int across = std::max(1, std::min(a->T, 65536 / std::max(1, a->B)));
+    ML_LAUNCH(h, launch_k(attention_any_kernel, dim3(across, a->B, a->q_heads), dim3(32 * kAnyWarps), 0, stream, false, p),
+              "attention launch");
+    return MOE_LORA_OK;
+  }
+  if (!h->attention_ready) {
+    ML_CUDA(prepare_attention_rows(), "attention shared memory");
+    ML_CUDA(prepare_attention_tiles(), "attention shared memory");
+    h->attention_ready = true;
+  }
+  const int dp = p.D <= 64 ? 64 : 128;
+  p.page_log2 = 0;
+  while ((1 << p.page_log2) < p.page) ++p.page_log2;
+  const Workspace at = workspace_for(p.T, p.Hq, p.Hk, p.D);
+  uint8_t* base = static_cast<uint8_t*>(workspace);
+  p.piece_ml = reinterpret_cast<float2*>(base + at.ml);
+  p.piece_o = reinterpret_cast<float*>(base + at.o);
+  p.prefix_ml = reinterpret_cast<float2*>(base + at.prefix_ml);
+  p.prefix_o = reinterpret_cast<float*>(base + at.prefix_o);
+  p.shared = a->B > 1 ? a->shared_len / kTileKeys * kTileKeys : 0;   // the rest is each request's own
+  auto maps = [&](int keys) {
+    return page_map(h, &p.tmap_k, p.k, p, p.k_t, p.k_h, p.k_p, keys) == CUDA_SUCCESS &&
+           page_map(h, &p.tmap_v, p.v, p, p.v_t, p.v_h, p.v_p, keys) == CUDA_SUCCESS;
+  };
+  const bool tiles = static_cast<long long>(a->max_query_len) * p.G > kFewRows;
+  if ((tiles || p.shared > 0) && !maps(kTileKeys)) return cuda_fail(cudaErrorInvalidValue, "attention tensor maps");
+  if (p.shared > 0) {
+    const PrefixRun run = prefix_run(p.T, p.G, p.Hk, p.shared, h->num_sms);
+    const long long blocks = static_cast<long long>(run.row_tiles) * p.Hk * run.splits;
+    if (blocks > 0x7fffffff) return MOE_LORA_ERR_UNSUPPORTED;
+    p.plan = Plan{};
+    ML_LAUNCH(h, launch_attention_tiles(p, run, static_cast<int>(blocks), dp, stream), "attention prefix launch");
+    p.prefix_splits = run.splits;
+  }
+  p.item_rows = slot_rows(tiles, p.T, p.G);
+  const long long own_keys = static_cast<long long>(p.width) * p.page - p.shared;   // of a request, at most
+  int join_across;
+  if (tiles) {
+    p.plan.ctas = h->num_sms;
+    p.plan.least = 2;
+    p.plan.whole = own_keys <= 2LL * kTileKeys;
+    p.long_queries = static_cast<long long>(a->max_query_len) * p.G > 8LL * kTileRows;
+    join_across = std::max(1, p.item_rows / 8);
+  } else {
+    if (!maps(kFewKeys)) return cuda_fail(cudaErrorInvalidValue, "attention tensor maps");
+    p.plan.ctas = kFewPerSm * h->num_sms;
+    p.plan.least = 8;
+    p.plan.whole = own_keys <= 16LL * kFewKeys;
+    p.long_queries = 0;
+    join_across = std::max(1, p.item_rows / 2);
+  }
+  if (!p.plan.whole) p.records = reinterpret_cast<PieceRecord*>(base + at.records);
+  ML_LAUNCH(h, tiles ? launch_attention_tiles(p, PrefixRun{}, p.plan.ctas, dp, stream) : launch_attention_rows(p, dp, stream),
             "attention launch");
+  if (!p.plan.whole) ML_LAUNCH(h, launch_join(p, dp, join_across, stream), "attention join launch");
   return MOE_LORA_OK;
 }

@@ -5,18 +5,57 @@
 
 namespace mlk {
 
+// How a call's work is dealt out.  Rows of a request and key head are its query rows times the G query
+// heads of that key head, row r being token r / G and head r % G: a key is read once for all of them.  An
+// item is up to `rows` of them (Plan::rows) with the keys that its last row sees, cut into units of
+// `keys` keys.  The units of all items, one request after another, are dealt to the blocks in equal runs,
+// whatever the requests' lengths (which only the device knows): a block works on the end of one item, whole
+// items, and the start of another.  Where a run holds part of an item its result is a piece (unnormalised
+// sums, maximum, sum of weights) in the workspace, at most two a block, and the block that has the item's
+// first unit leaves a record, by which the kernel that follows adds the pieces up.
+//
+// With `whole` (no item is long) items are not cut: a block takes those whose first unit is in its run.
+struct Plan {
+  int ctas;          // blocks of the launch
+  int least;         // units that a block takes at least, when that leaves blocks without work
+  int whole;
+};
+
+struct PieceRecord {
+  int pieces;        // 0: the block starts no item that was cut
+  int slot;          // of the first piece; the others are the first slots of the blocks that follow
+  int q0, kh;        // the request's first row, the key head
+  int row0, rows;    // rows of the item
+  int unused[2];
+};
+
 struct AttentionParams {
+  CUtensorMap tmap_k, tmap_v;                  // {D, page, Hk, pages}, box {64, keys of a page or unit, 1, 1}
   const __nv_bfloat16 *q, *k, *v;
   const int32_t *tables, *kv_lens, *offsets;   // offsets null: row b is request b's
   __nv_bfloat16* out;
   float* lse;
   long long q_t, q_h, o_t, o_h, k_p, k_h, k_t, v_p, v_h, v_t, table_stride;
   int T, B, Hq, Hk, G, D;
-  int num_pages, page, width;
-  int shared_len;
+  int num_pages, page, page_log2, width;
+  int shared;                                  // keys that are read from request 0's table
+  int long_queries;                            // requests have many items each
+  int out_vec;                                 // rows of `out` start on 16-byte boundaries
   float scale_log2;                            // scale * log2(e): weights are powers of two
+  Plan plan;
+  PieceRecord* records;                        // [ctas], null with `whole`
+  int item_rows;                               // rows of a piece's slot
+  float2* piece_ml;                            // [2 ctas][item_rows] maximum (of scaled scores, base 2), sum
+  float* piece_o;                              // [2 ctas][item_rows][DP]
+  // The shared keys' part of every row, made by a launch of its own: [prefix_splits][T * Hq]
+  float2* prefix_ml;
+  float* prefix_o;
+  int prefix_splits;                           // 0: none
   uint32_t* status;
+  int* flags;                                  // the handle's: error gathered so far, blocks that are done
 };
+
+constexpr float kLn2 = 0.693147180559945f;
 
 // A request's rows [q0, q0 + n) and its keys, checked: rows within [0, T), at most width * page keys.
 struct Request {
@@ -41,5 +80,339 @@ MLDEV Request request_of(const AttentionParams& p, int b) {
   r.kv = static_cast<int>(min(static_cast<long long>(max(kv, 0)), room));
   return r;
 }
+
+MLDEV float exp2_approx(float x) {   // 2^-22 relative; 0 for -inf
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The reference that weights are taken relative to: 0 while nothing is seen, so that they are 0 and not NaN.
+MLDEV float reference_of(float m) { return m == -INFINITY ? 0.0f : m; }
+
+// ---------------------------------------------------------------- the plan, worked out by every block
+template <int ROWS, int KEYS>
+struct Schedule {
+  // of this launch and block
+  int ctas;              // blocks that work
+  long long units;       // of the call
+  long long start, end;  // this block's run
+  bool bad;
+
+  // Units of item i of a request (at least one, so that rows that see nothing are written).
+  static MLDEV int units_of(const AttentionParams& p, const Request& r, int i) {
+    const int sees = seen_by(p, r, i) - p.shared;
+    return sees <= 0 ? 1 : (sees + KEYS - 1) / KEYS;
+  }
+  // Keys that the last row of item i sees.
+  static MLDEV int seen_by(const AttentionParams& p, const Request& r, int i) {
+    const long long last = min(static_cast<long long>(i + 1) * ROWS, static_cast<long long>(r.n) * p.G) - 1;
+    return max(r.kv - r.n + static_cast<int>(last / p.G) + 1, 0);
+  }
+  static MLDEV int items_of(const AttentionParams& p, const Request& r) {
+    return static_cast<int>((static_cast<long long>(r.n) * p.G + ROWS - 1) / ROWS);
+  }
+
+  // The block that has unit u.
+  MLDEV int block_of(long long u) const { return static_cast<int>(((u + 1) * ctas - 1) / units); }
+  MLDEV long long start_of(int c) const { return units * c / ctas; }
+};
+
+// A place in the schedule, advanced item by item; every role of a block walks through the same ones.
+template <int ROWS, int KEYS>
+struct Walk {
+  using S = Schedule<ROWS, KEYS>;
+  int b, kh, i, items, units;   // of the request's items; units of this item
+  long long u0;                 // the item's first unit
+  Request r;
+
+  MLDEV void enter(const AttentionParams& p) {   // the first item of request b, or of one behind it that has any
+    while (b < p.B) {
+      r = request_of(p, b);
+      items = S::items_of(p, r);
+      if (items > 0) break;
+      ++b;
+    }
+    kh = i = 0;
+    if (b < p.B) units = S::units_of(p, r, 0);
+  }
+  MLDEV void next(const AttentionParams& p) {
+    u0 += units;
+    if (++i == items) {
+      i = 0;
+      if (++kh == p.Hk) {
+        ++b;
+        enter(p);
+        return;
+      }
+    }
+    if (items > 1) units = S::units_of(p, r, i);
+  }
+};
+
+struct ScheduleSmem {
+  long long sums[32], head[2];
+  int items[32];
+  long long found_base;
+  int found_b, found_i, bad;
+  long long found_u;
+};
+
+// Works out the schedule and the block's first item.  All threads of the block; `sums_s` [blockDim] scratch.
+template <int ROWS, int KEYS>
+MLDEV void make_schedule(const AttentionParams& p, int cta, Schedule<ROWS, KEYS>& s, Walk<ROWS, KEYS>& w, ScheduleSmem& sm,
+                         long long* sums_s) {
+  using S = Schedule<ROWS, KEYS>;
+  const int tid = threadIdx.x, NT = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = NT >> 5;
+  // the units of request b0 + tid (and its items), for a chunk of NT requests
+  auto chunk = [&](int b0, int& items, bool& bad) -> long long {
+    long long sum = 0;
+    items = 0;
+    if (!p.long_queries) {
+      if (b0 + tid < p.B) {
+        const Request r = request_of(p, b0 + tid);
+        const int n = S::items_of(p, r);
+        for (int i = 0; i < n; ++i) sum += S::units_of(p, r, i);
+        items = n;
+        bad = bad || r.bad;
+      }
+      return sum * p.Hk;
+    }
+    for (int k = warp; k < NT && b0 + k < p.B; k += warps) {   // a warp a request
+      const Request r = request_of(p, b0 + k);
+      const int n = S::items_of(p, r);
+      long long part = 0;
+      for (int i = lane; i < n; i += 32) part += S::units_of(p, r, i);
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) part += __shfl_xor_sync(0xffffffffu, part, off);
+      if (lane == 0) sums_s[k] = part;
+      bad = bad || r.bad;
+    }
+    __syncthreads();
+    if (b0 + tid < p.B) {
+      sum = sums_s[tid];
+      items = S::items_of(p, request_of(p, b0 + tid));
+    }
+    __syncthreads();
+    return sum * p.Hk;
+  };
+  bool bad = false;
+  long long total = 0, mine = 0;
+  long long all_items = 0;
+  for (int b0 = 0; b0 < p.B; b0 += NT) {
+    int items;
+    mine = chunk(b0, items, bad);
+    total += mine;
+    all_items += static_cast<long long>(items) * p.Hk;
+  }
+  long long t = total, n = all_items;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    t += __shfl_xor_sync(0xffffffffu, t, off);
+    n += __shfl_xor_sync(0xffffffffu, n, off);
+  }
+  if (lane == 0) {
+    sm.sums[warp] = t;
+    sm.items[warp] = static_cast<int>(min(n, 0x3fffffffll));
+  }
+  s.bad = __syncthreads_or(bad) != 0;
+  t = n = 0;
+  for (int i = 0; i < warps; ++i) {
+    t += sm.sums[i];
+    n += sm.items[i];
+  }
+  s.units = t;
+  const long long want = max(t / p.plan.least, min(n, static_cast<long long>(p.plan.ctas)));
+  s.ctas = static_cast<int>(max(1ll, min(want, static_cast<long long>(p.plan.ctas))));
+  s.start = s.start_of(min(cta, s.ctas));
+  s.end = cta < s.ctas ? s.start_of(cta + 1) : s.start;
+  w.b = p.B;
+  if (s.start == s.end) return;
+  // the request that has unit `start`
+  __syncthreads();
+  long long base = 0;
+  for (int b0 = 0; b0 < p.B; b0 += NT) {
+    if (p.B > NT) {
+      int items;
+      bool ignored = false;
+      mine = chunk(b0, items, ignored);
+    }
+    long long incl = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += u;
+    }
+    if (lane == 31) sm.sums[warp] = incl;
+    __syncthreads();
+    long long before = base, all = 0;
+    for (int i = 0; i < warps; ++i) {
+      if (i < warp) before += sm.sums[i];
+      all += sm.sums[i];
+    }
+    if (before + incl - mine <= s.start && s.start < before + incl) {
+      sm.found_b = b0 + tid;
+      sm.found_base = before + incl - mine;
+    }
+    base += all;
+    __syncthreads();
+    if (s.start < base) break;
+  }
+  // its key head and item
+  w.b = sm.found_b;
+  w.r = request_of(p, w.b);
+  w.items = S::items_of(p, w.r);
+  w.u0 = sm.found_base;
+  if (w.items == 1) {
+    w.units = S::units_of(p, w.r, 0);
+    w.kh = static_cast<int>((s.start - w.u0) / w.units);
+    w.u0 += static_cast<long long>(w.kh) * w.units;
+    w.i = 0;
+    return;
+  }
+  if (warp == 0) {
+    long long per = 0;
+    for (int i = lane; i < w.items; i += 32) per += S::units_of(p, w.r, i);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) per += __shfl_xor_sync(0xffffffffu, per, off);
+    const int kh = static_cast<int>((s.start - w.u0) / per);
+    long long at = w.u0 + kh * per;   // first unit of items i0..
+    for (int i0 = 0; i0 < w.items; i0 += 32) {
+      const int own = i0 + lane < w.items ? S::units_of(p, w.r, i0 + lane) : 0;
+      int incl = own;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += u;
+      }
+      if (own > 0 && at + incl - own <= s.start && s.start < at + incl) {
+        sm.found_i = i0 + lane;
+        sm.found_u = at + incl - own;
+        sm.head[0] = kh;
+      }
+      at += __shfl_sync(0xffffffffu, incl, 31);
+    }
+  }
+  __syncthreads();
+  w.i = sm.found_i;
+  w.u0 = sm.found_u;
+  w.kh = static_cast<int>(sm.head[0]);
+  w.units = S::units_of(p, w.r, w.i);
+}
+
+// What a block does of the item that a walk is at: units [lo, hi), and where the result goes.
+struct Part {
+  int lo, hi;
+  bool all;      // the whole item: the result is final
+  int slot;      // else: the piece's slot
+};
+template <int ROWS, int KEYS>
+MLDEV Part part_of(const AttentionParams& p, const Schedule<ROWS, KEYS>& s, const Walk<ROWS, KEYS>& w, int cta) {
+  Part x;
+  if (p.plan.whole) {
+    x.lo = 0;
+    x.hi = w.u0 < s.start ? 0 : w.units;   // hi 0: begun in the run of a block before
+    x.all = true;
+    x.slot = 0;
+    return x;
+  }
+  x.lo = static_cast<int>(max(s.start - w.u0, 0ll));
+  x.hi = static_cast<int>(min(s.end - w.u0, static_cast<long long>(w.units)));
+  x.all = x.lo == 0 && x.hi == w.units;
+  x.slot = 2 * cta + (w.u0 > s.start ? 1 : 0);
+  return x;
+}
+template <int ROWS, int KEYS>
+MLDEV bool more(const Schedule<ROWS, KEYS>& s, const Walk<ROWS, KEYS>& w, const AttentionParams& p) {
+  return w.b < p.B && w.u0 < s.end;
+}
+// The record of a piece that begins an item (one thread).
+template <int ROWS, int KEYS>
+MLDEV PieceRecord record_of(const AttentionParams& p, const Schedule<ROWS, KEYS>& s, const Walk<ROWS, KEYS>& w, const Part& x,
+                            int cta) {
+  PieceRecord c;
+  c.pieces = s.block_of(w.u0 + w.units - 1) - cta + 1;
+  c.slot = x.slot;
+  c.q0 = w.r.q0;
+  c.kh = w.kh;
+  c.row0 = w.i * ROWS;
+  c.rows = static_cast<int>(min(static_cast<long long>(ROWS), static_cast<long long>(w.r.n) * p.G - c.row0));
+  return c;
+}
+
+// The end of a block's work (one thread): the last block of the launch writes the status word, 0 or an
+// error that some block met, and leaves the handle's flags zero.
+MLDEV void finish_status(const AttentionParams& p, uint32_t error) {
+  if (error != 0) atomicCAS(p.flags, 0, static_cast<int>(error));
+  __threadfence();
+  if (atomicAdd(p.flags + 1, 1) == static_cast<int>(gridDim.x) - 1) {
+    __threadfence();
+    *p.status = static_cast<uint32_t>(atomicExch(p.flags, 0));
+    atomicExch(p.flags + 1, 0);
+  }
+}
+
+// Adds the shared keys' part of 8 values of a row to (m, l, o); row = token * Hq + head.
+template <int DP>
+MLDEV void add_prefix(const AttentionParams& p, long long row, int d, float& m, float& l, float (&o)[8]) {
+  const long long rows = static_cast<long long>(p.T) * p.Hq;
+  for (int s = 0; s < p.prefix_splits; ++s) {
+    const float2 ml = p.prefix_ml[s * rows + row];
+    if (ml.y == 0.0f) continue;   // (a NaN is not)
+    const float4* src = reinterpret_cast<const float4*>(p.prefix_o + (s * rows + row) * DP + d);
+    const float4 a = src[0], c = src[1];
+    const float top = fmaxf(m, ml.x), ref = reference_of(top);
+    const float f = exp2_approx(m - ref), g = exp2_approx(ml.x - ref);
+    m = top;
+    l = l * f + ml.y * g;
+    const float v[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = o[i] * f + v[i] * g;
+  }
+}
+
+// Eight values of a finished row, and its logarithm where d is 0.
+MLDEV void write_row8(const AttentionParams& p, long long token, int head, int d, float m, float l, const float (&o)[8]) {
+  const float inv = 1.0f / l;
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = l == 0.0f ? 0.0f : o[i] * inv;
+  __nv_bfloat16* at = p.out + token * p.o_t + head * p.o_h + d;
+  if (d < p.D) {   // D is a multiple of 8
+    if (p.out_vec) {
+      *reinterpret_cast<uint4*>(at) = pack8(v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) at[i] = f2bf(v[i]);
+    }
+  }
+  if (d == 0 && p.lse != nullptr) p.lse[token * p.Hq + head] = (reference_of(m) + log2f(l)) * kLn2;
+}
+
+// Box of one page's keys (or a part of a page) from the caches' maps; x a multiple of 64.
+MLDEV void tma_load_page(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int token, int head, int page,
+                         uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(token), "r"(head), "r"(page), "l"(policy)
+      : "memory");
+}
+
+// The shared keys' part of all rows, as a launch of the tiles' kernel: for every key head, tile of 256 rows
+// (token-major, as an item's) and split of the keys a block.
+struct PrefixRun {
+  int splits;      // 0: an ordinary run
+  int row_tiles;   // of a key head
+  int units;       // of 128 keys
+};
+
+// Launches (attention_rows.cu, attention_tiles.cu)
+constexpr int kFewRows = 16, kFewKeys = 64, kFewPerSm = 2;
+constexpr int kTileRows = 256, kTileKeys = 128;
+cudaError_t prepare_attention_rows();
+cudaError_t launch_attention_rows(const AttentionParams& p, int dp, cudaStream_t stream);
+cudaError_t prepare_attention_tiles();
+cudaError_t launch_attention_tiles(const AttentionParams& p, const PrefixRun& prefix, int blocks, int dp, cudaStream_t stream);
 
 }  // namespace mlk
