@@ -106,11 +106,11 @@ struct Schedule {
   }
   // Keys that the last row of item i sees.
   static MLDEV int seen_by(const AttentionParams& p, const Request& r, int i) {
-    const long long last = min(static_cast<long long>(i + 1) * ROWS, static_cast<long long>(r.n) * p.G) - 1;
-    return max(r.kv - r.n + static_cast<int>(last / p.G) + 1, 0);
+    const int last = min(i * ROWS + ROWS, r.n * p.G) - 1;   // (T * Hq is below 2^31 - 256)
+    return max(r.kv - r.n + last / p.G + 1, 0);
   }
   static MLDEV int items_of(const AttentionParams& p, const Request& r) {
-    return static_cast<int>((static_cast<long long>(r.n) * p.G + ROWS - 1) / ROWS);
+    return (r.n * p.G + ROWS - 1) / ROWS;
   }
 
   // The block that has unit u.
@@ -336,7 +336,7 @@ MLDEV PieceRecord record_of(const AttentionParams& p, const Schedule<ROWS, KEYS>
   c.q0 = w.r.q0;
   c.kh = w.kh;
   c.row0 = w.i * ROWS;
-  c.rows = static_cast<int>(min(static_cast<long long>(ROWS), static_cast<long long>(w.r.n) * p.G - c.row0));
+  c.rows = min(ROWS, w.r.n * p.G - c.row0);
   return c;
 }
 

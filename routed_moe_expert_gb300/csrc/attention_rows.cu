@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(con
       const Part x = part_of<kRows, kKeys>(p, s, w, cta);
       if (x.lo >= x.hi) continue;
       const int row0 = w.i * kRows;
-      const int rows = static_cast<int>(min(static_cast<long long>(kRows), static_cast<long long>(w.r.n) * p.G - row0));
+      const int rows = min(kRows, w.r.n * p.G - row0);
       const int sees = Sched::seen_by(p, w.r, w.i);
       const bool upper = rows > 8;   // the fragments' rows 8 to 15 are in use
       int lim_a = 0, lim_b = 0;      // keys that this lane's two rows see

@@ -14,6 +14,9 @@
 // multiplied, only when it is more than 2^8 times the weights' scale away: in float32 and bf16 weights
 // up to 256 are as exact as weights up to 1, and O, which lives in TMEM, hardly ever has to be touched.
 //
+// Up to 128 rows take both tiles too: they hold the same rows and take the units of keys in turn, and their
+// two results are added at the end (each thread finds its row's other half in its own TMEM lanes).
+//
 // Warps 0-3 and 4-7: the rows of tiles 0 and 1, a thread a row; warp 8: TMA; warp 9: MMA issue; warp 10: zeroes
 // values behind the last key that is seen (0 times an infinity would stay).  Items come from the schedule in
 // attention.h; with `prefix` the block's item is a part of the shared keys for 256 rows of the whole batch.
@@ -24,37 +27,63 @@ namespace mlk {
 namespace {
 
 constexpr int kRows = kTileRows, kKeys = kTileKeys;
-constexpr int kThreads = 352;
-constexpr int kProducer = 8, kMma = 9, kCleaner = 10;
+constexpr int kThreads = 384;
+constexpr int kProducer = 8, kMma = 9, kCleaner = 10, kScheduler = 11;
 using Sched = Schedule<kRows, kKeys>;
 using Place = Walk<kRows, kKeys>;
 
 constexpr int kHalf = kKeys * 128;   // 64 values of 128 rows
 __host__ __device__ constexpr int tile_bytes(int dp) { return dp / 64 * kHalf; }
-__host__ __device__ constexpr int slots_of(int dp) { return dp == 64 ? 8 : 5; }
-constexpr int smem_bytes(int dp) { return (2 + slots_of(dp)) * tile_bytes(dp); }
+__host__ __device__ constexpr int slots_of(int dp) { return dp == 64 ? 8 : 4; }
+constexpr int smem_bytes(int dp) { return (2 + slots_of(dp)) * tile_bytes(dp) + 8 * 2048; }
 
-// D[tmem] (+)= A[tmem] * B[smem]: A K-major (a lane a row, two bf16 a column), B as its descriptor says.
-MLDEV void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+// D[tmem] (+)= A * B[smem], issued by the lane whose `leader` is not 0; A in shared memory (umma_ss) or in TMEM
+// (umma_ts: K-major, a lane a row, two bf16 a column).  Descriptors by halves: the upper is a constant.
+MLDEV void umma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t accumulate,
+                   uint32_t leader) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 e, %6, 0;\n\t"
+      "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate), "r"(leader)
       : "memory");
 }
-// MN-major operand with the 128-byte swizzle: 64 values (128 bytes) of 8 keys an atom of 1024 bytes, the next
-// 8 keys behind it (SBO), the next 64 values kHalf further (LBO).
-MLDEV uint64_t sw128_mnmajor_desc(uint32_t smem_addr) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(kHalf >> 4) << 16;
-  d |= static_cast<uint64_t>(1024 >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  d |= static_cast<uint64_t>(2) << 61;
-  return d;
+MLDEV void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi, uint32_t idesc, uint32_t accumulate,
+                   uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 e, %6, 0;\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
 }
+// Lower half of a descriptor: the address (and, of the MN-major one, LBO above it).  Upper half: SBO 1024 bytes
+// between atoms of eight rows, version 1, 128-byte swizzle.  K-major: rows of 64 values along K.  MN-major: 64
+// values (128 bytes) of eight keys an atom, the next eight keys behind it, the next 64 values kHalf further (LBO).
+MLDEV uint32_t desc_lo(uint32_t smem_addr) { return (smem_addr & 0x3FFFFu) >> 4; }
+constexpr uint32_t kMnMajorHi = (1024 >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t kKMajorHi = kMnMajorHi;
 constexpr uint32_t kMnMajorB = 1u << 16;
+
+// Two float32 operations an instruction.
+MLDEV float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+MLDEV float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
 
 // Keys that query row `token` of the whole batch sees, -1 if it is no request's.
 MLDEV int keys_of_token(const AttentionParams& p, int token) {
@@ -74,18 +103,42 @@ MLDEV int keys_of_token(const AttentionParams& p, int token) {
   return max(r.kv - r.n + (token - r.q0) + 1, 0);
 }
 
+// A part of an item as every role sees it, made by the scheduling warp.
+struct Step {
+  int end;             // no more parts
+  int lo, most;        // units [lo, most) that some tile takes
+  int hi0, hi1;        // tile k takes those below hi_k: as far as its last row sees
+  int lead;            // 2: both tiles hold the same rows, tile k takes units lo + k, lo + k + 2, ...; else 1
+  int rows0, rows1;    // rows of the tiles
+  int sees;            // keys that the item's last row sees
+  int b, kh, row0;     // request, key head, first row of the item
+  int q0, n, kv;       // the request's first query row, query rows, keys
+  int all, slot;       // the result is final, or a piece's slot
+  int unused[3];
+  MLDEV int hi(int k) const { return k == 0 ? hi0 : hi1; }
+  MLDEV int rows(int k) const { return k == 0 ? rows0 : rows1; }
+  MLDEV int first(int k) const { return lo + (lead == 2 ? k : 0); }
+  MLDEV bool has(int k, int j) const { return j < hi(k) && (lead == 1 || ((j - lo) & 1) == k); }
+};
+constexpr int kSteps = 4;
+
 template <int DP>
 __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __grid_constant__ AttentionParams p,
                                                                       const __grid_constant__ PrefixRun prefix) {
   constexpr int kSlots = slots_of(DP), TILE = tile_bytes(DP), HALVES = DP / 64;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* ring = smem + 2 * TILE;
-  __shared__ uint64_t full[kSlots], empty[kSlots], s_full[2], p_ready[2], o_full[2], q_full[2], v_asked, v_clean, drain;
+  uint8_t* stages = ring + kSlots * TILE;   // 2 KB a row warp
+  __shared__ uint64_t full[kSlots], empty[kSlots], s_full[2], p_ready[2], o_full[2], q_full[2], v_asked, v_clean, both[2], drain;
+  __shared__ uint64_t step_full[kSteps], step_empty[kSteps];
+  __shared__ Step steps[kSteps];
   __shared__ ScheduleSmem sched_s;
+  __shared__ float2 ml_s[2][128];
   __shared__ uint32_t tmem_s, error_s;
   __shared__ int abort_s;
   volatile int* abort_flag = &abort_s;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = static_cast<int>(blockIdx.x);
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
+  const int cta = static_cast<int>(blockIdx.x);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kSlots; ++i) {
@@ -97,6 +150,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
       mbar_init(&p_ready[t], 128);
       mbar_init(&o_full[t], 1);
       mbar_init(&q_full[t], 128);
+      mbar_init(&both[t], 256);
+    }
+    for (int i = 0; i < kSteps; ++i) {
+      mbar_init(&step_full[i], 1);
+      mbar_init(&step_empty[i], kScheduler);   // every other warp
     }
     mbar_init(&v_asked, 1);
     mbar_init(&v_clean, 1);
@@ -116,113 +174,177 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_s;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_s, 0);
   pdl_wait();
   pdl_trigger();
 
   Sched s;
   Place w;
-  Part only;   // of a prefix run
-  if (prefix.splits > 0) {
-    const int item = cta / prefix.splits, split = cta - item * prefix.splits;
-    w.kh = item / prefix.row_tiles;
-    w.i = item - w.kh * prefix.row_tiles;
-    w.b = 0;
-    w.r.q0 = 0;
-    w.r.n = p.T;
-    w.r.kv = prefix.units * kKeys;
-    w.u0 = 0;
-    only.lo = static_cast<int>(static_cast<long long>(prefix.units) * split / prefix.splits);
-    only.hi = static_cast<int>(static_cast<long long>(prefix.units) * (split + 1) / prefix.splits);
-    only.all = false;
-    only.slot = split;
-  } else {
+  if (prefix.splits == 0) {
     make_schedule<kRows, kKeys>(p, cta, s, w, sched_s, reinterpret_cast<long long*>(smem));
     __syncthreads();   // the scratch is the query tiles' again
     if (threadIdx.x == 0 && s.bad) record_status(&error_s, kDevBadSlot, kWhereAttention);
   }
-  // The block's parts of items, the same for every role.  A tile works up to hi[t]: as far as its last row sees.
-  bool first = true;
-  struct Step {
-    Part x;
-    int hi[2], most, rows[2], sees;
-  };
-  auto next_step = [&](Step& t) -> bool {
-    if (prefix.splits > 0) {
-      if (!first) return false;
-      first = false;
-      t.x = only;
-      t.sees = prefix.units * kKeys;
-    } else {
-      if (!first) w.next(p);
-      first = false;
-      while (true) {
-        if (!more<kRows, kKeys>(s, w, p)) return false;
-        t.x = part_of<kRows, kKeys>(p, s, w, cta);
-        if (t.x.lo < t.x.hi) break;
-        w.next(p);
-      }
-      t.sees = Sched::seen_by(p, w.r, w.i);
-    }
-    const long long left = static_cast<long long>(w.r.n) * p.G - static_cast<long long>(w.i) * kRows;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      t.rows[k] = static_cast<int>(max(0ll, min(128ll, left - 128 * k)));
-      int units = 0;
-      if (t.rows[k] > 0) {
-        if (prefix.splits > 0) {
-          units = prefix.units;
-        } else {
-          const long long last = static_cast<long long>(w.i) * kRows + 128 * k + t.rows[k] - 1;
-          const int sees = max(w.r.kv - w.r.n + static_cast<int>(last / p.G) + 1, 0) - p.shared;
-          units = sees <= 0 ? 0 : (sees + kKeys - 1) / kKeys;
-        }
-      }
-      t.hi[k] = max(t.x.lo, min(t.x.hi, units));
-    }
-    t.most = max(t.hi[0], t.hi[1]);
-    return true;
-  };
   const int key0 = prefix.splits > 0 ? 0 : p.shared;   // first key of unit 0
-  Step t;
   int ok = 1;
+  int at_step = 0;            // of the ring of steps
+  uint32_t step_phase = 0;
+  auto step_here = [&]() {    // waits for the next part; the warp's lanes together
+    ok = mbar_wait_sleep(&step_full[at_step], step_phase, abort_flag, &error_s, kWhereAttention);
+    ok = __all_sync(0xffffffffu, ok);
+    return ok != 0;
+  };
+  auto step_read = [&]() {    // the warp has what it needs of it
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&step_empty[at_step]);
+    if (++at_step == kSteps) {
+      at_step = 0;
+      step_phase ^= 1u;
+    }
+  };
 
-  if (warp == kProducer) {   // ------------------------------------------------ TMA
-    const uint64_t policy = l2_policy_evict_last();
-    const int box_log2 = min(p.page_log2, 7), box = 1 << box_log2, boxes = kKeys >> box_log2;
-    int slot = 0;
-    uint32_t phase = 0, issued = 0, parity = 0;
-    while (ok && next_step(t)) {
-      const int32_t* table = p.tables + w.b * p.table_stride;
-      auto page_at = [&](int j) -> int {
-        const int key = key0 + j * kKeys + (lane << box_log2);
-        return lane < boxes && j < t.most && key < t.sees ? table[key >> p.page_log2] : -1;
-      };
-      int ahead = page_at(t.x.lo);
-      for (int j = t.x.lo; ok && j < t.most; ++j) {
-        const int key = key0 + j * kKeys + (lane << box_log2);
-        const bool mine = lane < boxes && key < t.sees;
-        int page = ahead;
-        ahead = page_at(j + 1);
-        if (mine && (page < 0 || page >= p.num_pages)) {   // read as zeros: outside the map
-          record_status(&error_s, kDevBadSlot, kWhereAttention);
-          page = -1;
+  // Registers: the block starts with 168 a thread (64512); the row threads take 200 (51200), in which a row's 128
+  // scores stay, the other four warps keep 104 (13312).
+  if (warp >= kProducer) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    if (warp == kScheduler) {   // -------------------------------------------- the block's parts
+      bool first = true, started = false;
+      while (ok) {
+        Step t;
+        t.end = 0;
+        int hi, units[2];
+        if (prefix.splits > 0) {   // one: a split of the shared keys for a tile of all rows
+          t.end = first ? 0 : 1;
+          const int item = cta / prefix.splits, split = cta - item * prefix.splits;
+          t.kh = item / prefix.row_tiles;
+          t.row0 = (item - t.kh * prefix.row_tiles) * kRows;
+          t.b = t.q0 = 0;
+          t.n = p.T;
+          t.kv = t.sees = prefix.units * kKeys;
+          t.lo = static_cast<int>(static_cast<long long>(prefix.units) * split / prefix.splits);
+          hi = static_cast<int>(static_cast<long long>(prefix.units) * (split + 1) / prefix.splits);
+          t.all = 0;
+          t.slot = split;
+        } else {
+          if (!first) w.next(p);
+          Part x;
+          while (true) {
+            if (!more<kRows, kKeys>(s, w, p)) {
+              t.end = 1;
+              break;
+            }
+            x = part_of<kRows, kKeys>(p, s, w, cta);
+            if (x.lo < x.hi) break;
+            w.next(p);
+          }
+          if (t.end == 0) {
+            t.sees = Sched::seen_by(p, w.r, w.i);
+            t.b = w.b;
+            t.kh = w.kh;
+            t.row0 = w.i * kRows;
+            t.q0 = w.r.q0;
+            t.n = w.r.n;
+            t.kv = w.r.kv;
+            t.lo = x.lo;
+            hi = x.hi;
+            t.all = x.all;
+            t.slot = x.slot;
+            if (!x.all && x.lo == 0) {
+              if (lane == 0) p.records[cta] = record_of<kRows, kKeys>(p, s, w, x, cta);
+              started = true;
+            }
+          }
         }
-        const int n = __popc(__ballot_sync(0xffffffffu, mine));
-        const int token = key & (p.page - 1);
+        first = false;
+        if (t.end == 0) {
+          const int left = t.n * p.G - t.row0;
+          t.rows0 = min(128, left);
+          t.rows1 = max(0, min(128, left - 128));
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
+          for (int k = 0; k < 2; ++k) {
+            const int rows = t.rows(k);
+            int n = 0;
+            if (rows > 0 && prefix.splits > 0) n = prefix.units;
+            if (rows > 0 && prefix.splits == 0) {
+              const int last = t.row0 + 128 * k + rows - 1;
+              n = (max(max(t.kv - t.n + last / p.G + 1, 0) - p.shared, 0) + kKeys - 1) / kKeys;
+            }
+            units[k] = max(t.lo, min(hi, n));
+          }
+          t.lead = 1;
+          if (left <= 128) {
+            t.lead = 2;
+            t.rows1 = t.rows0;
+            units[1] = units[0];
+          }
+          t.hi0 = units[0];
+          t.hi1 = units[1];
+          t.most = max(units[0], units[1]);
+        }
+        ok = mbar_wait_sleep(&step_empty[at_step], step_phase ^ 1u, abort_flag, &error_s, kWhereAttention);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0) {
+          steps[at_step] = t;
+          mbar_arrive(&step_full[at_step]);
+        }
+        if (++at_step == kSteps) {
+          at_step = 0;
+          step_phase ^= 1u;
+        }
+        if (t.end) break;
+      }
+      if (prefix.splits == 0 && !started && lane == 0 && p.records != nullptr) p.records[cta].pieces = 0;
+    } else if (warp == kProducer) {   // -------------------------------------- TMA
+      const uint64_t policy = l2_policy_evict_last();
+      const int box_log2 = min(p.page_log2, 7), box = 1 << box_log2, boxes = kKeys >> box_log2;
+      int slot = 0;
+      uint32_t phase = 0, issued = 0, parity = 0;
+      while (ok && step_here()) {
+        const Step t = steps[at_step];
+        step_read();
+        if (t.end) break;
+        const int32_t* table = p.tables + t.b * p.table_stride;
+        // A lane a box; its page is looked up a unit ahead of its use.
+        auto page_at = [&](int j) -> int {
+          const int key = key0 + j * kKeys + (lane << box_log2);
+          return lane < boxes && j < t.most && key < t.sees ? table[key >> p.page_log2] : -1;
+        };
+        // The order of use: the first `lead` units' keys, then a unit's values and the keys `lead` units on.
+        const int n = t.most - t.lo, lead = min(t.lead, n);
+        int pages[2] = {-1, -1}, next_page = n > 0 ? page_at(t.lo) : -1;
+        for (int i = 0; i < 2 * n; ++i) {
+          const bool keys = i < lead || (i < 2 * n - lead && ((i - lead) & 1));
+          const int u = i < lead ? i : keys ? (i - lead) / 2 + lead : i < 2 * n - lead ? (i - lead) / 2 : i - n;
+          const int j = t.lo + u;
+          const int key = key0 + j * kKeys + (lane << box_log2);
+          const bool mine = lane < boxes && key < t.sees;
+          int page;
+          if (keys) {
+            page = next_page;
+            next_page = page_at(j + 1);
+            if (mine && (page < 0 || page >= p.num_pages)) {   // read as zeros: outside the map
+              record_status(&error_s, kDevBadSlot, kWhereAttention);
+              page = -1;
+            }
+            if (u & 1) pages[1] = page;
+            else pages[0] = page;
+          } else {
+            page = (u & 1) ? pages[1] : pages[0];
+          }
+          const int count = __popc(__ballot_sync(0xffffffffu, mine));
           if (lane == 0) {
-            ok = mbar_wait(&empty[slot], phase ^ 1u, abort_flag, &error_s, kWhereAttention);
-            if (ok) mbar_arrive_expect_tx(&full[slot], n * box * HALVES * 128);
+            ok = mbar_wait_sleep(&empty[slot], phase ^ 1u, abort_flag, &error_s, kWhereAttention);
+            if (ok) mbar_arrive_expect_tx(&full[slot], count * box * HALVES * 128);
           }
           ok = __shfl_sync(0xffffffffu, ok, 0);
           if (!ok) break;
           if (mine) {
             uint8_t* at = ring + slot * TILE + lane * box * 128;
+            const int token = key & (p.page - 1);
 #pragma unroll
             for (int half = 0; half < HALVES; ++half)
-              tma_load_page(at + half * kHalf, kv == 0 ? &p.tmap_k : &p.tmap_v, &full[slot], half * 64, token, w.kh, page, policy);
+              tma_load_page(at + half * kHalf, keys ? &p.tmap_k : &p.tmap_v, &full[slot], half * 64, token, t.kh, page, policy);
           }
           issued |= 1u << slot;
           parity = (parity & ~(1u << slot)) | (phase << slot);
@@ -232,272 +354,419 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
           }
         }
       }
-    }
-    if (!ok && lane == 0)
-      for (int i = 0; i < kSlots; ++i)
-        if ((issued >> i) & 1u) mbar_wait_drain(&full[i], (parity >> i) & 1u);
-    __syncwarp();
-  } else if (warp == kMma) {   // ---------------------------------------------- MMA issue
-    if (lane == 0) {
+      if (!ok && lane == 0)
+        for (int i = 0; i < kSlots; ++i)
+          if ((issued >> i) & 1u) mbar_wait_drain(&full[i], (parity >> i) & 1u);
+      __syncwarp();
+    } else if (warp == kMma) {   // ------------------------------------------ MMA issue
+      // The whole warp walks along, so that descriptors stay in uniform registers; one lane issues.
       const uint32_t s_idesc = idesc_bf16_f32(128, kKeys), o_idesc = idesc_bf16_f32(128, DP) | kMnMajorB;
       const uint32_t q_at = smem_u32(smem), ring_at = smem_u32(ring);
+      const uint32_t leader = lane == 0;
       int slot = 0;
       uint32_t phase = 0, q_phase = 0, p_phase = 0, clean_phase = 0;
-      auto wait_slot = [&]() { return mbar_wait(&full[slot], phase, abort_flag, &error_s, kWhereAttention); };
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, &error_s, kWhereAttention));
+        return ok != 0;
+      };
       auto advance = [&]() {
         if (++slot == kSlots) {
           slot = 0;
           phase ^= 1u;
         }
       };
+      auto commit = [&](uint64_t* bar) {
+        if (leader) umma_commit(bar);
+        __syncwarp();
+      };
       auto scores = [&](int k, uint32_t at) {   // S of tile k with the keys at `at`
-        const uint64_t ad = sw128_kmajor_desc(q_at + k * TILE), bd = sw128_kmajor_desc(at);
+        const uint32_t a = desc_lo(q_at + k * TILE) | (1u << 16), b = desc_lo(at) | (1u << 16);
 #pragma unroll
         for (int ks = 0; ks < DP / 16; ++ks) {
           const uint32_t step = (ks >> 2) * (kHalf >> 4) + 2 * (ks & 3);
-          umma_bf16(tmem + k * 128, ad + step, bd + step, s_idesc, ks > 0);
+          umma_ss(tmem + k * 128, a + step, b + step, kKMajorHi, s_idesc, ks > 0, leader);
         }
-        umma_commit(&s_full[k]);
+        commit(&s_full[k]);
       };
-      while (ok && next_step(t)) {
-        if (t.most == t.x.lo) continue;
-        ok = wait_slot();
-        if (!ok) break;
-        for (int k = 0; ok && k < 2; ++k) {
-          if (t.hi[k] <= t.x.lo) continue;
-          ok = mbar_wait(&q_full[k], (q_phase >> k) & 1u, abort_flag, &error_s, kWhereAttention);
-          q_phase ^= 1u << k;
-          tc_fence_after();
-          if (ok) scores(k, ring_at + slot * TILE);
-        }
-        if (!ok) break;
-        umma_commit(&empty[slot]);
-        advance();
-        for (int j = t.x.lo; ok && j < t.most; ++j) {
-          const int v_slot = slot;
-          ok = wait_slot();
+      while (step_here()) {
+        const Step& in = steps[at_step];
+        auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+        Step t;
+        t.end = uniform(in.end);
+        t.lo = uniform(in.lo);
+        t.most = uniform(in.most);
+        t.hi0 = uniform(in.hi0);
+        t.hi1 = uniform(in.hi1);
+        t.lead = uniform(in.lead);
+        t.sees = uniform(in.sees);
+        step_read();
+        if (t.end) break;
+        for (int i = 0; ok && i < t.lead && t.lo + i < t.most; ++i) {   // the first scores
+          if (!wait(&full[slot], phase)) break;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            if (!ok || !t.has(k, t.lo + i)) continue;
+            if (!wait(&q_full[k], (q_phase >> k) & 1u)) continue;
+            q_phase ^= 1u << k;
+            tc_fence_after();
+            scores(k, ring_at + slot * TILE);
+          }
+          if (!ok) break;
+          commit(&empty[slot]);
           advance();
-          if (ok && key0 + (j + 1) * kKeys > t.sees) {   // values behind the last key
-            mbar_arrive(&v_asked);
-            ok = mbar_wait(&v_clean, clean_phase, abort_flag, &error_s, kWhereAttention);
+        }
+        for (int j = t.lo; ok && j < t.most; ++j) {
+          const int v_slot = slot, ahead = j + t.lead;
+          if (!wait(&full[slot], phase)) break;
+          advance();
+          if (key0 + (j + 1) * kKeys > t.sees) {   // values behind the last key
+            if (leader) mbar_arrive(&v_asked);
+            __syncwarp();
+            if (!wait(&v_clean, clean_phase)) break;
             clean_phase ^= 1u;
           }
-          const bool another = j + 1 < t.most;
           const int k_slot = slot;
           bool have_keys = false;
-          for (int k = 0; ok && k < 2; ++k) {
-            if (j < t.hi[k]) {
-              ok = mbar_wait(&p_ready[k], (p_phase >> k) & 1u, abort_flag, &error_s, kWhereAttention);
-              if (!ok) break;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            if (!ok) continue;
+            if (t.has(k, j)) {
+              if (!wait(&p_ready[k], (p_phase >> k) & 1u)) continue;
               p_phase ^= 1u << k;
               tc_fence_after();
-              const uint64_t bd = sw128_mnmajor_desc(ring_at + v_slot * TILE);
+              const uint32_t b = desc_lo(ring_at + v_slot * TILE) | (static_cast<uint32_t>(kHalf >> 4) << 16);
 #pragma unroll
               for (int ks = 0; ks < kKeys / 16; ++ks)
-                umma_bf16_ts(tmem + 256 + k * DP, tmem + k * 128 + ks * 8, bd + ks * (2048 >> 4), o_idesc, j > t.x.lo || ks > 0);
-              if (j + 1 == t.hi[k]) umma_commit(&o_full[k]);
+                umma_ts(tmem + 256 + k * DP, tmem + k * 128 + ks * 8, b + ks * (2048 >> 4), kMnMajorHi, o_idesc,
+                        j >= t.lo + t.lead || ks > 0, leader);
+              if (ahead >= t.hi(k)) commit(&o_full[k]);
             }
-            if (j + 1 < t.hi[k]) {
-              if (!have_keys) ok = wait_slot();
+            if (t.has(k, ahead)) {
+              if (!have_keys && !wait(&full[slot], phase)) continue;
               have_keys = true;
-              if (ok) scores(k, ring_at + k_slot * TILE);
+              scores(k, ring_at + k_slot * TILE);
             }
           }
           if (!ok) break;
-          umma_commit(&empty[v_slot]);
-          if (another) {
-            umma_commit(&empty[k_slot]);
+          commit(&empty[v_slot]);
+          if (ahead < t.most) {
+            commit(&empty[k_slot]);
             advance();
           }
         }
+        if (!ok) break;
       }
-      if (!ok) {   // let what was issued finish before TMEM is released
+      if (!ok && leader) {   // let what was issued finish before TMEM is released
         umma_commit(&drain);
         mbar_wait_drain(&drain, 0);
       }
-    }
-    __syncwarp();
-  } else if (warp == kCleaner) {   // ------------------------------------------ values behind the last key
-    // Asked for by the MMA warp once they have landed: by itself this warp would run ahead of the ring by
-    // more than a lap, where a parity says nothing.
-    unsigned long long used = 0;   // ring slots of the steps before
-    uint32_t asked_phase = 0;
-    while (ok && next_step(t)) {
-      const int n = t.most - t.x.lo;
-      if (n > 0 && key0 + t.most * kKeys > t.sees) {   // the part's last unit
-        const unsigned long long at = used + 2ull * n - 1;
-        const int slot = static_cast<int>(at % kSlots);
-        ok = mbar_wait_sleep(&v_asked, asked_phase, abort_flag, &error_s, kWhereAttention) &&
-             mbar_wait(&full[slot], static_cast<uint32_t>(at / kSlots) & 1u, abort_flag, &error_s, kWhereAttention);
-        asked_phase ^= 1u;
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        const int k0 = key0 + (t.most - 1) * kKeys;
-        const int from = t.sees - k0;   // 1..127
-        for (int c = lane; c < (kKeys - from) * 8 * HALVES; c += 32) {
-          const int row = from + (c >> 3) % (kKeys - from), half = (c >> 3) / (kKeys - from);
-          *reinterpret_cast<uint4*>(ring + slot * TILE + half * kHalf + row * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&v_clean);
-      }
-      used += 2ull * n;
-    }
-  } else {   // -------------------------------------------------------------- rows
-    const int k = warp >> 2, r = threadIdx.x & 127;   // tile, row of it
-    const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const uint32_t s_at = lanes + k * 128, o_at = lanes + 256 + k * DP;
-    uint32_t s_phase = 0, o_phase = 0;
-    bool started = false;
-    const float sign = p.scale_log2 < 0.0f ? -1.0f : 1.0f, scale = fabsf(p.scale_log2);
-    while (ok && next_step(t)) {
-      const int rows = t.rows[k], lo = t.x.lo, hi = t.hi[k];
-      const long long row = static_cast<long long>(w.i) * kRows + k * 128 + r;   // of the request and key head
-      const int token_in = static_cast<int>(row / p.G), head = w.kh * p.G + static_cast<int>(row - static_cast<long long>(token_in) * p.G);
-      const long long token = w.r.q0 + token_in;
-      int sees = 0;
-      if (r < rows) {
-        if (prefix.splits > 0) sees = min(max(keys_of_token(p, static_cast<int>(token)), 0), t.sees);
-        else sees = max(w.r.kv - w.r.n + token_in + 1, 0);
-      }
-      float ref = -INFINITY, l = 0.0f;
-      if (hi > lo) {
-        // ---- the query row, in the products' layout; a negative scale is the row's sign
-        uint8_t* q_s = smem + k * TILE + r * 128;
-        const __nv_bfloat16* q = p.q + token * p.q_t + head * p.q_h;
-#pragma unroll
-        for (int c = 0; c < DP / 8; ++c) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (r < rows && c * 8 < p.D) v = *reinterpret_cast<const uint4*>(q + c * 8);
-          if (sign < 0.0f) {
-            v.x ^= 0x80008000u;
-            v.y ^= 0x80008000u;
-            v.z ^= 0x80008000u;
-            v.w ^= 0x80008000u;
-          }
-          *reinterpret_cast<uint4*>(q_s + (c >> 3) * kHalf + (((c & 7) ^ (r & 7)) << 4)) = v;
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(&q_full[k]);
-        for (int j = lo; j < hi; ++j) {
-          ok = mbar_wait(&s_full[k], s_phase, abort_flag, &error_s, kWhereAttention);
+      __syncwarp();
+    } else if (warp == kCleaner) {   // -------------------------------------- values behind the last key
+      // Asked for by the MMA warp once they have landed: by itself this warp would run ahead of the ring by
+      // more than a lap, where a parity says nothing.
+      unsigned long long used = 0;   // ring slots of the steps before
+      uint32_t asked_phase = 0;
+      while (step_here()) {
+        const Step t = steps[at_step];
+        step_read();
+        if (t.end) break;
+        const int n = t.most - t.lo;
+        if (n > 0 && key0 + t.most * kKeys > t.sees) {   // the part's last unit
+          const unsigned long long at = used + 2ull * n - 1;   // the part's last slot: its last unit's values
+          const int slot = static_cast<int>(at % kSlots);
+          ok = mbar_wait_sleep(&v_asked, asked_phase, abort_flag, &error_s, kWhereAttention) &&
+               mbar_wait(&full[slot], static_cast<uint32_t>(at / kSlots) & 1u, abort_flag, &error_s, kWhereAttention);
+          asked_phase ^= 1u;
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          s_phase ^= 1u;
-          tc_fence_after();
-          const int limit = sees - (key0 + j * kKeys);   // columns below it are seen
-          const bool cut = __any_sync(0xffffffffu, limit < kKeys);
-          float top = -INFINITY;
+          const int k0 = key0 + (t.most - 1) * kKeys;
+          const int from = t.sees - k0;   // 1..127
+          for (int c = lane; c < (kKeys - from) * 8; c += 32)
 #pragma unroll
-          for (int c = 0; c < kKeys; c += 32) {
-            uint32_t v[32];
-            tmem_ld_x32(s_at + c, v);
-            tmem_ld_wait();
-            if (cut) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) top = fmaxf(top, c + i < limit ? __uint_as_float(v[i]) : -INFINITY);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(v[i]));
-            }
-          }
-          top *= scale;   // (scale is not 0)
-          const bool grow = top > ref + 8.0f;
-          if (__any_sync(0xffffffffu, grow)) {
-            const float f = grow ? exp2_approx(ref - top) : 1.0f;
-            if (grow) ref = top;
-            l *= f;
-            if (j > lo) {
-#pragma unroll 1
-              for (int c = 0; c < DP; c += 32) {
-                uint32_t v[32];
-                tmem_ld_x32(o_at + c, v);
-                tmem_ld_wait();
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-                tmem_st_x32(o_at + c, v);
-              }
-              tmem_st_wait();
-            }
-          }
-          const float off = -reference_of(ref);
-          float sum0 = 0.0f, sum1 = 0.0f;
-#pragma unroll
-          for (int c = 0; c < kKeys; c += 32) {
-            uint32_t v[32], w2[16];
-            tmem_ld_x32(s_at + c, v);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              float a = __uint_as_float(v[i]), b = __uint_as_float(v[i + 1]);
-              if (cut) {
-                a = c + i < limit ? a : -INFINITY;
-                b = c + i + 1 < limit ? b : -INFINITY;
-              }
-              a = exp2_approx(fmaf(a, scale, off));
-              b = exp2_approx(fmaf(b, scale, off));
-              sum0 += a;
-              sum1 += b;
-              const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-              w2[i / 2] = *reinterpret_cast<const uint32_t*>(&h);
-            }
-            tmem_st_x16(s_at + c / 2, w2);   // over scores that are read already
-          }
-          l += sum0 + sum1;
-          tmem_st_wait();
-          tc_fence_before();
-          mbar_arrive(&p_ready[k]);
+            for (int half = 0; half < HALVES; ++half)
+              *reinterpret_cast<uint4*>(ring + slot * TILE + half * kHalf + from * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&v_clean);
         }
+        used += 2ull * n;
+      }
+    }
+  } else {   // ---------------------------------------------------------------- rows
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    const int k = warp >> 2, r = threadIdx.x & 127;   // tile, row of it
+    const int wr = (warp & 3) * 32;                   // the warp's first row
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(wr) << 16);
+    const uint32_t s_at = lanes + k * 128, o_at = lanes + 256 + k * DP;
+    uint8_t* stage = stages + warp * 2048;
+    uint32_t s_phase = 0, o_phase = 0, both_phase = 0;
+    const bool negative = p.scale_log2 < 0.0f;
+    const float scale = fabsf(p.scale_log2);
+    // Copies the part's query rows to the products' layout, a warp its own 32 of them, whole rows at a time.
+    auto fetch_queries = [&](const Step& t) {
+      const int row = t.row0 + (t.lead == 2 ? r : k * 128 + r);
+      const int token = row / p.G;
+      const __nv_bfloat16* from = nullptr;
+      if (r < t.rows(k)) from = p.q + (t.q0 + token) * p.q_t + (t.kh * p.G + row - token * p.G) * p.q_h;
+      constexpr int kLanes = DP / 8;   // a row
+#pragma unroll
+      for (int i = 0; i < 32; i += 32 / kLanes) {
+        const int of = i + lane / kLanes, c = lane % kLanes, tr = wr + of;
+        const __nv_bfloat16* src =
+            reinterpret_cast<const __nv_bfloat16*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(from), of));
+        const bool real = src != nullptr && c * 8 < p.D;
+        const uint32_t dst = smem_u32(smem) + k * TILE + (c >> 3) * kHalf + tr * 128 + (((c & 7) ^ (tr & 7)) << 4);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(real ? src + c * 8 : p.q), "r"(real ? 16 : 0)
+                     : "memory");
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto queries_there = [&]() {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      fence_proxy_async_smem();
+      mbar_arrive(&q_full[k]);
+    };
+    bool asked = false;   // the query rows of the part at hand are on their way, or there
+    while (step_here()) {
+      if (steps[at_step].end) {
+        step_read();
+        break;
+      }
+      const int lo = steps[at_step].lo, hi = steps[at_step].hi(k), lead = steps[at_step].lead, rows = steps[at_step].rows(k);
+      const int hi_other = steps[at_step].hi(k ^ 1);
+      const int first_unit = steps[at_step].first(k);
+      const int tile_row = lead == 2 ? r : k * 128 + r;
+      const int all = steps[at_step].all, slot = steps[at_step].slot;
+      int token, head, sees = 0;
+      {
+        const Step& t = steps[at_step];
+        const int row = t.row0 + tile_row;   // of the request and key head
+        const int token_in = row / p.G;
+        head = t.kh * p.G + row - token_in * p.G;
+        token = t.q0 + token_in;
+        if (r < rows) {
+          if (prefix.splits > 0) sees = min(max(keys_of_token(p, token), 0), t.sees);
+          else sees = max(t.kv - t.n + token_in + 1, 0);
+        }
+        if (!asked && first_unit < hi) {
+          fetch_queries(t);
+          queries_there();
+        }
+      }
+      step_read();
+      asked = false;
+      // The next part's query rows, as soon as the tile's last scores are there: they are what still reads these.
+      auto fetch_next = [&]() {
+        if (!step_here()) return;
+        const Step& t = steps[at_step];
+        if (t.end || t.first(k) >= t.hi(k)) return;
+        fetch_queries(t);
+        asked = true;
+      };
+      float ref = -INFINITY, l = 0.0f;
+      const bool idle = wr >= rows;   // no row of this warp is one: its weights may be anything
+      for (int j = first_unit; j < hi; j += lead) {
+        ok = mbar_wait(&s_full[k], s_phase, abort_flag, &error_s, kWhereAttention);
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
+        s_phase ^= 1u;
+        tc_fence_after();
+        if (j + lead >= hi) fetch_next();
+        if (!ok) break;
+        if (idle) {
+          mbar_arrive(&p_ready[k]);
+          continue;
+        }
+        uint32_t v[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld_x32(s_at + c * 32, v[c]);
+        tmem_ld_wait();
+        if (negative) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[c][i] ^= 0x80000000u;
+        }
+        const int limit = sees - (key0 + j * kKeys);   // columns below it are seen
+        if (__any_sync(0xffffffffu, limit < kKeys)) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[c][i] = c * 32 + i < limit ? v[c][i] : 0xff800000u;
+        }
+        float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tops[c] = fmaxf(tops[c], __uint_as_float(v[c][i]));
+        const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * scale;   // (scale is not 0)
+        const bool grow = top > ref + 8.0f;
+        if (__any_sync(0xffffffffu, grow)) {
+          const float f = grow ? exp2_approx(ref - top) : 1.0f;
+          if (grow) ref = top;
+          l *= f;
+          if (j >= lo + lead) {
+#pragma unroll 1
+            for (int c = 0; c < DP; c += 16) {
+              uint32_t o[16];
+              tmem_ld_x16(o_at + c, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st_x16(o_at + c, o);
+            }
+            tmem_st_wait();
+          }
+        }
+        const float2 scales = make_float2(scale, scale), off = make_float2(-reference_of(ref), -reference_of(ref));
+        float2 sums[2] = {};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            float2 x = fma2(make_float2(__uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1])), scales, off);
+            x.x = exp2_approx(x.x);
+            x.y = exp2_approx(x.y);
+            sums[(i >> 1) & 1] = add2(sums[(i >> 1) & 1], x);
+            const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
+            v[c >> 1][(c & 1) * 16 + i / 2] = *reinterpret_cast<const uint32_t*>(&h);   // (read already)
+          }
+          if (c & 1) tmem_st_x32(s_at + (c >> 1) * 32, v[c >> 1]);   // over the scores
+        }
+        l += (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&p_ready[k]);
+      }
+      if (!ok) break;
+      if (first_unit >= hi) fetch_next();
+      if (!ok) break;
+      if (asked) queries_there();
+      if (first_unit < hi) {
         ok = mbar_wait(&o_full[k], o_phase, abort_flag, &error_s, kWhereAttention);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         o_phase ^= 1u;
         tc_fence_after();
       }
-      // ---- the result, eight values at a time
-      const long long at = prefix.splits > 0 ? t.x.slot * (static_cast<long long>(p.T) * p.Hq) + token * p.Hq + head
-                                             : static_cast<long long>(t.x.slot) * p.item_rows + k * 128 + r;
+      // ---- with the same rows in both tiles: the other tile's maximum and sum, and half of the columns each
+      const bool pair = lead == 2;
+      float other = 0.0f, mine = 1.0f;   // factors of the other tile's result and this one's
+      if (pair) {
+        ml_s[k][r] = make_float2(ref, l);
+        tc_fence_before();
+        mbar_arrive(&both[0]);
+        ok = mbar_wait(&both[0], both_phase, abort_flag, &error_s, kWhereAttention);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const float2 a = ml_s[0][r], b = ml_s[1][r];
+        const float m = fmaxf(a.x, b.x), base = reference_of(m);
+        const float fa = exp2_approx(a.x - base), fb = exp2_approx(b.x - base);
+        ref = m;
+        l = a.y * fa + b.y * fb;
+        mine = k == 0 ? fa : fb;
+        other = k == 0 ? fb : fa;
+      }
+      const bool has_mine = first_unit < hi, has_other = pair && lo + (k ^ 1) < hi_other;
+      const int c_lo = pair ? k * (DP / 2) : 0, c_hi = pair ? c_lo + DP / 2 : DP;
+      const bool real = r < rows;
+      const long long at = prefix.splits > 0 ? (static_cast<long long>(slot) * p.T + token) * p.Hq + head
+                                             : static_cast<long long>(slot) * p.item_rows + tile_row;
+      // Results leave through shared memory, 64 bytes of a row at a time, so that a warp writes whole pieces of
+      // its rows: a thread a row would touch 32 rows a store.
+      const bool by_row = all && (p.prefix_splits > 0 || !p.out_vec);   // unless they need more than that
       float* piece_o = prefix.splits > 0 ? p.prefix_o : p.piece_o;
-      float2* piece_ml = prefix.splits > 0 ? p.prefix_ml : p.piece_ml;
+      unsigned long long to = 0;
+      if (real)
+        to = all ? reinterpret_cast<unsigned long long>(p.out + token * p.o_t + head * p.o_h)
+                 : reinterpret_cast<unsigned long long>(piece_o + at * DP);
+      unsigned long long dst[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) dst[i] = __shfl_sync(0xffffffffu, to, i * 8 + (lane >> 2));
+      if (all && !by_row) {
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        mine *= inv;
+        other *= inv;
+      }
+      const bool none = l == 0.0f && all;   // a row that sees nothing, or whose every score is -inf
+      const int width = all ? 32 : 16;      // columns of 64 bytes
+      if (wr < rows) {
 #pragma unroll 1
-      for (int c = 0; c < DP; c += 32) {
-        uint32_t v[32];
-        if (hi > lo) {
+        for (int c = c_lo; c < c_hi; c += width) {
+          uint32_t v[32];
+          float o[32];
           __syncwarp();
-          tmem_ld_x32(o_at + c, v);
-          tmem_ld_wait();
-        } else {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0u;
-        }
-        if (r < rows) {
+          for (int i = 0; i < 32; ++i) o[i] = 0.0f;
+          if (has_mine) {
+            if (all) tmem_ld_x32(o_at + c, v);
+            else tmem_ld_x16(o_at + c, reinterpret_cast<uint32_t(&)[16]>(v));
+            tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            float o[8];
+            for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(v[i]) * mine;
+          }
+          if (has_other) {
+            if (all) tmem_ld_x32(lanes + 256 + (k ^ 1) * DP + c, v);
+            else tmem_ld_x16(lanes + 256 + (k ^ 1) * DP + c, reinterpret_cast<uint32_t(&)[16]>(v));
+            tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = __uint_as_float(v[i + e]);
-            if (t.x.all) {
-              float m = ref, sum = l;
-              add_prefix<DP>(p, token * p.Hq + head, c + i, m, sum, o);
-              write_row8(p, token, head, c + i, m, sum, o);
-            } else {
-              float4* to = reinterpret_cast<float4*>(piece_o + at * DP + c + i);
-              to[0] = make_float4(o[0], o[1], o[2], o[3]);
-              to[1] = make_float4(o[4], o[5], o[6], o[7]);
+            for (int i = 0; i < 32; ++i) o[i] = fmaf(__uint_as_float(v[i]), other, o[i]);
+          }
+          if (by_row) {
+            if (real) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 8) {
+                float e[8];
+#pragma unroll
+                for (int n = 0; n < 8; ++n) e[n] = o[i + n];
+                float m = ref, sum = l;
+                add_prefix<DP>(p, static_cast<long long>(token) * p.Hq + head, c + i, m, sum, e);
+                write_row8(p, token, head, c + i, m, sum, e);
+              }
             }
+            continue;
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint4 x;
+            if (all) {
+              const float e[8] = {o[8 * i],     o[8 * i + 1], o[8 * i + 2], o[8 * i + 3],
+                                  o[8 * i + 4], o[8 * i + 5], o[8 * i + 6], o[8 * i + 7]};
+              x = pack8(e);
+              if (none) x = make_uint4(0, 0, 0, 0);
+            } else {
+              x = make_uint4(__float_as_uint(o[4 * i]), __float_as_uint(o[4 * i + 1]), __float_as_uint(o[4 * i + 2]),
+                             __float_as_uint(o[4 * i + 3]));
+            }
+            *reinterpret_cast<uint4*>(stage + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) = x;
+          }
+          __syncwarp();
+          const int part = lane & 3, bytes = (all ? 2 : 4) * c + 16 * part;
+          const bool inside = !all || c + part * 8 < p.D;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int of = i * 8 + (lane >> 2);
+            const uint4 x = *reinterpret_cast<const uint4*>(stage + of * 64 + ((part ^ ((of >> 1) & 3)) << 4));
+            if (dst[i] != 0 && inside) *reinterpret_cast<uint4*>(dst[i] + bytes) = x;
           }
         }
       }
-      if (!t.x.all && r < rows) piece_ml[at] = make_float2(ref, l);
+      if (real && c_lo == 0) {
+        if (!all) (prefix.splits > 0 ? p.prefix_ml : p.piece_ml)[at] = make_float2(ref, l);
+        else if (!by_row && p.lse != nullptr)
+          p.lse[static_cast<long long>(token) * p.Hq + head] = (reference_of(ref) + log2f(l)) * kLn2;
+      }
       tc_fence_before();
-      if (prefix.splits == 0 && !t.x.all && t.x.lo == 0 && threadIdx.x == 0) {
-        p.records[cta] = record_of<kRows, kKeys>(p, s, w, t.x, cta);
-        started = true;
+      if (pair) {   // neither tile's next item overwrites what the other still reads
+        mbar_arrive(&both[1]);
+        ok = mbar_wait(&both[1], both_phase, abort_flag, &error_s, kWhereAttention);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        both_phase ^= 1u;
       }
     }
-    if (prefix.splits == 0 && !started && threadIdx.x == 0 && p.records != nullptr) p.records[cta].pieces = 0;
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
   }
 
   tc_fence_before();
