@@ -102,72 +102,133 @@ __global__ void __launch_bounds__(32 * kAnyWarps) attention_any_kernel(const __g
 
 
 // ---------------------------------------------------------------------------------------
-// The pieces of an item together: a block a record and row (rows blockIdx.y, + gridDim.y, ...).  Sixteen
-// groups of threads take the pieces in turn, DP / 8 threads a group with eight values each, so that a long
-// request's 76 pieces are five loads deep; the groups are added in order.  Blocks without a record leave at
-// once.  The shared keys' part comes on top.
+// Results of a row from several places together.  Sixteen teams of threads a block, DP / 8 threads a team with eight
+// values each; `per_row` teams (1, 4 or 16, by the number of results) take those of a row in turn, so that the 76
+// pieces of a long request are five loads deep, and are added in order.
 // ---------------------------------------------------------------------------------------
-constexpr int kGroups = 16;
+constexpr int kTeams = 16;
 
-template <int DP>
-__global__ void __launch_bounds__(kGroups * DP / 8) attention_join_kernel(const __grid_constant__ AttentionParams p) {
+__host__ __device__ __forceinline__ int teams_per_row(int results) { return results <= 4 ? 1 : results <= 24 ? 4 : 16; }
+
+// The sum over i < n of the results at row(i) of (ml, o), for the rows that the block's teams have at hand; every
+// thread of the block takes part (`active`: the team has a row).  Valid in the first team of a row.
+template <int DP, typename RowOf>
+MLDEV void join_results(const float2* ml, const float* part, int n, int per_row, bool active, RowOf row, float& m, float& l,
+                        float (&o)[8]) {
   constexpr int kLanes = DP / 8;
-  __shared__ float o_s[kGroups][DP];
-  __shared__ float m_s[kGroups], l_s[kGroups];
-  pdl_wait();
-  pdl_trigger();
-  const PieceRecord c = p.records[blockIdx.x];
-  if (c.pieces == 0) return;
-  const int group = threadIdx.x / kLanes, d = (threadIdx.x % kLanes) * 8;
-  for (int r = static_cast<int>(blockIdx.y); r < c.rows; r += static_cast<int>(gridDim.y)) {
-    float m = -INFINITY, l = 0.0f, o[8] = {};
+  __shared__ float o_s[kTeams][DP];
+  __shared__ float m_s[kTeams], l_s[kTeams];
+  const int team = threadIdx.x / kLanes, d = (threadIdx.x % kLanes) * 8, member = team % per_row;
+  m = -INFINITY;
+  l = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) o[k] = 0.0f;
+  if (active) {
 #pragma unroll 4
-    for (int i = group; i < c.pieces; i += kGroups) {
-      const int slot = i == 0 ? c.slot : 2 * (static_cast<int>(blockIdx.x) + i);
-      const long long at = static_cast<long long>(slot) * p.item_rows + r;
-      const float2 ml = p.piece_ml[at];
-      const float4* src = reinterpret_cast<const float4*>(p.piece_o + at * DP + d);
-      const float4 x = src[0], y = src[1];
-      const float top = fmaxf(m, ml.x), ref = reference_of(top);
-      const float f = exp2_approx(m - ref), g = exp2_approx(ml.x - ref);
+    for (int i = member; i < n; i += per_row) {
+      const long long at = row(i);
+      const float2 x = ml[at];
+      if (x.y == 0.0f) continue;   // nothing was seen there, or nothing that weighs (a NaN is not 0)
+      const float4* src = reinterpret_cast<const float4*>(part + at * DP + d);
+      const float4 a = src[0], b = src[1];
+      const float top = fmaxf(m, x.x), ref = reference_of(top);
+      const float f = exp2_approx(m - ref), g = exp2_approx(x.x - ref);
       m = top;
-      l = l * f + ml.y * g;
-      const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+      l = l * f + x.y * g;
+      const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
       for (int k = 0; k < 8; ++k) o[k] = o[k] * f + v[k] * g;
     }
+  }
+  if (per_row == 1) return;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) o_s[group][d + k] = o[k];
-    if (d == 0) {
-      m_s[group] = m;
-      l_s[group] = l;
+  for (int k = 0; k < 8; ++k) o_s[team][d + k] = o[k];
+  if (d == 0) {
+    m_s[team] = m;
+    l_s[team] = l;
+  }
+  __syncthreads();
+  if (member == 0) {
+    for (int g = 1; g < per_row; ++g) m = fmaxf(m, m_s[team + g]);
+    const float ref = reference_of(m);
+    l = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) o[k] = 0.0f;
+    for (int g = 0; g < per_row; ++g) {
+      const float f = exp2_approx(m_s[team + g] - ref);
+      l += l_s[team + g] * f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) o[k] += o_s[team + g][d + k] * f;
     }
-    __syncthreads();
-    if (group == 0) {
-      for (int g = 0; g < kGroups; ++g) m = fmaxf(m, m_s[g]);
-      const float ref = reference_of(m);
-      l = 0.0f;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) o[k] = 0.0f;
-      for (int g = 0; g < kGroups; ++g) {
-        const float f = exp2_approx(m_s[g] - ref);
-        l += l_s[g] * f;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) o[k] += o_s[g][d + k] * f;
-      }
-      const long long token = c.q0 + (c.row0 + r) / p.G;
-      const int head = c.kh * p.G + (c.row0 + r) % p.G;
-      add_prefix<DP>(p, token * p.Hq + head, d, m, l, o);
+  }
+  __syncthreads();
+}
+
+// The pieces of items that were cut: blocks (x, .) take record x, if it is one, and its rows by team.  The result is
+// final, or with shared keys the last part of the row.
+template <int DP>
+__global__ void __launch_bounds__(kTeams * DP / 8) attention_join_kernel(const __grid_constant__ AttentionParams p) {
+  pdl_wait();
+  pdl_trigger();
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && p.prefix_splits == 0) take_status(p);
+  const PieceRecord c = p.records[blockIdx.x];
+  if (c.pieces == 0) return;
+  const int per_row = teams_per_row(c.pieces), at_once = kTeams / per_row;
+  const int team = threadIdx.x / (DP / 8), d = (threadIdx.x % (DP / 8)) * 8;
+  for (int r0 = static_cast<int>(blockIdx.y) * at_once; r0 < c.rows; r0 += static_cast<int>(gridDim.y) * at_once) {
+    const int r = r0 + team / per_row;
+    float m, l, o[8];
+    join_results<DP>(
+        p.piece_ml, p.piece_o, c.pieces, per_row, r < c.rows,
+        [&](int i) {
+          return static_cast<long long>(i == 0 ? c.slot : 2 * (static_cast<int>(blockIdx.x) + i)) * p.item_rows + r;
+        },
+        m, l, o);
+    if (r >= c.rows || team % per_row != 0) continue;
+    const long long token = c.q0 + (c.row0 + r) / p.G;
+    const int head = c.kh * p.G + (c.row0 + r) % p.G;
+    if (p.prefix_splits == 0) {
       write_row8(p, token, head, d, m, l, o);
+    } else {
+      const long long at = part_row(p, token, head);
+      float4* to = reinterpret_cast<float4*>(p.part_o + at * DP + d);
+      to[0] = make_float4(o[0], o[1], o[2], o[3]);
+      to[1] = make_float4(o[4], o[5], o[6], o[7]);
+      if (d == 0) p.part_ml[at] = make_float2(m, l);
     }
-    __syncthreads();
   }
 }
 
+// The parts of the rows of all requests: the shared keys' and the requests' own.
+template <int DP>
+__global__ void __launch_bounds__(kTeams * DP / 8) attention_fold_kernel(const __grid_constant__ AttentionParams p) {
+  pdl_wait();
+  pdl_trigger();
+  if (blockIdx.x == 0 && threadIdx.x == 0) take_status(p);
+  const int per_row = teams_per_row(p.prefix_splits + 1), at_once = kTeams / per_row;
+  const int team = threadIdx.x / (DP / 8), d = (threadIdx.x % (DP / 8)) * 8;
+  const int rows = p.T * p.Hq;
+  const int r = static_cast<int>(blockIdx.x) * at_once + team / per_row;
+  const int token = r / p.Hq;
+  // rows of no request are left alone (keys that all requests share make no part of them either)
+  const bool real = r < rows && keys_of_token(p, token) >= 0;
+  float m, l, o[8];
+  join_results<DP>(
+      p.part_ml, p.part_o, p.prefix_splits + 1, per_row, real,
+      [&](int i) { return static_cast<long long>(i) * rows + r; }, m, l, o);
+  if (real && team % per_row == 0) write_row8(p, token, r - token * p.Hq, d, m, l, o);
+}
+
 cudaError_t launch_join(const AttentionParams& p, int dp, int across, cudaStream_t stream) {
-  const dim3 grid(p.plan.ctas, across), block(kGroups * dp / 8);
+  const dim3 grid(p.plan.ctas, across), block(kTeams * dp / 8);
   return dp == 64 ? launch_k(attention_join_kernel<64>, grid, block, 0, stream, true, p)
                   : launch_k(attention_join_kernel<128>, grid, block, 0, stream, true, p);
+}
+cudaError_t launch_fold(const AttentionParams& p, int dp, cudaStream_t stream) {
+  const int per_row = teams_per_row(p.prefix_splits + 1);
+  const dim3 grid((p.T * p.Hq + kTeams / per_row - 1) / (kTeams / per_row)), block(kTeams * dp / 8);
+  return dp == 64 ? launch_k(attention_fold_kernel<64>, grid, block, 0, stream, true, p)
+                  : launch_k(attention_fold_kernel<128>, grid, block, 0, stream, true, p);
 }
 
 // ---------------------------------------------------------------- workspace
@@ -177,7 +238,7 @@ constexpr int kMaxSms = 160;   // blocks are a multiple of the GPU's 152
 constexpr int kPrefixSplits = 64, kPrefixBlocks = 2 * kMaxSms;
 constexpr size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 struct Workspace {
-  size_t records, ml, o, prefix_ml, prefix_o, bytes;
+  size_t records, ml, o, part_ml, part_o, bytes;
 };
 int slot_rows(bool tiles, long long T, int G) {
   return static_cast<int>(std::min<long long>(tiles ? kTileRows : kFewRows, T * G));
@@ -185,16 +246,16 @@ int slot_rows(bool tiles, long long T, int G) {
 Workspace workspace_for(int T, int Hq, int Hk, int D) {
   const int G = Hq / Hk, dp = D <= 64 ? 64 : 128;
   const size_t slots = std::max<size_t>(2 * kFewPerSm * kMaxSms * slot_rows(false, T, G), 2 * kMaxSms * slot_rows(true, T, G));
-  // rows x splits of the shared keys' launch: splits <= kPrefixBlocks / items + 1, rows <= 256 items
+  // rows x (splits of the shared keys' launch and one): splits <= kPrefixBlocks / items + 1, rows <= 256 items
   const size_t rows = static_cast<size_t>(T) * Hq;
-  const size_t parts = std::min<size_t>(kPrefixSplits * rows, kPrefixBlocks * kTileRows + rows);
+  const size_t parts = std::min<size_t>(kPrefixSplits * rows, kPrefixBlocks * kTileRows + rows) + rows;
   Workspace w;
   w.records = 256;
   w.ml = w.records + round256(sizeof(PieceRecord) * kFewPerSm * kMaxSms);
   w.o = w.ml + round256(sizeof(float2) * slots);
-  w.prefix_ml = w.o + round256(sizeof(float) * slots * dp);
-  w.prefix_o = w.prefix_ml + round256(sizeof(float2) * parts);
-  w.bytes = w.prefix_o + round256(sizeof(float) * parts * dp);
+  w.part_ml = w.o + round256(sizeof(float) * slots * dp);
+  w.part_o = w.part_ml + round256(sizeof(float2) * parts);
+  w.bytes = w.part_o + round256(sizeof(float) * parts * dp);
   return w;
 }
 
@@ -339,8 +400,8 @@ extern "C" moe_lora_status moe_lora_attention(moe_lora_handle* h, const moe_lora
   uint8_t* base = static_cast<uint8_t*>(workspace);
   p.piece_ml = reinterpret_cast<float2*>(base + at.ml);
   p.piece_o = reinterpret_cast<float*>(base + at.o);
-  p.prefix_ml = reinterpret_cast<float2*>(base + at.prefix_ml);
-  p.prefix_o = reinterpret_cast<float*>(base + at.prefix_o);
+  p.part_ml = reinterpret_cast<float2*>(base + at.part_ml);
+  p.part_o = reinterpret_cast<float*>(base + at.part_o);
   p.shared = a->B > 1 ? a->shared_len / kTileKeys * kTileKeys : 0;   // the rest is each request's own
   auto maps = [&](int keys) {
     return page_map(h, &p.tmap_k, p.k, p, p.k_t, p.k_h, p.k_p, keys) == CUDA_SUCCESS &&
@@ -364,18 +425,19 @@ extern "C" moe_lora_status moe_lora_attention(moe_lora_handle* h, const moe_lora
     p.plan.least = 2;
     p.plan.whole = own_keys <= 2LL * kTileKeys;
     p.long_queries = static_cast<long long>(a->max_query_len) * p.G > 8LL * kTileRows;
-    join_across = std::max(1, p.item_rows / 8);
+    join_across = (p.item_rows + kTeams - 1) / kTeams;
   } else {
     if (!maps(kFewKeys)) return cuda_fail(cudaErrorInvalidValue, "attention tensor maps");
     p.plan.ctas = kFewPerSm * h->num_sms;
     p.plan.least = 8;
     p.plan.whole = own_keys <= 16LL * kFewKeys;
     p.long_queries = 0;
-    join_across = std::max(1, p.item_rows / 2);
+    join_across = std::min(4, p.item_rows);
   }
   if (!p.plan.whole) p.records = reinterpret_cast<PieceRecord*>(base + at.records);
   ML_LAUNCH(h, tiles ? launch_attention_tiles(p, PrefixRun{}, p.plan.ctas, dp, stream) : launch_attention_rows(p, dp, stream),
             "attention launch");
   if (!p.plan.whole) ML_LAUNCH(h, launch_join(p, dp, join_across, stream), "attention join launch");
+  if (p.prefix_splits > 0) ML_LAUNCH(h, launch_fold(p, dp, stream), "attention fold launch");
   return MOE_LORA_OK;
 }

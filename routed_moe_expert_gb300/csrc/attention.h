@@ -47,10 +47,11 @@ struct AttentionParams {
   int item_rows;                               // rows of a piece's slot
   float2* piece_ml;                            // [2 ctas][item_rows] maximum (of scaled scores, base 2), sum
   float* piece_o;                              // [2 ctas][item_rows][DP]
-  // The shared keys' part of every row, made by a launch of its own: [prefix_splits][T * Hq]
-  float2* prefix_ml;
-  float* prefix_o;
-  int prefix_splits;                           // 0: none
+  // Parts of every row by token and head where keys are shared: the launch over those makes parts 0 to
+  // prefix_splits - 1, the requests' own keys the last.  [prefix_splits + 1][T * Hq]
+  float2* part_ml;
+  float* part_o;
+  int prefix_splits;                           // 0: no keys are shared
   uint32_t* status;
   int* flags;                                  // the handle's: error gathered so far, blocks that are done
 };
@@ -79,6 +80,24 @@ MLDEV Request request_of(const AttentionParams& p, int b) {
   r.bad = r.bad || kv < 0 || kv > room;
   r.kv = static_cast<int>(min(static_cast<long long>(max(kv, 0)), room));
   return r;
+}
+
+// Keys that query row `token` of the whole batch sees, -1 if it is no request's.
+MLDEV int keys_of_token(const AttentionParams& p, int token) {
+  int b = token;
+  Request r;
+  if (p.offsets != nullptr) {
+    int lo = 0, n = p.B;   // the last request that starts at or before the token
+    while (n > 1) {
+      const int half = n >> 1;
+      if (p.offsets[lo + half] <= token) lo += half;
+      n -= half;
+    }
+    b = lo;
+  }
+  r = request_of(p, b);
+  if (token < r.q0 || token >= r.q0 + r.n) return -1;
+  return max(r.kv - r.n + (token - r.q0) + 1, 0);
 }
 
 MLDEV float exp2_approx(float x) {   // 2^-22 relative; 0 for -inf
@@ -340,10 +359,12 @@ MLDEV PieceRecord record_of(const AttentionParams& p, const Schedule<ROWS, KEYS>
   return c;
 }
 
-// The end of a block's work (one thread): the last block of the launch writes the status word, 0 or an
-// error that some block met, and leaves the handle's flags zero.
-MLDEV void finish_status(const AttentionParams& p, uint32_t error) {
+// The end of a block's work (one thread): its error, if it met one, goes to the handle's flag.  Where no other
+// kernel of the call follows (`last`), the last block writes the status word and leaves the flags zero; else
+// the call's last kernel does (take_status).
+MLDEV void finish_status(const AttentionParams& p, uint32_t error, bool last) {
   if (error != 0) atomicCAS(p.flags, 0, static_cast<int>(error));
+  if (!last) return;
   __threadfence();
   if (atomicAdd(p.flags + 1, 1) == static_cast<int>(gridDim.x) - 1) {
     __threadfence();
@@ -352,23 +373,11 @@ MLDEV void finish_status(const AttentionParams& p, uint32_t error) {
   }
 }
 
-// Adds the shared keys' part of 8 values of a row to (m, l, o); row = token * Hq + head.
-template <int DP>
-MLDEV void add_prefix(const AttentionParams& p, long long row, int d, float& m, float& l, float (&o)[8]) {
-  const long long rows = static_cast<long long>(p.T) * p.Hq;
-  for (int s = 0; s < p.prefix_splits; ++s) {
-    const float2 ml = p.prefix_ml[s * rows + row];
-    if (ml.y == 0.0f) continue;   // (a NaN is not)
-    const float4* src = reinterpret_cast<const float4*>(p.prefix_o + (s * rows + row) * DP + d);
-    const float4 a = src[0], c = src[1];
-    const float top = fmaxf(m, ml.x), ref = reference_of(top);
-    const float f = exp2_approx(m - ref), g = exp2_approx(ml.x - ref);
-    m = top;
-    l = l * f + ml.y * g;
-    const float v[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = o[i] * f + v[i] * g;
-  }
+MLDEV void take_status(const AttentionParams& p) { *p.status = static_cast<uint32_t>(atomicExch(p.flags, 0)); }
+
+// Where the result of a row goes when it is not final: a piece, or the last part of the row.
+MLDEV long long part_row(const AttentionParams& p, long long token, int head) {
+  return (static_cast<long long>(p.prefix_splits) * p.T + token) * p.Hq + head;
 }
 
 // Eight values of a finished row, and its logarithm where d is 0.

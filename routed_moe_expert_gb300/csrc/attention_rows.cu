@@ -76,7 +76,9 @@ __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(con
     tma_prefetch_desc(&p.tmap_v);
   }
   __syncthreads();
-  pdl_wait();
+  // With shared keys the kernel in front is their launch, whose results are not needed here; what came before
+  // it is done, since it has waited for that.
+  if (p.prefix_splits == 0) pdl_wait();
   pdl_trigger();
 
   Sched s;
@@ -322,17 +324,16 @@ __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(con
         float val[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) val[i] = sum_s[r * DP + d + i];
-        if (x.all) {
-          const long long token = w.r.q0 + (row0 + r) / p.G;
-          const int head = w.kh * p.G + (row0 + r) % p.G;
-          add_prefix<DP>(p, token * p.Hq + head, d, m, l, val);
+        const long long token = w.r.q0 + (row0 + r) / p.G;
+        const int head = w.kh * p.G + (row0 + r) % p.G;
+        if (x.all && p.prefix_splits == 0) {
           write_row8(p, token, head, d, m, l, val);
         } else {
-          const long long at = static_cast<long long>(x.slot) * p.item_rows + r;
-          float4* to = reinterpret_cast<float4*>(p.piece_o + at * DP + d);
+          const long long at = x.all ? part_row(p, token, head) : static_cast<long long>(x.slot) * p.item_rows + r;
+          float4* to = reinterpret_cast<float4*>((x.all ? p.part_o : p.piece_o) + at * DP + d);
           to[0] = make_float4(val[0], val[1], val[2], val[3]);
           to[1] = make_float4(val[4], val[5], val[6], val[7]);
-          if (d == 0) p.piece_ml[at] = make_float2(m, l);
+          if (d == 0) (x.all ? p.part_ml : p.piece_ml)[at] = make_float2(m, l);
         }
       }
       if (!x.all && x.lo == 0 && threadIdx.x == 0) {
@@ -342,8 +343,9 @@ __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(con
     }
     if (!started && threadIdx.x == 0 && p.records != nullptr) p.records[cta].pieces = 0;
   }
+  if (p.prefix_splits > 0) pdl_wait();   // not to end before the launch in front, which the next one reads from
   __syncthreads();
-  if (threadIdx.x == 0) finish_status(p, error_s);
+  if (threadIdx.x == 0) finish_status(p, error_s, p.records == nullptr && p.prefix_splits == 0);
 }
 
 }  // namespace

@@ -85,24 +85,6 @@ MLDEV float2 add2(float2 a, float2 b) {
   return r;
 }
 
-// Keys that query row `token` of the whole batch sees, -1 if it is no request's.
-MLDEV int keys_of_token(const AttentionParams& p, int token) {
-  int b = token;
-  Request r;
-  if (p.offsets != nullptr) {
-    int lo = 0, n = p.B;   // the last request that starts at or before the token
-    while (n > 1) {
-      const int half = n >> 1;
-      if (p.offsets[lo + half] <= token) lo += half;
-      n -= half;
-    }
-    b = lo;
-  }
-  r = request_of(p, b);
-  if (token < r.q0 || token >= r.q0 + r.n) return -1;
-  return max(r.kv - r.n + (token - r.q0) + 1, 0);
-}
-
 // A part of an item as every role sees it, made by the scheduling warp.
 struct Step {
   int end;             // no more parts
@@ -175,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_s, 0);
-  pdl_wait();
+  if (p.prefix_splits == 0 || prefix.splits > 0) pdl_wait();   // (as in attention_rows.cu)
   pdl_trigger();
 
   Sched s;
@@ -652,6 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
       // ---- with the same rows in both tiles: the other tile's maximum and sum, and half of the columns each
       const bool pair = lead == 2;
       float other = 0.0f, mine = 1.0f;   // factors of the other tile's result and this one's
+      bool mine_0 = false, other_0 = false;   // nothing was seen there
       if (pair) {
         ml_s[k][r] = make_float2(ref, l);
         tc_fence_before();
@@ -667,30 +650,35 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
         l = a.y * fa + b.y * fb;
         mine = k == 0 ? fa : fb;
         other = k == 0 ? fb : fa;
+        mine_0 = (k == 0 ? a.y : b.y) == 0.0f;
+        other_0 = (k == 0 ? b.y : a.y) == 0.0f;
       }
       const bool has_mine = first_unit < hi, has_other = pair && lo + (k ^ 1) < hi_other;
       const int c_lo = pair ? k * (DP / 2) : 0, c_hi = pair ? c_lo + DP / 2 : DP;
       const bool real = r < rows;
+      const bool final = all && p.prefix_splits == 0;
+      const bool by_token = prefix.splits > 0 || all;   // not a piece but a part of the row
       const long long at = prefix.splits > 0 ? (static_cast<long long>(slot) * p.T + token) * p.Hq + head
+                           : all             ? part_row(p, token, head)
                                              : static_cast<long long>(slot) * p.item_rows + tile_row;
       // Results leave through shared memory, 64 bytes of a row at a time, so that a warp writes whole pieces of
       // its rows: a thread a row would touch 32 rows a store.
-      const bool by_row = all && (p.prefix_splits > 0 || !p.out_vec);   // unless they need more than that
-      float* piece_o = prefix.splits > 0 ? p.prefix_o : p.piece_o;
+      const bool by_row = final && !p.out_vec;   // unless `out` is not aligned to that
+      float* piece_o = by_token ? p.part_o : p.piece_o;
       unsigned long long to = 0;
       if (real)
-        to = all ? reinterpret_cast<unsigned long long>(p.out + token * p.o_t + head * p.o_h)
-                 : reinterpret_cast<unsigned long long>(piece_o + at * DP);
+        to = final ? reinterpret_cast<unsigned long long>(p.out + token * p.o_t + head * p.o_h)
+                   : reinterpret_cast<unsigned long long>(piece_o + at * DP);
       unsigned long long dst[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) dst[i] = __shfl_sync(0xffffffffu, to, i * 8 + (lane >> 2));
-      if (all && !by_row) {
+      if (final && !by_row) {
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         mine *= inv;
         other *= inv;
       }
-      const bool none = l == 0.0f && all;   // a row that sees nothing, or whose every score is -inf
-      const int width = all ? 32 : 16;      // columns of 64 bytes
+      const bool none = l == 0.0f;  // a row that sees nothing, or whose every score is -inf
+      const int width = final ? 32 : 16;     // columns of 64 bytes
       if (wr < rows) {
 #pragma unroll 1
         for (int c = c_lo; c < c_hi; c += width) {
@@ -700,18 +688,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = 0.0f;
           if (has_mine) {
-            if (all) tmem_ld_x32(o_at + c, v);
+            if (final) tmem_ld_x32(o_at + c, v);
             else tmem_ld_x16(o_at + c, reinterpret_cast<uint32_t(&)[16]>(v));
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(v[i]) * mine;
+            for (int i = 0; i < 32; ++i) o[i] = mine_0 ? 0.0f : __uint_as_float(v[i]) * mine;
           }
           if (has_other) {
-            if (all) tmem_ld_x32(lanes + 256 + (k ^ 1) * DP + c, v);
+            if (final) tmem_ld_x32(lanes + 256 + (k ^ 1) * DP + c, v);
             else tmem_ld_x16(lanes + 256 + (k ^ 1) * DP + c, reinterpret_cast<uint32_t(&)[16]>(v));
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = fmaf(__uint_as_float(v[i]), other, o[i]);
+            for (int i = 0; i < 32; ++i) o[i] = other_0 ? o[i] : fmaf(__uint_as_float(v[i]), other, o[i]);
           }
           if (by_row) {
             if (real) {
@@ -720,9 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
                 float e[8];
 #pragma unroll
                 for (int n = 0; n < 8; ++n) e[n] = o[i + n];
-                float m = ref, sum = l;
-                add_prefix<DP>(p, static_cast<long long>(token) * p.Hq + head, c + i, m, sum, e);
-                write_row8(p, token, head, c + i, m, sum, e);
+                write_row8(p, token, head, c + i, ref, l, e);
               }
             }
             continue;
@@ -730,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             uint4 x;
-            if (all) {
+            if (final) {
               const float e[8] = {o[8 * i],     o[8 * i + 1], o[8 * i + 2], o[8 * i + 3],
                                   o[8 * i + 4], o[8 * i + 5], o[8 * i + 6], o[8 * i + 7]};
               x = pack8(e);
@@ -742,8 +728,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
             *reinterpret_cast<uint4*>(stage + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) = x;
           }
           __syncwarp();
-          const int part = lane & 3, bytes = (all ? 2 : 4) * c + 16 * part;
-          const bool inside = !all || c + part * 8 < p.D;
+          const int part = lane & 3, bytes = (final ? 2 : 4) * c + 16 * part;
+          const bool inside = !final || c + part * 8 < p.D;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int of = i * 8 + (lane >> 2);
@@ -753,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
         }
       }
       if (real && c_lo == 0) {
-        if (!all) (prefix.splits > 0 ? p.prefix_ml : p.piece_ml)[at] = make_float2(ref, l);
+        if (!final) (by_token ? p.part_ml : p.piece_ml)[at] = make_float2(ref, l);
         else if (!by_row && p.lse != nullptr)
           p.lse[static_cast<long long>(token) * p.Hq + head] = (reference_of(ref) + log2f(l)) * kLn2;
       }
@@ -769,19 +755,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
     asm volatile("cp.async.wait_group 0;" ::: "memory");
   }
 
+  if (p.prefix_splits > 0 && prefix.splits == 0) pdl_wait();
   tc_fence_before();
   __syncthreads();
   if (warp == kMma) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  if (threadIdx.x == 0) {
-    if (prefix.splits > 0) {   // the launch that follows gathers errors
-      if (error_s != 0) atomicCAS(p.flags, 0, static_cast<int>(error_s));
-    } else {
-      finish_status(p, error_s);
-    }
-  }
+  if (threadIdx.x == 0) finish_status(p, error_s, p.records == nullptr && p.prefix_splits == 0 && prefix.splits == 0);
 }
 
 }  // namespace
