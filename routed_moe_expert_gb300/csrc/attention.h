@@ -10,7 +10,8 @@ namespace mlk {
 // item is up to `rows` of them (Plan::rows) with the keys that its last row sees, cut into units of
 // `keys` keys.  The units of all items, one request after another, are dealt to the blocks in equal runs,
 // whatever the requests' lengths (which only the device knows): a block works on the end of one item, whole
-// items, and the start of another.  Where a run holds part of an item its result is a piece (unnormalised
+// items, and the start of another.  An item weighs some units more than it has (OVER), for what a block does at its
+// start and end; a run that ends within these has none of the item.  Where a run holds part of an item its result is a piece (unnormalised
 // sums, maximum, sum of weights) in the workspace, at most two a block, and the block that has the item's
 // first unit leaves a record, by which the kernel that follows adds the pieces up.
 //
@@ -100,6 +101,15 @@ MLDEV int keys_of_token(const AttentionParams& p, int token) {
   return max(r.kv - r.n + (token - r.q0) + 1, 0);
 }
 
+// mbar_wait for the waits that a step's time is made of: the timer is read only after some tries, each of which
+// suspends the thread for a while (read before the second try it cost every blocked wait 0.3 us).
+MLDEV bool wait_soon(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* status) {
+#pragma unroll 1
+  for (int i = 0; i < 256; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait(bar, parity, abort_flag, status, kWhereAttention);
+}
+
 MLDEV float exp2_approx(float x) {   // 2^-22 relative; 0 for -inf
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -110,18 +120,18 @@ MLDEV float exp2_approx(float x) {   // 2^-22 relative; 0 for -inf
 MLDEV float reference_of(float m) { return m == -INFINITY ? 0.0f : m; }
 
 // ---------------------------------------------------------------- the plan, worked out by every block
-template <int ROWS, int KEYS>
+template <int ROWS, int KEYS, int OVER>
 struct Schedule {
   // of this launch and block
   int ctas;              // blocks that work
-  long long units;       // of the call
+  long long units;       // all items' weight
   long long start, end;  // this block's run
   bool bad;
 
-  // Units of item i of a request (at least one, so that rows that see nothing are written).
-  static MLDEV int units_of(const AttentionParams& p, const Request& r, int i) {
+  // What item i of a request weighs: its units (at least one, so that rows that see nothing are written) and OVER.
+  static MLDEV int weight_of(const AttentionParams& p, const Request& r, int i) {
     const int sees = seen_by(p, r, i) - p.shared;
-    return sees <= 0 ? 1 : (sees + KEYS - 1) / KEYS;
+    return (sees <= 0 ? 1 : (sees + KEYS - 1) / KEYS) + OVER;
   }
   // Keys that the last row of item i sees.
   static MLDEV int seen_by(const AttentionParams& p, const Request& r, int i) {
@@ -132,17 +142,17 @@ struct Schedule {
     return (r.n * p.G + ROWS - 1) / ROWS;
   }
 
-  // The block that has unit u.
+  // The block whose run has u.
   MLDEV int block_of(long long u) const { return static_cast<int>(((u + 1) * ctas - 1) / units); }
   MLDEV long long start_of(int c) const { return units * c / ctas; }
 };
 
 // A place in the schedule, advanced item by item; every role of a block walks through the same ones.
-template <int ROWS, int KEYS>
+template <int ROWS, int KEYS, int OVER>
 struct Walk {
-  using S = Schedule<ROWS, KEYS>;
-  int b, kh, i, items, units;   // of the request's items; units of this item
-  long long u0;                 // the item's first unit
+  using S = Schedule<ROWS, KEYS, OVER>;
+  int b, kh, i, items, units;   // of the request's items; weight of this item
+  long long u0;                 // of all items before it
   Request r;
 
   MLDEV void enter(const AttentionParams& p) {   // the first item of request b, or of one behind it that has any
@@ -153,7 +163,7 @@ struct Walk {
       ++b;
     }
     kh = i = 0;
-    if (b < p.B) units = S::units_of(p, r, 0);
+    if (b < p.B) units = S::weight_of(p, r, 0);
   }
   MLDEV void next(const AttentionParams& p) {
     u0 += units;
@@ -165,7 +175,7 @@ struct Walk {
         return;
       }
     }
-    if (items > 1) units = S::units_of(p, r, i);
+    if (items > 1) units = S::weight_of(p, r, i);
   }
 };
 
@@ -178,10 +188,10 @@ struct ScheduleSmem {
 };
 
 // Works out the schedule and the block's first item.  All threads of the block; `sums_s` [blockDim] scratch.
-template <int ROWS, int KEYS>
-MLDEV void make_schedule(const AttentionParams& p, int cta, Schedule<ROWS, KEYS>& s, Walk<ROWS, KEYS>& w, ScheduleSmem& sm,
+template <int ROWS, int KEYS, int OVER>
+MLDEV void make_schedule(const AttentionParams& p, int cta, Schedule<ROWS, KEYS, OVER>& s, Walk<ROWS, KEYS, OVER>& w, ScheduleSmem& sm,
                          long long* sums_s) {
-  using S = Schedule<ROWS, KEYS>;
+  using S = Schedule<ROWS, KEYS, OVER>;
   const int tid = threadIdx.x, NT = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = NT >> 5;
   // the units of request b0 + tid (and its items), for a chunk of NT requests
   auto chunk = [&](int b0, int& items, bool& bad) -> long long {
@@ -191,7 +201,7 @@ MLDEV void make_schedule(const AttentionParams& p, int cta, Schedule<ROWS, KEYS>
       if (b0 + tid < p.B) {
         const Request r = request_of(p, b0 + tid);
         const int n = S::items_of(p, r);
-        for (int i = 0; i < n; ++i) sum += S::units_of(p, r, i);
+        for (int i = 0; i < n; ++i) sum += S::weight_of(p, r, i);
         items = n;
         bad = bad || r.bad;
       }
@@ -201,7 +211,7 @@ MLDEV void make_schedule(const AttentionParams& p, int cta, Schedule<ROWS, KEYS>
       const Request r = request_of(p, b0 + k);
       const int n = S::items_of(p, r);
       long long part = 0;
-      for (int i = lane; i < n; i += 32) part += S::units_of(p, r, i);
+      for (int i = lane; i < n; i += 32) part += S::weight_of(p, r, i);
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) part += __shfl_xor_sync(0xffffffffu, part, off);
       if (lane == 0) sums_s[k] = part;
@@ -283,7 +293,7 @@ MLDEV void make_schedule(const AttentionParams& p, int cta, Schedule<ROWS, KEYS>
   w.items = S::items_of(p, w.r);
   w.u0 = sm.found_base;
   if (w.items == 1) {
-    w.units = S::units_of(p, w.r, 0);
+    w.units = S::weight_of(p, w.r, 0);
     w.kh = static_cast<int>((s.start - w.u0) / w.units);
     w.u0 += static_cast<long long>(w.kh) * w.units;
     w.i = 0;
@@ -291,13 +301,13 @@ MLDEV void make_schedule(const AttentionParams& p, int cta, Schedule<ROWS, KEYS>
   }
   if (warp == 0) {
     long long per = 0;
-    for (int i = lane; i < w.items; i += 32) per += S::units_of(p, w.r, i);
+    for (int i = lane; i < w.items; i += 32) per += S::weight_of(p, w.r, i);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) per += __shfl_xor_sync(0xffffffffu, per, off);
     const int kh = static_cast<int>((s.start - w.u0) / per);
     long long at = w.u0 + kh * per;   // first unit of items i0..
     for (int i0 = 0; i0 < w.items; i0 += 32) {
-      const int own = i0 + lane < w.items ? S::units_of(p, w.r, i0 + lane) : 0;
+      const int own = i0 + lane < w.items ? S::weight_of(p, w.r, i0 + lane) : 0;
       int incl = own;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -316,7 +326,7 @@ MLDEV void make_schedule(const AttentionParams& p, int cta, Schedule<ROWS, KEYS>
   w.i = sm.found_i;
   w.u0 = sm.found_u;
   w.kh = static_cast<int>(sm.head[0]);
-  w.units = S::units_of(p, w.r, w.i);
+  w.units = S::weight_of(p, w.r, w.i);
 }
 
 // What a block does of the item that a walk is at: units [lo, hi), and where the result goes.
@@ -325,29 +335,29 @@ struct Part {
   bool all;      // the whole item: the result is final
   int slot;      // else: the piece's slot
 };
-template <int ROWS, int KEYS>
-MLDEV Part part_of(const AttentionParams& p, const Schedule<ROWS, KEYS>& s, const Walk<ROWS, KEYS>& w, int cta) {
+template <int ROWS, int KEYS, int OVER>
+MLDEV Part part_of(const AttentionParams& p, const Schedule<ROWS, KEYS, OVER>& s, const Walk<ROWS, KEYS, OVER>& w, int cta) {
   Part x;
   if (p.plan.whole) {
     x.lo = 0;
-    x.hi = w.u0 < s.start ? 0 : w.units;   // hi 0: begun in the run of a block before
+    x.hi = w.u0 < s.start ? 0 : w.units - OVER;   // hi 0: begun in the run of a block before
     x.all = true;
     x.slot = 0;
     return x;
   }
-  x.lo = static_cast<int>(max(s.start - w.u0, 0ll));
-  x.hi = static_cast<int>(min(s.end - w.u0, static_cast<long long>(w.units)));
-  x.all = x.lo == 0 && x.hi == w.units;
+  x.lo = static_cast<int>(max(s.start - w.u0 - OVER, 0ll));
+  x.hi = static_cast<int>(min(s.end - w.u0 - OVER, static_cast<long long>(w.units - OVER)));
+  x.all = x.lo == 0 && x.hi == w.units - OVER;
   x.slot = 2 * cta + (w.u0 > s.start ? 1 : 0);
   return x;
 }
-template <int ROWS, int KEYS>
-MLDEV bool more(const Schedule<ROWS, KEYS>& s, const Walk<ROWS, KEYS>& w, const AttentionParams& p) {
+template <int ROWS, int KEYS, int OVER>
+MLDEV bool more(const Schedule<ROWS, KEYS, OVER>& s, const Walk<ROWS, KEYS, OVER>& w, const AttentionParams& p) {
   return w.b < p.B && w.u0 < s.end;
 }
 // The record of a piece that begins an item (one thread).
-template <int ROWS, int KEYS>
-MLDEV PieceRecord record_of(const AttentionParams& p, const Schedule<ROWS, KEYS>& s, const Walk<ROWS, KEYS>& w, const Part& x,
+template <int ROWS, int KEYS, int OVER>
+MLDEV PieceRecord record_of(const AttentionParams& p, const Schedule<ROWS, KEYS, OVER>& s, const Walk<ROWS, KEYS, OVER>& w, const Part& x,
                             int cta) {
   PieceRecord c;
   c.pieces = s.block_of(w.u0 + w.units - 1) - cta + 1;
@@ -417,8 +427,8 @@ struct PrefixRun {
 };
 
 // Launches (attention_rows.cu, attention_tiles.cu)
-constexpr int kFewRows = 16, kFewKeys = 64, kFewPerSm = 2;
-constexpr int kTileRows = 256, kTileKeys = 128;
+constexpr int kFewRows = 16, kFewKeys = 64, kFewPerSm = 2, kFewOver = 1;
+constexpr int kTileRows = 256, kTileKeys = 128, kTileOver = 2;
 cudaError_t prepare_attention_rows();
 cudaError_t launch_attention_rows(const AttentionParams& p, int dp, cudaStream_t stream);
 cudaError_t prepare_attention_tiles();

@@ -15,8 +15,8 @@ namespace {
 
 constexpr int kRows = kFewRows, kKeys = kFewKeys;
 constexpr int kConsumers = 4, kThreads = 32 * (kConsumers + 1);
-using Sched = Schedule<kRows, kKeys>;
-using Place = Walk<kRows, kKeys>;
+using Sched = Schedule<kRows, kKeys, kFewOver>;
+using Place = Walk<kRows, kKeys, kFewOver>;
 
 __host__ __device__ constexpr int stage_bytes(int dp) { return 2 * kKeys * dp * 2; }   // keys, then values
 __host__ __device__ constexpr int stages_of(int dp) { return dp == 64 ? 6 : 3; }
@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(con
 
   Sched s;
   Place w;
-  make_schedule<kRows, kKeys>(p, cta, s, w, sched_s, sums_s);
+  make_schedule<kRows, kKeys, kFewOver>(p, cta, s, w, sched_s, sums_s);
   if (threadIdx.x == 0 && s.bad) record_status(&error_s, kDevBadSlot, kWhereAttention);
 
   if (warp == kConsumers) {   // ------------------------------------------------ producer
@@ -91,8 +91,8 @@ __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(con
     const int box_log2 = min(p.page_log2, 6), box = 1 << box_log2, boxes = kKeys >> box_log2;   // boxes of a unit
     int stage = 0, ok = 1;
     uint32_t phase = 0, issued = 0, parity = 0;
-    for (; ok && more<kRows, kKeys>(s, w, p); w.next(p)) {
-      const Part x = part_of<kRows, kKeys>(p, s, w, cta);
+    for (; ok && more<kRows, kKeys, kFewOver>(s, w, p); w.next(p)) {
+      const Part x = part_of<kRows, kKeys, kFewOver>(p, s, w, cta);
       const int sees = Sched::seen_by(p, w.r, w.i);
       const int32_t* table = p.tables + w.b * p.table_stride;
       // A lane a box; its page is looked up a unit ahead of its use.
@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(con
         }
         const int n = __popc(__ballot_sync(0xffffffffu, mine));
         if (lane == 0) {
-          ok = mbar_wait(&empty[stage], phase ^ 1u, abort_flag, &error_s, kWhereAttention);
+          ok = wait_soon(&empty[stage], phase ^ 1u, abort_flag, &error_s);
           if (ok) mbar_arrive_expect_tx(&full[stage], n * 2 * box * HALVES * 128);
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -143,8 +143,8 @@ __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(con
     int stage = 0, ok = 1;
     uint32_t phase = 0;
     bool started = false;   // an item whose rest is other blocks'
-    for (; ok && more<kRows, kKeys>(s, w, p); w.next(p)) {
-      const Part x = part_of<kRows, kKeys>(p, s, w, cta);
+    for (; ok && more<kRows, kKeys, kFewOver>(s, w, p); w.next(p)) {
+      const Part x = part_of<kRows, kKeys, kFewOver>(p, s, w, cta);
       if (x.lo >= x.hi) continue;
       const int row0 = w.i * kRows;
       const int rows = min(kRows, w.r.n * p.G - row0);
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(con
       for (int n = 0; n < DP / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.0f;
       float ma = -INFINITY, mb = -INFINITY, la = 0.0f, lb = 0.0f;
       for (int j = x.lo; j < x.hi; ++j) {
-        ok = mbar_wait(&full[stage], phase, abort_flag, &error_s, kWhereAttention);
+        ok = wait_soon(&full[stage], phase, abort_flag, &error_s);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const int k0 = p.shared + j * kKeys + warp * 16;   // this warp's keys of the unit
@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(con
         }
       }
       if (!x.all && x.lo == 0 && threadIdx.x == 0) {
-        p.records[cta] = record_of<kRows, kKeys>(p, s, w, x, cta);
+        p.records[cta] = record_of<kRows, kKeys, kFewOver>(p, s, w, x, cta);
         started = true;
       }
     }

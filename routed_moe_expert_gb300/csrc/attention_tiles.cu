@@ -29,8 +29,8 @@ namespace {
 constexpr int kRows = kTileRows, kKeys = kTileKeys;
 constexpr int kThreads = 384;
 constexpr int kProducer = 8, kMma = 9, kCleaner = 10, kScheduler = 11;
-using Sched = Schedule<kRows, kKeys>;
-using Place = Walk<kRows, kKeys>;
+using Sched = Schedule<kRows, kKeys, kTileOver>;
+using Place = Walk<kRows, kKeys, kTileOver>;
 
 constexpr int kHalf = kKeys * 128;   // 64 values of 128 rows
 __host__ __device__ constexpr int tile_bytes(int dp) { return dp / 64 * kHalf; }
@@ -67,6 +67,11 @@ constexpr uint32_t kMnMajorHi = (1024 >> 4) | (1u << 14) | (2u << 29);
 constexpr uint32_t kKMajorHi = kMnMajorHi;
 constexpr uint32_t kMnMajorB = 1u << 16;
 
+MLDEV float max3(float a, float b, float c) {   // a NaN is left out, as fmaxf does
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 // Two float32 operations an instruction.
 MLDEV float2 fma2(float2 a, float2 b, float2 c) {
   float2 r;
@@ -111,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* ring = smem + 2 * TILE;
   uint8_t* stages = ring + kSlots * TILE;   // 2 KB a row warp
-  __shared__ uint64_t full[kSlots], empty[kSlots], s_full[2], p_ready[2], o_full[2], q_full[2], v_asked, v_clean, both[2], drain;
+  __shared__ uint64_t full[kSlots], empty[kSlots], s_full[2], p_ready[2][2], o_full[2], q_full[2], v_asked, v_clean, both[2], drain;
   __shared__ uint64_t step_full[kSteps], step_empty[kSteps];
   __shared__ Step steps[kSteps];
   __shared__ ScheduleSmem sched_s;
@@ -129,10 +134,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&s_full[t], 1);
-      mbar_init(&p_ready[t], 128);
+      mbar_init(&p_ready[t][0], 4);   // a lane a warp; the weights of the first 64 keys, and of the others
+      mbar_init(&p_ready[t][1], 4);
       mbar_init(&o_full[t], 1);
-      mbar_init(&q_full[t], 128);
-      mbar_init(&both[t], 256);
+      mbar_init(&q_full[t], 4);
+      mbar_init(&both[t], 8);
     }
     for (int i = 0; i < kSteps; ++i) {
       mbar_init(&step_full[i], 1);
@@ -163,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
   Sched s;
   Place w;
   if (prefix.splits == 0) {
-    make_schedule<kRows, kKeys>(p, cta, s, w, sched_s, reinterpret_cast<long long*>(smem));
+    make_schedule<kRows, kKeys, kTileOver>(p, cta, s, w, sched_s, reinterpret_cast<long long*>(smem));
     __syncthreads();   // the scratch is the query tiles' again
     if (threadIdx.x == 0 && s.bad) record_status(&error_s, kDevBadSlot, kWhereAttention);
   }
@@ -172,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
   int at_step = 0;            // of the ring of steps
   uint32_t step_phase = 0;
   auto step_here = [&]() {    // waits for the next part; the warp's lanes together
-    ok = mbar_wait_sleep(&step_full[at_step], step_phase, abort_flag, &error_s, kWhereAttention);
+    ok = wait_soon(&step_full[at_step], step_phase, abort_flag, &error_s);
     ok = __all_sync(0xffffffffu, ok);
     return ok != 0;
   };
@@ -211,11 +217,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
           if (!first) w.next(p);
           Part x;
           while (true) {
-            if (!more<kRows, kKeys>(s, w, p)) {
+            if (!more<kRows, kKeys, kTileOver>(s, w, p)) {
               t.end = 1;
               break;
             }
-            x = part_of<kRows, kKeys>(p, s, w, cta);
+            x = part_of<kRows, kKeys, kTileOver>(p, s, w, cta);
             if (x.lo < x.hi) break;
             w.next(p);
           }
@@ -232,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
             t.all = x.all;
             t.slot = x.slot;
             if (!x.all && x.lo == 0) {
-              if (lane == 0) p.records[cta] = record_of<kRows, kKeys>(p, s, w, x, cta);
+              if (lane == 0) p.records[cta] = record_of<kRows, kKeys, kTileOver>(p, s, w, x, cta);
               started = true;
             }
           }
@@ -263,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
           t.hi1 = units[1];
           t.most = max(units[0], units[1]);
         }
-        ok = mbar_wait_sleep(&step_empty[at_step], step_phase ^ 1u, abort_flag, &error_s, kWhereAttention);
+        ok = wait_soon(&step_empty[at_step], step_phase ^ 1u, abort_flag, &error_s);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (lane == 0) {
@@ -316,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
           }
           const int count = __popc(__ballot_sync(0xffffffffu, mine));
           if (lane == 0) {
-            ok = mbar_wait_sleep(&empty[slot], phase ^ 1u, abort_flag, &error_s, kWhereAttention);
+            ok = wait_soon(&empty[slot], phase ^ 1u, abort_flag, &error_s);
             if (ok) mbar_arrive_expect_tx(&full[slot], count * box * HALVES * 128);
           }
           ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -348,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
       int slot = 0;
       uint32_t phase = 0, q_phase = 0, p_phase = 0, clean_phase = 0;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, &error_s, kWhereAttention));
+        ok = __all_sync(0xffffffffu, wait_soon(bar, parity, abort_flag, &error_s));
         return ok != 0;
       };
       auto advance = [&]() {
@@ -413,14 +419,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
           for (int k = 0; k < 2; ++k) {
             if (!ok) continue;
             if (t.has(k, j)) {
-              if (!wait(&p_ready[k], (p_phase >> k) & 1u)) continue;
-              p_phase ^= 1u << k;
-              tc_fence_after();
               const uint32_t b = desc_lo(ring_at + v_slot * TILE) | (static_cast<uint32_t>(kHalf >> 4) << 16);
 #pragma unroll
-              for (int ks = 0; ks < kKeys / 16; ++ks)
+              for (int ks = 0; ks < kKeys / 16; ++ks) {
+                if (ks % 4 == 0) {
+                  if (!wait(&p_ready[k][ks / 4], (p_phase >> k) & 1u)) break;
+                  tc_fence_after();
+                }
                 umma_ts(tmem + 256 + k * DP, tmem + k * 128 + ks * 8, b + ks * (2048 >> 4), kMnMajorHi, o_idesc,
                         j >= t.lo + t.lead || ks > 0, leader);
+              }
+              if (!ok) continue;
+              p_phase ^= 1u << k;
               if (ahead >= t.hi(k)) commit(&o_full[k]);
             }
             if (t.has(k, ahead)) {
@@ -456,8 +466,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
         if (n > 0 && key0 + t.most * kKeys > t.sees) {   // the part's last unit
           const unsigned long long at = used + 2ull * n - 1;   // the part's last slot: its last unit's values
           const int slot = static_cast<int>(at % kSlots);
-          ok = mbar_wait_sleep(&v_asked, asked_phase, abort_flag, &error_s, kWhereAttention) &&
-               mbar_wait(&full[slot], static_cast<uint32_t>(at / kSlots) & 1u, abort_flag, &error_s, kWhereAttention);
+          ok = wait_soon(&v_asked, asked_phase, abort_flag, &error_s) &&
+               wait_soon(&full[slot], static_cast<uint32_t>(at / kSlots) & 1u, abort_flag, &error_s);
           asked_phase ^= 1u;
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
@@ -503,10 +513,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
+    auto arrive = [&](uint64_t* bar) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
     auto queries_there = [&]() {
       asm volatile("cp.async.wait_group 0;" ::: "memory");
       fence_proxy_async_smem();
-      mbar_arrive(&q_full[k]);
+      arrive(&q_full[k]);
     };
     bool asked = false;   // the query rows of the part at hand are on their way, or there
     while (step_here()) {
@@ -548,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
       float ref = -INFINITY, l = 0.0f;
       const bool idle = wr >= rows;   // no row of this warp is one: its weights may be anything
       for (int j = first_unit; j < hi; j += lead) {
-        ok = mbar_wait(&s_full[k], s_phase, abort_flag, &error_s, kWhereAttention);
+        ok = wait_soon(&s_full[k], s_phase, abort_flag, &error_s);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         s_phase ^= 1u;
@@ -556,7 +570,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
         if (j + lead >= hi) fetch_next();
         if (!ok) break;
         if (idle) {
-          mbar_arrive(&p_ready[k]);
+          arrive(&p_ready[k][0]);
+          arrive(&p_ready[k][1]);
           continue;
         }
         uint32_t v[4][32];
@@ -578,9 +593,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
         }
         float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
+        for (int i = 0; i < 32; i += 2)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tops[c] = fmaxf(tops[c], __uint_as_float(v[c][i]));
+          for (int c = 0; c < 4; ++c) tops[c] = max3(tops[c], __uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1]));
         const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * scale;   // (scale is not 0)
         const bool grow = top > ref + 8.0f;
         if (__any_sync(0xffffffffu, grow)) {
@@ -613,19 +628,21 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
             const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
             v[c >> 1][(c & 1) * 16 + i / 2] = *reinterpret_cast<const uint32_t*>(&h);   // (read already)
           }
-          if (c & 1) tmem_st_x32(s_at + (c >> 1) * 32, v[c >> 1]);   // over the scores
+          if (c & 1) {   // over the scores, which are all read
+            tmem_st_x32(s_at + (c >> 1) * 32, v[c >> 1]);
+            tmem_st_wait();
+            tc_fence_before();
+            arrive(&p_ready[k][c >> 1]);   // the product starts on the first half
+          }
         }
         l += (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y);
-        tmem_st_wait();
-        tc_fence_before();
-        mbar_arrive(&p_ready[k]);
       }
       if (!ok) break;
       if (first_unit >= hi) fetch_next();
       if (!ok) break;
       if (asked) queries_there();
       if (first_unit < hi) {
-        ok = mbar_wait(&o_full[k], o_phase, abort_flag, &error_s, kWhereAttention);
+        ok = wait_soon(&o_full[k], o_phase, abort_flag, &error_s);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         o_phase ^= 1u;
@@ -638,8 +655,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
       if (pair) {
         ml_s[k][r] = make_float2(ref, l);
         tc_fence_before();
-        mbar_arrive(&both[0]);
-        ok = mbar_wait(&both[0], both_phase, abort_flag, &error_s, kWhereAttention);
+        arrive(&both[0]);
+        ok = wait_soon(&both[0], both_phase, abort_flag, &error_s);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
@@ -653,8 +670,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
         mine_0 = (k == 0 ? a.y : b.y) == 0.0f;
         other_0 = (k == 0 ? b.y : a.y) == 0.0f;
       }
-      const bool has_mine = first_unit < hi, has_other = pair && lo + (k ^ 1) < hi_other;
-      const int c_lo = pair ? k * (DP / 2) : 0, c_hi = pair ? c_lo + DP / 2 : DP;
+      const bool use_mine = first_unit < hi && !mine_0, use_other = pair && lo + (k ^ 1) < hi_other && !other_0;
+      const int c_lo = pair ? k * (DP / 2) : 0;   // its columns: DP from there, or half as many
       const bool real = r < rows;
       const bool final = all && p.prefix_splits == 0;
       const bool by_token = prefix.splits > 0 || all;   // not a piece but a part of the row
@@ -678,29 +695,27 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
         other *= inv;
       }
       const bool none = l == 0.0f;  // a row that sees nothing, or whose every score is -inf
-      const int width = final ? 32 : 16;     // columns of 64 bytes
       if (wr < rows) {
-#pragma unroll 1
-        for (int c = c_lo; c < c_hi; c += width) {
-          uint32_t v[32];
-          float o[32];
+        // Chunks of 32 columns; the next one's load is under way while one is written.
+        const int chunks = pair ? DP / 64 : DP / 32;
+        uint32_t own[32], mate[32];
+        auto fetch = [&](int c) {
           __syncwarp();
+          tmem_ld_x32(o_at + c_lo + c * 32, own);   // (whatever is there, if the tile had no unit)
+          tmem_ld_x32(lanes + 256 + (k ^ 1) * DP + c_lo + c * 32, mate);
+        };
+        fetch(0);
+#pragma unroll 1
+        for (int c = 0; c < chunks; ++c) {
+          float o[32];
+          tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = 0.0f;
-          if (has_mine) {
-            if (final) tmem_ld_x32(o_at + c, v);
-            else tmem_ld_x16(o_at + c, reinterpret_cast<uint32_t(&)[16]>(v));
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = mine_0 ? 0.0f : __uint_as_float(v[i]) * mine;
+          for (int i = 0; i < 32; ++i) {
+            o[i] = use_mine ? __uint_as_float(own[i]) * mine : 0.0f;
+            o[i] = use_other ? fmaf(__uint_as_float(mate[i]), other, o[i]) : o[i];
           }
-          if (has_other) {
-            if (final) tmem_ld_x32(lanes + 256 + (k ^ 1) * DP + c, v);
-            else tmem_ld_x16(lanes + 256 + (k ^ 1) * DP + c, reinterpret_cast<uint32_t(&)[16]>(v));
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = other_0 ? o[i] : fmaf(__uint_as_float(v[i]), other, o[i]);
-          }
+          if (c + 1 < chunks) fetch(c + 1);
+          const int col = c_lo + c * 32;
           if (by_row) {
             if (real) {
 #pragma unroll
@@ -708,33 +723,46 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
                 float e[8];
 #pragma unroll
                 for (int n = 0; n < 8; ++n) e[n] = o[i + n];
-                write_row8(p, token, head, c + i, ref, l, e);
+                write_row8(p, token, head, col + i, ref, l, e);
               }
             }
             continue;
           }
+          const int part = lane & 3;
+          auto leave = [&](const uint4 (&x)[4], int bytes, bool inside) {   // 64 bytes of every row
+            __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint4 x;
-            if (final) {
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<uint4*>(stage + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) = x[i];
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int of = i * 8 + (lane >> 2);
+              const uint4 y = *reinterpret_cast<const uint4*>(stage + of * 64 + ((part ^ ((of >> 1) & 3)) << 4));
+              if (dst[i] != 0 && inside) *reinterpret_cast<uint4*>(dst[i] + bytes + 16 * part) = y;
+            }
+          };
+          uint4 x[4];
+          if (final) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
               const float e[8] = {o[8 * i],     o[8 * i + 1], o[8 * i + 2], o[8 * i + 3],
                                   o[8 * i + 4], o[8 * i + 5], o[8 * i + 6], o[8 * i + 7]};
-              x = pack8(e);
-              if (none) x = make_uint4(0, 0, 0, 0);
-            } else {
-              x = make_uint4(__float_as_uint(o[4 * i]), __float_as_uint(o[4 * i + 1]), __float_as_uint(o[4 * i + 2]),
-                             __float_as_uint(o[4 * i + 3]));
+              x[i] = pack8(e);
+              if (none) x[i] = make_uint4(0, 0, 0, 0);
             }
-            *reinterpret_cast<uint4*>(stage + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) = x;
-          }
-          __syncwarp();
-          const int part = lane & 3, bytes = (final ? 2 : 4) * c + 16 * part;
-          const bool inside = !final || c + part * 8 < p.D;
+            leave(x, 2 * col, col + part * 8 < p.D);
+          } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int of = i * 8 + (lane >> 2);
-            const uint4 x = *reinterpret_cast<const uint4*>(stage + of * 64 + ((part ^ ((of >> 1) & 3)) << 4));
-            if (dst[i] != 0 && inside) *reinterpret_cast<uint4*>(dst[i] + bytes) = x;
+            for (int half = 0; half < 2; ++half) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int at4 = half * 16 + 4 * i;
+                x[i] = make_uint4(__float_as_uint(o[at4]), __float_as_uint(o[at4 + 1]), __float_as_uint(o[at4 + 2]),
+                                  __float_as_uint(o[at4 + 3]));
+              }
+              leave(x, 4 * (col + half * 16), true);
+            }
           }
         }
       }
@@ -745,8 +773,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
       }
       tc_fence_before();
       if (pair) {   // neither tile's next item overwrites what the other still reads
-        mbar_arrive(&both[1]);
-        ok = mbar_wait(&both[1], both_phase, abort_flag, &error_s, kWhereAttention);
+        arrive(&both[1]);
+        ok = wait_soon(&both[1], both_phase, abort_flag, &error_s);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         both_phase ^= 1u;
