@@ -101,12 +101,14 @@ MLDEV int keys_of_token(const AttentionParams& p, int token) {
   return max(r.kv - r.n + (token - r.q0) + 1, 0);
 }
 
-// mbar_wait for the waits that a step's time is made of: the timer is read only after some tries, each of which
-// suspends the thread for a while (read before the second try it cost every blocked wait 0.3 us).
+// mbar_wait for the waits that a step's time is made of: the timer is read only after some tries.  Raises the abort
+// flag when it runs out, after which every wait of the block ends at once.
 MLDEV bool wait_soon(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* status) {
 #pragma unroll 1
-  for (int i = 0; i < 256; ++i)
+  for (int i = 0; i < 256; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 15) == 15 && *abort_flag) return false;
+  }
   return mbar_wait(bar, parity, abort_flag, status, kWhereAttention);
 }
 

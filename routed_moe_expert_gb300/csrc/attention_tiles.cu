@@ -8,17 +8,18 @@
 // A block takes two tiles of 128 rows, so that the tensor cores multiply for one while the threads of the
 // other take exponentials, and a key is fetched once for both.  TMEM: S of both tiles (2 x 128 columns), O of both
 // (2 x head size).  MMAs run in the order of issue, O_0 += P_0 V, S_0 of the next keys, then the same for
-// tile 1, so S may overwrite the P that was just multiplied.
+// tile 1, so S may overwrite the P that was just multiplied, and the tiles' weights are due in turn.
 //
-// The row's reference is its maximum when that was last taken over; a new maximum is taken over, and O
-// multiplied, only when it is more than 2^8 times the weights' scale away: in float32 and bf16 weights
-// up to 256 are as exact as weights up to 1, and O, which lives in TMEM, hardly ever has to be touched.
+// The row's reference is the maximum of its first 128 scores, and stays: what a later score is above it makes
+// weights above 1, which bf16 and float32 hold as exactly.  Only when a unit's weights come to more than 2^40
+// are its maximum taken and O, which lives in TMEM, multiplied.  So no maximum stands between a score and
+// its weight, and O is hardly ever touched.
 //
 // Up to 128 rows take both tiles too: they hold the same rows and take the units of keys in turn, and their
 // two results are added at the end (each thread finds its row's other half in its own TMEM lanes).
 //
-// Warps 0-3 and 4-7: the rows of tiles 0 and 1, a thread a row; warp 8: TMA; warp 9: MMA issue; warp 10: zeroes
-// values behind the last key that is seen (0 times an infinity would stay).  Items come from the schedule in
+// Warps 0-3 and 4-7: the rows of tiles 0 and 1, a thread a row; warp 8: TMA; warp 9: MMA issue, and zeroes for
+// values behind the last key that is seen; warp 11: the block's parts of items.  Items come from the schedule in
 // attention.h; with `prefix` the block's item is a part of the shared keys for 256 rows of the whole batch.
 #include "attention.h"
 #include "host.h"
@@ -28,14 +29,14 @@ namespace {
 
 constexpr int kRows = kTileRows, kKeys = kTileKeys;
 constexpr int kThreads = 384;
-constexpr int kProducer = 8, kMma = 9, kCleaner = 10, kScheduler = 11;
+constexpr int kProducer = 8, kMma = 9, kScheduler = 11;
 using Sched = Schedule<kRows, kKeys, kTileOver>;
 using Place = Walk<kRows, kKeys, kTileOver>;
 
 constexpr int kHalf = kKeys * 128;   // 64 values of 128 rows
 __host__ __device__ constexpr int tile_bytes(int dp) { return dp / 64 * kHalf; }
-__host__ __device__ constexpr int slots_of(int dp) { return dp == 64 ? 8 : 4; }
-constexpr int smem_bytes(int dp) { return (2 + slots_of(dp)) * tile_bytes(dp) + 8 * 2048; }
+__host__ __device__ constexpr int slots_of(int dp) { return dp == 64 ? 10 : 5; }
+constexpr int smem_bytes(int dp) { return (2 + slots_of(dp)) * tile_bytes(dp); }
 
 // D[tmem] (+)= A * B[smem], issued by the lane whose `leader` is not 0; A in shared memory (umma_ss) or in TMEM
 // (umma_ts: K-major, a lane a row, two bf16 a column).  Descriptors by halves: the upper is a constant.
@@ -90,6 +91,22 @@ MLDEV float2 add2(float2 a, float2 b) {
   return r;
 }
 
+// Transposes the 4 x 4 pieces of four neighbouring lanes: piece i of lane q becomes piece q of lane i.
+MLDEV void trade(uint4 (&x)[4], int lane) {
+  auto swap = [&](uint4& a, uint4& b, int mask, bool upper) {   // lanes apart by `mask`: a of the upper for b of the lower
+    uint4 give = upper ? a : b;
+    give.x = __shfl_xor_sync(0xffffffffu, give.x, mask);
+    give.y = __shfl_xor_sync(0xffffffffu, give.y, mask);
+    give.z = __shfl_xor_sync(0xffffffffu, give.z, mask);
+    give.w = __shfl_xor_sync(0xffffffffu, give.w, mask);
+    (upper ? a : b) = give;
+  };
+  swap(x[0], x[1], 1, lane & 1);
+  swap(x[2], x[3], 1, lane & 1);
+  swap(x[0], x[2], 2, lane & 2);
+  swap(x[1], x[3], 2, lane & 2);
+}
+
 // A part of an item as every role sees it, made by the scheduling warp.
 struct Step {
   int end;             // no more parts
@@ -105,9 +122,9 @@ struct Step {
   MLDEV int hi(int k) const { return k == 0 ? hi0 : hi1; }
   MLDEV int rows(int k) const { return k == 0 ? rows0 : rows1; }
   MLDEV int first(int k) const { return lo + (lead == 2 ? k : 0); }
-  MLDEV bool has(int k, int j) const { return j < hi(k) && (lead == 1 || ((j - lo) & 1) == k); }
 };
 constexpr int kSteps = 4;
+constexpr float kMostWeight = 1.099511627776e12f;   // 2^40: sums of a row's weights stay far below float32's end
 
 template <int DP>
 __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __grid_constant__ AttentionParams p,
@@ -115,8 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
   constexpr int kSlots = slots_of(DP), TILE = tile_bytes(DP), HALVES = DP / 64;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* ring = smem + 2 * TILE;
-  uint8_t* stages = ring + kSlots * TILE;   // 2 KB a row warp
-  __shared__ uint64_t full[kSlots], empty[kSlots], s_full[2], p_ready[2][2], o_full[2], q_full[2], v_asked, v_clean, both[2], drain;
+  __shared__ uint64_t full[kSlots], empty[kSlots], s_full[2], p_ready[2], o_full[2], q_full[2], both[2], drain;
   __shared__ uint64_t step_full[kSteps], step_empty[kSteps];
   __shared__ Step steps[kSteps];
   __shared__ ScheduleSmem sched_s;
@@ -134,18 +150,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&s_full[t], 1);
-      mbar_init(&p_ready[t][0], 4);   // a lane a warp; the weights of the first 64 keys, and of the others
-      mbar_init(&p_ready[t][1], 4);
+      mbar_init(&p_ready[t], 4);   // a lane a warp
       mbar_init(&o_full[t], 1);
       mbar_init(&q_full[t], 4);
       mbar_init(&both[t], 8);
     }
     for (int i = 0; i < kSteps; ++i) {
       mbar_init(&step_full[i], 1);
-      mbar_init(&step_empty[i], kScheduler);   // every other warp
+      mbar_init(&step_empty[i], 10);   // the other warps that work
     }
-    mbar_init(&v_asked, 1);
-    mbar_init(&v_clean, 1);
     mbar_init(&drain, 1);
     error_s = 0;
     abort_s = 0;
@@ -347,142 +360,103 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
           if ((issued >> i) & 1u) mbar_wait_drain(&full[i], (parity >> i) & 1u);
       __syncwarp();
     } else if (warp == kMma) {   // ------------------------------------------ MMA issue
-      // The whole warp walks along, so that descriptors stay in uniform registers; one lane issues.
+      // The whole warp walks along, so that descriptors stay in uniform registers; one lane issues.  The pipe holds
+      // only a few MMAs ahead, so whatever has to be waited for is waited for behind MMAs just issued.
       const uint32_t s_idesc = idesc_bf16_f32(128, kKeys), o_idesc = idesc_bf16_f32(128, DP) | kMnMajorB;
-      const uint32_t q_at = smem_u32(smem), ring_at = smem_u32(ring);
+      const uint32_t q_lo = desc_lo(smem_u32(smem)) | (1u << 16), ring_lo = desc_lo(smem_u32(ring));
       const uint32_t leader = lane == 0;
       int slot = 0;
-      uint32_t phase = 0, q_phase = 0, p_phase = 0, clean_phase = 0;
+      uint32_t phase = 0, q_phase = 0, p_phase = 0;
+      // No vote on a wait's outcome, which would be part of every unit's time: after one that ran out the others
+      // end at once, so the part's remaining steps are gone through on whatever is there.
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        ok = __all_sync(0xffffffffu, wait_soon(bar, parity, abort_flag, &error_s));
-        return ok != 0;
+        wait_soon(bar, parity, abort_flag, &error_s);
+        __syncwarp();
       };
-      auto advance = [&]() {
+      auto take_slot = [&]() {   // the next slot, filled
+        const int at = slot;
+        wait(&full[slot], phase);
         if (++slot == kSlots) {
           slot = 0;
           phase ^= 1u;
         }
+        return at;
       };
-      auto commit = [&](uint64_t* bar) {
-        if (leader) umma_commit(bar);
-        __syncwarp();
-      };
-      auto scores = [&](int k, uint32_t at) {   // S of tile k with the keys at `at`
-        const uint32_t a = desc_lo(q_at + k * TILE) | (1u << 16), b = desc_lo(at) | (1u << 16);
+      auto scores = [&](int k, int at) {   // S of tile k with the keys in slot `at`
+        const uint32_t a = q_lo + k * (TILE >> 4), b = (ring_lo + at * (TILE >> 4)) | (1u << 16);
 #pragma unroll
         for (int ks = 0; ks < DP / 16; ++ks) {
           const uint32_t step = (ks >> 2) * (kHalf >> 4) + 2 * (ks & 3);
           umma_ss(tmem + k * 128, a + step, b + step, kKMajorHi, s_idesc, ks > 0, leader);
         }
-        commit(&s_full[k]);
+        if (leader) umma_commit(&s_full[k]);
       };
       while (step_here()) {
         const Step& in = steps[at_step];
         auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
-        Step t;
-        t.end = uniform(in.end);
-        t.lo = uniform(in.lo);
-        t.most = uniform(in.most);
-        t.hi0 = uniform(in.hi0);
-        t.hi1 = uniform(in.hi1);
-        t.lead = uniform(in.lead);
-        t.sees = uniform(in.sees);
+        const int end = uniform(in.end), lo = uniform(in.lo), n = uniform(in.most) - lo, lead = uniform(in.lead);
+        const int units0 = uniform(in.hi0) - lo, units1 = uniform(in.hi1) - lo, sees = uniform(in.sees);
         step_read();
-        if (t.end) break;
-        for (int i = 0; ok && i < t.lead && t.lo + i < t.most; ++i) {   // the first scores
-          if (!wait(&full[slot], phase)) break;
+        if (end) break;
+        if (n == 0) continue;
+        const bool tail = key0 + (lo + n) * kKeys > sees;   // the part's last unit has values behind the last key
+        auto has = [&](int k, int u) { return u < (k == 0 ? units0 : units1) && (lead == 1 || (u & 1) == k); };
+        for (int u = 0; u < lead && u < n; ++u) {   // the first keys
+          const int at = take_slot();
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            if (!ok || !t.has(k, t.lo + i)) continue;
-            if (!wait(&q_full[k], (q_phase >> k) & 1u)) continue;
+            if (!has(k, u)) continue;
+            wait(&q_full[k], (q_phase >> k) & 1u);
             q_phase ^= 1u << k;
             tc_fence_after();
-            scores(k, ring_at + slot * TILE);
+            scores(k, at);
           }
-          if (!ok) break;
-          commit(&empty[slot]);
-          advance();
+          if (leader) umma_commit(&empty[at]);
+          __syncwarp();
         }
-        for (int j = t.lo; ok && j < t.most; ++j) {
-          const int v_slot = slot, ahead = j + t.lead;
-          if (!wait(&full[slot], phase)) break;
-          advance();
-          if (key0 + (j + 1) * kKeys > t.sees) {   // values behind the last key
-            if (leader) mbar_arrive(&v_asked);
+        int v_slot = take_slot(), k_slot = lead < n ? take_slot() : -1;
+        for (int u = 0; u < n; ++u) {   // a unit's values, and the keys `lead` units on
+          if (tail && u == n - 1) {   // zeroed, since 0 times an infinity would stay
+            const int from = sees - (key0 + (lo + u) * kKeys);   // 1..127
+            for (int c = lane; c < (kKeys - from) * 8; c += 32)
+#pragma unroll
+              for (int half = 0; half < HALVES; ++half)
+                *reinterpret_cast<uint4*>(ring + v_slot * TILE + half * kHalf + from * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
             __syncwarp();
-            if (!wait(&v_clean, clean_phase)) break;
-            clean_phase ^= 1u;
           }
-          const int k_slot = slot;
-          bool have_keys = false;
+          const uint32_t b = (ring_lo + v_slot * (TILE >> 4)) | (static_cast<uint32_t>(kHalf >> 4) << 16);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            if (!ok) continue;
-            if (t.has(k, j)) {
-              const uint32_t b = desc_lo(ring_at + v_slot * TILE) | (static_cast<uint32_t>(kHalf >> 4) << 16);
+            if (!has(k, u)) continue;
+            wait(&p_ready[k], (p_phase >> k) & 1u);
+            p_phase ^= 1u << k;
+            tc_fence_after();
 #pragma unroll
-              for (int ks = 0; ks < kKeys / 16; ++ks) {
-                if (ks % 4 == 0) {
-                  if (!wait(&p_ready[k][ks / 4], (p_phase >> k) & 1u)) break;
-                  tc_fence_after();
-                }
-                umma_ts(tmem + 256 + k * DP, tmem + k * 128 + ks * 8, b + ks * (2048 >> 4), kMnMajorHi, o_idesc,
-                        j >= t.lo + t.lead || ks > 0, leader);
-              }
-              if (!ok) continue;
-              p_phase ^= 1u << k;
-              if (ahead >= t.hi(k)) commit(&o_full[k]);
-            }
-            if (t.has(k, ahead)) {
-              if (!have_keys && !wait(&full[slot], phase)) continue;
-              have_keys = true;
-              scores(k, ring_at + k_slot * TILE);
-            }
+            for (int ks = 0; ks < kKeys / 16; ++ks)
+              umma_ts(tmem + 256 + k * DP, tmem + k * 128 + ks * 8, b + ks * (2048 >> 4), kMnMajorHi, o_idesc,
+                      u >= lead || ks > 0, leader);
+            if (u + lead >= (k == 0 ? units0 : units1) && leader) umma_commit(&o_full[k]);
+            if (has(k, u + lead)) scores(k, k_slot);
           }
-          if (!ok) break;
-          commit(&empty[v_slot]);
-          if (ahead < t.most) {
-            commit(&empty[k_slot]);
-            advance();
+          if (leader) {
+            umma_commit(&empty[v_slot]);
+            if (k_slot >= 0) umma_commit(&empty[k_slot]);
+          }
+          __syncwarp();
+          if (u + 1 < n) {
+            v_slot = take_slot();
+            k_slot = u + 1 + lead < n ? take_slot() : -1;
           }
         }
-        if (!ok) break;
+        if (*abort_flag != 0) break;
       }
+      ok = *abort_flag == 0;
       if (!ok && leader) {   // let what was issued finish before TMEM is released
         umma_commit(&drain);
         mbar_wait_drain(&drain, 0);
       }
       __syncwarp();
-    } else if (warp == kCleaner) {   // -------------------------------------- values behind the last key
-      // Asked for by the MMA warp once they have landed: by itself this warp would run ahead of the ring by
-      // more than a lap, where a parity says nothing.
-      unsigned long long used = 0;   // ring slots of the steps before
-      uint32_t asked_phase = 0;
-      while (step_here()) {
-        const Step t = steps[at_step];
-        step_read();
-        if (t.end) break;
-        const int n = t.most - t.lo;
-        if (n > 0 && key0 + t.most * kKeys > t.sees) {   // the part's last unit
-          const unsigned long long at = used + 2ull * n - 1;   // the part's last slot: its last unit's values
-          const int slot = static_cast<int>(at % kSlots);
-          ok = wait_soon(&v_asked, asked_phase, abort_flag, &error_s) &&
-               wait_soon(&full[slot], static_cast<uint32_t>(at / kSlots) & 1u, abort_flag, &error_s);
-          asked_phase ^= 1u;
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          const int k0 = key0 + (t.most - 1) * kKeys;
-          const int from = t.sees - k0;   // 1..127
-          for (int c = lane; c < (kKeys - from) * 8; c += 32)
-#pragma unroll
-            for (int half = 0; half < HALVES; ++half)
-              *reinterpret_cast<uint4*>(ring + slot * TILE + half * kHalf + from * 128 + c * 16) = make_uint4(0, 0, 0, 0);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&v_clean);
-        }
-        used += 2ull * n;
-      }
     }
   } else {   // ---------------------------------------------------------------- rows
     asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
@@ -490,7 +464,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
     const int wr = (warp & 3) * 32;                   // the warp's first row
     const uint32_t lanes = tmem + (static_cast<uint32_t>(wr) << 16);
     const uint32_t s_at = lanes + k * 128, o_at = lanes + 256 + k * DP;
-    uint8_t* stage = stages + warp * 2048;
     uint32_t s_phase = 0, o_phase = 0, both_phase = 0;
     const bool negative = p.scale_log2 < 0.0f;
     const float scale = fabsf(p.scale_log2);
@@ -551,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
       }
       step_read();
       asked = false;
-      // The next part's query rows, as soon as the tile's last scores are there: they are what still reads these.
+      // The next part's query rows, once the tile's last scores are there: they are what still reads these.
       auto fetch_next = [&]() {
         if (!step_here()) return;
         const Step& t = steps[at_step];
@@ -559,95 +532,119 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
         fetch_queries(t);
         asked = true;
       };
-      float ref = -INFINITY, l = 0.0f;
-      const bool idle = wr >= rows;   // no row of this warp is one: its weights may be anything
-      for (int j = first_unit; j < hi; j += lead) {
-        ok = wait_soon(&s_full[k], s_phase, abort_flag, &error_s);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        s_phase ^= 1u;
-        tc_fence_after();
-        if (j + lead >= hi) fetch_next();
-        if (!ok) break;
-        if (idle) {
-          arrive(&p_ready[k][0]);
-          arrive(&p_ready[k][1]);
-          continue;
+      // (As in the MMA warp, a wait that ran out is looked at behind the units.)
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        wait_soon(bar, parity, abort_flag, &error_s);
+        __syncwarp();
+      };
+      float ref = r < rows ? -INFINITY : 0.0f, l = 0.0f;
+      if (wr >= rows) {   // no row of this warp is one: its weights may be anything
+        for (int j = first_unit; j < hi; j += lead) {
+          wait(&s_full[k], s_phase);
+          s_phase ^= 1u;
+          arrive(&p_ready[k]);
         }
-        uint32_t v[4][32];
+      } else {
+        // Units in front of `whole` are seen in full by all rows of the warp.
+        const int whole = static_cast<int>(__reduce_min_sync(0xffffffffu, static_cast<unsigned>(max(sees - key0, 0)))) / kKeys;
+        const float2 scales = make_float2(scale, scale);
+        for (int j = first_unit; j < hi; j += lead) {
+          wait(&s_full[k], s_phase);
+          s_phase ^= 1u;
+          tc_fence_after();
+          const int limit = sees - (key0 + j * kKeys);   // columns below it are seen
+          float sum;
+          for (int tries = 0;; ++tries) {
+            uint32_t v[4][32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld_x32(s_at + c * 32, v[c]);
-        tmem_ld_wait();
-        if (negative) {
+            for (int c = 0; c < 4; ++c) tmem_ld_x32(s_at + c * 32, v[c]);
+            tmem_ld_wait();
+            if (negative) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+              for (int c = 0; c < 4; ++c)
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[c][i] ^= 0x80000000u;
-        }
-        const int limit = sees - (key0 + j * kKeys);   // columns below it are seen
-        if (__any_sync(0xffffffffu, limit < kKeys)) {
+                for (int i = 0; i < 32; ++i) v[c][i] ^= 0x80000000u;
+            }
+            if (j >= whole) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+              for (int c = 0; c < 4; ++c)
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[c][i] = c * 32 + i < limit ? v[c][i] : 0xff800000u;
-        }
-        float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                for (int i = 0; i < 32; ++i) v[c][i] = c * 32 + i < limit ? v[c][i] : 0xff800000u;
+            }
+            if (tries == 0 && j == first_unit) {   // the row's reference
+              float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < 32; i += 2)
+              for (int i = 0; i < 32; i += 2)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tops[c] = max3(tops[c], __uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1]));
-        const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * scale;   // (scale is not 0)
-        const bool grow = top > ref + 8.0f;
-        if (__any_sync(0xffffffffu, grow)) {
-          const float f = grow ? exp2_approx(ref - top) : 1.0f;
-          if (grow) ref = top;
-          l *= f;
-          if (j >= lo + lead) {
+                for (int c = 0; c < 4; ++c) tops[c] = max3(tops[c], __uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1]));
+              const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * scale;   // (scale is not 0)
+              if (r < rows) ref = top;
+            }
+            const float2 off = make_float2(-reference_of(ref), -reference_of(ref));
+            float2 sums[2] = {};
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                float2 x = fma2(make_float2(__uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1])), scales, off);
+                x.x = exp2_approx(x.x);
+                x.y = exp2_approx(x.y);
+                sums[(i >> 1) & 1] = add2(sums[(i >> 1) & 1], x);
+                const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
+                v[c >> 1][(c & 1) * 16 + i / 2] = *reinterpret_cast<const uint32_t*>(&h);   // (read already)
+              }
+            sum = (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y);
+            const bool renew = tries == 0 && (ref == -INFINITY || !(sum <= kMostWeight));
+            if (!__any_sync(0xffffffffu, renew)) {
+              tmem_st_x32(s_at, v[0]);   // over the scores
+              tmem_st_x32(s_at + 32, v[1]);
+              break;
+            }
+            // ---- rarely: the unit's maximum becomes the reference, and the unit is done again from TMEM
+            float top = -INFINITY;
 #pragma unroll 1
-            for (int c = 0; c < DP; c += 16) {
-              uint32_t o[16];
-              tmem_ld_x16(o_at + c, o);
+            for (int c = 0; c < kKeys; c += 16) {
+              uint32_t x[16];
+              tmem_ld_x16(s_at + c, x);
               tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-              tmem_st_x16(o_at + c, o);
+              for (int i = 0; i < 16; ++i) {
+                const float f = negative ? -__uint_as_float(x[i]) : __uint_as_float(x[i]);
+                if (c + i < limit) top = fmaxf(top, f);
+              }
             }
-            tmem_st_wait();
-          }
-        }
-        const float2 scales = make_float2(scale, scale), off = make_float2(-reference_of(ref), -reference_of(ref));
-        float2 sums[2] = {};
+            top *= scale;
+            const bool grow = renew && top > ref;
+            const float f = grow ? exp2_approx(ref - top) : 1.0f;
+            if (grow) ref = top;
+            l *= f;
+            if (j >= lo + lead) {
+#pragma unroll 1
+              for (int c = 0; c < DP; c += 16) {
+                uint32_t o[16];
+                tmem_ld_x16(o_at + c, o);
+                tmem_ld_wait();
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            float2 x = fma2(make_float2(__uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1])), scales, off);
-            x.x = exp2_approx(x.x);
-            x.y = exp2_approx(x.y);
-            sums[(i >> 1) & 1] = add2(sums[(i >> 1) & 1], x);
-            const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
-            v[c >> 1][(c & 1) * 16 + i / 2] = *reinterpret_cast<const uint32_t*>(&h);   // (read already)
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tmem_st_x16(o_at + c, o);
+              }
+            }
           }
-          if (c & 1) {   // over the scores, which are all read
-            tmem_st_x32(s_at + (c >> 1) * 32, v[c >> 1]);
-            tmem_st_wait();
-            tc_fence_before();
-            arrive(&p_ready[k][c >> 1]);   // the product starts on the first half
-          }
+          l += sum;
+          tmem_st_wait();
+          tc_fence_before();
+          arrive(&p_ready[k]);
         }
-        l += (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y);
       }
-      if (!ok) break;
-      if (first_unit >= hi) fetch_next();
+      fetch_next();
       if (!ok) break;
       if (asked) queries_there();
       if (first_unit < hi) {
-        ok = wait_soon(&o_full[k], o_phase, abort_flag, &error_s);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
+        wait(&o_full[k], o_phase);
         o_phase ^= 1u;
         tc_fence_after();
       }
+      if (*abort_flag != 0) break;
       // ---- with the same rows in both tiles: the other tile's maximum and sum, and half of the columns each
       const bool pair = lead == 2;
       float other = 0.0f, mine = 1.0f;   // factors of the other tile's result and this one's
@@ -678,8 +675,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
       const long long at = prefix.splits > 0 ? (static_cast<long long>(slot) * p.T + token) * p.Hq + head
                            : all             ? part_row(p, token, head)
                                              : static_cast<long long>(slot) * p.item_rows + tile_row;
-      // Results leave through shared memory, 64 bytes of a row at a time, so that a warp writes whole pieces of
-      // its rows: a thread a row would touch 32 rows a store.
+      // Results leave 64 bytes of a row at a time, four lanes having traded their rows' quarters, so that a warp
+      // writes whole pieces: a thread a row would touch 32 rows a store.
       const bool by_row = final && !p.out_vec;   // unless `out` is not aligned to that
       float* piece_o = by_token ? p.part_o : p.piece_o;
       unsigned long long to = 0;
@@ -688,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
                    : reinterpret_cast<unsigned long long>(piece_o + at * DP);
       unsigned long long dst[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) dst[i] = __shfl_sync(0xffffffffu, to, i * 8 + (lane >> 2));
+      for (int i = 0; i < 4; ++i) dst[i] = __shfl_sync(0xffffffffu, to, (lane & ~3) + i);
       if (final && !by_row) {
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         mine *= inv;
@@ -729,18 +726,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
             continue;
           }
           const int part = lane & 3;
-          auto leave = [&](const uint4 (&x)[4], int bytes, bool inside) {   // 64 bytes of every row
-            __syncwarp();
+          auto leave = [&](uint4 (&x)[4], int bytes, bool inside) {   // 64 bytes of every row
+            trade(x, lane);   // now x[i] is quarter `part` of the row of lane (lane & ~3) + i
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              *reinterpret_cast<uint4*>(stage + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) = x[i];
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int of = i * 8 + (lane >> 2);
-              const uint4 y = *reinterpret_cast<const uint4*>(stage + of * 64 + ((part ^ ((of >> 1) & 3)) << 4));
-              if (dst[i] != 0 && inside) *reinterpret_cast<uint4*>(dst[i] + bytes + 16 * part) = y;
-            }
+              if (dst[i] != 0 && inside) *reinterpret_cast<uint4*>(dst[i] + bytes + 16 * part) = x[i];
           };
           uint4 x[4];
           if (final) {
