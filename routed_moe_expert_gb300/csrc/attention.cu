@@ -435,7 +435,8 @@ extern "C" moe_lora_status moe_lora_attention(moe_lora_handle* h, const moe_lora
     join_across = std::min(4, p.item_rows);
   }
   if (!p.plan.whole) p.records = reinterpret_cast<PieceRecord*>(base + at.records);
-  ML_LAUNCH(h, tiles ? launch_attention_tiles(p, PrefixRun{}, p.plan.ctas, dp, stream) : launch_attention_rows(p, dp, stream),
+  ML_LAUNCH(h, tiles ? launch_attention_tiles(p, PrefixRun{}, p.plan.ctas, dp, stream)
+                     : launch_attention_rows(p, dp, static_cast<long long>(a->max_query_len) * p.G <= 8, stream),
             "attention launch");
   if (!p.plan.whole) ML_LAUNCH(h, launch_join(p, dp, join_across, stream), "attention join launch");
   if (p.prefix_splits > 0) ML_LAUNCH(h, launch_fold(p, dp, stream), "attention fold launch");

@@ -144,9 +144,17 @@ struct Schedule {
     return (r.n * p.G + ROWS - 1) / ROWS;
   }
 
-  // The block whose run has u.
-  MLDEV int block_of(long long u) const { return static_cast<int>(((u + 1) * ctas - 1) / units); }
-  MLDEV long long start_of(int c) const { return units * c / ctas; }
+  // The block whose run has u, and where a block's run starts (in 32 bits where that is enough: a division of
+  // 64 bits is some hundred cycles).
+  MLDEV int block_of(long long u) const {
+    return small() ? static_cast<int>(((static_cast<uint32_t>(u) + 1u) * static_cast<uint32_t>(ctas) - 1u) / static_cast<uint32_t>(units))
+                   : static_cast<int>(((u + 1) * ctas - 1) / units);
+  }
+  MLDEV long long start_of(int c) const {
+    return small() ? static_cast<long long>(static_cast<uint32_t>(units) * static_cast<uint32_t>(c) / static_cast<uint32_t>(ctas))
+                   : units * c / ctas;
+  }
+  MLDEV bool small() const { return units < (1ll << 31) / 512; }   // (blocks are at most 320)
 };
 
 // A place in the schedule, advanced item by item; every role of a block walks through the same ones.
@@ -253,7 +261,8 @@ MLDEV void make_schedule(const AttentionParams& p, int cta, Schedule<ROWS, KEYS,
     n += sm.items[i];
   }
   s.units = t;
-  const long long want = max(t / p.plan.least, min(n, static_cast<long long>(p.plan.ctas)));
+  const long long want = max(static_cast<long long>(t < (1ll << 31) ? static_cast<uint32_t>(t) / static_cast<uint32_t>(p.plan.least) : p.plan.ctas),
+                             min(n, static_cast<long long>(p.plan.ctas)));
   s.ctas = static_cast<int>(max(1ll, min(want, static_cast<long long>(p.plan.ctas))));
   s.start = s.start_of(min(cta, s.ctas));
   s.end = cta < s.ctas ? s.start_of(cta + 1) : s.start;
@@ -296,7 +305,7 @@ MLDEV void make_schedule(const AttentionParams& p, int cta, Schedule<ROWS, KEYS,
   w.u0 = sm.found_base;
   if (w.items == 1) {
     w.units = S::weight_of(p, w.r, 0);
-    w.kh = static_cast<int>((s.start - w.u0) / w.units);
+    w.kh = static_cast<int>(static_cast<uint32_t>(s.start - w.u0) / static_cast<uint32_t>(w.units));   // (below Hk * units)
     w.u0 += static_cast<long long>(w.kh) * w.units;
     w.i = 0;
     return;
@@ -432,7 +441,7 @@ struct PrefixRun {
 constexpr int kFewRows = 16, kFewKeys = 64, kFewPerSm = 2, kFewOver = 1;
 constexpr int kTileRows = 256, kTileKeys = 128, kTileOver = 2;
 cudaError_t prepare_attention_rows();
-cudaError_t launch_attention_rows(const AttentionParams& p, int dp, cudaStream_t stream);
+cudaError_t launch_attention_rows(const AttentionParams& p, int dp, bool eight, cudaStream_t stream);   // items of 8 rows, or 16
 cudaError_t prepare_attention_tiles();
 cudaError_t launch_attention_tiles(const AttentionParams& p, const PrefixRun& prefix, int blocks, int dp, cudaStream_t stream);
 

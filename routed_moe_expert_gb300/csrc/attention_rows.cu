@@ -3,9 +3,15 @@
 //
 // What bounds it is memory: 8 query heads on a key head of 128 do 16 operations a byte of the cache.  So the
 // cache is streamed by TMA (a box a page, 128-byte swizzle) through a ring of 32 KB stages, 64 keys and their
-// values each, two blocks an SM; the products are small enough for mma.sync, whose fragments keep a
-// warp's 16 keys x 16 rows in registers from the scores to the weights, and whose idle tile rows cost
-// nothing that is scarce here.  Each warp has a quarter of every stage and a softmax of its own; the four are
+// values each, two blocks an SM.  The products run on mma.sync with the keys, then the values' dimensions, as its 16
+// rows and up to 8 query rows as its 8 columns, so that nothing is padded:
+//
+//   S^T [16 keys, 8 rows] = K Q^T,   O^T [16 dimensions, 8 rows] += V^T P^T
+//
+// (with query rows on the 16-row side there were twice as many MMAs, 48 for a warp's 16 keys, and these, at
+// about 32 cycles each, and not the memory were what decoding waited for).  P^T goes from the first product's layout to
+// the second's by transposing 8 x 8 matrices between lanes.  Each warp has a quarter of every stage and a softmax of
+// its own, relative to the maxima of its first 16 keys (attention_tiles.cu says why that is enough); the four are
 // added at the end of the item's part.  Weights go into the second product as two bf16 pieces.
 #include "attention.h"
 #include "host.h"
@@ -13,15 +19,14 @@
 namespace mlk {
 namespace {
 
-constexpr int kRows = kFewRows, kKeys = kFewKeys;
+constexpr int kKeys = kFewKeys;
 constexpr int kConsumers = 4, kThreads = 32 * (kConsumers + 1);
-using Sched = Schedule<kRows, kKeys, kFewOver>;
-using Place = Walk<kRows, kKeys, kFewOver>;
 
 __host__ __device__ constexpr int stage_bytes(int dp) { return 2 * kKeys * dp * 2; }   // keys, then values
 __host__ __device__ constexpr int stages_of(int dp) { return dp == 64 ? 6 : 3; }
-// the ring, the block's sum of its warps' results, and the rest
-constexpr int smem_bytes(int dp) { return stages_of(dp) * stage_bytes(dp) + kRows * dp * 4 + 1024; }
+// the ring, and 8 rows of three warps' results
+constexpr int smem_bytes(int dp) { return stages_of(dp) * stage_bytes(dp) + 3 * 8 * dp * 4; }
+constexpr float kMostWeight = 1.099511627776e12f;   // 2^40: a unit's weights above it make a new reference
 
 MLDEV void ldsm4(uint32_t at, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -41,18 +46,27 @@ MLDEV void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+MLDEV uint32_t transposed(uint32_t x) {   // an 8 x 8 matrix of 16-bit values, two a lane
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
 MLDEV uint32_t pack2(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 MLDEV void consumer_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
 
-template <int DP>
+// NT: groups of 8 query rows of an item.
+template <int DP, int NT>
 __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(const __grid_constant__ AttentionParams p) {
+  constexpr int kRows = 8 * NT;
+  using Sched = Schedule<kRows, kKeys, kFewOver>;
+  using Place = Walk<kRows, kKeys, kFewOver>;
   constexpr int kStages = stages_of(DP), STAGE = stage_bytes(DP), HALVES = DP / 64;
   constexpr int kHalf = kKeys * 128;   // 64 values of every key of a stage
   extern __shared__ __align__(1024) uint8_t smem[];
-  float* sum_s = reinterpret_cast<float*>(smem + kStages * STAGE);   // [kRows][DP]
+  float* sum_s = reinterpret_cast<float*>(smem + kStages * STAGE);   // [3][8][DP]
   __shared__ uint64_t full[kStages], empty[kStages];
   __shared__ float m_s[kConsumers][kRows], l_s[kConsumers][kRows];
   __shared__ ScheduleSmem sched_s;
@@ -139,7 +153,8 @@ __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(con
         if ((issued >> t) & 1u) mbar_wait_drain(&full[t], (parity >> t) & 1u);
     __syncwarp();
   } else {   // ------------------------------------------------------------------ consumers
-    const int ra = lane >> 2, rb = ra + 8, pair = (lane & 3) * 2;
+    const int quad = lane >> 2, pair = (lane & 3) * 2;   // a fragment's row and first of two columns
+    const int t8 = lane & 7;
     int stage = 0, ok = 1;
     uint32_t phase = 0;
     bool started = false;   // an item whose rest is other blocks'
@@ -149,38 +164,39 @@ __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(con
       const int row0 = w.i * kRows;
       const int rows = min(kRows, w.r.n * p.G - row0);
       const int sees = Sched::seen_by(p, w.r, w.i);
-      const bool upper = rows > 8;   // the fragments' rows 8 to 15 are in use
-      int lim_a = 0, lim_b = 0;      // keys that this lane's two rows see
-      uint32_t qf[DP / 16][4];
-      {
-        const __nv_bfloat16 *qa = nullptr, *qb = nullptr;
-        if (ra < rows) {
-          const int t = (row0 + ra) / p.G;
-          qa = p.q + (w.r.q0 + t) * p.q_t + (w.kh * p.G + (row0 + ra) % p.G) * p.q_h;
-          lim_a = max(w.r.kv - w.r.n + t + 1, 0);
-        }
-        if (rb < rows) {
-          const int t = (row0 + rb) / p.G;
-          qb = p.q + (w.r.q0 + t) * p.q_t + (w.kh * p.G + (row0 + rb) % p.G) * p.q_h;
-          lim_b = max(w.r.kv - w.r.n + t + 1, 0);
-        }
+      uint32_t qf[NT][DP / 16][2];   // Q^T: dimensions pair, pair + 1 (and 8 on) of row quad
+      int limit[NT][2];              // keys that rows pair and pair + 1 see
 #pragma unroll
-        for (int ks = 0; ks < DP / 16; ++ks) {
-          const int c = ks * 16 + pair;
-          auto at = [&](const __nv_bfloat16* q, int d) {
-            return q != nullptr && d < p.D ? *reinterpret_cast<const uint32_t*>(q + d) : 0u;
-          };
-          qf[ks][0] = at(qa, c);
-          qf[ks][1] = at(qb, c);
-          qf[ks][2] = at(qa, c + 8);
-          qf[ks][3] = at(qb, c + 8);
+      for (int t = 0; t < NT; ++t) {
+        const int row = t * 8 + quad;
+        const int token = (row0 + row) / p.G;
+        const __nv_bfloat16* q =
+            row < rows ? p.q + (w.r.q0 + token) * p.q_t + (w.kh * p.G + (row0 + row) - token * p.G) * p.q_h : nullptr;
+#pragma unroll
+        for (int ks = 0; ks < DP / 16; ++ks)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int d = ks * 16 + e * 8 + pair;
+            qf[t][ks][e] = q != nullptr && d < p.D ? *reinterpret_cast<const uint32_t*>(q + d) : 0u;
+          }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = t * 8 + pair + e;
+          limit[t][e] = r < rows ? max(w.r.kv - w.r.n + (row0 + r) / p.G + 1, 0) : 0;
         }
       }
       const int all_see = max(w.r.kv - w.r.n + row0 / p.G + 1, 0);   // keys that every row of the item sees
-      float o[DP / 8][4];
+      float o[NT][DP / 16][4];
+      float ref[NT][2], l[NT][2];
 #pragma unroll
-      for (int n = 0; n < DP / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.0f;
-      float ma = -INFINITY, mb = -INFINITY, la = 0.0f, lb = 0.0f;
+      for (int t = 0; t < NT; ++t) {
+#pragma unroll
+        for (int n = 0; n < DP / 16; ++n) o[t][n][0] = o[t][n][1] = o[t][n][2] = o[t][n][3] = 0.0f;
+        // (columns that are no row have the reference 0 and weights of 0)
+        ref[t][0] = t * 8 + pair < rows ? -INFINITY : 0.0f;
+        ref[t][1] = t * 8 + pair + 1 < rows ? -INFINITY : 0.0f;
+        l[t][0] = l[t][1] = 0.0f;
+      }
       for (int j = x.lo; j < x.hi; ++j) {
         ok = wait_soon(&full[stage], phase, abort_flag, &error_s);
         ok = __all_sync(0xffffffffu, ok);
@@ -189,10 +205,8 @@ __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(con
         if (k0 < sees) {
           const uint32_t kb = smem_u32(smem) + stage * STAGE + warp * 16 * 128;
           const uint32_t vb = kb + HALVES * kHalf;
-          const int t8 = lane & 7;
-          bool wrote = false;
-          if (k0 + 16 > sees) {   // values that no row sees may be anything, and 0 times it would stay
-            wrote = true;
+          const bool tail = k0 + 16 > sees;
+          if (tail) {   // values that no row sees may be anything, and 0 times it would stay
             for (int c = lane; c < 16 * 8 * HALVES; c += 32) {
               const int t = (c >> 3) & 15;
               if (k0 + t >= sees)
@@ -201,73 +215,73 @@ __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(con
             }
             __syncwarp();
           }
-          float sc[2][4] = {};
-          // matrices of a ldmatrix: keys 0-7 and 8-15, each with 8 dims and the next 8
-          const uint32_t krow = kb + ((lane >> 4) * 8 + t8) * 128;
+          // ---- S^T: two sums of every second step, so that an MMA waits for one before the last
+          float sc[NT][2][4] = {};
+          const uint32_t krow = kb + (((lane >> 3) & 1) * 8 + t8) * 128;   // keys 0-7, 8-15; then 8 dimensions on
 #pragma unroll
           for (int ks = 0; ks < DP / 16; ++ks) {
             uint32_t f[4];
-            ldsm4(krow + (ks >> 2) * kHalf + (((((ks & 3) << 1) + ((lane >> 3) & 1)) ^ t8) << 4), f);
-            mma16816(sc[0], qf[ks], f[0], f[1]);
-            mma16816(sc[1], qf[ks], f[2], f[3]);
+            ldsm4(krow + (ks >> 2) * kHalf + (((((ks & 3) << 1) + (lane >> 4)) ^ t8) << 4), f);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) mma16816(sc[t][ks & 1], f, qf[t][ks][0], qf[t][ks][1]);
           }
           const bool cut = k0 + 16 > all_see;
-          float xa = ma, xb = mb;
+          uint32_t hi[NT][2], lo[NT][2];
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
+          for (int t = 0; t < NT; ++t) {
+            float v[4];   // keys quad, quad + 8 (e >> 1) of rows pair, pair + 1 (e & 1)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              sc[n][e] *= p.scale_log2;
-              if (cut && k0 + n * 8 + pair + (e & 1) >= (e < 2 ? lim_a : lim_b)) sc[n][e] = -INFINITY;
+              v[e] = (sc[t][0][e] + sc[t][1][e]) * p.scale_log2;
+              if (cut && k0 + quad + (e >> 1) * 8 >= limit[t][e & 1]) v[e] = -INFINITY;
             }
-            xa = fmaxf(xa, fmaxf(sc[n][0], sc[n][1]));
-            xb = fmaxf(xb, fmaxf(sc[n][2], sc[n][3]));
-          }
-          xa = fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, 1));
-          xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, 1));
-          xa = fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, 2));
-          xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, 2));
-          const float refa = reference_of(xa), refb = reference_of(xb);
-          if (__any_sync(0xffffffffu, xa > ma || xb > mb)) {
-            const float fa = exp2_approx(ma - refa), fb = exp2_approx(mb - refb);
-            la *= fa;
-            lb *= fb;
+            float wt[4];
+            for (int tries = 0;; ++tries) {
 #pragma unroll
-            for (int n = 0; n < DP / 8; ++n) {
-              o[n][0] *= fa;
-              o[n][1] *= fa;
-              o[n][2] *= fb;
-              o[n][3] *= fb;
+              for (int e = 0; e < 4; ++e) wt[e] = exp2_approx(v[e] - reference_of(ref[t][e & 1]));
+              const bool renew = ref[t][0] == -INFINITY || ref[t][1] == -INFINITY || !(wt[0] + wt[1] + wt[2] + wt[3] <= kMostWeight);
+              if (tries > 0 || !__any_sync(0xffffffffu, renew)) break;
+              // first, and rarely later: the maxima over the warp's keys become the references
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float top = fmaxf(v[e], v[e + 2]);
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+                if (t * 8 + pair + e < rows && top > ref[t][e]) {
+                  const float f = exp2_approx(ref[t][e] - top);
+                  ref[t][e] = top;
+                  l[t][e] *= f;
+#pragma unroll
+                  for (int n = 0; n < DP / 16; ++n) {
+                    o[t][n][e] *= f;
+                    o[t][n][e + 2] *= f;
+                  }
+                }
+              }
             }
-            ma = xa;
-            mb = xb;
-          }
-          uint32_t hi[4], lo[4];   // weights as the second product's operand, in two bf16 pieces
+            l[t][0] += wt[0] + wt[2];
+            l[t][1] += wt[1] + wt[3];
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            float w0 = exp2_approx(sc[n][0] - refa), w1 = exp2_approx(sc[n][1] - refa);
-            float w2 = exp2_approx(sc[n][2] - refb), w3 = exp2_approx(sc[n][3] - refb);
-            la += w0 + w1;
-            lb += w2 + w3;
-            hi[2 * n] = pack2(w0, w1);
-            hi[2 * n + 1] = pack2(w2, w3);
-            const __nv_bfloat162 ha = *reinterpret_cast<__nv_bfloat162*>(&hi[2 * n]);
-            const __nv_bfloat162 hb = *reinterpret_cast<__nv_bfloat162*>(&hi[2 * n + 1]);
-            lo[2 * n] = pack2(w0 - __low2float(ha), w1 - __high2float(ha));
-            lo[2 * n + 1] = pack2(w2 - __low2float(hb), w3 - __high2float(hb));
+            for (int e = 0; e < 2; ++e) {   // two bf16 pieces, as the second product's operand
+              const uint32_t h = pack2(wt[2 * e], wt[2 * e + 1]);
+              const __nv_bfloat162 hb = *reinterpret_cast<const __nv_bfloat162*>(&h);
+              hi[t][e] = transposed(h);
+              lo[t][e] = transposed(pack2(wt[2 * e] - __low2float(hb), wt[2 * e + 1] - __high2float(hb)));
+            }
           }
-          // matrices: keys 0-7 and 8-15 of 8 dims, then of the next 8
-          const uint32_t vrow = vb + (((lane >> 3) & 1) * 8 + t8) * 128;
+          // ---- O^T: dimensions 0-7 and 8-15 of keys 0-7, then of keys 8-15
+          const uint32_t vrow = vb + ((lane >> 4) * 8 + t8) * 128;
 #pragma unroll
-          for (int n2 = 0; n2 < DP / 16; ++n2) {
+          for (int n = 0; n < DP / 16; ++n) {
             uint32_t f[4];
-            ldsm4_t(vrow + (n2 >> 2) * kHalf + (((((n2 & 3) << 1) + (lane >> 4)) ^ t8) << 4), f);
-            mma16816(o[2 * n2], hi, f[0], f[1]);
-            mma16816(o[2 * n2 + 1], hi, f[2], f[3]);
-            mma16816(o[2 * n2], lo, f[0], f[1]);
-            mma16816(o[2 * n2 + 1], lo, f[2], f[3]);
+            ldsm4_t(vrow + (n >> 2) * kHalf + (((((n & 3) << 1) + ((lane >> 3) & 1)) ^ t8) << 4), f);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              mma16816(o[t][n], f, hi[t][0], hi[t][1]);
+              mma16816(o[t][n], f, lo[t][0], lo[t][1]);
+            }
           }
-          if (wrote) fence_proxy_async_smem();   // before the stage is filled again by TMA
+          if (tail) fence_proxy_async_smem();   // before the stage is filled again by TMA
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[stage]);
@@ -277,64 +291,80 @@ __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(con
         }
       }
       // ---- the four warps' results together
-      la += __shfl_xor_sync(0xffffffffu, la, 1);
-      lb += __shfl_xor_sync(0xffffffffu, lb, 1);
-      la += __shfl_xor_sync(0xffffffffu, la, 2);
-      lb += __shfl_xor_sync(0xffffffffu, lb, 2);
-      if ((lane & 3) == 0) {
-        m_s[warp][ra] = ma;
-        m_s[warp][rb] = mb;
-        l_s[warp][ra] = la;
-        l_s[warp][rb] = lb;
-      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], off);
+          if (quad == 0) {
+            m_s[warp][t * 8 + pair + e] = ref[t][e];
+            l_s[warp][t * 8 + pair + e] = l[t][e];
+          }
+        }
       ok = !any_of_128(!ok);   // a barrier; a wait that ran out ends the work of all four
       if (!ok) break;
-      float Ma = -INFINITY, Mb = -INFINITY;
 #pragma unroll
-      for (int v = 0; v < kConsumers; ++v) {
-        Ma = fmaxf(Ma, m_s[v][ra]);
-        Mb = fmaxf(Mb, m_s[v][rb]);
-      }
-      const float fa = exp2_approx(ma - reference_of(Ma)), fb = exp2_approx(mb - reference_of(Mb));
+      for (int t = 0; t < NT; ++t) {   // 8 rows at a time
+        if (t * 8 >= rows) break;
+        float f[2];
 #pragma unroll
-      for (int v = 0; v < kConsumers; ++v) {   // one warp after another: a fixed order
-        if (warp == v) {
+        for (int e = 0; e < 2; ++e) {
+          const int r = t * 8 + pair + e;
+          float m = -INFINITY;
 #pragma unroll
-          for (int n = 0; n < DP / 8; ++n) {
-            float2* a = reinterpret_cast<float2*>(sum_s + ra * DP + n * 8 + pair);
-            float2 t = v == 0 ? make_float2(0.0f, 0.0f) : *a;
-            *a = make_float2(t.x + o[n][0] * fa, t.y + o[n][1] * fa);
-            if (upper) {
-              float2* c = reinterpret_cast<float2*>(sum_s + rb * DP + n * 8 + pair);
-              t = v == 0 ? make_float2(0.0f, 0.0f) : *c;
-              *c = make_float2(t.x + o[n][2] * fb, t.y + o[n][3] * fb);
+          for (int v = 0; v < kConsumers; ++v)
+            if (l_s[v][r] != 0.0f) m = fmaxf(m, m_s[v][r]);
+          f[e] = l_s[warp][r] == 0.0f ? 0.0f : exp2_approx(m_s[warp][r] - reference_of(m));
+        }
+        if (warp > 0) {
+#pragma unroll
+          for (int n = 0; n < DP / 16; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              sum_s[((warp - 1) * 8 + pair + (e & 1)) * DP + n * 16 + (e >> 1) * 8 + quad] = f[e & 1] == 0.0f ? 0.0f : o[t][n][e] * f[e & 1];
+        }
+        consumer_sync();
+        if (warp == 0) {
+#pragma unroll
+          for (int n = 0; n < DP / 16; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int at = (pair + (e & 1)) * DP + n * 16 + (e >> 1) * 8 + quad;
+              float sum = f[e & 1] == 0.0f ? 0.0f : o[t][n][e] * f[e & 1];
+#pragma unroll
+              for (int v = 0; v < kConsumers - 1; ++v) sum += sum_s[v * 8 * DP + at];
+              sum_s[at] = sum;
             }
+        }
+        consumer_sync();
+        // ---- eight values of a row a thread
+        for (int c = threadIdx.x; c < min(8, rows - t * 8) * (DP / 8); c += 32 * kConsumers) {
+          const int r8 = c / (DP / 8), r = t * 8 + r8, d = (c % (DP / 8)) * 8;
+          float m = -INFINITY, all = 0.0f;
+#pragma unroll
+          for (int v = 0; v < kConsumers; ++v)
+            if (l_s[v][r] != 0.0f) m = fmaxf(m, m_s[v][r]);
+#pragma unroll
+          for (int v = 0; v < kConsumers; ++v)
+            if (l_s[v][r] != 0.0f) all += l_s[v][r] * exp2_approx(m_s[v][r] - reference_of(m));
+          float val[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) val[i] = sum_s[r8 * DP + d + i];
+          const int in = (row0 + r) / p.G;
+          const long long token = w.r.q0 + in;
+          const int head = w.kh * p.G + (row0 + r) - in * p.G;
+          if (x.all && p.prefix_splits == 0) {
+            write_row8(p, token, head, d, m, all, val);
+          } else {
+            const long long at = x.all ? part_row(p, token, head) : static_cast<long long>(x.slot) * p.item_rows + r;
+            float4* to = reinterpret_cast<float4*>((x.all ? p.part_o : p.piece_o) + at * DP + d);
+            to[0] = make_float4(val[0], val[1], val[2], val[3]);
+            to[1] = make_float4(val[4], val[5], val[6], val[7]);
+            if (d == 0) (x.all ? p.part_ml : p.piece_ml)[at] = make_float2(m, all);
           }
         }
         consumer_sync();
-      }
-      // ---- eight values of a row a thread
-      for (int c = threadIdx.x; c < rows * (DP / 8); c += 32 * kConsumers) {
-        const int r = c / (DP / 8), d = (c % (DP / 8)) * 8;
-        float m = -INFINITY, l = 0.0f;
-#pragma unroll
-        for (int v = 0; v < kConsumers; ++v) m = fmaxf(m, m_s[v][r]);
-#pragma unroll
-        for (int v = 0; v < kConsumers; ++v) l += l_s[v][r] * exp2_approx(m_s[v][r] - reference_of(m));
-        float val[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) val[i] = sum_s[r * DP + d + i];
-        const long long token = w.r.q0 + (row0 + r) / p.G;
-        const int head = w.kh * p.G + (row0 + r) % p.G;
-        if (x.all && p.prefix_splits == 0) {
-          write_row8(p, token, head, d, m, l, val);
-        } else {
-          const long long at = x.all ? part_row(p, token, head) : static_cast<long long>(x.slot) * p.item_rows + r;
-          float4* to = reinterpret_cast<float4*>((x.all ? p.part_o : p.piece_o) + at * DP + d);
-          to[0] = make_float4(val[0], val[1], val[2], val[3]);
-          to[1] = make_float4(val[4], val[5], val[6], val[7]);
-          if (d == 0) (x.all ? p.part_ml : p.piece_ml)[at] = make_float2(m, l);
-        }
       }
       if (!x.all && x.lo == 0 && threadIdx.x == 0) {
         p.records[cta] = record_of<kRows, kKeys, kFewOver>(p, s, w, x, cta);
@@ -351,16 +381,24 @@ __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(con
 }  // namespace
 
 cudaError_t prepare_attention_rows() {
-  cudaError_t e = cudaFuncSetAttribute(attention_rows_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(64));
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(attention_rows_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(128));
-  return e;
+  for (auto* k : {attention_rows_kernel<64, 1>, attention_rows_kernel<64, 2>}) {
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(64));
+    if (e != cudaSuccess) return e;
+  }
+  for (auto* k : {attention_rows_kernel<128, 1>, attention_rows_kernel<128, 2>}) {
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(128));
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
-cudaError_t launch_attention_rows(const AttentionParams& p, int dp, cudaStream_t stream) {
+cudaError_t launch_attention_rows(const AttentionParams& p, int dp, bool eight, cudaStream_t stream) {
   const dim3 grid(p.plan.ctas), block(kThreads);
-  return dp == 64 ? launch_k(attention_rows_kernel<64>, grid, block, smem_bytes(64), stream, true, p)
-                  : launch_k(attention_rows_kernel<128>, grid, block, smem_bytes(128), stream, true, p);
+  if (dp == 64)
+    return eight ? launch_k(attention_rows_kernel<64, 1>, grid, block, smem_bytes(64), stream, true, p)
+                 : launch_k(attention_rows_kernel<64, 2>, grid, block, smem_bytes(64), stream, true, p);
+  return eight ? launch_k(attention_rows_kernel<128, 1>, grid, block, smem_bytes(128), stream, true, p)
+               : launch_k(attention_rows_kernel<128, 2>, grid, block, smem_bytes(128), stream, true, p);
 }
 
 }  // namespace mlk
