@@ -279,21 +279,22 @@ PrefixRun prefix_run(int T, int G, int Hk, int keys, int sms) {
   return r;
 }
 
-// The caches' tensor map: 64 values of up to `keys` tokens of a page at a time.  Extents of one have no stride
-// of their own.
-CUresult page_map(moe_lora_handle* h, CUtensorMap* m, const void* base, const AttentionParams& p, long long s_token,
-                  long long s_head, long long s_page, int keys) {
-  const long long any = 2LL * p.D;   // (D is a multiple of 8)
-  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(p.D), static_cast<cuuint64_t>(p.page), static_cast<cuuint64_t>(p.Hk),
-                              static_cast<cuuint64_t>(p.num_pages)};
-  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(p.page > 1 ? 2 * s_token : any),
-                                 static_cast<cuuint64_t>(p.Hk > 1 ? 2 * s_head : any),
-                                 static_cast<cuuint64_t>(p.num_pages > 1 ? 2 * s_page : any)};
-  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(p.page < keys ? p.page : keys), 1, 1};
-  const cuuint32_t ones[4] = {1, 1, 1, 1};
-  return h->encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, ones,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+// The caches' tensor map: 64 values of up to `keys` tokens of a page at a time, or both halves of 128 values.
+// Extents of one have no stride of their own.
+bool page_map(moe_lora_handle* h, CUtensorMap* m, const void* base, const AttentionParams& p, long long s_token,
+              long long s_head, long long s_page, int keys, bool both) {
+  const cuuint64_t any = 2ull * p.D;   // (D is a multiple of 8)
+  const cuuint64_t token = p.page > 1 ? 2 * s_token : any, head = p.Hk > 1 ? 2 * s_head : any,
+                   page = p.num_pages > 1 ? 2 * s_page : any;
+  const cuuint64_t tokens = p.page, heads = p.Hk, pages = p.num_pages;
+  const cuuint32_t rows = static_cast<cuuint32_t>(p.page < keys ? p.page : keys);
+  const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
+  const cuuint64_t dims4[4] = {static_cast<cuuint64_t>(p.D), tokens, heads, pages}, strides4[3] = {token, head, page};
+  const cuuint64_t dims5[5] = {64, tokens, 2, heads, pages}, strides5[4] = {token, 128, head, page};
+  const cuuint32_t box4[4] = {64, rows, 1, 1}, box5[5] = {64, rows, 2, 1, 1};
+  return h->encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, both ? 5 : 4, const_cast<void*>(base), both ? dims5 : dims4,
+                   both ? strides5 : strides4, both ? box5 : box4, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Whether whole 16-byte pieces and the caches' maps can be used.
@@ -403,12 +404,13 @@ extern "C" moe_lora_status moe_lora_attention(moe_lora_handle* h, const moe_lora
   p.part_ml = reinterpret_cast<float2*>(base + at.part_ml);
   p.part_o = reinterpret_cast<float*>(base + at.part_o);
   p.shared = a->B > 1 ? a->shared_len / kTileKeys * kTileKeys : 0;   // the rest is each request's own
-  auto maps = [&](int keys) {
-    return page_map(h, &p.tmap_k, p.k, p, p.k_t, p.k_h, p.k_p, keys) == CUDA_SUCCESS &&
-           page_map(h, &p.tmap_v, p.v, p, p.v_t, p.v_h, p.v_p, keys) == CUDA_SUCCESS;
+  p.both_halves = p.D == 128;   // (fewer values would be read past)
+  auto maps = [&](int keys, bool both) {
+    return page_map(h, &p.tmap_k, p.k, p, p.k_t, p.k_h, p.k_p, keys, both) &&
+           page_map(h, &p.tmap_v, p.v, p, p.v_t, p.v_h, p.v_p, keys, both);
   };
   const bool tiles = static_cast<long long>(a->max_query_len) * p.G > kFewRows;
-  if ((tiles || p.shared > 0) && !maps(kTileKeys)) return cuda_fail(cudaErrorInvalidValue, "attention tensor maps");
+  if ((tiles || p.shared > 0) && !maps(kTileKeys, false)) return cuda_fail(cudaErrorInvalidValue, "attention tensor maps");
   if (p.shared > 0) {
     const PrefixRun run = prefix_run(p.T, p.G, p.Hk, p.shared, h->num_sms);
     const long long blocks = static_cast<long long>(run.row_tiles) * p.Hk * run.splits;
@@ -427,7 +429,7 @@ extern "C" moe_lora_status moe_lora_attention(moe_lora_handle* h, const moe_lora
     p.long_queries = static_cast<long long>(a->max_query_len) * p.G > 8LL * kTileRows;
     join_across = (p.item_rows + kTeams - 1) / kTeams;
   } else {
-    if (!maps(kFewKeys)) return cuda_fail(cudaErrorInvalidValue, "attention tensor maps");
+    if (!maps(kFewKeys, p.both_halves)) return cuda_fail(cudaErrorInvalidValue, "attention tensor maps");
     p.plan.ctas = kFewPerSm * h->num_sms;
     p.plan.least = 8;
     p.plan.whole = own_keys <= 16LL * kFewKeys;

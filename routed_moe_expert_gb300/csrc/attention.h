@@ -42,6 +42,7 @@ struct AttentionParams {
   int shared;                                  // keys that are read from request 0's table
   int long_queries;                            // requests have many items each
   int out_vec;                                 // rows of `out` start on 16-byte boundaries
+  int both_halves;                             // the maps have both halves of a key in a box (tma_load_page2)
   float scale_log2;                            // scale * log2(e): weights are powers of two
   Plan plan;
   PieceRecord* records;                        // [ctas], null with `whole`
@@ -203,6 +204,56 @@ MLDEV void make_schedule(const AttentionParams& p, int cta, Schedule<ROWS, KEYS,
                          long long* sums_s) {
   using S = Schedule<ROWS, KEYS, OVER>;
   const int tid = threadIdx.x, NT = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = NT >> 5;
+  auto runs = [&](long long units, long long items) {   // the blocks that work, and this one's run
+    s.units = units;
+    const long long by_least = units < (1ll << 31) ? static_cast<uint32_t>(units) / static_cast<uint32_t>(p.plan.least) : p.plan.ctas;
+    s.ctas = static_cast<int>(max(1ll, min(static_cast<long long>(p.plan.ctas), max(by_least, items))));
+    s.start = s.start_of(min(cta, s.ctas));
+    s.end = cta < s.ctas ? s.start_of(cta + 1) : s.start;
+  };
+  w.b = p.B;
+  if (p.B <= 32 && !p.long_queries) {   // few requests, a lane each: every warp by itself
+    Request r;
+    r.q0 = r.n = r.kv = 0;
+    r.bad = false;
+    int items = 0;
+    long long mine = 0;
+    if (lane < p.B) {
+      r = request_of(p, lane);
+      items = S::items_of(p, r);
+      for (int i = 0; i < items; ++i) mine += S::weight_of(p, r, i);
+      mine *= p.Hk;
+    }
+    s.bad = __any_sync(0xffffffffu, r.bad);
+    long long incl = mine;
+    int all_items = items;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += u;
+      all_items += __shfl_xor_sync(0xffffffffu, all_items, off);
+    }
+    runs(__shfl_sync(0xffffffffu, incl, 31), static_cast<long long>(all_items) * p.Hk);
+    if (s.start == s.end) return;
+    const unsigned at = __ballot_sync(0xffffffffu, incl - mine <= s.start && s.start < incl);
+    w.b = __ffs(at) - 1;
+    w.r.q0 = __shfl_sync(0xffffffffu, r.q0, w.b);
+    w.r.n = __shfl_sync(0xffffffffu, r.n, w.b);
+    w.r.kv = __shfl_sync(0xffffffffu, r.kv, w.b);
+    w.r.bad = false;
+    w.items = __shfl_sync(0xffffffffu, items, w.b);
+    w.u0 = __shfl_sync(0xffffffffu, incl - mine, w.b);
+    const long long per = w.items == 1 ? S::weight_of(p, w.r, 0) : __shfl_sync(0xffffffffu, mine, w.b) / p.Hk;
+    w.kh = static_cast<int>(per < (1ll << 31) ? static_cast<long long>(static_cast<uint32_t>(s.start - w.u0) / static_cast<uint32_t>(per)) : (s.start - w.u0) / per);
+    w.u0 += w.kh * per;
+    w.units = static_cast<int>(w.items == 1 ? per : S::weight_of(p, w.r, 0));
+    w.i = 0;
+    while (w.u0 + w.units <= s.start) {   // (few: queries are not long)
+      w.u0 += w.units;
+      w.units = S::weight_of(p, w.r, ++w.i);
+    }
+    return;
+  }
   // the units of request b0 + tid (and its items), for a chunk of NT requests
   auto chunk = [&](int b0, int& items, bool& bad) -> long long {
     long long sum = 0;
@@ -260,13 +311,7 @@ MLDEV void make_schedule(const AttentionParams& p, int cta, Schedule<ROWS, KEYS,
     t += sm.sums[i];
     n += sm.items[i];
   }
-  s.units = t;
-  const long long want = max(static_cast<long long>(t < (1ll << 31) ? static_cast<uint32_t>(t) / static_cast<uint32_t>(p.plan.least) : p.plan.ctas),
-                             min(n, static_cast<long long>(p.plan.ctas)));
-  s.ctas = static_cast<int>(max(1ll, min(want, static_cast<long long>(p.plan.ctas))));
-  s.start = s.start_of(min(cta, s.ctas));
-  s.end = cta < s.ctas ? s.start_of(cta + 1) : s.start;
-  w.b = p.B;
+  runs(t, n);
   if (s.start == s.end) return;
   // the request that has unit `start`
   __syncthreads();
@@ -426,6 +471,15 @@ MLDEV void tma_load_page(void* dst, const CUtensorMap* map, uint64_t* bar, int x
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
       " [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(token), "r"(head), "r"(page), "l"(policy)
+      : "memory");
+}
+
+// Both halves of a page's keys of 128 values, one behind the other (map {64, page, 2, Hk, pages}).
+MLDEV void tma_load_page2(void* dst, const CUtensorMap* map, uint64_t* bar, int token, int head, int page, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %3, %5, %6}], [%2], %7;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(0), "r"(token), "r"(head), "r"(page), "l"(policy)
       : "memory");
 }
 

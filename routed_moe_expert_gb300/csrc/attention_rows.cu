@@ -25,7 +25,7 @@ constexpr int kConsumers = 4, kThreads = 32 * (kConsumers + 1);
 __host__ __device__ constexpr int stage_bytes(int dp) { return 2 * kKeys * dp * 2; }   // keys, then values
 __host__ __device__ constexpr int stages_of(int dp) { return dp == 64 ? 6 : 3; }
 // the ring, and 8 rows of three warps' results
-constexpr int smem_bytes(int dp) { return stages_of(dp) * stage_bytes(dp) + 3 * 8 * dp * 4; }
+constexpr int smem_bytes(int dp) { return stages_of(dp) * stage_bytes(dp) + 3 * 8 * (dp + 4) * 4; }
 constexpr float kMostWeight = 1.099511627776e12f;   // 2^40: a unit's weights above it make a new reference
 
 MLDEV void ldsm4(uint32_t at, uint32_t (&r)[4]) {
@@ -64,9 +64,13 @@ __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(con
   using Sched = Schedule<kRows, kKeys, kFewOver>;
   using Place = Walk<kRows, kKeys, kFewOver>;
   constexpr int kStages = stages_of(DP), STAGE = stage_bytes(DP), HALVES = DP / 64;
-  constexpr int kHalf = kKeys * 128;   // 64 values of every key of a stage
+  // A stage holds the unit's boxes one after another, each 64 values of its keys (rows of 128 bytes), then the
+  // other 64: keys, then values.
+  constexpr int kKeyBytes = DP * 2, kValues = kKeys * kKeyBytes;
+  const int box_log2 = min(p.page_log2, 6), box = 1 << box_log2, half_bytes = box * 128;
   extern __shared__ __align__(1024) uint8_t smem[];
-  float* sum_s = reinterpret_cast<float*>(smem + kStages * STAGE);   // [3][8][DP]
+  constexpr int kSum = DP + 4;   // (rows two apart on other banks)
+  float* sum_s = reinterpret_cast<float*>(smem + kStages * STAGE);   // [3][8][kSum]
   __shared__ uint64_t full[kStages], empty[kStages];
   __shared__ float m_s[kConsumers][kRows], l_s[kConsumers][kRows];
   __shared__ ScheduleSmem sched_s;
@@ -102,24 +106,29 @@ __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(con
 
   if (warp == kConsumers) {   // ------------------------------------------------ producer
     const uint64_t policy = l2_policy_evict_first();
-    const int box_log2 = min(p.page_log2, 6), box = 1 << box_log2, boxes = kKeys >> box_log2;   // boxes of a unit
+    const int boxes = kKeys >> box_log2;   // of a unit
     int stage = 0, ok = 1;
     uint32_t phase = 0, issued = 0, parity = 0;
     for (; ok && more<kRows, kKeys, kFewOver>(s, w, p); w.next(p)) {
       const Part x = part_of<kRows, kKeys, kFewOver>(p, s, w, cta);
+      if (x.lo >= x.hi) continue;
       const int sees = Sched::seen_by(p, w.r, w.i);
       const int32_t* table = p.tables + w.b * p.table_stride;
-      // A lane a box; its page is looked up a unit ahead of its use.
-      auto page_at = [&](int j) -> int {
-        const int key = p.shared + j * kKeys + (lane << box_log2);
-        return lane < boxes && j < x.hi && key < sees ? table[key >> p.page_log2] : -1;
-      };
-      int ahead = x.lo < x.hi ? page_at(x.lo) : -1;
+      // A lane holds the page of one of 32 boxes in a row, and of one of the next 32.
+      const int first = (p.shared + x.lo * kKeys) >> box_log2, count = (min(sees, p.shared + x.hi * kKeys) + box - 1) >> box_log2;
+      const int per_page = p.page_log2 - box_log2;
+      auto page_at = [&](int b) { return b < count ? table[b >> per_page] : -1; };
+      int base = first, here = page_at(base + lane), ahead = page_at(base + 32 + lane);
       for (int j = x.lo; j < x.hi; ++j) {
-        const int key = p.shared + j * kKeys + (lane << box_log2);
+        const int b0 = (p.shared + j * kKeys) >> box_log2;   // the unit's first box
+        if (b0 - base >= 32) {   // (32 is a multiple of a unit's boxes)
+          base += 32;
+          here = ahead;
+          ahead = page_at(base + 32 + lane);
+        }
+        const int key = (b0 + lane) << box_log2;
         const bool mine = lane < boxes && key < sees;
-        int page = ahead;
-        ahead = page_at(j + 1);
+        int page = __shfl_sync(0xffffffffu, here, (b0 - base + lane) & 31);
         if (mine && (page < 0 || page >= p.num_pages)) {   // read as zeros: outside the map
           record_status(&error_s, kDevBadSlot, kWhereAttention);
           page = -1;
@@ -127,17 +136,22 @@ __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(con
         const int n = __popc(__ballot_sync(0xffffffffu, mine));
         if (lane == 0) {
           ok = wait_soon(&empty[stage], phase ^ 1u, abort_flag, &error_s);
-          if (ok) mbar_arrive_expect_tx(&full[stage], n * 2 * box * HALVES * 128);
+          if (ok) mbar_arrive_expect_tx(&full[stage], n * 2 * box * kKeyBytes);
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
         if (mine) {
-          uint8_t* at = smem + stage * STAGE + lane * box * 128;
+          uint8_t* at = smem + stage * STAGE + lane * box * kKeyBytes;
           const int token = key & (p.page - 1);
+          if (HALVES == 2 && p.both_halves) {
+            tma_load_page2(at, &p.tmap_k, &full[stage], token, w.kh, page, policy);
+            tma_load_page2(at + kValues, &p.tmap_v, &full[stage], token, w.kh, page, policy);
+          } else {
 #pragma unroll
-          for (int half = 0; half < HALVES; ++half) {
-            tma_load_page(at + half * kHalf, &p.tmap_k, &full[stage], half * 64, token, w.kh, page, policy);
-            tma_load_page(at + (HALVES + half) * kHalf, &p.tmap_v, &full[stage], half * 64, token, w.kh, page, policy);
+            for (int half = 0; half < HALVES; ++half) {
+              tma_load_page(at + half * half_bytes, &p.tmap_k, &full[stage], half * 64, token, w.kh, page, policy);
+              tma_load_page(at + kValues + half * half_bytes, &p.tmap_v, &full[stage], half * 64, token, w.kh, page, policy);
+            }
           }
         }
         issued |= 1u << stage;
@@ -155,6 +169,8 @@ __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(con
   } else {   // ------------------------------------------------------------------ consumers
     const int quad = lane >> 2, pair = (lane & 3) * 2;   // a fragment's row and first of two columns
     const int t8 = lane & 7;
+    // the warp's 16 keys of a unit: within their box, and further on in the unit
+    const int first_key = (warp * 16 >> box_log2) * box * kKeyBytes + (warp * 16 & (box - 1)) * 128;
     int stage = 0, ok = 1;
     uint32_t phase = 0;
     bool started = false;   // an item whose rest is other blocks'
@@ -203,14 +219,13 @@ __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(con
         if (!ok) break;
         const int k0 = p.shared + j * kKeys + warp * 16;   // this warp's keys of the unit
         if (k0 < sees) {
-          const uint32_t kb = smem_u32(smem) + stage * STAGE + warp * 16 * 128;
-          const uint32_t vb = kb + HALVES * kHalf;
+          const uint32_t kb = smem_u32(smem) + stage * STAGE + first_key, vb = kb + kValues;
           const bool tail = k0 + 16 > sees;
           if (tail) {   // values that no row sees may be anything, and 0 times it would stay
             for (int c = lane; c < 16 * 8 * HALVES; c += 32) {
               const int t = (c >> 3) & 15;
               if (k0 + t >= sees)
-                *reinterpret_cast<uint4*>(smem + stage * STAGE + (HALVES + (c >> 7)) * kHalf + (warp * 16 + t) * 128 +
+                *reinterpret_cast<uint4*>(smem + stage * STAGE + kValues + first_key + (c >> 7) * half_bytes + t * 128 +
                                           (c & 7) * 16) = make_uint4(0, 0, 0, 0);
             }
             __syncwarp();
@@ -221,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(con
 #pragma unroll
           for (int ks = 0; ks < DP / 16; ++ks) {
             uint32_t f[4];
-            ldsm4(krow + (ks >> 2) * kHalf + (((((ks & 3) << 1) + (lane >> 4)) ^ t8) << 4), f);
+            ldsm4(krow + (ks >> 2) * half_bytes + (((((ks & 3) << 1) + (lane >> 4)) ^ t8) << 4), f);
 #pragma unroll
             for (int t = 0; t < NT; ++t) mma16816(sc[t][ks & 1], f, qf[t][ks][0], qf[t][ks][1]);
           }
@@ -274,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(con
 #pragma unroll
           for (int n = 0; n < DP / 16; ++n) {
             uint32_t f[4];
-            ldsm4_t(vrow + (n >> 2) * kHalf + (((((n & 3) << 1) + ((lane >> 3) & 1)) ^ t8) << 4), f);
+            ldsm4_t(vrow + (n >> 2) * half_bytes + (((((n & 3) << 1) + ((lane >> 3) & 1)) ^ t8) << 4), f);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
               mma16816(o[t][n], f, hi[t][0], hi[t][1]);
@@ -322,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(con
           for (int n = 0; n < DP / 16; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              sum_s[((warp - 1) * 8 + pair + (e & 1)) * DP + n * 16 + (e >> 1) * 8 + quad] = f[e & 1] == 0.0f ? 0.0f : o[t][n][e] * f[e & 1];
+              sum_s[((warp - 1) * 8 + pair + (e & 1)) * kSum + n * 16 + (e >> 1) * 8 + quad] = f[e & 1] == 0.0f ? 0.0f : o[t][n][e] * f[e & 1];
         }
         consumer_sync();
         if (warp == 0) {
@@ -330,10 +345,10 @@ __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(con
           for (int n = 0; n < DP / 16; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int at = (pair + (e & 1)) * DP + n * 16 + (e >> 1) * 8 + quad;
+              const int at = (pair + (e & 1)) * kSum + n * 16 + (e >> 1) * 8 + quad;
               float sum = f[e & 1] == 0.0f ? 0.0f : o[t][n][e] * f[e & 1];
 #pragma unroll
-              for (int v = 0; v < kConsumers - 1; ++v) sum += sum_s[v * 8 * DP + at];
+              for (int v = 0; v < kConsumers - 1; ++v) sum += sum_s[v * 8 * kSum + at];
               sum_s[at] = sum;
             }
         }
@@ -350,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(con
             if (l_s[v][r] != 0.0f) all += l_s[v][r] * exp2_approx(m_s[v][r] - reference_of(m));
           float val[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) val[i] = sum_s[r8 * DP + d + i];
+          for (int i = 0; i < 8; ++i) val[i] = sum_s[r8 * kSum + d + i];
           const int in = (row0 + r) / p.G;
           const long long token = w.r.q0 + in;
           const int head = w.kh * p.G + (row0 + r) - in * p.G;
