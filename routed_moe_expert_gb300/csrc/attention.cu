@@ -431,12 +431,17 @@ extern "C" moe_lora_status moe_lora_attention(moe_lora_handle* h, const moe_lora
   } else {
     if (!maps(kFewKeys, p.both_halves)) return cuda_fail(cudaErrorInvalidValue, "attention tensor maps");
     p.plan.ctas = kFewPerSm * h->num_sms;
-    p.plan.least = 8;
-    p.plan.whole = own_keys <= 16LL * kFewKeys;
+    p.plan.least = 2;
+    p.plan.whole = own_keys <= 8LL * kFewKeys;
     p.long_queries = 0;
     join_across = std::min(4, p.item_rows);
   }
   if (!p.plan.whole) p.records = reinterpret_cast<PieceRecord*>(base + at.records);
+  {
+    const int rows = tiles ? kTileRows : 8, keys = tiles ? kTileKeys : kFewKeys;
+    const long long items = (static_cast<long long>(p.T) * p.G / rows + p.B) * p.Hk, most = own_keys / keys + 1 + kTileOver;
+    p.plan.few = p.B <= 32 && !p.long_queries && items * most < (1LL << 30);
+  }
   ML_LAUNCH(h, tiles ? launch_attention_tiles(p, PrefixRun{}, p.plan.ctas, dp, stream)
                      : launch_attention_rows(p, dp, static_cast<long long>(a->max_query_len) * p.G <= 8, stream),
             "attention launch");

@@ -20,6 +20,7 @@ struct Plan {
   int ctas;          // blocks of the launch
   int least;         // units that a block takes at least, when that leaves blocks without work
   int whole;
+  int few;           // up to 32 requests whose weights fit 32 bits together: every warp plans for itself
 };
 
 struct PieceRecord {
@@ -212,12 +213,11 @@ MLDEV void make_schedule(const AttentionParams& p, int cta, Schedule<ROWS, KEYS,
     s.end = cta < s.ctas ? s.start_of(cta + 1) : s.start;
   };
   w.b = p.B;
-  if (p.B <= 32 && !p.long_queries) {   // few requests, a lane each: every warp by itself
+  if (p.plan.few) {   // a lane a request
     Request r;
     r.q0 = r.n = r.kv = 0;
     r.bad = false;
-    int items = 0;
-    long long mine = 0;
+    int items = 0, mine = 0;
     if (lane < p.B) {
       r = request_of(p, lane);
       items = S::items_of(p, r);
@@ -225,33 +225,32 @@ MLDEV void make_schedule(const AttentionParams& p, int cta, Schedule<ROWS, KEYS,
       mine *= p.Hk;
     }
     s.bad = __any_sync(0xffffffffu, r.bad);
-    long long incl = mine;
-    int all_items = items;
+    int incl = mine;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const long long u = __shfl_up_sync(0xffffffffu, incl, off);
+      const int u = __shfl_up_sync(0xffffffffu, incl, off);
       if (lane >= off) incl += u;
-      all_items += __shfl_xor_sync(0xffffffffu, all_items, off);
     }
-    runs(__shfl_sync(0xffffffffu, incl, 31), static_cast<long long>(all_items) * p.Hk);
+    runs(__shfl_sync(0xffffffffu, incl, 31), static_cast<long long>(__reduce_add_sync(0xffffffffu, items)) * p.Hk);
     if (s.start == s.end) return;
-    const unsigned at = __ballot_sync(0xffffffffu, incl - mine <= s.start && s.start < incl);
-    w.b = __ffs(at) - 1;
+    const int start = static_cast<int>(s.start);
+    w.b = __ffs(__ballot_sync(0xffffffffu, incl - mine <= start && start < incl)) - 1;
     w.r.q0 = __shfl_sync(0xffffffffu, r.q0, w.b);
     w.r.n = __shfl_sync(0xffffffffu, r.n, w.b);
     w.r.kv = __shfl_sync(0xffffffffu, r.kv, w.b);
     w.r.bad = false;
     w.items = __shfl_sync(0xffffffffu, items, w.b);
-    w.u0 = __shfl_sync(0xffffffffu, incl - mine, w.b);
-    const long long per = w.items == 1 ? S::weight_of(p, w.r, 0) : __shfl_sync(0xffffffffu, mine, w.b) / p.Hk;
-    w.kh = static_cast<int>(per < (1ll << 31) ? static_cast<long long>(static_cast<uint32_t>(s.start - w.u0) / static_cast<uint32_t>(per)) : (s.start - w.u0) / per);
-    w.u0 += w.kh * per;
-    w.units = static_cast<int>(w.items == 1 ? per : S::weight_of(p, w.r, 0));
+    const int before = __shfl_sync(0xffffffffu, incl - mine, w.b);
+    w.units = S::weight_of(p, w.r, 0);
+    const int per = w.items == 1 ? w.units : __shfl_sync(0xffffffffu, mine, w.b) / p.Hk;
+    w.kh = (start - before) / per;
+    int at = before + w.kh * per;
     w.i = 0;
-    while (w.u0 + w.units <= s.start) {   // (few: queries are not long)
-      w.u0 += w.units;
+    while (at + w.units <= start) {   // (few: queries are not long)
+      at += w.units;
       w.units = S::weight_of(p, w.r, ++w.i);
     }
+    w.u0 = at;
     return;
   }
   // the units of request b0 + tid (and its items), for a chunk of NT requests

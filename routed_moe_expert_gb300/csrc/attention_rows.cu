@@ -126,9 +126,9 @@ __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(con
           here = ahead;
           ahead = page_at(base + 32 + lane);
         }
-        const int key = (b0 + lane) << box_log2;
-        const bool mine = lane < boxes && key < sees;
-        int page = __shfl_sync(0xffffffffu, here, (b0 - base + lane) & 31);
+        const int which = lane & (boxes - 1), key = (b0 + which) << box_log2;   // lanes for the keys' boxes, then the values'
+        const bool mine = lane < 2 * boxes && key < sees;
+        int page = __shfl_sync(0xffffffffu, here, (b0 - base + which) & 31);
         if (mine && (page < 0 || page >= p.num_pages)) {   // read as zeros: outside the map
           record_status(&error_s, kDevBadSlot, kWhereAttention);
           page = -1;
@@ -136,22 +136,21 @@ __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(con
         const int n = __popc(__ballot_sync(0xffffffffu, mine));
         if (lane == 0) {
           ok = wait_soon(&empty[stage], phase ^ 1u, abort_flag, &error_s);
-          if (ok) mbar_arrive_expect_tx(&full[stage], n * 2 * box * kKeyBytes);
+          if (ok) mbar_arrive_expect_tx(&full[stage], n * box * kKeyBytes);
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
         if (mine) {
-          uint8_t* at = smem + stage * STAGE + lane * box * kKeyBytes;
+          const bool values = lane >= boxes;
+          uint8_t* at = smem + stage * STAGE + (values ? kValues : 0) + which * box * kKeyBytes;
+          const CUtensorMap* map = values ? &p.tmap_v : &p.tmap_k;
           const int token = key & (p.page - 1);
           if (HALVES == 2 && p.both_halves) {
-            tma_load_page2(at, &p.tmap_k, &full[stage], token, w.kh, page, policy);
-            tma_load_page2(at + kValues, &p.tmap_v, &full[stage], token, w.kh, page, policy);
+            tma_load_page2(at, map, &full[stage], token, w.kh, page, policy);
           } else {
 #pragma unroll
-            for (int half = 0; half < HALVES; ++half) {
-              tma_load_page(at + half * half_bytes, &p.tmap_k, &full[stage], half * 64, token, w.kh, page, policy);
-              tma_load_page(at + kValues + half * half_bytes, &p.tmap_v, &full[stage], half * 64, token, w.kh, page, policy);
-            }
+            for (int half = 0; half < HALVES; ++half)
+              tma_load_page(at + half * half_bytes, map, &full[stage], half * 64, token, w.kh, page, policy);
           }
         }
         issued |= 1u << stage;
@@ -184,10 +183,9 @@ __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(con
       int limit[NT][2];              // keys that rows pair and pair + 1 see
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const int row = t * 8 + quad;
-        const int token = (row0 + row) / p.G;
+        const int row = row0 + t * 8 + quad, token = row / p.G;
         const __nv_bfloat16* q =
-            row < rows ? p.q + (w.r.q0 + token) * p.q_t + (w.kh * p.G + (row0 + row) - token * p.G) * p.q_h : nullptr;
+            t * 8 + quad < rows ? p.q + (w.r.q0 + token) * p.q_t + (w.kh * p.G + row - token * p.G) * p.q_h : nullptr;
 #pragma unroll
         for (int ks = 0; ks < DP / 16; ++ks)
 #pragma unroll
