@@ -662,7 +662,7 @@ moe_lora_status moe_lora_attention_workspace_size(int T, int q_heads, int k_head
    table, once for all rows instead of once for each request; the results are the same up to float32 sums.
    Scores, sums and the result are float32, rounded once at the end; the weights p_j are an operand of the
    tensor cores in between, as bf16 (two bf16 pieces where requests have up to 16 rows a key head).
-   head_dim a multiple of 8 up to 128, pages of a power of two of at least 16 tokens, and 16-byte pieces in q
+   head_dim a multiple of 8 up to 128, pages of a power of two of at least 16 tokens, and 16-byte pieces in q, out
    and the caches are the fast case; anything else runs on plain cores.
    `workspace` (16-byte aligned, contents on entry do not matter) starts with the status word:
    DEVICE_CHECK when query_offsets are not rising within [0, T], a length is negative or past its table, or a

@@ -302,7 +302,8 @@ bool fast_layout(const moe_lora_attention_args* a) {
   if (a->head_dim % 8 != 0 || a->head_dim > 128 || a->page_size < 16 || (a->page_size & (a->page_size - 1)) != 0 ||
       a->num_pages < 1 || a->table_width < 1)
     return false;
-  if (!aligned16(a->q) || !aligned16(a->k_cache) || !aligned16(a->v_cache) || a->q_stride_t % 8 != 0 || a->q_stride_h % 8 != 0)
+  if (!aligned16(a->q) || !aligned16(a->out) || !aligned16(a->k_cache) || !aligned16(a->v_cache) || a->q_stride_t % 8 != 0 ||
+      a->q_stride_h % 8 != 0 || a->out_stride_t % 8 != 0 || a->out_stride_h % 8 != 0)
     return false;
   const long long limit = 1LL << 38;   // of a map's strides, in elements
   auto fits = [&](long long s, int extent) { return extent <= 1 || (s > 0 && s < limit && s % 8 == 0); };
@@ -379,7 +380,6 @@ extern "C" moe_lora_status moe_lora_attention(moe_lora_handle* h, const moe_lora
   p.status = static_cast<uint32_t*>(workspace);
   p.flags = reinterpret_cast<int*>(h->linear_flags + kLinearFlags);
   p.prefix_splits = 0;
-  p.out_vec = aligned16(p.out) && p.o_t % 8 == 0 && p.o_h % 8 == 0;
   p.records = nullptr;
   ML_ON_DEVICE(h);
   if (!fast_layout(a) || p.scale_log2 == 0.0f || h->num_sms > kMaxSms) {

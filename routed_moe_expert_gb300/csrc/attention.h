@@ -42,7 +42,6 @@ struct AttentionParams {
   int num_pages, page, page_log2, width;
   int shared;                                  // keys that are read from request 0's table
   int long_queries;                            // requests have many items each
-  int out_vec;                                 // rows of `out` start on 16-byte boundaries
   int both_halves;                             // the maps have both halves of a key in a box (tma_load_page2)
   float scale_log2;                            // scale * log2(e): weights are powers of two
   Plan plan;
@@ -452,14 +451,7 @@ MLDEV void write_row8(const AttentionParams& p, long long token, int head, int d
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = l == 0.0f ? 0.0f : o[i] * inv;
   __nv_bfloat16* at = p.out + token * p.o_t + head * p.o_h + d;
-  if (d < p.D) {   // D is a multiple of 8
-    if (p.out_vec) {
-      *reinterpret_cast<uint4*>(at) = pack8(v);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) at[i] = f2bf(v[i]);
-    }
-  }
+  if (d < p.D) *reinterpret_cast<uint4*>(at) = pack8(v);   // (D is a multiple of 8)
   if (d == 0 && p.lse != nullptr) p.lse[token * p.Hq + head] = (reference_of(m) + log2f(l)) * kLn2;
 }
 

@@ -68,11 +68,6 @@ constexpr uint32_t kMnMajorHi = (1024 >> 4) | (1u << 14) | (2u << 29);
 constexpr uint32_t kKMajorHi = kMnMajorHi;
 constexpr uint32_t kMnMajorB = 1u << 16;
 
-MLDEV float max3(float a, float b, float c) {   // a NaN is left out, as fmaxf does
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
 // Two float32 operations an instruction.
 MLDEV float2 fma2(float2 a, float2 b, float2 c) {
   float2 r;
@@ -465,8 +460,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
     const uint32_t lanes = tmem + (static_cast<uint32_t>(wr) << 16);
     const uint32_t s_at = lanes + k * 128, o_at = lanes + 256 + k * DP;
     uint32_t s_phase = 0, o_phase = 0, both_phase = 0;
-    const bool negative = p.scale_log2 < 0.0f;
-    const float scale = fabsf(p.scale_log2);
+    const float scale = p.scale_log2;   // (not 0)
+    const uint32_t unseen = scale < 0.0f ? 0x7f800000u : 0xff800000u;   // the score that scaled is -inf
     // Copies the part's query rows to the products' layout, a warp its own 32 of them, whole rows at a time.
     auto fetch_queries = [&](const Step& t) {
       const int row = t.row0 + (t.lead == 2 ? r : k * 128 + r);
@@ -554,31 +549,43 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
           tc_fence_after();
           const int limit = sees - (key0 + j * kKeys);   // columns below it are seen
           float sum;
+          bool renew = j == first_unit;   // the row's reference, and rarely a new one
           for (int tries = 0;; ++tries) {
+            if (tries > 0 || j == first_unit) {   // (in loops: this is one unit's work, and its code waits to be fetched)
+              float top = -INFINITY;
+#pragma unroll 1
+              for (int c = 0; c < kKeys; c += 16) {
+                uint32_t x[16];
+                tmem_ld_x16(s_at + c, x);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) top = fmaxf(top, c + i < limit ? __uint_as_float(x[i]) * scale : -INFINITY);
+              }
+              const bool grow = renew && top > ref;
+              const float f = grow ? exp2_approx(ref - top) : 1.0f;
+              if (grow) ref = top;
+              l *= f;
+              if (j >= lo + lead) {
+#pragma unroll 1
+                for (int c = 0; c < DP; c += 16) {
+                  uint32_t o[16];
+                  tmem_ld_x16(o_at + c, o);
+                  tmem_ld_wait();
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                  tmem_st_x16(o_at + c, o);
+                }
+              }
+            }
             uint32_t v[4][32];
 #pragma unroll
             for (int c = 0; c < 4; ++c) tmem_ld_x32(s_at + c * 32, v[c]);
             tmem_ld_wait();
-            if (negative) {
-#pragma unroll
-              for (int c = 0; c < 4; ++c)
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[c][i] ^= 0x80000000u;
-            }
             if (j >= whole) {
 #pragma unroll
               for (int c = 0; c < 4; ++c)
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[c][i] = c * 32 + i < limit ? v[c][i] : 0xff800000u;
-            }
-            if (tries == 0 && j == first_unit) {   // the row's reference
-              float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-              for (int i = 0; i < 32; i += 2)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tops[c] = max3(tops[c], __uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1]));
-              const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * scale;   // (scale is not 0)
-              if (r < rows) ref = top;
+                for (int i = 0; i < 32; ++i) v[c][i] = c * 32 + i < limit ? v[c][i] : unseen;
             }
             const float2 off = make_float2(-reference_of(ref), -reference_of(ref));
             float2 sums[2] = {};
@@ -594,40 +601,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
                 v[c >> 1][(c & 1) * 16 + i / 2] = *reinterpret_cast<const uint32_t*>(&h);   // (read already)
               }
             sum = (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y);
-            const bool renew = tries == 0 && (ref == -INFINITY || !(sum <= kMostWeight));
-            if (!__any_sync(0xffffffffu, renew)) {
+            renew = ref == -INFINITY || !(sum <= kMostWeight);
+            if (tries > 0 || !__any_sync(0xffffffffu, renew)) {
               tmem_st_x32(s_at, v[0]);   // over the scores
               tmem_st_x32(s_at + 32, v[1]);
               break;
-            }
-            // ---- rarely: the unit's maximum becomes the reference, and the unit is done again from TMEM
-            float top = -INFINITY;
-#pragma unroll 1
-            for (int c = 0; c < kKeys; c += 16) {
-              uint32_t x[16];
-              tmem_ld_x16(s_at + c, x);
-              tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const float f = negative ? -__uint_as_float(x[i]) : __uint_as_float(x[i]);
-                if (c + i < limit) top = fmaxf(top, f);
-              }
-            }
-            top *= scale;
-            const bool grow = renew && top > ref;
-            const float f = grow ? exp2_approx(ref - top) : 1.0f;
-            if (grow) ref = top;
-            l *= f;
-            if (j >= lo + lead) {
-#pragma unroll 1
-              for (int c = 0; c < DP; c += 16) {
-                uint32_t o[16];
-                tmem_ld_x16(o_at + c, o);
-                tmem_ld_wait();
-#pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                tmem_st_x16(o_at + c, o);
-              }
             }
           }
           l += sum;
@@ -677,7 +655,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
                                              : static_cast<long long>(slot) * p.item_rows + tile_row;
       // Results leave 64 bytes of a row at a time, four lanes having traded their rows' quarters, so that a warp
       // writes whole pieces: a thread a row would touch 32 rows a store.
-      const bool by_row = final && !p.out_vec;   // unless `out` is not aligned to that
       float* piece_o = by_token ? p.part_o : p.piece_o;
       unsigned long long to = 0;
       if (real)
@@ -686,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
       unsigned long long dst[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) dst[i] = __shfl_sync(0xffffffffu, to, (lane & ~3) + i);
-      if (final && !by_row) {
+      if (final) {
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         mine *= inv;
         other *= inv;
@@ -713,18 +690,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
           }
           if (c + 1 < chunks) fetch(c + 1);
           const int col = c_lo + c * 32;
-          if (by_row) {
-            if (real) {
-#pragma unroll
-              for (int i = 0; i < 32; i += 8) {
-                float e[8];
-#pragma unroll
-                for (int n = 0; n < 8; ++n) e[n] = o[i + n];
-                write_row8(p, token, head, col + i, ref, l, e);
-              }
-            }
-            continue;
-          }
           const int part = lane & 3;
           auto leave = [&](uint4 (&x)[4], int bytes, bool inside) {   // 64 bytes of every row
             trade(x, lane);   // now x[i] is quarter `part` of the row of lane (lane & ~3) + i
@@ -758,7 +723,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
       }
       if (real && c_lo == 0) {
         if (!final) (by_token ? p.part_ml : p.piece_ml)[at] = make_float2(ref, l);
-        else if (!by_row && p.lse != nullptr)
+        else if (p.lse != nullptr)
           p.lse[static_cast<long long>(token) * p.Hq + head] = (reference_of(ref) + log2f(l)) * kLn2;
       }
       tc_fence_before();
