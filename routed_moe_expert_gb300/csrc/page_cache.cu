@@ -14,8 +14,8 @@ namespace {
 //
 // Every block takes both sums over all requests (they are a few KB), 1024 requests at a time, and then its
 // share of the new pages and tokens, each of which finds its request by bisection in the block's table of
-// sums: a request with a long prompt is spread like any other.  Blocks form one cluster, whose barrier
-// stands between the last read of lengths and cursor and the first write, so those may be updated in place.
+// sums: a request with a long prompt is spread like any other.  Where lengths or cursor are updated in place the blocks
+// form one cluster, whose barrier stands between the last read of them and the first write.
 //
 // Bound by latency: lengths, sums, one dependent load (table or free list), store.
 // ---------------------------------------------------------------------------------------
@@ -27,6 +27,7 @@ struct TableParams {
   int32_t *kv, *offsets, *slots, *positions, *taken_out;
   long long stride;
   int B, width, page, num_free, T;
+  int in_place;   // kv is cached, or taken_out is taken: the blocks are one cluster
   uint32_t* status;
 };
 
@@ -90,7 +91,7 @@ __global__ void __launch_bounds__(kTableThreads) page_tables_kernel(const __grid
   __shared__ int cached_s[kTableThreads], held_s[kTableThreads], pages_s[kTableThreads];   // pages: held and granted
   __shared__ long long wa[32];
   __shared__ int wb[32];
-  const int C = static_cast<int>(cluster_nctas()), rank = static_cast<int>(cluster_ctarank());
+  const int C = static_cast<int>(gridDim.x), rank = static_cast<int>(blockIdx.x);
   const int tid = threadIdx.x, NT = blockDim.x;
   pdl_wait();
   pdl_trigger();
@@ -111,7 +112,7 @@ __global__ void __launch_bounds__(kTableThreads) page_tables_kernel(const __grid
       cached = max(cached, 0);
       added = max(added, 0);
     }
-    if (C > 1) {   // kv_lens may be cached_lens
+    if (p.in_place && C > 1) {   // the lengths are read by all blocks first
       cluster_arrive();
       cluster_wait();
     }
@@ -178,17 +179,21 @@ __global__ void __launch_bounds__(kTableThreads) page_tables_kernel(const __grid
 }
 
 // ---------------------------------------------------------------------------------------
-// Cache writes: a copy of T rows of heads to scattered rows, in pieces of V values.  Bound by memory at
-// length (each thread keeps four pieces in flight), by latency below.
+// Cache writes: a copy of T rows of heads to scattered rows, in pieces of V values.  A thread keeps to one piece of
+// a row (its head and place are worked out once) and takes tokens in turn, kFlight of them in flight: all loads,
+// which do not wait for the slots, then the stores.  Bound by memory at length, by latency below.
 // ---------------------------------------------------------------------------------------
+constexpr int kFlight = 4;
+
 struct WriteParams {
   const __nv_bfloat16 *k, *v;
   __nv_bfloat16 *kc, *vc;
   const int32_t* slots;
   long long k_t, k_h, v_t, v_h, kc_p, kc_h, kc_t, vc_p, vc_h, vc_t;
-  int T, H, D, page, num_slots;
+  int T, page, page_log2, num_slots;   // page_log2 -1: not a power of two
   int pieces;        // of a token: keys' heads, then values'
   int per_head;      // pieces of a head
+  int at_once;       // tokens that a block takes side by side
   uint32_t* status;
 };
 
@@ -204,11 +209,10 @@ struct Piece<8> {
 template <int V>
 __global__ void __launch_bounds__(256) cache_write_kernel(const __grid_constant__ WriteParams p) {
   using U = typename Piece<V>::type;
-  constexpr int kFlight = 4;
   pdl_wait();
   pdl_trigger();
   if (blockIdx.x == gridDim.x - 1) {   // the status word, by a block of its own
-    if (p.status == nullptr) return;
+    if (p.status == nullptr || blockIdx.y > 0) return;
     int most = -1;
     for (long long t = threadIdx.x; t < p.T; t += 8 * blockDim.x) {
       int s[8];   // in flight together: at 8192 tokens this block takes less time than the copy
@@ -217,37 +221,38 @@ __global__ void __launch_bounds__(256) cache_write_kernel(const __grid_constant_
 #pragma unroll
       for (int j = 0; j < 8; ++j) most = max(most, s[j]);
     }
-    const bool bad = most >= p.num_slots;
-    const bool any = __syncthreads_or(bad) != 0;
+    const bool any = __syncthreads_or(most >= p.num_slots) != 0;
     if (threadIdx.x == 0) *p.status = any ? kDevBadSlot | (kWhereCacheWrite << 8) : 0u;
     return;
   }
-  const long long total = static_cast<long long>(p.T) * p.pieces;
-  const long long step = static_cast<long long>(gridDim.x - 1) * blockDim.x;
-  for (long long i0 = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i0 < total; i0 += kFlight * step) {
+  const int lane_token = p.at_once > 1 ? static_cast<int>(threadIdx.x) / p.pieces : 0;
+  int piece = static_cast<int>(blockIdx.y) * blockDim.x + threadIdx.x - lane_token * p.pieces;
+  if (piece >= p.pieces || lane_token >= p.at_once) return;
+  const bool values = piece >= p.pieces / 2;
+  if (values) piece -= p.pieces / 2;
+  const int h = piece / p.per_head, d = (piece - h * p.per_head) * V;
+  const __nv_bfloat16* src = (values ? p.v + h * p.v_h : p.k + h * p.k_h) + d;
+  __nv_bfloat16* dst = (values ? p.vc + h * p.vc_h : p.kc + h * p.kc_h) + d;
+  const long long src_t = values ? p.v_t : p.k_t, dst_p = values ? p.vc_p : p.kc_p, dst_t = values ? p.vc_t : p.kc_t;
+  const long long step = static_cast<long long>(gridDim.x - 1) * p.at_once;
+  for (long long t0 = static_cast<long long>(blockIdx.x) * p.at_once + lane_token; t0 < p.T; t0 += kFlight * step) {
     U val[kFlight];
-    U* to[kFlight];
+    int slot[kFlight];
 #pragma unroll
     for (int f = 0; f < kFlight; ++f) {
-      const long long i = i0 + f * step;
-      to[f] = nullptr;
-      if (i >= total) continue;
-      const int t = total <= 0x7fffffff ? static_cast<int>(i) / p.pieces : static_cast<int>(i / p.pieces);
-      const int slot = p.slots[t];
-      if (slot < 0 || slot >= p.num_slots) continue;
-      int at = static_cast<int>(i - static_cast<long long>(t) * p.pieces);
-      const bool is_v = at >= p.pieces / 2;
-      if (is_v) at -= p.pieces / 2;
-      const int h = at / p.per_head, d = (at - h * p.per_head) * V;
-      const int page = slot / p.page, in = slot - page * p.page;
-      const __nv_bfloat16* src = is_v ? p.v + t * p.v_t + h * p.v_h + d : p.k + t * p.k_t + h * p.k_h + d;
-      val[f] = *reinterpret_cast<const U*>(src);
-      to[f] = reinterpret_cast<U*>(is_v ? p.vc + page * p.vc_p + h * p.vc_h + in * p.vc_t + d
-                                        : p.kc + page * p.kc_p + h * p.kc_h + in * p.kc_t + d);
+      const long long t = t0 + f * step;
+      slot[f] = -1;
+      if (t < p.T) {
+        slot[f] = p.slots[t];
+        val[f] = *reinterpret_cast<const U*>(src + t * src_t);
+      }
     }
 #pragma unroll
-    for (int f = 0; f < kFlight; ++f)
-      if (to[f] != nullptr) *to[f] = val[f];
+    for (int f = 0; f < kFlight; ++f) {
+      if (slot[f] < 0 || slot[f] >= p.num_slots) continue;
+      const int page = p.page_log2 >= 0 ? slot[f] >> p.page_log2 : slot[f] / p.page;
+      *reinterpret_cast<U*>(dst + page * dst_p + (slot[f] - page * p.page) * dst_t) = val[f];
+    }
   }
 }
 
@@ -292,11 +297,12 @@ extern "C" moe_lora_status moe_lora_page_tables(moe_lora_handle* h, const moe_lo
   p.num_free = a->num_free;
   p.T = a->T;
   p.status = static_cast<uint32_t*>(workspace);
-  // a block more for every 2048 tokens, eight at most (the portable cluster)
-  const int ctas = std::min(8, 1 + a->T / 2048);
+  p.in_place = a->kv_lens == a->cached_lens || a->taken_out == a->taken;
+  // a block for every 1024 tokens; a cluster has eight at most
+  const int ctas = std::min(p.in_place ? 8 : 64, 1 + a->T / 1024);
   const int threads = std::max(a->B, a->T) <= 128 ? 128 : kTableThreads;
   ML_ON_DEVICE(h);
-  ML_LAUNCH(h, launch_kc(page_tables_kernel, dim3(ctas), dim3(threads), 0, stream, true, ctas, p), "page_tables launch");
+  ML_LAUNCH(h, launch_kc(page_tables_kernel, dim3(ctas), dim3(threads), 0, stream, true, p.in_place ? ctas : 1, p), "page_tables launch");
   return MOE_LORA_OK;
 }
 
@@ -333,27 +339,31 @@ extern "C" moe_lora_status moe_lora_cache_write(moe_lora_handle* h, const moe_lo
   p.vc_h = a->v_stride_head;
   p.vc_t = a->v_stride_token;
   p.T = a->T;
-  p.H = a->heads;
-  p.D = a->head_dim;
   p.page = a->page_size;
+  p.page_log2 = -1;
+  if ((p.page & (p.page - 1)) == 0)
+    for (p.page_log2 = 0; (1 << p.page_log2) < p.page;) ++p.page_log2;
   p.num_slots = a->num_pages * a->page_size;
   p.status = static_cast<uint32_t*>(workspace);
-  uintptr_t bits = static_cast<uintptr_t>(p.D);
+  uintptr_t bits = static_cast<uintptr_t>(a->head_dim);
   for (const void* q : {static_cast<const void*>(p.k), static_cast<const void*>(p.v), static_cast<const void*>(p.kc),
                         static_cast<const void*>(p.vc)})
     bits |= reinterpret_cast<uintptr_t>(q) / 2;
   for (long long s : {p.k_t, p.k_h, p.v_t, p.v_h, p.kc_p, p.kc_h, p.kc_t, p.vc_p, p.vc_h, p.vc_t}) bits |= static_cast<uintptr_t>(s);
   const int V = (bits & 7) == 0 ? 8 : 1;
-  p.per_head = p.D / V;
-  if (2LL * p.H * p.per_head > 0x7fffffffLL) return MOE_LORA_ERR_INVALID_ARG;
-  p.pieces = 2 * p.H * p.per_head;
-  const long long total = static_cast<long long>(p.T) * p.pieces;
-  // as many threads as the GPU holds, one piece each while that is enough
-  const int threads = total <= 128LL * h->num_sms ? 128 : 256;
-  const int blocks = static_cast<int>(std::min<long long>((total + threads - 1) / threads, 8LL * h->num_sms)) + 1;
+  p.per_head = a->head_dim / V;
+  p.pieces = 2 * a->heads * p.per_head;   // (at most 2^27)
+  p.at_once = p.pieces >= 256 ? 1 : 256 / p.pieces;
+  const int across = (p.pieces + 255) / 256;
+  if (across > 65535) return MOE_LORA_ERR_UNSUPPORTED;
+  // as many blocks as the GPU holds, and threads of them with one token to copy while that is enough
+  const long long groups = (static_cast<long long>(p.T) + p.at_once - 1) / p.at_once;
+  const int blocks = static_cast<int>(std::min<long long>(groups, std::max(1, 8 * h->num_sms / across))) + 1;
+  const dim3 grid(blocks, across);
+  const int threads = p.at_once > 1 ? (p.at_once * p.pieces + 31) / 32 * 32 : std::min(256, (p.pieces + 31) / 32 * 32);
   ML_ON_DEVICE(h);
-  ML_LAUNCH(h, V == 8 ? launch_k(cache_write_kernel<8>, dim3(blocks), dim3(threads), 0, stream, true, p)
-                      : launch_k(cache_write_kernel<1>, dim3(blocks), dim3(threads), 0, stream, true, p),
+  ML_LAUNCH(h, V == 8 ? launch_k(cache_write_kernel<8>, grid, dim3(threads), 0, stream, true, p)
+                      : launch_k(cache_write_kernel<1>, grid, dim3(threads), 0, stream, true, p),
             "cache_write launch");
   return MOE_LORA_OK;
 }
