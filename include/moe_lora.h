@@ -657,7 +657,8 @@ moe_lora_status moe_lora_attention_workspace_size(int T, int q_heads, int k_head
    j < kv_lens[b] - n + i + 1, and
      out[row, h] = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale q . k_j - max).
    A row that sees no key, or whose every score is -inf, gets zeros and lse -inf.  Rows of no request are left
-   as they are.  Keys that a row does not see, the rest of a last page among them, may hold anything.
+   as they are.  Keys and values that a row does not see, the rest of a last page among them, may hold anything;
+   a value that is not finite makes those rows' results that see it infinite or NaN.
    shared_len names keys that all requests have in common (a common prompt): they are read from request 0's
    table, once for all rows instead of once for each request; the results are the same up to float32 sums.
    Scores, sums and the result are float32, rounded once at the end; the weights p_j are an operand of the

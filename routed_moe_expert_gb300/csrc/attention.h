@@ -455,6 +455,64 @@ MLDEV void write_row8(const AttentionParams& p, long long token, int head, int d
   if (d == 0 && p.lse != nullptr) p.lse[token * p.Hq + head] = (reference_of(m) + log2f(l)) * kLn2;
 }
 
+// A row whose result is not finite although its weights are: a warp looks whether a value that the row does not see, of
+// the keys [key_lo, key_hi) that were multiplied, is not finite (0 times it is NaN), and if so sums columns
+// [d_lo, d_lo + d_n) of the row again over the keys below `limit` on plain cores and
+// writes them: factor * sum as bf16 to `out`, or the sum to `piece`.  Returns whether it did.  Rare, so it is
+// out of the way.
+template <int DP>
+__device__ __noinline__ bool repair_row(const AttentionParams& p, int b, int kh, long long token, int head, int key_lo,
+                                        int key_hi, int limit, float ref, float factor, int d_lo, int d_n,
+                                        __nv_bfloat16* out, float* piece) {
+  const int lane = threadIdx.x & 31;
+  const int32_t* table = p.tables + b * p.table_stride;
+  auto row_of = [&](const __nv_bfloat16* base, long long s_page, long long s_head, long long s_token, int key) {
+    const int page = table[key >> p.page_log2];
+    return page < 0 || page >= p.num_pages ? nullptr
+                                           : base + page * s_page + kh * s_head + (key & (p.page - 1)) * s_token;
+  };
+  const int from = max(limit, key_lo), per = d_n / 8;
+  bool found = false;
+  for (int c = lane; c < (key_hi - from) * per; c += 32) {
+    const int d = d_lo + c % per * 8;
+    const __nv_bfloat16* v = row_of(p.v, p.v_p, p.v_h, p.v_t, from + c / per);
+    if (v == nullptr || d >= p.D) continue;
+    const uint4 x = *reinterpret_cast<const uint4*>(v + d);
+    for (const uint32_t y : {x.x, x.y, x.z, x.w})
+      found = found || (y & 0x7f80u) == 0x7f80u || (y & 0x7f800000u) == 0x7f800000u;
+  }
+  if (!__any_sync(0xffffffffu, found)) return false;
+  const __nv_bfloat16* q = p.q + token * p.q_t + head * p.q_h;
+  float o[DP / 32] = {};
+  for (int j0 = key_lo; j0 < min(limit, key_hi); j0 += 32) {
+    const int n = min(32, min(limit, key_hi) - j0);
+    float dot = 0.0f;
+    if (lane < n) {
+      const __nv_bfloat16* k = row_of(p.k, p.k_p, p.k_h, p.k_t, j0 + lane);
+      for (int d = 0; k != nullptr && d < p.D; ++d) dot += bf2f(q[d]) * bf2f(k[d]);
+    }
+    const float w = exp2_approx(dot * p.scale_log2 - ref);
+    for (int t = 0; t < n; ++t) {
+      const float wt = __shfl_sync(0xffffffffu, w, t);
+      const __nv_bfloat16* v = row_of(p.v, p.v_p, p.v_h, p.v_t, j0 + t);
+#pragma unroll
+      for (int i = 0; i < DP / 32; ++i) {
+        const int d = d_lo + i * 32 + lane;
+        if (v != nullptr && i * 32 + lane < d_n && d < p.D) o[i] += wt * bf2f(v[d]);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < DP / 32; ++i) {
+    const int d = d_lo + i * 32 + lane;
+    if (i * 32 + lane >= d_n) continue;
+    if (piece != nullptr) piece[d] = o[i];
+    else if (d < p.D) out[d] = f2bf(o[i] * factor);
+  }
+  __syncwarp();
+  return true;
+}
+
 // Box of one page's keys (or a part of a page) from the caches' maps; x a multiple of 64.
 MLDEV void tma_load_page(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int token, int head, int page,
                          uint64_t policy) {

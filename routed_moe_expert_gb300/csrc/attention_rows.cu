@@ -77,6 +77,7 @@ __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(con
   __shared__ long long sums_s[kThreads];
   __shared__ uint32_t error_s;
   __shared__ int abort_s;
+  __shared__ unsigned odd_s, done_s;   // rows whose result is not finite, and those that are written already
   volatile int* abort_flag = &abort_s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = static_cast<int>(blockIdx.x);
 
@@ -87,6 +88,7 @@ __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(con
     }
     error_s = 0;
     abort_s = 0;
+    odd_s = done_s = 0;
     fence_mbar_init();
   }
   if (warp == kConsumers && lane == 0) {
@@ -351,31 +353,81 @@ __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(con
             }
         }
         consumer_sync();
-        // ---- eight values of a row a thread
-        for (int c = threadIdx.x; c < min(8, rows - t * 8) * (DP / 8); c += 32 * kConsumers) {
-          const int r8 = c / (DP / 8), r = t * 8 + r8, d = (c % (DP / 8)) * 8;
-          float m = -INFINITY, all = 0.0f;
+        // ---- eight values of a row a thread; rows that an unseen value has spoilt first, if any is not finite
+        const int here = min(8, rows - t * 8) * (DP / 8);
+        auto total = [&](int r, float& m, float& all) {
+          m = -INFINITY;
+          all = 0.0f;
 #pragma unroll
           for (int v = 0; v < kConsumers; ++v)
             if (l_s[v][r] != 0.0f) m = fmaxf(m, m_s[v][r]);
 #pragma unroll
           for (int v = 0; v < kConsumers; ++v)
             if (l_s[v][r] != 0.0f) all += l_s[v][r] * exp2_approx(m_s[v][r] - reference_of(m));
+        };
+        auto place = [&](int r, long long& token, int& head) {   // where the result goes, as a piece or part (index of its row)
+          const int in = (row0 + r) / p.G;
+          token = w.r.q0 + in;
+          head = w.kh * p.G + (row0 + r) - in * p.G;
+          return x.all ? part_row(p, token, head) : static_cast<long long>(x.slot) * p.item_rows + r;
+        };
+        const bool final = x.all && p.prefix_splits == 0;
+        float* parts = x.all ? p.part_o : p.piece_o;
+        if (all_see < sees) {   // some row does not see some of these keys
+          for (int c = threadIdx.x; c < here; c += 32 * kConsumers) {
+            const int r8 = c / (DP / 8), d = (c % (DP / 8)) * 8;
+            float odd = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) odd = fmaf(sum_s[r8 * kSum + d + i], 0.0f, odd);
+            if (odd != 0.0f) atomicOr(&odd_s, 1u << r8);
+          }
+          consumer_sync();
+          const unsigned odd = odd_s;
+          if (odd != 0) {
+            for (int r8 = warp; r8 < 8; r8 += kConsumers) {
+              if (((odd >> r8) & 1u) == 0) continue;
+              const int r = t * 8 + r8;
+              float m, all;
+              total(r, m, all);
+              if (!(all > 0.0f && all < INFINITY)) continue;
+              long long token;
+              int head;
+              const long long at = place(r, token, head);
+              if (repair_row<DP>(p, w.b, w.kh, token, head, p.shared + x.lo * kKeys, min(sees, p.shared + x.hi * kKeys),
+                                 max(w.r.kv - w.r.n + (row0 + r) / p.G + 1, 0), m, 1.0f / all, 0, DP,
+                                 p.out + token * p.o_t + head * p.o_h, final ? nullptr : parts + at * DP) &&
+                  lane == 0)
+                atomicOr(&done_s, 1u << r8);
+            }
+            consumer_sync();
+          }
+        }
+        const unsigned done = done_s;
+        for (int c = threadIdx.x; c < here; c += 32 * kConsumers) {
+          const int r8 = c / (DP / 8), r = t * 8 + r8, d = (c % (DP / 8)) * 8;
+          float m, all;
+          total(r, m, all);
           float val[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) val[i] = sum_s[r8 * kSum + d + i];
-          const int in = (row0 + r) / p.G;
-          const long long token = w.r.q0 + in;
-          const int head = w.kh * p.G + (row0 + r) - in * p.G;
-          if (x.all && p.prefix_splits == 0) {
-            write_row8(p, token, head, d, m, all, val);
+          long long token;
+          int head;
+          const long long at = place(r, token, head);
+          if (final) {
+            if (((done >> r8) & 1u) == 0) write_row8(p, token, head, d, m, all, val);
+            else if (d == 0 && p.lse != nullptr) p.lse[token * p.Hq + head] = (reference_of(m) + log2f(all)) * kLn2;
           } else {
-            const long long at = x.all ? part_row(p, token, head) : static_cast<long long>(x.slot) * p.item_rows + r;
-            float4* to = reinterpret_cast<float4*>((x.all ? p.part_o : p.piece_o) + at * DP + d);
-            to[0] = make_float4(val[0], val[1], val[2], val[3]);
-            to[1] = make_float4(val[4], val[5], val[6], val[7]);
+            if (((done >> r8) & 1u) == 0) {
+              float4* to = reinterpret_cast<float4*>(parts + at * DP + d);
+              to[0] = make_float4(val[0], val[1], val[2], val[3]);
+              to[1] = make_float4(val[4], val[5], val[6], val[7]);
+            }
             if (d == 0) (x.all ? p.part_ml : p.piece_ml)[at] = make_float2(m, all);
           }
+        }
+        if (all_see < sees) {
+          consumer_sync();
+          if (threadIdx.x == 0) odd_s = done_s = 0;
         }
         consumer_sync();
       }

@@ -501,6 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
       const int first_unit = steps[at_step].first(k);
       const int tile_row = lead == 2 ? r : k * 128 + r;
       const int all = steps[at_step].all, slot = steps[at_step].slot;
+      const int request = steps[at_step].b, seen_here = steps[at_step].sees;
       int token, head, sees = 0;
       {
         const Step& t = steps[at_step];
@@ -672,6 +673,40 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
       if (wr < rows) {
         // Chunks of 32 columns; the next one's load is under way while one is written.
         const int chunks = pair ? DP / 64 : DP / 32;
+        // ---- rows that an unseen value has spoilt, if any is not finite (a sum of 0 times each result tells)
+        float odd = 0.0f;
+        const int key_hi = min(seen_here, key0 + hi * kKeys);
+        if (__any_sync(0xffffffffu, real && sees < key_hi)) {
+#pragma unroll 1
+          for (int c = 0; c < chunks; ++c) {
+            uint32_t x[32];
+            tmem_ld_x32(o_at + c_lo + c * 32, x);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) odd = use_mine ? fmaf(__uint_as_float(x[i]), 0.0f, odd) : odd;
+            if (pair) {
+              tmem_ld_x32(lanes + 256 + (k ^ 1) * DP + c_lo + c * 32, x);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) odd = use_other ? fmaf(__uint_as_float(x[i]), 0.0f, odd) : odd;
+            }
+          }
+        }
+        for (unsigned spoilt = __ballot_sync(0xffffffffu, real && odd != 0.0f && l > 0.0f && l < INFINITY); spoilt != 0;
+             spoilt &= spoilt - 1) {
+          const int of = __ffs(spoilt) - 1;
+          auto of_row = [&](auto x) { return __shfl_sync(0xffffffffu, x, of); };
+          const unsigned long long there = of_row(to);
+          const float sum = of_row(l);
+          if (!repair_row<DP>(p, request, of_row(head) / p.G, of_row(token), of_row(head), key0 + lo * kKeys,
+                              key_hi, of_row(sees), of_row(ref), 1.0f / sum, c_lo,
+                              pair ? DP / 2 : DP, reinterpret_cast<__nv_bfloat16*>(there),
+                              final ? nullptr : reinterpret_cast<float*>(there)))
+            continue;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if ((lane & ~3) + i == of) dst[i] = 0;   // written
+        }
         uint32_t own[32], mate[32];
         auto fetch = [&](int c) {
           __syncwarp();

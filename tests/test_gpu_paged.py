@@ -216,8 +216,8 @@ def _attention(handle, lens, Hq, Hk, D, page, seed=0, layout="heads", shared=0, 
     o, e, want, want_lse, tol, lse_tol = (t[~rowless] for t in (o, e, want, want_lse, tol, lse_tol))
     empty = want_lse == -math.inf
     assert (o[empty] == 0).all() and (e[empty] == -math.inf).all()
-    nan = torch.isnan(want)
-    assert torch.equal(nan, torch.isnan(o))
+    nan = ~torch.isfinite(want)   # (infinite or NaN, whatever comes of a value that is not finite)
+    assert torch.equal(nan, ~torch.isfinite(o))
     off = (o - want).abs()[~nan] - tol[~nan]
     assert off.numel() == 0 or off.max() <= 0, f"{off.max():.3g} past the bound, {(off > 0).sum()} values"
     ok = ~empty & ~torch.isnan(want_lse)
@@ -301,6 +301,23 @@ def test_attention_values_that_are_not_finite(handle, m, D):
                     kc[tables[row][i // 16], 0, i % 16, 0] = -math.inf
 
     _attention(handle, [(300, m), (40, m), (77, m)], 4, 1, D, 16, tamper=dead)
+
+
+@pytest.mark.parametrize("Hq,Hk,D,m", [(4, 1, 128, 4), (2, 2, 64, 9), (8, 1, 128, 40), (3, 3, 64, 300), (8, 1, 96, 17)])
+@pytest.mark.parametrize("bad", [NAN, math.inf, -math.inf])
+def test_attention_values_not_finite_stay_with_the_rows_that_see_them(handle, Hq, Hk, D, m, bad):
+    """A value that is not finite in the middle of the new tokens: rows in front of it are as without it."""
+    def spoil(q, kc, vc, tables):
+        for b, at in ((0, 700 - m // 2), (1, 333 - 1)):
+            vc[tables[b][at // 16], Hk - 1, at % 16, 5] = bad
+            vc[tables[b][at // 16], 0, at % 16, D - 1] = bad
+
+    lens = [(700, m), (333, m), (m + 60, m)]
+    _attention(handle, lens, Hq, Hk, D, 16, tamper=spoil)
+    _attention(handle, [(n + 1024, k) for n, k in lens], Hq, Hk, D, 16, shared=1024,
+               tamper=lambda q, kc, vc, tables: [vc.__setitem__((tables[0][(1724 - m // 2) // 16], 0, (1724 - m // 2) % 16, 3), bad)])
+    _attention(handle, [(9000, m)], Hq, Hk, D, 16,
+               tamper=lambda q, kc, vc, tables: [vc.__setitem__((tables[0][(9000 - m // 2) // 16], 0, (9000 - m // 2) % 16, 3), bad)])
 
 
 def test_attention_bad_pages_are_reported(handle):
