@@ -170,7 +170,7 @@ template <int DP>
 __global__ void __launch_bounds__(kTeams * DP / 8) attention_join_kernel(const __grid_constant__ AttentionParams p) {
   pdl_wait();
   pdl_trigger();
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && p.prefix_splits == 0) take_status(p);
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && p.alone) take_status(p);
   const PieceRecord c = p.records[blockIdx.x];
   if (c.pieces == 0) return;
   const int per_row = teams_per_row(c.pieces), at_once = kTeams / per_row;
@@ -232,28 +232,32 @@ cudaError_t launch_fold(const AttentionParams& p, int dp, cudaStream_t stream) {
 }
 
 // ---------------------------------------------------------------- workspace
-// The status word, then the records, then the pieces (2 slots a block), then the shared keys' part of each row.
+// The status word; records and pieces (2 slots a block) of the tiles' kernel, and of that for few rows; the parts of each
+// row where keys are shared.
 // Every part grows with T alone, so what is enough for T rows is enough for fewer.
 constexpr int kMaxSms = 160;   // blocks are a multiple of the GPU's 152
 constexpr int kPrefixSplits = 64, kPrefixBlocks = 2 * kMaxSms;
 constexpr size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 struct Workspace {
-  size_t records, ml, o, part_ml, part_o, bytes;
+  size_t records, ml, o, few_records, few_ml, few_o, part_ml, part_o, bytes;
 };
 int slot_rows(bool tiles, long long T, int G) {
   return static_cast<int>(std::min<long long>(tiles ? kTileRows : kFewRows, T * G));
 }
 Workspace workspace_for(int T, int Hq, int Hk, int D) {
   const int G = Hq / Hk, dp = D <= 64 ? 64 : 128;
-  const size_t slots = std::max<size_t>(2 * kFewPerSm * kMaxSms * slot_rows(false, T, G), 2 * kMaxSms * slot_rows(true, T, G));
+  const size_t slots = 2 * kMaxSms * slot_rows(true, T, G), few = 2 * kFewPerSm * kMaxSms * slot_rows(false, T, G);
   // rows x (splits of the shared keys' launch and one): splits <= kPrefixBlocks / items + 1, rows <= 256 items
   const size_t rows = static_cast<size_t>(T) * Hq;
   const size_t parts = std::min<size_t>(kPrefixSplits * rows, kPrefixBlocks * kTileRows + rows) + rows;
   Workspace w;
   w.records = 256;
-  w.ml = w.records + round256(sizeof(PieceRecord) * kFewPerSm * kMaxSms);
+  w.ml = w.records + round256(sizeof(PieceRecord) * kMaxSms);
   w.o = w.ml + round256(sizeof(float2) * slots);
-  w.part_ml = w.o + round256(sizeof(float) * slots * dp);
+  w.few_records = w.o + round256(sizeof(float) * slots * dp);
+  w.few_ml = w.few_records + round256(sizeof(PieceRecord) * kFewPerSm * kMaxSms);
+  w.few_o = w.few_ml + round256(sizeof(float2) * few);
+  w.part_ml = w.few_o + round256(sizeof(float) * few * dp);
   w.part_o = w.part_ml + round256(sizeof(float2) * parts);
   w.bytes = w.part_o + round256(sizeof(float) * parts * dp);
   return w;
@@ -381,6 +385,8 @@ extern "C" moe_lora_status moe_lora_attention(moe_lora_handle* h, const moe_lora
   p.flags = reinterpret_cast<int*>(h->linear_flags + kLinearFlags);
   p.prefix_splits = 0;
   p.records = nullptr;
+  p.piece_ml = nullptr;
+  p.piece_o = nullptr;
   ML_ON_DEVICE(h);
   if (!fast_layout(a) || p.scale_log2 == 0.0f || h->num_sms > kMaxSms) {
     ML_CUDA(cudaMemsetAsync(workspace, 0, 4, stream), "attention status");
@@ -399,53 +405,78 @@ extern "C" moe_lora_status moe_lora_attention(moe_lora_handle* h, const moe_lora
   while ((1 << p.page_log2) < p.page) ++p.page_log2;
   const Workspace at = workspace_for(p.T, p.Hq, p.Hk, p.D);
   uint8_t* base = static_cast<uint8_t*>(workspace);
-  p.piece_ml = reinterpret_cast<float2*>(base + at.ml);
-  p.piece_o = reinterpret_cast<float*>(base + at.o);
   p.part_ml = reinterpret_cast<float2*>(base + at.part_ml);
   p.part_o = reinterpret_cast<float*>(base + at.part_o);
   p.shared = a->B > 1 ? a->shared_len / kTileKeys * kTileKeys : 0;   // the rest is each request's own
   p.both_halves = p.D == 128;   // (fewer values would be read past)
-  auto maps = [&](int keys, bool both) {
-    return page_map(h, &p.tmap_k, p.k, p, p.k_t, p.k_h, p.k_p, keys, both) &&
-           page_map(h, &p.tmap_v, p.v, p, p.v_t, p.v_h, p.v_p, keys, both);
+  auto maps = [&](AttentionParams& x, int keys, bool both) {
+    return page_map(h, &x.tmap_k, x.k, x, x.k_t, x.k_h, x.k_p, keys, both) &&
+           page_map(h, &x.tmap_v, x.v, x, x.v_t, x.v_h, x.v_p, keys, both);
   };
+  // Requests of up to 8 rows a key head (16, where the heads alone are more than 8) run on the kernel for few rows, the
+  // others on tiles; in a batch that may have both, each kernel takes its own.  (32 single tokens and 512 of a
+  // prompt, 2000 keys each: 71 us with all of them on tiles.)
   const bool tiles = static_cast<long long>(a->max_query_len) * p.G > kFewRows;
-  if ((tiles || p.shared > 0) && !maps(kTileKeys, false)) return cuda_fail(cudaErrorInvalidValue, "attention tensor maps");
+  const bool mixed = tiles && a->B > 1 && p.offsets != nullptr && static_cast<long long>(a->max_query_len) * a->B != p.T;
+  const bool eight = mixed ? p.G <= 8 : static_cast<long long>(a->max_query_len) * p.G <= 8;
+  const long long own_keys = static_cast<long long>(p.width) * p.page - p.shared;   // of a request, at most
+  AttentionParams few = p;
+  if ((tiles || p.shared > 0) && !maps(p, kTileKeys, false)) return cuda_fail(cudaErrorInvalidValue, "attention tensor maps");
+  if ((!tiles || mixed) && !maps(few, kFewKeys, p.both_halves)) return cuda_fail(cudaErrorInvalidValue, "attention tensor maps");
+  auto plan_few = [&](AttentionParams& x, int ctas, int least, int whole_keys, int rows, int keys) {
+    x.plan.ctas = ctas;
+    x.plan.least = least;
+    x.plan.whole = own_keys <= whole_keys;
+    const long long items = (static_cast<long long>(p.T) * p.G / rows + p.B) * p.Hk, most = own_keys / keys + 1 + kTileOver;
+    x.plan.few = p.B <= 32 && !x.long_queries && items * most < (1LL << 30);
+  };
+  p.follows = few.follows = 0;
+  p.alone = few.alone = 0;
+  p.few_rows = few.few_rows = 0;
   if (p.shared > 0) {
     const PrefixRun run = prefix_run(p.T, p.G, p.Hk, p.shared, h->num_sms);
     const long long blocks = static_cast<long long>(run.row_tiles) * p.Hk * run.splits;
     if (blocks > 0x7fffffff) return MOE_LORA_ERR_UNSUPPORTED;
     p.plan = Plan{};
     ML_LAUNCH(h, launch_attention_tiles(p, run, static_cast<int>(blocks), dp, stream), "attention prefix launch");
-    p.prefix_splits = run.splits;
+    p.prefix_splits = few.prefix_splits = run.splits;
+    p.follows = few.follows = 1;
   }
-  p.item_rows = slot_rows(tiles, p.T, p.G);
-  const long long own_keys = static_cast<long long>(p.width) * p.page - p.shared;   // of a request, at most
-  int join_across;
+  const bool fold = p.prefix_splits > 0;
+  p.item_rows = slot_rows(true, p.T, p.G);
+  p.long_queries = static_cast<long long>(a->max_query_len) * p.G > 8LL * kTileRows;
+  plan_few(p, h->num_sms, 2, 4 * kTileKeys, kTileRows, kTileKeys);
+  p.piece_ml = reinterpret_cast<float2*>(base + at.ml);
+  p.piece_o = reinterpret_cast<float*>(base + at.o);
+  p.records = p.plan.whole ? nullptr : reinterpret_cast<PieceRecord*>(base + at.records);
+  few.item_rows = slot_rows(false, p.T, p.G);
+  few.long_queries = 0;
+  plan_few(few, kFewPerSm * h->num_sms, 2, 8 * kFewKeys, 8, kFewKeys);
+  few.piece_ml = reinterpret_cast<float2*>(base + at.few_ml);
+  few.piece_o = reinterpret_cast<float*>(base + at.few_o);
+  few.records = few.plan.whole ? nullptr : reinterpret_cast<PieceRecord*>(base + at.few_records);
+  const bool join_tiles = tiles && !p.plan.whole, join_few = (!tiles || mixed) && !few.plan.whole;
+  if (mixed) {
+    few.few_rows = eight ? 8 : kFewRows;
+    p.few_rows = -few.few_rows;
+  }
   if (tiles) {
-    p.plan.ctas = h->num_sms;
-    p.plan.least = 2;
-    p.plan.whole = own_keys <= 2LL * kTileKeys;
-    p.long_queries = static_cast<long long>(a->max_query_len) * p.G > 8LL * kTileRows;
-    join_across = (p.item_rows + kTeams - 1) / kTeams;
-  } else {
-    if (!maps(kFewKeys, p.both_halves)) return cuda_fail(cudaErrorInvalidValue, "attention tensor maps");
-    p.plan.ctas = kFewPerSm * h->num_sms;
-    p.plan.least = 2;
-    p.plan.whole = own_keys <= 8LL * kFewKeys;
-    p.long_queries = 0;
-    join_across = std::min(4, p.item_rows);
+    p.alone = !mixed && !join_tiles && !fold;
+    ML_LAUNCH(h, launch_attention_tiles(p, PrefixRun{}, p.plan.ctas, dp, stream), "attention launch");
   }
-  if (!p.plan.whole) p.records = reinterpret_cast<PieceRecord*>(base + at.records);
-  {
-    const int rows = tiles ? kTileRows : 8, keys = tiles ? kTileKeys : kFewKeys;
-    const long long items = (static_cast<long long>(p.T) * p.G / rows + p.B) * p.Hk, most = own_keys / keys + 1 + kTileOver;
-    p.plan.few = p.B <= 32 && !p.long_queries && items * most < (1LL << 30);
+  if (!tiles || mixed) {
+    few.follows = few.follows || tiles;
+    few.alone = !join_tiles && !join_few && !fold;
+    ML_LAUNCH(h, launch_attention_rows(few, dp, eight, stream), "attention launch");
   }
-  ML_LAUNCH(h, tiles ? launch_attention_tiles(p, PrefixRun{}, p.plan.ctas, dp, stream)
-                     : launch_attention_rows(p, dp, static_cast<long long>(a->max_query_len) * p.G <= 8, stream),
-            "attention launch");
-  if (!p.plan.whole) ML_LAUNCH(h, launch_join(p, dp, join_across, stream), "attention join launch");
-  if (p.prefix_splits > 0) ML_LAUNCH(h, launch_fold(p, dp, stream), "attention fold launch");
+  if (join_tiles) {
+    p.alone = !join_few && !fold;
+    ML_LAUNCH(h, launch_join(p, dp, (p.item_rows + kTeams - 1) / kTeams, stream), "attention join launch");
+  }
+  if (join_few) {
+    few.alone = !fold;
+    ML_LAUNCH(h, launch_join(few, dp, std::min(4, few.item_rows), stream), "attention join launch");
+  }
+  if (fold) ML_LAUNCH(h, launch_fold(p, dp, stream), "attention fold launch");
   return MOE_LORA_OK;
 }

@@ -41,6 +41,9 @@ struct AttentionParams {
   int T, B, Hq, Hk, G, D;
   int num_pages, page, page_log2, width;
   int shared;                                  // keys that are read from request 0's table
+  int few_rows;                                // > 0: requests of up to so many rows a key head alone, < 0: the others
+  int follows;                                 // the kernel in front is one of this call whose results are not needed
+  int alone;                                   // no other kernel of the call follows: it writes the status word
   int long_queries;                            // requests have many items each
   int both_halves;                             // the maps have both halves of a key in a box (tma_load_page2)
   float scale_log2;                            // scale * log2(e): weights are powers of two
@@ -142,7 +145,9 @@ struct Schedule {
     return max(r.kv - r.n + last / p.G + 1, 0);
   }
   static MLDEV int items_of(const AttentionParams& p, const Request& r) {
-    return (r.n * p.G + ROWS - 1) / ROWS;
+    const int rows = r.n * p.G;
+    if (p.few_rows != 0 && (rows <= abs(p.few_rows)) != (p.few_rows > 0)) return 0;   // another kernel's
+    return (rows + ROWS - 1) / ROWS;
   }
 
   // The block whose run has u, and where a block's run starts (in 32 bits where that is enough: a division of
@@ -166,18 +171,28 @@ struct Walk {
   long long u0;                 // of all items before it
   Request r;
 
-  MLDEV void enter(const AttentionParams& p) {   // the first item of request b, or of one behind it that has any
+  // The first item of request b, or of one behind it that has any (32 looked at together; a whole warp).
+  MLDEV void enter(const AttentionParams& p) {
+    const int lane = threadIdx.x & 31;
     while (b < p.B) {
+      const int n = b + lane < p.B ? S::items_of(p, request_of(p, b + lane)) : 0;
+      const unsigned any = __ballot_sync(0xffffffffu, n > 0);
+      if (any == 0) {
+        b += 32;
+        continue;
+      }
+      const int at = __ffs(any) - 1;
+      b += at;
+      items = __shfl_sync(0xffffffffu, n, at);
       r = request_of(p, b);
-      items = S::items_of(p, r);
-      if (items > 0) break;
-      ++b;
+      units = S::weight_of(p, r, 0);
+      break;
     }
     kh = i = 0;
-    if (b < p.B) units = S::weight_of(p, r, 0);
   }
-  MLDEV void next(const AttentionParams& p) {
+  MLDEV void next(const AttentionParams& p, long long end) {   // (behind `end` nothing is looked up any more)
     u0 += units;
+    if (u0 >= end) return;
     if (++i == items) {
       i = 0;
       if (++kh == p.Hk) {
@@ -542,7 +557,7 @@ struct PrefixRun {
 
 // Launches (attention_rows.cu, attention_tiles.cu)
 constexpr int kFewRows = 16, kFewKeys = 64, kFewPerSm = 2, kFewOver = 1;
-constexpr int kTileRows = 256, kTileKeys = 128, kTileOver = 2;
+constexpr int kTileRows = 256, kTileKeys = 128, kTileOver = 4;
 cudaError_t prepare_attention_rows();
 cudaError_t launch_attention_rows(const AttentionParams& p, int dp, bool eight, cudaStream_t stream);   // items of 8 rows, or 16
 cudaError_t prepare_attention_tiles();

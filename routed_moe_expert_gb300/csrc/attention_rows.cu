@@ -96,9 +96,8 @@ __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(con
     tma_prefetch_desc(&p.tmap_v);
   }
   __syncthreads();
-  // With shared keys the kernel in front is their launch, whose results are not needed here; what came before
-  // it is done, since it has waited for that.
-  if (p.prefix_splits == 0) pdl_wait();
+  // Where the kernel in front is another of this call, what came before that one is done, since it has waited for it.
+  if (!p.follows) pdl_wait();
   pdl_trigger();
 
   Sched s;
@@ -111,7 +110,7 @@ __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(con
     const int boxes = kKeys >> box_log2;   // of a unit
     int stage = 0, ok = 1;
     uint32_t phase = 0, issued = 0, parity = 0;
-    for (; ok && more<kRows, kKeys, kFewOver>(s, w, p); w.next(p)) {
+    for (; ok && more<kRows, kKeys, kFewOver>(s, w, p); w.next(p, s.end)) {
       const Part x = part_of<kRows, kKeys, kFewOver>(p, s, w, cta);
       if (x.lo >= x.hi) continue;
       const int sees = Sched::seen_by(p, w.r, w.i);
@@ -175,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(con
     int stage = 0, ok = 1;
     uint32_t phase = 0;
     bool started = false;   // an item whose rest is other blocks'
-    for (; ok && more<kRows, kKeys, kFewOver>(s, w, p); w.next(p)) {
+    for (; ok && more<kRows, kKeys, kFewOver>(s, w, p); w.next(p, s.end)) {
       const Part x = part_of<kRows, kKeys, kFewOver>(p, s, w, cta);
       if (x.lo >= x.hi) continue;
       const int row0 = w.i * kRows;
@@ -438,9 +437,9 @@ __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(con
     }
     if (!started && threadIdx.x == 0 && p.records != nullptr) p.records[cta].pieces = 0;
   }
-  if (p.prefix_splits > 0) pdl_wait();   // not to end before the launch in front, which the next one reads from
+  if (p.follows) pdl_wait();   // not to end before it: what comes next reads its results, too
   __syncthreads();
-  if (threadIdx.x == 0) finish_status(p, error_s, p.records == nullptr && p.prefix_splits == 0);
+  if (threadIdx.x == 0) finish_status(p, error_s, p.alone);
 }
 
 }  // namespace

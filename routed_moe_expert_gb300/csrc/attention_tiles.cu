@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_s, 0);
-  if (p.prefix_splits == 0 || prefix.splits > 0) pdl_wait();   // (as in attention_rows.cu)
+  if (!p.follows) pdl_wait();   // (as in attention_rows.cu)
   pdl_trigger();
 
   Sched s;
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
           t.all = 0;
           t.slot = split;
         } else {
-          if (!first) w.next(p);
+          if (!first) w.next(p, s.end);
           Part x;
           while (true) {
             if (!more<kRows, kKeys, kTileOver>(s, w, p)) {
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
             }
             x = part_of<kRows, kKeys, kTileOver>(p, s, w, cta);
             if (x.lo < x.hi) break;
-            w.next(p);
+            w.next(p, s.end);
           }
           if (t.end == 0) {
             t.sees = Sched::seen_by(p, w.r, w.i);
@@ -496,29 +496,35 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
         step_read();
         break;
       }
-      const int lo = steps[at_step].lo, hi = steps[at_step].hi(k), lead = steps[at_step].lead, rows = steps[at_step].rows(k);
-      const int hi_other = steps[at_step].hi(k ^ 1);
-      const int first_unit = steps[at_step].first(k);
-      const int tile_row = lead == 2 ? r : k * 128 + r;
-      const int all = steps[at_step].all, slot = steps[at_step].slot;
-      const int request = steps[at_step].b, seen_here = steps[at_step].sees;
-      int token, head, sees = 0;
-      {
-        const Step& t = steps[at_step];
-        const int row = t.row0 + tile_row;   // of the request and key head
+      // What the units need; the rest is looked up behind them, since registers are short there.
+      const int step_at = at_step;
+      const int lo = steps[step_at].lo, hi = steps[step_at].hi(k), lead = steps[step_at].lead, rows = steps[step_at].rows(k);
+      const int first_unit = steps[step_at].first(k);
+      auto row_token = [&](int& head) {   // this thread's row: its token, and head
+        const Step& t = steps[step_at];
+        const int row = t.row0 + (lead == 2 ? r : k * 128 + r);   // of the request and key head
         const int token_in = row / p.G;
         head = t.kh * p.G + row - token_in * p.G;
-        token = t.q0 + token_in;
+        return t.q0 + token_in;
+      };
+      int sees = 0;
+      {
+        const Step& t = steps[step_at];
+        int head;
+        const int token = row_token(head);
         if (r < rows) {
           if (prefix.splits > 0) sees = min(max(keys_of_token(p, token), 0), t.sees);
-          else sees = max(t.kv - t.n + token_in + 1, 0);
+          else sees = max(t.kv - t.n + (token - t.q0) + 1, 0);
         }
         if (!asked && first_unit < hi) {
           fetch_queries(t);
           queries_there();
         }
       }
-      step_read();
+      if (++at_step == kSteps) {
+        at_step = 0;
+        step_phase ^= 1u;
+      }
       asked = false;
       // The next part's query rows, once the tile's last scores are there: they are what still reads these.
       auto fetch_next = [&]() {
@@ -553,15 +559,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
           bool renew = j == first_unit;   // the row's reference, and rarely a new one
           for (int tries = 0;; ++tries) {
             if (tries > 0 || j == first_unit) {   // (in loops: this is one unit's work, and its code waits to be fetched)
-              float top = -INFINITY;
+              float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-              for (int c = 0; c < kKeys; c += 16) {
-                uint32_t x[16];
-                tmem_ld_x16(s_at + c, x);
+              for (int c = 0; c < kKeys; c += 32) {
+                uint32_t x[32];
+                tmem_ld_x32(s_at + c, x);
                 tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) top = fmaxf(top, c + i < limit ? __uint_as_float(x[i]) * scale : -INFINITY);
+                for (int i = 0; i < 32; ++i)
+                  tops[i & 3] = fmaxf(tops[i & 3], c + i < limit ? __uint_as_float(x[i]) * scale : -INFINITY);
               }
+              const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
               const bool grow = renew && top > ref;
               const float f = grow ? exp2_approx(ref - top) : 1.0f;
               if (grow) ref = top;
@@ -624,6 +632,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
         tc_fence_after();
       }
       if (*abort_flag != 0) break;
+      const int hi_other = steps[step_at].hi(k ^ 1), all = steps[step_at].all, slot = steps[step_at].slot;
+      const int request = steps[step_at].b, seen_here = steps[step_at].sees;
+      const int tile_row = lead == 2 ? r : k * 128 + r;
+      int head;
+      const int token = row_token(head);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&step_empty[step_at]);
       // ---- with the same rows in both tiles: the other tile's maximum and sum, and half of the columns each
       const bool pair = lead == 2;
       float other = 0.0f, mine = 1.0f;   // factors of the other tile's result and this one's
@@ -677,20 +692,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
         float odd = 0.0f;
         const int key_hi = min(seen_here, key0 + hi * kKeys);
         if (__any_sync(0xffffffffu, real && sees < key_hi)) {
+          float odds[4] = {};
 #pragma unroll 1
-          for (int c = 0; c < chunks; ++c) {
+          for (int c = 0; c < (pair ? 2 : 1) * chunks; ++c) {
+            const bool mates = c >= chunks;
             uint32_t x[32];
-            tmem_ld_x32(o_at + c_lo + c * 32, x);
+            tmem_ld_x32((mates ? lanes + 256 + (k ^ 1) * DP + (c - chunks) * 32 : o_at + c * 32) + c_lo, x);
             tmem_ld_wait();
+            const bool used = mates ? use_other : use_mine;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) odd = use_mine ? fmaf(__uint_as_float(x[i]), 0.0f, odd) : odd;
-            if (pair) {
-              tmem_ld_x32(lanes + 256 + (k ^ 1) * DP + c_lo + c * 32, x);
-              tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < 32; ++i) odd = use_other ? fmaf(__uint_as_float(x[i]), 0.0f, odd) : odd;
-            }
+            for (int i = 0; i < 32; ++i) odds[i & 3] = used ? fmaf(__uint_as_float(x[i]), 0.0f, odds[i & 3]) : odds[i & 3];
           }
+          odd = (odds[0] + odds[1]) + (odds[2] + odds[3]);
         }
         for (unsigned spoilt = __ballot_sync(0xffffffffu, real && odd != 0.0f && l > 0.0f && l < INFINITY); spoilt != 0;
              spoilt &= spoilt - 1) {
@@ -711,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
         auto fetch = [&](int c) {
           __syncwarp();
           tmem_ld_x32(o_at + c_lo + c * 32, own);   // (whatever is there, if the tile had no unit)
-          tmem_ld_x32(lanes + 256 + (k ^ 1) * DP + c_lo + c * 32, mate);
+          if (pair) tmem_ld_x32(lanes + 256 + (k ^ 1) * DP + c_lo + c * 32, mate);
         };
         fetch(0);
 #pragma unroll 1
@@ -773,14 +786,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
     asm volatile("cp.async.wait_group 0;" ::: "memory");
   }
 
-  if (p.prefix_splits > 0 && prefix.splits == 0) pdl_wait();
+  if (p.follows) pdl_wait();
   tc_fence_before();
   __syncthreads();
   if (warp == kMma) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  if (threadIdx.x == 0) finish_status(p, error_s, p.records == nullptr && p.prefix_splits == 0 && prefix.splits == 0);
+  if (threadIdx.x == 0) finish_status(p, error_s, p.alone);
 }
 
 }  // namespace
