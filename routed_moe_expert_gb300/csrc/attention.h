@@ -45,6 +45,8 @@ struct AttentionParams {
   int follows;                                 // the kernel in front is one of this call whose results are not needed
   int alone;                                   // no other kernel of the call follows: it writes the status word
   int long_queries;                            // requests have many items each
+  int out_wide;                                // rows of `out` start on 32-byte boundaries
+  int in_place;                                // `out` is q
   int both_halves;                             // the maps have both halves of a key in a box (tma_load_page2)
   float scale_log2;                            // scale * log2(e): weights are powers of two
   Plan plan;

@@ -86,20 +86,17 @@ MLDEV float2 add2(float2 a, float2 b) {
   return r;
 }
 
-// Transposes the 4 x 4 pieces of four neighbouring lanes: piece i of lane q becomes piece q of lane i.
-MLDEV void trade(uint4 (&x)[4], int lane) {
-  auto swap = [&](uint4& a, uint4& b, int mask, bool upper) {   // lanes apart by `mask`: a of the upper for b of the lower
-    uint4 give = upper ? a : b;
-    give.x = __shfl_xor_sync(0xffffffffu, give.x, mask);
-    give.y = __shfl_xor_sync(0xffffffffu, give.y, mask);
-    give.z = __shfl_xor_sync(0xffffffffu, give.z, mask);
-    give.w = __shfl_xor_sync(0xffffffffu, give.w, mask);
-    (upper ? a : b) = give;
-  };
-  swap(x[0], x[1], 1, lane & 1);
-  swap(x[2], x[3], 1, lane & 1);
-  swap(x[0], x[2], 2, lane & 2);
-  swap(x[1], x[3], 2, lane & 2);
+// 32 bytes of a thread's row: whole sectors, where the address allows (`wide`), else two pieces of 16.  (Four lanes trading
+// pieces, so that a warp wrote longer runs, took twice the time of this.)
+MLDEV void st_row16(unsigned long long at, const uint32_t (&x)[8], bool wide, bool first, bool second) {
+  if (wide && second) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]),
+                 "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                 : "memory");
+    return;
+  }
+  if (first) *reinterpret_cast<uint4*>(at) = make_uint4(x[0], x[1], x[2], x[3]);
+  if (second) *reinterpret_cast<uint4*>(at + 16) = make_uint4(x[4], x[5], x[6], x[7]);
 }
 
 // A part of an item as every role sees it, made by the scheduling warp.
@@ -669,105 +666,91 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
       const long long at = prefix.splits > 0 ? (static_cast<long long>(slot) * p.T + token) * p.Hq + head
                            : all             ? part_row(p, token, head)
                                              : static_cast<long long>(slot) * p.item_rows + tile_row;
-      // Results leave 64 bytes of a row at a time, four lanes having traded their rows' quarters, so that a warp
-      // writes whole pieces: a thread a row would touch 32 rows a store.
       float* piece_o = by_token ? p.part_o : p.piece_o;
-      unsigned long long to = 0;
+      unsigned long long to = 0;   // the row's result
       if (real)
         to = final ? reinterpret_cast<unsigned long long>(p.out + token * p.o_t + head * p.o_h)
                    : reinterpret_cast<unsigned long long>(piece_o + at * DP);
-      unsigned long long dst[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) dst[i] = __shfl_sync(0xffffffffu, to, (lane & ~3) + i);
       if (final) {
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         mine *= inv;
         other *= inv;
       }
-      const bool none = l == 0.0f;  // a row that sees nothing, or whose every score is -inf
       if (wr < rows) {
-        // Chunks of 32 columns; the next one's load is under way while one is written.
-        const int chunks = pair ? DP / 64 : DP / 32;
-        // ---- rows that an unseen value has spoilt, if any is not finite (a sum of 0 times each result tells)
-        float odd = 0.0f;
+        const int chunks = pair ? DP / 64 : DP / 32;   // of 32 columns
         const int key_hi = min(seen_here, key0 + hi * kKeys);
-        if (__any_sync(0xffffffffu, real && sees < key_hi)) {
-          float odds[4] = {};
-#pragma unroll 1
-          for (int c = 0; c < (pair ? 2 : 1) * chunks; ++c) {
-            const bool mates = c >= chunks;
-            uint32_t x[32];
-            tmem_ld_x32((mates ? lanes + 256 + (k ^ 1) * DP + (c - chunks) * 32 : o_at + c * 32) + c_lo, x);
-            tmem_ld_wait();
-            const bool used = mates ? use_other : use_mine;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) odds[i & 3] = used ? fmaf(__uint_as_float(x[i]), 0.0f, odds[i & 3]) : odds[i & 3];
+        // Rows that a value which they do not see has spoilt; `odd` is a sum of 0 times each of a row's results.
+        auto repair = [&](float odd) {
+          bool written = false;
+          for (unsigned spoilt = __ballot_sync(0xffffffffu, real && odd != 0.0f && sees < key_hi && l > 0.0f && l < INFINITY);
+               spoilt != 0; spoilt &= spoilt - 1) {
+            const int of = __ffs(spoilt) - 1;
+            auto of_row = [&](auto x) { return __shfl_sync(0xffffffffu, x, of); };
+            const unsigned long long there = of_row(to);
+            const float sum = of_row(l);
+            const bool done = repair_row<DP>(p, request, of_row(head) / p.G, of_row(token), of_row(head), key0 + lo * kKeys, key_hi,
+                                             of_row(sees), of_row(ref), 1.0f / sum, c_lo, pair ? DP / 2 : DP,
+                                             reinterpret_cast<__nv_bfloat16*>(there), final ? nullptr : reinterpret_cast<float*>(there));
+            if (lane == of) written = done;
           }
-          odd = (odds[0] + odds[1]) + (odds[2] + odds[3]);
-        }
-        for (unsigned spoilt = __ballot_sync(0xffffffffu, real && odd != 0.0f && l > 0.0f && l < INFINITY); spoilt != 0;
-             spoilt &= spoilt - 1) {
-          const int of = __ffs(spoilt) - 1;
-          auto of_row = [&](auto x) { return __shfl_sync(0xffffffffu, x, of); };
-          const unsigned long long there = of_row(to);
-          const float sum = of_row(l);
-          if (!repair_row<DP>(p, request, of_row(head) / p.G, of_row(token), of_row(head), key0 + lo * kKeys,
-                              key_hi, of_row(sees), of_row(ref), 1.0f / sum, c_lo,
-                              pair ? DP / 2 : DP, reinterpret_cast<__nv_bfloat16*>(there),
-                              final ? nullptr : reinterpret_cast<float*>(there)))
-            continue;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if ((lane & ~3) + i == of) dst[i] = 0;   // written
-        }
+          return written;
+        };
         uint32_t own[32], mate[32];
         auto fetch = [&](int c) {
           __syncwarp();
           tmem_ld_x32(o_at + c_lo + c * 32, own);   // (whatever is there, if the tile had no unit)
           if (pair) tmem_ld_x32(lanes + 256 + (k ^ 1) * DP + c_lo + c * 32, mate);
         };
+        auto result = [&](int i) {
+          const float o = use_mine ? __uint_as_float(own[i]) * mine : 0.0f;
+          return use_other ? fmaf(__uint_as_float(mate[i]), other, o) : o;
+        };
+        bool write = real;
+        if (p.in_place && final) {   // the query row is needed for the repair, and gone afterwards
+          float odd = 0.0f;
+#pragma unroll 1
+          for (int c = 0; c < chunks; ++c) {
+            fetch(c);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) odd = fmaf(result(i), 0.0f, odd);
+          }
+          if (repair(odd)) write = false;
+        }
+        float odds[4] = {};
         fetch(0);
 #pragma unroll 1
-        for (int c = 0; c < chunks; ++c) {
+        for (int c = 0; c < chunks; ++c) {   // the next chunk's load is under way while one is written
           float o[32];
           tmem_ld_wait();
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            o[i] = use_mine ? __uint_as_float(own[i]) * mine : 0.0f;
-            o[i] = use_other ? fmaf(__uint_as_float(mate[i]), other, o[i]) : o[i];
+            o[i] = result(i);
+            odds[i & 3] = fmaf(o[i], 0.0f, odds[i & 3]);
           }
           if (c + 1 < chunks) fetch(c + 1);
           const int col = c_lo + c * 32;
-          const int part = lane & 3;
-          auto leave = [&](uint4 (&x)[4], int bytes, bool inside) {   // 64 bytes of every row
-            trade(x, lane);   // now x[i] is quarter `part` of the row of lane (lane & ~3) + i
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (dst[i] != 0 && inside) *reinterpret_cast<uint4*>(dst[i] + bytes + 16 * part) = x[i];
-          };
-          uint4 x[4];
+          uint32_t x[8];
           if (final) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float e[8] = {o[8 * i],     o[8 * i + 1], o[8 * i + 2], o[8 * i + 3],
-                                  o[8 * i + 4], o[8 * i + 5], o[8 * i + 6], o[8 * i + 7]};
-              x[i] = pack8(e);
-              if (none) x[i] = make_uint4(0, 0, 0, 0);
+            for (int i = 0; i < 32; i += 16) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(o[i + 2 * e], o[i + 2 * e + 1]);
+                x[e] = l == 0.0f ? 0u : *reinterpret_cast<const uint32_t*>(&h);   // nothing is seen, or nothing weighs
+              }
+              if (write) st_row16(to + 2 * (col + i), x, p.out_wide, col + i < p.D, col + i + 8 < p.D);
             }
-            leave(x, 2 * col, col + part * 8 < p.D);
           } else {
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
+            for (int i = 0; i < 32; i += 8) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int at4 = half * 16 + 4 * i;
-                x[i] = make_uint4(__float_as_uint(o[at4]), __float_as_uint(o[at4 + 1]), __float_as_uint(o[at4 + 2]),
-                                  __float_as_uint(o[at4 + 3]));
-              }
-              leave(x, 4 * (col + half * 16), true);
+              for (int e = 0; e < 8; ++e) x[e] = __float_as_uint(o[i + e]);
+              if (write) st_row16(to + 4 * (col + i), x, true, true, true);
             }
           }
         }
+        if (!(p.in_place && final)) repair((odds[0] + odds[1]) + (odds[2] + odds[3]));
       }
       if (real && c_lo == 0) {
         if (!final) (by_token ? p.part_ml : p.piece_ml)[at] = make_float2(ref, l);

@@ -320,6 +320,22 @@ def test_attention_values_not_finite_stay_with_the_rows_that_see_them(handle, Hq
                tamper=lambda q, kc, vc, tables: [vc.__setitem__((tables[0][(9000 - m // 2) // 16], 0, (9000 - m // 2) % 16, 3), bad)])
 
 
+def test_attention_spoilt_rows_in_place(handle):
+    """The same with the result over the queries, which the rows in front of the bad value are worked out from again."""
+    g = torch.Generator(device="cuda").manual_seed(4)
+    for m in (4, 100):
+        q = torch.randn((m, 4, 64), generator=g, device="cuda").bfloat16()
+        kc, vc = (torch.randn((40, 2, 16, 64), generator=g, device="cuda").bfloat16() for _ in range(2))
+        table = torch.randperm(40, generator=g, device="cuda").to(I32)[None, :20]
+        clean = pkg.moe_lora_attention(handle, q, kc, vc, table, ints([300]), ints([0, m]))
+        at = 300 - m // 2
+        vc[int(table[0, at // 16]), :, at % 16, 7] = math.inf
+        got = pkg.moe_lora_attention(handle, q, kc, vc, table, ints([300]), ints([0, m]), out=q)
+        assert got is q
+        near = (got[:m // 2].float() - clean[:m // 2].float()).abs() <= 2.0 ** -6 * clean[:m // 2].float().abs() + 2.0 ** -7
+        assert near.all() and not torch.isfinite(got[m // 2:, :, 7].float()).any()
+
+
 def test_attention_bad_pages_are_reported(handle):
     """A page outside the cache is read as zeros and reported; nothing outside is touched."""
     for m, Hq in ((1, 4), (30, 8)):
