@@ -2,7 +2,8 @@
 
   merged q/k/v projection with per-token adapters  (moe_lora_linear)
   norm of q and k heads and position rotation       (moe_lora_qk_norm_rope, in place on the rows)
-  attention                                          (the caller's; plain torch here)
+  attention over the cache of the requests           (moe_lora_page_tables, moe_lora_cache_write, moe_lora_attention;
+                                                      without a cache, over this call's tokens in plain torch)
   output projection with adapters                    (moe_lora_linear)
   router logits in float32                           (moe_lora_linear)
   choice of experts, packed                          (moe_lora_select_experts)
@@ -34,6 +35,31 @@ class Shape:
     n_group: int = 8
     topk_group: int = 4
     max_positions: int = 4096
+
+
+class Cache:
+    """The pages of a block's keys and values, and the requests that have them: what a serving program keeps
+    from step to step.  One step's tables, slots and positions serve all of a model's blocks."""
+
+    def __init__(self, handle, shape, requests, pages, page_size=16, max_pages=64, device="cuda"):
+        self.handle, self.page_size, self.max_tokens = handle, page_size, max_pages * page_size
+        size = (pages, shape.k_heads, page_size, shape.head_dim)
+        self.k, self.v = (torch.zeros(size, dtype=torch.bfloat16, device=device) for _ in range(2))
+        self.tables = torch.full((requests, max_pages), -1, dtype=torch.int32, device=device)
+        self.lens = torch.zeros(requests, dtype=torch.int32, device=device)
+        self.free = torch.arange(pages, dtype=torch.int32, device=device)
+        self.taken = torch.zeros(1, dtype=torch.int32, device=device)
+
+    def step(self, new_lens, tokens):
+        """Room for new_lens [requests] tokens in a batch of `tokens` rows; lengths and cursor go on in place."""
+        self.plan = pkg.moe_lora_page_tables(self.handle, self.tables, self.lens, new_lens, self.page_size, self.free, self.taken,
+                                             tokens, outputs={"kv_lens": self.lens, "taken": self.taken})
+        return self.plan["positions"]
+
+    def attention(self, q, k, v, max_query_len):
+        pkg.moe_lora_cache_write(self.handle, k, v, self.k, self.v, self.plan["slot_map"])
+        return pkg.moe_lora_attention(self.handle, q, self.k, self.v, self.tables, self.lens, self.plan["query_offsets"],
+                                      max_query_len).reshape(q.shape[0], -1)
 
 
 def rms(x, eps=1e-6):
@@ -77,8 +103,9 @@ class DecoderBlock:
         s = s.masked_fill(torch.ones((T, T), dtype=torch.bool, device=q.device).triu(1), -math.inf)
         return torch.einsum("htu,uhd->thd", s.softmax(2), v.float()).bfloat16().reshape(T, -1)
 
-    def __call__(self, x, positions, slots):
-        """x [T, H] bf16 -> (x after the block, every stage's tensors by name)."""
+    def __call__(self, x, positions, slots, cache=None, max_query_len=None):
+        """x [T, H] bf16 -> (x after the block, every stage's tensors by name).  With a cache, whose step was
+        begun for these tokens, they attend to their requests' earlier ones as well."""
         s, cfg, h, T = self.shape, self.shape.experts, self.handle, x.shape[0]
         D, nq = s.head_dim, s.q_heads * s.head_dim
         st = {"x": x, "h1": rms(x)}
@@ -88,7 +115,7 @@ class DecoderBlock:
         st["q_in"], st["k_in"] = q.clone(), k.clone()
         pkg.moe_lora_qk_norm_rope(h, q, k, self.norm_q, self.norm_k, self.table, positions, q_out=q, k_out=k)
         st["q"], st["k"] = q, k
-        st["attn"] = self.attention(q, k, v)
+        st["attn"] = self.attention(q, k, v) if cache is None else cache.attention(q, k, v, max_query_len or T)
         st["out"] = pkg.moe_lora_linear(h, st["attn"], self.w_out, self.a_out, slots)
         x = st["x2"] = x + st["out"]
         st["h2"] = rms(x)
@@ -114,6 +141,12 @@ def main(tokens=64):
     y, st = block(x, positions, slots)
     torch.cuda.synchronize()
     load = torch.bincount(st["route"]["topk_ids"].flatten().long(), minlength=cfg.E)
+    cache = Cache(handle, block.shape, requests=2, pages=64)
+    for new in ([tokens, 3], [1, 1], [0, 1]):   # two prompts, then single tokens
+        lens = torch.tensor(new, dtype=torch.int32, device="cuda")
+        rows = torch.randn((sum(new), cfg.H), device="cuda").bfloat16()
+        block(rows, cache.step(lens, sum(new)), torch.zeros(sum(new), dtype=torch.int32, device="cuda"), cache, max(new))
+    print(f"tokens cached: {cache.lens.tolist()} in {int(cache.taken)} pages")
     print(f"{tokens} tokens: block output rms {y.float().square().mean().sqrt().item():.3f}, "
           f"{int((load > 0).sum())} of {cfg.E} experts used")
 

@@ -50,7 +50,8 @@ EXPORTED = ["moe_lora_create", "moe_lora_destroy", "moe_lora_status_string", "mo
             "moe_lora_packed_lora_b_size", "moe_lora_pack_lora_b", "moe_lora_packed_lora_a_size",
             "moe_lora_pack_lora_a", "moe_lora_select_experts", "moe_lora_qk_norm_rope",
             "moe_lora_linear_adapters_size", "moe_lora_linear_pack_adapters", "moe_lora_linear_workspace_size",
-            "moe_lora_linear"]
+            "moe_lora_linear", "moe_lora_page_tables", "moe_lora_cache_write", "moe_lora_attention",
+            "moe_lora_attention_workspace_size"]
 
 
 class MoELoRAError(RuntimeError):
