@@ -185,8 +185,8 @@ __global__ void __launch_bounds__(kTeams * DP / 8) attention_join_kernel(const _
         },
         m, l, o);
     if (r >= c.rows || team % per_row != 0) continue;
-    const long long token = c.q0 + (c.row0 + r) / p.G;
-    const int head = c.kh * p.G + (c.row0 + r) % p.G;
+    const long long token = c.q0 + token_of(p, c.row0 + r);
+    const int head = c.kh * p.G + c.row0 + r - static_cast<int>(token - c.q0) * p.G;
     if (p.prefix_splits == 0) {
       write_row8(p, token, head, d, m, l, o);
     } else {
@@ -375,6 +375,7 @@ extern "C" moe_lora_status moe_lora_attention(moe_lora_handle* h, const moe_lora
   p.Hq = a->q_heads;
   p.Hk = a->k_heads;
   p.G = a->q_heads / a->k_heads;
+  p.g_inverse = static_cast<uint32_t>(((1ull << 32) + p.G - 1) / p.G);
   p.D = a->head_dim;
   p.num_pages = a->num_pages;
   p.page = a->page_size;
@@ -390,7 +391,8 @@ extern "C" moe_lora_status moe_lora_attention(moe_lora_handle* h, const moe_lora
   p.piece_ml = nullptr;
   p.piece_o = nullptr;
   ML_ON_DEVICE(h);
-  if (!fast_layout(a) || p.scale_log2 == 0.0f || h->num_sms > kMaxSms) {
+  const long long group_rows = static_cast<long long>(p.T) * p.G;
+  if (!fast_layout(a) || std::max<long long>(group_rows, p.Hq) * p.G >= (1LL << 32) || p.scale_log2 == 0.0f || h->num_sms > kMaxSms) {
     ML_CUDA(cudaMemsetAsync(workspace, 0, 4, stream), "attention status");
     const int across = std::max(1, std::min(a->T, 65536 / std::max(1, a->B)));
     ML_LAUNCH(h, launch_k(attention_any_kernel, dim3(across, a->B, a->q_heads), dim3(32 * kAnyWarps), 0, stream, false, p),

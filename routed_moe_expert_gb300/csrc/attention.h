@@ -39,6 +39,7 @@ struct AttentionParams {
   float* lse;
   long long q_t, q_h, o_t, o_h, k_p, k_h, k_t, v_p, v_h, v_t, table_stride;
   int T, B, Hq, Hk, G, D;
+  uint32_t g_inverse;                          // 2^32 / G rounded up: rows are divided by G by its product's upper half
   int num_pages, page, page_log2, width;
   int shared;                                  // keys that are read from request 0's table
   int few_rows;                                // > 0: requests of up to so many rows a key head alone, < 0: the others
@@ -64,6 +65,12 @@ struct AttentionParams {
 };
 
 constexpr float kLn2 = 0.693147180559945f;
+
+// row / G, exact while row * G < 2^32, which the host sees to.  (A division is some 20 instructions, and these kernels'
+// time is partly that of fetching their code.)
+MLDEV int token_of(const AttentionParams& p, int row) {
+  return p.G == 1 ? row : static_cast<int>(__umulhi(static_cast<uint32_t>(row), p.g_inverse));
+}
 
 // A request's rows [q0, q0 + n) and its keys, checked: rows within [0, T), at most width * page keys.
 struct Request {
@@ -95,6 +102,7 @@ MLDEV int keys_of_token(const AttentionParams& p, int token) {
   Request r;
   if (p.offsets != nullptr) {
     int lo = 0, n = p.B;   // the last request that starts at or before the token
+#pragma unroll 1
     while (n > 1) {
       const int half = n >> 1;
       if (p.offsets[lo + half] <= token) lo += half;
@@ -107,15 +115,23 @@ MLDEV int keys_of_token(const AttentionParams& p, int token) {
   return max(r.kv - r.n + (token - r.q0) + 1, 0);
 }
 
-// mbar_wait for the waits that a step's time is made of: the timer is read only after some tries.  Raises the abort
-// flag when it runs out, after which every wait of the block ends at once.
+// mbar_wait in little code, and with the timer read only now and then.  Raises the abort flag when it runs out, after which
+// every wait of the block ends soon.
 MLDEV bool wait_soon(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* status) {
+  uint64_t since = 0;
 #pragma unroll 1
-  for (int i = 0; i < 256; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 15) == 15 && *abort_flag) return false;
+  for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
+    if ((i & 31u) != 0) continue;
+    if (*abort_flag) return false;
+    const uint64_t now = globaltimer_ns();
+    if (since == 0) since = now;
+    if (now - since > kWaitLimitNs) {
+      *abort_flag = 1;
+      record_status(status, kDevTimeout, kWhereAttention);
+      return false;
+    }
   }
-  return mbar_wait(bar, parity, abort_flag, status, kWhereAttention);
+  return true;
 }
 
 MLDEV float exp2_approx(float x) {   // 2^-22 relative; 0 for -inf
@@ -144,7 +160,7 @@ struct Schedule {
   // Keys that the last row of item i sees.
   static MLDEV int seen_by(const AttentionParams& p, const Request& r, int i) {
     const int last = min(i * ROWS + ROWS, r.n * p.G) - 1;   // (T * Hq is below 2^31 - 256)
-    return max(r.kv - r.n + last / p.G + 1, 0);
+    return max(r.kv - r.n + token_of(p, last) + 1, 0);
   }
   static MLDEV int items_of(const AttentionParams& p, const Request& r) {
     const int rows = r.n * p.G;
@@ -176,6 +192,7 @@ struct Walk {
   // The first item of request b, or of one behind it that has any (32 looked at together; a whole warp).
   MLDEV void enter(const AttentionParams& p) {
     const int lane = threadIdx.x & 31;
+#pragma unroll 1
     while (b < p.B) {
       const int n = b + lane < p.B ? S::items_of(p, request_of(p, b + lane)) : 0;
       const unsigned any = __ballot_sync(0xffffffffu, n > 0);
@@ -215,60 +232,70 @@ struct ScheduleSmem {
   long long found_u;
 };
 
-// Works out the schedule and the block's first item.  All threads of the block; `sums_s` [blockDim] scratch.
 template <int ROWS, int KEYS, int OVER>
-MLDEV void make_schedule(const AttentionParams& p, int cta, Schedule<ROWS, KEYS, OVER>& s, Walk<ROWS, KEYS, OVER>& w, ScheduleSmem& sm,
-                         long long* sums_s) {
+MLDEV void deal_out(const AttentionParams& p, int cta, Schedule<ROWS, KEYS, OVER>& s, long long units, long long items) {
+  s.units = units;
+  const long long by_least = units < (1ll << 31) ? static_cast<uint32_t>(units) / static_cast<uint32_t>(p.plan.least) : p.plan.ctas;
+  s.ctas = static_cast<int>(max(1ll, min(static_cast<long long>(p.plan.ctas), max(by_least, items))));
+  s.start = s.start_of(min(cta, s.ctas));
+  s.end = cta < s.ctas ? s.start_of(cta + 1) : s.start;
+}
+
+// The plan of few requests, a lane each; every warp by itself.
+template <int ROWS, int KEYS, int OVER>
+MLDEV void plan_few(const AttentionParams& p, int cta, Schedule<ROWS, KEYS, OVER>& s, Walk<ROWS, KEYS, OVER>& w) {
+  using S = Schedule<ROWS, KEYS, OVER>;
+  const int lane = threadIdx.x & 31;
+  w.b = p.B;
+  Request r;
+  r.q0 = r.n = r.kv = 0;
+  r.bad = false;
+  int items = 0, mine = 0;
+  if (lane < p.B) {
+    r = request_of(p, lane);
+    items = S::items_of(p, r);
+  #pragma unroll 1
+    for (int i = 0; i < items; ++i) mine += S::weight_of(p, r, i);
+    mine *= p.Hk;
+  }
+  s.bad = __any_sync(0xffffffffu, r.bad);
+  int incl = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += u;
+  }
+  deal_out(p, cta, s, __shfl_sync(0xffffffffu, incl, 31), static_cast<long long>(__reduce_add_sync(0xffffffffu, items)) * p.Hk);
+  if (s.start == s.end) return;
+  const int start = static_cast<int>(s.start);
+  w.b = __ffs(__ballot_sync(0xffffffffu, incl - mine <= start && start < incl)) - 1;
+  w.r.q0 = __shfl_sync(0xffffffffu, r.q0, w.b);
+  w.r.n = __shfl_sync(0xffffffffu, r.n, w.b);
+  w.r.kv = __shfl_sync(0xffffffffu, r.kv, w.b);
+  w.r.bad = false;
+  w.items = __shfl_sync(0xffffffffu, items, w.b);
+  const int before = __shfl_sync(0xffffffffu, incl - mine, w.b);
+  w.units = S::weight_of(p, w.r, 0);
+  const int per = w.items == 1 ? w.units : __shfl_sync(0xffffffffu, mine, w.b) / p.Hk;
+  w.kh = (start - before) / per;
+  int at = before + w.kh * per;
+  w.i = 0;
+#pragma unroll 1
+  while (at + w.units <= start) {   // (few: queries are not long)
+    at += w.units;
+    w.units = S::weight_of(p, w.r, ++w.i);
+  }
+  w.u0 = at;
+}
+
+// The plan of any requests.  All threads of the block; `sums_s` [blockDim] scratch.  (Not inlined, as the code that
+// every call runs is to be short.)
+template <int ROWS, int KEYS, int OVER>
+__device__ __noinline__ void plan_many(const AttentionParams& p, int cta, Schedule<ROWS, KEYS, OVER>& s, Walk<ROWS, KEYS, OVER>& w,
+                                       ScheduleSmem& sm, long long* sums_s) {
   using S = Schedule<ROWS, KEYS, OVER>;
   const int tid = threadIdx.x, NT = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = NT >> 5;
-  auto runs = [&](long long units, long long items) {   // the blocks that work, and this one's run
-    s.units = units;
-    const long long by_least = units < (1ll << 31) ? static_cast<uint32_t>(units) / static_cast<uint32_t>(p.plan.least) : p.plan.ctas;
-    s.ctas = static_cast<int>(max(1ll, min(static_cast<long long>(p.plan.ctas), max(by_least, items))));
-    s.start = s.start_of(min(cta, s.ctas));
-    s.end = cta < s.ctas ? s.start_of(cta + 1) : s.start;
-  };
   w.b = p.B;
-  if (p.plan.few) {   // a lane a request
-    Request r;
-    r.q0 = r.n = r.kv = 0;
-    r.bad = false;
-    int items = 0, mine = 0;
-    if (lane < p.B) {
-      r = request_of(p, lane);
-      items = S::items_of(p, r);
-      for (int i = 0; i < items; ++i) mine += S::weight_of(p, r, i);
-      mine *= p.Hk;
-    }
-    s.bad = __any_sync(0xffffffffu, r.bad);
-    int incl = mine;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, incl, off);
-      if (lane >= off) incl += u;
-    }
-    runs(__shfl_sync(0xffffffffu, incl, 31), static_cast<long long>(__reduce_add_sync(0xffffffffu, items)) * p.Hk);
-    if (s.start == s.end) return;
-    const int start = static_cast<int>(s.start);
-    w.b = __ffs(__ballot_sync(0xffffffffu, incl - mine <= start && start < incl)) - 1;
-    w.r.q0 = __shfl_sync(0xffffffffu, r.q0, w.b);
-    w.r.n = __shfl_sync(0xffffffffu, r.n, w.b);
-    w.r.kv = __shfl_sync(0xffffffffu, r.kv, w.b);
-    w.r.bad = false;
-    w.items = __shfl_sync(0xffffffffu, items, w.b);
-    const int before = __shfl_sync(0xffffffffu, incl - mine, w.b);
-    w.units = S::weight_of(p, w.r, 0);
-    const int per = w.items == 1 ? w.units : __shfl_sync(0xffffffffu, mine, w.b) / p.Hk;
-    w.kh = (start - before) / per;
-    int at = before + w.kh * per;
-    w.i = 0;
-    while (at + w.units <= start) {   // (few: queries are not long)
-      at += w.units;
-      w.units = S::weight_of(p, w.r, ++w.i);
-    }
-    w.u0 = at;
-    return;
-  }
   // the units of request b0 + tid (and its items), for a chunk of NT requests
   auto chunk = [&](int b0, int& items, bool& bad) -> long long {
     long long sum = 0;
@@ -277,16 +304,19 @@ MLDEV void make_schedule(const AttentionParams& p, int cta, Schedule<ROWS, KEYS,
       if (b0 + tid < p.B) {
         const Request r = request_of(p, b0 + tid);
         const int n = S::items_of(p, r);
+#pragma unroll 1
         for (int i = 0; i < n; ++i) sum += S::weight_of(p, r, i);
         items = n;
         bad = bad || r.bad;
       }
       return sum * p.Hk;
     }
+#pragma unroll 1
     for (int k = warp; k < NT && b0 + k < p.B; k += warps) {   // a warp a request
       const Request r = request_of(p, b0 + k);
       const int n = S::items_of(p, r);
       long long part = 0;
+#pragma unroll 1
       for (int i = lane; i < n; i += 32) part += S::weight_of(p, r, i);
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) part += __shfl_xor_sync(0xffffffffu, part, off);
@@ -304,6 +334,7 @@ MLDEV void make_schedule(const AttentionParams& p, int cta, Schedule<ROWS, KEYS,
   bool bad = false;
   long long total = 0, mine = 0;
   long long all_items = 0;
+#pragma unroll 1
   for (int b0 = 0; b0 < p.B; b0 += NT) {
     int items;
     mine = chunk(b0, items, bad);
@@ -322,15 +353,17 @@ MLDEV void make_schedule(const AttentionParams& p, int cta, Schedule<ROWS, KEYS,
   }
   s.bad = __syncthreads_or(bad) != 0;
   t = n = 0;
+#pragma unroll 1
   for (int i = 0; i < warps; ++i) {
     t += sm.sums[i];
     n += sm.items[i];
   }
-  runs(t, n);
+  deal_out(p, cta, s, t, n);
   if (s.start == s.end) return;
   // the request that has unit `start`
   __syncthreads();
   long long base = 0;
+#pragma unroll 1
   for (int b0 = 0; b0 < p.B; b0 += NT) {
     if (p.B > NT) {
       int items;
@@ -346,6 +379,7 @@ MLDEV void make_schedule(const AttentionParams& p, int cta, Schedule<ROWS, KEYS,
     if (lane == 31) sm.sums[warp] = incl;
     __syncthreads();
     long long before = base, all = 0;
+#pragma unroll 1
     for (int i = 0; i < warps; ++i) {
       if (i < warp) before += sm.sums[i];
       all += sm.sums[i];
@@ -372,11 +406,13 @@ MLDEV void make_schedule(const AttentionParams& p, int cta, Schedule<ROWS, KEYS,
   }
   if (warp == 0) {
     long long per = 0;
+#pragma unroll 1
     for (int i = lane; i < w.items; i += 32) per += S::weight_of(p, w.r, i);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) per += __shfl_xor_sync(0xffffffffu, per, off);
     const int kh = static_cast<int>((s.start - w.u0) / per);
     long long at = w.u0 + kh * per;   // first unit of items i0..
+#pragma unroll 1
     for (int i0 = 0; i0 < w.items; i0 += 32) {
       const int own = i0 + lane < w.items ? S::weight_of(p, w.r, i0 + lane) : 0;
       int incl = own;
@@ -398,6 +434,21 @@ MLDEV void make_schedule(const AttentionParams& p, int cta, Schedule<ROWS, KEYS,
   w.u0 = sm.found_u;
   w.kh = static_cast<int>(sm.head[0]);
   w.units = S::weight_of(p, w.r, w.i);
+}
+
+// Works out the schedule and the block's first item.  All threads of the block; `sums_s` [blockDim] scratch.
+template <int ROWS, int KEYS, int OVER>
+MLDEV void make_schedule(const AttentionParams& p, int cta, Schedule<ROWS, KEYS, OVER>& s, Walk<ROWS, KEYS, OVER>& w, ScheduleSmem& sm,
+                         long long* sums_s) {
+  if (p.plan.few) {
+    plan_few<ROWS, KEYS, OVER>(p, cta, s, w);
+  } else {
+    Schedule<ROWS, KEYS, OVER> made;   // (what a function takes by its address stays in memory)
+    Walk<ROWS, KEYS, OVER> place;
+    plan_many<ROWS, KEYS, OVER>(p, cta, made, place, sm, sums_s);
+    s = made;
+    w = place;
+  }
 }
 
 // What a block does of the item that a walk is at: units [lo, hi), and where the result goes.
@@ -490,6 +541,7 @@ __device__ __noinline__ bool repair_row(const AttentionParams& p, int b, int kh,
   };
   const int from = max(limit, key_lo), per = d_n / 8;
   bool found = false;
+#pragma unroll 1
   for (int c = lane; c < (key_hi - from) * per; c += 32) {
     const int d = d_lo + c % per * 8;
     const __nv_bfloat16* v = row_of(p.v, p.v_p, p.v_h, p.v_t, from + c / per);
@@ -501,14 +553,17 @@ __device__ __noinline__ bool repair_row(const AttentionParams& p, int b, int kh,
   if (!__any_sync(0xffffffffu, found)) return false;
   const __nv_bfloat16* q = p.q + token * p.q_t + head * p.q_h;
   float o[DP / 32] = {};
+#pragma unroll 1
   for (int j0 = key_lo; j0 < min(limit, key_hi); j0 += 32) {
     const int n = min(32, min(limit, key_hi) - j0);
     float dot = 0.0f;
     if (lane < n) {
       const __nv_bfloat16* k = row_of(p.k, p.k_p, p.k_h, p.k_t, j0 + lane);
+#pragma unroll 1
       for (int d = 0; k != nullptr && d < p.D; ++d) dot += bf2f(q[d]) * bf2f(k[d]);
     }
     const float w = exp2_approx(dot * p.scale_log2 - ref);
+#pragma unroll 1
     for (int t = 0; t < n; ++t) {
       const float wt = __shfl_sync(0xffffffffu, w, t);
       const __nv_bfloat16* v = row_of(p.v, p.v_p, p.v_h, p.v_t, j0 + t);

@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(con
       int limit[NT][2];              // keys that rows pair and pair + 1 see
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const int row = row0 + t * 8 + quad, token = row / p.G;
+        const int row = row0 + t * 8 + quad, token = token_of(p, row);
         const __nv_bfloat16* q =
             t * 8 + quad < rows ? p.q + (w.r.q0 + token) * p.q_t + (w.kh * p.G + row - token * p.G) * p.q_h : nullptr;
 #pragma unroll
@@ -197,10 +197,10 @@ __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(con
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int r = t * 8 + pair + e;
-          limit[t][e] = r < rows ? max(w.r.kv - w.r.n + (row0 + r) / p.G + 1, 0) : 0;
+          limit[t][e] = r < rows ? max(w.r.kv - w.r.n + token_of(p, row0 + r) + 1, 0) : 0;
         }
       }
-      const int all_see = max(w.r.kv - w.r.n + row0 / p.G + 1, 0);   // keys that every row of the item sees
+      const int all_see = max(w.r.kv - w.r.n + token_of(p, row0) + 1, 0);   // keys that every row of the item sees
       float o[NT][DP / 16][4];
       float ref[NT][2], l[NT][2];
 #pragma unroll
@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(con
             if (l_s[v][r] != 0.0f) all += l_s[v][r] * exp2_approx(m_s[v][r] - reference_of(m));
         };
         auto place = [&](int r, long long& token, int& head) {   // where the result goes, as a piece or part (index of its row)
-          const int in = (row0 + r) / p.G;
+          const int in = token_of(p, row0 + r);
           token = w.r.q0 + in;
           head = w.kh * p.G + (row0 + r) - in * p.G;
           return x.all ? part_row(p, token, head) : static_cast<long long>(x.slot) * p.item_rows + r;
@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(con
               int head;
               const long long at = place(r, token, head);
               if (repair_row<DP>(p, w.b, w.kh, token, head, p.shared + x.lo * kKeys, min(sees, p.shared + x.hi * kKeys),
-                                 max(w.r.kv - w.r.n + (row0 + r) / p.G + 1, 0), m, 1.0f / all, 0, DP,
+                                 max(w.r.kv - w.r.n + token_of(p, row0 + r) + 1, 0), m, 1.0f / all, 0, DP,
                                  p.out + token * p.o_t + head * p.o_h, final ? nullptr : parts + at * DP) &&
                   lane == 0)
                 atomicOr(&done_s, 1u << r8);

@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
             if (rows > 0 && prefix.splits > 0) n = prefix.units;
             if (rows > 0 && prefix.splits == 0) {
               const int last = t.row0 + 128 * k + rows - 1;
-              n = (max(max(t.kv - t.n + last / p.G + 1, 0) - p.shared, 0) + kKeys - 1) / kKeys;
+              n = (max(max(t.kv - t.n + token_of(p, last) + 1, 0) - p.shared, 0) + kKeys - 1) / kKeys;
             }
             units[k] = max(t.lo, min(hi, n));
           }
@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
     // Copies the part's query rows to the products' layout, a warp its own 32 of them, whole rows at a time.
     auto fetch_queries = [&](const Step& t) {
       const int row = t.row0 + (t.lead == 2 ? r : k * 128 + r);
-      const int token = row / p.G;
+      const int token = token_of(p, row);
       const __nv_bfloat16* from = nullptr;
       if (r < t.rows(k)) from = p.q + (t.q0 + token) * p.q_t + (t.kh * p.G + row - token * p.G) * p.q_h;
       constexpr int kLanes = DP / 8;   // a row
@@ -500,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
       auto row_token = [&](int& head) {   // this thread's row: its token, and head
         const Step& t = steps[step_at];
         const int row = t.row0 + (lead == 2 ? r : k * 128 + r);   // of the request and key head
-        const int token_in = row / p.G;
+        const int token_in = token_of(p, row);
         head = t.kh * p.G + row - token_in * p.G;
         return t.q0 + token_in;
       };
@@ -688,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
             auto of_row = [&](auto x) { return __shfl_sync(0xffffffffu, x, of); };
             const unsigned long long there = of_row(to);
             const float sum = of_row(l);
-            const bool done = repair_row<DP>(p, request, of_row(head) / p.G, of_row(token), of_row(head), key0 + lo * kKeys, key_hi,
+            const bool done = repair_row<DP>(p, request, token_of(p, of_row(head)), of_row(token), of_row(head), key0 + lo * kKeys, key_hi,
                                              of_row(sees), of_row(ref), 1.0f / sum, c_lo, pair ? DP / 2 : DP,
                                              reinterpret_cast<__nv_bfloat16*>(there), final ? nullptr : reinterpret_cast<float*>(there));
             if (lane == of) written = done;
