@@ -432,7 +432,7 @@ extern "C" moe_lora_status moe_lora_attention(moe_lora_handle* h, const moe_lora
     x.plan.least = least;
     x.plan.whole = own_keys <= whole_keys;
     const long long items = (static_cast<long long>(p.T) * p.G / rows + p.B) * p.Hk, most = own_keys / keys + 1 + kTileOver;
-    x.plan.few = p.B <= 32 && !x.long_queries && items * most < (1LL << 30);
+    x.plan.few = p.B <= 32 && items * most < (1LL << 30);
   };
   p.follows = few.follows = 0;
   p.alone = few.alone = 0;

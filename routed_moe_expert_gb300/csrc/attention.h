@@ -254,10 +254,25 @@ MLDEV void plan_few(const AttentionParams& p, int cta, Schedule<ROWS, KEYS, OVER
   if (lane < p.B) {
     r = request_of(p, lane);
     items = S::items_of(p, r);
-  #pragma unroll 1
-    for (int i = 0; i < items; ++i) mine += S::weight_of(p, r, i);
-    mine *= p.Hk;
   }
+  if (!p.long_queries) {
+#pragma unroll 1
+    for (int i = 0; i < items; ++i) mine += S::weight_of(p, r, i);
+  } else {   // requests of many items: the lanes add up one after the other's
+#pragma unroll 1
+    for (int b = 0; b < p.B; ++b) {
+      Request other;
+      other.n = __shfl_sync(0xffffffffu, r.n, b);
+      other.kv = __shfl_sync(0xffffffffu, r.kv, b);
+      const int n = __shfl_sync(0xffffffffu, items, b);
+      int part = 0;
+#pragma unroll 1
+      for (int i = lane; i < n; i += 32) part += S::weight_of(p, other, i);
+      part = __reduce_add_sync(0xffffffffu, part);
+      if (lane == b) mine = part;
+    }
+  }
+  mine *= p.Hk;
   s.bad = __any_sync(0xffffffffu, r.bad);
   int incl = mine;
 #pragma unroll
@@ -275,15 +290,27 @@ MLDEV void plan_few(const AttentionParams& p, int cta, Schedule<ROWS, KEYS, OVER
   w.r.bad = false;
   w.items = __shfl_sync(0xffffffffu, items, w.b);
   const int before = __shfl_sync(0xffffffffu, incl - mine, w.b);
-  w.units = S::weight_of(p, w.r, 0);
-  const int per = w.items == 1 ? w.units : __shfl_sync(0xffffffffu, mine, w.b) / p.Hk;
+  const int per = __shfl_sync(0xffffffffu, mine, w.b) / p.Hk;
   w.kh = (start - before) / per;
   int at = before + w.kh * per;
-  w.i = 0;
 #pragma unroll 1
-  while (at + w.units <= start) {   // (few: queries are not long)
-    at += w.units;
-    w.units = S::weight_of(p, w.r, ++w.i);
+  for (w.i = 0;; w.i += 32) {   // 32 items at a time
+    const int own = w.i + lane < w.items ? S::weight_of(p, w.r, w.i + lane) : 0;
+    int to = own;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, to, off);
+      if (lane >= off) to += u;
+    }
+    const unsigned found = __ballot_sync(0xffffffffu, start < at + to);
+    if (found != 0) {
+      const int l = __ffs(found) - 1;
+      w.i += l;
+      w.units = __shfl_sync(0xffffffffu, own, l);
+      at += __shfl_sync(0xffffffffu, to, l) - w.units;
+      break;
+    }
+    at += __shfl_sync(0xffffffffu, to, 31);
   }
   w.u0 = at;
 }

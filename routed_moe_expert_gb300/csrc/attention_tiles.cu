@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
       const __nv_bfloat16* from = nullptr;
       if (r < t.rows(k)) from = p.q + (t.q0 + token) * p.q_t + (t.kh * p.G + row - token * p.G) * p.q_h;
       constexpr int kLanes = DP / 8;   // a row
-#pragma unroll
+#pragma unroll 2
       for (int i = 0; i < 32; i += 32 / kLanes) {
         const int of = i + lane / kLanes, c = lane % kLanes, tr = wr + of;
         const __nv_bfloat16* src =
@@ -677,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
         other *= inv;
       }
       if (wr < rows) {
-        const int chunks = pair ? DP / 64 : DP / 32;   // of 32 columns
+        const int chunks = pair ? DP / 32 : DP / 16;   // of 16 columns: little code, which has to be fetched
         const int key_hi = min(seen_here, key0 + hi * kKeys);
         // Rows that a value which they do not see has spoilt; `odd` is a sum of 0 times each of a row's results.
         auto repair = [&](float odd) {
@@ -695,11 +695,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
           }
           return written;
         };
-        uint32_t own[32], mate[32];
+        uint32_t own[16], mate[16];
         auto fetch = [&](int c) {
           __syncwarp();
-          tmem_ld_x32(o_at + c_lo + c * 32, own);   // (whatever is there, if the tile had no unit)
-          if (pair) tmem_ld_x32(lanes + 256 + (k ^ 1) * DP + c_lo + c * 32, mate);
+          tmem_ld_x16(o_at + c_lo + c * 16, own);   // (whatever is there, if the tile had no unit)
+          if (pair) tmem_ld_x16(lanes + 256 + (k ^ 1) * DP + c_lo + c * 16, mate);
         };
         auto result = [&](int i) {
           const float o = use_mine ? __uint_as_float(own[i]) * mine : 0.0f;
@@ -713,7 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
             fetch(c);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) odd = fmaf(result(i), 0.0f, odd);
+            for (int i = 0; i < 16; ++i) odd = fmaf(result(i), 0.0f, odd);
           }
           if (repair(odd)) write = false;
         }
@@ -721,29 +721,26 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
         fetch(0);
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {   // the next chunk's load is under way while one is written
-          float o[32];
+          float o[16];
           tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
+          for (int i = 0; i < 16; ++i) {
             o[i] = result(i);
             odds[i & 3] = fmaf(o[i], 0.0f, odds[i & 3]);
           }
           if (c + 1 < chunks) fetch(c + 1);
-          const int col = c_lo + c * 32;
+          const int col = c_lo + c * 16;
           uint32_t x[8];
           if (final) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 16) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const __nv_bfloat162 h = __floats2bfloat162_rn(o[i + 2 * e], o[i + 2 * e + 1]);
-                x[e] = l == 0.0f ? 0u : *reinterpret_cast<const uint32_t*>(&h);   // nothing is seen, or nothing weighs
-              }
-              if (write) st_row16(to + 2 * (col + i), x, p.out_wide, col + i < p.D, col + i + 8 < p.D);
+            for (int e = 0; e < 8; ++e) {
+              const __nv_bfloat162 h = __floats2bfloat162_rn(o[2 * e], o[2 * e + 1]);
+              x[e] = l == 0.0f ? 0u : *reinterpret_cast<const uint32_t*>(&h);   // nothing is seen, or nothing weighs
             }
+            if (write) st_row16(to + 2 * col, x, p.out_wide, col < p.D, col + 8 < p.D);
           } else {
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
+            for (int i = 0; i < 16; i += 8) {
 #pragma unroll
               for (int e = 0; e < 8; ++e) x[e] = __float_as_uint(o[i + e]);
               if (write) st_row16(to + 4 * (col + i), x, true, true, true);
