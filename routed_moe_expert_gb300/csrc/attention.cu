@@ -391,8 +391,18 @@ extern "C" moe_lora_status moe_lora_attention(moe_lora_handle* h, const moe_lora
   p.piece_ml = nullptr;
   p.piece_o = nullptr;
   ML_ON_DEVICE(h);
+  // what the kernels' 32-bit arithmetic holds: rows divided by G (token_of), and the weight of all items, at most
   const long long group_rows = static_cast<long long>(p.T) * p.G;
-  if (!fast_layout(a) || std::max<long long>(group_rows, p.Hq) * p.G >= (1LL << 32) || p.scale_log2 == 0.0f || h->num_sms > kMaxSms) {
+  const long long own_most = static_cast<long long>(p.width) * p.page;
+  // Requests of up to 8 rows a key head (16, where the heads alone are more than 8) run on the kernel for few rows, the
+  // others on tiles; in a batch that may have both, each kernel takes its own.
+  const bool tiles = static_cast<long long>(a->max_query_len) * p.G > kFewRows;
+  const bool mixed = tiles && a->B > 1 && p.offsets != nullptr && static_cast<long long>(a->max_query_len) * a->B != p.T;
+  const long long few_items = tiles ? 2LL * p.B : group_rows / 8 + p.B;
+  const bool fits = std::max<long long>(group_rows, p.Hq) * p.G < (1LL << 32) &&
+                    (!tiles || (group_rows / kTileRows + p.B) * p.Hk * (own_most / kTileKeys + 1 + kTileOver) < (1LL << 30)) &&
+                    ((tiles && !mixed) || few_items * p.Hk * (own_most / kFewKeys + 1 + kFewOver) < (1LL << 30));
+  if (!fast_layout(a) || !fits || p.scale_log2 == 0.0f || h->num_sms > kMaxSms) {
     ML_CUDA(cudaMemsetAsync(workspace, 0, 4, stream), "attention status");
     const int across = std::max(1, std::min(a->T, 65536 / std::max(1, a->B)));
     ML_LAUNCH(h, launch_k(attention_any_kernel, dim3(across, a->B, a->q_heads), dim3(32 * kAnyWarps), 0, stream, false, p),
@@ -417,22 +427,16 @@ extern "C" moe_lora_status moe_lora_attention(moe_lora_handle* h, const moe_lora
     return page_map(h, &x.tmap_k, x.k, x, x.k_t, x.k_h, x.k_p, keys, both) &&
            page_map(h, &x.tmap_v, x.v, x, x.v_t, x.v_h, x.v_p, keys, both);
   };
-  // Requests of up to 8 rows a key head (16, where the heads alone are more than 8) run on the kernel for few rows, the
-  // others on tiles; in a batch that may have both, each kernel takes its own.  (32 single tokens and 512 of a
-  // prompt, 2000 keys each: 71 us with all of them on tiles.)
-  const bool tiles = static_cast<long long>(a->max_query_len) * p.G > kFewRows;
-  const bool mixed = tiles && a->B > 1 && p.offsets != nullptr && static_cast<long long>(a->max_query_len) * a->B != p.T;
   const bool eight = mixed ? p.G <= 8 : static_cast<long long>(a->max_query_len) * p.G <= 8;
   const long long own_keys = static_cast<long long>(p.width) * p.page - p.shared;   // of a request, at most
   AttentionParams few = p;
   if ((tiles || p.shared > 0) && !maps(p, kTileKeys, false)) return cuda_fail(cudaErrorInvalidValue, "attention tensor maps");
   if ((!tiles || mixed) && !maps(few, kFewKeys, p.both_halves)) return cuda_fail(cudaErrorInvalidValue, "attention tensor maps");
-  auto plan_few = [&](AttentionParams& x, int ctas, int least, int whole_keys, int rows, int keys) {
+  auto plan_for = [&](AttentionParams& x, int ctas, int least, int whole_keys) {
     x.plan.ctas = ctas;
     x.plan.least = least;
     x.plan.whole = own_keys <= whole_keys;
-    const long long items = (static_cast<long long>(p.T) * p.G / rows + p.B) * p.Hk, most = own_keys / keys + 1 + kTileOver;
-    x.plan.few = p.B <= 32 && items * most < (1LL << 30);
+    x.plan.few = p.B <= 32;
   };
   p.follows = few.follows = 0;
   p.alone = few.alone = 0;
@@ -449,13 +453,13 @@ extern "C" moe_lora_status moe_lora_attention(moe_lora_handle* h, const moe_lora
   const bool fold = p.prefix_splits > 0;
   p.item_rows = slot_rows(true, p.T, p.G);
   p.long_queries = static_cast<long long>(a->max_query_len) * p.G > 8LL * kTileRows;
-  plan_few(p, h->num_sms, 2, 4 * kTileKeys, kTileRows, kTileKeys);
+  plan_for(p, h->num_sms, 2, 4 * kTileKeys);
   p.piece_ml = reinterpret_cast<float2*>(base + at.ml);
   p.piece_o = reinterpret_cast<float*>(base + at.o);
   p.records = p.plan.whole ? nullptr : reinterpret_cast<PieceRecord*>(base + at.records);
   few.item_rows = slot_rows(false, p.T, p.G);
   few.long_queries = 0;
-  plan_few(few, kFewPerSm * h->num_sms, 2, 8 * kFewKeys, 8, kFewKeys);
+  plan_for(few, kFewPerSm * h->num_sms, 2, 8 * kFewKeys);
   few.piece_ml = reinterpret_cast<float2*>(base + at.few_ml);
   few.piece_o = reinterpret_cast<float*>(base + at.few_o);
   few.records = few.plan.whole ? nullptr : reinterpret_cast<PieceRecord*>(base + at.few_records);

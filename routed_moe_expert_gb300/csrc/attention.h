@@ -5,6 +5,10 @@
 
 namespace mlk {
 
+// Items of the kernel for few rows (attention_rows.cu) and of the tiles' (attention_tiles.cu).
+constexpr int kFewRows = 16, kFewKeys = 64, kFewPerSm = 2, kFewOver = 1;
+constexpr int kTileRows = 256, kTileKeys = 128, kTileOver = 4;
+
 // How a call's work is dealt out.  Rows of a request and key head are its query rows times the G query
 // heads of that key head, row r being token r / G and head r % G: a key is read once for all of them.  An
 // item is up to `rows` of them (Plan::rows) with the keys that its last row sees, cut into units of
@@ -20,7 +24,7 @@ struct Plan {
   int ctas;          // blocks of the launch
   int least;         // units that a block takes at least, when that leaves blocks without work
   int whole;
-  int few;           // up to 32 requests whose weights fit 32 bits together: every warp plans for itself
+  int few;           // up to 32 requests: every warp plans for itself
 };
 
 struct PieceRecord {
@@ -146,10 +150,11 @@ MLDEV float reference_of(float m) { return m == -INFINITY ? 0.0f : m; }
 // ---------------------------------------------------------------- the plan, worked out by every block
 template <int ROWS, int KEYS, int OVER>
 struct Schedule {
-  // of this launch and block
+  // of this launch and block (the host sees to it that all items' weight is below 2^30)
   int ctas;              // blocks that work
-  long long units;       // all items' weight
-  long long start, end;  // this block's run
+  int units;             // all items' weight
+  int each, rest;        // units = each * ctas + rest
+  int start, end;        // this block's run
   bool bad;
 
   // What item i of a request weighs: its units (at least one, so that rows that see nothing are written) and OVER.
@@ -168,17 +173,16 @@ struct Schedule {
     return (rows + ROWS - 1) / ROWS;
   }
 
-  // The block whose run has u, and where a block's run starts (in 32 bits where that is enough: a division of
-  // 64 bits is some hundred cycles).
-  MLDEV int block_of(long long u) const {
-    return small() ? static_cast<int>(((static_cast<uint32_t>(u) + 1u) * static_cast<uint32_t>(ctas) - 1u) / static_cast<uint32_t>(units))
-                   : static_cast<int>(((u + 1) * ctas - 1) / units);
+  // Where a block's run starts, floor(units c / ctas), and the block whose run has u.
+  MLDEV int start_of(int c) const { return each * c + static_cast<int>(static_cast<uint32_t>(rest * c) / static_cast<uint32_t>(ctas)); }
+  MLDEV int block_of(int u) const {
+    int c = min(ctas - 1, static_cast<int>(static_cast<float>(u) * (static_cast<float>(ctas) / static_cast<float>(units))));
+#pragma unroll 1
+    while (c + 1 < ctas && start_of(c + 1) <= u) ++c;   // (the estimate is one off at most)
+#pragma unroll 1
+    while (start_of(c) > u) --c;
+    return c;
   }
-  MLDEV long long start_of(int c) const {
-    return small() ? static_cast<long long>(static_cast<uint32_t>(units) * static_cast<uint32_t>(c) / static_cast<uint32_t>(ctas))
-                   : units * c / ctas;
-  }
-  MLDEV bool small() const { return units < (1ll << 31) / 512; }   // (blocks are at most 320)
 };
 
 // A place in the schedule, advanced item by item; every role of a block walks through the same ones.
@@ -186,7 +190,7 @@ template <int ROWS, int KEYS, int OVER>
 struct Walk {
   using S = Schedule<ROWS, KEYS, OVER>;
   int b, kh, i, items, units;   // of the request's items; weight of this item
-  long long u0;                 // of all items before it
+  int u0;                       // of all items before it
   Request r;
 
   // The first item of request b, or of one behind it that has any (32 looked at together; a whole warp).
@@ -209,7 +213,7 @@ struct Walk {
     }
     kh = i = 0;
   }
-  MLDEV void next(const AttentionParams& p, long long end) {   // (behind `end` nothing is looked up any more)
+  MLDEV void next(const AttentionParams& p, int end) {   // (behind `end` nothing is looked up any more)
     u0 += units;
     if (u0 >= end) return;
     if (++i == items) {
@@ -225,18 +229,17 @@ struct Walk {
 };
 
 struct ScheduleSmem {
-  long long sums[32], head[2];
-  int items[32];
-  long long found_base;
-  int found_b, found_i, bad;
-  long long found_u;
+  int sums[32], items[32];
+  int found_base, found_b, found_i, found_u, found_kh;
 };
 
+// The blocks that work, and this one's run.
 template <int ROWS, int KEYS, int OVER>
-MLDEV void deal_out(const AttentionParams& p, int cta, Schedule<ROWS, KEYS, OVER>& s, long long units, long long items) {
+MLDEV void deal_out(const AttentionParams& p, int cta, Schedule<ROWS, KEYS, OVER>& s, int units, int items) {
   s.units = units;
-  const long long by_least = units < (1ll << 31) ? static_cast<uint32_t>(units) / static_cast<uint32_t>(p.plan.least) : p.plan.ctas;
-  s.ctas = static_cast<int>(max(1ll, min(static_cast<long long>(p.plan.ctas), max(by_least, items))));
+  s.ctas = max(1, min(p.plan.ctas, max(units / p.plan.least, items)));
+  s.each = units / s.ctas;
+  s.rest = units - s.each * s.ctas;
   s.start = s.start_of(min(cta, s.ctas));
   s.end = cta < s.ctas ? s.start_of(cta + 1) : s.start;
 }
@@ -255,7 +258,7 @@ MLDEV void plan_few(const AttentionParams& p, int cta, Schedule<ROWS, KEYS, OVER
     r = request_of(p, lane);
     items = S::items_of(p, r);
   }
-  if (!p.long_queries) {
+  if (ROWS <= kFewRows || !p.long_queries) {
 #pragma unroll 1
     for (int i = 0; i < items; ++i) mine += S::weight_of(p, r, i);
   } else {   // requests of many items: the lanes add up one after the other's
@@ -280,9 +283,9 @@ MLDEV void plan_few(const AttentionParams& p, int cta, Schedule<ROWS, KEYS, OVER
     const int u = __shfl_up_sync(0xffffffffu, incl, off);
     if (lane >= off) incl += u;
   }
-  deal_out(p, cta, s, __shfl_sync(0xffffffffu, incl, 31), static_cast<long long>(__reduce_add_sync(0xffffffffu, items)) * p.Hk);
+  deal_out(p, cta, s, __shfl_sync(0xffffffffu, incl, 31), __reduce_add_sync(0xffffffffu, items) * p.Hk);
   if (s.start == s.end) return;
-  const int start = static_cast<int>(s.start);
+  const int start = s.start;
   w.b = __ffs(__ballot_sync(0xffffffffu, incl - mine <= start && start < incl)) - 1;
   w.r.q0 = __shfl_sync(0xffffffffu, r.q0, w.b);
   w.r.n = __shfl_sync(0xffffffffu, r.n, w.b);
@@ -319,77 +322,61 @@ MLDEV void plan_few(const AttentionParams& p, int cta, Schedule<ROWS, KEYS, OVER
 // every call runs is to be short.)
 template <int ROWS, int KEYS, int OVER>
 __device__ __noinline__ void plan_many(const AttentionParams& p, int cta, Schedule<ROWS, KEYS, OVER>& s, Walk<ROWS, KEYS, OVER>& w,
-                                       ScheduleSmem& sm, long long* sums_s) {
+                                       ScheduleSmem& sm, int* sums_s) {
   using S = Schedule<ROWS, KEYS, OVER>;
   const int tid = threadIdx.x, NT = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = NT >> 5;
   w.b = p.B;
-  // the units of request b0 + tid (and its items), for a chunk of NT requests
-  auto chunk = [&](int b0, int& items, bool& bad) -> long long {
-    long long sum = 0;
+  // What the requests b0 + tid of a chunk weigh, and their items.
+  auto chunk = [&](int b0, int& items, bool& bad) -> int {
+    int sum = 0;
     items = 0;
-    if (!p.long_queries) {
-      if (b0 + tid < p.B) {
-        const Request r = request_of(p, b0 + tid);
-        const int n = S::items_of(p, r);
-#pragma unroll 1
-        for (int i = 0; i < n; ++i) sum += S::weight_of(p, r, i);
-        items = n;
-        bad = bad || r.bad;
-      }
-      return sum * p.Hk;
-    }
-#pragma unroll 1
-    for (int k = warp; k < NT && b0 + k < p.B; k += warps) {   // a warp a request
-      const Request r = request_of(p, b0 + k);
-      const int n = S::items_of(p, r);
-      long long part = 0;
-#pragma unroll 1
-      for (int i = lane; i < n; i += 32) part += S::weight_of(p, r, i);
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) part += __shfl_xor_sync(0xffffffffu, part, off);
-      if (lane == 0) sums_s[k] = part;
-      bad = bad || r.bad;
-    }
-    __syncthreads();
     if (b0 + tid < p.B) {
-      sum = sums_s[tid];
-      items = S::items_of(p, request_of(p, b0 + tid));
+      const Request r = request_of(p, b0 + tid);
+      items = S::items_of(p, r);
+      bad = bad || r.bad;
+      if (ROWS <= kFewRows || !p.long_queries)
+#pragma unroll 1
+        for (int i = 0; i < items; ++i) sum += S::weight_of(p, r, i);
     }
-    __syncthreads();
+    if (ROWS > kFewRows && p.long_queries) {   // a warp a request
+#pragma unroll 1
+      for (int k = warp; k < NT && b0 + k < p.B; k += warps) {
+        const Request r = request_of(p, b0 + k);
+        const int n = S::items_of(p, r);
+        int part = 0;
+#pragma unroll 1
+        for (int i = lane; i < n; i += 32) part += S::weight_of(p, r, i);
+        part = __reduce_add_sync(0xffffffffu, part);
+        if (lane == 0) sums_s[k] = part;
+      }
+      __syncthreads();
+      if (b0 + tid < p.B) sum = sums_s[tid];
+      __syncthreads();
+    }
     return sum * p.Hk;
   };
   bool bad = false;
-  long long total = 0, mine = 0;
-  long long all_items = 0;
+  int total = 0, mine = 0, all_items = 0;
 #pragma unroll 1
   for (int b0 = 0; b0 < p.B; b0 += NT) {
     int items;
     mine = chunk(b0, items, bad);
     total += mine;
-    all_items += static_cast<long long>(items) * p.Hk;
+    all_items += items * p.Hk;
   }
-  long long t = total, n = all_items;
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    t += __shfl_xor_sync(0xffffffffu, t, off);
-    n += __shfl_xor_sync(0xffffffffu, n, off);
-  }
+  total = __reduce_add_sync(0xffffffffu, total);
+  all_items = __reduce_add_sync(0xffffffffu, all_items);
   if (lane == 0) {
-    sm.sums[warp] = t;
-    sm.items[warp] = static_cast<int>(min(n, 0x3fffffffll));
+    sm.sums[warp] = total;
+    sm.items[warp] = all_items;
   }
   s.bad = __syncthreads_or(bad) != 0;
-  t = n = 0;
-#pragma unroll 1
-  for (int i = 0; i < warps; ++i) {
-    t += sm.sums[i];
-    n += sm.items[i];
-  }
-  deal_out(p, cta, s, t, n);
+  deal_out(p, cta, s, __reduce_add_sync(0xffffffffu, lane < warps ? sm.sums[lane] : 0),
+           __reduce_add_sync(0xffffffffu, lane < warps ? sm.items[lane] : 0));
   if (s.start == s.end) return;
   // the request that has unit `start`
   __syncthreads();
-  long long base = 0;
+  int base = 0;
 #pragma unroll 1
   for (int b0 = 0; b0 < p.B; b0 += NT) {
     if (p.B > NT) {
@@ -397,25 +384,20 @@ __device__ __noinline__ void plan_many(const AttentionParams& p, int cta, Schedu
       bool ignored = false;
       mine = chunk(b0, items, ignored);
     }
-    long long incl = mine;
+    int incl = mine;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const long long u = __shfl_up_sync(0xffffffffu, incl, off);
+      const int u = __shfl_up_sync(0xffffffffu, incl, off);
       if (lane >= off) incl += u;
     }
     if (lane == 31) sm.sums[warp] = incl;
     __syncthreads();
-    long long before = base, all = 0;
-#pragma unroll 1
-    for (int i = 0; i < warps; ++i) {
-      if (i < warp) before += sm.sums[i];
-      all += sm.sums[i];
-    }
+    const int before = base + __reduce_add_sync(0xffffffffu, lane < warp ? sm.sums[lane] : 0);
+    base += __reduce_add_sync(0xffffffffu, lane < warps ? sm.sums[lane] : 0);
     if (before + incl - mine <= s.start && s.start < before + incl) {
       sm.found_b = b0 + tid;
       sm.found_base = before + incl - mine;
     }
-    base += all;
     __syncthreads();
     if (s.start < base) break;
   }
@@ -423,22 +405,13 @@ __device__ __noinline__ void plan_many(const AttentionParams& p, int cta, Schedu
   w.b = sm.found_b;
   w.r = request_of(p, w.b);
   w.items = S::items_of(p, w.r);
-  w.u0 = sm.found_base;
-  if (w.items == 1) {
-    w.units = S::weight_of(p, w.r, 0);
-    w.kh = static_cast<int>(static_cast<uint32_t>(s.start - w.u0) / static_cast<uint32_t>(w.units));   // (below Hk * units)
-    w.u0 += static_cast<long long>(w.kh) * w.units;
-    w.i = 0;
-    return;
-  }
   if (warp == 0) {
-    long long per = 0;
+    int per = 0;
 #pragma unroll 1
     for (int i = lane; i < w.items; i += 32) per += S::weight_of(p, w.r, i);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) per += __shfl_xor_sync(0xffffffffu, per, off);
-    const int kh = static_cast<int>((s.start - w.u0) / per);
-    long long at = w.u0 + kh * per;   // first unit of items i0..
+    per = __reduce_add_sync(0xffffffffu, per);
+    const int kh = (s.start - sm.found_base) / per;
+    int at = sm.found_base + kh * per;   // first unit of items i0..
 #pragma unroll 1
     for (int i0 = 0; i0 < w.items; i0 += 32) {
       const int own = i0 + lane < w.items ? S::weight_of(p, w.r, i0 + lane) : 0;
@@ -451,7 +424,7 @@ __device__ __noinline__ void plan_many(const AttentionParams& p, int cta, Schedu
       if (own > 0 && at + incl - own <= s.start && s.start < at + incl) {
         sm.found_i = i0 + lane;
         sm.found_u = at + incl - own;
-        sm.head[0] = kh;
+        sm.found_kh = kh;
       }
       at += __shfl_sync(0xffffffffu, incl, 31);
     }
@@ -459,14 +432,14 @@ __device__ __noinline__ void plan_many(const AttentionParams& p, int cta, Schedu
   __syncthreads();
   w.i = sm.found_i;
   w.u0 = sm.found_u;
-  w.kh = static_cast<int>(sm.head[0]);
+  w.kh = sm.found_kh;
   w.units = S::weight_of(p, w.r, w.i);
 }
 
 // Works out the schedule and the block's first item.  All threads of the block; `sums_s` [blockDim] scratch.
 template <int ROWS, int KEYS, int OVER>
 MLDEV void make_schedule(const AttentionParams& p, int cta, Schedule<ROWS, KEYS, OVER>& s, Walk<ROWS, KEYS, OVER>& w, ScheduleSmem& sm,
-                         long long* sums_s) {
+                         int* sums_s) {
   if (p.plan.few) {
     plan_few<ROWS, KEYS, OVER>(p, cta, s, w);
   } else {
@@ -494,8 +467,8 @@ MLDEV Part part_of(const AttentionParams& p, const Schedule<ROWS, KEYS, OVER>& s
     x.slot = 0;
     return x;
   }
-  x.lo = static_cast<int>(max(s.start - w.u0 - OVER, 0ll));
-  x.hi = static_cast<int>(min(s.end - w.u0 - OVER, static_cast<long long>(w.units - OVER)));
+  x.lo = max(s.start - w.u0 - OVER, 0);
+  x.hi = min(s.end - w.u0 - OVER, w.units - OVER);
   x.all = x.lo == 0 && x.hi == w.units - OVER;
   x.slot = 2 * cta + (w.u0 > s.start ? 1 : 0);
   return x;
@@ -640,8 +613,6 @@ struct PrefixRun {
 };
 
 // Launches (attention_rows.cu, attention_tiles.cu)
-constexpr int kFewRows = 16, kFewKeys = 64, kFewPerSm = 2, kFewOver = 1;
-constexpr int kTileRows = 256, kTileKeys = 128, kTileOver = 4;
 cudaError_t prepare_attention_rows();
 cudaError_t launch_attention_rows(const AttentionParams& p, int dp, bool eight, cudaStream_t stream);   // items of 8 rows, or 16
 cudaError_t prepare_attention_tiles();

@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(con
   __shared__ uint64_t full[kStages], empty[kStages];
   __shared__ float m_s[kConsumers][kRows], l_s[kConsumers][kRows];
   __shared__ ScheduleSmem sched_s;
-  __shared__ long long sums_s[kThreads];
+  __shared__ int sums_s[kThreads];
   __shared__ uint32_t error_s;
   __shared__ int abort_s;
   __shared__ unsigned odd_s, done_s;   // rows whose result is not finite, and those that are written already

@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
   Sched s;
   Place w;
   if (prefix.splits == 0) {
-    make_schedule<kRows, kKeys, kTileOver>(p, cta, s, w, sched_s, reinterpret_cast<long long*>(smem));
+    make_schedule<kRows, kKeys, kTileOver>(p, cta, s, w, sched_s, reinterpret_cast<int*>(smem));
     __syncthreads();   // the scratch is the query tiles' again
     if (threadIdx.x == 0 && s.bad) record_status(&error_s, kDevBadSlot, kWhereAttention);
   }
