@@ -436,7 +436,7 @@ extern "C" moe_lora_status moe_lora_attention(moe_lora_handle* h, const moe_lora
     x.plan.ctas = ctas;
     x.plan.least = least;
     x.plan.whole = own_keys <= whole_keys;
-    x.plan.few = p.B <= 32;
+    x.plan.few = p.B <= (x.long_queries ? 32 : 256);
   };
   p.follows = few.follows = 0;
   p.alone = few.alone = 0;

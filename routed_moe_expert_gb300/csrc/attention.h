@@ -24,7 +24,7 @@ struct Plan {
   int ctas;          // blocks of the launch
   int least;         // units that a block takes at least, when that leaves blocks without work
   int whole;
-  int few;           // up to 32 requests: every warp plans for itself
+  int few;           // up to 256 requests (32 long ones): every warp plans for itself
 };
 
 struct PieceRecord {
@@ -244,24 +244,28 @@ MLDEV void deal_out(const AttentionParams& p, int cta, Schedule<ROWS, KEYS, OVER
   s.end = cta < s.ctas ? s.start_of(cta + 1) : s.start;
 }
 
-// The plan of few requests, a lane each; every warp by itself.
+// The plan of up to 256 requests (32 long ones), by every warp for itself: a lane has up to eight neighbouring ones.
 template <int ROWS, int KEYS, int OVER>
 MLDEV void plan_few(const AttentionParams& p, int cta, Schedule<ROWS, KEYS, OVER>& s, Walk<ROWS, KEYS, OVER>& w) {
   using S = Schedule<ROWS, KEYS, OVER>;
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, of_lane = (p.B + 31) >> 5, b0 = lane * of_lane;
   w.b = p.B;
+  int items = 0, mine = 0;
+  bool bad = false;
   Request r;
   r.q0 = r.n = r.kv = 0;
-  r.bad = false;
-  int items = 0, mine = 0;
-  if (lane < p.B) {
-    r = request_of(p, lane);
-    items = S::items_of(p, r);
-  }
-  if (ROWS <= kFewRows || !p.long_queries) {
+#pragma unroll 4
+  for (int k = 0; k < of_lane; ++k) {
+    if (b0 + k >= p.B) break;
+    r = request_of(p, b0 + k);
+    bad = bad || r.bad;
+    const int n = S::items_of(p, r);
+    items += n;
+    if (ROWS <= kFewRows || !p.long_queries)
 #pragma unroll 1
-    for (int i = 0; i < items; ++i) mine += S::weight_of(p, r, i);
-  } else {   // requests of many items: the lanes add up one after the other's
+      for (int i = 0; i < n; ++i) mine += S::weight_of(p, r, i);
+  }
+  if (ROWS > kFewRows && p.long_queries) {   // one of many items a lane: the lanes add up one after the other's
 #pragma unroll 1
     for (int b = 0; b < p.B; ++b) {
       Request other;
@@ -276,7 +280,7 @@ MLDEV void plan_few(const AttentionParams& p, int cta, Schedule<ROWS, KEYS, OVER
     }
   }
   mine *= p.Hk;
-  s.bad = __any_sync(0xffffffffu, r.bad);
+  s.bad = __any_sync(0xffffffffu, bad);
   int incl = mine;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -286,14 +290,26 @@ MLDEV void plan_few(const AttentionParams& p, int cta, Schedule<ROWS, KEYS, OVER
   deal_out(p, cta, s, __shfl_sync(0xffffffffu, incl, 31), __reduce_add_sync(0xffffffffu, items) * p.Hk);
   if (s.start == s.end) return;
   const int start = s.start;
-  w.b = __ffs(__ballot_sync(0xffffffffu, incl - mine <= start && start < incl)) - 1;
-  w.r.q0 = __shfl_sync(0xffffffffu, r.q0, w.b);
-  w.r.n = __shfl_sync(0xffffffffu, r.n, w.b);
-  w.r.kv = __shfl_sync(0xffffffffu, r.kv, w.b);
-  w.r.bad = false;
-  w.items = __shfl_sync(0xffffffffu, items, w.b);
-  const int before = __shfl_sync(0xffffffffu, incl - mine, w.b);
-  const int per = __shfl_sync(0xffffffffu, mine, w.b) / p.Hk;
+  // the lane whose requests have it, then which of them
+  const int l = __ffs(__ballot_sync(0xffffffffu, incl - mine <= start && start < incl)) - 1;
+  int before = __shfl_sync(0xffffffffu, incl - mine, l), all = __shfl_sync(0xffffffffu, mine, l);
+  w.b = l * of_lane;
+  w.r = request_of(p, w.b);
+  w.items = S::items_of(p, w.r);
+  if (of_lane > 1) {
+#pragma unroll 1
+    for (;;) {
+      all = 0;
+#pragma unroll 1
+      for (int i = 0; i < w.items; ++i) all += S::weight_of(p, w.r, i);
+      all *= p.Hk;
+      if (start < before + all) break;
+      before += all;
+      w.r = request_of(p, ++w.b);
+      w.items = S::items_of(p, w.r);
+    }
+  }
+  const int per = all / p.Hk;
   w.kh = (start - before) / per;
   int at = before + w.kh * per;
 #pragma unroll 1
