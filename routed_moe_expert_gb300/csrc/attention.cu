@@ -350,6 +350,8 @@ extern "C" moe_lora_status moe_lora_attention(moe_lora_handle* h, const moe_lora
   if (!aligned2(a->q) || !aligned2(a->out) || !aligned2(a->k_cache) || !aligned2(a->v_cache) || !aligned4(a->block_tables) ||
       !aligned4(a->kv_lens) || !aligned4(a->query_offsets) || !aligned4(a->lse))
     return MOE_LORA_ERR_INVALID_ARG;
+  if (a->out == a->q && ((a->T > 1 && a->out_stride_t != a->q_stride_t) || (a->q_heads > 1 && a->out_stride_h != a->q_stride_h)))
+    return MOE_LORA_ERR_INVALID_ARG;   // in place is row by row
   AttentionParams p;
   p.q = reinterpret_cast<const __nv_bfloat16*>(a->q);
   p.k = reinterpret_cast<const __nv_bfloat16*>(a->k_cache);

@@ -94,6 +94,12 @@ def test_attention_host_checks(built_lib, over, code):
     assert _call("moe_lora_attention", AttentionArgs, ATTEND, over, **kw) == code
 
 
+@pytest.mark.parametrize("over", [dict(q_t=1024), dict(q_h=128, o_t=1024, q_t=1024), dict(o_t=520)])
+def test_attention_in_place_takes_its_strides(built_lib, over):
+    """`out` that is q has its strides."""
+    assert _call("moe_lora_attention", AttentionArgs, ATTEND, over, ws=FAKE, nbytes=1 << 32) == 1
+
+
 def test_attention_workspace_never_less_for_more_rows(built_lib):
     for Hq, Hk, D in ((32, 4, 128), (7, 1, 96), (16, 16, 64), (64, 1, 128)):
         sizes = [B.moe_lora_attention_workspace_size(T, Hq, Hk, D)
