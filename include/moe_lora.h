@@ -621,7 +621,8 @@ typedef struct {
    both).  Any alignment of a bf16 element is taken; addresses and strides of whole 16-byte pieces are the
    fast case.  `workspace` (optional, 4 bytes): status word, DEVICE_CHECK when a slot lies past the cache
    (that token is left out); an empty batch does not write it.  One launch.
-   Errors: INVALID_ARG, UNSUPPORTED (head_dim > 512, T above 2^31 - 256), WORKSPACE_TOO_SMALL, CUDA. */
+   Errors: INVALID_ARG, UNSUPPORTED (head_dim > 512, T above 2^31 - 256, more than 65535 * 256 pieces a token: values of
+   all heads of k and v, by eight in the fast case), WORKSPACE_TOO_SMALL, CUDA. */
 moe_lora_status moe_lora_cache_write(moe_lora_handle* h, const moe_lora_cache_write_args* a, void* workspace,
                                      size_t workspace_bytes, moe_lora_stream stream);
 
@@ -633,7 +634,7 @@ typedef struct {
   const int32_t* block_tables;    /* [B, table_width]                                                  */
   const int32_t* kv_lens;         /* [B] keys of each request, its new tokens' among them              */
   const int32_t* query_offsets;   /* [B + 1] first query row of each request; NULL: row b is request b's */
-  moe_lora_bf16* out;             /* [T, q_heads, head_dim]; may be q itself                           */
+  moe_lora_bf16* out;             /* [T, q_heads, head_dim]; may be q itself, with its strides         */
   float* lse;                     /* [T, q_heads], optional: natural logarithm of the softmax's sum    */
   int64_t q_stride_t, q_stride_h, out_stride_t, out_stride_h;
   int64_t k_stride_page, k_stride_head, k_stride_token;
@@ -660,16 +661,20 @@ moe_lora_status moe_lora_attention_workspace_size(int T, int q_heads, int k_head
    as they are.  Keys and values that a row does not see, the rest of a last page among them, may hold anything;
    a value that is not finite makes those rows' results that see it infinite or NaN.
    shared_len names keys that all requests have in common (a common prompt): they are read from request 0's
-   table, once for all rows instead of once for each request; the results are the same up to float32 sums.
+   table, once for all rows instead of once for each request; the results are the same up to float32 sums.  That
+   table names the pages of all shared_len keys even where request 0 has fewer; a request sees no more than its
+   kv_lens.  (The fast case takes whole 128 keys of them so, and the rest as each request's own.)
    Scores, sums and the result are float32, rounded once at the end; the weights p_j are an operand of the
    tensor cores in between, as bf16 (two bf16 pieces where requests have up to 16 rows a key head).
-   head_dim a multiple of 8 up to 128, pages of a power of two of at least 16 tokens, and 16-byte pieces in q, out
-   and the caches are the fast case; anything else runs on plain cores.
+   head_dim a multiple of 8 up to 128, pages of a power of two of at least 16 tokens, 16-byte pieces in q, out
+   and the caches, and a scale other than 0 are the fast case; anything else runs on plain cores, and so does a batch
+   whose units of keys (64 or 128 for every 8, 16 or 256 rows of a key head, tables counted as full) come near 2^30.
    `workspace` (16-byte aligned, contents on entry do not matter) starts with the status word:
-   DEVICE_CHECK when query_offsets are not rising within [0, T], a length is negative or past its table, or a
-   page that is read lies outside the cache (its keys count as zeros); TIMEOUT when a bounded wait ran out.
+   DEVICE_CHECK when query_offsets are not rising within [0, T] (what the requests' rows hold is then undefined), a
+   length is negative or past its table (it counts as 0, or as what the table holds), or a page that is read lies
+   outside the cache (its keys count as zeros); TIMEOUT when a bounded wait ran out.  An empty batch does not write it.
    No atomics on values: the same call gives the same bits.
-   Errors: INVALID_ARG, UNSUPPORTED (head_dim > 512, sizes past 2^31 - 256), WORKSPACE_TOO_SMALL, CUDA. */
+   Errors: INVALID_ARG, UNSUPPORTED (head_dim > 512, T * q_heads above 2^31 - 256, B > 65535), WORKSPACE_TOO_SMALL, CUDA. */
 moe_lora_status moe_lora_attention(moe_lora_handle* h, const moe_lora_attention_args* a, void* workspace,
                                    size_t workspace_bytes, moe_lora_stream stream);
 

@@ -77,25 +77,25 @@ MLDEV int token_of(const AttentionParams& p, int row) {
 }
 
 // A request's rows [q0, q0 + n) and its keys, checked: rows within [0, T), at most width * page keys.
+constexpr int kBadLength = 1, kBadRows = 2;
 struct Request {
-  int q0, n, kv;
-  bool bad;
+  int q0, n, kv, bad;
 };
 MLDEV Request request_of(const AttentionParams& p, int b) {
   Request r;
-  r.bad = false;
+  r.bad = 0;
   if (p.offsets == nullptr) {
     r.q0 = b;
     r.n = 1;
   } else {
     const int lo = p.offsets[b], hi = p.offsets[b + 1];
-    r.bad = lo < 0 || hi < lo || hi > p.T;
+    if (lo < 0 || hi < lo || hi > p.T) r.bad = kBadRows;
     r.q0 = r.bad ? 0 : lo;
     r.n = r.bad ? 0 : hi - lo;
   }
   const int kv = p.kv_lens[b];
   const long long room = static_cast<long long>(p.width) * p.page;
-  r.bad = r.bad || kv < 0 || kv > room;
+  if (kv < 0 || kv > room) r.bad |= kBadLength;
   r.kv = static_cast<int>(min(static_cast<long long>(max(kv, 0)), room));
   return r;
 }
@@ -155,7 +155,7 @@ struct Schedule {
   int units;             // all items' weight
   int each, rest;        // units = each * ctas + rest
   int start, end;        // this block's run
-  bool bad;
+  int bad;               // of all requests; with kBadRows, no block works
 
   // What item i of a request weighs: its units (at least one, so that rows that see nothing are written) and OVER.
   static MLDEV int weight_of(const AttentionParams& p, const Request& r, int i) {
@@ -244,21 +244,27 @@ MLDEV void deal_out(const AttentionParams& p, int cta, Schedule<ROWS, KEYS, OVER
   s.end = cta < s.ctas ? s.start_of(cta + 1) : s.start;
 }
 
+// No work for any block: rows out of order may be several requests', whose weights' sum could pass 32 bits.
+template <int ROWS, int KEYS, int OVER>
+MLDEV void deal_nothing(Schedule<ROWS, KEYS, OVER>& s) {
+  s.ctas = 1;
+  s.units = s.each = s.rest = s.start = s.end = 0;
+}
+
 // The plan of up to 256 requests (32 long ones), by every warp for itself: a lane has up to eight neighbouring ones.
 template <int ROWS, int KEYS, int OVER>
 MLDEV void plan_few(const AttentionParams& p, int cta, Schedule<ROWS, KEYS, OVER>& s, Walk<ROWS, KEYS, OVER>& w) {
   using S = Schedule<ROWS, KEYS, OVER>;
   const int lane = threadIdx.x & 31, of_lane = (p.B + 31) >> 5, b0 = lane * of_lane;
   w.b = p.B;
-  int items = 0, mine = 0;
-  bool bad = false;
+  int items = 0, mine = 0, bad = 0;
   Request r;
   r.q0 = r.n = r.kv = 0;
 #pragma unroll 4
   for (int k = 0; k < of_lane; ++k) {
     if (b0 + k >= p.B) break;
     r = request_of(p, b0 + k);
-    bad = bad || r.bad;
+    bad |= r.bad;
     const int n = S::items_of(p, r);
     items += n;
     if (ROWS <= kFewRows || !p.long_queries)
@@ -280,7 +286,8 @@ MLDEV void plan_few(const AttentionParams& p, int cta, Schedule<ROWS, KEYS, OVER
     }
   }
   mine *= p.Hk;
-  s.bad = __any_sync(0xffffffffu, bad);
+  s.bad = static_cast<int>(__reduce_or_sync(0xffffffffu, static_cast<unsigned>(bad)));
+  if (s.bad & kBadRows) return deal_nothing(s);
   int incl = mine;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -343,13 +350,13 @@ __device__ __noinline__ void plan_many(const AttentionParams& p, int cta, Schedu
   const int tid = threadIdx.x, NT = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = NT >> 5;
   w.b = p.B;
   // What the requests b0 + tid of a chunk weigh, and their items.
-  auto chunk = [&](int b0, int& items, bool& bad) -> int {
+  auto chunk = [&](int b0, int& items, int& bad) -> int {
     int sum = 0;
     items = 0;
     if (b0 + tid < p.B) {
       const Request r = request_of(p, b0 + tid);
       items = S::items_of(p, r);
-      bad = bad || r.bad;
+      bad |= r.bad;
       if (ROWS <= kFewRows || !p.long_queries)
 #pragma unroll 1
         for (int i = 0; i < items; ++i) sum += S::weight_of(p, r, i);
@@ -371,8 +378,7 @@ __device__ __noinline__ void plan_many(const AttentionParams& p, int cta, Schedu
     }
     return sum * p.Hk;
   };
-  bool bad = false;
-  int total = 0, mine = 0, all_items = 0;
+  int bad = 0, total = 0, mine = 0, all_items = 0;
 #pragma unroll 1
   for (int b0 = 0; b0 < p.B; b0 += NT) {
     int items;
@@ -386,7 +392,8 @@ __device__ __noinline__ void plan_many(const AttentionParams& p, int cta, Schedu
     sm.sums[warp] = total;
     sm.items[warp] = all_items;
   }
-  s.bad = __syncthreads_or(bad) != 0;
+  s.bad = (__syncthreads_or(bad & kBadRows) ? kBadRows : 0) | (__syncthreads_or(bad & kBadLength) ? kBadLength : 0);
+  if (s.bad & kBadRows) return deal_nothing(s);
   deal_out(p, cta, s, __reduce_add_sync(0xffffffffu, lane < warps ? sm.sums[lane] : 0),
            __reduce_add_sync(0xffffffffu, lane < warps ? sm.items[lane] : 0));
   if (s.start == s.end) return;
@@ -396,8 +403,7 @@ __device__ __noinline__ void plan_many(const AttentionParams& p, int cta, Schedu
 #pragma unroll 1
   for (int b0 = 0; b0 < p.B; b0 += NT) {
     if (p.B > NT) {
-      int items;
-      bool ignored = false;
+      int items, ignored = 0;
       mine = chunk(b0, items, ignored);
     }
     int incl = mine;
