@@ -164,25 +164,36 @@ MLDEV void join_results(const float2* ml, const float* part, int n, int per_row,
   __syncthreads();
 }
 
-// The pieces of items that were cut: blocks (x, .) take record x, if it is one, and its rows by team.  The result is
-// final, or with shared keys the last part of the row.
+// A kernel's pieces: records by block, of which `across` blocks here take each.
+struct Pieces {
+  const PieceRecord* records;
+  const float2* ml;
+  const float* o;
+  int item_rows, ctas, across;
+};
+
+// The pieces of items that were cut, of the tiles' kernel and that for few rows together: `across` blocks take a record, if
+// it is one, and its rows by team.  The result is final, or with shared keys the last part of the row.
 template <int DP>
-__global__ void __launch_bounds__(kTeams * DP / 8) attention_join_kernel(const __grid_constant__ AttentionParams p) {
+__global__ void __launch_bounds__(kTeams * DP / 8) attention_join_kernel(const __grid_constant__ AttentionParams p, const Pieces first,
+                                                                         const Pieces second) {
+  const bool later = static_cast<int>(blockIdx.x) >= first.ctas * first.across;
+  const Pieces& x = later ? second : first;
+  const int at = static_cast<int>(blockIdx.x) - (later ? first.ctas * first.across : 0);
+  const int share = at / x.ctas, cta = at - share * x.ctas;   // (blocks with rows come first, since most items have few)
   pdl_wait();
   pdl_trigger();
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && p.alone) take_status(p);
-  const PieceRecord c = p.records[blockIdx.x];
+  if (blockIdx.x == 0 && threadIdx.x == 0 && p.alone) take_status(p);
+  const PieceRecord c = x.records[cta];
   if (c.pieces == 0) return;
   const int per_row = teams_per_row(c.pieces), at_once = kTeams / per_row;
   const int team = threadIdx.x / (DP / 8), d = (threadIdx.x % (DP / 8)) * 8;
-  for (int r0 = static_cast<int>(blockIdx.y) * at_once; r0 < c.rows; r0 += static_cast<int>(gridDim.y) * at_once) {
+  for (int r0 = share * at_once; r0 < c.rows; r0 += x.across * at_once) {
     const int r = r0 + team / per_row;
     float m, l, o[8];
     join_results<DP>(
-        p.piece_ml, p.piece_o, c.pieces, per_row, r < c.rows,
-        [&](int i) {
-          return static_cast<long long>(i == 0 ? c.slot : 2 * (static_cast<int>(blockIdx.x) + i)) * p.item_rows + r;
-        },
+        x.ml, x.o, c.pieces, per_row, r < c.rows,
+        [&](int i) { return static_cast<long long>(i == 0 ? c.slot : 2 * (cta + i)) * x.item_rows + r; },
         m, l, o);
     if (r >= c.rows || team % per_row != 0) continue;
     const long long token = c.q0 + token_of(p, c.row0 + r);
@@ -190,11 +201,11 @@ __global__ void __launch_bounds__(kTeams * DP / 8) attention_join_kernel(const _
     if (p.prefix_splits == 0) {
       write_row8(p, token, head, d, m, l, o);
     } else {
-      const long long at = part_row(p, token, head);
-      float4* to = reinterpret_cast<float4*>(p.part_o + at * DP + d);
+      const long long part = part_row(p, token, head);
+      float4* to = reinterpret_cast<float4*>(p.part_o + part * DP + d);
       to[0] = make_float4(o[0], o[1], o[2], o[3]);
       to[1] = make_float4(o[4], o[5], o[6], o[7]);
-      if (d == 0) p.part_ml[at] = make_float2(m, l);
+      if (d == 0) p.part_ml[part] = make_float2(m, l);
     }
   }
 }
@@ -219,10 +230,15 @@ __global__ void __launch_bounds__(kTeams * DP / 8) attention_fold_kernel(const _
   if (real && team % per_row == 0) write_row8(p, token, r - token * p.Hq, d, m, l, o);
 }
 
-cudaError_t launch_join(const AttentionParams& p, int dp, int across, cudaStream_t stream) {
-  const dim3 grid(p.plan.ctas, across), block(kTeams * dp / 8);
-  return dp == 64 ? launch_k(attention_join_kernel<64>, grid, block, 0, stream, true, p)
-                  : launch_k(attention_join_kernel<128>, grid, block, 0, stream, true, p);
+// Blocks to a record: its rows by sixteen, and four for few rows, so that items of many pieces are joined side by side.
+Pieces pieces_of(const AttentionParams& p, bool any) {
+  const int across = p.item_rows <= kFewRows ? std::min(4, p.item_rows) : (p.item_rows + kTeams - 1) / kTeams;
+  return any ? Pieces{p.records, p.piece_ml, p.piece_o, p.item_rows, p.plan.ctas, across} : Pieces{nullptr, nullptr, nullptr, 0, 0, 1};
+}
+cudaError_t launch_join(const AttentionParams& p, const Pieces& first, const Pieces& second, int dp, cudaStream_t stream) {
+  const dim3 grid(first.ctas * first.across + second.ctas * second.across), block(kTeams * dp / 8);
+  return dp == 64 ? launch_k(attention_join_kernel<64>, grid, block, 0, stream, true, p, first, second)
+                  : launch_k(attention_join_kernel<128>, grid, block, 0, stream, true, p, first, second);
 }
 cudaError_t launch_fold(const AttentionParams& p, int dp, cudaStream_t stream) {
   const int per_row = teams_per_row(p.prefix_splits + 1);
@@ -479,13 +495,9 @@ extern "C" moe_lora_status moe_lora_attention(moe_lora_handle* h, const moe_lora
     few.alone = !join_tiles && !join_few && !fold;
     ML_LAUNCH(h, launch_attention_rows(few, dp, eight, stream), "attention launch");
   }
-  if (join_tiles) {
-    p.alone = !join_few && !fold;
-    ML_LAUNCH(h, launch_join(p, dp, (p.item_rows + kTeams - 1) / kTeams, stream), "attention join launch");
-  }
-  if (join_few) {
-    few.alone = !fold;
-    ML_LAUNCH(h, launch_join(few, dp, std::min(4, few.item_rows), stream), "attention join launch");
+  if (join_tiles || join_few) {
+    p.alone = !fold;
+    ML_LAUNCH(h, launch_join(p, pieces_of(p, join_tiles), pieces_of(few, join_few), dp, stream), "attention join launch");
   }
   if (fold) ML_LAUNCH(h, launch_fold(p, dp, stream), "attention fold launch");
   return MOE_LORA_OK;
