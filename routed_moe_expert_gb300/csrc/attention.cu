@@ -251,6 +251,7 @@ cudaError_t launch_fold(const AttentionParams& p, int dp, cudaStream_t stream) {
 // The status word; records and pieces (2 slots a block) of the tiles' kernel, and of that for few rows; the parts of each
 // row where keys are shared.
 // Every part grows with T alone, so what is enough for T rows is enough for fewer.
+constexpr int kWholeUnits = 10;   // see moe_lora_attention
 constexpr int kMaxSms = 160;   // blocks are a multiple of the GPU's 152
 constexpr int kPrefixSplits = 64, kPrefixBlocks = 2 * kMaxSms;
 constexpr size_t round256(size_t n) { return (n + 255) / 256 * 256; }
@@ -412,10 +413,16 @@ extern "C" moe_lora_status moe_lora_attention(moe_lora_handle* h, const moe_lora
   // what the kernels' 32-bit arithmetic holds: rows divided by G (token_of), and the weight of all items, at most
   const long long group_rows = static_cast<long long>(p.T) * p.G;
   const long long own_most = static_cast<long long>(p.width) * p.page;
-  // Requests of up to 8 rows a key head (16, where the heads alone are more than 8) run on the kernel for few rows, the
-  // others on tiles; in a batch that may have both, each kernel takes its own.
+  // Up to 16 rows a key head run on the kernel for few rows, more on tiles (4 drafts of 7 heads, 24 requests: 44.9 us on
+  // tiles, 65.3 on the other; of 4 heads 43.9 and 41.7).  A batch that may have both, by its longest request and the rows left
+  // to the others, is split by request, each kernel taking its own, where the short ones have an item for every SM: 256
+  // requests of one token on 1000 keys beside a prompt of 512 128 us, 160 on tiles alone; with 32 of them 67.2 and 64.5.
   const bool tiles = static_cast<long long>(a->max_query_len) * p.G > kFewRows;
-  const bool mixed = tiles && a->B > 1 && p.offsets != nullptr && static_cast<long long>(a->max_query_len) * a->B != p.T;
+  const bool eight = (tiles ? p.G : static_cast<long long>(a->max_query_len) * p.G) <= 8;
+  const int few_rows = eight ? 8 : kFewRows;
+  const long long others = p.B - 1LL;
+  const bool mixed = tiles && p.offsets != nullptr && p.G <= few_rows && others * p.Hk > h->num_sms &&
+                     (p.T - static_cast<long long>(a->max_query_len)) * p.G <= 2 * others * few_rows;
   const long long few_items = tiles ? 2LL * p.B : group_rows / 8 + p.B;
   const bool fits = std::max<long long>(group_rows, p.Hq) * p.G < (1LL << 32) &&
                     (!tiles || (group_rows / kTileRows + p.B) * p.Hk * (own_most / kTileKeys + 1 + kTileOver) < (1LL << 30)) &&
@@ -445,17 +452,24 @@ extern "C" moe_lora_status moe_lora_attention(moe_lora_handle* h, const moe_lora
     return page_map(h, &x.tmap_k, x.k, x, x.k_t, x.k_h, x.k_p, keys, both) &&
            page_map(h, &x.tmap_v, x.v, x, x.v_t, x.v_h, x.v_p, keys, both);
   };
-  const bool eight = mixed ? p.G <= 8 : static_cast<long long>(a->max_query_len) * p.G <= 8;
   const long long own_keys = static_cast<long long>(p.width) * p.page - p.shared;   // of a request, at most
   AttentionParams few = p;
   if ((tiles || p.shared > 0) && !maps(p, kTileKeys, false)) return cuda_fail(cudaErrorInvalidValue, "attention tensor maps");
   if ((!tiles || mixed) && !maps(few, kFewKeys, p.both_halves)) return cuda_fail(cudaErrorInvalidValue, "attention tensor maps");
-  auto plan_for = [&](AttentionParams& x, int ctas, int least, int whole_keys) {
+  auto plan_for = [&](AttentionParams& x, int ctas, bool whole, int least, int whole_units) {
     x.plan.ctas = ctas;
+    x.plan.whole = whole;
     x.plan.least = least;
-    x.plan.whole = own_keys <= whole_keys;
+    x.plan.whole_units = whole_units;
     x.plan.few = p.B <= (x.long_queries ? 32 : 256);
   };
+  // Items are whole, without pieces and the launch that joins them, where tables hold few keys.  On tiles: 4 units (16
+  // prompts of 200 35.0 us, cut 39.0), or 10 where there are many items (a prompt of 512 17.3 us, cut 20.9, of 1024 23.7 and
+  // 30.1; but 8 drafts of one request on 1000 keys 16.6, cut 13.9).  Few rows: 8 units (64 requests of up to 300 keys
+  // 13.4 us, cut 14.8; with four times as much one request of 700 keys took 13.5 us, cut 9.5).
+  const long long most_items = std::max<long long>(group_rows / kTileRows, std::min(p.B, p.T)) * p.Hk;
+  const bool tiles_whole = own_keys <= 4 * kTileKeys || (own_keys <= kWholeUnits * kTileKeys && 3 * most_items >= h->num_sms);
+  const bool few_whole = own_keys <= 8 * kFewKeys;
   p.follows = few.follows = 0;
   p.alone = few.alone = 0;
   p.few_rows = few.few_rows = 0;
@@ -471,20 +485,20 @@ extern "C" moe_lora_status moe_lora_attention(moe_lora_handle* h, const moe_lora
   const bool fold = p.prefix_splits > 0;
   p.item_rows = slot_rows(true, p.T, p.G);
   p.long_queries = static_cast<long long>(a->max_query_len) * p.G > 8LL * kTileRows;
-  plan_for(p, h->num_sms, 2, 4 * kTileKeys);
+  plan_for(p, h->num_sms, tiles_whole, 2, kWholeUnits);
   p.piece_ml = reinterpret_cast<float2*>(base + at.ml);
   p.piece_o = reinterpret_cast<float*>(base + at.o);
   p.records = p.plan.whole ? nullptr : reinterpret_cast<PieceRecord*>(base + at.records);
   few.item_rows = slot_rows(false, p.T, p.G);
   few.long_queries = 0;
-  plan_for(few, kFewPerSm * h->num_sms, 2, 8 * kFewKeys);
+  plan_for(few, kFewPerSm * h->num_sms, few_whole, few_whole ? 1 + kFewOver : 2, 0);
   few.piece_ml = reinterpret_cast<float2*>(base + at.few_ml);
   few.piece_o = reinterpret_cast<float*>(base + at.few_o);
   few.records = few.plan.whole ? nullptr : reinterpret_cast<PieceRecord*>(base + at.few_records);
   const bool join_tiles = tiles && !p.plan.whole, join_few = (!tiles || mixed) && !few.plan.whole;
   if (mixed) {
-    few.few_rows = eight ? 8 : kFewRows;
-    p.few_rows = -few.few_rows;
+    few.few_rows = few_rows;
+    p.few_rows = -few_rows;
   }
   if (tiles) {
     p.alone = !mixed && !join_tiles && !fold;

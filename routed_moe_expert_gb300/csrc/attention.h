@@ -6,7 +6,7 @@
 namespace mlk {
 
 // Items of the kernel for few rows (attention_rows.cu) and of the tiles' (attention_tiles.cu).
-constexpr int kFewRows = 16, kFewKeys = 64, kFewPerSm = 2, kFewOver = 1;
+constexpr int kFewRows = 16, kFewKeys = 64, kFewPerSm = 2, kFewOver = 3;
 constexpr int kTileRows = 256, kTileKeys = 128, kTileOver = 4;
 
 // How a call's work is dealt out.  Rows of a request and key head are its query rows times the G query
@@ -19,11 +19,12 @@ constexpr int kTileRows = 256, kTileKeys = 128, kTileOver = 4;
 // sums, maximum, sum of weights) in the workspace, at most two a block, and the block that has the item's
 // first unit leaves a record, by which the kernel that follows adds the pieces up.
 //
-// With `whole` (no item is long) items are not cut: a block takes those whose first unit is in its run.
+// With `whole` (no item is long) items are not cut: a block takes those whose first unit is in its run.  `whole_units` is the
+// same by the lengths themselves: where no item has more units, and there are items for a third of the blocks.
 struct Plan {
   int ctas;          // blocks of the launch
   int least;         // units that a block takes at least, when that leaves blocks without work
-  int whole;
+  int whole, whole_units;
   int few;           // up to 256 requests (32 long ones): every warp plans for itself
 };
 
@@ -156,6 +157,7 @@ struct Schedule {
   int each, rest;        // units = each * ctas + rest
   int start, end;        // this block's run
   int bad;               // of all requests; with kBadRows, no block works
+  int whole;             // items are not cut
 
   // What item i of a request weighs: its units (at least one, so that rows that see nothing are written) and OVER.
   static MLDEV int weight_of(const AttentionParams& p, const Request& r, int i) {
@@ -229,14 +231,15 @@ struct Walk {
 };
 
 struct ScheduleSmem {
-  int sums[32], items[32];
+  int sums[32], items[32], most[32];
   int found_base, found_b, found_i, found_u, found_kh;
 };
 
-// The blocks that work, and this one's run.
+// The blocks that work, and this one's run.  `most`: what the largest item weighs.
 template <int ROWS, int KEYS, int OVER>
-MLDEV void deal_out(const AttentionParams& p, int cta, Schedule<ROWS, KEYS, OVER>& s, int units, int items) {
+MLDEV void deal_out(const AttentionParams& p, int cta, Schedule<ROWS, KEYS, OVER>& s, int units, int items, int most) {
   s.units = units;
+  s.whole = p.plan.whole || (most <= p.plan.whole_units + OVER && 3 * items >= p.plan.ctas);
   s.ctas = max(1, min(p.plan.ctas, max(units / p.plan.least, items)));
   s.each = units / s.ctas;
   s.rest = units - s.each * s.ctas;
@@ -248,7 +251,7 @@ MLDEV void deal_out(const AttentionParams& p, int cta, Schedule<ROWS, KEYS, OVER
 template <int ROWS, int KEYS, int OVER>
 MLDEV void deal_nothing(Schedule<ROWS, KEYS, OVER>& s) {
   s.ctas = 1;
-  s.units = s.each = s.rest = s.start = s.end = 0;
+  s.units = s.each = s.rest = s.start = s.end = s.whole = 0;
 }
 
 // The plan of up to 256 requests (32 long ones), by every warp for itself: a lane has up to eight neighbouring ones.
@@ -257,7 +260,7 @@ MLDEV void plan_few(const AttentionParams& p, int cta, Schedule<ROWS, KEYS, OVER
   using S = Schedule<ROWS, KEYS, OVER>;
   const int lane = threadIdx.x & 31, of_lane = (p.B + 31) >> 5, b0 = lane * of_lane;
   w.b = p.B;
-  int items = 0, mine = 0, bad = 0;
+  int items = 0, mine = 0, bad = 0, most = 0;
   Request r;
   r.q0 = r.n = r.kv = 0;
 #pragma unroll 4
@@ -267,6 +270,7 @@ MLDEV void plan_few(const AttentionParams& p, int cta, Schedule<ROWS, KEYS, OVER
     bad |= r.bad;
     const int n = S::items_of(p, r);
     items += n;
+    if (ROWS > kFewRows && n > 0) most = max(most, S::weight_of(p, r, n - 1));   // (the last item sees most)
     if (ROWS <= kFewRows || !p.long_queries)
 #pragma unroll 1
       for (int i = 0; i < n; ++i) mine += S::weight_of(p, r, i);
@@ -294,7 +298,8 @@ MLDEV void plan_few(const AttentionParams& p, int cta, Schedule<ROWS, KEYS, OVER
     const int u = __shfl_up_sync(0xffffffffu, incl, off);
     if (lane >= off) incl += u;
   }
-  deal_out(p, cta, s, __shfl_sync(0xffffffffu, incl, 31), __reduce_add_sync(0xffffffffu, items) * p.Hk);
+  deal_out(p, cta, s, __shfl_sync(0xffffffffu, incl, 31), __reduce_add_sync(0xffffffffu, items) * p.Hk,
+           ROWS > kFewRows ? __reduce_max_sync(0xffffffffu, most) : 0x7fffffff);
   if (s.start == s.end) return;
   const int start = s.start;
   // the lane whose requests have it, then which of them
@@ -350,6 +355,7 @@ __device__ __noinline__ void plan_many(const AttentionParams& p, int cta, Schedu
   const int tid = threadIdx.x, NT = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = NT >> 5;
   w.b = p.B;
   // What the requests b0 + tid of a chunk weigh, and their items.
+  int most = 0;
   auto chunk = [&](int b0, int& items, int& bad) -> int {
     int sum = 0;
     items = 0;
@@ -357,6 +363,7 @@ __device__ __noinline__ void plan_many(const AttentionParams& p, int cta, Schedu
       const Request r = request_of(p, b0 + tid);
       items = S::items_of(p, r);
       bad |= r.bad;
+      if (ROWS > kFewRows && items > 0) most = max(most, S::weight_of(p, r, items - 1));
       if (ROWS <= kFewRows || !p.long_queries)
 #pragma unroll 1
         for (int i = 0; i < items; ++i) sum += S::weight_of(p, r, i);
@@ -388,14 +395,17 @@ __device__ __noinline__ void plan_many(const AttentionParams& p, int cta, Schedu
   }
   total = __reduce_add_sync(0xffffffffu, total);
   all_items = __reduce_add_sync(0xffffffffu, all_items);
+  most = __reduce_max_sync(0xffffffffu, most);
   if (lane == 0) {
     sm.sums[warp] = total;
     sm.items[warp] = all_items;
+    sm.most[warp] = most;
   }
   s.bad = (__syncthreads_or(bad & kBadRows) ? kBadRows : 0) | (__syncthreads_or(bad & kBadLength) ? kBadLength : 0);
   if (s.bad & kBadRows) return deal_nothing(s);
   deal_out(p, cta, s, __reduce_add_sync(0xffffffffu, lane < warps ? sm.sums[lane] : 0),
-           __reduce_add_sync(0xffffffffu, lane < warps ? sm.items[lane] : 0));
+           __reduce_add_sync(0xffffffffu, lane < warps ? sm.items[lane] : 0),
+           ROWS > kFewRows ? __reduce_max_sync(0xffffffffu, lane < warps ? sm.most[lane] : 0) : 0x7fffffff);
   if (s.start == s.end) return;
   // the request that has unit `start`
   __syncthreads();
@@ -482,7 +492,7 @@ struct Part {
 template <int ROWS, int KEYS, int OVER>
 MLDEV Part part_of(const AttentionParams& p, const Schedule<ROWS, KEYS, OVER>& s, const Walk<ROWS, KEYS, OVER>& w, int cta) {
   Part x;
-  if (p.plan.whole) {
+  if (s.whole) {
     x.lo = 0;
     x.hi = w.u0 < s.start ? 0 : w.units - OVER;   // hi 0: begun in the run of a block before
     x.all = true;

@@ -48,6 +48,21 @@ def test_shared_keys_of_many_requests(handle, B, rows):  # noqa: F811
     _attention(handle, lens, 8, 2, 64, 32, seed=B, shared=256)
 
 
+@pytest.mark.parametrize("B,long", [(200, 40), (300, 300)])
+def test_shared_keys_of_many_requests_beside_a_long_one(handle, B, long):  # noqa: F811
+    r = random.Random(B)
+    lens = [(256 + r.randint(1, 60), r.randint(0, 1)) for _ in range(B)]
+    lens[7] = (256 + long + 9, long)
+    _attention(handle, lens, 8, 2, 64, 32, seed=B, shared=256)
+
+
+@pytest.mark.parametrize("lens", [[(1024, 1024)], [(1280, 1280)], [(1281, 700)], [(700, 400)] * 3, [(1100, 130)] * 5 + [(0, 0)] * 30])
+@pytest.mark.parametrize("wide", [0, 70])
+def test_whole_items_by_length(handle, lens, wide):  # noqa: F811
+    """Prompts about the length up to which items are not cut, in tables as long as they are, and longer ones."""
+    _attention(handle, lens + [(wide * 32, 0)], 16, 8, 64, 32, seed=wide)
+
+
 def test_pages_named_twice(handle):  # noqa: F811
     """Requests that share pages without saying so, and one whose table names a page again and again."""
     g = torch.Generator().manual_seed(8)
