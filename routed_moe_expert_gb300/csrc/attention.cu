@@ -230,9 +230,11 @@ __global__ void __launch_bounds__(kTeams * DP / 8) attention_fold_kernel(const _
   if (real && team % per_row == 0) write_row8(p, token, r - token * p.Hq, d, m, l, o);
 }
 
-// Blocks to a record: its rows by sixteen, and four for few rows, so that items of many pieces are joined side by side.
-Pieces pieces_of(const AttentionParams& p, bool any) {
-  const int across = p.item_rows <= kFewRows ? std::min(4, p.item_rows) : (p.item_rows + kTeams - 1) / kTeams;
+// Blocks to a record: four for few rows; of tiles a block for every 16 rows, or 8 where the items are few, and so of many
+// pieces each (64 tokens on 4000 keys 26.2 us for 30.5; but 24 requests of 4 drafts 55.4 for 54.4, of blocks with nothing to do).
+Pieces pieces_of(const AttentionParams& p, bool any, bool few_items) {
+  const int each = few_items ? kTeams / 2 : kTeams;
+  const int across = p.item_rows <= kFewRows ? std::min(4, p.item_rows) : (p.item_rows + each - 1) / each;
   return any ? Pieces{p.records, p.piece_ml, p.piece_o, p.item_rows, p.plan.ctas, across} : Pieces{nullptr, nullptr, nullptr, 0, 0, 1};
 }
 cudaError_t launch_join(const AttentionParams& p, const Pieces& first, const Pieces& second, int dp, cudaStream_t stream) {
@@ -251,7 +253,7 @@ cudaError_t launch_fold(const AttentionParams& p, int dp, cudaStream_t stream) {
 // The status word; records and pieces (2 slots a block) of the tiles' kernel, and of that for few rows; the parts of each
 // row where keys are shared.
 // Every part grows with T alone, so what is enough for T rows is enough for fewer.
-constexpr int kWholeUnits = 10;   // see moe_lora_attention
+constexpr int kWholeUnits = 12;   // see moe_lora_attention
 constexpr int kMaxSms = 160;   // blocks are a multiple of the GPU's 152
 constexpr int kPrefixSplits = 64, kPrefixBlocks = 2 * kMaxSms;
 constexpr size_t round256(size_t n) { return (n + 255) / 256 * 256; }
@@ -464,9 +466,9 @@ extern "C" moe_lora_status moe_lora_attention(moe_lora_handle* h, const moe_lora
     x.plan.few = p.B <= (x.long_queries ? 32 : 256);
   };
   // Items are whole, without pieces and the launch that joins them, where tables hold few keys.  On tiles: 4 units (16
-  // prompts of 200 35.0 us, cut 39.0), or 10 where there are many items (a prompt of 512 17.3 us, cut 20.9, of 1024 23.7 and
-  // 30.1; but 8 drafts of one request on 1000 keys 16.6, cut 13.9).  Few rows: 8 units (64 requests of up to 300 keys
-  // 13.4 us, cut 14.8; with four times as much one request of 700 keys took 13.5 us, cut 9.5).
+  // prompts of 200 35.0 us, cut 39.0), or 12 where there are many items (a prompt of 512 17.3 us, cut 20.9, of 1500 38.6 and
+  // 40.3; but 8 drafts of one request on 1000 keys 16.6, cut 13.9, and with 16 units a prompt of 2048 61.0, cut 53.3).  Few
+  // rows: 8 units (64 requests of up to 300 keys 13.4 us, cut 14.8; with 16 one request of 700 keys took 13.6 us, cut 9.2).
   const long long most_items = std::max<long long>(group_rows / kTileRows, std::min(p.B, p.T)) * p.Hk;
   const bool tiles_whole = own_keys <= 4 * kTileKeys || (own_keys <= kWholeUnits * kTileKeys && 3 * most_items >= h->num_sms);
   const bool few_whole = own_keys <= 8 * kFewKeys;
@@ -511,7 +513,7 @@ extern "C" moe_lora_status moe_lora_attention(moe_lora_handle* h, const moe_lora
   }
   if (join_tiles || join_few) {
     p.alone = !fold;
-    ML_LAUNCH(h, launch_join(p, pieces_of(p, join_tiles), pieces_of(few, join_few), dp, stream), "attention join launch");
+    ML_LAUNCH(h, launch_join(p, pieces_of(p, join_tiles, 8 * most_items <= h->num_sms), pieces_of(few, join_few, false), dp, stream), "attention join launch");
   }
   if (fold) ML_LAUNCH(h, launch_fold(p, dp, stream), "attention fold launch");
   return MOE_LORA_OK;
