@@ -10,21 +10,34 @@
 namespace mlk {
 namespace {
 
+MLDEV float low_half(uint32_t x) { return __uint_as_float(x << 16); }    // of two bf16
+MLDEV float high_half(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
+
 // ---------------------------------------------------------------------------------------
 // Any head size, page size and alignment, on plain cores: a block per query row and head.  Its warps take
 // the keys 32 at a time in turn, a lane a key, each warp with a running maximum m, sum l and result o
-// (o <- o 2^(m - m') + sum p v), and the block adds the warps' results at the end.
+// (o <- o 2^(m - m') + sum p v), and the block adds the warps' results at the end.  Bound by loads from L2: every head of
+// a group reads its keys again.  16 requests on 4000 keys, 32 + 4 heads of 128, pages of 48: 215 us (value by value, as
+// where pieces of 16 bytes do not fit, 1245); heads of 192 360, heads of 100 649; a prompt of 512 461.
 // ---------------------------------------------------------------------------------------
 constexpr int kAnyWarps = 8;
 
+// V: values of a piece, 8 where head size, addresses and strides allow.  Then a lane reads its key by pieces, and the values
+// a lane a piece, as many keys side by side as fit into a warp.
+template <int V>
 __global__ void __launch_bounds__(32 * kAnyWarps) attention_any_kernel(const __grid_constant__ AttentionParams p) {
-  __shared__ float q_s[512];
+  constexpr int kPasses = 512 / (32 * V);   // of a warp over a row's pieces, at most
+  __shared__ __align__(16) float q_s[512];
   __shared__ float o_s[kAnyWarps][512];
   __shared__ float m_s[kAnyWarps], l_s[kAnyWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
   pdl_trigger();
   const int b = static_cast<int>(blockIdx.y), h = static_cast<int>(blockIdx.z), kh = h / p.G;
+  const int pieces = p.D / V;
+  int of_key = 32;   // lanes to a key's values
+  while (of_key / 2 >= pieces && of_key > 1) of_key /= 2;
+  const int side = 32 / of_key, mine = lane / of_key, piece0 = lane - mine * of_key;
   const Request r = request_of(p, b);
   if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0 && r.bad) record_status(p.status, kDevBadSlot, kWhereAttention);
   for (int i = static_cast<int>(blockIdx.x); i < r.n; i += static_cast<int>(gridDim.x)) {
@@ -34,9 +47,11 @@ __global__ void __launch_bounds__(32 * kAnyWarps) attention_any_kernel(const __g
     const int sees = max(r.kv - r.n + i + 1, 0);
     const int of_shared = min(sees, p.shared);
     float m = -INFINITY, l = 0.0f;
-    float o[16];
+    float o[kPasses][V];
 #pragma unroll
-    for (int c = 0; c < 16; ++c) o[c] = 0.0f;
+    for (int c = 0; c < kPasses; ++c)
+#pragma unroll
+      for (int e = 0; e < V; ++e) o[c][e] = 0.0f;
     for (int j0 = warp * 32; j0 < sees; j0 += 32 * kAnyWarps) {
       const int j = j0 + lane;
       int page = -1;
@@ -50,7 +65,17 @@ __global__ void __launch_bounds__(32 * kAnyWarps) attention_any_kernel(const __g
         float dot = 0.0f;
         if (page >= 0) {
           const __nv_bfloat16* k = p.k + page * p.k_p + kh * p.k_h + (j % p.page) * p.k_t;
-          for (int d = 0; d < p.D; ++d) dot += q_s[d] * bf2f(k[d]);
+          if constexpr (V == 8) {
+#pragma unroll 8
+            for (int c = 0; c < pieces; ++c) {
+              const uint4 x = *reinterpret_cast<const uint4*>(k + 8 * c);
+              const uint32_t x4[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) dot += q_s[8 * c + 2 * e] * low_half(x4[e]) + q_s[8 * c + 2 * e + 1] * high_half(x4[e]);
+            }
+          } else {
+            for (int d = 0; d < p.D; ++d) dot += q_s[d] * bf2f(k[d]);
+          }
         }
         s = dot * p.scale_log2;
       }
@@ -65,21 +90,48 @@ __global__ void __launch_bounds__(32 * kAnyWarps) attention_any_kernel(const __g
       l = l * old + sum;
       m = m2;
 #pragma unroll
-      for (int c = 0; c < 16; ++c) o[c] *= old;
-      const int n = min(32, sees - j0);
-      for (int t = 0; t < n; ++t) {
-        const float wt = __shfl_sync(0xffffffffu, w, t);
-        const int pg = __shfl_sync(0xffffffffu, page, t);
-        if (pg < 0) continue;
-        const __nv_bfloat16* v = p.v + pg * p.v_p + kh * p.v_h + ((j0 + t) % p.page) * p.v_t;
+      for (int c = 0; c < kPasses; ++c)
 #pragma unroll
-        for (int c = 0; c < 16; ++c)
-          if (c * 32 + lane < p.D) o[c] += wt * bf2f(v[c * 32 + lane]);
+        for (int e = 0; e < V; ++e) o[c][e] *= old;
+      const int n = min(32, sees - j0);
+      const __nv_bfloat16* row = page < 0 ? nullptr : p.v + page * p.v_p + kh * p.v_h + (j % p.page) * p.v_t;
+#pragma unroll 4
+      for (int t0 = 0; t0 < n; t0 += side) {
+        const int t = t0 + mine;   // (below 32; the weight of a key from n on is 0, and its page none)
+        const float wt = __shfl_sync(0xffffffffu, w, t);
+        const __nv_bfloat16* v =
+            reinterpret_cast<const __nv_bfloat16*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), t));
+        if (v == nullptr) continue;
+#pragma unroll
+        for (int c = 0; c < kPasses; ++c) {
+          const int piece = c * 32 + piece0;
+          if (piece >= pieces) break;
+          if constexpr (V == 8) {
+            const uint4 x = *reinterpret_cast<const uint4*>(v + 8 * piece);
+            const uint32_t x4[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              o[c][2 * e] += wt * low_half(x4[e]);
+              o[c][2 * e + 1] += wt * high_half(x4[e]);
+            }
+          } else {
+            o[c][0] += wt * bf2f(v[piece]);
+          }
+        }
       }
     }
+    for (int off = of_key; off < 32; off <<= 1)   // keys side by side
 #pragma unroll
-    for (int c = 0; c < 16; ++c)
-      if (c * 32 + lane < p.D) o_s[warp][c * 32 + lane] = o[c];
+      for (int c = 0; c < kPasses; ++c)
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[c][e] += __shfl_xor_sync(0xffffffffu, o[c][e], off);
+#pragma unroll
+    for (int c = 0; c < kPasses; ++c) {
+      const int piece = c * 32 + piece0;
+      if (mine == 0 && piece < pieces)
+#pragma unroll
+        for (int e = 0; e < V; ++e) o_s[warp][piece * V + e] = o[c][e];
+    }
     if (lane == 0) {
       m_s[warp] = m;
       l_s[warp] = l;
@@ -104,7 +156,9 @@ __global__ void __launch_bounds__(32 * kAnyWarps) attention_any_kernel(const __g
 // ---------------------------------------------------------------------------------------
 // Results of a row from several places together.  Sixteen teams of threads a block, DP / 8 threads a team with eight
 // values each; `per_row` teams (1, 4 or 16, by the number of results) take those of a row in turn, so that the 76
-// pieces of a long request are five loads deep, and are added in order.
+// pieces of a long request are five loads deep, and are added in order.  (Fewer teams are slower where there are many
+// pieces: one request on 1000 keys 11.8 us for 9.4; more where there are few: 64 tokens on 4000 keys 41 us for 30.)
+// Bound by latency, and by the L2 reads of the pieces: 2.5 us behind the 6.7 of one request's 700 keys, beginning early.
 // ---------------------------------------------------------------------------------------
 constexpr int kTeams = 16;
 
@@ -432,7 +486,10 @@ extern "C" moe_lora_status moe_lora_attention(moe_lora_handle* h, const moe_lora
   if (!fast_layout(a) || !fits || p.scale_log2 == 0.0f || h->num_sms > kMaxSms) {
     ML_CUDA(cudaMemsetAsync(workspace, 0, 4, stream), "attention status");
     const int across = std::max(1, std::min(a->T, 65536 / std::max(1, a->B)));
-    ML_LAUNCH(h, launch_k(attention_any_kernel, dim3(across, a->B, a->q_heads), dim3(32 * kAnyWarps), 0, stream, false, p),
+    uintptr_t bits = reinterpret_cast<uintptr_t>(p.k) / 2 | reinterpret_cast<uintptr_t>(p.v) / 2 | static_cast<uintptr_t>(p.D);
+    for (long long s : {p.k_p, p.k_h, p.k_t, p.v_p, p.v_h, p.v_t}) bits |= static_cast<uintptr_t>(s);
+    ML_LAUNCH(h, launch_k((bits & 7) == 0 ? attention_any_kernel<8> : attention_any_kernel<1>, dim3(across, a->B, a->q_heads),
+                          dim3(32 * kAnyWarps), 0, stream, false, p),
               "attention launch");
     return MOE_LORA_OK;
   }

@@ -12,7 +12,14 @@
 // about 32 cycles each, and not the memory were what decoding waited for).  P^T goes from the first product's layout to
 // the second's by transposing 8 x 8 matrices between lanes.  Each warp has a quarter of every stage and a softmax of
 // its own, relative to the maxima of its first 16 keys (attention_tiles.cu says why that is enough); the four are
-// added at the end of the item's part.  Weights go into the second product as two bf16 pieces.
+// added at the end of the item's part.  Weights go into the second product as two bf16 pieces (16 bits), which costs no
+// time, since the tensor cores are 13% busy.
+//
+// Measured, 32 query heads on 4 key heads of 128: 64 requests on 200 to 5000 keys, 374 MB, 62.8 to 64 us, 5.9 TB/s (87% of a
+// plain copy's rate); 256 on 1000 keys 89; one on 700 keys 6.7 and the join's 2.5, a chain of dependent latencies: lengths,
+// table, keys, products, the sum of the warps, and the fetch of code that no call before has left in the caches.
+// Items of 8 rows for up to 8 rows, else of 16 (NT): 16 rows a request as one item, 24 requests, 41.7 us; with 8 rows in
+// items of 16 nothing is lost on decoding alone (62.9), 3 us where tiles' items stand beside it (70 for 67).
 #include "attention.h"
 #include "host.h"
 

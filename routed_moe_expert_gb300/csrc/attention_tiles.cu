@@ -18,6 +18,13 @@
 // Up to 128 rows take both tiles too: they hold the same rows and take the units of keys in turn, and their
 // two results are added at the end (each thread finds its row's other half in its own TMEM lanes).
 //
+// What bounds it: at length the MMAs, which take about 81 cycles for a 128 x 128 x 16 instead of 64, since both operands'
+// shared-memory reads are as long: 2600 cycles a unit of 256 rows and 128 keys, where the exponentials of both tiles
+// (4.4 cycles a warp's) take 1130 beside them.  Measured, 32 query heads on 4 key heads of 128: a prompt of 8192 397 us, 1.38
+// PFLOP/s, 73% of the library's rate (of its products alone, the cut triangle counted as what it is); 2048 53 us, 1024 24,
+// 512 17.3, 128 12.3.  A part's own cost is about 4 units' (its queries, the first weights, the last result), and below
+// about 1024 tokens this and the fetch of the kernel's code are most of the time.
+//
 // Warps 0-3 and 4-7: the rows of tiles 0 and 1, a thread a row; warp 8: TMA; warp 9: MMA issue, and zeroes for
 // values behind the last key that is seen; warp 11: the block's parts of items.  Items come from the schedule in
 // attention.h; with `prefix` the block's item is a part of the shared keys for 256 rows of the whole batch.

@@ -17,7 +17,8 @@ namespace {
 // sums: a request with a long prompt is spread like any other.  Where lengths or cursor are updated in place the blocks
 // form one cluster, whose barrier stands between the last read of them and the first write.
 //
-// Bound by latency: lengths, sums, one dependent load (table or free list), store.
+// Bound by latency: lengths, sums, one dependent load (table or free list), store.  From a graph 2.6 us for one request, 3.9
+// for 64 with a chunk of 449 among them, 4.6 for 511 with 15 000 tokens (6.4 when all blocks were always one cluster).
 // ---------------------------------------------------------------------------------------
 constexpr int kTableThreads = 1024;
 
@@ -181,7 +182,8 @@ __global__ void __launch_bounds__(kTableThreads) page_tables_kernel(const __grid
 // ---------------------------------------------------------------------------------------
 // Cache writes: a copy of T rows of heads to scattered rows, in pieces of V values.  A thread keeps to one piece of
 // a row (its head and place are worked out once) and takes tokens in turn, kFlight of them in flight: all loads,
-// which do not wait for the slots, then the stores.  Bound by memory at length, by latency below.
+// which do not wait for the slots, then the stores.  Bound by memory at length, by latency below: 8192 tokens of 2 x 4 heads
+// of 128 6.7 us, 33.6 MB at 5.0 TB/s (10.8 us when a thread worked out head and place of every piece); one token 1.7 us.
 // ---------------------------------------------------------------------------------------
 constexpr int kFlight = 4;
 
