@@ -943,9 +943,9 @@ def moe_lora_attention(handle: Handle, q: torch.Tensor, k_cache: torch.Tensor, v
     """Causal attention of the rows q [T, Hq, D] (bf16) to their requests' keys and values in the pages
     block_tables [B, width] of k_cache, v_cache [pages, Hk, page size, D] (Hq a multiple of Hk).  Request b
     has the rows from query_offsets[b] to query_offsets[b + 1] (without them: row b), the last of its
-    kv_lens[b] tokens; a row sees the keys up to its own.  max_query_len (the longest request's rows, for the
-    choice of the kernel), scale (1 / sqrt(D) unless given), shared_len: so many first keys of every request
-    are in the same pages (those of request 0) and are read once for all.  Returns out, a new dense tensor
+    kv_lens[b] tokens; a row sees the keys up to its own.  max_query_len: the longest request's rows, for the
+    choice of the kernel (all of T unless given); scale: 1 / sqrt(D) unless given; shared_len: so many first keys of
+    every request are in the same pages, all of them named by request 0's table, and are read once for all.  Returns out, a new dense tensor
     unless given, or (out, lse) with return_lse or lse [T, Hq] float32, the logarithms of the softmax sums.
     Rows that see no key are zero, rows of no request are left as they are."""
     r = (_marshal or _native()).attention(handle.address, q, k_cache, v_cache, block_tables, kv_lens, query_offsets,
