@@ -182,16 +182,16 @@ MLDEV void join_results(const float2* ml, const float* part, int n, int per_row,
     for (int i = member; i < n; i += per_row) {
       const long long at = row(i);
       const float2 x = ml[at];
-      if (x.y == 0.0f) continue;   // nothing was seen there, or nothing that weighs (a NaN is not 0)
       const float4* src = reinterpret_cast<const float4*>(part + at * DP + d);
-      const float4 a = src[0], b = src[1];
-      const float top = fmaxf(m, x.x), ref = reference_of(top);
-      const float f = exp2_approx(m - ref), g = exp2_approx(x.x - ref);
+      const float4 a = src[0], b = src[1];   // (no branch in front of them, so that several results' loads are in flight)
+      const bool none = x.y == 0.0f;         // nothing was seen there, or nothing that weighs (a NaN is not 0)
+      const float top = none ? m : fmaxf(m, x.x), ref = reference_of(top);
+      const float f = exp2_approx(m - ref), g = none ? 0.0f : exp2_approx(x.x - ref);
       m = top;
-      l = l * f + x.y * g;
+      l = l * f + (none ? 0.0f : x.y * g);
       const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-      for (int k = 0; k < 8; ++k) o[k] = o[k] * f + v[k] * g;
+      for (int k = 0; k < 8; ++k) o[k] = o[k] * f + (none ? 0.0f : v[k] * g);
     }
   }
   if (per_row == 1) return;
@@ -472,7 +472,8 @@ extern "C" moe_lora_status moe_lora_attention(moe_lora_handle* h, const moe_lora
   // Up to 16 rows a key head run on the kernel for few rows, more on tiles (4 drafts of 7 heads, 24 requests: 44.9 us on
   // tiles, 65.3 on the other; of 4 heads 43.9 and 41.7).  A batch that may have both, by its longest request and the rows left
   // to the others, is split by request, each kernel taking its own, where the short ones have an item for every SM: 256
-  // requests of one token on 1000 keys beside a prompt of 512 128 us, 160 on tiles alone; with 32 of them 67.2 and 64.5.
+  // requests of one token on 1000 keys beside a prompt of 512 117 us, 158 on tiles alone; with 16 of them on 4000 keys beside
+  // a prompt of 2048 161 and 156.
   const bool tiles = static_cast<long long>(a->max_query_len) * p.G > kFewRows;
   const bool eight = (tiles ? p.G : static_cast<long long>(a->max_query_len) * p.G) <= 8;
   const int few_rows = eight ? 8 : kFewRows;
