@@ -156,9 +156,9 @@ __global__ void __launch_bounds__(32 * kAnyWarps) attention_any_kernel(const __g
 // ---------------------------------------------------------------------------------------
 // Results of a row from several places together.  Sixteen teams of threads a block, DP / 8 threads a team with eight
 // values each; `per_row` teams (1, 4 or 16, by the number of results) take those of a row in turn, so that the 76
-// pieces of a long request are five loads deep, and are added in order.  (Fewer teams are slower where there are many
-// pieces: one request on 1000 keys 11.8 us for 9.4; more where there are few: 64 tokens on 4000 keys 41 us for 30.)
-// Bound by latency, and by the L2 reads of the pieces: 2.5 us behind the 6.7 of one request's 700 keys, beginning early.
+// pieces of a long request are five loads deep, and are added in order.  (One team up to 8 results: one request on
+// 1000 keys 9.5 us for 8.9; 16 teams from 13 on: 64 tokens on 4000 keys 31.7 us for 25.1.)  Bound by latency, and by the L2
+// reads of the pieces: about 2 us behind the 6.7 of one request's 700 keys, beginning early.
 // ---------------------------------------------------------------------------------------
 constexpr int kTeams = 16;
 
