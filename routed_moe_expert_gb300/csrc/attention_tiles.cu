@@ -131,7 +131,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
   constexpr int kSlots = slots_of(DP), TILE = tile_bytes(DP), HALVES = DP / 64;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* ring = smem + 2 * TILE;
-  __shared__ uint64_t full[kSlots], empty[kSlots], s_full[2], p_ready[2], o_full[2], q_full[2], both[2], drain;
+  __shared__ uint64_t full[kSlots], empty[kSlots], s_full[2], p_ready[2], o_full[2], q_full[2], both[2], repaired[4],
+      drain;
   __shared__ uint64_t step_full[kSteps], step_empty[kSteps];
   __shared__ Step steps[kSteps];
   __shared__ ScheduleSmem sched_s;
@@ -158,6 +159,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
       mbar_init(&step_full[i], 1);
       mbar_init(&step_empty[i], 10);   // the other warps that work
     }
+    for (int i = 0; i < 4; ++i) mbar_init(&repaired[i], 1);
     mbar_init(&drain, 1);
     error_s = 0;
     abort_s = 0;
@@ -463,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
     const int wr = (warp & 3) * 32;                   // the warp's first row
     const uint32_t lanes = tmem + (static_cast<uint32_t>(wr) << 16);
     const uint32_t s_at = lanes + k * 128, o_at = lanes + 256 + k * DP;
-    uint32_t s_phase = 0, o_phase = 0, both_phase = 0;
+    uint32_t s_phase = 0, o_phase = 0, both_phase = 0;   // of `both`, and above it of `repaired`
     const float scale = p.scale_log2;   // (not 0)
     const uint32_t unseen = scale < 0.0f ? 0x7f800000u : 0xff800000u;   // the score that scaled is -inf
     // Copies the part's query rows to the products' layout, a warp its own 32 of them, whole rows at a time.
@@ -651,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
         ml_s[k][r] = make_float2(ref, l);
         tc_fence_before();
         arrive(&both[0]);
-        ok = wait_soon(&both[0], both_phase, abort_flag, &error_s);
+        ok = wait_soon(&both[0], both_phase & 1u, abort_flag, &error_s);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
@@ -687,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
         const int chunks = pair ? DP / 32 : DP / 16;   // of 16 columns: little code, which has to be fetched
         const int key_hi = min(seen_here, key0 + hi * kKeys);
         // Rows that a value which they do not see has spoilt; `odd` is a sum of 0 times each of a row's results.
-        auto repair = [&](float odd) {
+        auto repair = [&](float odd, int columns) {
           bool written = false;
           for (unsigned spoilt = __ballot_sync(0xffffffffu, real && odd != 0.0f && sees < key_hi && l > 0.0f && l < INFINITY);
                spoilt != 0; spoilt &= spoilt - 1) {
@@ -696,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
             const unsigned long long there = of_row(to);
             const float sum = of_row(l);
             const bool done = repair_row<DP>(p, request, token_of(p, of_row(head)), of_row(token), of_row(head), key0 + lo * kKeys, key_hi,
-                                             of_row(sees), of_row(ref), 1.0f / sum, c_lo, pair ? DP / 2 : DP,
+                                             of_row(sees), of_row(ref), 1.0f / sum, c_lo, columns,
                                              reinterpret_cast<__nv_bfloat16*>(there), final ? nullptr : reinterpret_cast<float*>(there));
             if (lane == of) written = done;
           }
@@ -714,15 +716,31 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
         };
         bool write = real;
         if (p.in_place && final) {   // the query row is needed for the repair, and gone afterwards
-          float odd = 0.0f;
+          // Rows that both tiles hold: the first tile repairs them whole, and the other one, whose columns lie over the
+          // query as well, writes only behind that.
+          uint32_t* left_s = reinterpret_cast<uint32_t*>(sched_s.items);   // rows of a warp that are still to be written
+          if (k == 0 || !pair) {
+            float odd = 0.0f;
 #pragma unroll 1
-          for (int c = 0; c < chunks; ++c) {
-            fetch(c);
-            tmem_ld_wait();
+            for (int c = 0; c < DP / 16; ++c) {
+              fetch(c);
+              tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) odd = fmaf(result(i), 0.0f, odd);
+              for (int i = 0; i < 16; ++i) odd = fmaf(result(i), 0.0f, odd);
+            }
+            if (repair(odd, DP)) write = false;
+            if (pair) {
+              const unsigned left = __ballot_sync(0xffffffffu, write);
+              if (lane == 0) left_s[warp] = left;
+              arrive(&repaired[warp]);
+            }
+          } else {
+            ok = wait_soon(&repaired[warp - 4], both_phase >> 1, abort_flag, &error_s);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            write = (left_s[warp - 4] >> lane) & 1u;
+            both_phase ^= 2u;
           }
-          if (repair(odd)) write = false;
         }
         float odds[4] = {};
         fetch(0);
@@ -754,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
             }
           }
         }
-        if (!(p.in_place && final)) repair((odds[0] + odds[1]) + (odds[2] + odds[3]));
+        if (!(p.in_place && final)) repair((odds[0] + odds[1]) + (odds[2] + odds[3]), pair ? DP / 2 : DP);
       }
       if (real && c_lo == 0) {
         if (!final) (by_token ? p.part_ml : p.piece_ml)[at] = make_float2(ref, l);
@@ -764,7 +782,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
       tc_fence_before();
       if (pair) {   // neither tile's next item overwrites what the other still reads
         arrive(&both[1]);
-        ok = wait_soon(&both[1], both_phase, abort_flag, &error_s);
+        ok = wait_soon(&both[1], both_phase & 1u, abort_flag, &error_s);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         both_phase ^= 1u;
