@@ -461,6 +461,7 @@ extern "C" moe_lora_status moe_lora_attention(moe_lora_handle* h, const moe_lora
   p.flags = reinterpret_cast<int*>(h->linear_flags + kLinearFlags);
   p.prefix_splits = 0;
   p.out_wide = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0 && p.o_t % 16 == 0 && p.o_h % 16 == 0;
+  p.pieces_wide = (reinterpret_cast<uintptr_t>(workspace) & 31u) == 0;   // (16 are asked for)
   p.in_place = p.out == p.q;
   p.records = nullptr;
   p.piece_ml = nullptr;

@@ -54,6 +54,7 @@ struct AttentionParams {
   int alone;                                   // no other kernel of the call follows: it writes the status word
   int long_queries;                            // requests have many items each
   int out_wide;                                // rows of `out` start on 32-byte boundaries
+  int pieces_wide;                             // the workspace does, and so pieces and parts
   int in_place;                                // `out` is q
   int both_halves;                             // the maps have both halves of a key in a box (tma_load_page2)
   float scale_log2;                            // scale * log2(e): weights are powers of two

@@ -768,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
             for (int i = 0; i < 16; i += 8) {
 #pragma unroll
               for (int e = 0; e < 8; ++e) x[e] = __float_as_uint(o[i + e]);
-              if (write) st_row16(to + 4 * (col + i), x, true, true, true);
+              if (write) st_row16(to + 4 * (col + i), x, p.pieces_wide, true, true);
             }
           }
         }
