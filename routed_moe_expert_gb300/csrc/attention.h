@@ -18,7 +18,7 @@ constexpr int kTileRows = 256, kTileKeys = 128, kTileOver = 4;
 // start and end; a run that ends within these has none of the item.  (Tiles 4: a prompt of 8192 397 us, with 6
 // 406, and with 2 451 for 419 when it was chosen; 16 prompts on up to 1500 keys 72, with 0 99, with 8 76.  Few rows 3: 64
 // requests on up to 2000 keys 25.2 us, with 0 32.5, with 1 28.8, with 6 25.7.)  Where a run holds part of an item its result is a piece (unnormalised
-// sums, maximum, sum of weights) in the workspace, at most two a block, and the block that has the item's
+// sums, reference, sum of weights) in the workspace, at most two a block, and the block that has the item's
 // first unit leaves a record, by which the kernel that follows adds the pieces up.
 //
 // With `whole` (no item is long) items are not cut: a block takes those whose first unit is in its run.  `whole_units` is the
@@ -61,7 +61,7 @@ struct AttentionParams {
   Plan plan;
   PieceRecord* records;                        // [ctas], null with `whole`
   int item_rows;                               // rows of a piece's slot
-  float2* piece_ml;                            // [2 ctas][item_rows] maximum (of scaled scores, base 2), sum
+  float2* piece_ml;                            // [2 ctas][item_rows] reference (of scaled scores, base 2), sum
   float* piece_o;                              // [2 ctas][item_rows][DP]
   // Parts of every row by token and head where keys are shared: the launch over those makes parts 0 to
   // prefix_splits - 1, the requests' own keys the last.  [prefix_splits + 1][T * Hq]
@@ -150,6 +150,16 @@ MLDEV float exp2_approx(float x) {   // 2^-22 relative; 0 for -inf
 
 // The reference that weights are taken relative to: 0 while nothing is seen, so that they are 0 and not NaN.
 MLDEV float reference_of(float m) { return m == -INFINITY ? 0.0f : m; }
+
+// A row's reference is kHeadroom above the maximum of its first scores, and stays: weights start at 2^-20, and later scores
+// that are up to 20 higher (base 2) have weights of at most 1.  When some come to more than kMostWeight, their maximum and
+// kHeadroom are the new reference.  So no weight is above 1, and sum p v passes float32's end only where it does with
+// a running maximum, values of 1e37 under rising scores included.  (bf16 and float32 hold the smaller weights as
+// exactly; those below 2^-126 are 0, which is 2^-106 of the largest.)
+constexpr float kHeadroom = 20.0f, kMostWeight = 1.0f;
+
+// Natural logarithm of a softmax's sum from a reference and the sum l relative to it.
+MLDEV float log_of_sum(float ref, float l) { return ((reference_of(ref) - kHeadroom) + log2f(l * 1048576.0f)) * kLn2; }
 
 // ---------------------------------------------------------------- the plan, worked out by every block
 template <int ROWS, int KEYS, int OVER>
@@ -556,7 +566,7 @@ MLDEV void write_row8(const AttentionParams& p, long long token, int head, int d
   for (int i = 0; i < 8; ++i) v[i] = l == 0.0f ? 0.0f : o[i] * inv;
   __nv_bfloat16* at = p.out + token * p.o_t + head * p.o_h + d;
   if (d < p.D) *reinterpret_cast<uint4*>(at) = pack8(v);   // (D is a multiple of 8)
-  if (d == 0 && p.lse != nullptr) p.lse[token * p.Hq + head] = (reference_of(m) + log2f(l)) * kLn2;
+  if (d == 0 && p.lse != nullptr) p.lse[token * p.Hq + head] = log_of_sum(m, l);
 }
 
 // A row whose result is not finite although its weights are: a warp looks whether a value that the row does not see, of

@@ -11,7 +11,7 @@
 // (with query rows on the 16-row side there were twice as many MMAs, 48 for a warp's 16 keys, and these, at
 // about 32 cycles each, and not the memory were what decoding waited for).  P^T goes from the first product's layout to
 // the second's by transposing 8 x 8 matrices between lanes.  Each warp has a quarter of every stage and a softmax of
-// its own, relative to the maxima of its first 16 keys (attention_tiles.cu says why that is enough); the four are
+// its own, relative to the maxima of its first 16 keys (attention.h, kHeadroom, says why that is enough); the four are
 // added at the end of the item's part.  Weights go into the second product as two bf16 pieces (16 bits), which costs no
 // time, since the tensor cores are 13% busy.
 //
@@ -33,7 +33,6 @@ __host__ __device__ constexpr int stage_bytes(int dp) { return 2 * kKeys * dp * 
 __host__ __device__ constexpr int stages_of(int dp) { return dp == 64 ? 6 : 3; }
 // the ring, and 8 rows of three warps' results
 constexpr int smem_bytes(int dp) { return stages_of(dp) * stage_bytes(dp) + 3 * 8 * (dp + 4) * 4; }
-constexpr float kMostWeight = 1.099511627776e12f;   // 2^40: a unit's weights above it make a new reference
 
 MLDEV void ldsm4(uint32_t at, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -262,12 +261,13 @@ __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(con
               for (int e = 0; e < 4; ++e) wt[e] = exp2_approx(v[e] - reference_of(ref[t][e & 1]));
               const bool renew = ref[t][0] == -INFINITY || ref[t][1] == -INFINITY || !(wt[0] + wt[1] + wt[2] + wt[3] <= kMostWeight);
               if (tries > 0 || !__any_sync(0xffffffffu, renew)) break;
-              // first, and rarely later: the maxima over the warp's keys become the references
+              // first, and rarely later: the maxima over the warp's keys give the references
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 float top = fmaxf(v[e], v[e + 2]);
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+                top += kHeadroom;
                 if (t * 8 + pair + e < rows && top > ref[t][e]) {
                   const float f = exp2_approx(ref[t][e] - top);
                   ref[t][e] = top;
@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(con
           const long long at = place(r, token, head);
           if (final) {
             if (((done >> r8) & 1u) == 0) write_row8(p, token, head, d, m, all, val);
-            else if (d == 0 && p.lse != nullptr) p.lse[token * p.Hq + head] = (reference_of(m) + log2f(all)) * kLn2;
+            else if (d == 0 && p.lse != nullptr) p.lse[token * p.Hq + head] = log_of_sum(m, all);
           } else {
             if (((done >> r8) & 1u) == 0) {
               float4* to = reinterpret_cast<float4*>(parts + at * DP + d);

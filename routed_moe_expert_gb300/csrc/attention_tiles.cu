@@ -10,10 +10,9 @@
 // (2 x head size).  MMAs run in the order of issue, O_0 += P_0 V, S_0 of the next keys, then the same for
 // tile 1, so S may overwrite the P that was just multiplied, and the tiles' weights are due in turn.
 //
-// The row's reference is the maximum of its first 128 scores, and stays: what a later score is above it makes
-// weights above 1, which bf16 and float32 hold as exactly.  Only when a unit's weights come to more than 2^40
-// are its maximum taken and O, which lives in TMEM, multiplied.  So no maximum stands between a score and
-// its weight, and O is hardly ever touched.
+// The row's reference is 20 above the maximum of its first 128 scores, and stays (attention.h, kHeadroom).  Only when a
+// unit's weights come to more than 1, at scores some 13 to 20 above the first ones, are its maximum taken and O, which
+// lives in TMEM, multiplied.  So no maximum stands between a score and its weight, and O is hardly ever touched.
 //
 // Up to 128 rows take both tiles too: they hold the same rows and take the units of keys in turn, and their
 // two results are added at the end (each thread finds its row's other half in its own TMEM lanes).
@@ -123,7 +122,6 @@ struct Step {
   MLDEV int first(int k) const { return lo + (lead == 2 ? k : 0); }
 };
 constexpr int kSteps = 4;
-constexpr float kMostWeight = 1.099511627776e12f;   // 2^40: sums of a row's weights stay far below float32's end
 
 template <int DP>
 __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __grid_constant__ AttentionParams p,
@@ -575,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
                 for (int i = 0; i < 32; ++i)
                   tops[i & 3] = fmaxf(tops[i & 3], c + i < limit ? __uint_as_float(x[i]) * scale : -INFINITY);
               }
-              const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+              const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) + kHeadroom;
               const bool grow = renew && top > ref;
               const float f = grow ? exp2_approx(ref - top) : 1.0f;
               if (grow) ref = top;
@@ -777,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
       if (real && c_lo == 0) {
         if (!final) (by_token ? p.part_ml : p.piece_ml)[at] = make_float2(ref, l);
         else if (p.lse != nullptr)
-          p.lse[static_cast<long long>(token) * p.Hq + head] = (reference_of(ref) + log2f(l)) * kLn2;
+          p.lse[static_cast<long long>(token) * p.Hq + head] = log_of_sum(ref, l);
       }
       tc_fence_before();
       if (pair) {   // neither tile's next item overwrites what the other still reads
