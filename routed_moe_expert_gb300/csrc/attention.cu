@@ -10,9 +10,6 @@
 namespace mlk {
 namespace {
 
-MLDEV float low_half(uint32_t x) { return __uint_as_float(x << 16); }    // of two bf16
-MLDEV float high_half(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
-
 // ---------------------------------------------------------------------------------------
 // Any head size, page size and alignment, on plain cores: a block per query row and head.  Its warps take
 // the keys 32 at a time in turn, a lane a key, each warp with a running maximum m, sum l and result o

@@ -124,7 +124,9 @@ MLDEV int keys_of_token(const AttentionParams& p, int token) {
 }
 
 // mbar_wait in little code, and with the timer read only now and then.  Raises the abort flag when it runs out, after which
-// every wait of the block ends soon.
+// every wait of the block ends soon.  The limit leaves time for a repair (repair_rows) over more than a million keys, at
+// 6.3 us a key for 32 rows.
+constexpr uint64_t kWaitRepairNs = 10000000000ull;   // 10 s
 MLDEV bool wait_soon(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* status) {
   uint64_t since = 0;
 #pragma unroll 1
@@ -133,7 +135,7 @@ MLDEV bool wait_soon(uint64_t* bar, uint32_t parity, volatile int* abort_flag, u
     if (*abort_flag) return false;
     const uint64_t now = globaltimer_ns();
     if (since == 0) since = now;
-    if (now - since > kWaitLimitNs) {
+    if (now - since > kWaitRepairNs) {
       *abort_flag = 1;
       record_status(status, kDevTimeout, kWhereAttention);
       return false;
@@ -141,6 +143,9 @@ MLDEV bool wait_soon(uint64_t* bar, uint32_t parity, volatile int* abort_flag, u
   }
   return true;
 }
+
+MLDEV float low_half(uint32_t x) { return __uint_as_float(x << 16); }    // of two bf16
+MLDEV float high_half(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 
 MLDEV float exp2_approx(float x) {   // 2^-22 relative; 0 for -inf
   float y;
@@ -569,66 +574,107 @@ MLDEV void write_row8(const AttentionParams& p, long long token, int head, int d
   if (d == 0 && p.lse != nullptr) p.lse[token * p.Hq + head] = log_of_sum(m, l);
 }
 
-// A row whose result is not finite although its weights are: a warp looks whether a value that the row does not see, of
-// the keys [key_lo, key_hi) that were multiplied, is not finite (0 times it is NaN), and if so sums columns
-// [d_lo, d_lo + d_n) of the row again over the keys below `limit` on plain cores and
-// writes them: factor * sum as bf16 to `out`, or the sum to `piece`.  Returns whether it did.  Rare, so it is
-// out of the way.
-template <int DP>
-__device__ __noinline__ bool repair_row(const AttentionParams& p, int b, int kh, long long token, int head, int key_lo,
-                                        int key_hi, int limit, float ref, float factor, int d_lo, int d_n,
-                                        __nv_bfloat16* out, float* piece) {
-  const int lane = threadIdx.x & 31;
+// Rows whose result is not finite although their weights are may have been spoilt by a value that they do not see: 0 times
+// it is NaN.  A warp has up to 32 of them, a lane a row: whether it may be one, its token and head, the keys that it sees,
+// its reference and sum of weights, the place of its result.  Of the keys [key_lo, key_hi) that were multiplied the last one
+// is looked for of which one of the values [d_lo, d_lo + d_n) is not finite, and rows that do not see it are summed again
+// on plain cores and written, as bf16 over their sum of weights, or as they are (`piece`).  Returns whether the lane's was.
+//
+// Rare, so it is out of the way, and called with what is at hand.  It takes as long as there are keys, 32 rows in turn at
+// most: a prompt of 8192 whose last value but one is infinite 51 ms (value by value 363), one with an infinity at its 100th
+// key 1.2.  The waits leave time for that (kWaitRepairNs).
+__device__ __noinline__ inline bool repair_rows(const AttentionParams& p, int b, bool maybe, int token, int head, int key_lo,
+                                                int key_hi, int sees, float ref, float sum, int d_lo, int d_n,
+                                                unsigned long long result, bool piece) {
+  const int lane = threadIdx.x & 31, per = d_n / 8, side = 32 / per, mine = lane / per, d = d_lo + lane % per * 8;
+  const int kh = __shfl_sync(0xffffffffu, token_of(p, head), 0);   // (the first row is one)
+  const int limit = maybe && sum > 0.0f && sum < INFINITY ? min(sees, key_hi) : key_hi;
   const int32_t* table = p.tables + b * p.table_stride;
-  auto row_of = [&](const __nv_bfloat16* base, long long s_page, long long s_head, long long s_token, int key) {
-    const int page = table[key >> p.page_log2];
-    return page < 0 || page >= p.num_pages ? nullptr
-                                           : base + page * s_page + kh * s_head + (key & (p.page - 1)) * s_token;
-  };
-  const int from = max(limit, key_lo), per = d_n / 8;
-  bool found = false;
-#pragma unroll 1
-  for (int c = lane; c < (key_hi - from) * per; c += 32) {
-    const int d = d_lo + c % per * 8;
-    const __nv_bfloat16* v = row_of(p.v, p.v_p, p.v_h, p.v_t, from + c / per);
-    if (v == nullptr || d >= p.D) continue;
-    const uint4 x = *reinterpret_cast<const uint4*>(v + d);
-    for (const uint32_t y : {x.x, x.y, x.z, x.w})
-      found = found || (y & 0x7f80u) == 0x7f80u || (y & 0x7f800000u) == 0x7f800000u;
+  int last = -1;   // a lane a piece of a key's values, as many keys side by side as fit
+#pragma unroll 4
+  for (int j = max(key_lo, static_cast<int>(__reduce_min_sync(0xffffffffu, limit))) + mine; j < key_hi; j += side) {
+    const int page = table[j >> p.page_log2];
+    const bool real = page >= 0 && page < p.num_pages && d < p.D;   // (loads without a branch, several in flight)
+    const uint4 x =
+        *reinterpret_cast<const uint4*>(real ? p.v + page * p.v_p + kh * p.v_h + (j & (p.page - 1)) * p.v_t + d : p.v);
+    bool bad = false;
+    for (const uint32_t y : {x.x, x.y, x.z, x.w}) bad = bad || (y & 0x7f80u) == 0x7f80u || (y & 0x7f800000u) == 0x7f800000u;
+    if (real && bad) last = j;
   }
-  if (!__any_sync(0xffffffffu, found)) return false;
-  const __nv_bfloat16* q = p.q + token * p.q_t + head * p.q_h;
-  float o[DP / 32] = {};
+  last = __reduce_max_sync(0xffffffffu, last);
+  const unsigned all = __ballot_sync(0xffffffffu, limit <= last);
 #pragma unroll 1
-  for (int j0 = key_lo; j0 < min(limit, key_hi); j0 += 32) {
-    const int n = min(32, min(limit, key_hi) - j0);
-    float dot = 0.0f;
-    if (lane < n) {
-      const __nv_bfloat16* k = row_of(p.k, p.k_p, p.k_h, p.k_t, j0 + lane);
+  for (unsigned left = all; left != 0; left &= left - 1) {
+    const int of = __ffs(left) - 1;
+    const __nv_bfloat16* q =
+        p.q + __shfl_sync(0xffffffffu, token, of) * p.q_t + __shfl_sync(0xffffffffu, head, of) * p.q_h;
+    const int end = __shfl_sync(0xffffffffu, limit, of);
+    const float reference = __shfl_sync(0xffffffffu, ref, of);
+    float o[8] = {};
 #pragma unroll 1
-      for (int d = 0; k != nullptr && d < p.D; ++d) dot += bf2f(q[d]) * bf2f(k[d]);
-    }
-    const float w = exp2_approx(dot * p.scale_log2 - ref);
-#pragma unroll 1
-    for (int t = 0; t < n; ++t) {
-      const float wt = __shfl_sync(0xffffffffu, w, t);
-      const __nv_bfloat16* v = row_of(p.v, p.v_p, p.v_h, p.v_t, j0 + t);
+    for (int j0 = key_lo; j0 < end; j0 += 32) {   // a lane a key for the scores, then a lane a piece of the values
+      const int j = j0 + lane, page = j < end ? table[j >> p.page_log2] : -1;
+      const __nv_bfloat16* row = nullptr;
+      float w = 0.0f;
+      if (page >= 0 && page < p.num_pages) {   // (the values of another page count as zeros)
+        const long long place = j & (p.page - 1);
+        const __nv_bfloat16* k = p.k + page * p.k_p + kh * p.k_h + place * p.k_t;
+        row = p.v + page * p.v_p + kh * p.v_h + place * p.v_t;
+        float dot[2] = {0.0f, 0.0f};
+#pragma unroll 8
+        for (int c = 0; c < p.D; c += 8) {
+          const uint4 x = *reinterpret_cast<const uint4*>(k + c), y = *reinterpret_cast<const uint4*>(q + c);
+          const uint32_t x4[4] = {x.x, x.y, x.z, x.w}, y4[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-      for (int i = 0; i < DP / 32; ++i) {
-        const int d = d_lo + i * 32 + lane;
-        if (v != nullptr && i * 32 + lane < d_n && d < p.D) o[i] += wt * bf2f(v[d]);
+          for (int e = 0; e < 4; ++e) {
+            dot[0] = fmaf(low_half(x4[e]), low_half(y4[e]), dot[0]);
+            dot[1] = fmaf(high_half(x4[e]), high_half(y4[e]), dot[1]);
+          }
+        }
+        w = exp2_approx((dot[0] + dot[1]) * p.scale_log2 - reference);
+      }
+#pragma unroll 8
+      for (int t0 = 0; t0 < 32; t0 += side) {
+        const float wt = __shfl_sync(0xffffffffu, w, t0 + mine);
+        const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), t0 + mine));
+        const bool real = v != nullptr && d < p.D;
+        const uint4 x = *reinterpret_cast<const uint4*>(real ? v + d : q);
+        const uint32_t x4[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          o[2 * e] += real ? wt * low_half(x4[e]) : 0.0f;
+          o[2 * e + 1] += real ? wt * high_half(x4[e]) : 0.0f;
+        }
       }
     }
-  }
+    for (int off = per; off < 32; off <<= 1)
 #pragma unroll
-  for (int i = 0; i < DP / 32; ++i) {
-    const int d = d_lo + i * 32 + lane;
-    if (i * 32 + lane >= d_n) continue;
-    if (piece != nullptr) piece[d] = o[i];
-    else if (d < p.D) out[d] = f2bf(o[i] * factor);
+      for (int e = 0; e < 8; ++e) o[e] += __shfl_xor_sync(0xffffffffu, o[e], off);
+    const float f = 1.0f / __shfl_sync(0xffffffffu, sum, of);
+    const unsigned long long to = __shfl_sync(0xffffffffu, result, of);
+    if (mine == 0) {
+      if (piece) {
+        float4* at = reinterpret_cast<float4*>(to) + d / 4;
+        at[0] = make_float4(o[0], o[1], o[2], o[3]);
+        at[1] = make_float4(o[4], o[5], o[6], o[7]);
+      } else if (d < p.D) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] *= f;
+        *(reinterpret_cast<uint4*>(to) + d / 8) = pack8(o);
+      }
+    }
+    __syncwarp();
   }
-  __syncwarp();
-  return true;
+  return (all >> lane) & 1u;
+}
+
+// The same for one row of the whole warp.
+__device__ __noinline__ inline bool repair_row(const AttentionParams& p, int b, int token, int head, int key_lo, int key_hi, int sees,
+                                               float ref, float sum, int d_n, __nv_bfloat16* out, float* piece) {
+  const unsigned long long to = piece != nullptr ? reinterpret_cast<unsigned long long>(piece) : reinterpret_cast<unsigned long long>(out);
+  return __any_sync(0xffffffffu, repair_rows(p, b, (threadIdx.x & 31) == 0, token, head, key_lo, key_hi, sees, ref, sum, 0, d_n, to,
+                                             piece != nullptr));
 }
 
 // Box of one page's keys (or a part of a page) from the caches' maps; x a multiple of 64.

@@ -399,9 +399,9 @@ __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(con
               long long token;
               int head;
               const long long at = place(r, token, head);
-              if (repair_row<DP>(p, w.b, w.kh, token, head, p.shared + x.lo * kKeys, min(sees, p.shared + x.hi * kKeys),
-                                 max(w.r.kv - w.r.n + token_of(p, row0 + r) + 1, 0), m, 1.0f / all, 0, DP,
-                                 p.out + token * p.o_t + head * p.o_h, final ? nullptr : parts + at * DP) &&
+              if (repair_row(p, w.b, token, head, p.shared + x.lo * kKeys, min(sees, p.shared + x.hi * kKeys),
+                             max(w.r.kv - w.r.n + token_of(p, row0 + r) + 1, 0), m, all, DP, p.out + token * p.o_t + head * p.o_h,
+                             final ? nullptr : parts + at * DP) &&
                   lane == 0)
                 atomicOr(&done_s, 1u << r8);
             }

@@ -688,19 +688,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
         const int key_hi = min(seen_here, key0 + hi * kKeys);
         // Rows that a value which they do not see has spoilt; `odd` is a sum of 0 times each of a row's results.
         auto repair = [&](float odd, int columns) {
-          bool written = false;
-          for (unsigned spoilt = __ballot_sync(0xffffffffu, real && odd != 0.0f && sees < key_hi && l > 0.0f && l < INFINITY);
-               spoilt != 0; spoilt &= spoilt - 1) {
-            const int of = __ffs(spoilt) - 1;
-            auto of_row = [&](auto x) { return __shfl_sync(0xffffffffu, x, of); };
-            const unsigned long long there = of_row(to);
-            const float sum = of_row(l);
-            const bool done = repair_row<DP>(p, request, token_of(p, of_row(head)), of_row(token), of_row(head), key0 + lo * kKeys, key_hi,
-                                             of_row(sees), of_row(ref), 1.0f / sum, c_lo, columns,
-                                             reinterpret_cast<__nv_bfloat16*>(there), final ? nullptr : reinterpret_cast<float*>(there));
-            if (lane == of) written = done;
-          }
-          return written;
+          const bool maybe = real && odd != 0.0f && sees < key_hi;
+          return __any_sync(0xffffffffu, maybe) && repair_rows(p, request, maybe, token, head, key0 + lo * kKeys, key_hi, sees, ref, l,
+                                                               c_lo, columns, to, !final);
         };
         uint32_t own[16], mate[16];
         auto fetch = [&](int c) {
