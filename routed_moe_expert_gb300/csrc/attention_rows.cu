@@ -213,9 +213,9 @@ __global__ void __launch_bounds__(kThreads, kFewPerSm) attention_rows_kernel(con
       for (int t = 0; t < NT; ++t) {
 #pragma unroll
         for (int n = 0; n < DP / 16; ++n) o[t][n][0] = o[t][n][1] = o[t][n][2] = o[t][n][3] = 0.0f;
-        // (columns that are no row have the reference 0 and weights of 0)
-        ref[t][0] = t * 8 + pair < rows ? -INFINITY : 0.0f;
-        ref[t][1] = t * 8 + pair + 1 < rows ? -INFINITY : 0.0f;
+        // (columns that are no row, or see none of this warp's keys, have the reference 0 and weights of 0)
+        ref[t][0] = limit[t][0] > p.shared + x.lo * kKeys + warp * 16 ? -INFINITY : 0.0f;
+        ref[t][1] = limit[t][1] > p.shared + x.lo * kKeys + warp * 16 ? -INFINITY : 0.0f;
         l[t][0] = l[t][1] = 0.0f;
       }
       for (int j = x.lo; j < x.hi; ++j) {

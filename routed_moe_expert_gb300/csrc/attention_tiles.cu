@@ -543,7 +543,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
         wait_soon(bar, parity, abort_flag, &error_s);
         __syncwarp();
       };
-      float ref = r < rows ? -INFINITY : 0.0f, l = 0.0f;
+      // (A row that sees nothing here asks for no reference: a whole warp looks for it, unit by unit, until it has one.)
+      float ref = sees > key0 + first_unit * kKeys ? -INFINITY : 0.0f, l = 0.0f;
       if (wr >= rows) {   // no row of this warp is one: its weights may be anything
         for (int j = first_unit; j < hi; j += lead) {
           wait(&s_full[k], s_phase);
@@ -627,6 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tiles_kernel(const __gr
           arrive(&p_ready[k]);
         }
       }
+      if (l == 0.0f) ref = -INFINITY;
       fetch_next();
       if (!ok) break;
       if (asked) queries_there();
