@@ -631,7 +631,7 @@ typedef struct {
   const moe_lora_bf16* q;         /* [T, q_heads, head_dim]                                            */
   const moe_lora_bf16* k_cache;   /* [num_pages, k_heads, page_size, head_dim] in any order of strides */
   const moe_lora_bf16* v_cache;
-  const int32_t* block_tables;    /* [B, table_width]                                                  */
+  const int32_t* block_tables;    /* [B, table_width], table_width * page_size up to 2^31 - 8192       */
   const int32_t* kv_lens;         /* [B] keys of each request, its new tokens' among them              */
   const int32_t* query_offsets;   /* [B + 1] first query row of each request; NULL: row b is request b's */
   moe_lora_bf16* out;             /* [T, q_heads, head_dim]; may be q itself, with its strides         */

@@ -305,6 +305,7 @@ cudaError_t launch_fold(const AttentionParams& p, int dp, cudaStream_t stream) {
 // row where keys are shared.
 // Every part grows with T alone, so what is enough for T rows is enough for fewer.
 constexpr int kWholeUnits = 12;   // see moe_lora_attention
+constexpr long long kMostKeys = 0x80000000LL - 8192;   // of a table: the kernels round up to units and look ahead in 32 bits
 constexpr int kMaxSms = 160;   // blocks are a multiple of the GPU's 152
 constexpr int kPrefixSplits = 64, kPrefixBlocks = 2 * kMaxSms;
 constexpr size_t round256(size_t n) { return (n + 255) / 256 * 256; }
@@ -403,7 +404,7 @@ extern "C" moe_lora_status moe_lora_attention(moe_lora_handle* h, const moe_lora
       a->head_dim < 1 || a->num_pages < 0 || a->page_size < 1 || a->table_width < 0 || a->max_query_len < 0 ||
       a->shared_len < 0 || (a->B > 1 && a->table_stride < a->table_width) ||
       static_cast<long long>(a->num_pages) * a->page_size > 0x7fffffffLL ||
-      static_cast<long long>(a->table_width) * a->page_size > 0x7fffffffLL)
+      static_cast<long long>(a->table_width) * a->page_size > kMostKeys)
     return MOE_LORA_ERR_INVALID_ARG;
   if (a->query_offsets == nullptr && a->T != a->B) return MOE_LORA_ERR_INVALID_ARG;
   if (!(std::fabs(a->scale) < INFINITY)) return MOE_LORA_ERR_INVALID_ARG;
