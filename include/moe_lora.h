@@ -646,7 +646,7 @@ typedef struct {
   int num_pages, page_size, table_width;
   int max_query_len;              /* the longest request's query rows; only chooses among the kernels  */
   int shared_len;                 /* >= 0: the first shared_len keys of every request lie in the same pages */
-  float scale;                    /* of the scores, usually 1 / sqrt(head_dim)                         */
+  float scale;                    /* of the scores, usually 1 / sqrt(head_dim); up to 2.3e38           */
 } moe_lora_attention_args;
 
 /* Host-only: bytes of workspace that are enough for moe_lora_attention on up to T query rows of these heads,

@@ -407,7 +407,8 @@ extern "C" moe_lora_status moe_lora_attention(moe_lora_handle* h, const moe_lora
       static_cast<long long>(a->table_width) * a->page_size > kMostKeys)
     return MOE_LORA_ERR_INVALID_ARG;
   if (a->query_offsets == nullptr && a->T != a->B) return MOE_LORA_ERR_INVALID_ARG;
-  if (!(std::fabs(a->scale) < INFINITY)) return MOE_LORA_ERR_INVALID_ARG;
+  const float scale_log2 = a->scale * 1.4426950408889634f;
+  if (!(std::fabs(scale_log2) < INFINITY)) return MOE_LORA_ERR_INVALID_ARG;
   if (a->shared_len > static_cast<long long>(a->table_width) * a->page_size) return MOE_LORA_ERR_INVALID_ARG;
   if (a->head_dim > 512 || a->B > 65535 || static_cast<long long>(a->T) * a->q_heads > kMaxExtent) return MOE_LORA_ERR_UNSUPPORTED;
   if (a->T == 0 || a->B == 0) return MOE_LORA_OK;
@@ -454,7 +455,7 @@ extern "C" moe_lora_status moe_lora_attention(moe_lora_handle* h, const moe_lora
   p.page = a->page_size;
   p.width = a->table_width;
   p.shared = a->shared_len;
-  p.scale_log2 = a->scale * 1.4426950408889634f;
+  p.scale_log2 = scale_log2;
   p.status = static_cast<uint32_t*>(workspace);
   p.flags = reinterpret_cast<int*>(h->linear_flags + kLinearFlags);
   p.prefix_splits = 0;
