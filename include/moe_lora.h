@@ -595,9 +595,9 @@ typedef struct {
    ones one after another.  Only new entries of the tables are written, so a repeated call from the same
    `taken` gives the same.  Captured in a graph it follows the lengths of each replay.
    `workspace` (optional, 4 bytes): its first word is the status that moe_lora_check_status reads,
-   DEVICE_CHECK when a length is negative (it counts as 0), the free list ends (requests get what is left,
-   in order), a table is too narrow, `taken` lies outside the list, or the requests bring more than T
-   tokens (offsets stop at T).  A token without a page gets slot -1 and kv_lens counts those before it alone.
+   DEVICE_CHECK when a length is negative (it counts as 0) or passes 2^31 - 1, the free list ends (requests
+   get what is left, in order), a table is too narrow, `taken` lies outside the list, or the requests bring
+   more than T tokens (offsets stop at T).  A token without a page gets slot -1 and kv_lens counts those before it alone.
    One launch.  Outputs must not overlap inputs but as named.  Errors: INVALID_ARG, WORKSPACE_TOO_SMALL, CUDA. */
 moe_lora_status moe_lora_page_tables(moe_lora_handle* h, const moe_lora_page_tables_args* a, void* workspace,
                                      size_t workspace_bytes, moe_lora_stream stream);

@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(kTableThreads) page_tables_kernel(const __grid
   bool bad = taken < 0 || taken > p.num_free;
   const int cursor = min(max(taken, 0), p.num_free);
   const int left = p.num_free - cursor;      // free pages
-  const long long room = static_cast<long long>(p.width) * p.page;
+  const long long room = min(static_cast<long long>(p.width) * p.page, 0x7fffffffll);   // (lengths are 32 bits)
   long long tokens = 0;                      // of the requests before this chunk, and
   int pages = 0;                             // the pages they lack (at most left: granted)
   for (int b0 = 0; b0 == 0 || b0 < p.B; b0 += NT) {
@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kTableThreads) page_tables_kernel(const __grid
     cached_s[tid] = cached;
     held_s[tid] = held;
     pages_s[tid] = held + granted;
-    const long long kv = min(after, static_cast<long long>(held + granted) * p.page);
+    const long long kv = min(min(after, room), static_cast<long long>(held + granted) * p.page);
     if (rank == 0 && b < p.B) {
       p.kv[b] = static_cast<int>(kv);
       p.offsets[b] = static_cast<int>(min(first_tok, static_cast<long long>(p.T)));
