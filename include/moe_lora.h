@@ -661,11 +661,15 @@ moe_lora_status moe_lora_attention_workspace_size(int T, int q_heads, int k_head
    as they are.  Keys and values that a row does not see, the rest of a last page among them, may hold anything;
    a value that is not finite makes those rows' results that see it infinite or NaN.
    shared_len names keys that all requests have in common (a common prompt): they are read from request 0's
-   table, once for all rows instead of once for each request; the results are the same up to float32 sums.  That
-   table names the pages of all shared_len keys even where request 0 has fewer; a request sees no more than its
-   kv_lens.  (The fast case takes whole 128 keys of them so, and the rest as each request's own.)
-   Scores, sums and the result are float32, rounded once at the end; the weights p_j are an operand of the
-   tensor cores in between, as bf16 (two bf16 pieces where requests have up to 16 rows a key head).
+   table, once for all rows instead of once for each request; the results are the same up to float32 sums and the
+   rounding of the weights, see below.  That table names the pages of all shared_len keys even where request 0 has
+   fewer; a request sees no more than its kv_lens.  (The fast case takes whole 128 keys of them so, and the rest
+   as each request's own.)
+   Scores, sums and the result are float32, rounded once at the end.  In between the weights p_j are an operand of
+   the tensor cores: two bf16 pieces, off by up to 2^-16 of each, where the batch's requests have up to 16 rows a key
+   head (max_query_len * q_heads / k_heads) and for such requests of a mixed batch where they are many enough to run
+   apart; one bf16, off by up to 2^-8 of each, for all other requests and for the keys of shared_len, whatever the
+   requests' rows.  On plain cores (below) they are float32.
    head_dim a multiple of 8 up to 128, pages of a power of two of at least 16 tokens, 16-byte pieces in q, out
    and the caches, and a scale other than 0 are the fast case; anything else runs on plain cores, and so does a batch
    whose units of keys (64 or 128 for every 8, 16 or 256 rows of a key head, tables counted as full) come near 2^30.

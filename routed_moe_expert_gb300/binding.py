@@ -903,7 +903,9 @@ def moe_lora_page_tables(handle: Handle, block_tables: torch.Tensor, cached_lens
     are entered in its row.  num_tokens: the rows of the step's batch, the requests' new tokens one after
     another and padding.  Returns a dict of kv_lens [B] (cached and new), query_offsets [B + 1], slot_map
     [num_tokens] (page * page_size + place, -1 for padding), positions [num_tokens] and taken [1];
-    `outputs` may bring any of them, also cached_lens as kv_lens and `taken` itself as taken."""
+    `outputs` may bring any of them, also cached_lens as kv_lens and `taken` itself as taken; those that it lacks
+    are allocated and entered in it, and it is what is returned, so a later call with the same dict writes the same
+    tensors (and wants as many tokens)."""
     r = (_marshal or _native()).page_tables(handle.address, block_tables, cached_lens, new_lens, page_size, free_pages,
                                             taken, num_tokens, outputs, workspace,
                                             None if stream is None else _stream(stream))
@@ -945,7 +947,8 @@ def moe_lora_attention(handle: Handle, q: torch.Tensor, k_cache: torch.Tensor, v
     has the rows from query_offsets[b] to query_offsets[b + 1] (without them: row b), the last of its
     kv_lens[b] tokens; a row sees the keys up to its own.  max_query_len: the longest request's rows, for the
     choice of the kernel (all of T unless given); scale: 1 / sqrt(D) unless given; shared_len: so many first keys of
-    every request are in the same pages, all of them named by request 0's table, and are read once for all.  Returns out, a new dense tensor
+    every request are in the same pages, all of them named by request 0's table, and are read once for all (their
+    weights are rounded to bf16, as those of requests with more than 16 rows a key head).  Returns out, a new dense tensor
     unless given, or (out, lse) with return_lse or lse [T, Hq] float32, the logarithms of the softmax sums.
     Rows that see no key are zero, rows of no request are left as they are."""
     r = (_marshal or _native()).attention(handle.address, q, k_cache, v_cache, block_tables, kv_lens, query_offsets,
