@@ -667,8 +667,8 @@ moe_lora_status moe_lora_attention_workspace_size(int T, int q_heads, int k_head
    as each request's own.)
    Scores, sums and the result are float32, rounded once at the end.  In between the weights p_j are an operand of
    the tensor cores: two bf16 pieces, off by up to 2^-16 of each, where the batch's requests have up to 16 rows a key
-   head (max_query_len * q_heads / k_heads) and for such requests of a mixed batch where they are many enough to run
-   apart; one bf16, off by up to 2^-8 of each, for all other requests and for the keys of shared_len, whatever the
+   head (max_query_len * q_heads / k_heads), and in a mixed batch for requests of up to 8 such rows (16 with 9 to 16
+   query heads to a key head) where they are many enough to run apart; one bf16, off by up to 2^-8 of each, for all other requests and for the keys of shared_len, whatever the
    requests' rows.  On plain cores (below) they are float32.
    head_dim a multiple of 8 up to 128, pages of a power of two of at least 16 tokens, 16-byte pieces in q, out
    and the caches, and a scale other than 0 are the fast case; anything else runs on plain cores, and so does a batch

@@ -14,8 +14,8 @@ namespace {
 // Any head size, page size and alignment, on plain cores: a block per query row and head.  Its warps take
 // the keys 32 at a time in turn, a lane a key, each warp with a running maximum m, sum l and result o
 // (o <- o 2^(m - m') + sum p v), and the block adds the warps' results at the end.  Bound by loads from L2: every head of
-// a group reads its keys again.  16 requests on 4000 keys, 32 + 4 heads of 128, pages of 48: 215 us (value by value, as
-// where pieces of 16 bytes do not fit, 1245); heads of 192 360, heads of 100 649; a prompt of 512 461.
+// a group reads its keys again.  16 requests on 4000 keys, 32 + 4 heads of 128, pages of 48: 214 us (value by value, as
+// where pieces of 16 bytes do not fit, 1245); heads of 192 358, heads of 100 639; a prompt of 512 461.
 // ---------------------------------------------------------------------------------------
 constexpr int kAnyWarps = 8;
 
@@ -469,11 +469,11 @@ extern "C" moe_lora_status moe_lora_attention(moe_lora_handle* h, const moe_lora
   // what the kernels' 32-bit arithmetic holds: rows divided by G (token_of), and the weight of all items, at most
   const long long group_rows = static_cast<long long>(p.T) * p.G;
   const long long own_most = static_cast<long long>(p.width) * p.page;
-  // Up to 16 rows a key head run on the kernel for few rows, more on tiles (4 drafts of 7 heads, 24 requests: 44.9 us on
-  // tiles, 65.3 on the other; of 4 heads 43.9 and 41.7).  A batch that may have both, by its longest request and the rows left
-  // to the others, is split by request, each kernel taking its own, where the short ones have an item for every SM: 256
-  // requests of one token on 1000 keys beside a prompt of 512 117 us, 158 on tiles alone; with 16 of them on 4000 keys beside
-  // a prompt of 2048 161 and 156.
+  // Up to 16 rows a key head run on the kernel for few rows, more on tiles (4 drafts of 24 requests on 1000 to 9000 keys, by
+  // 4, 5 and 7 query heads of 128 to each of 4 key heads: 47, 80 and 74 us on that kernel, 54 on tiles; on 1000 to 4000 keys 30, 44 and
+  // 46, and 36).  A batch that may have both, by its longest request and the rows left to the others, is split by request, each
+  // kernel taking its own, where the short ones have an item for every SM: 256 requests of one token on 1000 keys beside a
+  // prompt of 512 107 us, 141 on tiles alone; with 32 of them 36.7 and 34.9, and 16 on 4000 keys beside a prompt of 2048 77 and 76.
   const bool tiles = static_cast<long long>(a->max_query_len) * p.G > kFewRows;
   const bool eight = (tiles ? p.G : static_cast<long long>(a->max_query_len) * p.G) <= 8;
   const int few_rows = eight ? 8 : kFewRows;

@@ -15,11 +15,12 @@
 // added at the end of the item's part.  Weights go into the second product as two bf16 pieces (16 bits), which costs no
 // time, since the tensor cores are 13% busy.
 //
-// Measured, 32 query heads on 4 key heads of 128: 64 requests on 200 to 5000 keys, 374 MB, 62.8 to 64 us, 5.9 TB/s (87% of a
+// Measured, 32 query heads on 4 key heads of 128: 64 requests on 200 to 5000 keys, 374 MB, 62.5 to 63.7 us, 5.9 TB/s (88% of a
 // plain copy's rate); 256 on 1000 keys 89; one on 700 keys 6.7 and the join's 2, a chain of dependent latencies: lengths,
 // table, keys, products, the sum of the warps, and the fetch of code that no call before has left in the caches.
-// Items of 8 rows for up to 8 rows, else of 16 (NT): 16 requests of 8 rows on 2000 keys 18.3 us, in items of 16 20.2, and 256 on
-// 100 keys 23.3 and 27.4; 24 requests of 28 rows in items of 32, whose queries do not fit into registers, 99 (on tiles 54).
+// Items of 8 rows for up to 8 rows, else of 16 (NT): 16 requests of 8 rows on 2000 keys 16.4 us, in items of 16 19.7, and 256 on
+// 100 keys 21.5 and 27.1; 24 requests of 28 rows on 1000 to 9000 keys in items of 16 74, of 32, whose queries do not fit into
+// registers, 99 (on tiles 54).  (With items of 16 and heads of 128 a thread spills 76 bytes; no other instance does.)
 #include "attention.h"
 #include "host.h"
 

@@ -5,6 +5,9 @@
 //   P = 2^(scale S - reference)  by the row's thread, S read from TMEM, P written over it as bf16
 //   O += P V                     P from TMEM, V [keys][values] as the MN-major operand, O stays in TMEM
 //
+// P is one bf16 a weight, off by up to 2^-8 of it, while their sum is of the float32 weights: 0.0023 of the result in the 2-norm
+// where its own rounding is 0.0017.  A second bf16 for the rest would make three products of the two that prompts are bound by.
+//
 // A block takes two tiles of 128 rows, so that the tensor cores multiply for one while the threads of the
 // other take exponentials, and a key is fetched once for both.  TMEM: S of both tiles (2 x 128 columns), O of both
 // (2 x head size).  MMAs run in the order of issue, O_0 += P_0 V, S_0 of the next keys, then the same for
@@ -19,10 +22,10 @@
 //
 // What bounds it: at length the MMAs, which take about 81 cycles for a 128 x 128 x 16 instead of 64, since both operands'
 // shared-memory reads are as long: 2600 cycles a unit of 256 rows and 128 keys, where the exponentials of both tiles
-// (4.4 cycles a warp's) take 1130 beside them.  Measured, 32 query heads on 4 key heads of 128: a prompt of 8192 397 us, 1.38
-// PFLOP/s, 73% of the library's rate (of its products alone, the cut triangle counted as what it is); 2048 53 us, 1024 24,
-// 512 17.3, 128 12.3.  A part's own cost is about 4 units' (its queries, the first weights, the last result), and below
-// about 1024 tokens this and the fetch of the kernel's code are most of the time.
+// (4.4 cycles a warp's) take 1130 beside them.  Measured, 32 query heads on 4 key heads of 128: a prompt of 8192 399 us, 1.38
+// PFLOP/s, 72% of the library's rate (of its products alone, the cut triangle counted as what it is); 2048 52 us, 1024 23.5,
+// 512 17.2, 128 12.6.  A part's own cost is about 4 units' (its queries, the first weights, the last result), and below
+// about 1024 tokens this and the fetch of the kernel's code are most of the time.  (With heads of 64 a thread spills 20 bytes.)
 //
 // Warps 0-3 and 4-7: the rows of tiles 0 and 1, a thread a row; warp 8: TMA; warp 9: MMA issue, and zeroes for
 // values behind the last key that is seen; warp 11: the block's parts of items.  Items come from the schedule in
